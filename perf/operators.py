@@ -144,8 +144,8 @@ def _table(length, rot, dev):
 
 def _scale_of(amax):
     """The smallest power of two, at least MIN_SCALE, that brings amax to at most 448."""
-    m, e = torch.frexp(amax / E4M3_MAX)
-    return torch.ldexp(torch.ones_like(amax), torch.where(m == 0.5, e - 1, e)).clamp_min(MIN_SCALE)
+    m, e = torch.frexp(amax.clamp_min(E4M3_MAX * MIN_SCALE) / E4M3_MAX)
+    return torch.ldexp(torch.ones_like(amax), torch.where(m == 0.5, e - 1, e))
 
 
 def _filled_pool(case, gen, dev):
