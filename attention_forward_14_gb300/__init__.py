@@ -14,10 +14,16 @@ from .binding import (  # noqa: F401
     attn_fwd_host,
     attn_fwd_kvcache,
     attn_fwd_kvcache_paged,
+    attn_fwd_kvcache_paged_fp8,
     attn_fwd_splitkv,
     attn_fwd_varlen,
+    attn_kvcache_append_paged,
+    attn_qk_norm_rope,
+    attn_qk_norm_rope_bwd,
     bwd_workspace_bytes,
+    kvcache_paged_fp8_workspace_bytes,
     lib_path,
     load,
+    qk_norm_rope_bwd_workspace_bytes,
     status,
 )

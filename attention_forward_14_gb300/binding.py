@@ -27,7 +27,9 @@ EXPORTS = ["attn_fwd", "attn_fwd_host", "attn_fwd_varlen", "attn_fwd_fp8", "attn
            "attn_fwd_splitkv_default_splits", "attn_fwd_splitkv_noalloc", "attn_last_error", "attn_fwd_status", "attn_fwd_status_clear",
            "attn_fwd_debug_status", "attn_fwd_sched_pin_slot", "attn_fwd_bounds_selftest", "attn_bwd_bounds_selftest",
            "attn_fwd_watchdog_selftest", "attn_bwd_watchdog_selftest", "attn_version", "attn_bwd", "attn_bwd_workspace_bytes", "attn_bwd_varlen",
-           "attn_bwd_varlen_workspace_bytes", "attn_fwd_kvcache", "attn_fwd_kvcache_paged"]
+           "attn_bwd_varlen_workspace_bytes", "attn_fwd_kvcache", "attn_fwd_kvcache_paged", "attn_qk_norm_rope",
+           "attn_qk_norm_rope_bwd", "attn_qk_norm_rope_bwd_workspace_bytes", "attn_kvcache_append_paged",
+           "attn_fwd_kvcache_paged_fp8", "attn_fwd_kvcache_paged_fp8_workspace_bytes"]
 
 
 class AttnError(RuntimeError):
@@ -102,6 +104,18 @@ def _bind(lib):
                                     c_int, c_float, c_int, vp, i64, vp]
     lib.attn_bwd_varlen_workspace_bytes.restype = i64
     lib.attn_bwd_varlen_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
+    lib.attn_qk_norm_rope.restype = c_int
+    lib.attn_qk_norm_rope.argtypes = [vp] * 13 + [i64] * 8 + [c_int, c_float, c_int, vp]
+    lib.attn_qk_norm_rope_bwd.restype = c_int
+    lib.attn_qk_norm_rope_bwd.argtypes = [vp] * 19 + [i64] * 8 + [c_int, c_float, c_int, vp, i64, vp]
+    lib.attn_qk_norm_rope_bwd_workspace_bytes.restype = i64
+    lib.attn_qk_norm_rope_bwd_workspace_bytes.argtypes = [i64]
+    lib.attn_kvcache_append_paged.restype = c_int
+    lib.attn_kvcache_append_paged.argtypes = [vp] * 13 + [i64] * 10 + [c_int, c_int, vp]
+    lib.attn_fwd_kvcache_paged_fp8.restype = c_int
+    lib.attn_fwd_kvcache_paged_fp8.argtypes = [vp] * 9 + [i64] * 9 + [c_int, c_float, c_int, vp, i64, vp]
+    lib.attn_fwd_kvcache_paged_fp8_workspace_bytes.restype = i64
+    lib.attn_fwd_kvcache_paged_fp8_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
     return lib
 
 
@@ -572,3 +586,301 @@ def attn_bwd_varlen(q, k, v, o, dout, lse, cu_seqlens_q, cu_seqlens_k, max_seqle
                                  _stream_handle(stream, q.device))
     _check(rc, lib)
     return dq, dk, dv
+
+
+_Strides = ctypes.c_int64 * 3
+
+
+def _as_dense(name, t):
+    """A [b, h, s, d] tensor, or a packed [total, h, d] one as b = 1: its shape and its strides (b, head, token)."""
+    if not t.is_cuda:
+        raise AttnError(-2, f"{name} must be a CUDA tensor")
+    if t.dim() == 4:
+        (b, h, s, d), st = t.shape, t.stride()
+    elif t.dim() == 3:
+        (s, h, d), st = t.shape, t.stride()
+        b, st = 1, (0, st[1], st[0], st[2])
+    else:
+        raise AttnError(-2, f"{name} must be [b, h, s, d] or [total, h, d]")
+    if st[3] != 1 and d > 1 and t.numel() > 0:
+        raise AttnError(-2, f"the {d} values of a head of {name} must be contiguous")
+    # an axis of one has no stride of its own
+    return (b, h, s, d), _Strides(st[0] if b > 1 else 0, st[1] if h > 1 else 0, st[2] if s > 1 else 0)
+
+
+def _rotation(cos, sin, device):
+    """(pointer, pointer, rot, table_len) of the rotation's tables; nothing for none."""
+    import torch
+    if (cos is None) != (sin is None):
+        raise AttnError(-1, "cos and sin must both be given or both be None")
+    if cos is None:
+        return None, None, 0, 0
+    if cos.dim() != 2 or cos.shape != sin.shape:
+        raise AttnError(-2, "cos and sin must be [table_len, rot / 2]")
+    for name, t in (("cos", cos), ("sin", sin)):
+        if t.dtype != torch.float32 or t.device != device or not t.is_contiguous():
+            raise AttnError(-4, f"{name} must be a contiguous fp32 tensor on the inputs' device")
+    return cos.data_ptr(), sin.data_ptr(), 2 * cos.shape[1], cos.shape[0]
+
+
+def _positions(positions, b, s, packed, cos, device):
+    """(pointer, stride over b) of the positions of a dense [b, s] or packed [total] batch."""
+    import torch
+    if positions is None:
+        if packed and cos is not None:
+            raise AttnError(-1, "a packed batch needs positions: they start again in every sequence")
+        return None, 0
+    shapes = [(s,)] if packed else [(s,), (b, s)]
+    if positions.dtype != torch.int32 or positions.device != device or tuple(positions.shape) not in shapes:
+        raise AttnError(-4, f"positions must be int32 of shape {' or '.join(map(str, shapes))} on the inputs' device")
+    if positions.stride(-1) != 1 and s > 1:
+        raise AttnError(-2, "the positions of a sequence must be contiguous")
+    return positions.data_ptr(), positions.stride(0) if positions.dim() == 2 and b > 1 else 0
+
+
+def _check_norm_inputs(q, k, weights, d):
+    if q.dim() != k.dim() or q.dtype != k.dtype or q.device != k.device:
+        raise AttnError(-4, "q and k must have one layout, dtype and device")
+    for name, w in weights:
+        if w is not None and (tuple(w.shape) != (d,) or w.dtype != q.dtype or w.device != q.device or
+                              not w.is_contiguous()):
+            raise AttnError(-2, f"{name} must be a contiguous [{d}] tensor typed like q, on its device")
+
+
+def _used_on(stream, *tensors):
+    """Tensors allocated here for a call on a stream that was given: their
+    memory is not handed out again before that stream is done with them."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _like(name, t, ref):
+    if t.shape != ref.shape or t.dtype != ref.dtype or t.device != ref.device:
+        raise AttnError(-2, f"{name} must be shaped and typed like its input, on its device")
+
+
+def attn_qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, eps: float = 1e-6,
+                      interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """RMS norm of every query and key head and the rotary rotation, in one
+    pass, into the layout the attention reads.
+
+    q: [b, h, s, d] and k: [b, h_kv, s, d], or packed [total, h, d] and
+    [total, h_kv, d]; fp16 or bf16, any strides (multiples of 8 elements) with
+    contiguous heads, so views of a fused projection need no copy.
+    ``q_weight`` / ``k_weight`` [d] (None: no norm); ``cos`` / ``sin`` fp32
+    [table_len, rot / 2] (None: no rotation); ``positions`` int32 [b, s], [s]
+    or (packed) [total], None: 0..s-1.  ``interleaved``: adjacent pairs turn
+    instead of pairs (i, i + rot/2).  Negative positions are padding (zeros).
+    Returns (q_out, k_out), contiguous unless given."""
+    import torch
+    lib = load()
+    (b, h, s, d), qs = _as_dense("q", q)
+    (bk, hkv, sk, dk), ks = _as_dense("k", k)
+    if (bk, sk, dk) != (b, s, d):
+        raise AttnError(-2, f"shape mismatch q{tuple(q.shape)} k{tuple(k.shape)}")
+    _check_norm_inputs(q, k, (("q_weight", q_weight), ("k_weight", k_weight)), d)
+    dt = _dtype_code(q)
+    c, sn, rot, length = _rotation(cos, sin, q.device)
+    pos, pos_b = _positions(positions, b, s, q.dim() == 3, cos, q.device)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    _like("q_out", q_out, q)
+    _like("k_out", k_out, k)
+    _, qos = _as_dense("q_out", q_out)
+    _, kos = _as_dense("k_out", k_out)
+    with _OnDevice(q.device):
+        rc = lib.attn_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_weight.data_ptr() if q_weight is not None else None,
+                                   k_weight.data_ptr() if k_weight is not None else None, c, sn, pos,
+                                   q_out.data_ptr(), k_out.data_ptr(), qs, ks, qos, kos, b, h, hkv, s, d, rot, length,
+                                   pos_b, int(bool(interleaved)), float(eps), dt, _stream_handle(stream, q.device))
+    _check(rc, lib)
+    _used_on(stream, q_out, k_out)
+    return q_out, k_out
+
+
+def attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
+                          eps: float = 1e-6, interleaved: bool = False, dq=None, dk=None, workspace=None, stream=None):
+    """Gradients of attn_qk_norm_rope for the gradients of its outputs:
+    (dq, dk, dq_weight, dk_weight); the weights' gradients are fp32 [d], None
+    for a weight that is None.  ``dq`` / ``dk`` may be given (for example
+    slices of the fused projection's gradient), with any strides; ``workspace``
+    is a CUDA uint8 tensor of qk_norm_rope_bwd_workspace_bytes(d) bytes."""
+    import torch
+    lib = load()
+    (b, h, s, d), qs = _as_dense("q", q)
+    (bk, hkv, sk, dd), ks = _as_dense("k", k)
+    if (bk, sk, dd) != (b, s, d):
+        raise AttnError(-2, f"shape mismatch q{tuple(q.shape)} k{tuple(k.shape)}")
+    _check_norm_inputs(q, k, (("q_weight", q_weight), ("k_weight", k_weight)), d)
+    dt = _dtype_code(q)
+    _like("dq_out", dq_out, q)
+    _like("dk_out", dk_out, k)
+    _, gqs = _as_dense("dq_out", dq_out)
+    _, gks = _as_dense("dk_out", dk_out)
+    c, sn, rot, length = _rotation(cos, sin, q.device)
+    pos, pos_b = _positions(positions, b, s, q.dim() == 3, cos, q.device)
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if dk is None:
+        dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    _like("dq", dq, q)
+    _like("dk", dk, k)
+    _, dqs = _as_dense("dq", dq)
+    _, dks = _as_dense("dk", dk)
+    dwq = torch.empty(d, dtype=torch.float32, device=q.device) if q_weight is not None else None
+    dwk = torch.empty(d, dtype=torch.float32, device=q.device) if k_weight is not None else None
+    if workspace is None and (dwq is not None or dwk is not None):
+        workspace = torch.empty(qk_norm_rope_bwd_workspace_bytes(d), dtype=torch.uint8, device=q.device)
+    if workspace is not None and (workspace.device != q.device or not workspace.is_contiguous()):
+        raise AttnError(-2, "workspace must be a contiguous tensor on the inputs' device")
+    with _OnDevice(q.device):
+        rc = lib.attn_qk_norm_rope_bwd(dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(),
+                                       q_weight.data_ptr() if q_weight is not None else None,
+                                       k_weight.data_ptr() if k_weight is not None else None, c, sn, pos,
+                                       dq.data_ptr(), dk.data_ptr(), dwq.data_ptr() if dwq is not None else None,
+                                       dwk.data_ptr() if dwk is not None else None, gqs, gks, qs, ks, dqs, dks, b, h,
+                                       hkv, s, d, rot, length, pos_b, int(bool(interleaved)), float(eps), dt,
+                                       workspace.data_ptr() if workspace is not None else None,
+                                       workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                                       _stream_handle(stream, q.device))
+    _check(rc, lib)
+    _used_on(stream, dq, dk, dwq, dwk, workspace)
+    return dq, dk, dwq, dwk
+
+
+def qk_norm_rope_bwd_workspace_bytes(d: int) -> int:
+    lib = load()
+    return _check(int(lib.attn_qk_norm_rope_bwd_workspace_bytes(d)), lib)
+
+
+def _check_pools(k_pool, v_pool, k_scale, v_scale, block_table, cache_seqlens, b, hkv, d):
+    """The checks of a paged cache that need the tensors; returns (num_pages, page_size, pages_per_seq, scale_block)."""
+    import torch
+    dev = k_pool.device
+    if k_pool.dim() != 4 or tuple(k_pool.shape[2:]) != (hkv, d) or v_pool.shape != k_pool.shape or \
+            v_pool.dtype != k_pool.dtype:
+        raise AttnError(-2, f"pools {tuple(k_pool.shape)} / {tuple(v_pool.shape)} must be [num_pages, page_size, {hkv}, {d}]")
+    num_pages, page_size = k_pool.shape[:2]
+    if block_table.dim() != 2 or block_table.shape[0] != b or block_table.dtype != torch.int32:
+        raise AttnError(-2, "block_table must be int32 [b, pages_per_seq]")
+    if tuple(cache_seqlens.shape) != (b,) or cache_seqlens.dtype != torch.int32:
+        raise AttnError(-4, "cache_seqlens must be an int32 tensor of b elements")
+    block = 0
+    tensors = [("k_pool", k_pool), ("v_pool", v_pool), ("block_table", block_table), ("cache_seqlens", cache_seqlens)]
+    if (k_scale is None) != (v_scale is None):
+        raise AttnError(-1, "k_scale and v_scale must both be given or both be None")
+    if k_scale is not None:
+        if k_pool.dtype != torch.float8_e4m3fn:
+            raise AttnError(-4, "a cache with scales must be float8_e4m3fn")
+        if k_scale.dim() != 3 or tuple(k_scale.shape[:2]) != (num_pages, hkv) or v_scale.shape != k_scale.shape or \
+                k_scale.shape[2] < 1 or page_size % k_scale.shape[2] != 0:
+            raise AttnError(-2, "scales must be [num_pages, h_kv, page_size / scale_block]")
+        if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+            raise AttnError(-4, "scales must be fp32")
+        block = page_size // k_scale.shape[2]
+        tensors += [("k_scale", k_scale), ("v_scale", v_scale)]
+    for name, t in tensors:
+        if not t.is_cuda or t.device != dev or not t.is_contiguous():
+            raise AttnError(-2, f"{name} must be a contiguous CUDA tensor on one device")
+    return num_pages, page_size, block_table.shape[1], block
+
+
+def attn_kvcache_append_paged(k_new, v_new, k_pool, v_pool, cache_seqlens, block_table, cos=None, sin=None,
+                              interleaved: bool = False, k_scale=None, v_scale=None, new_seqlens=None, stream=None):
+    """Write new keys, rotated by their positions on the way, and values into
+    a paged cache, in place.
+
+    k_new / v_new: [b, h_kv, s_new, d] fp16 or bf16, any strides (multiples of
+    8 elements) with contiguous heads; k_pool / v_pool: [num_pages, page_size,
+    h_kv, d] of their dtype (the cache of attn_fwd_kvcache_paged), or
+    float8_e4m3fn with ``k_scale`` / ``v_scale`` fp32 [num_pages, h_kv,
+    page_size / scale_block] (the cache of attn_fwd_kvcache_paged_fp8).  Token
+    t of element e goes to position cache_seqlens[e] + t; ``new_seqlens`` int32
+    [b] says how many of a padded batch's tokens are there.  ``cos`` / ``sin``
+    fp32 [at least the capacity, rot / 2]; None: no rotation.  cache_seqlens is
+    not updated."""
+    import torch
+    lib = load()
+    if k_new.dim() != 4 or k_new.shape != v_new.shape:
+        raise AttnError(-2, f"k_new{tuple(k_new.shape)} and v_new{tuple(v_new.shape)} must be [b, h_kv, s_new, d]")
+    (b, hkv, s, d), ks = _as_dense("k_new", k_new)
+    _, vs = _as_dense("v_new", v_new)
+    dt = _dtype_code(k_new)
+    if v_new.dtype != k_new.dtype:
+        raise AttnError(-4, "k_new and v_new dtypes differ")
+    num_pages, page_size, pps, block = _check_pools(k_pool, v_pool, k_scale, v_scale, block_table, cache_seqlens, b,
+                                                    hkv, d)
+    if block == 0 and k_pool.dtype != k_new.dtype:
+        raise AttnError(-4, "a cache without scales must have the dtype of k_new")
+    if k_new.device != k_pool.device or v_new.device != k_pool.device:
+        raise AttnError(-2, "k_new, v_new and the pools must be on one device")
+    if new_seqlens is not None and (tuple(new_seqlens.shape) != (b,) or new_seqlens.dtype != torch.int32 or
+                                    new_seqlens.device != k_pool.device or not new_seqlens.is_contiguous()):
+        raise AttnError(-4, "new_seqlens must be an int32 tensor of b elements on the pools' device")
+    c, sn, rot, length = _rotation(cos, sin, k_pool.device)
+    with _OnDevice(k_pool.device):
+        rc = lib.attn_kvcache_append_paged(k_new.data_ptr(), v_new.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+                                           k_scale.data_ptr() if block else None,
+                                           v_scale.data_ptr() if block else None, cache_seqlens.data_ptr(),
+                                           new_seqlens.data_ptr() if new_seqlens is not None else None,
+                                           block_table.data_ptr(), c, sn, ks, vs, b, hkv, s, num_pages, page_size, pps,
+                                           block, d, rot, length, int(bool(interleaved)), dt,
+                                           _stream_handle(stream, k_pool.device))
+    _check(rc, lib)
+
+
+def kvcache_paged_fp8_workspace_bytes(b, h, h_kv, sq, d) -> int:
+    lib = load()
+    return _check(int(lib.attn_fwd_kvcache_paged_fp8_workspace_bytes(b, h, h_kv, sq, d)), lib)
+
+
+def attn_fwd_kvcache_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, cache_seqlens, block_table, causal: bool = False,
+                               scale: float | None = None, o=None, lse=None, workspace=None, stream=None):
+    """Attention of q [b, h, sq, d] (fp16 or bf16) over an e4m3 paged cache:
+    k_pool / v_pool float8_e4m3fn [num_pages, page_size, h_kv, d] with k_scale
+    / v_scale fp32 [num_pages, h_kv, page_size / scale_block], block_table
+    int32 [b, pages_per_seq].  Element e attends to its first cache_seqlens[e]
+    tokens (the new ones among them: append first); h / h_kv query heads share
+    a key head.  ``workspace``: a CUDA uint8 tensor of
+    kvcache_paged_fp8_workspace_bytes bytes.  Returns (o, lse)."""
+    import torch
+    lib = load()
+    if q.dim() != 4 or k_pool.dim() != 4:
+        raise AttnError(-2, "q must be [b, h, sq, d] and the pools [num_pages, page_size, h_kv, d]")
+    b, h, sq, d = q.shape
+    hkv = k_pool.shape[2]
+    dt = _dtype_code(q)
+    if k_scale is None or v_scale is None:
+        raise AttnError(-1, "k_scale and v_scale must be given")
+    num_pages, page_size, pps, block = _check_pools(k_pool, v_pool, k_scale, v_scale, block_table, cache_seqlens, b,
+                                                    hkv, d)
+    if not q.is_contiguous() or q.device != k_pool.device:
+        raise AttnError(-2, "q must be contiguous, on the pools' device")
+    if scale is None:
+        scale = 1.0 / float(d) ** 0.5
+    if o is None:
+        o = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((b, h, sq), dtype=torch.float32, device=q.device)
+    if o.shape != q.shape or o.dtype != q.dtype or not o.is_contiguous() or o.device != q.device:
+        raise AttnError(-2, "o must be a contiguous tensor shaped and typed like q, on its device")
+    if tuple(lse.shape) != (b, h, sq) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != q.device:
+        raise AttnError(-2, "lse must be contiguous fp32 [b, h, sq] on q's device")
+    if workspace is None:
+        workspace = torch.empty(kvcache_paged_fp8_workspace_bytes(b, h, hkv, sq, d), dtype=torch.uint8, device=q.device)
+    elif workspace.device != q.device or not workspace.is_contiguous():
+        raise AttnError(-2, "workspace must be a contiguous tensor on q's device")
+    with _OnDevice(q.device):
+        rc = lib.attn_fwd_kvcache_paged_fp8(q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(),
+                                            v_scale.data_ptr(), cache_seqlens.data_ptr(), block_table.data_ptr(),
+                                            o.data_ptr(), lse.data_ptr(), b, h, hkv, sq, num_pages, page_size, pps,
+                                            block, d, int(bool(causal)), float(scale), dt, workspace.data_ptr(),
+                                            workspace.numel() * workspace.element_size(),
+                                            _stream_handle(stream, q.device))
+    _check(rc, lib)
+    _used_on(stream, o, lse, workspace)
+    return o, lse

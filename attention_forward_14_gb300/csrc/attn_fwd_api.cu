@@ -16,7 +16,10 @@
 
 #include "attn_bwd_launch.h"
 #include "attn_fwd.h"
+#include "attn_kv8.h"
+#include "kv_append.h"
 #include "launch.h"
+#include "qk_norm_rope.h"
 #include "sched_ticket.h"
 
 namespace {
@@ -70,6 +73,7 @@ struct DeviceInfo {
     std::atomic<int> sched_pinned{-1};  // testing hook: every launch on this slot
     std::atomic<int> fwd_attr[kFwdInstances] = {};  // shared-memory opt-in set, per kernel instance
     std::atomic<int> bwd_attr[bwd::kBwdInstances] = {};
+    std::atomic<int> kv8_attr[kKv8Instances] = {};
 };
 DeviceInfo g_dev[kMaxDevices];
 
@@ -690,6 +694,111 @@ struct NoallocSlot {
 };
 NoallocSlot g_noalloc[kMaxDevices];
 
+// ---------------------------------------------------------------- q/k norm with rotation
+
+// What the rotation of a call is checked for: both tables or none, rot a
+// positive multiple of 16 up to d.
+int validate_rotation(const float *cos, const float *sin, int64_t rot, int64_t table_len, int64_t d)
+{
+    if ((cos == nullptr) != (sin == nullptr)) return fail(ATTN_ERR_NULL, "cos and sin must both be given or both be NULL");
+    if (!cos) return ATTN_OK;
+    if (rot < 16 || rot > d || rot % 16 != 0)
+        return fail(ATTN_ERR_SHAPE, "rot %lld is not a multiple of 16 in 16..%lld", (long long)rot, (long long)d);
+    if (table_len < 1 || table_len > kMaxSeq) return fail(ATTN_ERR_SHAPE, "table_len %lld not in 1..2^30", (long long)table_len);
+    if (!aligned(cos, 16) || !aligned(sin, 16)) return fail(ATTN_ERR_ALIGN, "cos and sin must be 16-byte aligned");
+    return ATTN_OK;
+}
+
+// Strides (elements) of a [b, heads, s, d] tensor whose d values are contiguous.
+int validate_strides(const int64_t *st, const char *what)
+{
+    if (!st) return fail(ATTN_ERR_NULL, "strides of %s are NULL", what);
+    for (int i = 0; i < 3; ++i)
+        if (st[i] < 0 || st[i] > (int64_t(1) << 46) || st[i] % 8 != 0)
+            return fail(ATTN_ERR_ALIGN, "strides of %s must be non-negative multiples of 8 elements (16 bytes)", what);
+    return ATTN_OK;
+}
+
+// First and last byte of a 16-bit [b, heads, s, d] tensor with strides.
+struct Extent {
+    uintptr_t lo, hi;
+};
+Extent extent_of(const void *p, const int64_t *st, int64_t b, int64_t h, int64_t s, int64_t d)
+{
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    const int64_t last = (b - 1) * st[0] + (h - 1) * st[1] + (s - 1) * st[2] + d;
+    return {lo, lo + static_cast<uintptr_t>(last) * 2};
+}
+
+// Rows of an output must not coincide: no stride of an axis longer than one
+// may be shorter than a row.
+int validate_out_strides(const int64_t *st, int64_t b, int64_t h, int64_t s, int64_t d, const char *what)
+{
+    const int64_t n[3] = {b, h, s};
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && st[i] < d) return fail(ATTN_ERR_SHAPE, "rows of %s overlap (stride %lld)", what, (long long)st[i]);
+    return ATTN_OK;
+}
+
+// The checks that the forward and the backward share; fills *p but for the
+// tensors.
+int norm_rope_common(NormRopeParams *p, const float *cos, const float *sin, const int32_t *positions, int64_t b,
+                     int64_t h, int64_t h_kv, int64_t s, int64_t d, int64_t rot, int64_t table_len, int64_t pos_stride,
+                     int interleaved, float eps, int dtype, bool *nothing)
+{
+    if (b < 0 || h < 0 || h_kv < 0 || s < 0) return fail(ATTN_ERR_SHAPE, "negative size");
+    if (s > INT32_MAX || h > (1 << 20) || h_kv > (1 << 20) || (s > 0 && b > INT32_MAX / s))
+        return fail(ATTN_ERR_SHAPE, "b * s above 2^31-1 or more than 2^20 heads");
+    if (d != 64 && d != 128) return fail(ATTN_ERR_HEADDIM, "head dim %lld not supported (64 or 128)", (long long)d);
+    if (dtype != ATTN_FP16 && dtype != ATTN_BF16) return fail(ATTN_ERR_DTYPE, "dtype %d is not fp16 (0) or bf16 (1)", dtype);
+    if (!std::isfinite(eps) || eps < 0.f) return fail(ATTN_ERR_SCALE, "eps must be finite and not negative");
+    int rc = validate_rotation(cos, sin, rot, table_len, d);
+    if (rc != ATTN_OK) return rc;
+    if (positions && !aligned(positions, 4)) return fail(ATTN_ERR_ALIGN, "positions must be 4-byte aligned");
+    if (positions && pos_stride < 0) return fail(ATTN_ERR_SHAPE, "negative stride of positions");
+    if (cos && !positions && s > table_len)
+        return fail(ATTN_ERR_SHAPE, "the tables have %lld positions, fewer than the %lld tokens", (long long)table_len, (long long)s);
+    if (b * s > INT32_MAX / (h + h_kv + 2)) return fail(ATTN_ERR_SHAPE, "more than 2^31-1 rows");
+    *nothing = b * s == 0 || h + h_kv == 0;
+    p->cos = cos;
+    p->sin = sin;
+    p->pos = cos ? positions : nullptr;
+    p->pos_b = pos_stride;
+    p->tokens = b * s;
+    p->s = s;
+    p->table_len = cos ? static_cast<int>(table_len) : 0;
+    p->rot = cos ? static_cast<int>(rot) : 0;
+    p->interleaved = interleaved != 0;
+    p->eps = eps;
+    return ATTN_OK;
+}
+
+int set_side(NormRopeSide *sd, const void *x, const void *w, const int64_t *xs, void *out, const int64_t *os, int64_t b,
+             int64_t heads, int64_t s, int64_t d, const char *what)
+{
+    sd->heads = static_cast<int>(heads);
+    if (heads == 0 || b * s == 0) return ATTN_OK;
+    if (!x || !out) return fail(ATTN_ERR_NULL, "%s or its output is NULL", what);
+    int rc = validate_strides(xs, what);
+    if (rc == ATTN_OK) rc = validate_strides(os, "an output");
+    if (rc == ATTN_OK) rc = validate_out_strides(os, b, heads, s, d, "an output");
+    if (rc != ATTN_OK) return rc;
+    if (!aligned(x, 16) || !aligned(out, 16) || (w && !aligned(w, 16)))
+        return fail(ATTN_ERR_ALIGN, "%s, its weight and its output must be 16-byte aligned", what);
+    // each unit reads its rows before it writes them: in place is fine when
+    // every row is written where it was read
+    const bool same = (b == 1 || xs[0] == os[0]) && (heads == 1 || xs[1] == os[1]) && (s == 1 || xs[2] == os[2]);
+    if (x == out && !same) return fail(ATTN_ERR_SHAPE, "%s and its output share memory with other strides", what);
+    sd->x = x;
+    sd->w = w;
+    sd->out = out;
+    sd->xb = xs[0], sd->xh = xs[1], sd->xs = xs[2];
+    sd->ob = os[0], sd->oh = os[1], sd->os = os[2];
+    return ATTN_OK;
+}
+
+int64_t norm_rope_workspace(int64_t d) { return int64_t(kNormRopeMaxBlocks) * 2 * d * 4; }
+
 }  // namespace
 
 extern "C" {
@@ -1146,6 +1255,273 @@ int attn_fwd_fp8(const void *q, const void *k, const void *v, void *o, float *ls
         e = causal ? launch_fwd<128, __nv_fp8_e4m3, true>(a) : launch_fwd<128, __nv_fp8_e4m3, false>(a);
     if (e != cudaSuccess) return cuda_fail(e, "kernel launch (e4m3)");
     return ATTN_OK;
+}
+
+// ---------------------------------------------------------------- operators around the attention
+
+int attn_qk_norm_rope(const void *q, const void *k, const void *q_weight, const void *k_weight, const float *cos,
+                      const float *sin, const int32_t *positions, void *q_out, void *k_out, const int64_t *q_strides,
+                      const int64_t *k_strides, const int64_t *q_out_strides, const int64_t *k_out_strides, int64_t b,
+                      int64_t h, int64_t h_kv, int64_t s, int64_t d, int64_t rot, int64_t table_len,
+                      int64_t pos_stride, int interleaved, float eps, int dtype, void *stream)
+{
+    g_err.clear();
+    NormRopeParams p;
+    bool nothing = false;
+    int rc = norm_rope_common(&p, cos, sin, positions, b, h, h_kv, s, d, rot, table_len, pos_stride, interleaved, eps,
+                              dtype, &nothing);
+    if (rc != ATTN_OK || nothing) return rc;
+    if ((rc = set_side(&p.side[0], q, q_weight, q_strides, q_out, q_out_strides, b, h, s, d, "q")) != ATTN_OK) return rc;
+    if ((rc = set_side(&p.side[1], k, k_weight, k_strides, k_out, k_out_strides, b, h_kv, s, d, "k")) != ATTN_OK) return rc;
+    DeviceInfo *di = nullptr;
+    if ((rc = device_info(&di)) != ATTN_OK) return rc;
+    p.status = di->status;
+    const cudaError_t e = launch_norm_rope(p, static_cast<int>(d), dtype == ATTN_BF16, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "launch (q/k norm with rotation)");
+}
+
+int64_t attn_qk_norm_rope_bwd_workspace_bytes(int64_t d)
+{
+    g_err.clear();
+    if (d != 64 && d != 128) return fail(ATTN_ERR_HEADDIM, "head dim %lld not supported (64 or 128)", (long long)d);
+    return norm_rope_workspace(d);
+}
+
+int attn_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const void *q, const void *k, const void *q_weight,
+                          const void *k_weight, const float *cos, const float *sin, const int32_t *positions, void *dq,
+                          void *dk, float *dq_weight, float *dk_weight, const int64_t *dq_out_strides,
+                          const int64_t *dk_out_strides, const int64_t *q_strides, const int64_t *k_strides,
+                          const int64_t *dq_strides, const int64_t *dk_strides, int64_t b, int64_t h, int64_t h_kv,
+                          int64_t s, int64_t d, int64_t rot, int64_t table_len, int64_t pos_stride, int interleaved,
+                          float eps, int dtype, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    g_err.clear();
+    NormRopeParams p;
+    bool nothing = false;
+    int rc = norm_rope_common(&p, cos, sin, positions, b, h, h_kv, s, d, rot, table_len, pos_stride, interleaved, eps,
+                              dtype, &nothing);
+    if (rc != ATTN_OK) return rc;
+    if ((dq_weight && !q_weight) || (dk_weight && !k_weight))
+        return fail(ATTN_ERR_NULL, "the gradient of a norm weight needs that weight");
+    if (!aligned(dq_weight, 4) || !aligned(dk_weight, 4)) return fail(ATTN_ERR_ALIGN, "weight gradients must be 4-byte aligned");
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool grads = dq_weight || dk_weight;
+    if (nothing) {  // sums over no rows
+        if (!grads) return ATTN_OK;
+        DeviceInfo *di = nullptr;
+        if ((rc = device_info(&di)) != ATTN_OK) return rc;
+        cudaError_t e = cudaSuccess;
+        if (dq_weight) e = cudaMemsetAsync(dq_weight, 0, static_cast<size_t>(d) * 4, st);
+        if (e == cudaSuccess && dk_weight) e = cudaMemsetAsync(dk_weight, 0, static_cast<size_t>(d) * 4, st);
+        return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "zero the weights' gradients");
+    }
+    // without a norm the gradient does not depend on the input
+    const void *xq = q_weight ? q : dq_out, *xk = k_weight ? k : dk_out;
+    const int64_t *xqs = q_weight ? q_strides : dq_out_strides, *xks = k_weight ? k_strides : dk_out_strides;
+    if ((rc = set_side(&p.side[0], xq, q_weight, xqs, dq, dq_strides, b, h, s, d, "q")) != ATTN_OK) return rc;
+    if ((rc = set_side(&p.side[1], xk, k_weight, xks, dk, dk_strides, b, h_kv, s, d, "k")) != ATTN_OK) return rc;
+    const void *gs[2] = {dq_out, dk_out};
+    const int64_t *gst[2] = {dq_out_strides, dk_out_strides};
+    for (int i = 0; i < 2; ++i) {
+        NormRopeSide &sd = p.side[i];
+        if (sd.heads == 0) continue;
+        if (!gs[i]) return fail(ATTN_ERR_NULL, "dq_out or dk_out is NULL");
+        if ((rc = validate_strides(gst[i], "an output's gradient")) != ATTN_OK) return rc;
+        if (!aligned(gs[i], 16)) return fail(ATTN_ERR_ALIGN, "dq_out and dk_out must be 16-byte aligned");
+        sd.g = gs[i];
+        sd.gb = gst[i][0], sd.gh = gst[i][1], sd.gs = gst[i][2];
+    }
+    if (grads) {
+        if (!workspace) return fail(ATTN_ERR_NULL, "workspace is NULL");
+        if (!aligned(workspace, 16)) return fail(ATTN_ERR_ALIGN, "workspace must be 16-byte aligned");
+        if (workspace_bytes < norm_rope_workspace(d))
+            return fail(ATTN_ERR_SHAPE, "workspace too small: %lld bytes, need %lld", (long long)workspace_bytes,
+                        (long long)norm_rope_workspace(d));
+        p.dw_part = static_cast<float *>(workspace);
+        p.dw[0] = dq_weight;
+        p.dw[1] = dk_weight;
+    }
+    DeviceInfo *di = nullptr;
+    if ((rc = device_info(&di)) != ATTN_OK) return rc;
+    p.status = di->status;
+    const cudaError_t e = launch_norm_rope_bwd(p, static_cast<int>(d), dtype == ATTN_BF16, di->sm_count, st);
+    return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "launch (q/k norm with rotation, backward)");
+}
+
+// The page and block sizes of a paged cache; `block` 0: a 16-bit pool.
+static int validate_pages(int64_t num_pages, int64_t page_size, int64_t pages_per_seq, int64_t block)
+{
+    if (page_size < 16 || page_size % 16 != 0)
+        return fail(ATTN_ERR_SHAPE, "page_size %lld is not a positive multiple of 16", (long long)page_size);
+    if (num_pages < 1 || pages_per_seq < 1) return fail(ATTN_ERR_SHAPE, "num_pages and pages_per_seq must be at least 1");
+    if (num_pages > INT32_MAX / page_size) return fail(ATTN_ERR_SHAPE, "the pool holds more than 2^31-1 tokens");
+    if (pages_per_seq > kMaxSeq / page_size) return fail(ATTN_ERR_SHAPE, "pages_per_seq * page_size above 2^30");
+    if (block != 0 && ((block != 16 && block != 32 && block != 64 && block != 128) || page_size % block != 0))
+        return fail(ATTN_ERR_SHAPE, "scale_block %lld is not 16, 32, 64 or 128, or does not divide page_size %lld",
+                    (long long)block, (long long)page_size);
+    return ATTN_OK;
+}
+
+static int log2_of(int64_t v)
+{
+    int n = 0;
+    while ((int64_t(1) << n) < v) ++n;
+    return n;
+}
+
+int attn_kvcache_append_paged(const void *k_new, const void *v_new, void *k_pool, void *v_pool, float *k_scale,
+                              float *v_scale, const int32_t *cache_seqlens, const int32_t *new_seqlens,
+                              const int32_t *block_table, const float *cos, const float *sin,
+                              const int64_t *k_strides, const int64_t *v_strides, int64_t b, int64_t h_kv,
+                              int64_t s_new, int64_t num_pages, int64_t page_size, int64_t pages_per_seq,
+                              int64_t scale_block, int64_t d, int64_t rot, int64_t table_len, int interleaved,
+                              int dtype, void *stream)
+{
+    g_err.clear();
+    const bool e4m3 = scale_block != 0;
+    int rc = validate_pages(num_pages, page_size, pages_per_seq, scale_block);
+    if (rc != ATTN_OK) return rc;
+    if (b < 0 || h_kv < 0 || s_new < 0) return fail(ATTN_ERR_SHAPE, "negative size");
+    if (s_new > kMaxSeq || h_kv > (1 << 20) || (b > 0 && s_new > INT32_MAX / b))
+        return fail(ATTN_ERR_SHAPE, "b * s_new above 2^31-1 or more than 2^20 heads");
+    if (d != 64 && d != 128) return fail(ATTN_ERR_HEADDIM, "head dim %lld not supported (64 or 128)", (long long)d);
+    if (dtype != ATTN_FP16 && dtype != ATTN_BF16) return fail(ATTN_ERR_DTYPE, "dtype %d is not fp16 (0) or bf16 (1)", dtype);
+    if ((rc = validate_rotation(cos, sin, rot, table_len, d)) != ATTN_OK) return rc;
+    const int64_t cap = pages_per_seq * page_size;
+    if (cos && table_len < cap)
+        return fail(ATTN_ERR_SHAPE, "the tables have %lld positions, fewer than the %lld of a request's pages",
+                    (long long)table_len, (long long)cap);
+    KvAppendParams p;
+    p.nblk = e4m3 ? (s_new + scale_block - 2) / scale_block + 1 : 0;
+    if (b * h_kv > 0 && (b * s_new > INT32_MAX / (2 * h_kv) || b * p.nblk > INT32_MAX / h_kv))
+        return fail(ATTN_ERR_SHAPE, "more than 2^31-1 rows");
+    if (b * h_kv * s_new == 0) return ATTN_OK;
+    if (!k_new || !v_new || !k_pool || !v_pool) return fail(ATTN_ERR_NULL, "k_new, v_new, k_pool or v_pool is NULL");
+    if (!cache_seqlens || !block_table) return fail(ATTN_ERR_NULL, "cache_seqlens or block_table is NULL");
+    if (e4m3 && (!k_scale || !v_scale)) return fail(ATTN_ERR_NULL, "an e4m3 pool needs k_scale and v_scale");
+    if (!e4m3 && (k_scale || v_scale)) return fail(ATTN_ERR_SHAPE, "a 16-bit pool has no scales");
+    if ((rc = validate_strides(k_strides, "k_new")) != ATTN_OK) return rc;
+    if ((rc = validate_strides(v_strides, "v_new")) != ATTN_OK) return rc;
+    if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16))
+        return fail(ATTN_ERR_ALIGN, "k_new, v_new, k_pool and v_pool must be 16-byte aligned");
+    if (!aligned(cache_seqlens, 4) || !aligned(new_seqlens, 4) || !aligned(block_table, 4) || !aligned(k_scale, 4) ||
+        !aligned(v_scale, 4))
+        return fail(ATTN_ERR_ALIGN, "lengths, block_table and scales must be 4-byte aligned");
+    // what is read must not lie in what is written, nor one pool in the other
+    const uintptr_t pool_bytes = static_cast<uintptr_t>(num_pages * page_size * h_kv * d) * (e4m3 ? 1 : 2);
+    const Extent news[2] = {extent_of(k_new, k_strides, b, h_kv, s_new, d), extent_of(v_new, v_strides, b, h_kv, s_new, d)};
+    const uintptr_t pools[2] = {reinterpret_cast<uintptr_t>(k_pool), reinterpret_cast<uintptr_t>(v_pool)};
+    for (const Extent &n : news)
+        for (const uintptr_t c : pools)
+            if (n.lo < c + pool_bytes && c < n.hi) return fail(ATTN_ERR_SHAPE, "k_new / v_new overlap k_pool / v_pool");
+    if (pools[0] < pools[1] + pool_bytes && pools[1] < pools[0] + pool_bytes)
+        return fail(ATTN_ERR_SHAPE, "k_pool and v_pool overlap");
+    DeviceInfo *di = nullptr;
+    if ((rc = device_info(&di)) != ATTN_OK) return rc;
+    p.x[0] = k_new, p.x[1] = v_new;
+    p.xb[0] = k_strides[0], p.xh[0] = k_strides[1], p.xs[0] = k_strides[2];
+    p.xb[1] = v_strides[0], p.xh[1] = v_strides[1], p.xs[1] = v_strides[2];
+    p.pool[0] = k_pool, p.pool[1] = v_pool;
+    p.scale[0] = k_scale, p.scale[1] = v_scale;
+    p.seqlens = cache_seqlens;
+    p.new_seqlens = new_seqlens;
+    p.block_table = block_table;
+    p.cos = cos, p.sin = sin;
+    p.b = b, p.s = s_new, p.num_pages = num_pages, p.pages_per_seq = pages_per_seq;
+    p.heads = static_cast<int>(h_kv);
+    p.page_size = static_cast<int>(page_size);
+    p.block_shift = e4m3 ? log2_of(scale_block) : 0;
+    p.rot = cos ? static_cast<int>(rot) : 0;
+    p.interleaved = interleaved != 0;
+    const cudaError_t e = launch_kv_append(p, static_cast<int>(d), dtype == ATTN_BF16, e4m3, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "launch (paged cache append)");
+}
+
+// Parts of the items that two or more CTAs share: at most two a CTA.
+static int64_t kv8_workspace(int64_t d) { return int64_t(2) * kKv8MaxCtas * kKv8Tile * (d + 2) * 4; }
+
+int64_t attn_fwd_kvcache_paged_fp8_workspace_bytes(int64_t b, int64_t h, int64_t h_kv, int64_t sq, int64_t d)
+{
+    g_err.clear();
+    if (b < 0 || h < 0 || h_kv < 0 || sq < 0 || sq > kMaxSeq)
+        return fail(ATTN_ERR_SHAPE, "invalid workspace query of the e4m3 paged attention");
+    if (d != 64 && d != 128) return fail(ATTN_ERR_HEADDIM, "head dim %lld not supported (64 or 128)", (long long)d);
+    return kv8_workspace(d);
+}
+
+int attn_fwd_kvcache_paged_fp8(const void *q, const void *k_pool, const void *v_pool, const float *k_scale,
+                               const float *v_scale, const int32_t *cache_seqlens, const int32_t *block_table, void *o,
+                               float *lse, int64_t b, int64_t h, int64_t h_kv, int64_t sq, int64_t num_pages,
+                               int64_t page_size, int64_t pages_per_seq, int64_t scale_block, int64_t d, int causal,
+                               float scale, int dtype, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    g_err.clear();
+    int rc = validate_pages(num_pages, page_size, pages_per_seq, scale_block);
+    if (rc != ATTN_OK) return rc;
+    if (scale_block == 0) return fail(ATTN_ERR_SHAPE, "scale_block must be 16, 32, 64 or 128");
+    const int64_t cap = pages_per_seq * page_size;
+    if ((rc = validate_sizes(b, h, sq, cap, d, scale, dtype)) != ATTN_OK) return rc;
+    if (h_kv < 0 || (h > 0 && (h_kv == 0 || h % h_kv != 0)))
+        return fail(ATTN_ERR_SHAPE, "h %lld is not a multiple of h_kv %lld", (long long)h, (long long)h_kv);
+    if (b * h * sq == 0) return ATTN_OK;
+    const int64_t group = h / h_kv;
+    if (group * sq > INT32_MAX - 16) return fail(ATTN_ERR_SHAPE, "too many query rows of one key head");
+    if (!q || !k_pool || !v_pool || !o) return fail(ATTN_ERR_NULL, "q, k_pool, v_pool or o is NULL");
+    if (!k_scale || !v_scale || !cache_seqlens || !block_table)
+        return fail(ATTN_ERR_NULL, "k_scale, v_scale, cache_seqlens or block_table is NULL");
+    if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(o, 16))
+        return fail(ATTN_ERR_ALIGN, "q, k_pool, v_pool and o must be 16-byte aligned");
+    if (!aligned(lse, 4) || !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(cache_seqlens, 4) || !aligned(block_table, 4))
+        return fail(ATTN_ERR_ALIGN, "lse, scales, cache_seqlens and block_table must be 4-byte aligned");
+    const int64_t need = kv8_workspace(d);
+    if (!workspace) return fail(ATTN_ERR_NULL, "workspace is NULL (%lld bytes needed)", (long long)need);
+    if (!aligned(workspace, 16)) return fail(ATTN_ERR_ALIGN, "workspace must be 16-byte aligned");
+    if (workspace_bytes < need)
+        return fail(ATTN_ERR_SHAPE, "workspace too small: %lld bytes, need %lld", (long long)workspace_bytes, (long long)need);
+    DeviceInfo *di = nullptr;
+    if ((rc = device_info(&di)) != ATTN_OK) return rc;
+    Kv8LaunchArgs a;
+    const int64_t pool = num_pages * page_size;
+    // boxes of 16 tokens of one head: rows of d bytes, in the swizzle of that width
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(h_kv), static_cast<cuuint64_t>(pool)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(h_kv * d)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(d), 1, 16};
+    const CUtensorMapSwizzle sw = d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    if ((rc = encode_map(&a.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, k_pool, dims, strides, box, sw, "e4m3 pool")) != ATTN_OK) return rc;
+    if ((rc = encode_map(&a.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, v_pool, dims, strides, box, sw, "e4m3 pool")) != ATTN_OK) return rc;
+    Kv8Params &p = a.p;
+    p.q = q;
+    p.o = o;
+    p.lse = lse;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.seqlens = cache_seqlens;
+    p.block_table = block_table;
+    p.status = di->status;
+    p.o_part = static_cast<float *>(workspace);
+    p.ml_part = p.o_part + int64_t(2) * kKv8MaxCtas * kKv8Tile * d;
+    p.sl2e = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+    p.b = static_cast<int32_t>(b);
+    p.h_kv = static_cast<int32_t>(h_kv);
+    p.group = static_cast<int32_t>(group);
+    p.sq = static_cast<int32_t>(sq);
+    p.rows = static_cast<int32_t>(group * sq);
+    p.tiles = (p.rows + kKv8Tile - 1) / kKv8Tile;
+    p.cap = static_cast<int32_t>(cap);
+    p.page_size = static_cast<int32_t>(page_size);
+    p.pages_per_seq = static_cast<int32_t>(pages_per_seq);
+    p.num_pages = static_cast<int32_t>(num_pages);
+    p.block_shift = log2_of(scale_block);
+    p.causal = causal != 0;
+    p.timeout_ns = kDefaultTimeoutNs;
+    // no more CTAs than units of 128 keys in full caches
+    const double units = static_cast<double>(b) * h_kv * p.tiles * static_cast<double>((cap + 127) / 128);
+    a.grid = di->sm_count < kKv8MaxCtas ? di->sm_count : kKv8MaxCtas;
+    if (units < a.grid) a.grid = static_cast<int>(units);
+    a.stream = static_cast<cudaStream_t>(stream);
+    a.attr_ready = di->kv8_attr;
+    const cudaError_t e = launch_kv8(a, static_cast<int>(d), dtype == ATTN_BF16);
+    return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "kernel launch (e4m3 paged cache)");
 }
 
 const char *attn_last_error(void) { return g_err.c_str(); }

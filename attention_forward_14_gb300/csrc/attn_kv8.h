@@ -1,0 +1,46 @@
+// Attention over an e4m3 paged cache with a scale for each block of tokens
+// and head: parameters and launches.
+#pragma once
+
+#include <atomic>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+namespace attn {
+
+struct Kv8Params {
+    const void *q;               // [b, h, sq, d] fp16 / bf16
+    void *o;                     // the same
+    float *lse;                  // [b, h, sq] or nullptr
+    const float *k_scale, *v_scale;  // [num_pages, h_kv, page_size >> block_shift]
+    const int32_t *seqlens;      // [b]
+    const int32_t *block_table;  // [b, pages_per_seq]
+    uint32_t *status;
+    float *o_part;               // [2 * grid][16][d]: parts of the items that several CTAs share
+    float *ml_part;              // [2 * grid][16][2]: their reference (log2) and sum
+    float sl2e;                  // scale * log2(e)
+    int32_t b, h_kv, group;      // group = h / h_kv query heads of one key head
+    int32_t sq, rows;            // rows = group * sq query rows of one key head
+    int32_t tiles;               // ceil(rows / 16)
+    int32_t cap;                 // pages_per_seq * page_size
+    int32_t page_size, pages_per_seq, num_pages, block_shift;
+    int32_t causal;
+    uint64_t timeout_ns;
+};
+
+constexpr int kKv8MaxCtas = 512;  // CTAs of a launch at most (sizes the workspace)
+constexpr int kKv8Instances = 4;  // head dim {64, 128} x {fp16, bf16}
+constexpr int kKv8Tile = 16;      // query rows of an item
+
+struct Kv8LaunchArgs {
+    CUtensorMap k, v;
+    Kv8Params p;
+    int grid;
+    cudaStream_t stream;
+    std::atomic<int> *attr_ready;  // the library's flags, for the current device: shared-memory opt-in set, per instance
+};
+
+cudaError_t launch_kv8(const Kv8LaunchArgs &a, int d, bool bf16);
+
+}  // namespace attn

@@ -398,6 +398,182 @@ int64_t attn_bwd_varlen_workspace_bytes(int64_t batch, int64_t h,
                                         int64_t total_q, int64_t max_seqlen_q,
                                         int64_t d);
 
+/*
+ * Norm of queries and keys with the position rotation, in one pass: what a
+ * model does between its projections and this library's attention.  For
+ * every head x (d values) of every token of q and of k:
+ *   y = w * x * (mean(x^2) + eps)^(-1/2)      (q_weight / k_weight; NULL: y = x)
+ *   out = R(position) y                       (cos, sin; NULL: out = y)
+ * R turns the pairs of the first `rot` values: (a, b) -> (a cos - b sin,
+ * b cos + a sin), with pairs (i, i + rot/2), or adjacent ones (2i, 2i + 1)
+ * when `interleaved` is nonzero; values rot..d-1 are left.  fp32 arithmetic,
+ * one rounding at the end.
+ *
+ *   q, q_out   : [b, h, s, d] of dtype by strides, 16-byte aligned;
+ *   k, k_out   : [b, h_kv, s, d], the same.  The strides arrays hold the
+ *                strides of b, of the head and of s, in elements (multiples
+ *                of 8); the d values are contiguous.  So q and k can be views
+ *                of a fused projection's output, and the outputs have the
+ *                layout that the attention reads.  A packed batch [total, h,
+ *                d] is b = 1, s = total.  An output may be its input (the
+ *                same strides); otherwise it must not overlap an input.
+ *                h or h_kv may be 0.
+ *   q_weight,
+ *   k_weight   : [d] of dtype, 16-byte aligned, or NULL.
+ *   cos, sin   : fp32 [table_len, rot / 2], 16-byte aligned, or both NULL.
+ *                rot is a multiple of 16, at most d.
+ *   positions  : device int32, token (b, s) at positions[b * pos_stride + s]
+ *                (pos_stride 0: the same for every b), or NULL: position s.
+ *                A token whose position is negative is padding: its outputs
+ *                (and gradients) are 0.  So are those of a position at or
+ *                past table_len, which also records ATTN_STATUS_POSITION.
+ *   eps        : finite, not negative.
+ * Returns ATTN_OK or a negative ATTN_ERR_* code.
+ */
+int attn_qk_norm_rope(const void *q, const void *k, const void *q_weight,
+                      const void *k_weight, const float *cos, const float *sin,
+                      const int32_t *positions, void *q_out, void *k_out,
+                      const int64_t *q_strides, const int64_t *k_strides,
+                      const int64_t *q_out_strides,
+                      const int64_t *k_out_strides, int64_t b, int64_t h,
+                      int64_t h_kv, int64_t s, int64_t d, int64_t rot,
+                      int64_t table_len, int64_t pos_stride, int interleaved,
+                      float eps, int dtype, void *stream);
+
+/*
+ * Gradients of attn_qk_norm_rope.  With dy = R^T dout, n = x * r, r =
+ * (mean(x^2) + eps)^(-1/2):
+ *   dw = sum over tokens and heads of dy * n      (fp32 [d])
+ *   dx = r * (w * dy - n * mean(w * dy * n))      (without a norm: dx = dy)
+ *   dq_out, dk_out : gradients of the outputs, by strides.
+ *   q, k           : the forward's inputs (not read for a NULL weight).
+ *   dq, dk         : gradients of the inputs, by strides; may be dq_out /
+ *                    dk_out, or q / k, with the same strides.
+ *   dq_weight,
+ *   dk_weight      : fp32 [d], or NULL when not wanted.
+ *   workspace      : caller-owned device scratch, 16-byte aligned, of at least
+ *                    attn_qk_norm_rope_bwd_workspace_bytes(d) bytes (NULL
+ *                    when no weight's gradient is wanted); its contents on
+ *                    entry do not matter.  Calls on different streams need
+ *                    different workspaces.
+ * The sums are added in a fixed order: equal calls give equal bits.
+ */
+int attn_qk_norm_rope_bwd(const void *dq_out, const void *dk_out,
+                          const void *q, const void *k, const void *q_weight,
+                          const void *k_weight, const float *cos,
+                          const float *sin, const int32_t *positions,
+                          void *dq, void *dk, float *dq_weight,
+                          float *dk_weight, const int64_t *dq_out_strides,
+                          const int64_t *dk_out_strides,
+                          const int64_t *q_strides, const int64_t *k_strides,
+                          const int64_t *dq_strides, const int64_t *dk_strides,
+                          int64_t b, int64_t h, int64_t h_kv, int64_t s,
+                          int64_t d, int64_t rot, int64_t table_len,
+                          int64_t pos_stride, int interleaved, float eps,
+                          int dtype, void *workspace, int64_t workspace_bytes,
+                          void *stream);
+
+/* Bytes of workspace attn_qk_norm_rope_bwd needs, or a negative code. */
+int64_t attn_qk_norm_rope_bwd_workspace_bytes(int64_t d);
+
+/*
+ * Append to a paged cache, the keys rotated by their positions on the way.
+ *   k_new, v_new : [b, h_kv, s_new, d] of dtype by strides (elements,
+ *                  multiples of 8; d contiguous), 16-byte aligned.
+ *   k_pool,
+ *   v_pool       : [num_pages, page_size, h_kv, d], contiguous, 16-byte
+ *                  aligned: of dtype (scale_block 0; the pool that
+ *                  attn_fwd_kvcache_paged reads), or e4m3 (scale_block 16,
+ *                  32, 64 or 128; the pool of attn_fwd_kvcache_paged_fp8).
+ *   k_scale,
+ *   v_scale      : fp32 [num_pages, h_kv, page_size / scale_block] of an
+ *                  e4m3 pool, else NULL.
+ *   cache_seqlens: device int32 [b], tokens cached before this call (read,
+ *                  not updated; clamped to the capacity pages_per_seq *
+ *                  page_size).
+ *   new_seqlens  : device int32 [b], how many of the s_new tokens are there
+ *                  (a padded batch; clamped to 0..s_new), or NULL: all.
+ *   block_table  : device int32 [b, pages_per_seq], as for
+ *                  attn_fwd_kvcache_paged.  No two entries may name one page.
+ *   page_size    : a positive multiple of 16.
+ *   cos, sin     : fp32 [table_len, rot / 2], as for attn_qk_norm_rope, or
+ *                  both NULL: no rotation.  table_len is at least the
+ *                  capacity.
+ * Token t of element e goes to logical position L + t (L the clamped
+ * cached length), which is also the position its key is rotated by; values
+ * are not rotated.  Tokens at or past the capacity, and pages outside the
+ * pool, are not written.
+ *
+ * e4m3: a block's scale is the smallest power of two, at least 2^-64, that
+ * brings the largest finite |x| of the block's tokens to at most 448; a
+ * stored value is x / scale rounded to e4m3 (an infinity is stored as +-448,
+ * NaN as NaN).  A block that holds tokens of an earlier append keeps its
+ * scale when that is large enough; otherwise its scale becomes the new
+ * tokens' and the earlier tokens are stored again as their value under it.
+ * A block that the new tokens begin takes no account of what it held.
+ * Returns ATTN_OK or a negative ATTN_ERR_* code.
+ */
+int attn_kvcache_append_paged(const void *k_new, const void *v_new,
+                              void *k_pool, void *v_pool, float *k_scale,
+                              float *v_scale, const int32_t *cache_seqlens,
+                              const int32_t *new_seqlens,
+                              const int32_t *block_table, const float *cos,
+                              const float *sin, const int64_t *k_strides,
+                              const int64_t *v_strides, int64_t b,
+                              int64_t h_kv, int64_t s_new, int64_t num_pages,
+                              int64_t page_size, int64_t pages_per_seq,
+                              int64_t scale_block, int64_t d, int64_t rot,
+                              int64_t table_len, int interleaved, int dtype,
+                              void *stream);
+
+/*
+ * Attention over an e4m3 paged cache: attn_fwd_kvcache_paged (without its
+ * append) on K = k_scale * k_pool, V = v_scale * v_pool, with one scale for
+ * each block of scale_block tokens and key head, and h / h_kv query heads
+ * sharing a key head.
+ *   q, o         : [b, h, sq, d] of dtype, contiguous, 16-byte aligned.
+ *   k_pool,
+ *   v_pool       : e4m3 [num_pages, page_size, h_kv, d], 16-byte aligned.
+ *   k_scale,
+ *   v_scale      : fp32 [num_pages, h_kv, page_size / scale_block], finite,
+ *                  not negative.
+ *   cache_seqlens: device int32 [b], the tokens to attend to, the new ones
+ *                  among them (clamped to 0..pages_per_seq * page_size).
+ *   block_table  : device int32 [b, pages_per_seq]; a page index outside
+ *                  the pool reads as zeros.
+ *   h            : a multiple of h_kv; query head i reads key head
+ *                  i / (h / h_kv).
+ *   page_size    : a positive multiple of 16 and of scale_block; scale_block
+ *                  is 16, 32, 64 or 128.
+ *   lse          : fp32 [b, h, sq] or NULL.
+ *   workspace    : caller-owned device scratch, 16-byte aligned, of at least
+ *                  attn_fwd_kvcache_paged_fp8_workspace_bytes(...) bytes; its
+ *                  contents on entry do not matter.  Calls on different
+ *                  streams need different workspaces.
+ * With `causal`, query i of element e sees keys j <= i + L - sq.  A row that
+ * sees no key gets O = 0 and LSE = -inf.  Slots at or past L are not read
+ * into the result.  The work is dealt out by the lengths on the device, so
+ * batches of unequal lengths need no split count.  P is rounded to fp16
+ * before the product with V; sums and statistics are fp32.
+ * Returns ATTN_OK or a negative ATTN_ERR_* code.
+ */
+int attn_fwd_kvcache_paged_fp8(const void *q, const void *k_pool,
+                               const void *v_pool, const float *k_scale,
+                               const float *v_scale,
+                               const int32_t *cache_seqlens,
+                               const int32_t *block_table, void *o, float *lse,
+                               int64_t b, int64_t h, int64_t h_kv, int64_t sq,
+                               int64_t num_pages, int64_t page_size,
+                               int64_t pages_per_seq, int64_t scale_block,
+                               int64_t d, int causal, float scale, int dtype,
+                               void *workspace, int64_t workspace_bytes,
+                               void *stream);
+
+/* Bytes of workspace attn_fwd_kvcache_paged_fp8 needs, or a negative code. */
+int64_t attn_fwd_kvcache_paged_fp8_workspace_bytes(int64_t b, int64_t h,
+                                                   int64_t h_kv, int64_t sq,
+                                                   int64_t d);
+
 /* Thread-local message describing the last non-OK return on this thread
  * ("" if none).  The pointer stays valid until the next call on the thread. */
 const char *attn_last_error(void);
@@ -411,7 +587,9 @@ const char *attn_last_error(void);
  *   code ATTN_STATUS_SCHED_COLLISION (2) a launch found its schedule slot
  *                                        held by another (attn_fwd_varlen);
  *   code ATTN_STATUS_BOUNDS (3)          checked build: a computed index was
- *                                        outside its bounds (see below).
+ *                                        outside its bounds (see below);
+ *   code ATTN_STATUS_POSITION (4)        attn_qk_norm_rope met a position past
+ *                                        the end of its tables.
  * attn_fwd_status synchronises the current device, copies the status into
  * out[0..3] = {code, block, warp, site} (out may be NULL) and returns code
  * (0 = nothing recorded, <0 = CUDA error while reading).
@@ -423,6 +601,7 @@ const char *attn_last_error(void);
 #define ATTN_STATUS_TIMEOUT 1
 #define ATTN_STATUS_SCHED_COLLISION 2
 #define ATTN_STATUS_BOUNDS 3
+#define ATTN_STATUS_POSITION 4
 int attn_fwd_status(uint32_t *out);
 int attn_fwd_status_clear(void);
 int attn_fwd_debug_status(void);
