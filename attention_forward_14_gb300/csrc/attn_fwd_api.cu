@@ -1438,7 +1438,10 @@ int attn_kvcache_append_paged(const void *k_new, const void *v_new, void *k_pool
 }
 
 // Parts of the items that two or more CTAs share: at most two a CTA.
-static int64_t kv8_workspace(int64_t d) { return int64_t(2) * kKv8MaxCtas * kKv8Tile * (d + 2) * 4; }
+static int64_t kv8_workspace(int64_t d) 
+{
+    return int64_t(2) * kKv8MaxCtas * kKv8Heads * kKv8Tile * (d + 2) * 4 + kKv8MaxCtas * static_cast<int64_t>(sizeof(Kv8Cut));
+}
 
 int64_t attn_fwd_kvcache_paged_fp8_workspace_bytes(int64_t b, int64_t h, int64_t h_kv, int64_t sq, int64_t d)
 {
@@ -1481,15 +1484,18 @@ int attn_fwd_kvcache_paged_fp8(const void *q, const void *k_pool, const void *v_
     DeviceInfo *di = nullptr;
     if ((rc = device_info(&di)) != ATTN_OK) return rc;
     Kv8LaunchArgs a;
+    Kv8Params &p = a.p;
     const int64_t pool = num_pages * page_size;
-    // boxes of 16 tokens of one head: rows of d bytes, in the swizzle of that width
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(h_kv), static_cast<cuuint64_t>(pool)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(h_kv * d)};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(d), 1, 16};
+    p.heads = kKv8Heads;
+    while (h_kv % p.heads != 0) p.heads /= 2;
+    // [head][token][d]: boxes of p.heads heads and 32 tokens, or 16 where 32 could straddle two pages, which land
+    // head by head in rows of d bytes, in the swizzle of that width
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(pool), static_cast<cuuint64_t>(h_kv)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(h_kv * d), static_cast<cuuint64_t>(d)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(d), page_size % 32 == 0 ? 32u : 16u, static_cast<cuuint32_t>(p.heads)};
     const CUtensorMapSwizzle sw = d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
     if ((rc = encode_map(&a.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, k_pool, dims, strides, box, sw, "e4m3 pool")) != ATTN_OK) return rc;
     if ((rc = encode_map(&a.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, v_pool, dims, strides, box, sw, "e4m3 pool")) != ATTN_OK) return rc;
-    Kv8Params &p = a.p;
     p.q = q;
     p.o = o;
     p.lse = lse;
@@ -1499,11 +1505,13 @@ int attn_fwd_kvcache_paged_fp8(const void *q, const void *k_pool, const void *v_
     p.block_table = block_table;
     p.status = di->status;
     p.o_part = static_cast<float *>(workspace);
-    p.ml_part = p.o_part + int64_t(2) * kKv8MaxCtas * kKv8Tile * d;
+    p.ml_part = p.o_part + int64_t(2) * kKv8MaxCtas * kKv8Heads * kKv8Tile * d;
+    p.cut = reinterpret_cast<Kv8Cut *>(p.ml_part + int64_t(2) * kKv8MaxCtas * kKv8Heads * kKv8Tile * 2);
     p.sl2e = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
     p.b = static_cast<int32_t>(b);
     p.h_kv = static_cast<int32_t>(h_kv);
-    p.group = static_cast<int32_t>(group);
+    p.head_groups = p.h_kv / p.heads;
+    p.unit_keys = 32 * kKv8Heads / p.heads;
     p.sq = static_cast<int32_t>(sq);
     p.rows = static_cast<int32_t>(group * sq);
     p.tiles = (p.rows + kKv8Tile - 1) / kKv8Tile;
@@ -1514,8 +1522,8 @@ int attn_fwd_kvcache_paged_fp8(const void *q, const void *k_pool, const void *v_
     p.block_shift = log2_of(scale_block);
     p.causal = causal != 0;
     p.timeout_ns = kDefaultTimeoutNs;
-    // no more CTAs than units of 128 keys in full caches
-    const double units = static_cast<double>(b) * h_kv * p.tiles * static_cast<double>((cap + 127) / 128);
+    // no more CTAs than units in full caches
+    const double units = static_cast<double>(b) * p.head_groups * p.tiles * static_cast<double>((cap + p.unit_keys - 1) / p.unit_keys);
     a.grid = di->sm_count < kKv8MaxCtas ? di->sm_count : kKv8MaxCtas;
     if (units < a.grid) a.grid = static_cast<int>(units);
     a.stream = static_cast<cudaStream_t>(stream);

@@ -9,6 +9,13 @@
 
 namespace attn {
 
+// An item that a CTA begins and later CTAs go on with.
+struct Kv8Cut {
+    int32_t parts;        // CTAs that have a part (0: there is no such item)
+    int32_t second;       // 1: the item is not this CTA's first
+    int32_t b, hg, tile;  // batch element, group of key heads, tile of query rows
+};
+
 struct Kv8Params {
     const void *q;               // [b, h, sq, d] fp16 / bf16
     void *o;                     // the same
@@ -17,11 +24,15 @@ struct Kv8Params {
     const int32_t *seqlens;      // [b]
     const int32_t *block_table;  // [b, pages_per_seq]
     uint32_t *status;
-    float *o_part;               // [2 * grid][16][d]: parts of the items that several CTAs share
-    float *ml_part;              // [2 * grid][16][2]: their reference (log2) and sum
+    float *o_part;               // [2 * grid][8][16][d]: parts of the items that several CTAs share
+    float *ml_part;              // [2 * grid][8][16][2]: their reference (log2) and sum
+    Kv8Cut *cut;                 // [grid]
     float sl2e;                  // scale * log2(e)
-    int32_t b, h_kv, group;      // group = h / h_kv query heads of one key head
-    int32_t sq, rows;            // rows = group * sq query rows of one key head
+    int32_t b, h_kv;
+    int32_t heads;               // key heads that a CTA works on at a time: 8, 4, 2 or 1, a divisor of h_kv
+    int32_t head_groups;         // h_kv / heads
+    int32_t unit_keys;           // 32 * 8 / heads
+    int32_t sq, rows;            // rows = (h / h_kv) * sq query rows of one key head
     int32_t tiles;               // ceil(rows / 16)
     int32_t cap;                 // pages_per_seq * page_size
     int32_t page_size, pages_per_seq, num_pages, block_shift;
@@ -29,8 +40,9 @@ struct Kv8Params {
     uint64_t timeout_ns;
 };
 
-constexpr int kKv8MaxCtas = 512;  // CTAs of a launch at most (sizes the workspace)
+constexpr int kKv8MaxCtas = 160;  // CTAs of a launch at most (sizes the workspace)
 constexpr int kKv8Instances = 4;  // head dim {64, 128} x {fp16, bf16}
+constexpr int kKv8Heads = 8;       // key heads of an item at most
 constexpr int kKv8Tile = 16;      // query rows of an item
 
 struct Kv8LaunchArgs {
