@@ -1514,7 +1514,8 @@ int attn_fwd_kvcache_paged_fp8(const void *q, const void *k_pool, const void *v_
     p.unit_keys = 32 * kKv8Heads / p.heads;
     p.sq = static_cast<int32_t>(sq);
     p.rows = static_cast<int32_t>(group * sq);
-    p.tiles = (p.rows + kKv8Tile - 1) / kKv8Tile;
+    p.tile_rows = p.rows <= 8 ? 8 : kKv8Tile;
+    p.tiles = (p.rows + p.tile_rows - 1) / p.tile_rows;
     p.cap = static_cast<int32_t>(cap);
     p.page_size = static_cast<int32_t>(page_size);
     p.pages_per_seq = static_cast<int32_t>(pages_per_seq);

@@ -8,7 +8,7 @@
 // `heads` (8, 4, 2 or 1) consecutive key heads, 8 / heads warps to a head.  A
 // cached token's heads lie side by side, so this is what makes a CTA's reads
 // contiguous (8 heads of 128 values: 1 KB; one head's 128 bytes at that
-// stride reached 2.2 of 6.8 TB/s).  An item is 16 query rows of such a group
+// stride reached 2.2 of 6.8 TB/s).  An item is 8 or 16 query rows of such a group
 // of heads of one batch element; a unit is the 32 * 8 / heads keys that the
 // warps take together.  The units of all items, in order, are dealt to the
 // CTAs in equal contiguous shares, from the lengths that the device holds:
@@ -19,17 +19,22 @@
 // A CTA.  A producer warp copies a unit's K and V rows of all the heads with
 // one TMA copy each ([head][key][d] in shared memory, swizzled) and the
 // blocks' scales, a few units ahead and across items.  The consumers of one
-// head meet at an item's end only.  Per 32 keys a warp computes S = Q K^T
-// (16 x 32) and O += P V with fp16 matrix instructions on e4m3 values
-// converted to fp16 (exact) in registers.  The order of the head's values in a
-// dot product is free, so a lane takes 32 contiguous ones (d = 128) of its
-// key's row in two 16-byte loads; the columns of O are dealt likewise.
-//
-// Types.  Q enters the product as fp16: fp16 inputs as they are, bf16 inputs
-// times a power of two for each row that puts the row's largest value at
-// 2^14, which keeps all 8 significant bits of every value down to 2^-29 of
-// the largest.  P is rounded to fp16 (2^-11 relative) between 2^-24 and
-// 2^14.  Sums and statistics are fp32.
+// head meet at an item's end only.  Per 32 keys a warp computes S^T = K Q^T
+// and O^T += V^T P^T: keys, and values of the head, are the 16 rows of a
+// matrix instruction and the query rows its 8 columns (one or two sets of
+// them), so that few query rows waste little.
+//   K and V enter as fp16, converted (exactly) in registers.  The order of
+//   the head's values in a dot product is free, so a lane takes 32 contiguous
+//   ones (d = 128) of a key's row in two 16-byte loads.
+//   Q enters as fp16: fp16 inputs as they are, bf16 inputs times a power of
+//   two for each row that puts the row's largest value at 2^14, which keeps
+//   all 8 significant bits of every value down to 2^-21 of the largest, and
+//   rounds smaller ones at 2^-39 of it.
+//   P is rounded to fp16 (2^-11 relative, between 2^-14 and 2^14) and
+//   transposed in registers.
+// (e4m3 products on these matrix instructions are no way round the
+// conversions: they are made of the same conversions and two fp16 products,
+// 560 clocks for 16 of them against 224 for the fp16 products they replace.)
 //
 // Softmax, in log2: x = ks scale log2(e) (q . k8) + log2(vs).  P = 2^(x - m +
 // 10) carries the value scale, so O needs no product with it, and the sum of
@@ -47,7 +52,7 @@ namespace {
 
 constexpr int kWarps = 8;                         // consumers
 constexpr int kThreads = (kWarps + 4) * 32;       // and a warpgroup of which one warp copies
-constexpr int kConsumerRegs = 232, kProducerRegs = 40;  // 256 * 232 + 128 * 40 = 384 * 168
+constexpr int kConsumerRegs = 216, kProducerRegs = 72;  // 256 * 216 + 128 * 72 = 384 * 168
 constexpr int kStepKeys = 32;                     // keys of a warp's step
 constexpr float kOffset = 10.f, kSlack = 4.f;
 enum : uint32_t { SITE_KV8_FULL = 40, SITE_KV8_EMPTY = 41 };
@@ -58,20 +63,37 @@ struct Kv8Cfg {
     static constexpr int STAGE = 2 * kWarps * KBYTES;      // K of all warps, then V
     static constexpr int STAGES = D == 128 ? 2 : 4;        // 128 KB in flight
     static constexpr int O_OFF = STAGES * STAGE;           // where the warps of one head meet [warps][8 rows][D]
-    static constexpr int ML_OFF = O_OFF + kWarps * 8 * D * 4;     // [warps][16] float2
-    static constexpr int SC_OFF = ML_OFF + kWarps * 16 * 8;       // [STAGES][warps] scales: K, K, V, V
+    static constexpr int ML_OFF = O_OFF + kWarps * 8 * D * 4;     // [warps][8] float2
+    static constexpr int SC_OFF = ML_OFF + kWarps * 8 * 8;        // [STAGES][warps] scales: K, K, V, V
     static constexpr int BAR_OFF = SC_OFF + kWarps * STAGES * 16; // [STAGES] full, then empty
     static constexpr int CTL_OFF = BAR_OFF + 2 * STAGES * 8;
     static constexpr int SMEM = CTL_OFF + 16 + 1024;       // +1 KiB for alignment
     static_assert(SMEM <= 232448, "shared memory budget");
 };
 
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1)
+// c += A B: A 16 x 16, B 16 x 8, fp16.
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1)
 {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// An 8 x 8 tile of 16-bit values, two of a row to a lane, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t v)
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// fp16 of the e4m3 values in the low and in the high half of a word.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
 }
 
 __device__ __forceinline__ void cp_async4(uint32_t dst, const float *src)
@@ -222,7 +244,7 @@ struct Seen {
 __device__ __forceinline__ Seen seen_keys(const Kv8Params &p, const Place &c)
 {
     if (!p.causal) return {c.len, c.len};
-    const int r0 = c.tile * kKv8Tile, r1 = min(r0 + kKv8Tile, p.rows) - 1;
+    const int r0 = c.tile * p.tile_rows, r1 = min(r0 + p.tile_rows, p.rows) - 1;
     const bool wraps = r0 / p.sq != r1 / p.sq;  // the rows of one query head are consecutive
     const int i0 = wraps ? 0 : r0 % p.sq, i1 = wraps ? p.sq - 1 : r1 % p.sq;
     return {max(c.len - p.sq + i1 + 1, 0), max(c.len - p.sq + i0 + 1, 0)};
@@ -249,7 +271,7 @@ __device__ __forceinline__ void store4(T *o, float4 v)
     *reinterpret_cast<uint2 *>(o) = make_uint2(Pair<T>::put(v.x, v.y), Pair<T>::put(v.z, v.w));
 }
 
-template <int D, typename T>
+template <int D, typename T, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_kv8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const __grid_constant__ Kv8Params p)
@@ -258,8 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int STAGES = C::STAGES;
     constexpr int KS = D / 16;      // k-steps of S, and words of a lane's share of a K row
     constexpr int VW = D / 32;      // words of a lane's share of a V row
-    constexpr int NO = D / 8;       // column tiles of O
-    constexpr bool BF16 = Elem<T>::BF16;
+    constexpr int NO = D / 16;      // row tiles of O^T
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw_addr = smem_addr(smem_raw);
     const uint32_t base = (raw_addr + 1023u) & ~1023u;
@@ -292,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Place cur = place_of(p, u0);
 
     auto wait = [&](uint32_t bar, uint32_t parity, uint32_t site) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
         const uint64_t t0 = global_timer_ns();
         while (true) {
             for (int i = 0; i < 64; ++i)
@@ -313,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Lane 4 w + 2 kv + half fetches the scale of consumer w's 16 keys
         // `half`, of K or V; the lanes of each share's first head copy.
         regs_dec<kProducerRegs>();
-        if (warp != kWarps) return;
+        if (warp == kWarps) {
         const int half = lane & 1, kv = (lane >> 1) & 1, w = lane >> 2;
         const int hw = w & (p.heads - 1), kshare = w >> head_shift;
         const float *scales = kv ? p.v_scale : p.k_scale;
@@ -365,8 +386,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // wait (bounded) for the last copies, so that none lands after the CTA
         for (uint32_t n = issued > STAGES ? issued - STAGES : 0u; n < issued; ++n)
             drain_wait(full_bar(n % STAGES), (n / STAGES) & 1u, p.timeout_ns);
-        return;
-    }
+        }
+    } else {
     regs_inc<kConsumerRegs>();
 
     // ---------------------------------------------------------------- consumers
@@ -378,344 +399,360 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float4 *sc_ptr = reinterpret_cast<const float4 *>(smem + C::SC_OFF + warp * 16);
     uint32_t used = 0u;
     bool ok = true;
-    uint32_t qa[KS][4];
-    float acc[NO][4];
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, c0 = 0.f, c1 = 0.f;
-    int lim0 = 0, lim1 = 0;
-    Seen seen{0, 0};
-    for (int it = 0; it < n_units; ++it) {
-        if (it == 0 || cur.j == 0) {  // an item begins
-            seen = seen_keys(p, cur);
-            const int r = cur.tile * kKv8Tile + g;
-            float f[2] = {1.f, 1.f};
+    // A lane's share: of keys, g and g + 8 of each 16; of query rows, 2 t and
+    // 2 t + 1 of each 8; of O's columns, 2 NO from 2 NO g on.
+    uint32_t qb[NT][KS][2];
+    float acc[NT][NO][4];   // [.][.][0], [1]: an even column of rows 2 t, 2 t + 1; [2], [3]: the odd one after it
+    float m[NT][2], l[NT][2], coef[NT][2];
+    int lim[NT][2];
+    // One step of 32 keys from k0 on, in stage st.  PARTLY: some query row
+    // does not see some of the keys.
+    Place at = cur;
+    auto step = [&](int k0, uint32_t st, auto partly) __attribute__((always_inline)) {
+        constexpr bool PARTLY = decltype(partly)::value;
+        const uint8_t *ks_at = mine + st * C::STAGE, *vs_at = ks_at + kWarps * C::KBYTES;
+        const float4 sc = sc_ptr[st * kWarps];
+        // the scales of the two halves; a V scale of 0 is a block of zeros
+        float lv[2], ivs[2];
+        bool vzero[2];
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                const int rr = r + 8 * hh;
-                uint32_t w[KS * 2];
-                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) +
-                                                                   row_at(p, cur.b, cur.hg * p.heads + hw, rr < p.rows ? rr : 0) * D +
-                                                                   t * (D / 4));
-#pragma unroll
-                for (int i = 0; i < KS / 2; ++i) {
-                    const uint4 v = rr < p.rows ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-                    w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-                }
-                if constexpr (BF16) {
-                    uint32_t mx = 0u;  // largest magnitude of the row, as the bits of a non-negative float
-#pragma unroll
-                    for (int i = 0; i < KS * 2; ++i) mx = max(mx, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-                    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    const int e = max(static_cast<int>(mx >> 7) - 127, -100);
-                    const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
-                    f[hh] = __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
-#pragma unroll
-                    for (int i = 0; i < KS * 2; ++i) {
-                        const float2 v = Pair<T>::get(w[i]);
-                        w[i] = Pair<__half>::put(v.x * up, v.y * up);
-                    }
-                }
-#pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    qa[s][hh] = w[2 * s];
-                    qa[s][2 + hh] = w[2 * s + 1];
-                }
-            }
-            c0 = p.sl2e * f[0];
-            c1 = p.sl2e * f[1];
-            lim0 = lim1 = cur.len;
-            if (p.causal) {
-                lim0 = cur.len - p.sq + r % p.sq + 1;
-                lim1 = cur.len - p.sq + (r + 8) % p.sq + 1;
-            }
-            m0 = m1 = -INFINITY;
-            l0 = l1 = 0.f;
-#pragma unroll
-            for (int i = 0; i < NO; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+        for (int h = 0; h < 2; ++h) {
+            float vs = h ? sc.w : sc.z;
+            vzero[h] = vs < 1.1754944e-38f;
+            vs = vzero[h] ? 1.f : vs;
+            lv[h] = lg2_approx(vs);
+            ivs[h] = rcp_approx(vs);
         }
-        const int k0 = cur.j * p.unit_keys + kshare * kStepKeys;
-        const uint32_t st = used % STAGES;
-        const bool loaded = cur.j * p.unit_keys < seen.end;  // the unit has a stage
-        if (ok && loaded) ok = __all_sync(0xffffffffu, wait(full_bar(st), (used / STAGES) & 1u, SITE_KV8_FULL));
-        if (ok && k0 < seen.end) {
-            const uint8_t *ks_at = mine + st * C::STAGE, *vs_at = ks_at + kWarps * C::KBYTES;
-            const float4 sc = sc_ptr[st * kWarps];
-            // S: four tiles of eight keys
-            float s[4][4];
+        // S^T: two tiles of 16 keys
+        float s[2][NT][4];
+        {
+            uint32_t w0[2][KS], w1[2][KS];  // of keys g and g + 8
 #pragma unroll
-            for (int n = 0; n < 4; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int c = 0; c < KS / 4; ++c) {  // 16 bytes of the lane's share of each key's row
-                uint32_t w[4][4];
+                for (int c = 0; c < KS / 4; ++c) {  // 16 bytes of the lane's share of each
+                    const uint8_t *src = ks_at + (h ? second : 0u) +
+                                         (D == 128 ? g * 128 + (((2 * t + c) ^ g) << 4) : g * 64 + ((t ^ ((g >> 1) & 3)) << 4));
+                    const uint4 a = *reinterpret_cast<const uint4 *>(src);
+                    const uint4 b = *reinterpret_cast<const uint4 *>(src + 8 * D);  // the swizzle repeats
+                    w0[h][4 * c] = a.x, w0[h][4 * c + 1] = a.y, w0[h][4 * c + 2] = a.z, w0[h][4 * c + 3] = a.w;
+                    w1[h][4 * c] = b.x, w1[h][4 * c + 1] = b.y, w1[h][4 * c + 2] = b.z, w1[h][4 * c + 3] = b.w;
+                }
+            // two sums for each tile, so that a product waits for its own only
+            float c2[2][NT][2][4];
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const int row = (n & 1) * 8 + g;
-                    const uint4 a = *reinterpret_cast<const uint4 *>(
-                        ks_at + (n >= 2 ? second : 0u) + (D == 128 ? row * 128 + (((2 * t + c) ^ g) << 4) : row * 64 + ((t ^ ((row >> 1) & 3)) << 4)));
-                    w[n][0] = a.x, w[n][1] = a.y, w[n][2] = a.z, w[n][3] = a.w;
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) c2[h][nt][0][i] = c2[h][nt][1][i] = 0.f;
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t a0, a1, a2, a3;
+                    e4m3x4_to_f16(w0[h][k], a0, a2);
+                    e4m3x4_to_f16(w1[h][k], a1, a3);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_f16(c2[h][nt][k & 1], a0, a1, a2, a3, qb[nt][k][0], qb[nt][k][1]);
                 }
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int n = 0; n < 4; ++n)
-                        mma16816(s[n], qa[4 * c + k][0], qa[4 * c + k][1], qa[4 * c + k][2], qa[4 * c + k][3],
-                                 e4m3x2_to_f16x2(w[n][k]), e4m3x2_to_f16x2(w[n][k] >> 16));
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        s[h][nt][i] = fmaf(c2[h][nt][0][i] + c2[h][nt][1][i], coef[nt][i & 1] * (h ? sc.y : sc.x), lv[h]);
+        }
+        if constexpr (PARTLY) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (k0 + 16 * h + g + 8 * (i >> 1) >= lim[nt][i & 1]) s[h][nt][i] = -INFINITY;
+        }
+        bool over = false;
+        float top[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                top[nt][i] = fmaxf(max3f(s[0][nt][i], s[0][nt][2 + i], s[1][nt][i]), s[1][nt][2 + i]);
+                over = over || top[nt][i] > m[nt][i] + kSlack;
             }
-            // the scales of the two halves; a V scale of 0 is a block of zeros
-            float lv[2], ivs[2];
-            bool vzero[2];
+        if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float vs = h ? sc.w : sc.z;
-                vzero[h] = vs < 1.1754944e-38f;
-                vs = vzero[h] ? 1.f : vs;
-                lv[h] = lg2_approx(vs);
-                ivs[h] = rcp_approx(vs);
-            }
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const float ks = n < 2 ? sc.x : sc.y, a0 = c0 * ks, a1 = c1 * ks;
-                s[n][0] = fmaf(s[n][0], a0, lv[n >> 1]);
-                s[n][1] = fmaf(s[n][1], a0, lv[n >> 1]);
-                s[n][2] = fmaf(s[n][2], a1, lv[n >> 1]);
-                s[n][3] = fmaf(s[n][3], a1, lv[n >> 1]);
-            }
-            const bool partly = k0 + kStepKeys > seen.all;  // some row does not see some of these keys
-            if (partly) {
+                for (int i = 0; i < 2; ++i) {
+                    float n = top[nt][i];
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const int k = k0 + n * 8 + 2 * t;
-                    s[n][0] = k < lim0 ? s[n][0] : -INFINITY;
-                    s[n][1] = k + 1 < lim0 ? s[n][1] : -INFINITY;
-                    s[n][2] = k < lim1 ? s[n][2] : -INFINITY;
-                    s[n][3] = k + 1 < lim1 ? s[n][3] : -INFINITY;
-                }
-            }
-            const float t0 = max3f(max3f(s[0][0], s[0][1], s[1][0]), max3f(s[1][1], s[2][0], s[2][1]), fmaxf(s[3][0], s[3][1]));
-            const float t1 = max3f(max3f(s[0][2], s[0][3], s[1][2]), max3f(s[1][3], s[2][2], s[2][3]), fmaxf(s[3][2], s[3][3]));
-            if (__any_sync(0xffffffffu, t0 > m0 + kSlack || t1 > m1 + kSlack)) {
-                float n0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
-                float n1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
-                n0 = fmaxf(m0, fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, 2)));
-                n1 = fmaxf(m1, fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, 2)));
-                const float f0 = n0 == m0 ? 1.f : ex2_approx(m0 - n0);
-                const float f1 = n1 == m1 ? 1.f : ex2_approx(m1 - n1);
-                m0 = n0;
-                m1 = n1;
-                l0 *= f0;
-                l1 *= f1;
+                    for (int off = 4; off < 32; off <<= 1) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, off));
+                    n = fmaxf(n, m[nt][i]);
+                    const float f = n == m[nt][i] ? 1.f : ex2_approx(m[nt][i] - n);
+                    m[nt][i] = n;
+                    l[nt][i] *= f;
 #pragma unroll
-                for (int i = 0; i < NO; ++i) {
-                    acc[i][0] *= f0;
-                    acc[i][1] *= f0;
-                    acc[i][2] *= f1;
-                    acc[i][3] *= f1;
-                }
-            }
-            const float b0 = m0 == -INFINITY ? 0.f : m0 - kOffset, b1 = m1 == -INFINITY ? 0.f : m1 - kOffset;
-            uint32_t pa[2][4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const float p0 = ex2_approx(s[2 * h + n][0] - b0), p1 = ex2_approx(s[2 * h + n][1] - b0);
-                    const float p2 = ex2_approx(s[2 * h + n][2] - b1), p3 = ex2_approx(s[2 * h + n][3] - b1);
-                    sum0 += p0 + p1;
-                    sum1 += p2 + p3;
-                    pa[h][2 * n] = vzero[h] ? 0u : Pair<__half>::put(p0, p1);
-                    pa[h][2 * n + 1] = vzero[h] ? 0u : Pair<__half>::put(p2, p3);
-                }
-                l0 = fmaf(sum0, ivs[h], l0);
-                l1 = fmaf(sum1, ivs[h], l1);
-            }
-            // O += P V, 16 keys at a time
-            const int tail = cur.len - k0;  // rows of V from `tail` on are not keys: zero them
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t v[4][VW];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = 2 * t + (i & 1) + 8 * (i >> 1);
-                    if constexpr (D == 128) {
-                        const uint4 a = *reinterpret_cast<const uint4 *>(vs_at + (h ? second : 0u) + row * 128 + ((g ^ (row & 7)) << 4));
-                        v[i][0] = a.x, v[i][1] = a.y, v[i][2] = a.z, v[i][3] = a.w;
-                    } else {
-                        const uint2 a = *reinterpret_cast<const uint2 *>(
-                            vs_at + (h ? second : 0u) + row * 64 + ((((g >> 1) ^ ((row >> 1) & 3)) << 4) | ((g & 1) << 3)));
-                        v[i][0] = a.x, v[i][1] = a.y;
-                    }
-                    if (tail < kStepKeys) {
-#pragma unroll
-                        for (int w = 0; w < VW; ++w) v[i][w] = row + 16 * h < tail ? v[i][w] : 0u;
+                    for (int j = 0; j < NO; ++j) {
+                        acc[nt][j][i] *= f;
+                        acc[nt][j][2 + i] *= f;
                     }
                 }
-                if (partly) {
-                    // A NaN among V must reach the rows that see its key and
-                    // no other, but a row that does not still multiplies it,
-                    // by 0: take it out of the product and put it into the
-                    // rows that see it (the product of what each row sees
-                    // with where V is NaN counts them).
-                    uint32_t any = 0u;
+        }
+        uint32_t pb[2][NT][2];  // P^T: two keys of query row g
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0] - kOffset;
+            const float b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1] - kOffset;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float p0 = ex2_approx(s[h][nt][0] - b0), p1 = ex2_approx(s[h][nt][1] - b1);
+                const float p2 = ex2_approx(s[h][nt][2] - b0), p3 = ex2_approx(s[h][nt][3] - b1);
+                l[nt][0] = fmaf(p0 + p2, ivs[h], l[nt][0]);
+                l[nt][1] = fmaf(p1 + p3, ivs[h], l[nt][1]);
+                pb[h][nt][0] = transposed(vzero[h] ? 0u : Pair<__half>::put(p0, p1));
+                pb[h][nt][1] = transposed(vzero[h] ? 0u : Pair<__half>::put(p2, p3));
+            }
+        }
+        // O^T += V^T P^T, 16 keys at a time
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t v[4][VW];  // of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = 2 * t + (i & 1) + 8 * (i >> 1);
+                const uint8_t *at = vs_at + (h ? second : 0u);
+                if constexpr (D == 128) {
+                    const uint4 a = *reinterpret_cast<const uint4 *>(at + row * 128 + ((g ^ (row & 7)) << 4));
+                    v[i][0] = a.x, v[i][1] = a.y, v[i][2] = a.z, v[i][3] = a.w;
+                } else {
+                    const uint2 a = *reinterpret_cast<const uint2 *>(
+                        at + row * 64 + ((((g >> 1) ^ ((row >> 1) & 3)) << 4) | ((g & 1) << 3)));
+                    v[i][0] = a.x, v[i][1] = a.y;
+                }
+            }
+            if constexpr (PARTLY) {
+                // Rows from the length on are no keys: zero them.  A NaN
+                // among V must reach the query rows that see its key and
+                // no other, but a row that does not still multiplies it,
+                // by 0: take it out of the product and put it into the
+                // rows that see it (the product of where V is NaN with
+                // what each row sees counts them).
+                uint32_t any = 0u;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int w = 0; w < VW; ++w) {
+                        if (k0 + 16 * h + 2 * t + (i & 1) + 8 * (i >> 1) >= at.len) v[i][w] = 0u;
+                        any |= nan_bytes(v[i][w]);
+                    }
+                if (__any_sync(0xffffffffu, any != 0u)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        // limit of query row g of the set: lane (g >> 1) of the shares has it
+                        const int l0 = __shfl_sync(0xffffffffu, lim[nt][0], g >> 1), l1 = __shfl_sync(0xffffffffu, lim[nt][1], g >> 1);
+                        const int lg = (g & 1) ? l1 : l0, k = k0 + 16 * h + 2 * t;
+                        const uint32_t see0 = (k < lg ? 0x3C00u : 0u) | (k + 1 < lg ? 0x3C000000u : 0u);
+                        const uint32_t see1 = (k + 8 < lg ? 0x3C00u : 0u) | (k + 9 < lg ? 0x3C000000u : 0u);
+#pragma unroll
+                        for (int j = 0; j < NO; ++j) {
+                            const uint32_t sel = j & 1 ? 0x7362u : 0x5140u;
+                            uint32_t ind[4];  // e4m3's 1 where V is NaN
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) ind[i] = (nan_bytes(v[i][j >> 1]) >> 7) * 0x38u;
+                            const uint32_t a = __byte_perm(ind[0], ind[1], sel), b = __byte_perm(ind[2], ind[3], sel);
+                            float c[4] = {0.f, 0.f, 0.f, 0.f};
+                            mma_f16(c, e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(a >> 16), e4m3x2_to_f16x2(b), e4m3x2_to_f16x2(b >> 16),
+                                    see0, see1);
+#pragma unroll
+                            for (int k2 = 0; k2 < 4; ++k2)
+                                acc[nt][j][k2] = c[k2] > 0.f ? __int_as_float(0x7FC00000) : acc[nt][j][k2];
+                        }
+                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
-                        for (int w = 0; w < VW; ++w) any |= nan_bytes(v[i][w]);
-                    if (__any_sync(0xffffffffu, any != 0u)) {
-                        uint32_t see[4];
-#pragma unroll
-                        for (int n = 0; n < 2; ++n) {
-                            const int k = k0 + 16 * h + n * 8 + 2 * t;
-                            see[2 * n] = (k < lim0 ? 0x3C00u : 0u) | (k + 1 < lim0 ? 0x3C000000u : 0u);
-                            see[2 * n + 1] = (k < lim1 ? 0x3C00u : 0u) | (k + 1 < lim1 ? 0x3C000000u : 0u);
-                        }
-#pragma unroll
-                        for (int w = 0; w < VW; ++w) {
-                            uint32_t ind[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint32_t m = nan_bytes(v[i][w]) >> 7;
-                                ind[i] = m * 0x38u;  // e4m3's 1
-                                v[i][w] &= ~(m * 0xFFu);
-                            }
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint32_t sel = e < 2 ? 0x5140u : 0x7362u;
-                                const uint32_t lo = __byte_perm(ind[0], ind[1], sel) >> (16 * (e & 1));
-                                const uint32_t hi = __byte_perm(ind[2], ind[3], sel) >> (16 * (e & 1));
-                                float c[4] = {0.f, 0.f, 0.f, 0.f};
-                                mma16816(c, see[0], see[1], see[2], see[3], e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(hi));
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    acc[4 * w + e][k] = c[k] > 0.f ? __int_as_float(0x7FC00000) : acc[4 * w + e][k];
-                            }
-                        }
-                    }
-                }
-#pragma unroll
-                for (int w = 0; w < VW; ++w) {
-                    const uint32_t lo0 = __byte_perm(v[0][w], v[1][w], 0x5140), hi0 = __byte_perm(v[0][w], v[1][w], 0x7362);
-                    const uint32_t lo1 = __byte_perm(v[2][w], v[3][w], 0x5140), hi1 = __byte_perm(v[2][w], v[3][w], 0x7362);
-                    const uint32_t(&a)[4] = pa[h];
-                    mma16816(acc[4 * w], a[0], a[1], a[2], a[3], e4m3x2_to_f16x2(lo0), e4m3x2_to_f16x2(lo1));
-                    mma16816(acc[4 * w + 1], a[0], a[1], a[2], a[3], e4m3x2_to_f16x2(lo0 >> 16), e4m3x2_to_f16x2(lo1 >> 16));
-                    mma16816(acc[4 * w + 2], a[0], a[1], a[2], a[3], e4m3x2_to_f16x2(hi0), e4m3x2_to_f16x2(hi1));
-                    mma16816(acc[4 * w + 3], a[0], a[1], a[2], a[3], e4m3x2_to_f16x2(hi0 >> 16), e4m3x2_to_f16x2(hi1 >> 16));
+                        for (int w = 0; w < VW; ++w) v[i][w] &= ~((nan_bytes(v[i][w]) >> 7) * 0xFFu);
                 }
             }
+#pragma unroll
+            for (int j = 0; j < NO; ++j) {
+                const uint32_t sel = j & 1 ? 0x7362u : 0x5140u;
+                const uint32_t a = __byte_perm(v[0][j >> 1], v[1][j >> 1], sel), b = __byte_perm(v[2][j >> 1], v[3][j >> 1], sel);
+                uint32_t a0, a1, a2, a3;
+                e4m3x4_to_f16(a, a0, a1);
+                e4m3x4_to_f16(b, a2, a3);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt][j], a0, a1, a2, a3, pb[h][nt][0], pb[h][nt][1]);
+            }
         }
-        __syncwarp();  // every lane has read the stage
-        if (ok && loaded) {
-            if (lane == 0) mbar_arrive(empty_bar(st));
-            ++used;
+    };
+    for (int it = 0; it < n_units;) {
+        // an item begins, or goes on from the CTA before
+        const Seen seen = seen_keys(p, at);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = at.tile * p.tile_rows + nt * 8 + g;  // the query row whose values this lane prepares
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                static_cast<const T *>(p.q) + row_at(p, at.b, at.hg * p.heads + hw, r < p.rows ? r : 0) * D + t * (D / 4));
+            uint32_t w[D / 8];
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const uint4 v = r < p.rows ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+                w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+            }
+            float down = 1.f;
+            if constexpr (Elem<T>::BF16) {
+                uint32_t mx = 0u;  // largest magnitude of the row, as the bits of a non-negative bf16
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) mx = max(mx, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+                mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const int e = max(static_cast<int>(mx >> 7) - 127, -100);
+                const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
+                down = __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    const float2 v = Pair<T>::get(w[i]);
+                    w[i] = Pair<__half>::put(v.x * up, v.y * up);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+                qb[nt][i][0] = w[2 * i];
+                qb[nt][i][1] = w[2 * i + 1];
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                coef[nt][i] = p.sl2e * __shfl_sync(0xffffffffu, down, (2 * t + i) * 4);
+                const int ri = at.tile * p.tile_rows + nt * 8 + 2 * t + i;
+                lim[nt][i] = p.causal ? at.len - p.sq + ri % p.sq + 1 : at.len;
+                m[nt][i] = -INFINITY;
+                l[nt][i] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < NO; ++j) acc[nt][j][0] = acc[nt][j][1] = acc[nt][j][2] = acc[nt][j][3] = 0.f;
         }
-
-        const bool item_ends = cur.j + 1 == cur.n;
-        if (item_ends || it + 1 == n_units) {
-            l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-            l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-            l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-            l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-            const int nr = min(kKv8Tile, p.rows - cur.tile * kKv8Tile);
-            const int64_t first_unit = u0 + it - cur.j;  // of the item
+        const int j_end = min(at.n, at.j + n_units - it);
+        // units of which some row sees a key; steps whose keys every row sees
+        const int j_seen = min(j_end, (seen.end + p.unit_keys - 1) / p.unit_keys);
+        const int whole_keys = seen.all - (kshare + 1) * kStepKeys;
+        const int j_whole = whole_keys < 0 ? 0 : min(j_seen, whole_keys / p.unit_keys + 1);
+        const int j_first = at.j;
+        int j = j_first;
+        auto unit = [&](auto partly) __attribute__((always_inline)) {
+            const uint32_t st = used % STAGES;
+            const int k0 = j * p.unit_keys + kshare * kStepKeys;
+            if (ok) ok = __all_sync(0xffffffffu, wait(full_bar(st), (used / STAGES) & 1u, SITE_KV8_FULL));
+            if (ok) {
+                if (!decltype(partly)::value || k0 < seen.end) step(k0, st, partly);
+                __syncwarp();  // every lane has read the stage
+                if (lane == 0) mbar_arrive(empty_bar(st));
+                ++used;
+            }
+        };
+#pragma unroll 1
+        for (; j < j_whole; ++j) unit(std::false_type());
+#pragma unroll 1
+        for (; j < j_seen; ++j) unit(std::true_type());
+        it += j_end - j_first;
+        // the item ends, or goes on in the next CTA
+        const bool item_ends = j_end == at.n;
+        {
+            const int nr = min(p.tile_rows, p.rows - at.tile * p.tile_rows);
+            const int64_t first_unit = u0 + it - j_end;  // of the item
             const bool whole = first_unit >= u0 && item_ends;
             const int64_t part = part_at(2 * static_cast<int64_t>(blockIdx.x) + (first_unit > u0 ? 1 : 0), hw);
-            const int64_t row0 = row_at(p, cur.b, cur.hg * p.heads + hw, cur.tile * kKv8Tile);
-            // a lane's columns of row g: 2 NO consecutive ones from 2 t NO on, acc[i][0] then acc[i][1]
-            if (shares == 1) {
+            const int64_t row0 = row_at(p, at.b, at.hg * p.heads + hw, at.tile * p.tile_rows);
+            float2 *ml = reinterpret_cast<float2 *>(smem + C::ML_OFF);
+            float *ob = reinterpret_cast<float *>(smem + C::O_OFF);
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    const int r = g + 8 * hh;
-                    if (r >= nr) continue;
-                    const float m = hh ? m1 : m0, l = hh ? l1 : l0;
-                    const float inv = !whole ? 1.f : (l == 0.f ? 0.f : 1.f / l);
-                    float4 v[NO / 2];
+            for (int nt = 0; nt < NT; ++nt) {
+                if (8 * nt >= nr) break;
 #pragma unroll
-                    for (int i = 0; i < NO; i += 4) {
-                        v[i / 4] = make_float4(acc[i][2 * hh] * inv, acc[i + 1][2 * hh] * inv, acc[i + 2][2 * hh] * inv,
-                                               acc[i + 3][2 * hh] * inv);
-                        v[NO / 4 + i / 4] = make_float4(acc[i][2 * hh + 1] * inv, acc[i + 1][2 * hh + 1] * inv,
-                                                        acc[i + 2][2 * hh + 1] * inv, acc[i + 3][2 * hh + 1] * inv);
+                for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], off);
+                    const int r = nt * 8 + 2 * t + i;
+                    if (shares == 1) {
+                        if (r >= nr) continue;
+                        const float inv = !whole ? 1.f : (l[nt][i] == 0.f ? 0.f : 1.f / l[nt][i]);
+                        if (whole) {
+                            uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(p.o) + (row0 + r) * D + 2 * NO * g);
+#pragma unroll
+                            for (int j = 0; j < NO; j += 4)
+                                *reinterpret_cast<uint4 *>(dst + j) =
+                                    make_uint4(Pair<T>::put(acc[nt][j][i] * inv, acc[nt][j][2 + i] * inv),
+                                               Pair<T>::put(acc[nt][j + 1][i] * inv, acc[nt][j + 1][2 + i] * inv),
+                                               Pair<T>::put(acc[nt][j + 2][i] * inv, acc[nt][j + 2][2 + i] * inv),
+                                               Pair<T>::put(acc[nt][j + 3][i] * inv, acc[nt][j + 3][2 + i] * inv));
+                            if (g == 0 && p.lse) p.lse[row0 + r] = lse_of(m[nt][i], l[nt][i]);
+                        } else {
+                            float *dst = p.o_part + (part + r) * D + 2 * NO * g;
+#pragma unroll
+                            for (int j = 0; j < NO; j += 2)
+                                *reinterpret_cast<float4 *>(dst + 2 * j) =
+                                    make_float4(acc[nt][j][i], acc[nt][j][2 + i], acc[nt][j + 1][i], acc[nt][j + 1][2 + i]);
+                            if (g == 0) *reinterpret_cast<float2 *>(p.ml_part + (part + r) * 2) = make_float2(m[nt][i], l[nt][i]);
+                        }
+                    } else {
+                        // several warps have parts of this head's rows: eight rows of each meet in shared memory
+                        if (g == 0) ml[warp * 8 + 2 * t + i] = make_float2(m[nt][i], l[nt][i]);
+                        float *dst = ob + (warp * 8 + 2 * t + i) * D + 2 * NO * g;
+#pragma unroll
+                        for (int j = 0; j < NO; j += 2)
+                            *reinterpret_cast<float4 *>(dst + 2 * j) =
+                                make_float4(acc[nt][j][i], acc[nt][j][2 + i], acc[nt][j + 1][i], acc[nt][j + 1][2 + i]);
+                    }
+                }
+                if (shares == 1) continue;
+                named_barrier(1, kWarps * 32);
+                for (int i = kshare * 32 + lane; i < min(8, nr - 8 * nt) * (D / 4); i += shares * 32) {
+                    const int r8 = i / (D / 4), c4 = i % (D / 4), r = r8 + 8 * nt;
+                    float mx = -INFINITY, lx = 0.f;
+                    for (int w = hw; w < kWarps; w += p.heads) mx = fmaxf(mx, ml[w * 8 + r8].x);
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int w = hw; w < kWarps; w += p.heads) {
+                        const float2 a = ml[w * 8 + r8];
+                        const float f = a.x == mx ? 1.f : ex2_approx(a.x - mx);
+                        const float4 v = *reinterpret_cast<const float4 *>(ob + (w * 8 + r8) * D + c4 * 4);
+                        o.x = fmaf(v.x, f, o.x);
+                        o.y = fmaf(v.y, f, o.y);
+                        o.z = fmaf(v.z, f, o.z);
+                        o.w = fmaf(v.w, f, o.w);
+                        lx = fmaf(a.y, f, lx);
                     }
                     if (whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(p.o) + (row0 + r) * D + 2 * t * NO);
-#pragma unroll
-                        for (int i = 0; i < NO / 2; i += 2)
-                            dst[i / 2] = make_uint4(Pair<T>::put(v[i].x, v[i].y), Pair<T>::put(v[i].z, v[i].w),
-                                                    Pair<T>::put(v[i + 1].x, v[i + 1].y), Pair<T>::put(v[i + 1].z, v[i + 1].w));
-                        if (t == 0 && p.lse) p.lse[row0 + r] = lse_of(m, l);
+                        const float inv = lx == 0.f ? 0.f : 1.f / lx;
+                        store4<D, T>(static_cast<T *>(p.o) + (row0 + r) * D + c4 * 4,
+                                     make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+                        if (c4 == 0 && p.lse) p.lse[row0 + r] = lse_of(mx, lx);
                     } else {
-                        float4 *dst = reinterpret_cast<float4 *>(p.o_part + (part + r) * D + 2 * t * NO);
-#pragma unroll
-                        for (int i = 0; i < NO / 2; ++i) dst[i] = v[i];
-                        if (t == 0) *reinterpret_cast<float2 *>(p.ml_part + (part + r) * 2) = make_float2(m, l);
+                        *reinterpret_cast<float4 *>(p.o_part + (part + r) * D + c4 * 4) = o;
+                        if (c4 == 0) *reinterpret_cast<float2 *>(p.ml_part + (part + r) * 2) = make_float2(mx, lx);
                     }
                 }
-            } else {
-                // the warps of one head join their parts
-                float2 *ml = reinterpret_cast<float2 *>(smem + C::ML_OFF);
-                float *ob = reinterpret_cast<float *>(smem + C::O_OFF);
-                if (t == 0) {
-                    ml[warp * 16 + g] = make_float2(m0, l0);
-                    ml[warp * 16 + g + 8] = make_float2(m1, l1);
-                }
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {  // eight rows at a time
-                    if (8 * hh >= nr) break;
-                    if (g + 8 * hh < nr) {
-                        float *dst = ob + (warp * 8 + g) * D + 2 * t * NO;
-#pragma unroll
-                        for (int i = 0; i < NO; i += 4) {
-                            *reinterpret_cast<float4 *>(dst + i) =
-                                make_float4(acc[i][2 * hh], acc[i + 1][2 * hh], acc[i + 2][2 * hh], acc[i + 3][2 * hh]);
-                            *reinterpret_cast<float4 *>(dst + NO + i) = make_float4(
-                                acc[i][2 * hh + 1], acc[i + 1][2 * hh + 1], acc[i + 2][2 * hh + 1], acc[i + 3][2 * hh + 1]);
-                        }
-                    }
-                    named_barrier(1, kWarps * 32);
-                    for (int i = kshare * 32 + lane; i < min(8, nr - 8 * hh) * (D / 4); i += shares * 32) {
-                        const int r8 = i / (D / 4), c4 = i % (D / 4), r = r8 + 8 * hh;
-                        float mx = -INFINITY, l = 0.f;
-                        for (int w = hw; w < kWarps; w += p.heads) mx = fmaxf(mx, ml[w * 16 + r].x);
-                        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                        for (int w = hw; w < kWarps; w += p.heads) {
-                            const float2 a = ml[w * 16 + r];
-                            const float f = a.x == mx ? 1.f : ex2_approx(a.x - mx);
-                            const float4 v = *reinterpret_cast<const float4 *>(ob + (w * 8 + r8) * D + c4 * 4);
-                            o.x = fmaf(v.x, f, o.x);
-                            o.y = fmaf(v.y, f, o.y);
-                            o.z = fmaf(v.z, f, o.z);
-                            o.w = fmaf(v.w, f, o.w);
-                            l = fmaf(a.y, f, l);
-                        }
-                        if (whole) {
-                            const float inv = l == 0.f ? 0.f : 1.f / l;
-                            store4<D, T>(static_cast<T *>(p.o) + (row0 + r) * D + c4 * 4,
-                                         make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-                            if (c4 == 0 && p.lse) p.lse[row0 + r] = lse_of(mx, l);
-                        } else {
-                            *reinterpret_cast<float4 *>(p.o_part + (part + r) * D + c4 * 4) = o;
-                            if (c4 == 0) *reinterpret_cast<float2 *>(p.ml_part + (part + r) * 2) = make_float2(mx, l);
-                        }
-                    }
-                    named_barrier(1, kWarps * 32);
-                }
+                named_barrier(1, kWarps * 32);
             }
         }
-        if (it + 1 == n_units && threadIdx.x == 0) {
+        if (it == n_units && threadIdx.x == 0) {
             // the item that this CTA begins and others go on with, if there is one
-            const int64_t first_unit = u0 + it - cur.j;
+            const int64_t first_unit = u0 + it - j_end;
             Kv8Cut c = {0, 0, 0, 0, 0};
             if (!item_ends && first_unit >= u0) {
-                c.parts = static_cast<int>(shared_out.owner(first_unit + cur.n - 1) - blockIdx.x) + 1;
+                c.parts = static_cast<int>(shared_out.owner(first_unit + at.n - 1) - blockIdx.x) + 1;
                 c.second = first_unit > u0 ? 1 : 0;
-                c.b = cur.b;
-                c.hg = cur.hg;
-                c.tile = cur.tile;
+                c.b = at.b;
+                c.hg = at.hg;
+                c.tile = at.tile;
             }
             p.cut[blockIdx.x] = c;
         }
-        next_unit(p, cur);
+        at.j = at.n - 1;
+        next_unit(p, at);
+    }
     }
 }
 
@@ -734,9 +771,9 @@ __global__ void __launch_bounds__(256) attn_kv8_join_kernel(const __grid_constan
     const int n = cut.parts;
     if (n == 0) return;
     const int hw = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int nr = min(kKv8Tile, p.rows - cut.tile * kKv8Tile);
+    const int nr = min(p.tile_rows, p.rows - cut.tile * p.tile_rows);
     auto part_of = [&](int k) { return part_at(2 * (static_cast<int64_t>(blockIdx.x) + k) + (k == 0 ? cut.second : 0), hw); };
-    const int64_t row0 = row_at(p, cut.b, cut.hg * p.heads + hw, cut.tile * kKv8Tile);
+    const int64_t row0 = row_at(p, cut.b, cut.hg * p.heads + hw, cut.tile * p.tile_rows);
     for (int r = warp; r < nr; r += 8) {
         float2 a[LOADS];
         float m = -INFINITY, l = 0.f;
@@ -797,11 +834,11 @@ __global__ void __launch_bounds__(256) attn_kv8_join_kernel(const __grid_constan
     }
 }
 
-template <int D, typename T>
+template <int D, typename T, int NT>
 cudaError_t launch_kv8_t(const Kv8LaunchArgs &a)
 {
-    auto kern = attn_kv8_kernel<D, T>;
-    std::atomic<int> &ready = a.attr_ready[(D == 64 ? 0 : 2) + (Elem<T>::BF16 ? 1 : 0)];
+    auto kern = attn_kv8_kernel<D, T, NT>;
+    std::atomic<int> &ready = a.attr_ready[(D == 64 ? 0 : 4) + (Elem<T>::BF16 ? 2 : 0) + NT - 1];
     cudaError_t e;
     if (ready.load(std::memory_order_acquire) == 0) {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Kv8Cfg<D>::SMEM);
@@ -824,12 +861,18 @@ cudaError_t launch_kv8_t(const Kv8LaunchArgs &a)
     return cudaLaunchKernelEx(&cfg, attn_kv8_join_kernel<D, T>, a.p);
 }
 
+template <int D, typename T>
+cudaError_t launch_kv8_rows(const Kv8LaunchArgs &a)
+{
+    return a.p.tile_rows == 8 ? launch_kv8_t<D, T, 1>(a) : launch_kv8_t<D, T, 2>(a);
+}
+
 }  // namespace
 
 cudaError_t launch_kv8(const Kv8LaunchArgs &a, int d, bool bf16)
 {
-    if (d == 64) return bf16 ? launch_kv8_t<64, __nv_bfloat16>(a) : launch_kv8_t<64, __half>(a);
-    return bf16 ? launch_kv8_t<128, __nv_bfloat16>(a) : launch_kv8_t<128, __half>(a);
+    if (d == 64) return bf16 ? launch_kv8_rows<64, __nv_bfloat16>(a) : launch_kv8_rows<64, __half>(a);
+    return bf16 ? launch_kv8_rows<128, __nv_bfloat16>(a) : launch_kv8_rows<128, __half>(a);
 }
 
 }  // namespace attn

@@ -33,7 +33,7 @@ struct Kv8Params {
     int32_t head_groups;         // h_kv / heads
     int32_t unit_keys;           // 32 * 8 / heads
     int32_t sq, rows;            // rows = (h / h_kv) * sq query rows of one key head
-    int32_t tiles;               // ceil(rows / 16)
+    int32_t tile_rows, tiles;    // query rows of an item: 8 or 16; ceil(rows / tile_rows)
     int32_t cap;                 // pages_per_seq * page_size
     int32_t page_size, pages_per_seq, num_pages, block_shift;
     int32_t causal;
@@ -41,7 +41,7 @@ struct Kv8Params {
 };
 
 constexpr int kKv8MaxCtas = 160;  // CTAs of a launch at most (sizes the workspace)
-constexpr int kKv8Instances = 4;  // head dim {64, 128} x {fp16, bf16}
+constexpr int kKv8Instances = 8;  // head dim {64, 128} x {fp16, bf16} x {8, 16 rows}
 constexpr int kKv8Heads = 8;       // key heads of an item at most
 constexpr int kKv8Tile = 16;      // query rows of an item
 
