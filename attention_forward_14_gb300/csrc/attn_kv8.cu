@@ -756,31 +756,67 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Joins the parts of an item that several CTAs share: blockIdx.x is the CTA
-// that begins the item, blockIdx.y the head of its group.  Few rows: several
-// warps share a row's parts and add up what they have, in a fixed order.
+// Joins the parts of an item that several CTAs share: the blockIdx.x-th of
+// such items, blockIdx.y the head of its group.  A warp takes a row
+// and, when there are few rows, a share of its parts: the first parts' values
+// are on their way while it forms the weights of all of them.  The shares are
+// added up in a fixed order.
 template <int D, typename T>
-__global__ void __launch_bounds__(256) attn_kv8_join_kernel(const __grid_constant__ Kv8Params p)
+__global__ void __launch_bounds__(256) attn_kv8_join_kernel(const __grid_constant__ Kv8Params p, int grid)
 {
-    constexpr int VEC = D / 32;
-    constexpr int LOADS = kKv8MaxCtas / 32;
-    __shared__ float weight[kKv8MaxCtas][kKv8Tile];  // of each part in each row
-    __shared__ float red[8][D];
+    constexpr int VEC = D / 32, LOADS = kKv8MaxCtas / 32, AHEAD = 8;
+    __shared__ float red[8][D], weight[8][kKv8MaxCtas];
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
-    const Kv8Cut cut = p.cut[blockIdx.x];
-    const int n = cut.parts;
-    if (n == 0) return;
     const int hw = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int64_t cta = -1;  // the one that begins the item
+    {
+        int parts[LOADS], before = 0;
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) parts[i] = lane + 32 * i < grid ? __ldcg(&p.cut[lane + 32 * i].parts) : 0;
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const uint32_t cuts = __ballot_sync(0xffffffffu, parts[i] > 0);
+            const bool it_is = parts[i] > 0 && before + __popc(cuts & ((1u << lane) - 1u)) == static_cast<int>(blockIdx.x);
+            const uint32_t found = __ballot_sync(0xffffffffu, it_is);
+            if (found != 0u) cta = 32 * i + __ffs(found) - 1;
+            before += __popc(cuts);
+        }
+    }
+    if (cta < 0) return;
+    const Kv8Cut cut = p.cut[cta];
+    const int n = cut.parts;
     const int nr = min(p.tile_rows, p.rows - cut.tile * p.tile_rows);
-    auto part_of = [&](int k) { return part_at(2 * (static_cast<int64_t>(blockIdx.x) + k) + (k == 0 ? cut.second : 0), hw); };
+    auto part_of = [&](int k) { return part_at(2 * (cta + k) + (k == 0 ? cut.second : 0), hw); };
     const int64_t row0 = row_at(p, cut.b, cut.hg * p.heads + hw, cut.tile * p.tile_rows);
-    for (int r = warp; r < nr; r += 8) {
+    const int wide = nr > 4 ? 8 : (nr > 2 ? 4 : nr);  // warps that have rows of their own
+    const int sub = warp / wide, subs = 8 / wide;
+    for (int r0 = 0; r0 < nr; r0 += wide) {
+        const int r = r0 + warp % wide;
+        const bool have = r < nr;
+        auto value = [&](int k, float (&v)[VEC]) {
+            const float *src = p.o_part + (part_of(k) + r) * D + lane * VEC;
+            if constexpr (VEC == 4) {
+                const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
+                v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+            } else {
+                const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
+                v[0] = x.x, v[1] = x.y;
+            }
+        };
+        float v[AHEAD][VEC];
+        auto load = [&](int k0) {
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                if (have && k0 + i * subs < n) value(k0 + i * subs, v[i]);
+        };
+        load(sub);
         float2 a[LOADS];
         float m = -INFINITY, l = 0.f;
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
             const int k = lane + 32 * i;
-            a[i] = k < n ? __ldcg(reinterpret_cast<const float2 *>(p.ml_part + (part_of(k) + r) * 2)) : make_float2(-INFINITY, 0.f);
+            a[i] = have && k < n ? __ldcg(reinterpret_cast<const float2 *>(p.ml_part + (part_of(k) + r) * 2))
+                                 : make_float2(-INFINITY, 0.f);
             m = fmaxf(m, a[i].x);
         }
         m = warp_max(m);
@@ -791,31 +827,23 @@ __global__ void __launch_bounds__(256) attn_kv8_join_kernel(const __grid_constan
         }
         l = row_sum<32>(l);
         const float inv = l == 0.f ? 0.f : 1.f / l;
+        if (have && sub == 0 && lane == 0 && p.lse) p.lse[row0 + r] = lse_of(m, l);
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i)
-            if (lane + 32 * i < n) weight[lane + 32 * i][r] = a[i].x * inv;
-        if (lane == 0 && p.lse) p.lse[row0 + r] = lse_of(m, l);
-    }
-    __syncthreads();
-    const int wide = nr >= 8 ? 8 : (nr > 2 ? (nr > 4 ? 8 : 4) : nr);  // warps that have rows of their own
-    const int sub = warp / wide, subs = 8 / wide;
-    for (int r0 = 0; r0 < nr; r0 += wide) {
-        const int r = r0 + warp % wide;
+        for (int i = 0; i < LOADS; ++i) weight[warp][lane + 32 * i] = a[i].x;
+        __syncwarp();
         float o[VEC] = {};
-        if (r < nr) {
-#pragma unroll 8
-            for (int k = sub; k < n; k += subs) {
-                const float f = weight[k][r];
-                const float *src = p.o_part + (part_of(k) + r) * D + lane * VEC;
-                if constexpr (VEC == 4) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
-                    o[0] = fmaf(v.x, f, o[0]), o[1] = fmaf(v.y, f, o[1]), o[2] = fmaf(v.z, f, o[2]), o[3] = fmaf(v.w, f, o[3]);
-                } else {
-                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
-                    o[0] = fmaf(v.x, f, o[0]), o[1] = fmaf(v.y, f, o[1]);
+        for (int k = sub; have && k < n;) {
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                if (k + i * subs < n) {
+                    const float f = weight[warp][k + i * subs];
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) o[e] = fmaf(v[i][e], f, o[e]);
                 }
-            }
+            k += AHEAD * subs;
+            load(k);
         }
+        __syncwarp();
         if (subs > 1) {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) red[warp][lane * VEC + i] = o[i];
@@ -826,10 +854,10 @@ __global__ void __launch_bounds__(256) attn_kv8_join_kernel(const __grid_constan
                     for (int i = 0; i < VEC; ++i) o[i] += red[warp + q * wide][lane * VEC + i];
             __syncthreads();
         }
-        if (sub == 0 && r < nr) {
+        if (sub == 0 && have) {
             uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(p.o) + (row0 + r) * D + lane * VEC);
 #pragma unroll
-            for (int i = 0; i < VEC / 2; ++i) dst[i] = Pair<T>::put(o[2 * i], o[2 * i + 1]);
+            for (int i = 0; i < VEC / 2; ++i) dst[i] = Pair<T>::put(o[2 * i] * inv, o[2 * i + 1] * inv);
         }
     }
 }
@@ -853,12 +881,14 @@ cudaError_t launch_kv8_t(const Kv8LaunchArgs &a)
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.grid), static_cast<unsigned>(a.p.heads));
+    // no more items are cut than there are items, or cuts
+    const int64_t items = static_cast<int64_t>(a.p.b) * a.p.head_groups * a.p.tiles;
+    cfg.gridDim = dim3(static_cast<unsigned>(items < a.grid - 1 ? items : a.grid - 1), static_cast<unsigned>(a.p.heads));
     cfg.blockDim = dim3(256);
     cfg.stream = a.stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_kv8_join_kernel<D, T>, a.p);
+    return cudaLaunchKernelEx(&cfg, attn_kv8_join_kernel<D, T>, a.p, a.grid);
 }
 
 template <int D, typename T>
