@@ -301,7 +301,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_barrier_init();
     }
     __syncthreads();
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     const Shares shared_out(total_units(p), static_cast<int>(gridDim.x));
     if (blockIdx.x >= shared_out.ctas) {
@@ -766,7 +765,6 @@ __global__ void __launch_bounds__(256) attn_kv8_join_kernel(const __grid_constan
 {
     constexpr int VEC = D / 32, LOADS = kKv8MaxCtas / 32, AHEAD = 8;
     __shared__ float red[8][D], weight[8][kKv8MaxCtas];
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
     const int hw = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int64_t cta = -1;  // the one that begins the item
     {
@@ -876,19 +874,11 @@ cudaError_t launch_kv8_t(const Kv8LaunchArgs &a)
     kern<<<a.grid, kThreads, Kv8Cfg<D>::SMEM, a.stream>>>(a.k, a.v, a.p);
     e = cudaGetLastError();
     if (e != cudaSuccess || a.grid < 2) return e;
-    // the join may be brought up while the last parts are computed; it waits for them itself
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
     // no more items are cut than there are items, or cuts
     const int64_t items = static_cast<int64_t>(a.p.b) * a.p.head_groups * a.p.tiles;
-    cfg.gridDim = dim3(static_cast<unsigned>(items < a.grid - 1 ? items : a.grid - 1), static_cast<unsigned>(a.p.heads));
-    cfg.blockDim = dim3(256);
-    cfg.stream = a.stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_kv8_join_kernel<D, T>, a.p, a.grid);
+    const dim3 blocks(static_cast<unsigned>(items < a.grid - 1 ? items : a.grid - 1), static_cast<unsigned>(a.p.heads));
+    attn_kv8_join_kernel<D, T><<<blocks, 256, 0, a.stream>>>(a.p, a.grid);
+    return cudaGetLastError();
 }
 
 template <int D, typename T>
