@@ -1392,8 +1392,8 @@ int attn_kvcache_append_paged(const void *k_new, const void *v_new, void *k_pool
         return fail(ATTN_ERR_SHAPE, "the tables have %lld positions, fewer than the %lld of a request's pages",
                     (long long)table_len, (long long)cap);
     KvAppendParams p;
-    p.nblk = e4m3 ? (s_new + scale_block - 2) / scale_block + 1 : 0;
-    if (b * h_kv > 0 && (b * s_new > INT32_MAX / (2 * h_kv) || b * p.nblk > INT32_MAX / h_kv))
+    const int64_t nblk = e4m3 ? (s_new + scale_block - 2) / scale_block + 1 : 0;
+    if (b * h_kv > 0 && (b * s_new > INT32_MAX / (2 * h_kv) || b * nblk > INT32_MAX / h_kv))
         return fail(ATTN_ERR_SHAPE, "more than 2^31-1 rows");
     if (b * h_kv * s_new == 0) return ATTN_OK;
     if (!k_new || !v_new || !k_pool || !v_pool) return fail(ATTN_ERR_NULL, "k_new, v_new, k_pool or v_pool is NULL");
@@ -1429,6 +1429,7 @@ int attn_kvcache_append_paged(const void *k_new, const void *v_new, void *k_pool
     p.cos = cos, p.sin = sin;
     p.b = b, p.s = s_new, p.num_pages = num_pages, p.pages_per_seq = pages_per_seq;
     p.heads = static_cast<int>(h_kv);
+    p.nblk_heads = static_cast<uint32_t>(nblk * h_kv);
     p.page_size = static_cast<int>(page_size);
     p.block_shift = e4m3 ? log2_of(scale_block) : 0;
     p.rot = cos ? static_cast<int>(rot) : 0;

@@ -25,65 +25,71 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMinScaleExp = -64;
 
-__device__ __forceinline__ int64_t start_of(const KvAppendParams &p, int64_t e, int64_t cap)
-{
-    return min(max(static_cast<int64_t>(p.seqlens[e]), int64_t(0)), cap);
-}
+// Cached tokens of element e, and how many of its new ones are there and fit.
+struct NewRows {
+    int start, end;  // logical positions [start, end)
+};
 
-__device__ __forceinline__ int64_t count_of(const KvAppendParams &p, int64_t e)
+__device__ __forceinline__ NewRows new_rows(const KvAppendParams &p, int e)
 {
-    return p.new_seqlens ? min(max(static_cast<int64_t>(p.new_seqlens[e]), int64_t(0)), p.s) : p.s;
+    const int cap = static_cast<int>(p.pages_per_seq) * p.page_size;
+    const int count = p.new_seqlens ? min(max(p.new_seqlens[e], 0), static_cast<int>(p.s)) : static_cast<int>(p.s);
+    const int start = min(max(p.seqlens[e], 0), cap);
+    return {start, static_cast<int>(min(static_cast<int64_t>(start) + count, static_cast<int64_t>(cap)))};
 }
 
 // Pool row (token) of logical position `pos` of element e, or -1.
-__device__ __forceinline__ int64_t pool_token(const KvAppendParams &p, int64_t e, int64_t pos)
+__device__ __forceinline__ int pool_token(const KvAppendParams &p, int e, int pos)
 {
-    const int64_t page = p.block_table[e * p.pages_per_seq + pos / p.page_size];
+    const int pg = pos / p.page_size;
+    const int page = p.block_table[static_cast<int64_t>(e) * p.pages_per_seq + pg];
     if (page < 0 || page >= p.num_pages) return -1;
-    return page * p.page_size + pos % p.page_size;
+    return page * p.page_size + (pos - pg * p.page_size);
 }
 
-// 16-bit pool.  A unit is one new token and RPW * 4 of its 2 * heads rows
+// 16-bit pool.  A unit is one new token and RPW * ROWS of its 2 * heads rows
 // (the keys' first), one warp.
-template <int D, typename T>
+template <int D, typename T, bool ADJACENT>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ KvAppendParams p)
 {
     constexpr int LPR = D / 8, RPW = 32 / LPR, ROWS = 4;
     const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
-    const int64_t unit = blockIdx.x * static_cast<int64_t>(kThreads / 32) + (threadIdx.x >> 5);
-    const int groups = (p.heads + RPW * ROWS - 1) / (RPW * ROWS);
-    const int64_t tok = unit / (2 * groups);
+    const uint32_t unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const uint32_t groups = (p.heads + RPW * ROWS - 1) / (RPW * ROWS);
+    const uint32_t tok = unit / (2 * groups), gi = unit - tok * 2 * groups;
     if (tok >= p.b * p.s) return;
-    const int gi = static_cast<int>(unit - tok * 2 * groups);
     const int kv = gi >= groups ? 1 : 0;
-    const int h0 = (gi - kv * groups) * RPW * ROWS;
-    const int64_t e = tok / p.s, t = tok - e * p.s;
-    const T *x = static_cast<const T *>(p.x[kv]) + e * p.xb[kv] + t * p.xs[kv] + l * 8;
-    uint4 raw[ROWS];
+    const int h0 = static_cast<int>(gi - kv * groups) * RPW * ROWS;
+    const int e = static_cast<int>(tok / static_cast<uint32_t>(p.s)), t = static_cast<int>(tok - e * static_cast<uint32_t>(p.s));
+    const RowLane rl = row_lane<ADJACENT>(l, kv == 0 ? p.rot : 0);
+    const T *x = static_cast<const T *>(p.x[kv]) + e * p.xb[kv] + t * p.xs[kv];
+    uint2 raw[ROWS][2];
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
         const int h = h0 + i * RPW + sub;
-        raw[i] = h < p.heads ? __ldcs(reinterpret_cast<const uint4 *>(x + h * p.xh[kv])) : make_uint4(0u, 0u, 0u, 0u);
+        raw[i][0] = raw[i][1] = make_uint2(0u, 0u);
+        if (h < p.heads) load_row<ADJACENT>(x + h * p.xh[kv], rl, raw[i]);
     }
-    const int64_t cap = p.pages_per_seq * p.page_size;
-    const int64_t pos = start_of(p, e, cap) + t;
-    if (t >= count_of(p, e) || pos >= cap) return;
-    const int64_t token = pool_token(p, e, pos);
+    const NewRows nr = new_rows(p, e);
+    const int pos = nr.start + t;
+    if (pos >= nr.end) return;
+    const int token = pool_token(p, e, pos);
     if (token < 0) return;
-    T *dst = static_cast<T *>(p.pool[kv]) + token * p.heads * D + l * 8;
-    const bool il = p.interleaved != 0;
-    const RotLane rl = rot_lane(lane, l, p.cos && kv == 0 ? p.rot : 0, il);
-    float c[8], s[8];
-    load_angles(p.cos, p.sin, pos * (p.rot / 2), rl, il, c, s);
+    T *dst = static_cast<T *>(p.pool[kv]) + static_cast<int64_t>(token) * p.heads * D;
+    float c[4], s[4];
+    load_angles(p.cos, p.sin, static_cast<int64_t>(pos) * (p.rot / 2), rl, c, s);
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
         const int h = h0 + i * RPW + sub;
-        float v[8], o[8];
-        unpack8<T>(raw[i], v);
-        unpack8<T>(shfl4(raw[i], rl.partner), o);
-        rotate8<false>(v, o, c, s, rl, il);
-        // a row that is not rotated is a copy, bit for bit
-        if (h < p.heads) *reinterpret_cast<uint4 *>(dst + h * D) = rl.on ? pack8<T>(v) : raw[i];
+        if (rl.on) {  // a row that is not rotated is a copy, bit for bit
+            float v[8];
+            unpack4<T>(raw[i][0], v);
+            unpack4<T>(raw[i][1], v + 4);
+            rotate8<ADJACENT, false>(v, c, s, rl);
+            raw[i][0] = pack4<T>(v);
+            raw[i][1] = pack4<T>(v + 4);
+        }
+        if (h < p.heads) store_row<ADJACENT>(dst + h * D, rl, raw[i]);
     }
 }
 
@@ -109,137 +115,172 @@ __device__ __forceinline__ int scale_exponent(uint32_t a)
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
-__device__ __forceinline__ uint2 to_e4m3(const float (&v)[8], float f)
+__device__ __forceinline__ uint32_t to_e4m3(const float *v, float f)
 {
-    const uint32_t a = pack_e4m3x2(v[0] * f, v[1] * f), b = pack_e4m3x2(v[2] * f, v[3] * f);
-    const uint32_t c = pack_e4m3x2(v[4] * f, v[5] * f), d = pack_e4m3x2(v[6] * f, v[7] * f);
-    return make_uint2(a | (b << 16), c | (d << 16));
+    return pack_e4m3x2(v[0] * f, v[1] * f) | (pack_e4m3x2(v[2] * f, v[3] * f) << 16);
 }
 
-// e4m3 pool.  A unit is one block of one head of the keys or of the values:
-// BLOCK rows of D values, eight to a lane, ITEMS of them to a thread.
-template <int D, typename T, int THREADS, int ITEMS>
-__global__ void __launch_bounds__(THREADS) kv_append_e4m3_kernel(const __grid_constant__ KvAppendParams p)
+// e4m3 pool.  A unit is one block of one head of the keys or of the values,
+// WPU warps of 16 rows.  A warp loads all of its new rows before it looks at
+// them, finds the largest value, and once the unit's warps have agreed on the
+// scale rotates the rows again (from registers, with angles that the first
+// time left in L1) and stores them: holding the rotated fp32 values instead
+// would take twice the registers.  Consecutive units are consecutive heads,
+// so a block's stores are contiguous in the pool.
+template <int D, typename T, bool ADJACENT, int WPU>
+__global__ void __launch_bounds__(kThreads) kv_append_e4m3_kernel(const __grid_constant__ KvAppendParams p)
 {
-    constexpr int LPR = D / 8;
-    constexpr int BLOCK = THREADS * ITEMS / LPR;
-    __shared__ uint32_t warp_max[THREADS / 32];
-    const int lane = threadIdx.x & 31, l = lane % LPR;
+    constexpr int LPR = D / 8, RPW = 32 / LPR, ITER = 16 / RPW, BLOCK = 16 * WPU, UPC = kThreads / 32 / WPU;
+    __shared__ uint32_t warp_max[kThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, sub = lane / LPR;
     const int kv = blockIdx.y;
-    int64_t u = blockIdx.x;
-    const int h = static_cast<int>(u % p.heads);
-    u /= p.heads;
-    const int64_t j = u % p.nblk, e = u / p.nblk;
-    const int64_t cap = p.pages_per_seq * p.page_size;
-    const int64_t start = start_of(p, e, cap);
-    const int64_t end = min(start + count_of(p, e), cap);
-    const int64_t first = (start / BLOCK + j) * BLOCK;  // logical position of the block's first row
-    if (first >= end || start >= end) return;
-    const int64_t token = pool_token(p, e, first);
-    if (token < 0) return;
-
-    const int r_new = static_cast<int>(max(start - first, int64_t(0)));        // the block's rows [r_new, r_end) are new
-    const int r_end = static_cast<int>(min(end - first, int64_t(BLOCK)));
-    const T *x = static_cast<const T *>(p.x[kv]) + e * p.xb[kv] + h * p.xh[kv] + (first - start) * p.xs[kv] + l * 8;
-    const bool il = p.interleaved != 0;
-    const RotLane rl = rot_lane(lane, l, p.cos && kv == 0 ? p.rot : 0, il);
-    uint4 raw[ITEMS];
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-        const int row = (i * THREADS + threadIdx.x) / LPR;
-        raw[i] = row >= r_new && row < r_end ? __ldcs(reinterpret_cast<const uint4 *>(x + row * p.xs[kv]))
-                                             : make_uint4(0u, 0u, 0u, 0u);
+    uint32_t u = blockIdx.x * UPC + warp / WPU;
+    const uint32_t eh = u / p.nblk_heads;
+    const int e = static_cast<int>(eh);
+    u -= eh * p.nblk_heads;
+    const int j = static_cast<int>(u / static_cast<uint32_t>(p.heads)), h = static_cast<int>(u - j * static_cast<uint32_t>(p.heads));
+    // new rows [lo, hi) of the warp's 16, rows [0, old) of them cached before
+    int start = 0, first = 0, lo = 0, hi = 0, old = 0;
+    bool fresh = true;  // the block holds nothing from before
+    if (e < p.b) {
+        const NewRows nr = new_rows(p, e);
+        start = nr.start;
+        first = (nr.start / BLOCK + j) * BLOCK;
+        if (first < nr.end && nr.start < nr.end) {
+            const int base = first + (warp % WPU) * 16;
+            lo = min(max(nr.start - base, 0), 16);
+            hi = max(min(nr.end - base, 16), lo);
+            old = lo;
+            fresh = nr.start <= first;
+        }
     }
-    float *scale_at = p.scale[kv] + (token / p.page_size * p.heads + h) * static_cast<int64_t>(p.page_size / BLOCK) +
-                      token % p.page_size / BLOCK;
-    const float was = r_new > 0 ? *scale_at : 0.f;
+    const bool any = hi > lo || old > 0;
+    const RowLane rl = row_lane<ADJACENT>(l, kv == 0 ? p.rot : 0);
+    const int row0 = (warp % WPU) * 16 + sub;  // of the block; the lane's rows are RPW apart
+    const int token = any ? pool_token(p, e, first) : -1;
+    uint2 raw[ITER][2];
+    if (hi > lo) {
+        const T *x = static_cast<const T *>(p.x[kv]) + e * p.xb[kv] + h * p.xh[kv] +
+                     static_cast<int64_t>(first + row0 - start) * p.xs[kv];
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) {
+            const int r = i * RPW + sub;
+            raw[i][0] = raw[i][1] = make_uint2(0u, 0u);
+            if (r >= lo && r < hi) load_row<ADJACENT>(x + i * RPW * p.xs[kv], rl, raw[i]);
+        }
+    }
+    float *scale_at = nullptr;
+    float was = 0.f;
+    if (token >= 0) {
+        const int page = token / p.page_size;
+        scale_at = p.scale[kv] + (static_cast<int64_t>(page) * p.heads + h) * (p.page_size / BLOCK) + (token - page * p.page_size) / BLOCK;
+        if (!fresh) was = *scale_at;
+    }
     auto value = [&](int i, float (&v)[8]) {
-        const int row = (i * THREADS + threadIdx.x) / LPR;
-        float o[8], c[8], s[8];
-        unpack8<T>(raw[i], v);
-        unpack8<T>(shfl4(raw[i], rl.partner), o);
-        if (row >= r_new && row < r_end) {
-            load_angles(p.cos, p.sin, (first + row) * (p.rot / 2), rl, il, c, s);
-            rotate8<false>(v, o, c, s, rl, il);
+        unpack4<T>(raw[i][0], v);
+        unpack4<T>(raw[i][1], v + 4);
+        if (rl.on) {
+            float c[4], s[4];
+            const int r = i * RPW + sub;
+            load_angles(p.cos, p.sin, static_cast<int64_t>(first + (r >= lo && r < hi ? i * RPW + row0 : 0)) * (p.rot / 2), rl, c, s);
+            rotate8<ADJACENT, false>(v, c, s, rl);
         }
     };
     uint32_t m = 0u;
+    if (hi > lo) {
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-        float v[8];
-        value(i, v);
-        m = amax_bits(v, m);
+        for (int i = 0; i < ITER; ++i) {
+            if (i * RPW + RPW <= lo || i * RPW >= hi) continue;
+            float v[8];
+            value(i, v);
+            m = amax_bits(v, m);
+        }
     }
     m = __reduce_max_sync(0xffffffffu, m);
-    if (lane == 0) warp_max[threadIdx.x >> 5] = m;
-    __syncthreads();
+    if constexpr (WPU > 1) {
+        if (lane == 0) warp_max[warp] = m;
+        __syncthreads();
 #pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) m = max(m, warp_max[i]);
+        for (int i = 0; i < WPU; ++i) m = max(m, warp_max[warp / WPU * WPU + i]);
+    }
+    if (token < 0) return;
     const int ex = scale_exponent(m);
     const float need = pow2(ex);
     const bool grows = need > was;  // false too for a stored NaN: its rows are left
-    const bool keep = r_new > 0 && !grows;
-    const float now = keep ? was : need;
+    const bool keep = !fresh && !grows;
     const float inv = keep ? 1.f / was : pow2(-ex);
-    if (threadIdx.x == 0) *scale_at = now;
-    uint8_t *dst = static_cast<uint8_t *>(p.pool[kv]) + (token * p.heads + h) * D + l * 8;
-    const int64_t row_bytes = static_cast<int64_t>(p.heads) * D;
+    // (every warp of the unit has read the scale: the barrier above)
+    if (warp % WPU == 0 && lane == 0) *scale_at = keep ? was : need;
+    uint8_t *dst = static_cast<uint8_t *>(p.pool[kv]) + (static_cast<int64_t>(token + row0) * p.heads + h) * D;
+    const int64_t step = static_cast<int64_t>(RPW) * p.heads * D;
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-        const int row = (i * THREADS + threadIdx.x) / LPR;
+    for (int i = 0; i < ITER; ++i) {
+        if (i * RPW + RPW <= lo || i * RPW >= hi) continue;
+        const int r = i * RPW + sub;
         float v[8];
         value(i, v);
-        if (row >= r_new && row < r_end)
-            *reinterpret_cast<uint2 *>(dst + row * row_bytes) = to_e4m3(v, inv);
-        else if (row < r_new && grows) {
-            const uint2 old = *reinterpret_cast<const uint2 *>(dst + row * row_bytes);
-            const uint32_t w[2] = {old.x, old.y};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t hh = e4m3x2_to_f16x2(w[q >> 1] >> (16 * (q & 1)));
-                const float2 f = Pair<__half>::get(hh);
-                v[2 * q] = f.x;
-                v[2 * q + 1] = f.y;
+        if (r >= lo && r < hi) {
+            const uint32_t a = to_e4m3(v, inv), b = to_e4m3(v + 4, inv);
+            if constexpr (ADJACENT) {
+                *reinterpret_cast<uint2 *>(dst + i * step + rl.lo) = make_uint2(a, b);
+            } else {
+                *reinterpret_cast<uint32_t *>(dst + i * step + rl.lo) = a;
+                *reinterpret_cast<uint32_t *>(dst + i * step + rl.hi) = b;
             }
-            *reinterpret_cast<uint2 *>(dst + row * row_bytes) = to_e4m3(v, was * inv);
+        }
+    }
+    if (!fresh && grows) {  // the rows from before, at the new scale
+        const float f = was * inv;
+        for (int i = 0; i * RPW < old; ++i) {
+            if (i * RPW + sub >= old) break;
+            uint2 *at = reinterpret_cast<uint2 *>(dst + i * step + 8 * l);
+            const uint2 w = *at;
+            float v[8];
+            unpack4<__half>(make_uint2(e4m3x2_to_f16x2(w.x), e4m3x2_to_f16x2(w.x >> 16)), v);
+            unpack4<__half>(make_uint2(e4m3x2_to_f16x2(w.y), e4m3x2_to_f16x2(w.y >> 16)), v + 4);
+            *at = make_uint2(to_e4m3(v, f), to_e4m3(v + 4, f));
         }
     }
 }
 
-template <int D, typename T>
+template <int D, typename T, bool ADJACENT>
 cudaError_t launch_e4m3(const KvAppendParams &p, cudaStream_t stream)
 {
-    const dim3 grid(static_cast<unsigned>(p.b * p.nblk * p.heads), 2);
-    constexpr int L = D / 8;  // lanes per row; a block of 16 rows is 16 * L threads
-    switch (p.block_shift) {
-    case 4: kv_append_e4m3_kernel<D, T, 16 * L, 1><<<grid, 16 * L, 0, stream>>>(p); break;
-    case 5: kv_append_e4m3_kernel<D, T, 256, 32 * L / 256><<<grid, 256, 0, stream>>>(p); break;
-    case 6: kv_append_e4m3_kernel<D, T, 256, 64 * L / 256><<<grid, 256, 0, stream>>>(p); break;
-    default: kv_append_e4m3_kernel<D, T, 256, 128 * L / 256><<<grid, 256, 0, stream>>>(p); break;
+    const int wpu = 1 << (p.block_shift - 4), upc = kThreads / 32 / wpu;
+    const int64_t units = p.b * static_cast<int64_t>(p.nblk_heads);
+    const dim3 grid(static_cast<unsigned>((units + upc - 1) / upc), 2);
+    switch (wpu) {
+    case 1: kv_append_e4m3_kernel<D, T, ADJACENT, 1><<<grid, kThreads, 0, stream>>>(p); break;
+    case 2: kv_append_e4m3_kernel<D, T, ADJACENT, 2><<<grid, kThreads, 0, stream>>>(p); break;
+    case 4: kv_append_e4m3_kernel<D, T, ADJACENT, 4><<<grid, kThreads, 0, stream>>>(p); break;
+    default: kv_append_e4m3_kernel<D, T, ADJACENT, 8><<<grid, kThreads, 0, stream>>>(p); break;
     }
     return cudaGetLastError();
 }
 
-template <int D, typename T>
+template <int D, typename T, bool ADJACENT>
 cudaError_t launch_16bit(const KvAppendParams &p, cudaStream_t stream)
 {
     constexpr int HPU = 4 * (32 / (D / 8));
     const int64_t units = p.b * p.s * 2 * ((p.heads + HPU - 1) / HPU);
     const unsigned blocks = static_cast<unsigned>((units + kThreads / 32 - 1) / (kThreads / 32));
-    kv_append_kernel<D, T><<<blocks, kThreads, 0, stream>>>(p);
+    kv_append_kernel<D, T, ADJACENT><<<blocks, kThreads, 0, stream>>>(p);
     return cudaGetLastError();
+}
+
+template <int D, typename T>
+cudaError_t launch_t(const KvAppendParams &p, bool e4m3, cudaStream_t stream)
+{
+    if (e4m3) return p.interleaved ? launch_e4m3<D, T, true>(p, stream) : launch_e4m3<D, T, false>(p, stream);
+    return p.interleaved ? launch_16bit<D, T, true>(p, stream) : launch_16bit<D, T, false>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append(const KvAppendParams &p, int d, bool bf16, bool e4m3, cudaStream_t stream)
 {
-    if (e4m3) {
-        if (d == 64) return bf16 ? launch_e4m3<64, __nv_bfloat16>(p, stream) : launch_e4m3<64, __half>(p, stream);
-        return bf16 ? launch_e4m3<128, __nv_bfloat16>(p, stream) : launch_e4m3<128, __half>(p, stream);
-    }
-    if (d == 64) return bf16 ? launch_16bit<64, __nv_bfloat16>(p, stream) : launch_16bit<64, __half>(p, stream);
-    return bf16 ? launch_16bit<128, __nv_bfloat16>(p, stream) : launch_16bit<128, __half>(p, stream);
+    if (d == 64) return bf16 ? launch_t<64, __nv_bfloat16>(p, e4m3, stream) : launch_t<64, __half>(p, e4m3, stream);
+    return bf16 ? launch_t<128, __nv_bfloat16>(p, e4m3, stream) : launch_t<128, __half>(p, e4m3, stream);
 }
 
 }  // namespace attn

@@ -18,7 +18,7 @@ struct KvAppendParams {
     int64_t b, s, num_pages, pages_per_seq;
     int heads, page_size, block_shift;  // a block of the scales is 1 << block_shift tokens
     int rot, interleaved;
-    int64_t nblk;                // e4m3: blocks that a request's new rows can touch
+    uint32_t nblk_heads;         // e4m3: blocks that a request's new rows can touch, times heads
 };
 
 cudaError_t launch_kv_append(const KvAppendParams &p, int d, bool bf16, bool e4m3, cudaStream_t stream);

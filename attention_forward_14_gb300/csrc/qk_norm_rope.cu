@@ -21,12 +21,12 @@ namespace attn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRowsInFlight = 4;  // rows that each lane group loads ahead
 
+// Rows that each lane group loads ahead, and the heads of a unit.
 template <int D>
-constexpr int heads_per_unit() { return kRowsInFlight * (32 / (D / 8)); }
+constexpr int heads_per_unit(int rows) { return rows * (32 / (D / 8)); }
 
-// Position of token `tok`; false when it lies outside the tables (the
+// Position of token (bi, si); false when it lies outside the tables (the
 // token's rows are then zeros, and a position past the end is reported).
 __device__ __forceinline__ bool token_position(const NormRopeParams &p, int64_t bi, int64_t si, int &pos)
 {
@@ -36,150 +36,163 @@ __device__ __forceinline__ bool token_position(const NormRopeParams &p, int64_t 
     return pos >= 0 && pos < p.table_len;
 }
 
-template <int D, typename T>
+// The unit of a warp: a token and ROWS rows of each of the warp's lane groups.
+struct NormUnit {
+    bool key;
+    int h0;           // its first head
+    int64_t bi, si;   // its token
+};
+
+__device__ __forceinline__ NormUnit norm_unit(const NormRopeParams &p, uint32_t unit, int hpu)
+{
+    const uint32_t groups = p.side[0].groups + p.side[1].groups;
+    const uint32_t tok = unit / groups, gi = unit - tok * groups;
+    NormUnit u;
+    u.key = gi >= static_cast<uint32_t>(p.side[0].groups);
+    u.h0 = static_cast<int>(u.key ? gi - p.side[0].groups : gi) * hpu;
+    const uint32_t s = static_cast<uint32_t>(p.s), bi = tok / s;
+    u.bi = bi;
+    u.si = tok - bi * s;
+    return u;
+}
+
+template <int D, typename T, bool ADJACENT, int ROWS>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p)
 {
-    constexpr int LPR = D / 8, RPW = 32 / LPR, HPU = heads_per_unit<D>();
+    constexpr int LPR = D / 8, RPW = 32 / LPR;
     const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
-    const int64_t unit = blockIdx.x * static_cast<int64_t>(kThreads / 32) + (threadIdx.x >> 5);
-    const int groups = p.side[0].groups + p.side[1].groups;
-    const int64_t tok = unit / groups;
-    if (tok >= p.tokens) return;
-    const int gi = static_cast<int>(unit - tok * groups);
-    const bool key = gi >= p.side[0].groups;
-    const NormRopeSide &sd = p.side[key ? 1 : 0];
-    const int h0 = (key ? gi - p.side[0].groups : gi) * HPU;
-    const int64_t bi = tok / p.s, si = tok - bi * p.s;
+    const uint32_t unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    if (unit >= p.units) return;
+    const NormUnit u = norm_unit(p, unit, heads_per_unit<D>(ROWS));
+    const NormRopeSide &sd = p.side[u.key ? 1 : 0];
+    const RowLane rl = row_lane<ADJACENT>(l, p.rot);
 
-    const T *x = static_cast<const T *>(sd.x) + bi * sd.xb + si * sd.xs + l * 8;
-    uint4 raw[kRowsInFlight];
+    const T *x = static_cast<const T *>(sd.x) + u.bi * sd.xb + u.si * sd.xs;
+    uint2 raw[ROWS][2];
 #pragma unroll
-    for (int i = 0; i < kRowsInFlight; ++i) {
-        const int h = h0 + i * RPW + sub;
-        raw[i] = h < sd.heads ? __ldcs(reinterpret_cast<const uint4 *>(x + h * sd.xh)) : make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < ROWS; ++i) {
+        const int h = u.h0 + i * RPW + sub;
+        raw[i][0] = raw[i][1] = make_uint2(0u, 0u);
+        if (h < sd.heads) load_row<ADJACENT>(x + h * sd.xh, rl, raw[i]);
     }
     int pos;
-    const bool valid = token_position(p, bi, si, pos);
-    const bool il = p.interleaved != 0;
-    const RotLane rl = rot_lane(lane, l, p.cos ? p.rot : 0, il);
-    float c[8], s[8];
-    if (valid) load_angles(p.cos, p.sin, static_cast<int64_t>(pos) * (p.rot / 2), rl, il, c, s);
-    float w[8], wo[8];
+    const bool valid = token_position(p, u.bi, u.si, pos);
+    float c[4], s[4], w[8];
+    if (valid) load_angles(p.cos, p.sin, static_cast<int64_t>(pos) * (p.rot / 2), rl, c, s);
     if (sd.w) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(sd.w) + l * 8));
-        unpack8<T>(u, w);
-        unpack8<T>(shfl4(u, rl.partner), wo);
+        unpack4<T>(__ldg(reinterpret_cast<const uint2 *>(static_cast<const T *>(sd.w) + rl.lo)), w);
+        unpack4<T>(__ldg(reinterpret_cast<const uint2 *>(static_cast<const T *>(sd.w) + rl.hi)), w + 4);
     }
-    T *out = static_cast<T *>(sd.out) + bi * sd.ob + si * sd.os + l * 8;
+    T *out = static_cast<T *>(sd.out) + u.bi * sd.ob + u.si * sd.os;
 #pragma unroll
-    for (int i = 0; i < kRowsInFlight; ++i) {
-        const int h = h0 + i * RPW + sub;
-        float v[8], o[8];
-        unpack8<T>(raw[i], v);
-        unpack8<T>(shfl4(raw[i], rl.partner), o);
+    for (int i = 0; i < ROWS; ++i) {
+        const int h = u.h0 + i * RPW + sub;
+        float v[8];
+        unpack4<T>(raw[i][0], v);
+        unpack4<T>(raw[i][1], v + 4);
         if (sd.w) {
             float ss = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
             const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                v[e] *= r * w[e];
-                o[e] *= r * wo[e];
-            }
+            for (int e = 0; e < 8; ++e) v[e] *= r * w[e];
         }
-        rotate8<false>(v, o, c, s, rl, il);
+        rotate8<ADJACENT, false>(v, c, s, rl);
         if (h < sd.heads) {
-            const uint4 y = valid ? pack8<T>(v) : make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4 *>(out + h * sd.oh) = y;
+            const uint2 y[2] = {valid ? pack4<T>(v) : make_uint2(0u, 0u), valid ? pack4<T>(v + 4) : make_uint2(0u, 0u)};
+            store_row<ADJACENT>(out + h * sd.oh, rl, y);
         }
     }
 }
 
-template <int D, typename T>
+// The backward's blocks go over the units of the queries, then over those of
+// the keys, so that a lane adds up one weight's gradient at a time.
+template <int D, typename T, bool ADJACENT, int ROWS>
 __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p)
 {
-    constexpr int LPR = D / 8, RPW = 32 / LPR, HPU = heads_per_unit<D>();
-    __shared__ float acc_s[kThreads / 32][2][D];
-    const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
-    const int groups = p.side[0].groups + p.side[1].groups;
-    const int64_t units = p.tokens * groups;
-    const bool il = p.interleaved != 0;
-    const RotLane rl = rot_lane(lane, l, p.cos ? p.rot : 0, il);
-    float dw[2][8] = {};
-    for (int64_t unit = blockIdx.x * static_cast<int64_t>(kThreads / 32) + (threadIdx.x >> 5); unit < units;
-         unit += static_cast<int64_t>(gridDim.x) * (kThreads / 32)) {
-        const int64_t tok = unit / groups;
-        const int gi = static_cast<int>(unit - tok * groups);
-        const bool key = gi >= p.side[0].groups;
-        const NormRopeSide &sd = p.side[key ? 1 : 0];
-        const int h0 = (key ? gi - p.side[0].groups : gi) * HPU;
-        const int64_t bi = tok / p.s, si = tok - bi * p.s;
-        const T *x = static_cast<const T *>(sd.x) + bi * sd.xb + si * sd.xs + l * 8;
-        const T *g = static_cast<const T *>(sd.g) + bi * sd.gb + si * sd.gs + l * 8;
-        uint4 rx[kRowsInFlight], rg[kRowsInFlight];
-#pragma unroll
-        for (int i = 0; i < kRowsInFlight; ++i) {
-            const int h = h0 + i * RPW + sub;
-            const bool in = h < sd.heads;
-            rx[i] = in ? __ldcs(reinterpret_cast<const uint4 *>(x + h * sd.xh)) : make_uint4(0u, 0u, 0u, 0u);
-            rg[i] = in ? __ldcs(reinterpret_cast<const uint4 *>(g + h * sd.gh)) : make_uint4(0u, 0u, 0u, 0u);
+    constexpr int LPR = D / 8, RPW = 32 / LPR, HPU = heads_per_unit<D>(ROWS);
+    __shared__ float acc_s[kThreads / 32][D];
+    const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR, warp = threadIdx.x >> 5;
+    const RowLane rl = row_lane<ADJACENT>(l, p.rot);
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+        const NormRopeSide &sd = p.side[k];
+        float dw[8] = {}, w[8];
+        if (sd.w) {
+            unpack4<T>(__ldg(reinterpret_cast<const uint2 *>(static_cast<const T *>(sd.w) + rl.lo)), w);
+            unpack4<T>(__ldg(reinterpret_cast<const uint2 *>(static_cast<const T *>(sd.w) + rl.hi)), w + 4);
         }
-        int pos;
-        const bool valid = token_position(p, bi, si, pos);
-        float c[8], s[8];
-        if (valid) load_angles(p.cos, p.sin, static_cast<int64_t>(pos) * (p.rot / 2), rl, il, c, s);
-        float w[8];
-        if (sd.w) unpack8<T>(__ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(sd.w) + l * 8)), w);
-        T *out = static_cast<T *>(sd.out) + bi * sd.ob + si * sd.os + l * 8;
+        const uint32_t units = static_cast<uint32_t>(p.tokens) * sd.groups;
+        for (uint32_t unit = blockIdx.x * (kThreads / 32) + warp; unit < units; unit += gridDim.x * (kThreads / 32)) {
+            const uint32_t tok = unit / sd.groups, h0 = (unit - tok * sd.groups) * HPU;
+            const int64_t bi = tok / static_cast<uint32_t>(p.s), si = tok - bi * p.s;
+            const T *x = static_cast<const T *>(sd.x) + bi * sd.xb + si * sd.xs;
+            const T *g = static_cast<const T *>(sd.g) + bi * sd.gb + si * sd.gs;
+            uint2 rx[ROWS][2], rg[ROWS][2];
 #pragma unroll
-        for (int i = 0; i < kRowsInFlight; ++i) {
-            const int h = h0 + i * RPW + sub;
-            float dy[8], o[8];
-            unpack8<T>(rg[i], dy);
-            unpack8<T>(shfl4(rg[i], rl.partner), o);
-            rotate8<true>(dy, o, c, s, rl, il);
-            if (sd.w) {
-                float n[8];
-                unpack8<T>(rx[i], n);
-                float ss = 0.f, dot = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    ss = fmaf(n[e], n[e], ss);
-                    dot = fmaf(dy[e] * w[e], n[e], dot);
-                }
-                const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
-                const float mean = row_sum<LPR>(dot) * r * (1.f / D);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    n[e] *= r;
-                    const float t = valid ? dy[e] * n[e] : 0.f;  // rows past the last head are zeros
-                    if (key) dw[1][e] += t;
-                    else dw[0][e] += t;
-                    dy[e] = r * (dy[e] * w[e] - n[e] * mean);
+            for (int i = 0; i < ROWS; ++i) {
+                const int h = static_cast<int>(h0) + i * RPW + sub;
+                rx[i][0] = rx[i][1] = rg[i][0] = rg[i][1] = make_uint2(0u, 0u);
+                if (h < sd.heads) {
+                    load_row<ADJACENT>(g + h * sd.gh, rl, rg[i]);
+                    if (sd.w) load_row<ADJACENT>(x + h * sd.xh, rl, rx[i]);
                 }
             }
-            if (h < sd.heads)
-                *reinterpret_cast<uint4 *>(out + h * sd.oh) = valid ? pack8<T>(dy) : make_uint4(0u, 0u, 0u, 0u);
-        }
-    }
-    if (p.dw_part == nullptr) return;
-    // the block's sums, in a fixed order: the lane groups of a warp, then the warps
+            int pos;
+            const bool valid = token_position(p, bi, si, pos);
+            float c[4], s[4];
+            if (valid) load_angles(p.cos, p.sin, static_cast<int64_t>(pos) * (p.rot / 2), rl, c, s);
+            T *out = static_cast<T *>(sd.out) + bi * sd.ob + si * sd.os;
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+            for (int i = 0; i < ROWS; ++i) {
+                const int h = static_cast<int>(h0) + i * RPW + sub;
+                float dy[8];
+                unpack4<T>(rg[i][0], dy);
+                unpack4<T>(rg[i][1], dy + 4);
+                rotate8<ADJACENT, true>(dy, c, s, rl);
+                if (sd.w) {
+                    float n[8];
+                    unpack4<T>(rx[i][0], n);
+                    unpack4<T>(rx[i][1], n + 4);
+                    float ss = 0.f, dot = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        ss = fmaf(n[e], n[e], ss);
+                        dot = fmaf(dy[e] * w[e], n[e], dot);
+                    }
+                    const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
+                    const float mean = row_sum<LPR>(dot) * r * (1.f / D);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        n[e] *= r;
+                        if (valid) dw[e] = fmaf(dy[e], n[e], dw[e]);  // rows past the last head are zeros
+                        dy[e] = r * (dy[e] * w[e] - n[e] * mean);
+                    }
+                }
+                if (h < sd.heads) {
+                    const uint2 y[2] = {valid ? pack4<T>(dy) : make_uint2(0u, 0u), valid ? pack4<T>(dy + 4) : make_uint2(0u, 0u)};
+                    store_row<ADJACENT>(out + h * sd.oh, rl, y);
+                }
+            }
+        }
+        if (p.dw_part == nullptr) continue;
+        // the block's sums, in a fixed order: the lane groups of a warp, then the warps
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            float v = dw[k][e];
+            float v = dw[e];
 #pragma unroll
             for (int off = 16; off >= LPR; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-            if (sub == 0) acc_s[threadIdx.x >> 5][k][l * 8 + e] = v;
+            if (sub == 0) acc_s[warp][(e < 4 ? rl.lo : rl.hi - 4) + e] = v;
         }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
-        float v = 0.f;
+        __syncthreads();
+        for (int i = threadIdx.x; i < D; i += kThreads) {
+            float v = 0.f;
 #pragma unroll
-        for (int wi = 0; wi < kThreads / 32; ++wi) v += acc_s[wi][i / D][i % D];
-        p.dw_part[static_cast<int64_t>(blockIdx.x) * 2 * D + i] = v;
+            for (int wi = 0; wi < kThreads / 32; ++wi) v += acc_s[wi][i];
+            p.dw_part[(static_cast<int64_t>(blockIdx.x) * 2 + k) * D + i] = v;
+        }
+        __syncthreads();
     }
 }
 
@@ -203,59 +216,56 @@ __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float *part, i
     }
 }
 
-NormRopeParams with_groups(const NormRopeParams &p, int d)
+NormRopeParams with_units(const NormRopeParams &p, int d, int rows)
 {
     NormRopeParams q = p;
-    const int hpu = d == 64 ? heads_per_unit<64>() : heads_per_unit<128>();
+    const int hpu = d == 64 ? heads_per_unit<64>(rows) : heads_per_unit<128>(rows);
     for (NormRopeSide &sd : q.side) sd.groups = (sd.heads + hpu - 1) / hpu;
+    q.units = static_cast<uint32_t>(q.tokens * (q.side[0].groups + q.side[1].groups));
     return q;
 }
 
-int64_t unit_blocks(const NormRopeParams &p)
+int blocks_of(const NormRopeParams &p) { return static_cast<int>((static_cast<int64_t>(p.units) + kThreads / 32 - 1) / (kThreads / 32)); }
+
+constexpr int kFwdRows = 4, kBwdRows = 2;
+
+template <int D, typename T>
+cudaError_t launch_fwd_t(const NormRopeParams &p0, cudaStream_t stream)
 {
-    const int64_t units = p.tokens * (p.side[0].groups + p.side[1].groups);
-    return (units + kThreads / 32 - 1) / (kThreads / 32);
+    const NormRopeParams p = with_units(p0, D, kFwdRows);
+    if (p.interleaved) norm_rope_kernel<D, T, true, kFwdRows><<<blocks_of(p), kThreads, 0, stream>>>(p);
+    else norm_rope_kernel<D, T, false, kFwdRows><<<blocks_of(p), kThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <int D, typename T>
+cudaError_t launch_bwd_t(const NormRopeParams &p0, int sm_count, cudaStream_t stream)
+{
+    const NormRopeParams p = with_units(p0, D, kBwdRows);
+    int blocks = blocks_of(p);
+    const int cap = sm_count * 4 < kNormRopeMaxBlocks ? sm_count * 4 : kNormRopeMaxBlocks;
+    if (blocks > cap) blocks = cap;
+    if (p.interleaved) norm_rope_bwd_kernel<D, T, true, kBwdRows><<<blocks, kThreads, 0, stream>>>(p);
+    else norm_rope_bwd_kernel<D, T, false, kBwdRows><<<blocks, kThreads, 0, stream>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || p.dw_part == nullptr) return e;
+    norm_rope_dw_kernel<<<2 * D / 32, 1024, 0, stream>>>(p.dw_part, blocks, D, p.dw[0], p.dw[1]);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-int norm_rope_bwd_blocks(const NormRopeParams &p, int d, int sm_count)
+cudaError_t launch_norm_rope(const NormRopeParams &p, int d, bool bf16, cudaStream_t stream)
 {
-    const int64_t n = unit_blocks(with_groups(p, d));
-    int64_t cap = static_cast<int64_t>(sm_count) * 4;
-    if (cap > kNormRopeMaxBlocks) cap = kNormRopeMaxBlocks;
-    return static_cast<int>(n < cap ? n : cap);
+    if (d == 64) return bf16 ? launch_fwd_t<64, __nv_bfloat16>(p, stream) : launch_fwd_t<64, __half>(p, stream);
+    return bf16 ? launch_fwd_t<128, __nv_bfloat16>(p, stream) : launch_fwd_t<128, __half>(p, stream);
 }
 
-cudaError_t launch_norm_rope(const NormRopeParams &p0, int d, bool bf16, cudaStream_t stream)
+cudaError_t launch_norm_rope_bwd(const NormRopeParams &p, int d, bool bf16, int sm_count, cudaStream_t stream)
 {
-    const NormRopeParams p = with_groups(p0, d);
-    const unsigned blocks = static_cast<unsigned>(unit_blocks(p));
-    if (d == 64) {
-        if (bf16) norm_rope_kernel<64, __nv_bfloat16><<<blocks, kThreads, 0, stream>>>(p);
-        else norm_rope_kernel<64, __half><<<blocks, kThreads, 0, stream>>>(p);
-    } else {
-        if (bf16) norm_rope_kernel<128, __nv_bfloat16><<<blocks, kThreads, 0, stream>>>(p);
-        else norm_rope_kernel<128, __half><<<blocks, kThreads, 0, stream>>>(p);
-    }
-    return cudaGetLastError();
-}
-
-cudaError_t launch_norm_rope_bwd(const NormRopeParams &p0, int d, bool bf16, int sm_count, cudaStream_t stream)
-{
-    const NormRopeParams p = with_groups(p0, d);
-    const int blocks = norm_rope_bwd_blocks(p0, d, sm_count);
-    if (d == 64) {
-        if (bf16) norm_rope_bwd_kernel<64, __nv_bfloat16><<<blocks, kThreads, 0, stream>>>(p);
-        else norm_rope_bwd_kernel<64, __half><<<blocks, kThreads, 0, stream>>>(p);
-    } else {
-        if (bf16) norm_rope_bwd_kernel<128, __nv_bfloat16><<<blocks, kThreads, 0, stream>>>(p);
-        else norm_rope_bwd_kernel<128, __half><<<blocks, kThreads, 0, stream>>>(p);
-    }
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || p.dw_part == nullptr) return e;
-    norm_rope_dw_kernel<<<2 * d / 32, 1024, 0, stream>>>(p.dw_part, blocks, d, p.dw[0], p.dw[1]);
-    return cudaGetLastError();
+    if (d == 64)
+        return bf16 ? launch_bwd_t<64, __nv_bfloat16>(p, sm_count, stream) : launch_bwd_t<64, __half>(p, sm_count, stream);
+    return bf16 ? launch_bwd_t<128, __nv_bfloat16>(p, sm_count, stream) : launch_bwd_t<128, __half>(p, sm_count, stream);
 }
 
 }  // namespace attn

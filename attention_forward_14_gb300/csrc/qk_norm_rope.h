@@ -18,7 +18,7 @@ struct NormRopeSide {
     int64_t gb = 0, gh = 0, gs = 0;
     int64_t ob = 0, oh = 0, os = 0;
     int heads = 0;
-    int groups = 0;             // units of kHeadsPerUnit heads
+    int groups = 0;             // units that a token's heads make
 };
 
 struct NormRopeParams {
@@ -27,6 +27,7 @@ struct NormRopeParams {
     const int32_t *pos = nullptr;                // position of token (b, s) at pos[b * pos_b + s]; nullptr: s
     int64_t pos_b = 0;
     int64_t tokens = 0;                          // b * s
+    uint32_t units = 0;                          // units of work
     int64_t s = 0;
     int table_len = 0;
     int rot = 0;
@@ -39,7 +40,6 @@ struct NormRopeParams {
 
 constexpr int kNormRopeMaxBlocks = 1024;  // partial sums of the weights' gradients at most
 
-int norm_rope_bwd_blocks(const NormRopeParams &p, int d, int sm_count);
 cudaError_t launch_norm_rope(const NormRopeParams &p, int d, bool bf16, cudaStream_t stream);
 cudaError_t launch_norm_rope_bwd(const NormRopeParams &p, int d, bool bf16, int sm_count, cudaStream_t stream);
 

@@ -2,13 +2,17 @@
 // rotary rotation and the sums that the q/k norm, the rotated cache append
 // and their gradients share.
 //
-// A row of D 16-bit values is D/8 lanes of eight values (one 16-byte piece
-// each), so a warp holds 32 / (D/8) rows: four at D = 64, two at D = 128.
+// A row of D 16-bit values is D/8 lanes of eight values, so a warp holds
+// 32 / (D/8) rows: four at D = 64, two at D = 128.
 //
 // Rotation of the first `rot` values of a row by the angles of its position
 // (cos/sin tables of rot/2 columns; rot a multiple of 16):
 //   pairs (i, i + rot/2), or adjacent pairs (2i, 2i + 1):
 //   (a, b) -> (a cos - b sin, b cos + a sin);  its transpose has -sin.
+// A lane's eight values are two runs of four, placed so that both of a pair
+// are the same lane's: no value is fetched from another lane or twice, and a
+// lane needs four columns of the tables.  The price is two 8-byte accesses
+// for a 16-byte one.
 // The products and the sum are rounded one by one (no fused multiply-add),
 // so the result is the same whichever of the two orders a caller writes, and
 // equals the formula evaluated step by step in fp32.
@@ -47,99 +51,88 @@ struct Pair<__nv_bfloat16> {
     }
 };
 
-// Eight 16-bit values (a 16-byte piece of a row) as fp32.
+// Four 16-bit values as fp32, and back.
 template <typename T>
-__device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8])
+__device__ __forceinline__ void unpack4(const uint2 &u, float *x)
 {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = Pair<T>::get(w[i]);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-    }
+    const float2 a = Pair<T>::get(u.x), b = Pair<T>::get(u.y);
+    x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
 }
 
 template <typename T>
-__device__ __forceinline__ uint4 pack8(const float (&x)[8])
+__device__ __forceinline__ uint2 pack4(const float *x)
 {
-    return make_uint4(Pair<T>::put(x[0], x[1]), Pair<T>::put(x[2], x[3]), Pair<T>::put(x[4], x[5]),
-                      Pair<T>::put(x[6], x[7]));
+    return make_uint2(Pair<T>::put(x[0], x[1]), Pair<T>::put(x[2], x[3]));
 }
 
-// Which part of the rotation this lane of a row does.
-struct RotLane {
-    bool on;        // the lane's values are rotated
-    bool upper;     // pairs (i, i + rot/2): the lane holds the second of each pair
-    int partner;    // lane (of the warp) that holds the other of each pair
-    int col;        // first column of the cos/sin tables
+// Where the two runs of a lane's values lie in its row, and what it does in
+// the rotation (x[0..3] from `lo`, x[4..7] from `hi`).
+struct RowLane {
+    int lo, hi;
+    bool on;   // rotated, by columns [col, col + 4) of the tables
+    int col;
 };
 
-// `l`: the lane within its row; `lane`: within the warp.
-__device__ __forceinline__ RotLane rot_lane(int lane, int l, int rot, bool interleaved)
+// `l`: the lane within its row.
+template <bool ADJACENT>
+__device__ __forceinline__ RowLane row_lane(int l, int rot)
 {
-    RotLane r;
+    RowLane r;
     r.on = 8 * l < rot;
-    r.upper = false;
-    r.partner = lane;
     r.col = 4 * l;
-    if (!interleaved) {
-        const int half = rot >> 4;  // lanes that hold the first of each pair
-        r.upper = r.on && l >= half;
-        r.partner = !r.on ? lane : (r.upper ? lane - half : lane + half);
-        r.col = 8 * (r.upper ? l - half : l);
-    }
+    r.lo = ADJACENT || !r.on ? 8 * l : 4 * l;
+    r.hi = r.lo + (ADJACENT || !r.on ? 4 : rot >> 1);
     return r;
 }
 
-// The lane's columns of one position's cos and sin: eight, or four (adjacent
-// pairs) of which the others are not used.
-__device__ __forceinline__ void load_angles(const float *cos_t, const float *sin_t, int64_t at, const RotLane &r,
-                                            bool interleaved, float (&c)[8], float (&s)[8])
+// Both runs of a row at `row`, read once (streaming) or written.
+template <bool ADJACENT, typename T>
+__device__ __forceinline__ void load_row(const T *row, const RowLane &r, uint2 (&u)[2])
 {
-    if (!r.on) return;
-    const float4 *cp = reinterpret_cast<const float4 *>(cos_t + at + r.col);
-    const float4 *sp = reinterpret_cast<const float4 *>(sin_t + at + r.col);
-    const float4 c0 = __ldg(cp), s0 = __ldg(sp);
-    c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w;
-    s[0] = s0.x, s[1] = s0.y, s[2] = s0.z, s[3] = s0.w;
-    if (!interleaved) {
-        const float4 c1 = __ldg(cp + 1), s1 = __ldg(sp + 1);
-        c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
-        s[4] = s1.x, s[5] = s1.y, s[6] = s1.z, s[7] = s1.w;
+    if constexpr (ADJACENT) {  // one run of eight
+        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(row + r.lo));
+        u[0] = make_uint2(v.x, v.y), u[1] = make_uint2(v.z, v.w);
+    } else {
+        u[0] = __ldcs(reinterpret_cast<const uint2 *>(row + r.lo));
+        u[1] = __ldcs(reinterpret_cast<const uint2 *>(row + r.hi));
     }
 }
 
-// x rotated (back, when `BACK`); `other` holds the partner lane's values
-// (pairs (i, i + rot/2); not read for adjacent pairs).
-template <bool BACK>
-__device__ __forceinline__ void rotate8(float (&x)[8], const float (&other)[8], const float (&c)[8],
-                                        const float (&s)[8], const RotLane &r, bool interleaved)
+template <bool ADJACENT, typename T>
+__device__ __forceinline__ void store_row(T *row, const RowLane &r, const uint2 (&u)[2])
 {
-    if (!r.on) return;
-    if (interleaved) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = x[2 * i], b = x[2 * i + 1];
-            const float ac = __fmul_rn(a, c[i]), bs = __fmul_rn(b, s[i]);
-            const float bc = __fmul_rn(b, c[i]), as = __fmul_rn(a, s[i]);
-            x[2 * i] = BACK ? __fadd_rn(ac, bs) : __fsub_rn(ac, bs);
-            x[2 * i + 1] = BACK ? __fsub_rn(bc, as) : __fadd_rn(bc, as);
-        }
-        return;
-    }
-    const bool plus = r.upper != BACK;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float xc = __fmul_rn(x[i], c[i]), os = __fmul_rn(other[i], s[i]);
-        x[i] = plus ? __fadd_rn(xc, os) : __fsub_rn(xc, os);
+    if constexpr (ADJACENT) {
+        *reinterpret_cast<uint4 *>(row + r.lo) = make_uint4(u[0].x, u[0].y, u[1].x, u[1].y);
+    } else {
+        *reinterpret_cast<uint2 *>(row + r.lo) = u[0];
+        *reinterpret_cast<uint2 *>(row + r.hi) = u[1];
     }
 }
 
-__device__ __forceinline__ uint4 shfl4(const uint4 &u, int src)
+// The lane's columns of one position's cos and sin, at element `at` of the tables.
+__device__ __forceinline__ void load_angles(const float *cos_t, const float *sin_t, int64_t at, const RowLane &r,
+                                            float (&c)[4], float (&s)[4])
 {
-    return make_uint4(__shfl_sync(0xffffffffu, u.x, src), __shfl_sync(0xffffffffu, u.y, src),
-                      __shfl_sync(0xffffffffu, u.z, src), __shfl_sync(0xffffffffu, u.w, src));
+    if (!r.on) return;
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(cos_t + at + r.col));
+    const float4 b = __ldg(reinterpret_cast<const float4 *>(sin_t + at + r.col));
+    c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w;
+    s[0] = b.x, s[1] = b.y, s[2] = b.z, s[3] = b.w;
+}
+
+// x rotated (back, when `BACK`).
+template <bool ADJACENT, bool BACK>
+__device__ __forceinline__ void rotate8(float (&x)[8], const float (&c)[4], const float (&s)[4], const RowLane &r)
+{
+    if (!r.on) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float &x0 = ADJACENT ? x[2 * i] : x[i], &x1 = ADJACENT ? x[2 * i + 1] : x[i + 4];
+        const float ac = __fmul_rn(x0, c[i]), bs = __fmul_rn(x1, s[i]);
+        const float bc = __fmul_rn(x1, c[i]), as = __fmul_rn(x0, s[i]);
+        x0 = BACK ? __fadd_rn(ac, bs) : __fsub_rn(ac, bs);
+        x1 = BACK ? __fsub_rn(bc, as) : __fadd_rn(bc, as);
+    }
 }
 
 // Sum over the LPR lanes of each row, the same in every lane.
