@@ -736,13 +736,10 @@ def attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, co
     dk_out, gks = _output("dk_out", dk_out, k)
     dq, dqs = _output("dq", dq, q)
     dk, dks = _output("dk", dk, k)
-    dwq = dwk = None
-    if wq is not None or wk is not None:
-        dw = torch.empty((2, d), dtype=torch.float32, device=dev)
-        dwq, dwk = dw.unbind(0)
-        dwq, dwk = dwq if wq is not None else None, dwk if wk is not None else None
-        if workspace is None:
-            workspace = torch.empty(qk_norm_rope_bwd_workspace_bytes(d), dtype=torch.uint8, device=dev)
+    dwq = torch.empty(d, dtype=torch.float32, device=dev) if wq is not None else None
+    dwk = torch.empty(d, dtype=torch.float32, device=dev) if wk is not None else None
+    if workspace is None and (wq is not None or wk is not None):
+        workspace = torch.empty(qk_norm_rope_bwd_workspace_bytes(d), dtype=torch.uint8, device=dev)
     if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
         raise AttnError(-2, "workspace must be a contiguous tensor on the inputs' device")
     with _OnDevice(dev):

@@ -93,14 +93,13 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
     }
 }
 
-// Largest |x| of the finite ones of eight values, as the bits of a
-// non-negative float (which compare like integers).
-__device__ __forceinline__ uint32_t amax_bits(const float (&v)[8], uint32_t m)
+// Largest |x| of the finite ones of eight values, and m.
+__device__ __forceinline__ float amax8(const float (&v)[8], float m)
 {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t a = __float_as_uint(v[i]) & 0x7FFFFFFFu;
-        if (a < 0x7F800000u) m = max(m, a);
+    for (int i = 0; i < 8; i += 2) {
+        const float a = fabsf(v[i]) < INFINITY ? fabsf(v[i]) : 0.f, b = fabsf(v[i + 1]) < INFINITY ? fabsf(v[i + 1]) : 0.f;
+        m = max3f(m, a, b);
     }
     return m;
 }
@@ -186,17 +185,18 @@ __global__ void __launch_bounds__(kThreads) kv_append_e4m3_kernel(const __grid_c
             rotate8<ADJACENT, false>(v, c, s, rl);
         }
     };
-    uint32_t m = 0u;
+    float top = 0.f;
     if (hi > lo) {
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
             if (i * RPW + RPW <= lo || i * RPW >= hi) continue;
             float v[8];
             value(i, v);
-            m = amax_bits(v, m);
+            top = amax8(v, top);
         }
     }
-    m = __reduce_max_sync(0xffffffffu, m);
+    // the bits of non-negative floats compare like integers
+    uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
     if constexpr (WPU > 1) {
         if (lane == 0) warp_max[warp] = m;
         __syncthreads();

@@ -21,16 +21,16 @@ namespace attn {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBwdBlocks = 2;  // of the backward on an SM; the grid is what fits at a time
 
 // Rows that each lane group loads ahead, and the heads of a unit.
 template <int D>
 constexpr int heads_per_unit(int rows) { return rows * (32 / (D / 8)); }
 
-// Position of token (bi, si); false when it lies outside the tables (the
-// token's rows are then zeros, and a position past the end is reported).
-__device__ __forceinline__ bool token_position(const NormRopeParams &p, int64_t bi, int64_t si, int &pos)
+// False when a position lies outside the tables (the token's rows are then
+// zeros, and a position past the end is reported).
+__device__ __forceinline__ bool known_position(const NormRopeParams &p, int pos)
 {
-    pos = p.pos ? p.pos[bi * p.pos_b + si] : static_cast<int>(si);
     if (p.cos == nullptr) return true;
     if (pos >= p.table_len) record_status(p.status, 4u, 0u);
     return pos >= 0 && pos < p.table_len;
@@ -56,6 +56,18 @@ __device__ __forceinline__ NormUnit norm_unit(const NormRopeParams &p, uint32_t 
     return u;
 }
 
+// The lane's values of a norm weight, or ones.
+template <typename T>
+__device__ __forceinline__ void load_weight(const void *w, const RowLane &rl, float (&v)[8])
+{
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 1.f;
+    if (w) {
+        unpack4<T>(__ldg(reinterpret_cast<const uint2 *>(static_cast<const T *>(w) + rl.lo)), v);
+        unpack4<T>(__ldg(reinterpret_cast<const uint2 *>(static_cast<const T *>(w) + rl.hi)), v + 4);
+    }
+}
+
 template <int D, typename T, bool ADJACENT, int ROWS>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p)
 {
@@ -66,50 +78,54 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
     const NormUnit u = norm_unit(p, unit, heads_per_unit<D>(ROWS));
     const NormRopeSide &sd = p.side[u.key ? 1 : 0];
     const RowLane rl = row_lane<ADJACENT>(l, p.rot);
+    const int left = sd.heads - u.h0 - sub;  // row i of the lane group is there when i * RPW < left
 
-    const T *x = static_cast<const T *>(sd.x) + u.bi * sd.xb + u.si * sd.xs;
     uint2 raw[ROWS][2];
+    {
+        const T *x = static_cast<const T *>(sd.x) + u.bi * sd.xb + u.si * sd.xs + (u.h0 + sub) * sd.xh;
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-        const int h = u.h0 + i * RPW + sub;
-        raw[i][0] = raw[i][1] = make_uint2(0u, 0u);
-        if (h < sd.heads) load_row<ADJACENT>(x + h * sd.xh, rl, raw[i]);
+        for (int i = 0; i < ROWS; ++i) {
+            raw[i][0] = raw[i][1] = make_uint2(0u, 0u);
+            if (i * RPW < left) load_row<ADJACENT>(x, rl, raw[i]);
+            x += RPW * sd.xh;
+        }
     }
-    int pos;
-    const bool valid = token_position(p, u.bi, u.si, pos);
+    T *out = static_cast<T *>(sd.out) + u.bi * sd.ob + u.si * sd.os + (u.h0 + sub) * sd.oh;
+    const int pos = p.pos ? __ldg(p.pos + u.bi * p.pos_b + u.si) : static_cast<int>(u.si);
+    if (!known_position(p, pos)) {
+        const uint2 zero[2] = {make_uint2(0u, 0u), make_uint2(0u, 0u)};
+        for (int i = 0; i < ROWS; ++i, out += RPW * sd.oh)
+            if (i * RPW < left) store_row<ADJACENT>(out, rl, zero);
+        return;
+    }
     float c[4], s[4], w[8];
-    if (valid) load_angles(p.cos, p.sin, static_cast<int64_t>(pos) * (p.rot / 2), rl, c, s);
-    if (sd.w) {
-        unpack4<T>(__ldg(reinterpret_cast<const uint2 *>(static_cast<const T *>(sd.w) + rl.lo)), w);
-        unpack4<T>(__ldg(reinterpret_cast<const uint2 *>(static_cast<const T *>(sd.w) + rl.hi)), w + 4);
-    }
-    T *out = static_cast<T *>(sd.out) + u.bi * sd.ob + u.si * sd.os;
+    load_angles(p.cos, p.sin, static_cast<int64_t>(pos) * (p.rot / 2), rl, c, s);
+    load_weight<T>(sd.w, rl, w);
+    const Turn turn = make_turn<ADJACENT, false>(c, s, w);
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-        const int h = u.h0 + i * RPW + sub;
-        float v[8];
-        unpack4<T>(raw[i][0], v);
-        unpack4<T>(raw[i][1], v + 4);
-        if (sd.w) {
-            float ss = 0.f;
+        float2 v[4];
+        unpack_pairs<T>(raw[i], v);
+        float r = 1.f;
+        if (sd.w) r = rsqrtf(row_sum<LPR>(dot8(v, v)) * (1.f / D) + p.eps);
+        if (rl.on) {
+            turned<ADJACENT>(v, turn);
+        } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
-            const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
+            for (int e = 0; e < 4; ++e) v[e] = __fmul2_rn(v[e], make_float2(w[2 * e], w[2 * e + 1]));
+        }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= r * w[e];
-        }
-        rotate8<ADJACENT, false>(v, c, s, rl);
-        if (h < sd.heads) {
-            const uint2 y[2] = {valid ? pack4<T>(v) : make_uint2(0u, 0u), valid ? pack4<T>(v + 4) : make_uint2(0u, 0u)};
-            store_row<ADJACENT>(out + h * sd.oh, rl, y);
-        }
+        for (int e = 0; e < 4; ++e) v[e] = __fmul2_rn(v[e], make_float2(r, r));
+        pack_pairs<T>(v, raw[i]);
+        if (i * RPW < left) store_row<ADJACENT>(out, rl, raw[i]);
+        out += RPW * sd.oh;
     }
 }
 
 // The backward's blocks go over the units of the queries, then over those of
 // the keys, so that a lane adds up one weight's gradient at a time.
 template <int D, typename T, bool ADJACENT, int ROWS>
-__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p)
+__global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p)
 {
     constexpr int LPR = D / 8, RPW = 32 / LPR, HPU = heads_per_unit<D>(ROWS);
     __shared__ float acc_s[kThreads / 32][D];
@@ -118,69 +134,88 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_co
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
         const NormRopeSide &sd = p.side[k];
-        float dw[8] = {}, w[8];
-        if (sd.w) {
-            unpack4<T>(__ldg(reinterpret_cast<const uint2 *>(static_cast<const T *>(sd.w) + rl.lo)), w);
-            unpack4<T>(__ldg(reinterpret_cast<const uint2 *>(static_cast<const T *>(sd.w) + rl.hi)), w + 4);
+        float2 dw[4] = {}, w[4];
+        {
+            float w8[8];
+            load_weight<T>(sd.w, rl, w8);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = make_float2(w8[2 * e], w8[2 * e + 1]);
         }
         const uint32_t units = static_cast<uint32_t>(p.tokens) * sd.groups;
-        for (uint32_t unit = blockIdx.x * (kThreads / 32) + warp; unit < units; unit += gridDim.x * (kThreads / 32)) {
-            const uint32_t tok = unit / sd.groups, h0 = (unit - tok * sd.groups) * HPU;
-            const int64_t bi = tok / static_cast<uint32_t>(p.s), si = tok - bi * p.s;
-            const T *x = static_cast<const T *>(sd.x) + bi * sd.xb + si * sd.xs;
-            const T *g = static_cast<const T *>(sd.g) + bi * sd.gb + si * sd.gs;
-            uint2 rx[ROWS][2], rg[ROWS][2];
-#pragma unroll
-            for (int i = 0; i < ROWS; ++i) {
-                const int h = static_cast<int>(h0) + i * RPW + sub;
-                rx[i][0] = rx[i][1] = rg[i][0] = rg[i][1] = make_uint2(0u, 0u);
-                if (h < sd.heads) {
-                    load_row<ADJACENT>(g + h * sd.gh, rl, rg[i]);
-                    if (sd.w) load_row<ADJACENT>(x + h * sd.xh, rl, rx[i]);
-                }
-            }
+        // a unit's rows, its gradients' rows and its position, as they come from memory
+        struct Fetched {
+            uint2 x[ROWS][2], g[ROWS][2];
             int pos;
-            const bool valid = token_position(p, bi, si, pos);
-            float c[4], s[4];
-            if (valid) load_angles(p.cos, p.sin, static_cast<int64_t>(pos) * (p.rot / 2), rl, c, s);
-            T *out = static_cast<T *>(sd.out) + bi * sd.ob + si * sd.os;
+        };
+        auto fetch = [&](uint32_t unit, Fetched &f) {
+            const uint32_t tok = unit / sd.groups;
+            const int h = static_cast<int>(unit - tok * sd.groups) * HPU + sub;
+            const uint32_t bi = tok / static_cast<uint32_t>(p.s), si = tok - bi * static_cast<uint32_t>(p.s);
+            f.pos = p.pos ? __ldg(p.pos + bi * p.pos_b + si) : static_cast<int>(si);
+            const T *x = static_cast<const T *>(sd.x) + bi * sd.xb + si * sd.xs + h * sd.xh;
+            const T *g = static_cast<const T *>(sd.g) + bi * sd.gb + si * sd.gs + h * sd.gh;
 #pragma unroll
             for (int i = 0; i < ROWS; ++i) {
-                const int h = static_cast<int>(h0) + i * RPW + sub;
-                float dy[8];
-                unpack4<T>(rg[i][0], dy);
-                unpack4<T>(rg[i][1], dy + 4);
-                rotate8<ADJACENT, true>(dy, c, s, rl);
+                f.x[i][0] = f.x[i][1] = f.g[i][0] = f.g[i][1] = make_uint2(0u, 0u);
+                if (h + i * RPW < sd.heads) {
+                    load_row<ADJACENT>(g, rl, f.g[i]);
+                    if (sd.w) load_row<ADJACENT>(x, rl, f.x[i]);
+                }
+                x += RPW * sd.xh;
+                g += RPW * sd.gh;
+            }
+        };
+        const uint32_t stride = gridDim.x * (kThreads / 32);
+        for (uint32_t unit = blockIdx.x * (kThreads / 32) + warp; unit < units; unit += stride) {
+            Fetched cur;
+            fetch(unit, cur);
+            const uint32_t tok = unit / sd.groups;
+            const int h = static_cast<int>(unit - tok * sd.groups) * HPU + sub;
+            const int left = sd.heads - h;
+            const uint32_t bi = tok / static_cast<uint32_t>(p.s), si = tok - bi * static_cast<uint32_t>(p.s);
+            T *out = static_cast<T *>(sd.out) + bi * sd.ob + si * sd.os + h * sd.oh;
+            const int pos = cur.pos;
+            if (!known_position(p, pos)) {
+                const uint2 zero[2] = {make_uint2(0u, 0u), make_uint2(0u, 0u)};
+                for (int i = 0; i < ROWS; ++i, out += RPW * sd.oh)
+                    if (i * RPW < left) store_row<ADJACENT>(out, rl, zero);
+                continue;
+            }
+            float c[4], s[4];
+            load_angles(p.cos, p.sin, static_cast<int64_t>(pos) * (p.rot / 2), rl, c, s);
+            const float ones[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+            const Turn turn = make_turn<ADJACENT, true>(c, s, ones);
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) {
+                float2 dy[4];
+                unpack_pairs<T>(cur.g[i], dy);
+                if (rl.on) turned<ADJACENT>(dy, turn);
                 if (sd.w) {
-                    float n[8];
-                    unpack4<T>(rx[i][0], n);
-                    unpack4<T>(rx[i][1], n + 4);
-                    float ss = 0.f, dot = 0.f;
+                    float2 x[4], wdy[4];
+                    unpack_pairs<T>(cur.x[i], x);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        ss = fmaf(n[e], n[e], ss);
-                        dot = fmaf(dy[e] * w[e], n[e], dot);
-                    }
-                    const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
-                    const float mean = row_sum<LPR>(dot) * r * (1.f / D);
+                    for (int e = 0; e < 4; ++e) wdy[e] = __fmul2_rn(dy[e], w[e]);
+                    const float r = rsqrtf(row_sum<LPR>(dot8(x, x)) * (1.f / D) + p.eps);
+                    // dx = r (wdy - n mean(wdy n)), n = r x: x enters with -r^3 mean(wdy x)
+                    const float f = row_sum<LPR>(dot8(wdy, x)) * (-1.f / D) * r * r * r;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        n[e] *= r;
-                        if (valid) dw[e] = fmaf(dy[e], n[e], dw[e]);  // rows past the last head are zeros
-                        dy[e] = r * (dy[e] * w[e] - n[e] * mean);
+                    for (int e = 0; e < 4; ++e) {
+                        // rows past the last head are zeros
+                        dw[e] = __ffma2_rn(dy[e], __fmul2_rn(x[e], make_float2(r, r)), dw[e]);
+                        dy[e] = __ffma2_rn(x[e], make_float2(f, f), __fmul2_rn(wdy[e], make_float2(r, r)));
                     }
                 }
-                if (h < sd.heads) {
-                    const uint2 y[2] = {valid ? pack4<T>(dy) : make_uint2(0u, 0u), valid ? pack4<T>(dy + 4) : make_uint2(0u, 0u)};
-                    store_row<ADJACENT>(out + h * sd.oh, rl, y);
-                }
+                uint2 y[2];
+                pack_pairs<T>(dy, y);
+                if (i * RPW < left) store_row<ADJACENT>(out, rl, y);
+                out += RPW * sd.oh;
             }
         }
         if (p.dw_part == nullptr) continue;
         // the block's sums, in a fixed order: the lane groups of a warp, then the warps
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            float v = dw[e];
+            float v = e & 1 ? dw[e >> 1].y : dw[e >> 1].x;
 #pragma unroll
             for (int off = 16; off >= LPR; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
             if (sub == 0) acc_s[warp][(e < 4 ? rl.lo : rl.hi - 4) + e] = v;
@@ -227,7 +262,7 @@ NormRopeParams with_units(const NormRopeParams &p, int d, int rows)
 
 int blocks_of(const NormRopeParams &p) { return static_cast<int>((static_cast<int64_t>(p.units) + kThreads / 32 - 1) / (kThreads / 32)); }
 
-constexpr int kFwdRows = 4, kBwdRows = 2;
+constexpr int kFwdRows = 4, kBwdRows = 4;  // 2 rows ahead: +14% and +7% at b2 h32 s4096 d128; 8: +15% (forward)
 
 template <int D, typename T>
 cudaError_t launch_fwd_t(const NormRopeParams &p0, cudaStream_t stream)
@@ -243,7 +278,7 @@ cudaError_t launch_bwd_t(const NormRopeParams &p0, int sm_count, cudaStream_t st
 {
     const NormRopeParams p = with_units(p0, D, kBwdRows);
     int blocks = blocks_of(p);
-    const int cap = sm_count * 4 < kNormRopeMaxBlocks ? sm_count * 4 : kNormRopeMaxBlocks;
+    const int cap = sm_count * kBwdBlocks < kNormRopeMaxBlocks ? sm_count * kBwdBlocks : kNormRopeMaxBlocks;
     if (blocks > cap) blocks = cap;
     if (p.interleaved) norm_rope_bwd_kernel<D, T, true, kBwdRows><<<blocks, kThreads, 0, stream>>>(p);
     else norm_rope_bwd_kernel<D, T, false, kBwdRows><<<blocks, kThreads, 0, stream>>>(p);

@@ -135,6 +135,72 @@ __device__ __forceinline__ void rotate8(float (&x)[8], const float (&c)[4], cons
     }
 }
 
+// The same in packed two-wide arithmetic with fused multiply-adds (half the
+// instructions, one rounding less): a lane's values as four pairs of
+// registers, u[0..1] the first run, u[2..3] the second.  `turn` is what both
+// forms need of the angles, and of a weight for each value that is folded
+// into them: out = u * a + partner(u) * b.
+struct Turn {
+    float2 a[4], b[4];
+};
+
+template <bool ADJACENT, bool BACK>
+__device__ __forceinline__ Turn make_turn(const float (&c)[4], const float (&s)[4], const float (&w)[8])
+{
+    Turn t;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (ADJACENT) {  // the partner of a value is the other one of its register pair
+            const float si = BACK ? -s[i] : s[i];
+            t.a[i] = make_float2(w[2 * i] * c[i], w[2 * i + 1] * c[i]);
+            t.b[i] = make_float2(-w[2 * i + 1] * si, w[2 * i] * si);
+        } else {                   // u[i] and u[i ^ 2]
+            const int k = 2 * (i & 1);
+            const bool upper = i >= 2;
+            const float s0 = upper != BACK ? s[k] : -s[k], s1 = upper != BACK ? s[k + 1] : -s[k + 1];
+            const int own = (upper ? 4 : 0) + k, other = (upper ? 0 : 4) + k;
+            t.a[i] = make_float2(w[own] * c[k], w[own + 1] * c[k + 1]);
+            t.b[i] = make_float2(w[other] * s0, w[other + 1] * s1);
+        }
+    }
+    return t;
+}
+
+template <bool ADJACENT>
+__device__ __forceinline__ void turned(float2 (&u)[4], const Turn &t)
+{
+    float2 o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 other = ADJACENT ? make_float2(u[i].y, u[i].x) : u[i ^ 2];
+        o[i] = __ffma2_rn(other, t.b[i], __fmul2_rn(u[i], t.a[i]));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = o[i];
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack_pairs(const uint2 (&r)[2], float2 (&u)[4])
+{
+    u[0] = Pair<T>::get(r[0].x), u[1] = Pair<T>::get(r[0].y);
+    u[2] = Pair<T>::get(r[1].x), u[3] = Pair<T>::get(r[1].y);
+}
+
+template <typename T>
+__device__ __forceinline__ void pack_pairs(const float2 (&u)[4], uint2 (&r)[2])
+{
+    r[0] = make_uint2(Pair<T>::put(u[0].x, u[0].y), Pair<T>::put(u[1].x, u[1].y));
+    r[1] = make_uint2(Pair<T>::put(u[2].x, u[2].y), Pair<T>::put(u[3].x, u[3].y));
+}
+
+// Sum of the products of the lane's values.
+__device__ __forceinline__ float dot8(const float2 (&x)[4], const float2 (&y)[4])
+{
+    const float2 p = __ffma2_rn(x[1], y[1], __fmul2_rn(x[0], y[0])), q = __ffma2_rn(x[3], y[3], __fmul2_rn(x[2], y[2]));
+    const float2 t = __fadd2_rn(p, q);
+    return t.x + t.y;
+}
+
 // Sum over the LPR lanes of each row, the same in every lane.
 template <int LPR>
 __device__ __forceinline__ float row_sum(float v)
