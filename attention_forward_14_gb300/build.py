@@ -26,7 +26,8 @@ LIB = os.path.join(HERE, "libattn_fwd.so")
 LIB_CHECKED = os.path.join(HERE, "libattn_fwd_checked.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["attn_fwd_api.cu", "inst_d64.cu", "inst_d128_noncausal.cu", "inst_d128_causal.cu", "inst_fp8.cu",
-           "attn_bwd_inst.cu", "attn_bwd_inst_varlen.cu", "qk_norm_rope.cu", "kv_append.cu", "attn_kv8.cu"]
+           "attn_bwd_inst.cu", "attn_bwd_inst_varlen.cu", "qk_norm_rope.cu", "kv_append.cu", "attn_kv8.cu",
+           "attn_kv8_wide.cu"]
 # the translation units compiled again, checked (all of them: forward and backward)
 CHECKED_SOURCES = SOURCES
 

@@ -1438,19 +1438,26 @@ int attn_kvcache_append_paged(const void *k_new, const void *v_new, void *k_pool
     return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "launch (paged cache append)");
 }
 
-// Parts of the items that two or more CTAs share: at most two a CTA.
-static int64_t kv8_workspace(int64_t d) 
+// Query rows of one key head from which the kernel for many rows is taken.
+constexpr int64_t kKv8WideFrom = 17;
+
+// Rows of the parts of a CTA's item: 16 of each head of a group, or 256.
+static int64_t kv8_part_rows(int64_t rows) { return rows >= kKv8WideFrom ? kKv8WideRows : kKv8Heads * kKv8Tile; }
+
+// Parts of the items that two or more CTAs share, at most two a CTA, and what
+// tells which they are.
+static int64_t kv8_workspace(int64_t rows, int64_t d)
 {
-    return int64_t(2) * kKv8MaxCtas * kKv8Heads * kKv8Tile * (d + 2) * 4 + kKv8MaxCtas * static_cast<int64_t>(sizeof(Kv8Cut));
+    return 2 * kKv8MaxCtas * kv8_part_rows(rows) * (d + 2) * 4 + kKv8MaxCtas * static_cast<int64_t>(sizeof(Kv8Cut));
 }
 
 int64_t attn_fwd_kvcache_paged_fp8_workspace_bytes(int64_t b, int64_t h, int64_t h_kv, int64_t sq, int64_t d)
 {
     g_err.clear();
-    if (b < 0 || h < 0 || h_kv < 0 || sq < 0 || sq > kMaxSeq)
+    if (b < 0 || h < 0 || h_kv < 0 || sq < 0 || sq > kMaxSeq || h >= (int64_t(1) << 31))
         return fail(ATTN_ERR_SHAPE, "invalid workspace query of the e4m3 paged attention");
     if (d != 64 && d != 128) return fail(ATTN_ERR_HEADDIM, "head dim %lld not supported (64 or 128)", (long long)d);
-    return kv8_workspace(d);
+    return kv8_workspace(h_kv > 0 ? h / h_kv * sq : 0, d);
 }
 
 int attn_fwd_kvcache_paged_fp8(const void *q, const void *k_pool, const void *v_pool, const float *k_scale,
@@ -1469,7 +1476,7 @@ int attn_fwd_kvcache_paged_fp8(const void *q, const void *k_pool, const void *v_
         return fail(ATTN_ERR_SHAPE, "h %lld is not a multiple of h_kv %lld", (long long)h, (long long)h_kv);
     if (b * h * sq == 0) return ATTN_OK;
     const int64_t group = h / h_kv;
-    if (group * sq > INT32_MAX - 16) return fail(ATTN_ERR_SHAPE, "too many query rows of one key head");
+    if (group * sq > INT32_MAX - kKv8WideRows) return fail(ATTN_ERR_SHAPE, "too many query rows of one key head");
     if (!q || !k_pool || !v_pool || !o) return fail(ATTN_ERR_NULL, "q, k_pool, v_pool or o is NULL");
     if (!k_scale || !v_scale || !cache_seqlens || !block_table)
         return fail(ATTN_ERR_NULL, "k_scale, v_scale, cache_seqlens or block_table is NULL");
@@ -1477,7 +1484,8 @@ int attn_fwd_kvcache_paged_fp8(const void *q, const void *k_pool, const void *v_
         return fail(ATTN_ERR_ALIGN, "q, k_pool, v_pool and o must be 16-byte aligned");
     if (!aligned(lse, 4) || !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(cache_seqlens, 4) || !aligned(block_table, 4))
         return fail(ATTN_ERR_ALIGN, "lse, scales, cache_seqlens and block_table must be 4-byte aligned");
-    const int64_t need = kv8_workspace(d);
+    const int64_t rows = group * sq;
+    const int64_t need = kv8_workspace(rows, d);
     if (!workspace) return fail(ATTN_ERR_NULL, "workspace is NULL (%lld bytes needed)", (long long)need);
     if (!aligned(workspace, 16)) return fail(ATTN_ERR_ALIGN, "workspace must be 16-byte aligned");
     if (workspace_bytes < need)
@@ -1487,35 +1495,39 @@ int attn_fwd_kvcache_paged_fp8(const void *q, const void *k_pool, const void *v_
     Kv8LaunchArgs a;
     Kv8Params &p = a.p;
     const int64_t pool = num_pages * page_size;
+    const bool wide = rows >= kKv8WideFrom;
     p.heads = kKv8Heads;
     while (h_kv % p.heads != 0) p.heads /= 2;
-    // [head][token][d]: boxes of p.heads heads and 32 tokens, or 16 where 32 could straddle two pages, which land
-    // head by head in rows of d bytes, in the swizzle of that width
+    p.box = wide ? 128 : 32;
+    while (page_size % p.box != 0) p.box /= 2;  // a box lies in one page
+    // [head][token][d]: boxes of p.heads heads and up to 32 tokens, or of one head and up to 128, which land head
+    // by head in rows of d bytes, in the swizzle of that width
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(pool), static_cast<cuuint64_t>(h_kv)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(h_kv * d), static_cast<cuuint64_t>(d)};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(d), page_size % 32 == 0 ? 32u : 16u, static_cast<cuuint32_t>(p.heads)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(d), static_cast<cuuint32_t>(p.box), wide ? 1u : static_cast<cuuint32_t>(p.heads)};
     const CUtensorMapSwizzle sw = d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
     if ((rc = encode_map(&a.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, k_pool, dims, strides, box, sw, "e4m3 pool")) != ATTN_OK) return rc;
     if ((rc = encode_map(&a.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, v_pool, dims, strides, box, sw, "e4m3 pool")) != ATTN_OK) return rc;
     p.q = q;
     p.o = o;
     p.lse = lse;
+    p.v_pool = static_cast<const uint8_t *>(v_pool);
     p.k_scale = k_scale;
     p.v_scale = v_scale;
     p.seqlens = cache_seqlens;
     p.block_table = block_table;
     p.status = di->status;
     p.o_part = static_cast<float *>(workspace);
-    p.ml_part = p.o_part + int64_t(2) * kKv8MaxCtas * kKv8Heads * kKv8Tile * d;
-    p.cut = reinterpret_cast<Kv8Cut *>(p.ml_part + int64_t(2) * kKv8MaxCtas * kKv8Heads * kKv8Tile * 2);
+    p.ml_part = p.o_part + 2 * kKv8MaxCtas * kv8_part_rows(rows) * d;
+    p.cut = reinterpret_cast<Kv8Cut *>(p.ml_part + 2 * kKv8MaxCtas * kv8_part_rows(rows) * 2);
     p.sl2e = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
     p.b = static_cast<int32_t>(b);
     p.h_kv = static_cast<int32_t>(h_kv);
     p.head_groups = p.h_kv / p.heads;
     p.unit_keys = 32 * kKv8Heads / p.heads;
     p.sq = static_cast<int32_t>(sq);
-    p.rows = static_cast<int32_t>(group * sq);
-    p.tile_rows = p.rows <= 8 ? 8 : kKv8Tile;
+    p.rows = static_cast<int32_t>(rows);
+    p.tile_rows = wide ? kKv8WideRows : (rows <= 8 ? 8 : kKv8Tile);
     p.tiles = (p.rows + p.tile_rows - 1) / p.tile_rows;
     p.cap = static_cast<int32_t>(cap);
     p.page_size = static_cast<int32_t>(page_size);
@@ -1525,12 +1537,15 @@ int attn_fwd_kvcache_paged_fp8(const void *q, const void *k_pool, const void *v_
     p.causal = causal != 0;
     p.timeout_ns = kDefaultTimeoutNs;
     // no more CTAs than units in full caches
-    const double units = static_cast<double>(b) * p.head_groups * p.tiles * static_cast<double>((cap + p.unit_keys - 1) / p.unit_keys);
+    const int64_t unit_keys = wide ? 128 : p.unit_keys;
+    const double units = static_cast<double>(b) * (wide ? h_kv : p.head_groups) * p.tiles *
+                         static_cast<double>((cap + unit_keys - 1) / unit_keys);
     a.grid = di->sm_count < kKv8MaxCtas ? di->sm_count : kKv8MaxCtas;
     if (units < a.grid) a.grid = static_cast<int>(units);
     a.stream = static_cast<cudaStream_t>(stream);
     a.attr_ready = di->kv8_attr;
-    const cudaError_t e = launch_kv8(a, static_cast<int>(d), dtype == ATTN_BF16);
+    const cudaError_t e = wide ? launch_kv8_wide(a, static_cast<int>(d), dtype == ATTN_BF16)
+                               : launch_kv8(a, static_cast<int>(d), dtype == ATTN_BF16);
     return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "kernel launch (e4m3 paged cache)");
 }
 

@@ -41,10 +41,7 @@
 // the weights is sum(P) / vs, in fp32.  m follows the maximum of x lazily: it
 // is raised (and O and the sum rescaled) only when some x exceeds it by more
 // than 4, so P <= 2^14.
-#include "attn_kv8.h"
-
-#include "attn_fwd_kernel.cuh"
-#include "rows.cuh"
+#include "attn_kv8_common.cuh"
 
 namespace attn {
 
@@ -54,8 +51,6 @@ constexpr int kWarps = 8;                         // consumers
 constexpr int kThreads = (kWarps + 4) * 32;       // and a warpgroup of which one warp copies
 constexpr int kConsumerRegs = 216, kProducerRegs = 72;  // 256 * 216 + 128 * 72 = 384 * 168
 constexpr int kStepKeys = 32;                     // keys of a warp's step
-constexpr float kOffset = 10.f, kSlack = 4.f;
-enum : uint32_t { SITE_KV8_FULL = 40, SITE_KV8_EMPTY = 41 };
 
 template <int D>
 struct Kv8Cfg {
@@ -88,50 +83,6 @@ __device__ __forceinline__ uint32_t transposed(uint32_t v)
     return r;
 }
 
-// fp16 of the e4m3 values in the low and in the high half of a word.
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi)
-{
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-}
-
-__device__ __forceinline__ void cp_async4(uint32_t dst, const float *src)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-
-// Arrives on `bar` when this thread's earlier cp.async have landed (the
-// barrier's count includes it).
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar)
-{
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ float lg2_approx(float x)
-{
-    float y;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ float rcp_approx(float x)
-{
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ int cached_len(const Kv8Params &p, int b) { return min(max(p.seqlens[b], 0), p.cap); }
-
-__device__ __forceinline__ void named_barrier(int id, int threads)
-{
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
-// The top bit of every byte that is an e4m3 NaN (0x7F, 0xFF).
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
-
 // Units of one item of a batch element with n keys: an item that sees no
 // key still has one, which writes its rows.
 __device__ __forceinline__ int units_of(const Kv8Params &p, int n) { return max((n + p.unit_keys - 1) / p.unit_keys, 1); }
@@ -152,36 +103,6 @@ __device__ __forceinline__ int64_t total_units(const Kv8Params &p)
     for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
     return t * p.head_groups * p.tiles;
 }
-
-// a / b of non-negative numbers that mostly fit 32 bits (a 64-bit division
-// is a hundred instructions).
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
-{
-    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-    return a / b;
-}
-
-// The units dealt to the CTAs: the first `rem` get one more than `per`.  No
-// more CTAs than there are units, and none with fewer than kMinUnits of them
-// when that leaves a CTA.
-constexpr int kMinUnits = 2;
-struct Shares {
-    int64_t per, rem;
-    int ctas;
-    __device__ __forceinline__ Shares(int64_t total, int grid)
-    {
-        ctas = static_cast<int>(min(static_cast<int64_t>(grid), max(total / kMinUnits, int64_t(1))));
-        per = quotient(total, ctas);
-        rem = total - per * ctas;
-    }
-    __device__ __forceinline__ int64_t start(int64_t c) const { return c * per + min(c, rem); }
-    // the CTA that has unit u
-    __device__ __forceinline__ int64_t owner(int64_t u) const
-    {
-        const int64_t big = rem * (per + 1);
-        return u < big ? quotient(u, per + 1) : rem + quotient(u - big, per);
-    }
-};
 
 // The place of unit u (< total), by every lane of a warp.
 __device__ __forceinline__ Place place_of(const Kv8Params &p, int64_t u)
@@ -229,13 +150,6 @@ __device__ __forceinline__ void next_unit(const Kv8Params &p, Place &c)
     c.n = units_of(p, c.len);
 }
 
-__device__ __forceinline__ float warp_max(float v)
-{
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-    return v;
-}
-
 // Keys [0, end) are seen by some row of the tile, keys [0, all) by every one.
 struct Seen {
     int end, all;
@@ -259,11 +173,6 @@ __device__ __forceinline__ int64_t row_at(const Kv8Params &p, int b, int kvh, in
 // Partial results: slot 2 c for CTA c's first item, 2 c + 1 for its last, and
 // `hw` the head of the item's group.
 __device__ __forceinline__ int64_t part_at(int64_t slot, int hw) { return (slot * kWarps + hw) * kKv8Tile; }
-
-__device__ __forceinline__ float lse_of(float m, float l)
-{
-    return l == 0.f ? -INFINITY : (m - kOffset + log2f(l)) * 0.69314718055994531f;
-}
 
 template <int D, typename T>
 __device__ __forceinline__ void store4(T *o, float4 v)
@@ -756,7 +665,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of an item that several CTAs share: the blockIdx.x-th of
-// such items, blockIdx.y the head of its group.  A warp takes a row
+// such items, blockIdx.y the head of its group (or, of an item of 256 rows of
+// one head, which 16 of them).  A warp takes a row
 // and, when there are few rows, a share of its parts: the first parts' values
 // are on their way while it forms the weights of all of them.  The shares are
 // added up in a fixed order.
@@ -765,7 +675,7 @@ __global__ void __launch_bounds__(256) attn_kv8_join_kernel(const __grid_constan
 {
     constexpr int VEC = D / 32, LOADS = kKv8MaxCtas / 32, AHEAD = 8;
     __shared__ float red[8][D], weight[8][kKv8MaxCtas];
-    const int hw = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int64_t cta = -1;  // the one that begins the item
     {
         int parts[LOADS], before = 0;
@@ -783,9 +693,14 @@ __global__ void __launch_bounds__(256) attn_kv8_join_kernel(const __grid_constan
     if (cta < 0) return;
     const Kv8Cut cut = p.cut[cta];
     const int n = cut.parts;
-    const int nr = min(p.tile_rows, p.rows - cut.tile * p.tile_rows);
-    auto part_of = [&](int k) { return part_at(2 * (cta + k) + (k == 0 ? cut.second : 0), hw); };
-    const int64_t row0 = row_at(p, cut.b, cut.hg * p.heads + hw, cut.tile * p.tile_rows);
+    const bool many = p.tile_rows > kKv8Tile;
+    const int first = cut.tile * p.tile_rows + (many ? blockIdx.y * kKv8Tile : 0);  // of its key head's rows
+    const int nr = min(min(p.tile_rows, kKv8Tile), p.rows - first);
+    if (nr <= 0) return;
+    auto part_of = [&](int k) {
+        return (2 * (cta + k) + (k == 0 ? cut.second : 0)) * (many ? p.tile_rows : kWarps * kKv8Tile) + blockIdx.y * kKv8Tile;
+    };
+    const int64_t row0 = row_at(p, cut.b, many ? cut.hg : cut.hg * p.heads + static_cast<int>(blockIdx.y), first);
     const int wide = nr > 4 ? 8 : (nr > 2 ? 4 : nr);  // warps that have rows of their own
     const int sub = warp / wide, subs = 8 / wide;
     for (int r0 = 0; r0 < nr; r0 += wide) {
@@ -873,10 +788,18 @@ cudaError_t launch_kv8_t(const Kv8LaunchArgs &a)
     }
     kern<<<a.grid, kThreads, Kv8Cfg<D>::SMEM, a.stream>>>(a.k, a.v, a.p);
     e = cudaGetLastError();
-    if (e != cudaSuccess || a.grid < 2) return e;
+    return e == cudaSuccess ? launch_kv8_join(a, D, Elem<T>::BF16) : e;
+}
+
+template <int D, typename T>
+cudaError_t launch_join_t(const Kv8LaunchArgs &a)
+{
+    if (a.grid < 2) return cudaSuccess;
+    const bool many = a.p.tile_rows > kKv8Tile;
     // no more items are cut than there are items, or cuts
-    const int64_t items = static_cast<int64_t>(a.p.b) * a.p.head_groups * a.p.tiles;
-    const dim3 blocks(static_cast<unsigned>(items < a.grid - 1 ? items : a.grid - 1), static_cast<unsigned>(a.p.heads));
+    const int64_t items = static_cast<int64_t>(a.p.b) * (many ? a.p.h_kv : a.p.head_groups) * a.p.tiles;
+    const dim3 blocks(static_cast<unsigned>(items < a.grid - 1 ? items : a.grid - 1),
+                      static_cast<unsigned>(many ? a.p.tile_rows / kKv8Tile : a.p.heads));
     attn_kv8_join_kernel<D, T><<<blocks, 256, 0, a.stream>>>(a.p, a.grid);
     return cudaGetLastError();
 }
@@ -888,6 +811,12 @@ cudaError_t launch_kv8_rows(const Kv8LaunchArgs &a)
 }
 
 }  // namespace
+
+cudaError_t launch_kv8_join(const Kv8LaunchArgs &a, int d, bool bf16)
+{
+    if (d == 64) return bf16 ? launch_join_t<64, __nv_bfloat16>(a) : launch_join_t<64, __half>(a);
+    return bf16 ? launch_join_t<128, __nv_bfloat16>(a) : launch_join_t<128, __half>(a);
+}
 
 cudaError_t launch_kv8(const Kv8LaunchArgs &a, int d, bool bf16)
 {

@@ -20,12 +20,13 @@ struct Kv8Params {
     const void *q;               // [b, h, sq, d] fp16 / bf16
     void *o;                     // the same
     float *lse;                  // [b, h, sq] or nullptr
+    const uint8_t *v_pool;       // [num_pages, page_size, h_kv, d] (read directly for its NaNs only)
     const float *k_scale, *v_scale;  // [num_pages, h_kv, page_size >> block_shift]
     const int32_t *seqlens;      // [b]
     const int32_t *block_table;  // [b, pages_per_seq]
     uint32_t *status;
-    float *o_part;               // [2 * grid][8][16][d]: parts of the items that several CTAs share
-    float *ml_part;              // [2 * grid][8][16][2]: their reference (log2) and sum
+    float *o_part;               // [2 * grid][8][16][d], or [2 * grid][256][d]: parts of the items that several CTAs share
+    float *ml_part;              // [2 * grid][8][16][2] or [2 * grid][256][2]: their reference (log2) and sum
     Kv8Cut *cut;                 // [grid]
     float sl2e;                  // scale * log2(e)
     int32_t b, h_kv;
@@ -33,7 +34,8 @@ struct Kv8Params {
     int32_t head_groups;         // h_kv / heads
     int32_t unit_keys;           // 32 * 8 / heads
     int32_t sq, rows;            // rows = (h / h_kv) * sq query rows of one key head
-    int32_t tile_rows, tiles;    // query rows of an item: 8 or 16; ceil(rows / tile_rows)
+    int32_t tile_rows, tiles;    // query rows of an item: 8, 16 or 256; ceil(rows / tile_rows)
+    int32_t box;                 // tokens of a copy (256 rows): 128, 64, 32 or 16, a divisor of page_size
     int32_t cap;                 // pages_per_seq * page_size
     int32_t page_size, pages_per_seq, num_pages, block_shift;
     int32_t causal;
@@ -41,8 +43,9 @@ struct Kv8Params {
 };
 
 constexpr int kKv8MaxCtas = 160;  // CTAs of a launch at most (sizes the workspace)
-constexpr int kKv8Instances = 8;  // head dim {64, 128} x {fp16, bf16} x {8, 16 rows}
+constexpr int kKv8Instances = 12;  // head dim {64, 128} x {fp16, bf16} x {8, 16, 256 rows}
 constexpr int kKv8Heads = 8;       // key heads of an item at most
+constexpr int kKv8WideRows = 256;  // query rows of an item of the kernel for many
 constexpr int kKv8Tile = 16;      // query rows of an item
 
 struct Kv8LaunchArgs {
@@ -53,6 +56,8 @@ struct Kv8LaunchArgs {
     std::atomic<int> *attr_ready;  // the library's flags, for the current device: shared-memory opt-in set, per instance
 };
 
-cudaError_t launch_kv8(const Kv8LaunchArgs &a, int d, bool bf16);
+cudaError_t launch_kv8(const Kv8LaunchArgs &a, int d, bool bf16);       // tile_rows 8 or 16
+cudaError_t launch_kv8_wide(const Kv8LaunchArgs &a, int d, bool bf16);  // tile_rows 256
+cudaError_t launch_kv8_join(const Kv8LaunchArgs &a, int d, bool bf16);
 
 }  // namespace attn
