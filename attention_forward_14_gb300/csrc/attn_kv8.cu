@@ -37,10 +37,10 @@
 // 560 clocks for 16 of them against 224 for the fp16 products they replace.)
 //
 // Softmax, in log2: x = ks scale log2(e) (q . k8) + log2(vs).  P = 2^(x - m +
-// 10) carries the value scale, so O needs no product with it, and the sum of
+// 6) carries the value scale, so O needs no product with it, and the sum of
 // the weights is sum(P) / vs, in fp32.  m follows the maximum of x lazily: it
 // is raised (and O and the sum rescaled) only when some x exceeds it by more
-// than 4, so P <= 2^14.
+// than 8, so P <= 2^14.
 #include "attn_kv8_common.cuh"
 
 namespace attn {

@@ -10,7 +10,7 @@ namespace attn {
 
 // P = 2^(x - m + kOffset) against a reference m that is raised when some x
 // exceeds it by more than kSlack: P <= 2^14, within fp16.
-constexpr float kOffset = 10.f, kSlack = 4.f;
+constexpr float kOffset = 6.f, kSlack = 8.f;
 enum : uint32_t { SITE_KV8_FULL = 40, SITE_KV8_EMPTY = 41, SITE_KV8_Q = 42, SITE_KV8_CONV = 43, SITE_KV8_S = 44,
                   SITE_KV8_P = 45, SITE_KV8_O = 46 };
 

@@ -9,13 +9,13 @@
 // CTAs share is joined by the same kernel: 256 items of a 2048-token chunk
 // fill 152 CTAs evenly, which whole items would not (two rounds, 84%).
 //
-// A CTA, 16 warps:
+// A CTA, 12 warps:
 //   warps 0-3, 4-7  softmax group t, one thread to a row of Q tile t (128
 //                   rows); it also brings its row of Q and stores its row of O
 //   warp  8         issues the matrix products
 //   warp  9         copies raw K and V tiles (128 keys, TMA) and their scales
-//   warps 12-15     convert raw tiles to fp16 in the swizzled layout that the
-//                   products read
+//   warps 10, 11    convert raw K and V tiles to fp16 in the swizzled layout
+//                   that the products read
 // S_t = Q_t K_j^T and O_t += P_t V_j accumulate in tensor memory (128 lanes x
 // 128 or d columns of fp32 for each tile); the softmax group overwrites S_t
 // with P_t in fp16.  While one group works on its tile, the tensor cores work
@@ -39,8 +39,9 @@ namespace attn {
 namespace {
 
 constexpr int kTileRows = 128, kItemRows = 2 * kTileRows, kTileKeys = 128;
-constexpr int kThreads = 512;
-constexpr int kSoftmaxRegs = 200, kOtherRegs = 56;  // 256 * 200 + 256 * 56 = 512 * 128
+constexpr int kTeam = 3;  // warps that convert K tiles, and as many V tiles
+constexpr int kThreads = kTeam == 1 ? 384 : 512;
+constexpr int kSoftmaxRegs = kTeam == 1 ? 208 : 200, kOtherRegs = kTeam == 1 ? 88 : 56;
 constexpr int kRefRing = 8;
 
 template <int D>
@@ -48,7 +49,7 @@ struct WideCfg {
     static constexpr int PANEL = kTileRows * 128;        // 128 rows of 64 fp16 values, 128-byte swizzle
     static constexpr int TILE = PANEL * (D / 64);        // a Q tile, or a converted K or V tile
     static constexpr int RAW = kTileKeys * D;            // a raw tile
-    static constexpr int CONV_SLOTS = D == 128 ? 3 : 4, RAW_SLOTS = D == 128 ? 4 : 8;
+    static constexpr int CONV_SLOTS = 4, RAW_SLOTS = D == 128 ? 2 : 8;
     static constexpr int CTL = 1024;
     static constexpr int Q_OFF = CTL;
     static constexpr int CONV_OFF = Q_OFF + 2 * TILE;
@@ -177,6 +178,14 @@ __device__ __forceinline__ void wide_next(const Kv8Params &p, WidePlace &c)
     c.n = wide_units(p, c.len, c.blk);
 }
 
+// A store into a converted tile, ordered with the fence and the arrival that
+// follow it (volatile statements keep their order) but not with the reads of
+// the raw tile, which the compiler may move ahead of it.
+__device__ __forceinline__ void st_tile(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d));
+}
+
 template <int D, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -217,10 +226,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < C::RAW_SLOTS; ++i) {
             // the bytes' announcement and the scales: K's and V's with K (even slots), V's with V
             mbar_init(B(ctl->raw_full[i]), i % 2 == 0 ? 17 : 9);
-            mbar_init(B(ctl->raw_empty[i]), 4);  // the converting warps
+            mbar_init(B(ctl->raw_empty[i]), kTeam);  // the warps that convert its tile
         }
         for (int i = 0; i < C::CONV_SLOTS; ++i) {
-            mbar_init(B(ctl->conv_full[i]), 4);
+            mbar_init(B(ctl->conv_full[i]), kTeam);
             mbar_init(B(ctl->conv_empty[i]), 1);
         }
         for (int t = 0; t < 2; ++t) {
@@ -312,93 +321,92 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             for (uint32_t i = n > C::RAW_SLOTS ? n - C::RAW_SLOTS : 0u; i < n; ++i)
                 drain_wait(B(ctl->raw_full[i % C::RAW_SLOTS]), (i / C::RAW_SLOTS) & 1u, p.timeout_ns);
-        } else if (warp >= 12) {
+        } else if (warp >= 10 && warp < 10 + 2 * kTeam) {
             // -------------------------------------------------------- conversion
-            // A warp converts 32 keys of a tile: eight at a time, 16 values
-            // to a lane, which for odd keys are the other half of the row than
-            // for even ones, so that neither the raw reads nor the writes of
-            // eight lanes meet in a bank.
-            const int w = warp - 12;
-            uint32_t n = 0u, tiles = 0u;  // raw tiles taken, key tiles begun
+            // One warp converts the K tiles and one the V tiles, eight keys
+            // at a time: 16 values to a lane, which for odd keys are the
+            // other half of the row than for even ones, so that neither the
+            // raw reads nor the writes of eight lanes meet in a bank.
+            const int kv = warp & 1, wi = (warp - 10) >> 1;
+            constexpr int PASSES = D == 128 ? 2 : 1;
+            // where a lane's 16 values lie in eight raw rows, and where their two halves go
+            uint32_t raw_at[PASSES], out_at[PASSES][2];
+#pragma unroll
+            for (int h = 0; h < PASSES; ++h) {
+                const int r = lane >> 2, c = (lane & 3) + (D == 128 ? 4 * ((r & 1) ^ h) : 0);
+                raw_at[h] = r * D + (D == 128 ? c ^ r : c ^ ((r >> 1) & 3)) * 16;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) out_at[h][i] = (c >> 2) * C::PANEL + r * 128 + (((2 * (c & 3) + i) ^ r) << 4);
+            }
+            uint32_t tiles = 0u;
             bool ok = true;
             for (int it = 0; ok && it < n_units;) {
                 const WideSeen seen = wide_seen(p, at.len, at.blk);
                 const int j_end = min(at.n, at.j + n_units - it);
-                for (int j = at.j; ok && seen.end > 0 && j < j_end; ++j) {
-                    const int left = at.len - j * kTileKeys;                // cached keys from the tile's first on
-                    const bool partly = (j + 1) * kTileKeys > seen.all;     // some row does not see some key
+                for (int j = at.j; ok && seen.end > 0 && j < j_end; ++j, ++tiles) {
+                    const int left = at.len - j * kTileKeys;                         // cached keys from the tile's first on
+                    const bool whole = (j + 1) * kTileKeys <= (kv ? seen.all : at.len);  // nothing to take out
+                    const uint32_t n = 2u * tiles + kv, rs = n % C::RAW_SLOTS, cs = n % C::CONV_SLOTS;
+                    ok = warp_waits(B(ctl->raw_full[rs]), (n / C::RAW_SLOTS) & 1u, SITE_KV8_FULL);
+                    if (!ok) break;
+                    const float sc = ctl->scales[rs][lane & 15];
+                    float ref = sc;
+#pragma unroll
+                    for (int off = 4; off > 0; off >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, off));
+                    const float vref = __shfl_sync(0xffffffffu, ref, 8);  // of a K slot
+                    if (kv == 0 && wi == 0 && lane == 0) ctl->refs[tiles % kRefRing] = make_float2(ref, vref);
+                    const float mul = ref > 0.f ? sc / ref : 0.f;  // lanes 0..7: of keys 16 lane ..
+                    ok = warp_waits(B(ctl->conv_empty[cs]), ((n / C::CONV_SLOTS) & 1u) ^ 1u, SITE_KV8_CONV);
+                    if (!ok) break;
+                    const uint8_t *raw = smem + C::RAW_OFF + rs * C::RAW;
+                    const uint32_t out = sConv + cs * C::TILE;
+                    uint32_t nans = 0u;
+                                        // eight keys at a time: a lane's row is 8 q + (lane >> 2), so only q moves its addresses
 #pragma unroll 1
-                    for (int kv = 0; kv < 2; ++kv, ++n) {
-                        const uint32_t rs = n % C::RAW_SLOTS, cs = n % C::CONV_SLOTS;
-                        ok = warp_waits(B(ctl->raw_full[rs]), (n / C::RAW_SLOTS) & 1u, SITE_KV8_FULL);
-                        if (!ok) break;
-                        const float sc = ctl->scales[rs][lane & 7];
-                        float ref = sc;
+                    for (int q = wi; q < 16; q += kTeam) {
+                        const float m = __shfl_sync(0xffffffffu, mul, q >> 1);
+                        uint4 v[PASSES];
 #pragma unroll
-                        for (int off = 4; off > 0; off >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, off));
-                        if (kv == 0 && w == 0) {
-                            float vref = ctl->scales[rs][8 + (lane & 7)];
+                        for (int h = 0; h < PASSES; ++h) v[h] = *reinterpret_cast<const uint4 *>(raw + raw_at[h] + q * 8 * D);
 #pragma unroll
-                            for (int off = 4; off > 0; off >>= 1) vref = fmaxf(vref, __shfl_xor_sync(0xffffffffu, vref, off));
-                            if (lane == 0) ctl->refs[tiles % kRefRing] = make_float2(ref, vref);
-                        }
-                        const float mul = ref > 0.f ? sc / ref : 0.f;  // of keys 16 (lane & 7) ..
-                        const float m0 = __shfl_sync(0xffffffffu, mul, 2 * w), m1 = __shfl_sync(0xffffffffu, mul, 2 * w + 1);
-                        ok = warp_waits(B(ctl->conv_empty[cs]), ((n / C::CONV_SLOTS) & 1u) ^ 1u, SITE_KV8_CONV);
-                        if (!ok) break;
-                        const uint8_t *raw = smem + C::RAW_OFF + rs * C::RAW;
-                        const uint32_t out = sConv + cs * C::TILE;
-                        uint32_t nans = 0u;
-                        constexpr int PASSES = D == 128 ? 2 : 1, KEYS = 8;
+                        for (int h = 0; h < PASSES; ++h) {
+                            uint32_t x[4] = {v[h].x, v[h].y, v[h].z, v[h].w};
+                            if (!whole) {
 #pragma unroll
-                        for (int i = 0; i < 32 / KEYS; ++i) {
-                            const float m = i < 2 ? m0 : m1;
-                            const uint32_t mm = Pair<__half>::put(m, m);
-                            const int row = w * 32 + i * KEYS + (lane >> 2);
-#pragma unroll
-                            for (int h = 0; h < PASSES; ++h) {
-                                // 16-byte chunk c of the raw row
-                                const int c = (lane & 3) + (D == 128 ? 4 * ((row & 1) ^ h) : 0);
-                                const int sw = D == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3);
-                                uint4 v = *reinterpret_cast<const uint4 *>(raw + row * D + sw * 16);
-                                if (row >= left) v = make_uint4(0u, 0u, 0u, 0u);
-                                uint32_t x[4] = {v.x, v.y, v.z, v.w};
-                                if (kv == 1 && partly) {
-                                    // a NaN that some row does not see must not reach it by way of 0 * NaN: it
-                                    // is taken out here and put into the rows that see it when they are stored
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e) {
+                                for (int e = 0; e < 4; ++e) {
+                                    if (q * 8 + (lane >> 2) >= left) x[e] = 0u;
+                                    if (kv == 1) {
+                                        // a NaN that some row does not see must not reach it by way of 0 * NaN: it is
+                                        // taken out here and put into the rows that see it when they are stored
                                         const uint32_t nb = nan_bytes(x[e]);
                                         nans |= nb;
                                         x[e] &= ~((nb >> 7) * 0xFFu);
                                     }
                                 }
-                                uint32_t y[8];
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) e4m3x4_to_f16(x[e], y[2 * e], y[2 * e + 1]);
-                                if (m != 1.f) {
-#pragma unroll
-                                    for (int e = 0; e < 8; ++e) {
-                                        const __half2 q = __hmul2(*reinterpret_cast<const __half2 *>(&y[e]),
-                                                                  *reinterpret_cast<const __half2 *>(&mm));
-                                        y[e] = *reinterpret_cast<const uint32_t *>(&q);
-                                    }
-                                }
-                                const uint32_t dst = out + (c >> 2) * C::PANEL + row * 128;
-                                const int o = 2 * (c & 3);
-                                st_shared_v4(dst + ((o ^ (row & 7)) << 4), y[0], y[1], y[2], y[3]);
-                                st_shared_v4(dst + (((o + 1) ^ (row & 7)) << 4), y[4], y[5], y[6], y[7]);
                             }
-                        }
-                        if (nans) *reinterpret_cast<volatile uint32_t *>(&ctl->v_nan) = 1u;
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(B(ctl->conv_full[cs]));
-                            mbar_arrive(B(ctl->raw_empty[rs]));
+                            uint32_t y[8];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) e4m3x4_to_f16(x[e], y[2 * e], y[2 * e + 1]);
+                            if (m != 1.f) {
+                                const uint32_t mm = Pair<__half>::put(m, m);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    const __half2 z = __hmul2(*reinterpret_cast<const __half2 *>(&y[e]),
+                                                              *reinterpret_cast<const __half2 *>(&mm));
+                                    y[e] = *reinterpret_cast<const uint32_t *>(&z);
+                                }
+                            }
+                            st_tile(out + out_at[h][0] + q * 1024, y[0], y[1], y[2], y[3]);
+                            st_tile(out + out_at[h][1] + q * 1024, y[4], y[5], y[6], y[7]);
                         }
                     }
-                    ++tiles;
+                    if (nans) *reinterpret_cast<volatile uint32_t *>(&ctl->v_nan) = 1u;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(B(ctl->conv_full[cs]));
+                        mbar_arrive(B(ctl->raw_empty[rs]));
+                    }
                 }
                 it += j_end - at.j;
                 wide_next(p, at);
@@ -528,7 +536,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
                     down = __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
                 }
-                coef = p.sl2e * down;
+                // a negative scale turns Q's signs, so that a masked score is -inf in every case
+                coef = fabsf(p.sl2e) * down;
+                const uint32_t turn = p.sl2e < 0.f ? 0x80008000u : 0u;
 #pragma unroll 4
                 for (int c = 0; c < D / 8; ++c) {
                     uint4 v = valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
@@ -541,27 +551,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         v = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    st_shared_v4(dst + (c >> 3) * C::PANEL + (((c & 7) ^ (row_in_tile & 7)) << 4), v.x, v.y, v.z, v.w);
+                    st_shared_v4(dst + (c >> 3) * C::PANEL + (((c & 7) ^ (row_in_tile & 7)) << 4), v.x ^ turn, v.y ^ turn, v.z ^ turn,
+                                 v.w ^ turn);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(B(ctl->q_full[t]));
-                const bool neg = p.sl2e < 0.f;
                 for (int i = 0; i < n; ++i) {
                     ok = warp_waits(B(ctl->s_full[t]), s_it & 1u, SITE_KV8_S);
                     if (!ok) break;
                     ++s_it;
                     tc_fence_after();
-                    uint32_t sr[128];
-                    tmem_ld128_wait(tS, sr);
                     const float2 ref = *const_cast<const float2 *>(&ctl->refs[(tiles + i) % kRefRing]);
                     const float vs = ref.y > 0.f ? ref.y : 1.f;
-                    const float lv = lg2_approx(vs), c = coef * ref.x;
+                    const float lv = lg2_approx(vs), c = fmaxf(coef * ref.x, 1e-30f);
                     const int vis = lim - (at.j + i) * kTileKeys;  // columns >= vis are masked
                     const bool masked = __any_sync(0xffffffffu, vis < kTileKeys);
-                    if (masked) mask_columns(sr, vis, neg);
-                    const float raw = neg ? row_extreme<true>(sr) : row_extreme<false>(sr);
-                    const float mx = raw == (neg ? INFINITY : -INFINITY) ? -INFINITY : fmaf(raw, c, lv);
+                    uint32_t s[128];
+                    tmem_ld128_wait(tS, s);
+                    if (masked) mask_columns(s, vis, false);
+                    const float raw = row_extreme<false>(s);
+                    const float mx = fmaf(raw, c, lv);
                     const float m_new = fmaxf(m, mx);
                     const bool need = m_new > m + kSlack;
                     if (__any_sync(0xffffffffu, need)) {
@@ -571,8 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         m = m_new;
                     }
                     const float use = (m == -INFINITY ? 0.f : m - kOffset) - lv;
-                    const float2 sums = masked ? exp_store_tile<__half, true, false>(sr, vis, c, use, tS, B(ctl->p_half[t]))
-                                               : exp_store_tile<__half, false, false>(sr, vis, c, use, tS, B(ctl->p_half[t]));
+                    const float2 sums = exp_store_tile<__half, false, false>(s, 0, c, use, tS, B(ctl->p_half[t]));
                     l = fmaf(sums.x, rcp_approx(vs), l);
                     warp_announce_tmem(B(ctl->p_full[t]));
                 }
