@@ -1,5 +1,5 @@
 // Attention of many new queries over an e4m3 paged cache (chunks of a
-// prompt, long drafts): the operation of attn_kv8.cu on the tensor cores'
+// prompt, long drafts; more than 48 rows of a key head): the operation of attn_kv8.cu on the tensor cores'
 // tcgen05 path.
 //
 // Work.  An item is 256 query rows of one key head of one batch element
@@ -49,11 +49,13 @@ struct WideCfg {
     static constexpr int PANEL = kTileRows * 128;        // 128 rows of 64 fp16 values, 128-byte swizzle
     static constexpr int TILE = PANEL * (D / 64);        // a Q tile, or a converted K or V tile
     static constexpr int RAW = kTileKeys * D;            // a raw tile
-    static constexpr int CONV_SLOTS = 4, RAW_SLOTS = D == 128 ? 2 : 8;
+    // without a second Q tile there is room for two raw slots more (d = 128): 119 -> 101 us at 64 rows
+    static constexpr int CONV_SLOTS = 4, RAW_SLOTS = D == 128 ? 2 : 8, RAW_SLOTS_ONE = D == 128 ? 4 : 8;
     static constexpr int CTL = 1024;
     static constexpr int Q_OFF = CTL;
     static constexpr int CONV_OFF = Q_OFF + 2 * TILE;
     static constexpr int RAW_OFF = CONV_OFF + CONV_SLOTS * TILE;
+    static_assert((RAW_SLOTS_ONE - RAW_SLOTS) * RAW <= TILE, "the second Q tile's room");
     static constexpr int SMEM = RAW_OFF + RAW_SLOTS * RAW + 1024;  // +1 KiB for alignment
     static constexpr int TMEM_O = 2 * kTileKeys;         // O_t at TMEM_O + t * 128
     static_assert(SMEM <= 232448, "shared memory budget");
@@ -199,7 +201,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t base = (raw_addr + 1023u) & ~1023u;
     uint8_t *smem = smem_raw + (base - raw_addr);
     WideCtl *ctl = reinterpret_cast<WideCtl *>(smem);
-    const uint32_t sQ = base + C::Q_OFF, sConv = base + C::CONV_OFF, sRaw = base + C::RAW_OFF;
+    // with rows for one Q tile only, the converted tiles begin where the second
+    // would lie and more raw tiles are on their way
+    const bool one = p.rows <= kTileRows && C::RAW_SLOTS_ONE != C::RAW_SLOTS;
+    const uint32_t raw_slots = one ? C::RAW_SLOTS_ONE : C::RAW_SLOTS;  // a power of two
+    const uint32_t raw_shift = 31 - __clz(raw_slots);
+    const uint32_t sQ = base + C::Q_OFF, sConv = base + C::CONV_OFF - (one ? C::TILE : 0);
+    const uint32_t raw_off = one ? C::RAW_OFF - C::TILE : C::RAW_OFF, sRaw = base + raw_off;
     auto B = [&](const uint64_t &bar) { return smem_addr(&bar); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile uint32_t *abort_flag = &ctl->abort;
@@ -223,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::RAW_SLOTS; ++i) {
+        for (uint32_t i = 0; i < raw_slots; ++i) {
             // the bytes' announcement and the scales: K's and V's with K (even slots), V's with V
             mbar_init(B(ctl->raw_full[i]), i % 2 == 0 ? 17 : 9);
             mbar_init(B(ctl->raw_empty[i]), kTeam);  // the warps that convert its tile
@@ -295,8 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int64_t sc = (static_cast<int64_t>(page) * p.h_kv + at.kvh) * blocks_per_page + (off >> p.block_shift);
 #pragma unroll 1
                     for (int kv = 0; ok && kv < 2; ++kv, ++n) {
-                        const uint32_t st = n % C::RAW_SLOTS, bar = B(ctl->raw_full[st]);
-                        ok = warp_waits(B(ctl->raw_empty[st]), ((n / C::RAW_SLOTS) & 1u) ^ 1u, SITE_KV8_EMPTY);
+                        const uint32_t st = n & (raw_slots - 1), bar = B(ctl->raw_full[st]);
+                        ok = warp_waits(B(ctl->raw_empty[st]), ((n >> raw_shift) & 1u) ^ 1u, SITE_KV8_EMPTY);
                         if (!ok) break;
                         if (lane == 0) mbar_arrive_expect_tx(bar, boxes * p.box * D);
                         if (copies)
@@ -319,8 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 it += j_end - at.j;
                 wide_next(p, at);
             }
-            for (uint32_t i = n > C::RAW_SLOTS ? n - C::RAW_SLOTS : 0u; i < n; ++i)
-                drain_wait(B(ctl->raw_full[i % C::RAW_SLOTS]), (i / C::RAW_SLOTS) & 1u, p.timeout_ns);
+            for (uint32_t i = n > raw_slots ? n - raw_slots : 0u; i < n; ++i)
+                drain_wait(B(ctl->raw_full[i & (raw_slots - 1)]), (i >> raw_shift) & 1u, p.timeout_ns);
         } else if (warp >= 10 && warp < 10 + 2 * kTeam) {
             // -------------------------------------------------------- conversion
             // One warp converts the K tiles and one the V tiles, eight keys
@@ -346,8 +354,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = at.j; ok && seen.end > 0 && j < j_end; ++j, ++tiles) {
                     const int left = at.len - j * kTileKeys;                         // cached keys from the tile's first on
                     const bool whole = (j + 1) * kTileKeys <= (kv ? seen.all : at.len);  // nothing to take out
-                    const uint32_t n = 2u * tiles + kv, rs = n % C::RAW_SLOTS, cs = n % C::CONV_SLOTS;
-                    ok = warp_waits(B(ctl->raw_full[rs]), (n / C::RAW_SLOTS) & 1u, SITE_KV8_FULL);
+                    const uint32_t n = 2u * tiles + kv, rs = n & (raw_slots - 1), cs = n % C::CONV_SLOTS;
+                    ok = warp_waits(B(ctl->raw_full[rs]), (n >> raw_shift) & 1u, SITE_KV8_FULL);
                     if (!ok) break;
                     const float sc = ctl->scales[rs][lane & 15];
                     float ref = sc;
@@ -358,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float mul = ref > 0.f ? sc / ref : 0.f;  // lanes 0..7: of keys 16 lane ..
                     ok = warp_waits(B(ctl->conv_empty[cs]), ((n / C::CONV_SLOTS) & 1u) ^ 1u, SITE_KV8_CONV);
                     if (!ok) break;
-                    const uint8_t *raw = smem + C::RAW_OFF + rs * C::RAW;
+                    const uint8_t *raw = smem + raw_off + rs * C::RAW;
                     const uint32_t out = sConv + cs * C::TILE;
                     uint32_t nans = 0u;
                                         // eight keys at a time: a lane's row is 8 q + (lane >> 2), so only q moves its addresses

@@ -31,6 +31,11 @@ CASES = [
     (1, 6, 3, 130, 64, 128, 4, 16, "fp16", True, (490,)),
     (1, 2, 1, 300, 128, 256, 3, 32, "bf16", False, (650,)),
     (5, 3, 3, 2, 128, 16, 12, 16, "bf16", True, (0, 0, 0, 0, 0)),      # nothing cached
+    (2, 8, 2, 11, 128, 48, 9, 16, "fp16", True, (430, 25)),            # 44 rows: three tiles of 16
+    (3, 2, 1, 25, 64, 16, 30, 16, "bf16", True, (480, 0, 24)),         # 50 rows, one Q tile; no or too few keys
+    (2, 4, 2, 90, 128, 16, 40, 16, "bf16", True, (640, 89)),           # 180 rows, pages of 16
+    (2, 6, 2, 120, 64, 96, 7, 32, "fp16", False, (600, 1)),            # 360 rows
+    (1, 2, 2, 700, 128, 128, 11, 128, "fp16", True, (1400,)),          # items that several CTAs share
     (40, 2, 1, 1, 64, 64, 3, 64, "bf16", True, tuple((7 * i) % 193 for i in range(40))),
 ]
 
@@ -224,7 +229,8 @@ def test_two_streams_and_graphs_with_new_lengths():
 def test_queries_of_one_head_do_not_depend_on_their_neighbours():
     """A key that only later queries see takes no part in the earlier ones,
     whatever it holds: NaN in the last cached tokens."""
-    for case in ((1, 2, 1, 4, 128, 64, 4, 16, "bf16", True, (203,)), (1, 3, 3, 40, 64, 64, 4, 16, "fp16", True, (203,))):
+    for case in ((1, 2, 1, 4, 128, 64, 4, 16, "bf16", True, (203,)), (1, 3, 3, 40, 64, 64, 4, 16, "fp16", True, (203,)),
+                 (1, 4, 2, 40, 128, 64, 4, 16, "fp16", True, (203,)), (1, 1, 1, 190, 64, 64, 4, 32, "bf16", True, (203,))):
         st = draw(case, seed=51, nan=False)
         sq, n = case[3], 203
         clean = call(st, True)
