@@ -157,18 +157,6 @@ def _stream_handle(stream, device):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _raw_stream(stream, device):
-    """The same as a number, without building torch's stream object for the
-    current one (2 us of the 20 that a small call takes on the host)."""
-    import torch
-    if stream is not None:
-        return stream.cuda_stream
-    current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if current is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    return current(device.index)
-
-
 class _OnDevice:
     """Make `device` current for the call (the library works on the current
     device); does nothing when it already is."""
@@ -600,93 +588,26 @@ def attn_bwd_varlen(q, k, v, o, dout, lse, cu_seqlens_q, cu_seqlens_k, max_seqle
     return dq, dk, dv
 
 
-_Strides = ctypes.c_int64 * 3
+_fast = None
 
 
-def _as_dense(name, t):
-    """A [b, h, s, d] tensor, or a packed [total, h, d] one as b = 1: its shape and its strides (b, head, token)."""
-    shape, st = t.shape, t.stride()
-    if len(shape) == 4:
-        b, h, s, d = shape
-        sb, sh, ss, sd = st
-    elif len(shape) == 3:
-        s, h, d = shape
-        ss, sh, sd = st
-        b, sb = 1, 0
-    else:
-        raise AttnError(-2, f"{name} must be [b, h, s, d] or [total, h, d]")
-    if sd != 1 and d > 1 and t.numel() > 0:
-        raise AttnError(-2, f"the {d} values of a head of {name} must be contiguous")
-    # an axis of one has no stride of its own
-    return b, h, s, d, _Strides(sb if b > 1 else 0, sh if h > 1 else 0, ss if s > 1 else 0)
+def _marshal():
+    """The C++ module that checks the tensors of the operators below,
+    allocates their outputs and calls the library (loaded once)."""
+    global _fast
+    if _fast is None:
+        load()
+        try:
+            from . import _marshal as m
+        except ImportError as e:
+            raise AttnError(-8, f"_marshal.so cannot be loaded ({e}); run python -m attention_forward_14_gb300.build") from e
+        m.set_error(AttnError)
+        _fast = m
+    return _fast
 
 
-def _output(name, t, ref):
-    """An output shaped and typed like its input `ref`: allocated (contiguous) or checked; its strides as above."""
-    import torch
-    if t is None:
-        t = torch.empty_like(ref, memory_format=torch.contiguous_format)
-    elif t.shape != ref.shape or t.dtype != ref.dtype or t.device != ref.device:
-        raise AttnError(-2, f"{name} must be shaped and typed like its input, on its device")
-    return t, _as_dense(name, t)[4]
-
-
-def _rotation(cos, sin, device):
-    """(pointer, pointer, rot, table_len) of the rotation's tables; nothing for none."""
-    import torch
-    if cos is None or sin is None:
-        if cos is not sin:
-            raise AttnError(-1, "cos and sin must both be given or both be None")
-        return None, None, 0, 0
-    if cos.dim() != 2 or cos.shape != sin.shape:
-        raise AttnError(-2, "cos and sin must be [table_len, rot / 2]")
-    if cos.dtype != torch.float32 or sin.dtype != torch.float32 or cos.device != device or sin.device != device or \
-            not (cos.is_contiguous() and sin.is_contiguous()):
-        raise AttnError(-4, "cos and sin must be contiguous fp32 tensors on the inputs' device")
-    length, half = cos.shape
-    return cos.data_ptr(), sin.data_ptr(), 2 * half, length
-
-
-def _positions(positions, b, s, packed, cos, device):
-    """(pointer, stride over b) of the positions of a dense [b, s] or packed [total] batch."""
-    import torch
-    if positions is None:
-        if packed and cos is not None:
-            raise AttnError(-1, "a packed batch needs positions: they start again in every sequence")
-        return None, 0
-    shape = positions.shape
-    if positions.dtype != torch.int32 or positions.device != device or \
-            not (shape == (s,) or (not packed and shape == (b, s))):
-        raise AttnError(-4, f"positions must be int32 of {s} or (not packed) {b} x {s} on the inputs' device")
-    st = positions.stride()
-    if st[-1] != 1 and s > 1:
-        raise AttnError(-2, "the positions of a sequence must be contiguous")
-    return positions.data_ptr(), st[0] if len(st) == 2 and b > 1 else 0
-
-
-def _norm_inputs(q, k, q_weight, k_weight):
-    """Shapes and strides of q and k, and the pointers of their weights."""
-    b, h, s, d, qs = _as_dense("q", q)
-    bk, hkv, sk, dk, ks = _as_dense("k", k)
-    if bk != b or sk != s or dk != d or q.dim() != k.dim():
-        raise AttnError(-2, f"shape mismatch q{tuple(q.shape)} k{tuple(k.shape)}")
-    dt, dev = q.dtype, q.device
-    if not q.is_cuda or k.dtype != dt or k.device != dev:
-        raise AttnError(-4, "q and k must be CUDA tensors of one dtype on one device")
-    for w in (q_weight, k_weight):
-        if w is not None and (w.shape != (d,) or w.dtype != dt or w.device != dev or not w.is_contiguous()):
-            raise AttnError(-2, f"norm weights must be contiguous [{d}] tensors typed like q, on its device")
-    return (b, h, hkv, s, d, qs, ks, q_weight.data_ptr() if q_weight is not None else None,
-            k_weight.data_ptr() if k_weight is not None else None)
-
-
-def _used_on(stream, *tensors):
-    """Tensors allocated here for a call on a stream that was given: their
-    memory is not handed out again before that stream is done with them."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def attn_qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, eps: float = 1e-6,
@@ -702,21 +623,8 @@ def attn_qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, po
     or (packed) [total], None: 0..s-1.  ``interleaved``: adjacent pairs turn
     instead of pairs (i, i + rot/2).  Negative positions are padding (zeros).
     Returns (q_out, k_out), contiguous unless given."""
-    lib = load()
-    b, h, hkv, s, d, qs, ks, wq, wk = _norm_inputs(q, k, q_weight, k_weight)
-    dt, dev = _dtype_code(q), q.device
-    c, sn, rot, length = _rotation(cos, sin, dev)
-    pos, pos_b = _positions(positions, b, s, q.dim() == 3, cos, dev)
-    q_out, qos = _output("q_out", q_out, q)
-    k_out, kos = _output("k_out", k_out, k)
-    with _OnDevice(dev):
-        rc = lib.attn_qk_norm_rope(q.data_ptr(), k.data_ptr(), wq, wk, c, sn, pos, q_out.data_ptr(), k_out.data_ptr(),
-                                   qs, ks, qos, kos, b, h, hkv, s, d, rot, length, pos_b, 1 if interleaved else 0, eps,
-                                   dt, _raw_stream(stream, dev))
-    if rc < 0:
-        _check(rc, lib)
-    _used_on(stream, q_out, k_out)
-    return q_out, k_out
+    return (_fast or _marshal()).qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, q_out,
+                                              k_out, _handle(stream))
 
 
 def attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
@@ -726,70 +634,13 @@ def attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, co
     for a weight that is None.  ``dq`` / ``dk`` may be given (for example
     slices of the fused projection's gradient), with any strides; ``workspace``
     is a CUDA uint8 tensor of qk_norm_rope_bwd_workspace_bytes(d) bytes."""
-    import torch
-    lib = load()
-    b, h, hkv, s, d, qs, ks, wq, wk = _norm_inputs(q, k, q_weight, k_weight)
-    dt, dev = _dtype_code(q), q.device
-    c, sn, rot, length = _rotation(cos, sin, dev)
-    pos, pos_b = _positions(positions, b, s, q.dim() == 3, cos, dev)
-    dq_out, gqs = _output("dq_out", dq_out, q)
-    dk_out, gks = _output("dk_out", dk_out, k)
-    dq, dqs = _output("dq", dq, q)
-    dk, dks = _output("dk", dk, k)
-    dwq = torch.empty(d, dtype=torch.float32, device=dev) if wq is not None else None
-    dwk = torch.empty(d, dtype=torch.float32, device=dev) if wk is not None else None
-    if workspace is None and (wq is not None or wk is not None):
-        workspace = torch.empty(qk_norm_rope_bwd_workspace_bytes(d), dtype=torch.uint8, device=dev)
-    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
-        raise AttnError(-2, "workspace must be a contiguous tensor on the inputs' device")
-    with _OnDevice(dev):
-        rc = lib.attn_qk_norm_rope_bwd(dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), wq, wk, c, sn,
-                                       pos, dq.data_ptr(), dk.data_ptr(), dwq.data_ptr() if wq is not None else None,
-                                       dwk.data_ptr() if wk is not None else None, gqs, gks, qs, ks, dqs, dks, b, h,
-                                       hkv, s, d, rot, length, pos_b, 1 if interleaved else 0, eps, dt,
-                                       workspace.data_ptr() if workspace is not None else None,
-                                       workspace.nbytes if workspace is not None else 0, _raw_stream(stream, dev))
-    if rc < 0:
-        _check(rc, lib)
-    _used_on(stream, dq, dk, dwq, dwk, workspace)
-    return dq, dk, dwq, dwk
+    return (_fast or _marshal()).qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, cos, sin, positions, eps,
+                                                  interleaved, dq, dk, workspace, _handle(stream))
 
 
 def qk_norm_rope_bwd_workspace_bytes(d: int) -> int:
     lib = load()
     return _check(int(lib.attn_qk_norm_rope_bwd_workspace_bytes(d)), lib)
-
-
-def _check_pools(k_pool, v_pool, k_scale, v_scale, block_table, cache_seqlens, b, hkv, d):
-    """The checks of a paged cache that need the tensors; returns (num_pages, page_size, pages_per_seq, scale_block)."""
-    import torch
-    dev, shape = k_pool.device, k_pool.shape
-    if len(shape) != 4 or shape[2] != hkv or shape[3] != d or v_pool.shape != shape or v_pool.dtype != k_pool.dtype:
-        raise AttnError(-2, f"pools {tuple(shape)} / {tuple(v_pool.shape)} must be [num_pages, page_size, {hkv}, {d}]")
-    num_pages, page_size = shape[0], shape[1]
-    table = block_table.shape
-    if len(table) != 2 or table[0] != b or block_table.dtype != torch.int32:
-        raise AttnError(-2, "block_table must be int32 [b, pages_per_seq]")
-    if cache_seqlens.shape != (b,) or cache_seqlens.dtype != torch.int32:
-        raise AttnError(-4, "cache_seqlens must be an int32 tensor of b elements")
-    if not k_pool.is_cuda or v_pool.device != dev or block_table.device != dev or cache_seqlens.device != dev or \
-            not (k_pool.is_contiguous() and v_pool.is_contiguous() and block_table.is_contiguous() and
-                 cache_seqlens.is_contiguous()):
-        raise AttnError(-2, "pools, block_table and cache_seqlens must be contiguous CUDA tensors on one device")
-    if k_scale is None or v_scale is None:
-        if k_scale is not v_scale:
-            raise AttnError(-1, "k_scale and v_scale must both be given or both be None")
-        return num_pages, page_size, table[1], 0
-    if k_pool.dtype != torch.float8_e4m3fn:
-        raise AttnError(-4, "a cache with scales must be float8_e4m3fn")
-    scales = k_scale.shape
-    if len(scales) != 3 or scales[0] != num_pages or scales[1] != hkv or scales[2] < 1 or page_size % scales[2] != 0 or \
-            v_scale.shape != scales:
-        raise AttnError(-2, "scales must be [num_pages, h_kv, page_size / scale_block]")
-    if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 or k_scale.device != dev or \
-            v_scale.device != dev or not (k_scale.is_contiguous() and v_scale.is_contiguous()):
-        raise AttnError(-4, "scales must be contiguous fp32 tensors on the pools' device")
-    return num_pages, page_size, table[1], page_size // scales[2]
 
 
 def attn_kvcache_append_paged(k_new, v_new, k_pool, v_pool, cache_seqlens, block_table, cos=None, sin=None,
@@ -806,32 +657,8 @@ def attn_kvcache_append_paged(k_new, v_new, k_pool, v_pool, cache_seqlens, block
     [b] says how many of a padded batch's tokens are there.  ``cos`` / ``sin``
     fp32 [at least the capacity, rot / 2]; None: no rotation.  cache_seqlens is
     not updated."""
-    import torch
-    lib = load()
-    if k_new.dim() != 4 or k_new.shape != v_new.shape:
-        raise AttnError(-2, f"k_new{tuple(k_new.shape)} and v_new{tuple(v_new.shape)} must be [b, h_kv, s_new, d]")
-    b, hkv, s, d, ks = _as_dense("k_new", k_new)
-    vs = _as_dense("v_new", v_new)[4]
-    dt, dev = _dtype_code(k_new), k_pool.device
-    num_pages, page_size, pps, block = _check_pools(k_pool, v_pool, k_scale, v_scale, block_table, cache_seqlens, b,
-                                                    hkv, d)
-    if v_new.dtype != k_new.dtype or (block == 0 and k_pool.dtype != k_new.dtype):
-        raise AttnError(-4, "k_new, v_new and a cache without scales must have one dtype")
-    if k_new.device != dev or v_new.device != dev:
-        raise AttnError(-2, "k_new, v_new and the pools must be on one device")
-    if new_seqlens is not None and (new_seqlens.shape != (b,) or new_seqlens.dtype != torch.int32 or
-                                    new_seqlens.device != dev or not new_seqlens.is_contiguous()):
-        raise AttnError(-4, "new_seqlens must be an int32 tensor of b elements on the pools' device")
-    c, sn, rot, length = _rotation(cos, sin, dev)
-    with _OnDevice(dev):
-        rc = lib.attn_kvcache_append_paged(k_new.data_ptr(), v_new.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
-                                           k_scale.data_ptr() if block else None,
-                                           v_scale.data_ptr() if block else None, cache_seqlens.data_ptr(),
-                                           new_seqlens.data_ptr() if new_seqlens is not None else None,
-                                           block_table.data_ptr(), c, sn, ks, vs, b, hkv, s, num_pages, page_size, pps,
-                                           block, d, rot, length, 1 if interleaved else 0, dt, _raw_stream(stream, dev))
-    if rc < 0:
-        _check(rc, lib)
+    (_fast or _marshal()).kvcache_append_paged(k_new, v_new, k_pool, v_pool, cache_seqlens, block_table, cos, sin,
+                                               interleaved, k_scale, v_scale, new_seqlens, _handle(stream))
 
 
 def kvcache_paged_fp8_workspace_bytes(b, h, h_kv, sq, d) -> int:
@@ -848,38 +675,5 @@ def attn_fwd_kvcache_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, cache_seqlen
     tokens (the new ones among them: append first); h / h_kv query heads share
     a key head.  ``workspace``: a CUDA uint8 tensor of
     kvcache_paged_fp8_workspace_bytes bytes.  Returns (o, lse)."""
-    import torch
-    lib = load()
-    if q.dim() != 4 or k_pool.dim() != 4:
-        raise AttnError(-2, "q must be [b, h, sq, d] and the pools [num_pages, page_size, h_kv, d]")
-    b, h, sq, d = q.shape
-    hkv = k_pool.shape[2]
-    dt, dev = _dtype_code(q), q.device
-    if k_scale is None or v_scale is None:
-        raise AttnError(-1, "k_scale and v_scale must be given")
-    num_pages, page_size, pps, block = _check_pools(k_pool, v_pool, k_scale, v_scale, block_table, cache_seqlens, b,
-                                                    hkv, d)
-    if not q.is_contiguous() or dev != k_pool.device:
-        raise AttnError(-2, "q must be contiguous, on the pools' device")
-    if o is None:
-        o = torch.empty_like(q)
-    elif o.shape != q.shape or o.dtype != q.dtype or not o.is_contiguous() or o.device != dev:
-        raise AttnError(-2, "o must be a contiguous tensor shaped and typed like q, on its device")
-    if lse is None:
-        lse = torch.empty((b, h, sq), dtype=torch.float32, device=dev)
-    elif lse.shape != (b, h, sq) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != dev:
-        raise AttnError(-2, "lse must be contiguous fp32 [b, h, sq] on q's device")
-    if workspace is None:
-        workspace = torch.empty(kvcache_paged_fp8_workspace_bytes(b, h, hkv, sq, d), dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise AttnError(-2, "workspace must be a contiguous tensor on q's device")
-    with _OnDevice(dev):
-        rc = lib.attn_fwd_kvcache_paged_fp8(q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(),
-                                            v_scale.data_ptr(), cache_seqlens.data_ptr(), block_table.data_ptr(),
-                                            o.data_ptr(), lse.data_ptr(), b, h, hkv, sq, num_pages, page_size, pps,
-                                            block, d, 1 if causal else 0, d ** -0.5 if scale is None else scale, dt,
-                                            workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev))
-    if rc < 0:
-        _check(rc, lib)
-    _used_on(stream, o, lse, workspace)
-    return o, lse
+    return (_fast or _marshal()).fwd_kvcache_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, cache_seqlens, block_table,
+                                                       causal, scale, o, lse, workspace, _handle(stream))

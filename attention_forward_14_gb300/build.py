@@ -1,4 +1,6 @@
-"""Build libattn_fwd.so (sm_103a) in-tree with nvcc, and its checked variant.
+"""Build libattn_fwd.so (sm_103a) in-tree with nvcc, its checked variant, and
+the Python entry of the operators around the attention (``_marshal.so``, C++
+against torch's headers, linked to the library).
 
 Each translation unit under csrc/ is compiled in parallel, then linked into
 ``attention_forward_14_gb300/libattn_fwd.so``.  The checked variant,
@@ -24,6 +26,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libattn_fwd.so")
 LIB_CHECKED = os.path.join(HERE, "libattn_fwd_checked.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["attn_fwd_api.cu", "inst_d64.cu", "inst_d128_noncausal.cu", "inst_d128_causal.cu", "inst_fp8.cu",
            "attn_bwd_inst.cu", "attn_bwd_inst_varlen.cu", "qk_norm_rope.cu", "kv_append.cu", "attn_kv8.cu",
@@ -53,13 +56,44 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _compile_marshal() -> str:
+    """The object file of csrc/marshal.cpp (host code)."""
+    import sysconfig
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    obj = os.path.join(BUILD, "marshal.o")
+    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-c", os.path.join(CSRC, "marshal.cpp"), "-o", obj,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for d in (inc, os.path.join(inc, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"], cuda,
+              os.path.join(ROOT, "include")):
+        cmd += ["-I", d]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"marshal.cpp failed to compile:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_marshal(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, LIB, "-L", lib, "-ltorch_python", "-ltorch",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"_marshal.so failed to link:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
+
+
 def build(force: bool = False, verbose: bool = False, checked: bool = True) -> str:
     """Build the library (and, with ``checked``, its checked variant) when a
     source is newer than it; returns the library's path."""
     deps = _deps()
     want = [(LIB, False)] + ([(LIB_CHECKED, True)] if checked else [])
     todo = [(lib, chk) for lib, chk in want if force or _stale(lib, deps)]
-    if not todo:
+    marshal = force or _stale(MARSHAL, deps)
+    if not todo and not marshal:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -82,17 +116,22 @@ def build(force: bool = False, verbose: bool = False, checked: bool = True) -> s
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    jobs = [(src, False) for src in SOURCES]
+    jobs = [(src, False) for src in SOURCES] if todo else []
     jobs += [(src, True) for src in CHECKED_SOURCES if any(chk for _, chk in todo)]
-    with ThreadPoolExecutor(max_workers=len(jobs)) as ex:
+    with ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
+        host = ex.submit(_compile_marshal) if marshal else None
         list(ex.map(compile_one, jobs))
+        marshal_obj = host.result() if host else None
     for lib, chk in todo:
         objs = [obj_path(src, chk and src in CHECKED_SOURCES) for src in SOURCES]
         tmp = lib + f".tmp{os.getpid()}"
-        r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
+        r = subprocess.run([cc, *ARCH, "-shared", "-Xlinker", f"-soname={os.path.basename(lib)}", "-o", tmp, *objs],
+                           capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, lib)
+    if marshal_obj:
+        _link_marshal(marshal_obj)
     return LIB
 
 

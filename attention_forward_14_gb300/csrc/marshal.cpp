@@ -1,0 +1,453 @@
+// Python entry of the operators around the attention: checks torch tensors,
+// allocates outputs and workspaces and calls the C ABI (attn_fwd.h), which
+// does the rest.  The same in Python took more host time than the kernels of
+// a small batch take: a decoding step's norm issued in 24 us, now in 6; its
+// append in 14, now in 3; its attention in 26, now in 10.
+//
+// Every function takes its arguments by position (binding.py has the
+// signatures and documents them); None stands for what is left out, and the
+// stream is a number or None.  A failed check raises binding.AttnError.
+#include <Python.h>
+
+#include <cmath>
+#include <string>
+#include <utility>
+
+#include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include "attn_fwd.h"
+
+namespace {
+
+PyObject *g_error = nullptr;  // binding.AttnError
+
+struct Err {
+    int code;
+    std::string msg;
+};
+
+[[noreturn]] void fail(int code, std::string msg) { throw Err{code, std::move(msg)}; }
+
+void check(int rc)
+{
+    if (rc < 0) fail(rc, attn_last_error());
+}
+
+// The tensor of an argument that must be one / may be None.
+const at::Tensor &tensor(PyObject *o, const char *name)
+{
+    if (!THPVariable_Check(o)) fail(ATTN_ERR_NULL, std::string(name) + " must be a tensor");
+    return THPVariable_Unpack(o);
+}
+
+const at::Tensor *maybe(PyObject *o, const char *name) { return o == Py_None ? nullptr : &tensor(o, name); }
+
+void *ptr(const at::Tensor &t) { return t.data_ptr(); }
+void *ptr(const at::Tensor *t) { return t ? t->data_ptr() : nullptr; }
+
+std::string shape_of(const at::Tensor &t)
+{
+    std::string s = "(";
+    for (int64_t n : t.sizes()) s += (s.size() > 1 ? ", " : "") + std::to_string(n);
+    return s + ")";
+}
+
+double number(PyObject *o, const char *name)
+{
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) {
+        PyErr_Clear();
+        fail(ATTN_ERR_SCALE, std::string(name) + " must be a number");
+    }
+    return v;
+}
+
+int truth(PyObject *o)
+{
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) {
+        PyErr_Clear();
+        fail(ATTN_ERR_SHAPE, "a truth value is expected");
+    }
+    return v;
+}
+
+int dtype_code(const at::Tensor &t)
+{
+    if (t.scalar_type() == at::kHalf) return ATTN_FP16;
+    if (t.scalar_type() == at::kBFloat16) return ATTN_BF16;
+    fail(ATTN_ERR_DTYPE, std::string("unsupported dtype ") + c10::toString(t.scalar_type()));
+}
+
+// The stream of a call and the tensors allocated for it: on a stream that was
+// given, their memory is not handed out again before that stream is done.
+class Call {
+public:
+    Call(const at::Tensor &t, PyObject *stream) : device_(t.device()), guard_(t.device()), given_(stream != Py_None)
+    {
+        if (given_) {
+            raw_ = reinterpret_cast<cudaStream_t>(PyLong_AsVoidPtr(stream));
+            if (PyErr_Occurred()) {
+                PyErr_Clear();
+                fail(ATTN_ERR_NULL, "stream must be a stream");
+            }
+        } else {
+            raw_ = c10::cuda::getCurrentCUDAStream(device_.index()).stream();
+        }
+    }
+    void *stream() const { return raw_; }
+    at::Tensor empty(at::IntArrayRef sizes, at::ScalarType type) const
+    {
+        at::Tensor t = at::empty(sizes, at::TensorOptions().dtype(type).device(device_));
+        if (given_ && t.numel() > 0)
+            c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(),
+                                                          c10::cuda::getStreamFromExternal(raw_, device_.index()));
+        return t;
+    }
+
+private:
+    c10::Device device_;
+    c10::cuda::CUDAGuard guard_;
+    bool given_;
+    cudaStream_t raw_ = nullptr;
+};
+
+// A [b, h, s, d] tensor, or a packed [total, h, d] one as b = 1: shape, and
+// the strides of b, of the head and of s (an axis of one has none).
+struct Dense {
+    int64_t b, h, s, d;
+    int64_t st[3];
+};
+
+Dense as_dense(const char *name, const at::Tensor &t)
+{
+    const auto n = t.sizes(), st = t.strides();
+    Dense r;
+    int64_t last;
+    if (n.size() == 4) {
+        r = {n[0], n[1], n[2], n[3], {st[0], st[1], st[2]}};
+        last = st[3];
+    } else if (n.size() == 3) {
+        r = {1, n[1], n[0], n[2], {0, st[1], st[0]}};
+        last = st[2];
+    } else {
+        fail(ATTN_ERR_SHAPE, std::string(name) + " must be [b, h, s, d] or [total, h, d]");
+    }
+    if (last != 1 && r.d > 1 && t.numel() > 0)
+        fail(ATTN_ERR_SHAPE, std::string("the values of a head of ") + name + " must be contiguous");
+    if (r.b <= 1) r.st[0] = 0;
+    if (r.h <= 1) r.st[1] = 0;
+    if (r.s <= 1) r.st[2] = 0;
+    return r;
+}
+
+// An output shaped and typed like its input: allocated (contiguous) or checked.
+struct Output {
+    at::Tensor t;
+    PyObject *given;
+    Dense dense;
+    PyObject *object() const
+    {
+        if (!given) return THPVariable_Wrap(t);
+        Py_INCREF(given);
+        return given;
+    }
+};
+
+Output output(const Call &call, const char *name, PyObject *o, const at::Tensor &like)
+{
+    Output r{{}, o == Py_None ? nullptr : o, {}};
+    if (!r.given) {
+        r.t = call.empty(like.sizes(), like.scalar_type());
+    } else {
+        r.t = tensor(o, name);
+        if (r.t.sizes() != like.sizes() || r.t.scalar_type() != like.scalar_type() || r.t.device() != like.device())
+            fail(ATTN_ERR_SHAPE, std::string(name) + " must be shaped and typed like its input, on its device");
+    }
+    r.dense = as_dense(name, r.t);
+    return r;
+}
+
+struct Rotation {
+    const float *cos = nullptr, *sin = nullptr;
+    int64_t rot = 0, length = 0;
+};
+
+Rotation rotation(PyObject *co, PyObject *so, c10::Device dev)
+{
+    if ((co == Py_None) != (so == Py_None)) fail(ATTN_ERR_NULL, "cos and sin must both be given or both be None");
+    if (co == Py_None) return {};
+    const at::Tensor &c = tensor(co, "cos"), &s = tensor(so, "sin");
+    if (c.dim() != 2 || c.sizes() != s.sizes()) fail(ATTN_ERR_SHAPE, "cos and sin must be [table_len, rot / 2]");
+    if (c.scalar_type() != at::kFloat || s.scalar_type() != at::kFloat || c.device() != dev || s.device() != dev ||
+        !c.is_contiguous() || !s.is_contiguous())
+        fail(ATTN_ERR_DTYPE, "cos and sin must be contiguous fp32 tensors on the inputs' device");
+    return {static_cast<const float *>(ptr(c)), static_cast<const float *>(ptr(s)), 2 * c.size(1), c.size(0)};
+}
+
+// Queries, keys and their weights.
+struct NormInputs {
+    const at::Tensor &q, &k;
+    const at::Tensor *wq, *wk;
+    Dense dq, dk;
+    int dtype;
+};
+
+NormInputs norm_inputs(PyObject *qo, PyObject *ko, PyObject *wqo, PyObject *wko)
+{
+    NormInputs r{tensor(qo, "q"), tensor(ko, "k"), maybe(wqo, "q_weight"), maybe(wko, "k_weight"), {}, {}, 0};
+    r.dq = as_dense("q", r.q);
+    r.dk = as_dense("k", r.k);
+    if (r.dk.b != r.dq.b || r.dk.s != r.dq.s || r.dk.d != r.dq.d || r.q.dim() != r.k.dim())
+        fail(ATTN_ERR_SHAPE, "shape mismatch q" + shape_of(r.q) + " k" + shape_of(r.k));
+    if (!r.q.is_cuda() || r.k.scalar_type() != r.q.scalar_type() || r.k.device() != r.q.device())
+        fail(ATTN_ERR_DTYPE, "q and k must be CUDA tensors of one dtype on one device");
+    r.dtype = dtype_code(r.q);
+    for (const at::Tensor *w : {r.wq, r.wk})
+        if (w && (w->dim() != 1 || w->size(0) != r.dq.d || w->scalar_type() != r.q.scalar_type() ||
+                  w->device() != r.q.device() || !w->is_contiguous()))
+            fail(ATTN_ERR_SHAPE, "norm weights must be contiguous [d] tensors typed like q, on its device");
+    return r;
+}
+
+struct Positions {
+    const int32_t *p = nullptr;
+    int64_t stride = 0;
+};
+
+Positions positions(PyObject *o, const NormInputs &in, bool turns)
+{
+    const bool packed = in.q.dim() == 3;
+    if (o == Py_None) {
+        if (packed && turns) fail(ATTN_ERR_NULL, "a packed batch needs positions: they start again in every sequence");
+        return {};
+    }
+    const at::Tensor &t = tensor(o, "positions");
+    const bool one = t.dim() == 1 && t.size(0) == in.dq.s;
+    const bool each = !packed && t.dim() == 2 && t.size(0) == in.dq.b && t.size(1) == in.dq.s;
+    if (t.scalar_type() != at::kInt || t.device() != in.q.device() || !(one || each))
+        fail(ATTN_ERR_DTYPE, "positions must be int32 [s], [b, s] or (packed) [total] on the inputs' device");
+    if (in.dq.s > 1 && t.stride(-1) != 1) fail(ATTN_ERR_SHAPE, "the positions of a sequence must be contiguous");
+    return {static_cast<const int32_t *>(ptr(t)), each && in.dq.b > 1 ? t.stride(0) : 0};
+}
+
+PyObject *qk_norm_rope(PyObject *const *a)
+{
+    // q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, q_out, k_out, stream
+    const NormInputs in = norm_inputs(a[0], a[1], a[2], a[3]);
+    const Rotation r = rotation(a[4], a[5], in.q.device());
+    const Positions pos = positions(a[6], in, r.cos != nullptr);
+    const float eps = static_cast<float>(number(a[7], "eps"));
+    const Call call(in.q, a[11]);
+    const Output qo = output(call, "q_out", a[9], in.q), ko = output(call, "k_out", a[10], in.k);
+    check(attn_qk_norm_rope(ptr(in.q), ptr(in.k), ptr(in.wq), ptr(in.wk), r.cos, r.sin, pos.p, ptr(qo.t), ptr(ko.t),
+                            in.dq.st, in.dk.st, qo.dense.st, ko.dense.st, in.dq.b, in.dq.h, in.dk.h, in.dq.s, in.dq.d,
+                            r.rot, r.length, pos.stride, truth(a[8]), eps, in.dtype, call.stream()));
+    return Py_BuildValue("(NN)", qo.object(), ko.object());
+}
+
+PyObject *qk_norm_rope_bwd(PyObject *const *a)
+{
+    // dq_out, dk_out, q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, dq, dk, workspace, stream
+    const NormInputs in = norm_inputs(a[2], a[3], a[4], a[5]);
+    const Rotation r = rotation(a[6], a[7], in.q.device());
+    const Positions pos = positions(a[8], in, r.cos != nullptr);
+    const float eps = static_cast<float>(number(a[9], "eps"));
+    const Call call(in.q, a[14]);
+    tensor(a[0], "dq_out"), tensor(a[1], "dk_out");  // these are not allocated here
+    const Output gq = output(call, "dq_out", a[0], in.q), gk = output(call, "dk_out", a[1], in.k);
+    const Output dq = output(call, "dq", a[11], in.q), dk = output(call, "dk", a[12], in.k);
+    at::Tensor dwq, dwk, ws;
+    if (in.wq) dwq = call.empty({in.dq.d}, at::kFloat);
+    if (in.wk) dwk = call.empty({in.dq.d}, at::kFloat);
+    if (a[13] != Py_None) {
+        ws = tensor(a[13], "workspace");
+        if (ws.device() != in.q.device() || !ws.is_contiguous())
+            fail(ATTN_ERR_SHAPE, "workspace must be a contiguous tensor on the inputs' device");
+    } else if (in.wq || in.wk) {
+        const int64_t need = attn_qk_norm_rope_bwd_workspace_bytes(in.dq.d);
+        check(need < 0 ? static_cast<int>(need) : 0);
+        ws = call.empty({need}, at::kByte);
+    }
+    check(attn_qk_norm_rope_bwd(ptr(gq.t), ptr(gk.t), ptr(in.q), ptr(in.k), ptr(in.wq), ptr(in.wk), r.cos, r.sin, pos.p,
+                                ptr(dq.t), ptr(dk.t), in.wq ? dwq.data_ptr<float>() : nullptr,
+                                in.wk ? dwk.data_ptr<float>() : nullptr, gq.dense.st, gk.dense.st, in.dq.st, in.dk.st,
+                                dq.dense.st, dk.dense.st, in.dq.b, in.dq.h, in.dk.h, in.dq.s, in.dq.d, r.rot, r.length,
+                                pos.stride, truth(a[10]), eps, in.dtype, ws.defined() ? ptr(ws) : nullptr,
+                                ws.defined() ? static_cast<int64_t>(ws.nbytes()) : 0, call.stream()));
+    auto or_none = [](const at::Tensor &t) {
+        if (t.defined()) return THPVariable_Wrap(t);
+        Py_INCREF(Py_None);
+        return Py_None;
+    };
+    return Py_BuildValue("(NNNN)", dq.object(), dk.object(), or_none(dwq), or_none(dwk));
+}
+
+// A paged cache.
+struct Cache {
+    const at::Tensor &k, &v;
+    const at::Tensor *ks, *vs;
+    const at::Tensor &lens, &table;
+    int64_t num_pages, page_size, pages_per_seq, block;
+};
+
+Cache cache(PyObject *ko, PyObject *vo, PyObject *kso, PyObject *vso, PyObject *lo, PyObject *to, int64_t b, int64_t hkv,
+            int64_t d)
+{
+    Cache c{tensor(ko, "k_pool"), tensor(vo, "v_pool"), maybe(kso, "k_scale"), maybe(vso, "v_scale"),
+            tensor(lo, "cache_seqlens"), tensor(to, "block_table"), 0, 0, 0, 0};
+    const c10::Device dev = c.k.device();
+    if (c.k.dim() != 4 || c.k.size(2) != hkv || c.k.size(3) != d || c.v.sizes() != c.k.sizes() ||
+        c.v.scalar_type() != c.k.scalar_type())
+        fail(ATTN_ERR_SHAPE, "pools " + shape_of(c.k) + " / " + shape_of(c.v) + " must be [num_pages, page_size, h_kv, d]");
+    c.num_pages = c.k.size(0);
+    c.page_size = c.k.size(1);
+    if (c.table.dim() != 2 || c.table.size(0) != b || c.table.scalar_type() != at::kInt)
+        fail(ATTN_ERR_SHAPE, "block_table must be int32 [b, pages_per_seq]");
+    c.pages_per_seq = c.table.size(1);
+    if (c.lens.dim() != 1 || c.lens.size(0) != b || c.lens.scalar_type() != at::kInt)
+        fail(ATTN_ERR_DTYPE, "cache_seqlens must be an int32 tensor of b elements");
+    if (!c.k.is_cuda()) fail(ATTN_ERR_SHAPE, "the pools must be CUDA tensors");
+    for (const at::Tensor *t : {&c.k, &c.v, &c.lens, &c.table})
+        if (t->device() != dev || !t->is_contiguous())
+            fail(ATTN_ERR_SHAPE, "pools, block_table and cache_seqlens must be contiguous, on one device");
+    if (!c.ks != !c.vs) fail(ATTN_ERR_NULL, "k_scale and v_scale must both be given or both be None");
+    if (!c.ks) return c;
+    if (c.k.scalar_type() != at::kFloat8_e4m3fn) fail(ATTN_ERR_DTYPE, "a cache with scales must be float8_e4m3fn");
+    if (c.ks->dim() != 3 || c.ks->size(0) != c.num_pages || c.ks->size(1) != hkv || c.ks->size(2) < 1 ||
+        c.page_size % c.ks->size(2) != 0 || c.vs->sizes() != c.ks->sizes())
+        fail(ATTN_ERR_SHAPE, "scales must be [num_pages, h_kv, page_size / scale_block]");
+    for (const at::Tensor *t : {c.ks, c.vs})
+        if (t->scalar_type() != at::kFloat || t->device() != dev || !t->is_contiguous())
+            fail(ATTN_ERR_DTYPE, "scales must be contiguous fp32 tensors on the pools' device");
+    c.block = c.page_size / c.ks->size(2);
+    return c;
+}
+
+PyObject *kvcache_append_paged(PyObject *const *a)
+{
+    // k_new, v_new, k_pool, v_pool, cache_seqlens, block_table, cos, sin, interleaved, k_scale, v_scale, new_seqlens, stream
+    const at::Tensor &k = tensor(a[0], "k_new"), &v = tensor(a[1], "v_new");
+    if (k.dim() != 4 || k.sizes() != v.sizes())
+        fail(ATTN_ERR_SHAPE, "k_new" + shape_of(k) + " and v_new" + shape_of(v) + " must be [b, h_kv, s_new, d]");
+    const Dense kd = as_dense("k_new", k), vd = as_dense("v_new", v);
+    const int dtype = dtype_code(k);
+    const Cache c = cache(a[2], a[3], a[9], a[10], a[4], a[5], kd.b, kd.h, kd.d);
+    if (v.scalar_type() != k.scalar_type() || (c.block == 0 && c.k.scalar_type() != k.scalar_type()))
+        fail(ATTN_ERR_DTYPE, "k_new, v_new and a cache without scales must have one dtype");
+    if (k.device() != c.k.device() || v.device() != c.k.device())
+        fail(ATTN_ERR_SHAPE, "k_new, v_new and the pools must be on one device");
+    const at::Tensor *news = maybe(a[11], "new_seqlens");
+    if (news && (news->dim() != 1 || news->size(0) != kd.b || news->scalar_type() != at::kInt ||
+                 news->device() != c.k.device() || !news->is_contiguous()))
+        fail(ATTN_ERR_DTYPE, "new_seqlens must be an int32 tensor of b elements on the pools' device");
+    const Rotation r = rotation(a[6], a[7], c.k.device());
+    const Call call(c.k, a[12]);
+    check(attn_kvcache_append_paged(ptr(k), ptr(v), ptr(c.k), ptr(c.v), static_cast<float *>(ptr(c.ks)),
+                                    static_cast<float *>(ptr(c.vs)), static_cast<const int32_t *>(ptr(c.lens)),
+                                    static_cast<const int32_t *>(ptr(news)), static_cast<const int32_t *>(ptr(c.table)),
+                                    r.cos, r.sin, kd.st, vd.st, kd.b, kd.h, kd.s, c.num_pages, c.page_size,
+                                    c.pages_per_seq, c.block, kd.d, r.rot, r.length, truth(a[8]), dtype, call.stream()));
+    Py_RETURN_NONE;
+}
+
+PyObject *fwd_kvcache_paged_fp8(PyObject *const *a)
+{
+    // q, k_pool, v_pool, k_scale, v_scale, cache_seqlens, block_table, causal, scale, o, lse, workspace, stream
+    const at::Tensor &q = tensor(a[0], "q"), &pool = tensor(a[1], "k_pool");
+    if (q.dim() != 4 || pool.dim() != 4)
+        fail(ATTN_ERR_SHAPE, "q must be [b, h, sq, d] and the pools [num_pages, page_size, h_kv, d]");
+    const int64_t b = q.size(0), h = q.size(1), sq = q.size(2), d = q.size(3), hkv = pool.size(2);
+    const int dtype = dtype_code(q);
+    if (a[3] == Py_None || a[4] == Py_None) fail(ATTN_ERR_NULL, "k_scale and v_scale must be given");
+    const Cache c = cache(a[1], a[2], a[3], a[4], a[5], a[6], b, hkv, d);
+    if (!q.is_contiguous() || q.device() != c.k.device()) fail(ATTN_ERR_SHAPE, "q must be contiguous, on the pools' device");
+    const double scale = a[8] == Py_None ? 1.0 / std::sqrt(static_cast<double>(d)) : number(a[8], "scale");
+    const Call call(q, a[12]);
+    const Output o = output(call, "o", a[9], q);
+    if (!o.t.is_contiguous()) fail(ATTN_ERR_SHAPE, "o must be contiguous");
+    at::Tensor lse, ws;
+    if (a[10] == Py_None) {
+        lse = call.empty({b, h, sq}, at::kFloat);
+    } else {
+        lse = tensor(a[10], "lse");
+        if (lse.sizes() != at::IntArrayRef({b, h, sq}) || lse.scalar_type() != at::kFloat || !lse.is_contiguous() ||
+            lse.device() != q.device())
+            fail(ATTN_ERR_SHAPE, "lse must be contiguous fp32 [b, h, sq] on q's device");
+    }
+    if (a[11] == Py_None) {
+        const int64_t need = attn_fwd_kvcache_paged_fp8_workspace_bytes(b, h, hkv, sq, d);
+        check(need < 0 ? static_cast<int>(need) : 0);
+        ws = call.empty({need}, at::kByte);
+    } else {
+        ws = tensor(a[11], "workspace");
+        if (ws.device() != q.device() || !ws.is_contiguous())
+            fail(ATTN_ERR_SHAPE, "workspace must be a contiguous tensor on q's device");
+    }
+    check(attn_fwd_kvcache_paged_fp8(ptr(q), ptr(c.k), ptr(c.v), static_cast<const float *>(ptr(c.ks)),
+                                     static_cast<const float *>(ptr(c.vs)), static_cast<const int32_t *>(ptr(c.lens)),
+                                     static_cast<const int32_t *>(ptr(c.table)), ptr(o.t), lse.data_ptr<float>(), b, h, hkv,
+                                     sq, c.num_pages, c.page_size, c.pages_per_seq, c.block, d, truth(a[7]),
+                                     static_cast<float>(scale), dtype, ptr(ws), static_cast<int64_t>(ws.nbytes()),
+                                     call.stream()));
+    PyObject *l = a[10];
+    if (l == Py_None) l = THPVariable_Wrap(lse);
+    else Py_INCREF(l);
+    return Py_BuildValue("(NN)", o.object(), l);
+}
+
+// Runs a function on its positional arguments; what it throws becomes a
+// Python exception.
+template <PyObject *(*F)(PyObject *const *), int N>
+PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    if (n != N) {
+        PyErr_Format(PyExc_TypeError, "%d arguments are expected, got %zd", N, n);
+        return nullptr;
+    }
+    try {
+        return F(args);
+    } catch (const Err &e) {
+        PyObject *v = Py_BuildValue("(is)", e.code, e.msg.c_str());
+        if (v) PyErr_SetObject(g_error ? g_error : PyExc_RuntimeError, v);
+        Py_XDECREF(v);
+    } catch (const std::exception &e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {
+        PyErr_SetString(PyExc_RuntimeError, "unknown error");
+    }
+    return nullptr;
+}
+
+PyObject *set_error(PyObject *, PyObject *cls)
+{
+    Py_INCREF(cls);
+    Py_XDECREF(g_error);
+    g_error = cls;
+    Py_RETURN_NONE;
+}
+
+template <PyObject *(*F)(PyObject *const *), int N>
+PyMethodDef method(const char *name)
+{
+    return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<F, N>)), METH_FASTCALL, nullptr};
+}
+
+PyMethodDef g_methods[] = {
+    method<qk_norm_rope, 12>("qk_norm_rope"),
+    method<qk_norm_rope_bwd, 15>("qk_norm_rope_bwd"),
+    method<kvcache_append_paged, 13>("kvcache_append_paged"),
+    method<fwd_kvcache_paged_fp8, 13>("fwd_kvcache_paged_fp8"),
+    {"set_error", set_error, METH_O, nullptr},
+    {nullptr, nullptr, 0, nullptr},
+};
+
+PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__marshal() { return PyModule_Create(&g_module); }
