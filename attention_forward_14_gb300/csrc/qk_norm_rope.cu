@@ -195,7 +195,8 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
                     unpack_pairs<T>(cur.x[i], x);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) wdy[e] = __fmul2_rn(dy[e], w[e]);
-                    const float r = rsqrtf(row_sum<LPR>(dot8(x, x)) * (1.f / D) + p.eps);
+                    const float r0 = rsqrtf(row_sum<LPR>(dot8(x, x)) * (1.f / D) + p.eps);
+                    const float r = i * RPW < left ? r0 : 0.f;  // (no row: with eps 0 an infinity, times zeros)
                     // dx = r (wdy - n mean(wdy n)), n = r x: x enters with -r^3 mean(wdy x)
                     const float f = row_sum<LPR>(dot8(wdy, x)) * (-1.f / D) * r * r * r;
 #pragma unroll

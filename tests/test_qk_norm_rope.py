@@ -132,6 +132,24 @@ def test_backward(case):
 
 
 @gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_backward_without_eps_when_heads_do_not_fill_a_unit(d):
+    gen = torch.Generator().manual_seed(17)
+    q, gq = (torch.randn(1, 3, 5, d, generator=gen).to(torch.bfloat16) for _ in range(2))
+    k, gk = (torch.randn(1, 1, 5, d, generator=gen).to(torch.bfloat16) for _ in range(2))
+    w = torch.ones(d, dtype=torch.bfloat16)
+    dq, dk, dwq, dwk = af.attn_qk_norm_rope_bwd(*(t.cuda() for t in (gq, gk, q, k, w, w)), eps=0.0)
+    for dx, dw, g, x in ((dq, dwq, gq, q), (dk, dwk, gk, k)):
+        x, g = as_tokens(x), as_tokens(g)
+        r = 1 / np.sqrt((x * x).mean(-1, keepdims=True))
+        n = x * r
+        close(dx, r * (g - n * (g * n).mean(-1, keepdims=True)), dx.dtype, rows_of=r * g)
+        # each of 15 terms and of their sums has some ten fp32 roundings
+        bound = (np.abs(g * n).sum((0, 1)) + 1e-6) * 2.0 ** -24 * 200
+        assert (np.abs(R.f64(dw) - (g * n).sum((0, 1))) <= bound).all()
+
+
+@gpu
 @pytest.mark.parametrize("norm,turn", [(False, True), (True, False)])
 def test_norm_alone_and_rotation_alone(norm, turn):
     case = (2, 6, 2, 40, 128, 96, False, "bf16", "fused")
