@@ -267,7 +267,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const Shares shared_out(wide_total(p), static_cast<int>(gridDim.x));
     const bool works = blockIdx.x < shared_out.ctas;
-    if (!works && threadIdx.x == 0) p.cut[blockIdx.x].parts = 0;
+    // (a CTA that gives up on a wait leaves it so: the join must not meet what was in the workspace)
+    if (threadIdx.x == 0) p.cut[blockIdx.x].parts = 0;
     const int64_t u0 = works ? shared_out.start(blockIdx.x) : 0;
     const int n_units = works ? static_cast<int>(shared_out.start(blockIdx.x + 1) - u0) : 0;
     WidePlace at = wide_place(p, u0);
