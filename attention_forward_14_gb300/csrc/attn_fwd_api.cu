@@ -9,6 +9,7 @@
 #include <cstring>
 #include <mutex>
 #include <string>
+#include <utility>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -1494,6 +1495,14 @@ int attn_fwd_kvcache_paged_fp8(const void *q, const void *k_pool, const void *v_
     if (!aligned(workspace, 16)) return fail(ATTN_ERR_ALIGN, "workspace must be 16-byte aligned");
     if (workspace_bytes < need)
         return fail(ATTN_ERR_SHAPE, "workspace too small: %lld bytes, need %lld", (long long)workspace_bytes, (long long)need);
+    // rows of o are written while others' q and the pools are still read
+    const uintptr_t o0 = reinterpret_cast<uintptr_t>(o), o_bytes = static_cast<uintptr_t>(b * h * sq * d) * 2;
+    const uintptr_t pool_bytes = static_cast<uintptr_t>(num_pages * page_size * h_kv * d);
+    const std::pair<const void *, uintptr_t> reads[3] = {{q, o_bytes}, {k_pool, pool_bytes}, {v_pool, pool_bytes}};
+    for (const auto &r : reads) {
+        const uintptr_t r0 = reinterpret_cast<uintptr_t>(r.first);
+        if (o0 < r0 + r.second && r0 < o0 + o_bytes) return fail(ATTN_ERR_SHAPE, "o overlaps q, k_pool or v_pool");
+    }
     DeviceInfo *di = nullptr;
     if ((rc = device_info(&di)) != ATTN_OK) return rc;
     Kv8LaunchArgs a;

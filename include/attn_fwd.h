@@ -531,7 +531,8 @@ int attn_kvcache_append_paged(const void *k_new, const void *v_new,
  * append) on K = k_scale * k_pool, V = v_scale * v_pool, with one scale for
  * each block of scale_block tokens and key head, and h / h_kv query heads
  * sharing a key head.
- *   q, o         : [b, h, sq, d] of dtype, contiguous, 16-byte aligned.
+ *   q, o         : [b, h, sq, d] of dtype, contiguous, 16-byte aligned.  o
+ *                  must not overlap q or a pool (ATTN_ERR_SHAPE).
  *   k_pool,
  *   v_pool       : e4m3 [num_pages, page_size, h_kv, d], 16-byte aligned.
  *   k_scale,

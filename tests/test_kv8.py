@@ -273,6 +273,14 @@ def test_refusals(lib, kw, code):
     assert rc == code and lib.attn_last_error()
 
 
+@pytest.mark.parametrize("o", [P, P + 64, P - 64, (1 << 32) + 1024, (1 << 33) - 16])
+def test_an_output_over_an_input_is_refused(lib, o):
+    q, kp, vp = P, 1 << 32, 1 << 33
+    rc = lib.attn_fwd_kvcache_paged_fp8(q, kp, vp, P, P, P, P, o, None, 1, 4, 2, 1, 4, 64, 2, 16, 64, 1, 0.1, 1, P, 1 << 40,
+                                        None)
+    assert rc == -2 and b"overlaps" in lib.attn_last_error()
+
+
 def test_nothing_to_do_and_workspace(lib):
     for kw in (dict(b=0), dict(h=0), dict(sq=0)):
         n = dict(b=1, h=2, sq=1)
