@@ -774,6 +774,16 @@ int norm_rope_common(NormRopeParams *p, const float *cos, const float *sin, cons
     return ATTN_OK;
 }
 
+// A unit reads its rows before it writes them: in place is fine when every
+// row is written where it was read.
+int validate_in_place(const void *x, const int64_t *xs, const void *out, const int64_t *os, int64_t b, int64_t heads,
+                      int64_t s, const char *what)
+{
+    const bool same = (b == 1 || xs[0] == os[0]) && (heads == 1 || xs[1] == os[1]) && (s == 1 || xs[2] == os[2]);
+    if (x == out && !same) return fail(ATTN_ERR_SHAPE, "%s and its output share memory with other strides", what);
+    return ATTN_OK;
+}
+
 int set_side(NormRopeSide *sd, const void *x, const void *w, const int64_t *xs, void *out, const int64_t *os, int64_t b,
              int64_t heads, int64_t s, int64_t d, const char *what)
 {
@@ -786,10 +796,7 @@ int set_side(NormRopeSide *sd, const void *x, const void *w, const int64_t *xs, 
     if (rc != ATTN_OK) return rc;
     if (!aligned(x, 16) || !aligned(out, 16) || (w && !aligned(w, 16)))
         return fail(ATTN_ERR_ALIGN, "%s, its weight and its output must be 16-byte aligned", what);
-    // each unit reads its rows before it writes them: in place is fine when
-    // every row is written where it was read
-    const bool same = (b == 1 || xs[0] == os[0]) && (heads == 1 || xs[1] == os[1]) && (s == 1 || xs[2] == os[2]);
-    if (x == out && !same) return fail(ATTN_ERR_SHAPE, "%s and its output share memory with other strides", what);
+    if ((rc = validate_in_place(x, xs, out, os, b, heads, s, what)) != ATTN_OK) return rc;
     sd->x = x;
     sd->w = w;
     sd->out = out;
@@ -1329,6 +1336,8 @@ int attn_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const void *q,
         if (!gs[i]) return fail(ATTN_ERR_NULL, "dq_out or dk_out is NULL");
         if ((rc = validate_strides(gst[i], "an output's gradient")) != ATTN_OK) return rc;
         if (!aligned(gs[i], 16)) return fail(ATTN_ERR_ALIGN, "dq_out and dk_out must be 16-byte aligned");
+        rc = validate_in_place(gs[i], gst[i], sd.out, i ? dk_strides : dq_strides, b, sd.heads, s, "an output's gradient");
+        if (rc != ATTN_OK) return rc;
         sd.g = gs[i];
         sd.gb = gst[i][0], sd.gh = gst[i][1], sd.gs = gst[i][2];
     }

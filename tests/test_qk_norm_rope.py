@@ -300,6 +300,17 @@ def test_backward_refusals(lib):
     assert call(dw=P + 2) == -6 and call(g=None) == -1 and call(g=P + 8) == -6
 
 
+def test_backward_in_place_with_other_strides_is_refused(lib):
+    need = lib.attn_qk_norm_rope_bwd_workspace_bytes(64)
+
+    def call(g, x, dx, gs, xs):
+        return lib.attn_qk_norm_rope_bwd(g, None, x, None, P, None, None, None, None, dx, None, P + 64, None, S3(*gs), None,
+                                         S3(*xs), None, S3(512, 256, 64), None, 1, 2, 0, 4, 64, 0, 0, 0, 0, 1e-6, 1, P,
+                                         need, None)
+    assert call(P, P + 4096, P, (512, 64, 128), (512, 256, 64)) == -2    # over its output's gradient
+    assert call(P + 4096, P, P, (512, 256, 64), (512, 64, 128)) == -2    # over its input
+
+
 @gpu
 def test_binding_refusals():
     q = torch.zeros((2, 4, 8, 64), device=DEV).half()
