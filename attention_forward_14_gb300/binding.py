@@ -588,21 +588,24 @@ def attn_bwd_varlen(q, k, v, o, dout, lse, cu_seqlens_q, cu_seqlens_k, max_seqle
     return dq, dk, dv
 
 
-_fast = None
+# What csrc/marshal.cpp calls, in the order in which it takes their addresses.
+_MARSHALLED = ("attn_last_error", "attn_qk_norm_rope", "attn_qk_norm_rope_bwd", "attn_qk_norm_rope_bwd_workspace_bytes",
+               "attn_kvcache_append_paged", "attn_fwd_kvcache_paged_fp8", "attn_fwd_kvcache_paged_fp8_workspace_bytes")
+_fast, _fast_lib = None, None
 
 
 def _marshal():
     """The C++ module that checks the tensors of the operators below,
-    allocates their outputs and calls the library (loaded once)."""
-    global _fast
-    if _fast is None:
-        load()
+    allocates their outputs and calls the loaded library."""
+    global _fast, _fast_lib
+    lib = _lib or load()
+    if lib is not _fast_lib:
         try:
-            from . import _marshal as m
+            from . import _marshal_ext
         except ImportError as e:
-            raise AttnError(-8, f"_marshal.so cannot be loaded ({e}); run python -m attention_forward_14_gb300.build") from e
-        m.set_error(AttnError)
-        _fast = m
+            raise AttnError(-8, f"_marshal_ext.so cannot be loaded ({e}); run python -m attention_forward_14_gb300.build") from e
+        _marshal_ext.bind(AttnError, *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _MARSHALLED))
+        _fast, _fast_lib = _marshal_ext, lib
     return _fast
 
 
@@ -623,8 +626,8 @@ def attn_qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, po
     or (packed) [total], None: 0..s-1.  ``interleaved``: adjacent pairs turn
     instead of pairs (i, i + rot/2).  Negative positions are padding (zeros).
     Returns (q_out, k_out), contiguous unless given."""
-    return (_fast or _marshal()).qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, q_out,
-                                              k_out, _handle(stream))
+    return _marshal().qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, q_out, k_out,
+                                   _handle(stream))
 
 
 def attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
@@ -634,8 +637,8 @@ def attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, co
     for a weight that is None.  ``dq`` / ``dk`` may be given (for example
     slices of the fused projection's gradient), with any strides; ``workspace``
     is a CUDA uint8 tensor of qk_norm_rope_bwd_workspace_bytes(d) bytes."""
-    return (_fast or _marshal()).qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, cos, sin, positions, eps,
-                                                  interleaved, dq, dk, workspace, _handle(stream))
+    return _marshal().qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved,
+                                       dq, dk, workspace, _handle(stream))
 
 
 def qk_norm_rope_bwd_workspace_bytes(d: int) -> int:
@@ -657,8 +660,8 @@ def attn_kvcache_append_paged(k_new, v_new, k_pool, v_pool, cache_seqlens, block
     [b] says how many of a padded batch's tokens are there.  ``cos`` / ``sin``
     fp32 [at least the capacity, rot / 2]; None: no rotation.  cache_seqlens is
     not updated."""
-    (_fast or _marshal()).kvcache_append_paged(k_new, v_new, k_pool, v_pool, cache_seqlens, block_table, cos, sin,
-                                               interleaved, k_scale, v_scale, new_seqlens, _handle(stream))
+    _marshal().kvcache_append_paged(k_new, v_new, k_pool, v_pool, cache_seqlens, block_table, cos, sin, interleaved,
+                                    k_scale, v_scale, new_seqlens, _handle(stream))
 
 
 def kvcache_paged_fp8_workspace_bytes(b, h, h_kv, sq, d) -> int:
@@ -675,5 +678,5 @@ def attn_fwd_kvcache_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, cache_seqlen
     tokens (the new ones among them: append first); h / h_kv query heads share
     a key head.  ``workspace``: a CUDA uint8 tensor of
     kvcache_paged_fp8_workspace_bytes bytes.  Returns (o, lse)."""
-    return (_fast or _marshal()).fwd_kvcache_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, cache_seqlens, block_table,
-                                                       causal, scale, o, lse, workspace, _handle(stream))
+    return _marshal().fwd_kvcache_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, cache_seqlens, block_table, causal,
+                                            scale, o, lse, workspace, _handle(stream))

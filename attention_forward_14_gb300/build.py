@@ -1,6 +1,6 @@
 """Build libattn_fwd.so (sm_103a) in-tree with nvcc, its checked variant, and
-the Python entry of the operators around the attention (``_marshal.so``, C++
-against torch's headers, linked to the library).
+the Python entry of the operators around the attention (``_marshal_ext.so``,
+C++ against torch's headers).
 
 Each translation unit under csrc/ is compiled in parallel, then linked into
 ``attention_forward_14_gb300/libattn_fwd.so``.  The checked variant,
@@ -26,7 +26,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libattn_fwd.so")
 LIB_CHECKED = os.path.join(HERE, "libattn_fwd_checked.so")
-MARSHAL = os.path.join(HERE, "_marshal.so")
+MARSHAL = os.path.join(HERE, "_marshal_ext.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["attn_fwd_api.cu", "inst_d64.cu", "inst_d128_noncausal.cu", "inst_d128_causal.cu", "inst_fp8.cu",
            "attn_bwd_inst.cu", "attn_bwd_inst_varlen.cu", "qk_norm_rope.cu", "kv_append.cu", "attn_kv8.cu",
@@ -78,11 +78,11 @@ def _link_marshal(obj: str) -> None:
     import torch
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = MARSHAL + f".tmp{os.getpid()}"
-    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, LIB, "-L", lib, "-ltorch_python", "-ltorch",
-           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", lib, "-ltorch_python", "-ltorch",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"_marshal.so failed to link:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"_marshal_ext.so failed to link:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, MARSHAL)
 
 
@@ -125,8 +125,7 @@ def build(force: bool = False, verbose: bool = False, checked: bool = True) -> s
     for lib, chk in todo:
         objs = [obj_path(src, chk and src in CHECKED_SOURCES) for src in SOURCES]
         tmp = lib + f".tmp{os.getpid()}"
-        r = subprocess.run([cc, *ARCH, "-shared", "-Xlinker", f"-soname={os.path.basename(lib)}", "-o", tmp, *objs],
-                           capture_output=True, text=True)
+        r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, lib)

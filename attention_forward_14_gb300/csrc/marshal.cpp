@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <cmath>
+#include <cstring>
 #include <string>
 #include <utility>
 
@@ -25,6 +26,17 @@ namespace {
 
 PyObject *g_error = nullptr;  // binding.AttnError
 
+// The entry points of the library that binding.py has loaded.
+struct Library {
+    decltype(&attn_last_error) last_error;
+    decltype(&attn_qk_norm_rope) qk_norm_rope;
+    decltype(&attn_qk_norm_rope_bwd) qk_norm_rope_bwd;
+    decltype(&attn_qk_norm_rope_bwd_workspace_bytes) qk_norm_rope_bwd_workspace_bytes;
+    decltype(&attn_kvcache_append_paged) kvcache_append_paged;
+    decltype(&attn_fwd_kvcache_paged_fp8) fwd_kvcache_paged_fp8;
+    decltype(&attn_fwd_kvcache_paged_fp8_workspace_bytes) fwd_kvcache_paged_fp8_workspace_bytes;
+} g_lib;
+
 struct Err {
     int code;
     std::string msg;
@@ -34,7 +46,7 @@ struct Err {
 
 void check(int rc)
 {
-    if (rc < 0) fail(rc, attn_last_error());
+    if (rc < 0) fail(rc, g_lib.last_error());
 }
 
 // The tensor of an argument that must be one / may be None.
@@ -244,7 +256,7 @@ PyObject *qk_norm_rope(PyObject *const *a)
     const float eps = static_cast<float>(number(a[7], "eps"));
     const Call call(in.q, a[11]);
     const Output qo = output(call, "q_out", a[9], in.q), ko = output(call, "k_out", a[10], in.k);
-    check(attn_qk_norm_rope(ptr(in.q), ptr(in.k), ptr(in.wq), ptr(in.wk), r.cos, r.sin, pos.p, ptr(qo.t), ptr(ko.t),
+    check(g_lib.qk_norm_rope(ptr(in.q), ptr(in.k), ptr(in.wq), ptr(in.wk), r.cos, r.sin, pos.p, ptr(qo.t), ptr(ko.t),
                             in.dq.st, in.dk.st, qo.dense.st, ko.dense.st, in.dq.b, in.dq.h, in.dk.h, in.dq.s, in.dq.d,
                             r.rot, r.length, pos.stride, truth(a[8]), eps, in.dtype, call.stream()));
     return Py_BuildValue("(NN)", qo.object(), ko.object());
@@ -269,11 +281,11 @@ PyObject *qk_norm_rope_bwd(PyObject *const *a)
         if (ws.device() != in.q.device() || !ws.is_contiguous())
             fail(ATTN_ERR_SHAPE, "workspace must be a contiguous tensor on the inputs' device");
     } else if (in.wq || in.wk) {
-        const int64_t need = attn_qk_norm_rope_bwd_workspace_bytes(in.dq.d);
+        const int64_t need = g_lib.qk_norm_rope_bwd_workspace_bytes(in.dq.d);
         check(need < 0 ? static_cast<int>(need) : 0);
         ws = call.empty({need}, at::kByte);
     }
-    check(attn_qk_norm_rope_bwd(ptr(gq.t), ptr(gk.t), ptr(in.q), ptr(in.k), ptr(in.wq), ptr(in.wk), r.cos, r.sin, pos.p,
+    check(g_lib.qk_norm_rope_bwd(ptr(gq.t), ptr(gk.t), ptr(in.q), ptr(in.k), ptr(in.wq), ptr(in.wk), r.cos, r.sin, pos.p,
                                 ptr(dq.t), ptr(dk.t), in.wq ? dwq.data_ptr<float>() : nullptr,
                                 in.wk ? dwk.data_ptr<float>() : nullptr, gq.dense.st, gk.dense.st, in.dq.st, in.dk.st,
                                 dq.dense.st, dk.dense.st, in.dq.b, in.dq.h, in.dk.h, in.dq.s, in.dq.d, r.rot, r.length,
@@ -347,7 +359,7 @@ PyObject *kvcache_append_paged(PyObject *const *a)
         fail(ATTN_ERR_DTYPE, "new_seqlens must be an int32 tensor of b elements on the pools' device");
     const Rotation r = rotation(a[6], a[7], c.k.device());
     const Call call(c.k, a[12]);
-    check(attn_kvcache_append_paged(ptr(k), ptr(v), ptr(c.k), ptr(c.v), static_cast<float *>(ptr(c.ks)),
+    check(g_lib.kvcache_append_paged(ptr(k), ptr(v), ptr(c.k), ptr(c.v), static_cast<float *>(ptr(c.ks)),
                                     static_cast<float *>(ptr(c.vs)), static_cast<const int32_t *>(ptr(c.lens)),
                                     static_cast<const int32_t *>(ptr(news)), static_cast<const int32_t *>(ptr(c.table)),
                                     r.cos, r.sin, kd.st, vd.st, kd.b, kd.h, kd.s, c.num_pages, c.page_size,
@@ -380,7 +392,7 @@ PyObject *fwd_kvcache_paged_fp8(PyObject *const *a)
             fail(ATTN_ERR_SHAPE, "lse must be contiguous fp32 [b, h, sq] on q's device");
     }
     if (a[11] == Py_None) {
-        const int64_t need = attn_fwd_kvcache_paged_fp8_workspace_bytes(b, h, hkv, sq, d);
+        const int64_t need = g_lib.fwd_kvcache_paged_fp8_workspace_bytes(b, h, hkv, sq, d);
         check(need < 0 ? static_cast<int>(need) : 0);
         ws = call.empty({need}, at::kByte);
     } else {
@@ -388,7 +400,7 @@ PyObject *fwd_kvcache_paged_fp8(PyObject *const *a)
         if (ws.device() != q.device() || !ws.is_contiguous())
             fail(ATTN_ERR_SHAPE, "workspace must be a contiguous tensor on q's device");
     }
-    check(attn_fwd_kvcache_paged_fp8(ptr(q), ptr(c.k), ptr(c.v), static_cast<const float *>(ptr(c.ks)),
+    check(g_lib.fwd_kvcache_paged_fp8(ptr(q), ptr(c.k), ptr(c.v), static_cast<const float *>(ptr(c.ks)),
                                      static_cast<const float *>(ptr(c.vs)), static_cast<const int32_t *>(ptr(c.lens)),
                                      static_cast<const int32_t *>(ptr(c.table)), ptr(o.t), lse.data_ptr<float>(), b, h, hkv,
                                      sq, c.num_pages, c.page_size, c.pages_per_seq, c.block, d, truth(a[7]),
@@ -423,11 +435,19 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
     return nullptr;
 }
 
-PyObject *set_error(PyObject *, PyObject *cls)
+// bind(error class, address of each function of Library in its order)
+PyObject *bind(PyObject *const *a)
 {
-    Py_INCREF(cls);
+    constexpr int kFunctions = sizeof(Library) / sizeof(void *);
+    void *at[kFunctions];
+    for (int i = 0; i < kFunctions; ++i) {
+        at[i] = PyLong_AsVoidPtr(a[1 + i]);
+        if (PyErr_Occurred()) return nullptr;
+    }
+    std::memcpy(&g_lib, at, sizeof(g_lib));
+    Py_INCREF(a[0]);
     Py_XDECREF(g_error);
-    g_error = cls;
+    g_error = a[0];
     Py_RETURN_NONE;
 }
 
@@ -442,12 +462,12 @@ PyMethodDef g_methods[] = {
     method<qk_norm_rope_bwd, 15>("qk_norm_rope_bwd"),
     method<kvcache_append_paged, 13>("kvcache_append_paged"),
     method<fwd_kvcache_paged_fp8, 13>("fwd_kvcache_paged_fp8"),
-    {"set_error", set_error, METH_O, nullptr},
+    method<bind, 8>("bind"),
     {nullptr, nullptr, 0, nullptr},
 };
 
-PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
+PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal_ext", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal() { return PyModule_Create(&g_module); }
+PyMODINIT_FUNC PyInit__marshal_ext() { return PyModule_Create(&g_module); }
