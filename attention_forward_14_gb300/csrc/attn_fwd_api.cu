@@ -1439,6 +1439,7 @@ int attn_kvcache_append_paged(const void *k_new, const void *v_new, void *k_pool
     p.cos = cos, p.sin = sin;
     p.b = b, p.s = s_new, p.num_pages = num_pages, p.pages_per_seq = pages_per_seq;
     p.heads = static_cast<int>(h_kv);
+    p.status = di->status;
     p.nblk_heads = static_cast<uint32_t>(nblk * h_kv);
     p.page_size = static_cast<int>(page_size);
     p.block_shift = e4m3 ? log2_of(scale_block) : 0;

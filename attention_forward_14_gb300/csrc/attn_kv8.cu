@@ -219,6 +219,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t u0 = shared_out.start(blockIdx.x);
     const int n_units = static_cast<int>(shared_out.start(blockIdx.x + 1) - u0);
     Place cur = place_of(p, u0);
+    // of the unit of a CTA's warps; all of them come to the same answer
+    auto place_in_bounds = [&](const Place &c) {
+        const bool ok = ATTN_OPS_IN_BOUNDS(c.b >= 0 && c.b < p.b && c.hg >= 0 && c.hg < p.head_groups && c.tile >= 0 &&
+                                               c.tile < p.tiles && c.j >= 0 && c.j < c.n, p, SITE_OPS_UNIT);
+        if (!ok) *abort_flag = 1u;
+        return ok;
+    };
 
     auto wait = [&](uint32_t bar, uint32_t parity, uint32_t site) {
         if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
@@ -260,6 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float *head_scales = nullptr;
         for (int it = 0; it < n_units; ++it) {
             if (it == 0 || cur.j == 0) {
+                if (!place_in_bounds(cur)) break;
                 end = seen_keys(p, cur).end;
                 table = p.block_table + static_cast<int64_t>(cur.b) * p.pages_per_seq;
                 head_scales = scales + static_cast<int64_t>(cur.hg * p.heads + hw) * blocks_per_page;
@@ -279,8 +287,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_3d(base + st * C::STAGE + to, map, bar, 0, in ? page * p.page_size + off : nowhere,
                                 cur.hg * p.heads, pol);
                 const uint32_t sc = base + C::SC_OFF + st * (kWarps * 16) + (w * 4 + kv * 2 + half) * 4;
-                if (in) {
-                    cp_async4(sc, head_scales + static_cast<int64_t>(page) * p.h_kv * blocks_per_page + (off >> p.block_shift));
+                const int64_t from = static_cast<int64_t>(page) * p.h_kv * blocks_per_page + (off >> p.block_shift);
+                if (in && scale_in_bounds(p, head_scales - scales + from)) {
+                    cp_async4(sc, head_scales + from);
                     cp_async_arrive(bar);
                 } else {
                     asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc), "f"(1.f) : "memory");
@@ -499,6 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     for (int it = 0; it < n_units;) {
         // an item begins, or goes on from the CTA before
+        if (!place_in_bounds(at)) break;
         const Seen seen = seen_keys(p, at);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -693,6 +703,9 @@ __global__ void __launch_bounds__(256) attn_kv8_join_kernel(const __grid_constan
     if (cta < 0) return;
     const Kv8Cut cut = p.cut[cta];
     const int n = cut.parts;
+    if (!ATTN_OPS_IN_BOUNDS(cta + n <= grid && cut.b >= 0 && cut.b < p.b && cut.tile >= 0 && cut.tile < p.tiles && cut.hg >= 0 &&
+                                cut.hg < (p.tile_rows > kKv8Tile ? p.h_kv : p.head_groups), p, SITE_OPS_PART))
+        return;
     const bool many = p.tile_rows > kKv8Tile;
     const int first = cut.tile * p.tile_rows + (many ? blockIdx.y * kKv8Tile : 0);  // of its key head's rows
     const int nr = min(min(p.tile_rows, kKv8Tile), p.rows - first);

@@ -2,7 +2,6 @@
 // device: conversions, small copies, and how work is dealt out.
 #pragma once
 
-#include "attn_fwd_kernel.cuh"
 #include "attn_kv8.h"
 #include "rows.cuh"
 
@@ -11,8 +10,8 @@ namespace attn {
 // P = 2^(x - m + kOffset) against a reference m that is raised when some x
 // exceeds it by more than kSlack: P <= 2^14, within fp16.
 constexpr float kOffset = 6.f, kSlack = 8.f;
-enum : uint32_t { SITE_KV8_FULL = 40, SITE_KV8_EMPTY = 41, SITE_KV8_Q = 42, SITE_KV8_CONV = 43, SITE_KV8_S = 44,
-                  SITE_KV8_P = 45, SITE_KV8_O = 46 };
+enum : uint32_t { SITE_KV8_FULL = 60, SITE_KV8_EMPTY = 61, SITE_KV8_Q = 62, SITE_KV8_CONV = 63, SITE_KV8_S = 64,
+                  SITE_KV8_P = 65, SITE_KV8_O = 66 };
 
 // fp16 of the e4m3 values in the low and in the high half of a word.
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi)
@@ -49,6 +48,13 @@ __device__ __forceinline__ float rcp_approx(float x)
 }
 
 __device__ __forceinline__ int cached_len(const Kv8Params &p, int b) { return min(max(p.seqlens[b], 0), p.cap); }
+
+// Whether the scale at `i` is one of the pool's.
+__device__ __forceinline__ bool scale_in_bounds(const Kv8Params &p, int64_t i)
+{
+    return ATTN_OPS_IN_BOUNDS(i >= 0 && i < static_cast<int64_t>(p.num_pages) * p.h_kv * (p.page_size >> p.block_shift), p,
+                              SITE_OPS_SCALE);
+}
 
 __device__ __forceinline__ void named_barrier(int id, int threads)
 {

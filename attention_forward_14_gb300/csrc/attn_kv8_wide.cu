@@ -1,6 +1,6 @@
 // Attention of many new queries over an e4m3 paged cache (chunks of a
-// prompt, long drafts; more than 48 rows of a key head): the operation of attn_kv8.cu on the tensor cores'
-// tcgen05 path.
+// prompt, long drafts; more than 48 rows of a key head): the operation of
+// attn_kv8.cu on the tensor cores' tcgen05 path.
 //
 // Work.  An item is 256 query rows of one key head of one batch element
 // (rows of the query heads that share it, one after another); a unit is 128
@@ -9,13 +9,13 @@
 // CTAs share is joined by the same kernel: 256 items of a 2048-token chunk
 // fill 152 CTAs evenly, which whole items would not (two rounds, 84%).
 //
-// A CTA, 12 warps:
+// A CTA, 16 warps:
 //   warps 0-3, 4-7  softmax group t, one thread to a row of Q tile t (128
 //                   rows); it also brings its row of Q and stores its row of O
 //   warp  8         issues the matrix products
 //   warp  9         copies raw K and V tiles (128 keys, TMA) and their scales
-//   warps 10, 11    convert raw K and V tiles to fp16 in the swizzled layout
-//                   that the products read
+//   warps 10-15     convert raw tiles, even ones K's and odd ones V's, to fp16
+//                   in the swizzled layout that the products read
 // S_t = Q_t K_j^T and O_t += P_t V_j accumulate in tensor memory (128 lanes x
 // 128 or d columns of fp32 for each tile); the softmax group overwrites S_t
 // with P_t in fp16.  While one group works on its tile, the tensor cores work
@@ -29,9 +29,14 @@
 // scale enters the softmax's exponent: x = ks scale log2(e) (q . k) +
 // log2(vs), with the sum of the weights divided by vs, tile by tile.
 //
-// What bounds it: the tensor cores at many keys and rows, with the softmax
-// (one exponential for each score) close behind; below 256 rows the bytes of
-// the cache and their conversion.
+// What bounds it, at the last 2048 of 16384 tokens (causal, 32 heads on
+// 8 key heads, d = 128): 488 us, 1.06 of 1.91 PFLOP/s.  Without the
+// conversion (raw tiles fed as they are, wrong results) 420-439: a tile of
+// 128 keys serves two Q tiles only, so its conversion (16 KB read, 32 KB
+// written and read again by the products) takes the shared memory's time away
+// from them.  The rest is the softmax, one exponential for each score, in
+// step with the tensor cores.  At 64 rows (8 caches of up to 16383 tokens, 8
+// key heads) 101 us: the bytes of the cache and their conversion.
 #include "attn_kv8_common.cuh"
 
 namespace attn {
@@ -39,9 +44,10 @@ namespace attn {
 namespace {
 
 constexpr int kTileRows = 128, kItemRows = 2 * kTileRows, kTileKeys = 128;
-constexpr int kTeam = 3;  // warps that convert K tiles, and as many V tiles
-constexpr int kThreads = kTeam == 1 ? 384 : 512;
-constexpr int kSoftmaxRegs = kTeam == 1 ? 208 : 200, kOtherRegs = kTeam == 1 ? 88 : 56;
+constexpr int kTeam = 3;  // warps that convert K tiles, and as many V tiles (1: 681 us at the chunk below, 3: 498)
+constexpr int kThreads = (10 + 2 * kTeam) * 32;
+static_assert(kThreads % 128 == 0, "whole warpgroups: registers are dealt out by them");
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 56;  // 256 * 200 + 256 * 56 = 512 * 128
 constexpr int kRefRing = 8;
 
 template <int D>
@@ -272,6 +278,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t u0 = works ? shared_out.start(blockIdx.x) : 0;
     const int n_units = works ? static_cast<int>(shared_out.start(blockIdx.x + 1) - u0) : 0;
     WidePlace at = wide_place(p, u0);
+    // of an item that a warp begins or goes on with; all of a CTA's come to the same answer
+    auto place_in_bounds = [&]() {
+        const bool ok = ATTN_OPS_IN_BOUNDS(at.b >= 0 && at.b < p.b && at.kvh >= 0 && at.kvh < p.h_kv && at.blk >= 0 &&
+                                               at.blk < p.tiles && at.j >= 0 && at.j < at.n, p, SITE_OPS_UNIT);
+        if (!ok) *abort_flag = 1u;
+        return ok;
+    };
 
     if (warp >= 8) {
         regs_dec<kOtherRegs>();
@@ -288,6 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t n = 0u;  // raw tiles filled
             bool ok = true;
             for (int it = 0; ok && it < n_units;) {
+                if (!place_in_bounds()) break;
                 const int end = wide_seen(p, at.len, at.blk).end;
                 const int j_end = min(at.n, at.j + n_units - it);
                 const int32_t *table = p.block_table + static_cast<int64_t>(at.b) * p.pages_per_seq;
@@ -312,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tma_load_3d(sRaw + st * C::RAW + 16 * lane * D, kv ? &tmV : &tmK, bar, 0, tok, at.kvh, pol);
                         if (lane < (kv ? 8 : 16)) {
                             float *to = &ctl->scales[st][lane];
-                            if (in) {
+                            if (in && scale_in_bounds(p, sc)) {
                                 cp_async4(smem_addr(to), (kv || lane >= 8 ? p.v_scale : p.k_scale) + sc);
                                 cp_async_arrive(bar);
                             } else {
@@ -330,10 +344,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             for (uint32_t i = n > raw_slots ? n - raw_slots : 0u; i < n; ++i)
                 drain_wait(B(ctl->raw_full[i & (raw_slots - 1)]), (i >> raw_shift) & 1u, p.timeout_ns);
-        } else if (warp >= 10 && warp < 10 + 2 * kTeam) {
+        } else if (warp >= 10) {
             // -------------------------------------------------------- conversion
-            // One warp converts the K tiles and one the V tiles, eight keys
-            // at a time: 16 values to a lane, which for odd keys are the
+            // kTeam warps convert the K tiles and as many the V tiles, eight
+            // keys at a time: 16 values to a lane, which for odd keys are the
             // other half of the row than for even ones, so that neither the
             // raw reads nor the writes of eight lanes meet in a bank.
             const int kv = warp & 1, wi = (warp - 10) >> 1;
@@ -350,6 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t tiles = 0u;
             bool ok = true;
             for (int it = 0; ok && it < n_units;) {
+                if (!place_in_bounds()) break;
                 const WideSeen seen = wide_seen(p, at.len, at.blk);
                 const int j_end = min(at.n, at.j + n_units - it);
                 for (int j = at.j; ok && seen.end > 0 && j < j_end; ++j, ++tiles) {
@@ -370,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint8_t *raw = smem + raw_off + rs * C::RAW;
                     const uint32_t out = sConv + cs * C::TILE;
                     uint32_t nans = 0u;
-                                        // eight keys at a time: a lane's row is 8 q + (lane >> 2), so only q moves its addresses
+                    // eight keys at a time: a lane's row is 8 q + (lane >> 2), so only q moves its addresses
 #pragma unroll 1
                     for (int q = wi; q < 16; q += kTeam) {
                         const float m = __shfl_sync(0xffffffffu, mul, q >> 1);
@@ -449,6 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             for (int it = 0; ok && it < n_units;) {
+                if (!place_in_bounds()) break;
                 const int end = wide_seen(p, at.len, at.blk).end;
                 const int j_end = min(at.n, at.j + n_units - it);
                 const int tiles = end > 0 ? j_end - at.j : 0;
@@ -518,6 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t s_it = 0u, o_it = 0u, tiles = 0u;
         bool ok = true;
         for (int it = 0; ok && it < n_units;) {
+            if (!place_in_bounds()) break;
             const WideSeen seen = wide_seen(p, at.len, at.blk);
             const int j_end = min(at.n, at.j + n_units - it);
             const int n = seen.end > 0 ? j_end - at.j : 0;

@@ -15,7 +15,6 @@
 // value no precision, since its rounding is relative.
 #include "kv_append.h"
 
-#include "attn_fwd_kernel.cuh"
 #include "rows.cuh"
 
 namespace attn {
@@ -61,6 +60,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
     const int kv = gi >= groups ? 1 : 0;
     const int h0 = static_cast<int>(gi - kv * groups) * RPW * ROWS;
     const int e = static_cast<int>(tok / static_cast<uint32_t>(p.s)), t = static_cast<int>(tok - e * static_cast<uint32_t>(p.s));
+    if (!ATTN_OPS_IN_BOUNDS(e < p.b && t < p.s && h0 < p.heads, p, SITE_OPS_UNIT)) return;
     const RowLane rl = row_lane<ADJACENT>(l, kv == 0 ? p.rot : 0);
     const T *x = static_cast<const T *>(p.x[kv]) + e * p.xb[kv] + t * p.xs[kv];
     uint2 raw[ROWS][2];
@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
     const int pos = nr.start + t;
     if (pos >= nr.end) return;
     const int token = pool_token(p, e, pos);
-    if (token < 0) return;
+    if (token < 0 || !ATTN_OPS_IN_BOUNDS(token < p.num_pages * p.page_size, p, SITE_OPS_PAGE)) return;
     T *dst = static_cast<T *>(p.pool[kv]) + static_cast<int64_t>(token) * p.heads * D;
     float c[4], s[4];
     load_angles(p.cos, p.sin, static_cast<int64_t>(pos) * (p.rot / 2), rl, c, s);
@@ -156,7 +156,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_e4m3_kernel(const __grid_c
     const bool any = hi > lo || old > 0;
     const RowLane rl = row_lane<ADJACENT>(l, kv == 0 ? p.rot : 0);
     const int row0 = (warp % WPU) * 16 + sub;  // of the block; the lane's rows are RPW apart
-    const int token = any ? pool_token(p, e, first) : -1;
+    int token = any ? pool_token(p, e, first) : -1;
+    if (!ATTN_OPS_IN_BOUNDS(token + BLOCK <= p.num_pages * p.page_size, p, SITE_OPS_PAGE)) token = -1;
     uint2 raw[ITER][2];
     if (hi > lo) {
         const T *x = static_cast<const T *>(p.x[kv]) + e * p.xb[kv] + h * p.xh[kv] +
@@ -165,7 +166,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_e4m3_kernel(const __grid_c
         for (int i = 0; i < ITER; ++i) {
             const int r = i * RPW + sub;
             raw[i][0] = raw[i][1] = make_uint2(0u, 0u);
-            if (r >= lo && r < hi) load_row<ADJACENT>(x + i * RPW * p.xs[kv], rl, raw[i]);
+            if (r >= lo && r < hi && ATTN_OPS_IN_BOUNDS(first + row0 + i * RPW - start < p.s && h < p.heads, p, SITE_OPS_ROW))
+                load_row<ADJACENT>(x + i * RPW * p.xs[kv], rl, raw[i]);
         }
     }
     float *scale_at = nullptr;
@@ -173,7 +175,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_e4m3_kernel(const __grid_c
     if (token >= 0) {
         const int page = token / p.page_size;
         scale_at = p.scale[kv] + (static_cast<int64_t>(page) * p.heads + h) * (p.page_size / BLOCK) + (token - page * p.page_size) / BLOCK;
-        if (!fresh) was = *scale_at;
+        if (!ATTN_OPS_IN_BOUNDS(scale_at - p.scale[kv] < p.num_pages * p.heads * (p.page_size / BLOCK), p, SITE_OPS_SCALE)) token = -1;
+        else if (!fresh) was = *scale_at;
     }
     auto value = [&](int i, float (&v)[8]) {
         unpack4<T>(raw[i][0], v);
@@ -209,7 +212,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_e4m3_kernel(const __grid_c
     const bool grows = need > was;  // false too for a stored NaN: its rows are left
     const bool keep = !fresh && !grows;
     const float inv = keep ? 1.f / was : pow2(-ex);
-    // (every warp of the unit has read the scale: the barrier above)
+    // (every warp of the unit has read the scale: the barrier above; and every lane of this one)
+    __syncwarp();
     if (warp % WPU == 0 && lane == 0) *scale_at = keep ? was : need;
     uint8_t *dst = static_cast<uint8_t *>(p.pool[kv]) + (static_cast<int64_t>(token + row0) * p.heads + h) * D;
     const int64_t step = static_cast<int64_t>(RPW) * p.heads * D;

@@ -18,6 +18,7 @@ struct KvAppendParams {
     int64_t b, s, num_pages, pages_per_seq;
     int heads, page_size, block_shift;  // a block of the scales is 1 << block_shift tokens
     int rot, interleaved;
+    uint32_t *status;
     uint32_t nblk_heads;         // e4m3: blocks that a request's new rows can touch, times heads
 };
 

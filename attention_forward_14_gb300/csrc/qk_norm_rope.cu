@@ -13,7 +13,7 @@
 // them is used, which keeps enough bytes in flight.
 #include "qk_norm_rope.h"
 
-#include "attn_fwd_kernel.cuh"
+#include "attn_fwd.h"
 #include "rows.cuh"
 
 namespace attn {
@@ -32,7 +32,7 @@ constexpr int heads_per_unit(int rows) { return rows * (32 / (D / 8)); }
 __device__ __forceinline__ bool known_position(const NormRopeParams &p, int pos)
 {
     if (p.cos == nullptr) return true;
-    if (pos >= p.table_len) record_status(p.status, 4u, 0u);
+    if (pos >= p.table_len) record_status(p.status, ATTN_STATUS_POSITION, 0u);
     return pos >= 0 && pos < p.table_len;
 }
 
@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
     if (unit >= p.units) return;
     const NormUnit u = norm_unit(p, unit, heads_per_unit<D>(ROWS));
     const NormRopeSide &sd = p.side[u.key ? 1 : 0];
+    if (!ATTN_OPS_IN_BOUNDS(u.bi * p.s + u.si < p.tokens && u.h0 < sd.heads, p, SITE_OPS_UNIT)) return;
     const RowLane rl = row_lane<ADJACENT>(l, p.rot);
     const int left = sd.heads - u.h0 - sub;  // row i of the lane group is there when i * RPW < left
 
@@ -167,10 +168,11 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
         };
         const uint32_t stride = gridDim.x * (kThreads / 32);
         for (uint32_t unit = blockIdx.x * (kThreads / 32) + warp; unit < units; unit += stride) {
-            Fetched cur;
-            fetch(unit, cur);
             const uint32_t tok = unit / sd.groups;
             const int h = static_cast<int>(unit - tok * sd.groups) * HPU + sub;
+            if (!ATTN_OPS_IN_BOUNDS(tok < p.tokens && h - sub < sd.heads, p, SITE_OPS_UNIT)) continue;
+            Fetched cur;
+            fetch(unit, cur);
             const int left = sd.heads - h;
             const uint32_t bi = tok / static_cast<uint32_t>(p.s), si = tok - bi * static_cast<uint32_t>(p.s);
             T *out = static_cast<T *>(sd.out) + bi * sd.ob + si * sd.os + h * sd.oh;
@@ -223,6 +225,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
         }
         __syncthreads();
         for (int i = threadIdx.x; i < D; i += kThreads) {
+            if (!ATTN_OPS_IN_BOUNDS(blockIdx.x < kNormRopeMaxBlocks, p, SITE_OPS_PART)) break;
             float v = 0.f;
 #pragma unroll
             for (int wi = 0; wi < kThreads / 32; ++wi) v += acc_s[wi][i];

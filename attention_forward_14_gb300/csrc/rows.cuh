@@ -22,7 +22,30 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "attn_fwd_kernel.cuh"
+
 namespace attn {
+
+// Checked build (ATTN_CHECKED=1): the operators that use this file compare
+// what they decode and index with its bounds; a violation is recorded in the
+// status word, with its site, and the access is left out.
+enum : uint32_t {
+    SITE_OPS_UNIT = 70,   // decoded unit outside the problem
+    SITE_OPS_ROW = 71,    // row of an input
+    SITE_OPS_PAGE = 72,   // row of the pool
+    SITE_OPS_SCALE = 73,  // scale of a block
+    SITE_OPS_PART = 74,   // partial result
+};
+#if ATTN_CHECKED
+#define ATTN_OPS_IN_BOUNDS(cond, p, site) ops_in_bounds((cond), (p).status, (site))
+__device__ __forceinline__ bool ops_in_bounds(bool ok, uint32_t *status, uint32_t site)
+{
+    if (!ok) record_status(status, STATUS_BOUNDS, site);
+    return ok;
+}
+#else
+#define ATTN_OPS_IN_BOUNDS(cond, p, site) true
+#endif
 
 template <typename T>
 struct Pair;

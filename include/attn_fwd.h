@@ -494,7 +494,9 @@ int64_t attn_qk_norm_rope_bwd_workspace_bytes(int64_t d);
  *   new_seqlens  : device int32 [b], how many of the s_new tokens are there
  *                  (a padded batch; clamped to 0..s_new), or NULL: all.
  *   block_table  : device int32 [b, pages_per_seq], as for
- *                  attn_fwd_kvcache_paged.  No two entries may name one page.
+ *                  attn_fwd_kvcache_paged.  Requests may share pages that the
+ *                  new tokens do not reach; a page that they reach may be
+ *                  named once.
  *   page_size    : a positive multiple of 16.
  *   cos, sin     : fp32 [table_len, rot / 2], as for attn_qk_norm_rope, or
  *                  both NULL: no rotation.  table_len is at least the
@@ -555,7 +557,11 @@ int attn_kvcache_append_paged(const void *k_new, const void *v_new,
  * sees no key gets O = 0 and LSE = -inf.  Slots at or past L are not read
  * into the result.  The work is dealt out by the lengths on the device, so
  * batches of unequal lengths need no split count.  P is rounded to fp16
- * before the product with V; sums and statistics are fp32.
+ * before the product with V; sums and statistics are fp32.  With 49 or more
+ * query rows of a key head, keys and values enter the products divided by the
+ * largest scale among 128 consecutive tokens, in fp16: exact for scales that
+ * are powers of two within 2^15 of it; what is smaller loses bits below 2^-24
+ * of that scale, other ratios round a value by 2^-11.
  * Returns ATTN_OK or a negative ATTN_ERR_* code.
  */
 int attn_fwd_kvcache_paged_fp8(const void *q, const void *k_pool,
