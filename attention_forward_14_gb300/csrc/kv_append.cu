@@ -15,6 +15,8 @@
 // value no precision, since its rounding is relative.
 #include "kv_append.h"
 
+#include <type_traits>
+
 #include "rows.cuh"
 
 namespace attn {
@@ -82,25 +84,23 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
     for (int i = 0; i < ROWS; ++i) {
         const int h = h0 + i * RPW + sub;
         if (rl.on) {  // a row that is not rotated is a copy, bit for bit
-            float v[8];
-            unpack4<T>(raw[i][0], v);
-            unpack4<T>(raw[i][1], v + 4);
-            rotate8<ADJACENT, false>(v, c, s, rl);
-            raw[i][0] = pack4<T>(v);
-            raw[i][1] = pack4<T>(v + 4);
+            float2 v[4];
+            unpack_pairs<T>(raw[i], v);
+            rotate<ADJACENT>(v, c, s);
+            pack_pairs<T>(v, raw[i]);
         }
         if (h < p.heads) store_row<ADJACENT>(dst + h * D, rl, raw[i]);
     }
 }
 
-// Largest |x| of the finite ones of eight values, and m.
-__device__ __forceinline__ float amax8(const float (&v)[8], float m)
+// Largest |x| of eight values (of the FINITE ones; else of those that are no
+// NaN), and m.
+template <bool FINITE>
+__device__ __forceinline__ float amax8(const float2 (&v)[4], float m)
 {
+    auto size = [](float x) { return !FINITE || fabsf(x) < INFINITY ? fabsf(x) : 0.f; };
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-        const float a = fabsf(v[i]) < INFINITY ? fabsf(v[i]) : 0.f, b = fabsf(v[i + 1]) < INFINITY ? fabsf(v[i + 1]) : 0.f;
-        m = max3f(m, a, b);
-    }
+    for (int i = 0; i < 4; ++i) m = max3f(m, size(v[i].x), size(v[i].y));
     return m;
 }
 
@@ -114,9 +114,10 @@ __device__ __forceinline__ int scale_exponent(uint32_t a)
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
-__device__ __forceinline__ uint32_t to_e4m3(const float *v, float f)
+__device__ __forceinline__ uint32_t to_e4m3(float2 a, float2 b, float f)
 {
-    return pack_e4m3x2(v[0] * f, v[1] * f) | (pack_e4m3x2(v[2] * f, v[3] * f) << 16);
+    a = __fmul2_rn(a, make_float2(f, f)), b = __fmul2_rn(b, make_float2(f, f));
+    return pack_e4m3x2(a.x, a.y) | (pack_e4m3x2(b.x, b.y) << 16);
 }
 
 // e4m3 pool.  A unit is one block of one head of the keys or of the values,
@@ -178,28 +179,31 @@ __global__ void __launch_bounds__(kThreads) kv_append_e4m3_kernel(const __grid_c
         if (!ATTN_OPS_IN_BOUNDS(scale_at - p.scale[kv] < p.num_pages * p.heads * (p.page_size / BLOCK), p, SITE_OPS_SCALE)) token = -1;
         else if (!fresh) was = *scale_at;
     }
-    auto value = [&](int i, float (&v)[8]) {
-        unpack4<T>(raw[i][0], v);
-        unpack4<T>(raw[i][1], v + 4);
+    auto value = [&](int i, float2 (&v)[4]) {
+        unpack_pairs<T>(raw[i], v);
         if (rl.on) {
             float c[4], s[4];
             const int r = i * RPW + sub;
             load_angles(p.cos, p.sin, static_cast<int64_t>(first + (r >= lo && r < hi ? i * RPW + row0 : 0)) * (p.rot / 2), rl, c, s);
-            rotate8<ADJACENT, false>(v, c, s, rl);
+            rotate<ADJACENT>(v, c, s);
         }
     };
-    float top = 0.f;
-    if (hi > lo) {
+    auto largest = [&](auto finite) {
+        float top = 0.f;
+        if (hi > lo) {
 #pragma unroll
-        for (int i = 0; i < ITER; ++i) {
-            if (i * RPW + RPW <= lo || i * RPW >= hi) continue;
-            float v[8];
-            value(i, v);
-            top = amax8(v, top);
+            for (int i = 0; i < ITER; ++i) {
+                if (i * RPW + RPW <= lo || i * RPW >= hi) continue;
+                float2 v[4];
+                value(i, v);
+                top = amax8<decltype(finite)::value>(v, top);
+            }
         }
-    }
-    // the bits of non-negative floats compare like integers
-    uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+        // the bits of non-negative floats compare like integers
+        return __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+    };
+    uint32_t m = largest(std::false_type());
+    if (m >= 0x7F800000u) m = largest(std::true_type());  // an infinity among them: look again, past it
     if constexpr (WPU > 1) {
         if (lane == 0) warp_max[warp] = m;
         __syncthreads();
@@ -221,10 +225,10 @@ __global__ void __launch_bounds__(kThreads) kv_append_e4m3_kernel(const __grid_c
     for (int i = 0; i < ITER; ++i) {
         if (i * RPW + RPW <= lo || i * RPW >= hi) continue;
         const int r = i * RPW + sub;
-        float v[8];
+        float2 v[4];
         value(i, v);
         if (r >= lo && r < hi) {
-            const uint32_t a = to_e4m3(v, inv), b = to_e4m3(v + 4, inv);
+            const uint32_t a = to_e4m3(v[0], v[1], inv), b = to_e4m3(v[2], v[3], inv);
             if constexpr (ADJACENT) {
                 *reinterpret_cast<uint2 *>(dst + i * step + rl.lo) = make_uint2(a, b);
             } else {
@@ -239,10 +243,10 @@ __global__ void __launch_bounds__(kThreads) kv_append_e4m3_kernel(const __grid_c
             if (i * RPW + sub >= old) break;
             uint2 *at = reinterpret_cast<uint2 *>(dst + i * step + 8 * l);
             const uint2 w = *at;
-            float v[8];
-            unpack4<__half>(make_uint2(e4m3x2_to_f16x2(w.x), e4m3x2_to_f16x2(w.x >> 16)), v);
-            unpack4<__half>(make_uint2(e4m3x2_to_f16x2(w.y), e4m3x2_to_f16x2(w.y >> 16)), v + 4);
-            *at = make_uint2(to_e4m3(v, f), to_e4m3(v + 4, f));
+            auto scaled = [&](uint32_t x) {
+                return to_e4m3(Pair<__half>::get(e4m3x2_to_f16x2(x)), Pair<__half>::get(e4m3x2_to_f16x2(x >> 16)), f);
+            };
+            *at = make_uint2(scaled(w.x), scaled(w.y));
         }
     }
 }

@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
     const Turn turn = make_turn<ADJACENT, false>(c, s, w);
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
+        if (i * RPW >= sd.heads - u.h0) break;  // (by every lane)
         float2 v[4];
         unpack_pairs<T>(raw[i], v);
         float r = 1.f;
@@ -189,6 +190,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
             const Turn turn = make_turn<ADJACENT, true>(c, s, ones);
 #pragma unroll
             for (int i = 0; i < ROWS; ++i) {
+                if (i * RPW >= sd.heads - (h - sub)) break;  // (by every lane)
                 float2 dy[4];
                 unpack_pairs<T>(cur.g[i], dy);
                 if (rl.on) turned<ADJACENT>(dy, turn);

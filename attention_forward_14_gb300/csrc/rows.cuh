@@ -13,9 +13,9 @@
 // are the same lane's: no value is fetched from another lane or twice, and a
 // lane needs four columns of the tables.  The price is two 8-byte accesses
 // for a 16-byte one.
-// The products and the sum are rounded one by one (no fused multiply-add),
-// so the result is the same whichever of the two orders a caller writes, and
-// equals the formula evaluated step by step in fp32.
+// In `rotate` the products and the sum are rounded one by one (no fused
+// multiply-add), so that a key appended to a cache equals the formula
+// evaluated step by step in fp32.
 #pragma once
 
 #include <cstdint>
@@ -74,18 +74,12 @@ struct Pair<__nv_bfloat16> {
     }
 };
 
-// Four 16-bit values as fp32, and back.
+// Four 16-bit values as fp32.
 template <typename T>
 __device__ __forceinline__ void unpack4(const uint2 &u, float *x)
 {
     const float2 a = Pair<T>::get(u.x), b = Pair<T>::get(u.y);
     x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
-}
-
-template <typename T>
-__device__ __forceinline__ uint2 pack4(const float *x)
-{
-    return make_uint2(Pair<T>::put(x[0], x[1]), Pair<T>::put(x[2], x[3]));
 }
 
 // Where the two runs of a lane's values lie in its row, and what it does in
@@ -143,26 +137,31 @@ __device__ __forceinline__ void load_angles(const float *cos_t, const float *sin
     s[0] = b.x, s[1] = b.y, s[2] = b.z, s[3] = b.w;
 }
 
-// x rotated (back, when `BACK`).
-template <bool ADJACENT, bool BACK>
-__device__ __forceinline__ void rotate8(float (&x)[8], const float (&c)[4], const float (&s)[4], const RowLane &r)
+// u rotated; u[0..1] is the lane's first run, u[2..3] its second.  Packed
+// two-wide arithmetic; a - b is a + (-b), and x (-s) is -(x s).
+template <bool ADJACENT>
+__device__ __forceinline__ void rotate(float2 (&u)[4], const float (&c)[4], const float (&s)[4])
 {
-    if (!r.on) return;
+    if constexpr (ADJACENT) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float &x0 = ADJACENT ? x[2 * i] : x[i], &x1 = ADJACENT ? x[2 * i + 1] : x[i + 4];
-        const float ac = __fmul_rn(x0, c[i]), bs = __fmul_rn(x1, s[i]);
-        const float bc = __fmul_rn(x1, c[i]), as = __fmul_rn(x0, s[i]);
-        x0 = BACK ? __fadd_rn(ac, bs) : __fsub_rn(ac, bs);
-        x1 = BACK ? __fsub_rn(bc, as) : __fadd_rn(bc, as);
+        for (int i = 0; i < 4; ++i)
+            u[i] = __fadd2_rn(__fmul2_rn(u[i], make_float2(c[i], c[i])),
+                              __fmul2_rn(make_float2(u[i].y, u[i].x), make_float2(-s[i], s[i])));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float2 a = u[i], b = u[i + 2];
+            const float2 co = make_float2(c[2 * i], c[2 * i + 1]), si = make_float2(s[2 * i], s[2 * i + 1]);
+            const float2 ms = make_float2(-si.x, -si.y);
+            u[i] = __fadd2_rn(__fmul2_rn(a, co), __fmul2_rn(b, ms));
+            u[i + 2] = __fadd2_rn(__fmul2_rn(b, co), __fmul2_rn(a, si));
+        }
     }
 }
 
-// The same in packed two-wide arithmetic with fused multiply-adds (half the
-// instructions, one rounding less): a lane's values as four pairs of
-// registers, u[0..1] the first run, u[2..3] the second.  `turn` is what both
-// forms need of the angles, and of a weight for each value that is folded
-// into them: out = u * a + partner(u) * b.
+// The same with fused multiply-adds (fewer instructions, one rounding less):
+// a Turn is what it needs of the angles, and of a weight for each value that
+// is folded into them: out = u * a + partner(u) * b.
 struct Turn {
     float2 a[4], b[4];
 };
