@@ -210,6 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_barrier_init();
     }
     __syncthreads();
+    await_previous();
 
     const Shares shared_out(total_units(p), static_cast<int>(gridDim.x));
     if (blockIdx.x >= shared_out.ctas) {
@@ -686,6 +687,7 @@ __global__ void __launch_bounds__(256) attn_kv8_join_kernel(const __grid_constan
     constexpr int VEC = D / 32, LOADS = kKv8MaxCtas / 32, AHEAD = 8;
     __shared__ float red[8][D], weight[8][kKv8MaxCtas];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    await_previous();
     int64_t cta = -1;  // the one that begins the item
     {
         int parts[LOADS], before = 0;
@@ -799,8 +801,7 @@ cudaError_t launch_kv8_t(const Kv8LaunchArgs &a)
         if (e != cudaSuccess) return e;
         ready.store(1, std::memory_order_release);
     }
-    kern<<<a.grid, kThreads, Kv8Cfg<D>::SMEM, a.stream>>>(a.k, a.v, a.p);
-    e = cudaGetLastError();
+    e = launch_overlapped(kern, dim3(a.grid), kThreads, Kv8Cfg<D>::SMEM, a.stream, a.k, a.v, a.p);
     return e == cudaSuccess ? launch_kv8_join(a, D, Elem<T>::BF16) : e;
 }
 
@@ -813,8 +814,7 @@ cudaError_t launch_join_t(const Kv8LaunchArgs &a)
     const int64_t items = static_cast<int64_t>(a.p.b) * (many ? a.p.h_kv : a.p.head_groups) * a.p.tiles;
     const dim3 blocks(static_cast<unsigned>(items < a.grid - 1 ? items : a.grid - 1),
                       static_cast<unsigned>(many ? a.p.tile_rows / kKv8Tile : a.p.heads));
-    attn_kv8_join_kernel<D, T><<<blocks, 256, 0, a.stream>>>(a.p, a.grid);
-    return cudaGetLastError();
+    return launch_overlapped(attn_kv8_join_kernel<D, T>, blocks, 256, 0, a.stream, a.p, a.grid);
 }
 
 template <int D, typename T>

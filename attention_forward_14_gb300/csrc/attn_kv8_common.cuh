@@ -4,6 +4,7 @@
 
 #include "attn_kv8.h"
 #include "rows.cuh"
+#include "stream_order.cuh"
 
 namespace attn {
 

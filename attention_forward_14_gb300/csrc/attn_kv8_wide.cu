@@ -270,6 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
+    await_previous();
 
     const Shares shared_out(wide_total(p), static_cast<int>(gridDim.x));
     const bool works = blockIdx.x < shared_out.ctas;
@@ -719,8 +720,7 @@ cudaError_t launch_wide_t(const Kv8LaunchArgs &a)
         if (e != cudaSuccess) return e;
         ready.store(1, std::memory_order_release);
     }
-    kern<<<a.grid, kThreads, WideCfg<D>::SMEM, a.stream>>>(a.k, a.v, a.p);
-    return cudaGetLastError();
+    return launch_overlapped(kern, dim3(a.grid), kThreads, WideCfg<D>::SMEM, a.stream, a.k, a.v, a.p);
 }
 
 }  // namespace

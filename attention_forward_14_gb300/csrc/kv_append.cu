@@ -18,6 +18,7 @@
 #include <type_traits>
 
 #include "rows.cuh"
+#include "stream_order.cuh"
 
 namespace attn {
 
@@ -54,6 +55,7 @@ template <int D, typename T, bool ADJACENT>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ KvAppendParams p)
 {
     constexpr int LPR = D / 8, RPW = 32 / LPR, ROWS = 4;
+    await_previous();
     const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
     const uint32_t unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     const uint32_t groups = (p.heads + RPW * ROWS - 1) / (RPW * ROWS);
@@ -132,6 +134,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_e4m3_kernel(const __grid_c
 {
     constexpr int LPR = D / 8, RPW = 32 / LPR, ITER = 16 / RPW, BLOCK = 16 * WPU, UPC = kThreads / 32 / WPU;
     __shared__ uint32_t warp_max[kThreads / 32];
+    await_previous();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, sub = lane / LPR;
     const int kv = blockIdx.y;
     uint32_t u = blockIdx.x * UPC + warp / WPU;
@@ -257,13 +260,13 @@ cudaError_t launch_e4m3(const KvAppendParams &p, cudaStream_t stream)
     const int wpu = 1 << (p.block_shift - 4), upc = kThreads / 32 / wpu;
     const int64_t units = p.b * static_cast<int64_t>(p.nblk_heads);
     const dim3 grid(static_cast<unsigned>((units + upc - 1) / upc), 2);
+    auto kernel = kv_append_e4m3_kernel<D, T, ADJACENT, 8>;
     switch (wpu) {
-    case 1: kv_append_e4m3_kernel<D, T, ADJACENT, 1><<<grid, kThreads, 0, stream>>>(p); break;
-    case 2: kv_append_e4m3_kernel<D, T, ADJACENT, 2><<<grid, kThreads, 0, stream>>>(p); break;
-    case 4: kv_append_e4m3_kernel<D, T, ADJACENT, 4><<<grid, kThreads, 0, stream>>>(p); break;
-    default: kv_append_e4m3_kernel<D, T, ADJACENT, 8><<<grid, kThreads, 0, stream>>>(p); break;
+    case 1: kernel = kv_append_e4m3_kernel<D, T, ADJACENT, 1>; break;
+    case 2: kernel = kv_append_e4m3_kernel<D, T, ADJACENT, 2>; break;
+    case 4: kernel = kv_append_e4m3_kernel<D, T, ADJACENT, 4>; break;
     }
-    return cudaGetLastError();
+    return launch_overlapped(kernel, grid, kThreads, 0, stream, p);
 }
 
 template <int D, typename T, bool ADJACENT>
@@ -272,8 +275,7 @@ cudaError_t launch_16bit(const KvAppendParams &p, cudaStream_t stream)
     constexpr int HPU = 4 * (32 / (D / 8));
     const int64_t units = p.b * p.s * 2 * ((p.heads + HPU - 1) / HPU);
     const unsigned blocks = static_cast<unsigned>((units + kThreads / 32 - 1) / (kThreads / 32));
-    kv_append_kernel<D, T, ADJACENT><<<blocks, kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_overlapped(kv_append_kernel<D, T, ADJACENT>, dim3(blocks), kThreads, 0, stream, p);
 }
 
 template <int D, typename T>

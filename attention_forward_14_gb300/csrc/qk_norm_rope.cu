@@ -15,6 +15,7 @@
 
 #include "attn_fwd.h"
 #include "rows.cuh"
+#include "stream_order.cuh"
 
 namespace attn {
 
@@ -72,6 +73,7 @@ template <int D, typename T, bool ADJACENT, int ROWS>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p)
 {
     constexpr int LPR = D / 8, RPW = 32 / LPR;
+    await_previous();
     const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
     const uint32_t unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     if (unit >= p.units) return;
@@ -131,6 +133,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
 {
     constexpr int LPR = D / 8, RPW = 32 / LPR, HPU = heads_per_unit<D>(ROWS);
     __shared__ float acc_s[kThreads / 32][D];
+    await_previous();
     const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR, warp = threadIdx.x >> 5;
     const RowLane rl = row_lane<ADJACENT>(l, p.rot);
 #pragma unroll 1
@@ -242,6 +245,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
 __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float *part, int blocks, int d, float *dwq, float *dwk)
 {
     __shared__ float s[32][33];
+    await_previous();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + lane;
     float v = 0.f;
@@ -274,9 +278,8 @@ template <int D, typename T>
 cudaError_t launch_fwd_t(const NormRopeParams &p0, cudaStream_t stream)
 {
     const NormRopeParams p = with_units(p0, D, kFwdRows);
-    if (p.interleaved) norm_rope_kernel<D, T, true, kFwdRows><<<blocks_of(p), kThreads, 0, stream>>>(p);
-    else norm_rope_kernel<D, T, false, kFwdRows><<<blocks_of(p), kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_overlapped(p.interleaved ? norm_rope_kernel<D, T, true, kFwdRows> : norm_rope_kernel<D, T, false, kFwdRows>,
+                             dim3(blocks_of(p)), kThreads, 0, stream, p);
 }
 
 template <int D, typename T>
@@ -286,12 +289,11 @@ cudaError_t launch_bwd_t(const NormRopeParams &p0, int sm_count, cudaStream_t st
     int blocks = blocks_of(p);
     const int cap = sm_count * kBwdBlocks < kNormRopeMaxBlocks ? sm_count * kBwdBlocks : kNormRopeMaxBlocks;
     if (blocks > cap) blocks = cap;
-    if (p.interleaved) norm_rope_bwd_kernel<D, T, true, kBwdRows><<<blocks, kThreads, 0, stream>>>(p);
-    else norm_rope_bwd_kernel<D, T, false, kBwdRows><<<blocks, kThreads, 0, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_overlapped(
+        p.interleaved ? norm_rope_bwd_kernel<D, T, true, kBwdRows> : norm_rope_bwd_kernel<D, T, false, kBwdRows>,
+        dim3(blocks), kThreads, 0, stream, p);
     if (e != cudaSuccess || p.dw_part == nullptr) return e;
-    norm_rope_dw_kernel<<<2 * D / 32, 1024, 0, stream>>>(p.dw_part, blocks, D, p.dw[0], p.dw[1]);
-    return cudaGetLastError();
+    return launch_overlapped(norm_rope_dw_kernel, dim3(2 * D / 32), 1024, 0, stream, p.dw_part, blocks, D, p.dw[0], p.dw[1]);
 }
 
 }  // namespace

@@ -189,3 +189,43 @@ def test_a_captured_step_beside_an_eager_one():
     torch.cuda.synchronize()
     for out, ref in zip(outs, want):
         assert all(torch.equal(a, r) for a, r in zip(out, ref))
+
+
+def test_calls_one_after_another_equal_calls_one_at_a_time():
+    """Launches overlap the end of what came before them in the stream: each
+    result here is the next call's input (or written over by torch between
+    two calls), and nothing waits on the host."""
+    g = torch.Generator().manual_seed(29)
+    b, h, hkv, d, page, pages, block = 3, 8, 2, 128, 64, 8, 16
+    w = torch.rand(d, generator=g).to(torch.bfloat16).to(DEV)
+    cos, sin = (t.to(DEV) for t in R.tables(pages * page, d))
+    table = torch.randperm(b * pages, generator=g).to(torch.int32).reshape(b, pages).to(DEV)
+    x0 = torch.randn(b, h, 1, d, generator=g).to(torch.bfloat16).to(DEV)
+
+    def run(wait):
+        kp, vp = (torch.zeros(b * pages, page, hkv, d, dtype=torch.float8_e4m3fn, device=DEV) for _ in range(2))
+        ks, vs = (torch.ones(b * pages, hkv, page // block, device=DEV) for _ in range(2))
+        lens = torch.tensor([0, 17, 200], dtype=torch.int32, device=DEV)
+        pos = lens[:, None].clone()
+        x, outs = x0.clone(), []
+        for _ in range(40):
+            k = x[:, :hkv] * 2
+            wait()
+            q, kk = af.attn_qk_norm_rope(x, k, w, w, cos, sin, pos)
+            wait()
+            af.attn_kvcache_append_paged(kk, k, kp, vp, lens, table, k_scale=ks, v_scale=vs)
+            wait()
+            lens += 1
+            pos += 1
+            o, lse = af.attn_fwd_kvcache_paged_fp8(q, kp, vp, ks, vs, lens, table)
+            wait()
+            dq, dk, dw, _ = af.attn_qk_norm_rope_bwd(o, o[:, :hkv], x, k, w, w, cos, sin, pos)
+            wait()
+            x = x0 + 0.5 * o + 0.01 * (dq + dw.to(o.dtype))
+            k.zero_()
+            outs += [x, lse, dk]
+        torch.cuda.synchronize()
+        return outs + [kp.view(torch.uint8), vp.view(torch.uint8), ks, vs]
+
+    for a, c in zip(run(lambda: None), run(torch.cuda.synchronize)):
+        assert a.float().isfinite().all() and torch.equal(a, c)
