@@ -79,7 +79,7 @@ def _link_marshal(obj: str) -> None:
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = MARSHAL + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", lib, "-ltorch_python", "-ltorch",
-           "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
+           "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"_marshal_ext.so failed to link:\n{r.stdout}\n{r.stderr}")

@@ -14,7 +14,8 @@
 #include <string>
 #include <utility>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <ATen/core/Tensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -114,14 +115,24 @@ public:
     void *stream() const { return raw_; }
     at::Tensor empty(at::IntArrayRef sizes, at::ScalarType type) const
     {
-        at::Tensor t = at::empty(sizes, at::TensorOptions().dtype(type).device(device_));
-        if (given_ && t.numel() > 0)
-            c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(),
-                                                          c10::cuda::getStreamFromExternal(raw_, device_.index()));
+        at::Tensor t(at::detail::empty_cuda(sizes, type, device_, std::nullopt));
+        if (t.numel() > 0) used(t.storage().data_ptr());
         return t;
+    }
+    // Memory that nobody sees: from the same allocator, without a tensor.
+    c10::DataPtr scratch(int64_t bytes) const
+    {
+        c10::DataPtr p = c10::cuda::CUDACachingAllocator::get()->allocate(static_cast<size_t>(bytes));
+        used(p);
+        return p;
     }
 
 private:
+    void used(const c10::DataPtr &p) const
+    {
+        if (given_)
+            c10::cuda::CUDACachingAllocator::recordStream(p, c10::cuda::getStreamFromExternal(raw_, device_.index()));
+    }
     c10::Device device_;
     c10::cuda::CUDAGuard guard_;
     bool given_;
@@ -155,6 +166,32 @@ Dense as_dense(const char *name, const at::Tensor &t)
     if (r.h <= 1) r.st[1] = 0;
     if (r.s <= 1) r.st[2] = 0;
     return r;
+}
+
+// A workspace: allocated with the bytes that a call needs, or the given
+// tensor.
+struct Workspace {
+    c10::DataPtr own;
+    void *p = nullptr;
+    int64_t bytes = 0;
+};
+
+Workspace workspace(const Call &call, PyObject *o, int64_t need, c10::Device device)
+{
+    Workspace w;
+    if (o == Py_None) {
+        check(need < 0 ? static_cast<int>(need) : 0);
+        w.own = call.scratch(need);
+        w.p = w.own.get();
+        w.bytes = need;
+    } else {
+        const at::Tensor &t = tensor(o, "workspace");
+        if (t.device() != device || !t.is_contiguous())
+            fail(ATTN_ERR_SHAPE, "workspace must be a contiguous tensor on the inputs' device");
+        w.p = ptr(t);
+        w.bytes = static_cast<int64_t>(t.nbytes());
+    }
+    return w;
 }
 
 // An output shaped and typed like its input: allocated (contiguous) or checked.
@@ -273,24 +310,17 @@ PyObject *qk_norm_rope_bwd(PyObject *const *a)
     tensor(a[0], "dq_out"), tensor(a[1], "dk_out");  // these are not allocated here
     const Output gq = output(call, "dq_out", a[0], in.q), gk = output(call, "dk_out", a[1], in.k);
     const Output dq = output(call, "dq", a[11], in.q), dk = output(call, "dk", a[12], in.k);
-    at::Tensor dwq, dwk, ws;
+    at::Tensor dwq, dwk;
     if (in.wq) dwq = call.empty({in.dq.d}, at::kFloat);
     if (in.wk) dwk = call.empty({in.dq.d}, at::kFloat);
-    if (a[13] != Py_None) {
-        ws = tensor(a[13], "workspace");
-        if (ws.device() != in.q.device() || !ws.is_contiguous())
-            fail(ATTN_ERR_SHAPE, "workspace must be a contiguous tensor on the inputs' device");
-    } else if (in.wq || in.wk) {
-        const int64_t need = g_lib.qk_norm_rope_bwd_workspace_bytes(in.dq.d);
-        check(need < 0 ? static_cast<int>(need) : 0);
-        ws = call.empty({need}, at::kByte);
-    }
+    Workspace ws;
+    if (in.wq || in.wk || a[13] != Py_None)
+        ws = workspace(call, a[13], g_lib.qk_norm_rope_bwd_workspace_bytes(in.dq.d), in.q.device());
     check(g_lib.qk_norm_rope_bwd(ptr(gq.t), ptr(gk.t), ptr(in.q), ptr(in.k), ptr(in.wq), ptr(in.wk), r.cos, r.sin, pos.p,
                                 ptr(dq.t), ptr(dk.t), in.wq ? dwq.data_ptr<float>() : nullptr,
                                 in.wk ? dwk.data_ptr<float>() : nullptr, gq.dense.st, gk.dense.st, in.dq.st, in.dk.st,
                                 dq.dense.st, dk.dense.st, in.dq.b, in.dq.h, in.dk.h, in.dq.s, in.dq.d, r.rot, r.length,
-                                pos.stride, truth(a[10]), eps, in.dtype, ws.defined() ? ptr(ws) : nullptr,
-                                ws.defined() ? static_cast<int64_t>(ws.nbytes()) : 0, call.stream()));
+                                pos.stride, truth(a[10]), eps, in.dtype, ws.p, ws.bytes, call.stream()));
     auto or_none = [](const at::Tensor &t) {
         if (t.defined()) return THPVariable_Wrap(t);
         Py_INCREF(Py_None);
@@ -382,7 +412,7 @@ PyObject *fwd_kvcache_paged_fp8(PyObject *const *a)
     const Call call(q, a[12]);
     const Output o = output(call, "o", a[9], q);
     if (!o.t.is_contiguous()) fail(ATTN_ERR_SHAPE, "o must be contiguous");
-    at::Tensor lse, ws;
+    at::Tensor lse;
     if (a[10] == Py_None) {
         lse = call.empty({b, h, sq}, at::kFloat);
     } else {
@@ -391,21 +421,12 @@ PyObject *fwd_kvcache_paged_fp8(PyObject *const *a)
             lse.device() != q.device())
             fail(ATTN_ERR_SHAPE, "lse must be contiguous fp32 [b, h, sq] on q's device");
     }
-    if (a[11] == Py_None) {
-        const int64_t need = g_lib.fwd_kvcache_paged_fp8_workspace_bytes(b, h, hkv, sq, d);
-        check(need < 0 ? static_cast<int>(need) : 0);
-        ws = call.empty({need}, at::kByte);
-    } else {
-        ws = tensor(a[11], "workspace");
-        if (ws.device() != q.device() || !ws.is_contiguous())
-            fail(ATTN_ERR_SHAPE, "workspace must be a contiguous tensor on q's device");
-    }
+    const Workspace ws = workspace(call, a[11], g_lib.fwd_kvcache_paged_fp8_workspace_bytes(b, h, hkv, sq, d), q.device());
     check(g_lib.fwd_kvcache_paged_fp8(ptr(q), ptr(c.k), ptr(c.v), static_cast<const float *>(ptr(c.ks)),
                                      static_cast<const float *>(ptr(c.vs)), static_cast<const int32_t *>(ptr(c.lens)),
                                      static_cast<const int32_t *>(ptr(c.table)), ptr(o.t), lse.data_ptr<float>(), b, h, hkv,
                                      sq, c.num_pages, c.page_size, c.pages_per_seq, c.block, d, truth(a[7]),
-                                     static_cast<float>(scale), dtype, ptr(ws), static_cast<int64_t>(ws.nbytes()),
-                                     call.stream()));
+                                     static_cast<float>(scale), dtype, ws.p, ws.bytes, call.stream()));
     PyObject *l = a[10];
     if (l == Py_None) l = THPVariable_Wrap(lse);
     else Py_INCREF(l);
