@@ -13,6 +13,12 @@
 // they are stored again at the new one: their value times s / 2^n, exact but
 // for what falls below e4m3's smallest normal.  A power of two costs an e4m3
 // value no precision, since its rounding is relative.
+//
+// Measured, of 6.80 TB/s (a copy): 16-bit pool 6.2 TB/s at 8 x 1000 tokens of
+// 32 heads, d64 (21.4 us); e4m3 pool 3.2 TB/s at 4 x 4001 tokens of 8 heads,
+// d128, blocks of 16 (13.2 us: 42 MB are six microseconds of memory, and the
+// angles, the rotation done twice and the conversions take half of the issue
+// slots meanwhile).
 #include "kv_append.h"
 
 #include <type_traits>

@@ -11,7 +11,16 @@
 // heads: the token's cos and sin are read once for all of the unit's heads
 // and stay in registers, and the unit's rows are loaded before the first of
 // them is used, which keeps enough bytes in flight.
+//
+// Measured, of 6.80 TB/s (a copy): forward 5.37 TB/s at b2 h32+32 s4096 d128
+// (50.4 us), 4.56 at 30011 packed tokens of 16 + 4 heads, d64 (34.5 us; the
+// four key heads fill a quarter of their unit, and two thirds of the issue
+// slots are taken); backward 5.09 (79.5 us) at the first shape, 3.1 at 8191
+// packed tokens (20.9 us, of which 2.8 are the launch that joins the partial
+// sums and three to four units of latency a warp most of the rest).
 #include "qk_norm_rope.h"
+
+#include <type_traits>
 
 #include "attn_fwd.h"
 #include "rows.cuh"
@@ -22,7 +31,8 @@ namespace attn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBwdBlocks = 2;  // of the backward on an SM; the grid is what fits at a time
+constexpr int kBwdThreads = 128, kBwdBlocks = 4;  // of the backward on an SM; the grid is what fits at a time
+constexpr int kBwdStages = 2;  // units of a warp on their way and at work
 
 // Rows that each lane group loads ahead, and the heads of a unit.
 template <int D>
@@ -126,13 +136,38 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
     }
 }
 
-// The backward's blocks go over the units of the queries, then over those of
-// the keys, so that a lane adds up one weight's gradient at a time.
-template <int D, typename T, bool ADJACENT, int ROWS>
-__global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p)
+// Copies of 8 and of 16 bytes from `src` into shared memory; zeros when `!there`.
+__device__ __forceinline__ void fetch8(uint32_t dst, const void *src, bool there)
 {
-    constexpr int LPR = D / 8, RPW = 32 / LPR, HPU = heads_per_unit<D>(ROWS);
-    __shared__ float acc_s[kThreads / 32][D];
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(there ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void fetch16(uint32_t dst, const void *src, bool there)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
+// What a lane reads of a unit, put there by the same lane (no lane waits for
+// another): a row's two runs of each tensor, the angles.
+template <bool ADJACENT, int ROWS>
+struct BwdSlot {
+    std::conditional_t<ADJACENT, uint4[32], uint2[2][32]> x[ROWS], g[ROWS];
+    float4 c[32], s[32];
+};
+
+// The backward's blocks go over the units of the queries, then over those of
+// the keys, so that a lane adds up one weight's gradient at a time (some
+// blocks for the queries and the others for the keys: 94 us and not 80 at b2
+// h32 s4096 d128, more places of memory being read at a time).  Each warp has
+// the next unit's rows on their way, in shared memory, while it works on one,
+// and the position of the one after that; with the rows in registers, and no
+// room for a second unit's, 89 us.  Three blocks on an SM: 85; five: 96; half
+// the rows and twice the stages: 106.
+template <int D, typename T, bool ADJACENT, int ROWS>
+__global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p)
+{
+    constexpr int LPR = D / 8, RPW = 32 / LPR, HPU = heads_per_unit<D>(ROWS), WARPS = kBwdThreads / 32;
+    __shared__ BwdSlot<ADJACENT, ROWS> slots[WARPS][kBwdStages];
+    __shared__ float acc_s[WARPS][D];
     await_previous();
     const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR, warp = threadIdx.x >> 5;
     const RowLane rl = row_lane<ADJACENT>(l, p.rot);
@@ -147,59 +182,100 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
             for (int e = 0; e < 4; ++e) w[e] = make_float2(w8[2 * e], w8[2 * e + 1]);
         }
         const uint32_t units = static_cast<uint32_t>(p.tokens) * sd.groups;
-        // a unit's rows, its gradients' rows and its position, as they come from memory
-        struct Fetched {
-            uint2 x[ROWS][2], g[ROWS][2];
-            int pos;
+        const uint32_t stride = gridDim.x * WARPS, first = blockIdx.x * WARPS + warp;
+        struct At {
+            uint32_t bi, si;
+            int h;   // first head of the unit
         };
-        auto fetch = [&](uint32_t unit, Fetched &f) {
-            const uint32_t tok = unit / sd.groups;
-            const int h = static_cast<int>(unit - tok * sd.groups) * HPU + sub;
-            const uint32_t bi = tok / static_cast<uint32_t>(p.s), si = tok - bi * static_cast<uint32_t>(p.s);
-            f.pos = p.pos ? __ldg(p.pos + bi * p.pos_b + si) : static_cast<int>(si);
-            const T *x = static_cast<const T *>(sd.x) + bi * sd.xb + si * sd.xs + h * sd.xh;
-            const T *g = static_cast<const T *>(sd.g) + bi * sd.gb + si * sd.gs + h * sd.gh;
-#pragma unroll
-            for (int i = 0; i < ROWS; ++i) {
-                f.x[i][0] = f.x[i][1] = f.g[i][0] = f.g[i][1] = make_uint2(0u, 0u);
-                if (h + i * RPW < sd.heads) {
-                    load_row<ADJACENT>(g, rl, f.g[i]);
-                    if (sd.w) load_row<ADJACENT>(x, rl, f.x[i]);
-                }
-                x += RPW * sd.xh;
-                g += RPW * sd.gh;
+        auto place = [&](uint32_t unit) {
+            const uint32_t tok = unit / sd.groups, bi = tok / static_cast<uint32_t>(p.s);
+            return At{bi, tok - bi * static_cast<uint32_t>(p.s), static_cast<int>(unit - tok * sd.groups) * HPU};
+        };
+        auto position = [&](uint32_t unit) {
+            if (unit >= units) return 0;
+            const At at = place(unit);
+            return p.pos ? __ldg(p.pos + at.bi * p.pos_b + at.si) : static_cast<int>(at.si);
+        };
+        auto fetch_row = [&](auto &to, const T *row, bool there) {
+            if constexpr (ADJACENT) {
+                fetch16(smem_addr(&to[lane]), row + rl.lo, there);
+            } else {
+                fetch8(smem_addr(&to[0][lane]), row + rl.lo, there);
+                fetch8(smem_addr(&to[1][lane]), row + rl.hi, there);
             }
         };
-        const uint32_t stride = gridDim.x * (kThreads / 32);
-        for (uint32_t unit = blockIdx.x * (kThreads / 32) + warp; unit < units; unit += stride) {
-            const uint32_t tok = unit / sd.groups;
-            const int h = static_cast<int>(unit - tok * sd.groups) * HPU + sub;
-            if (!ATTN_OPS_IN_BOUNDS(tok < p.tokens && h - sub < sd.heads, p, SITE_OPS_UNIT)) continue;
-            Fetched cur;
-            fetch(unit, cur);
-            const int left = sd.heads - h;
-            const uint32_t bi = tok / static_cast<uint32_t>(p.s), si = tok - bi * static_cast<uint32_t>(p.s);
-            T *out = static_cast<T *>(sd.out) + bi * sd.ob + si * sd.os + h * sd.oh;
-            const int pos = cur.pos;
-            if (!known_position(p, pos)) {
+        auto row_of = [&](const auto &from, uint2 (&r)[2]) {
+            if constexpr (ADJACENT) {
+                const uint4 v = from[lane];
+                r[0] = make_uint2(v.x, v.y), r[1] = make_uint2(v.z, v.w);
+            } else {
+                r[0] = from[0][lane], r[1] = from[1][lane];
+            }
+        };
+        // the rows and angles of a unit begin their way (none past the last: the group of copies is empty)
+        auto fetch = [&](uint32_t unit, int pos, BwdSlot<ADJACENT, ROWS> &slot) {
+            if (unit < units) {
+                const At at = place(unit);
+                const int h = at.h + sub;
+                const T *x = static_cast<const T *>(sd.x) + at.bi * sd.xb + at.si * sd.xs + h * sd.xh;
+                const T *g = static_cast<const T *>(sd.g) + at.bi * sd.gb + at.si * sd.gs + h * sd.gh;
+#pragma unroll
+                for (int i = 0; i < ROWS; ++i) {
+                    const bool there = h + i * RPW < sd.heads;
+                    fetch_row(slot.g[i], g, there);
+                    if (sd.w) fetch_row(slot.x[i], x, there);
+                    x += RPW * sd.xh;
+                    g += RPW * sd.gh;
+                }
+                if (rl.on) {
+                    const bool known = pos >= 0 && pos < p.table_len;
+                    const int64_t from = static_cast<int64_t>(known ? pos : 0) * (p.rot / 2) + rl.col;
+                    fetch16(smem_addr(&slot.c[lane]), p.cos + from, known);
+                    fetch16(smem_addr(&slot.s[lane]), p.sin + from, known);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        int pos[kBwdStages + 1];  // of the unit at work and of the ones after it
+#pragma unroll
+        for (int i = 0; i < kBwdStages; ++i) pos[i] = position(first + i * stride);
+#pragma unroll
+        for (int i = 0; i + 1 < kBwdStages; ++i) fetch(first + i * stride, pos[i], slots[warp][i]);
+        int st = 0;
+        for (uint32_t unit = first; unit < units; unit += stride) {
+            pos[kBwdStages] = position(unit + kBwdStages * stride);
+            fetch(unit + (kBwdStages - 1) * stride, pos[kBwdStages - 1], slots[warp][(st + kBwdStages - 1) % kBwdStages]);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kBwdStages - 1) : "memory");
+            const BwdSlot<ADJACENT, ROWS> &cur = slots[warp][st];
+            st = (st + 1) % kBwdStages;
+            const At at = place(unit);
+            const int left = sd.heads - at.h - sub, here = pos[0];
+#pragma unroll
+            for (int i = 0; i < kBwdStages; ++i) pos[i] = pos[i + 1];
+            if (!ATTN_OPS_IN_BOUNDS(at.bi * p.s + at.si < p.tokens && at.h < sd.heads, p, SITE_OPS_UNIT)) continue;
+            T *out = static_cast<T *>(sd.out) + at.bi * sd.ob + at.si * sd.os + (at.h + sub) * sd.oh;
+            if (!known_position(p, here)) {
                 const uint2 zero[2] = {make_uint2(0u, 0u), make_uint2(0u, 0u)};
                 for (int i = 0; i < ROWS; ++i, out += RPW * sd.oh)
                     if (i * RPW < left) store_row<ADJACENT>(out, rl, zero);
                 continue;
             }
-            float c[4], s[4];
-            load_angles(p.cos, p.sin, static_cast<int64_t>(pos) * (p.rot / 2), rl, c, s);
+            const float4 c4 = cur.c[lane], s4 = cur.s[lane];
+            const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
             const float ones[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
             const Turn turn = make_turn<ADJACENT, true>(c, s, ones);
 #pragma unroll
             for (int i = 0; i < ROWS; ++i) {
-                if (i * RPW >= sd.heads - (h - sub)) break;  // (by every lane)
+                if (i * RPW >= sd.heads - at.h) break;  // (by every lane)
                 float2 dy[4];
-                unpack_pairs<T>(cur.g[i], dy);
+                uint2 raw[2];
+                row_of(cur.g[i], raw);
+                unpack_pairs<T>(raw, dy);
                 if (rl.on) turned<ADJACENT>(dy, turn);
                 if (sd.w) {
                     float2 x[4], wdy[4];
-                    unpack_pairs<T>(cur.x[i], x);
+                    row_of(cur.x[i], raw);
+                    unpack_pairs<T>(raw, x);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) wdy[e] = __fmul2_rn(dy[e], w[e]);
                     const float r0 = rsqrtf(row_sum<LPR>(dot8(x, x)) * (1.f / D) + p.eps);
@@ -219,6 +295,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
                 out += RPW * sd.oh;
             }
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");  // (groups without copies)
         if (p.dw_part == nullptr) continue;
         // the block's sums, in a fixed order: the lane groups of a warp, then the warps
 #pragma unroll
@@ -229,11 +306,11 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
             if (sub == 0) acc_s[warp][(e < 4 ? rl.lo : rl.hi - 4) + e] = v;
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < D; i += kThreads) {
+        for (int i = threadIdx.x; i < D; i += kBwdThreads) {
             if (!ATTN_OPS_IN_BOUNDS(blockIdx.x < kNormRopeMaxBlocks, p, SITE_OPS_PART)) break;
             float v = 0.f;
 #pragma unroll
-            for (int wi = 0; wi < kThreads / 32; ++wi) v += acc_s[wi][i];
+            for (int wi = 0; wi < WARPS; ++wi) v += acc_s[wi][i];
             p.dw_part[(static_cast<int64_t>(blockIdx.x) * 2 + k) * D + i] = v;
         }
         __syncthreads();
@@ -249,7 +326,9 @@ __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float *part, i
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + lane;
     float v = 0.f;
-    for (int r = warp; r < blocks; r += 32) v += part[static_cast<int64_t>(r) * 2 * d + col];
+#pragma unroll
+    for (int i = 0; i < kNormRopeMaxBlocks / 32; ++i)  // all on their way at a time
+        if (const int r = warp + 32 * i; r < blocks) v += part[static_cast<int64_t>(r) * 2 * d + col];
     s[warp][lane] = v;
     __syncthreads();
     if (warp == 0) {
@@ -270,28 +349,28 @@ NormRopeParams with_units(const NormRopeParams &p, int d, int rows)
     return q;
 }
 
-int blocks_of(const NormRopeParams &p) { return static_cast<int>((static_cast<int64_t>(p.units) + kThreads / 32 - 1) / (kThreads / 32)); }
+int blocks_of(const NormRopeParams &p, int warps) { return static_cast<int>((static_cast<int64_t>(p.units) + warps - 1) / warps); }
 
-constexpr int kFwdRows = 4, kBwdRows = 4;  // 2 rows ahead: +14% and +7% at b2 h32 s4096 d128; 8: +15% (forward)
+constexpr int kFwdRows = 4, kBwdRows = 4;  // forward, at b2 h32 s4096 d128: 2 rows ahead +14%, 8 +15%
 
 template <int D, typename T>
 cudaError_t launch_fwd_t(const NormRopeParams &p0, cudaStream_t stream)
 {
     const NormRopeParams p = with_units(p0, D, kFwdRows);
     return launch_overlapped(p.interleaved ? norm_rope_kernel<D, T, true, kFwdRows> : norm_rope_kernel<D, T, false, kFwdRows>,
-                             dim3(blocks_of(p)), kThreads, 0, stream, p);
+                             dim3(blocks_of(p, kThreads / 32)), kThreads, 0, stream, p);
 }
 
 template <int D, typename T>
 cudaError_t launch_bwd_t(const NormRopeParams &p0, int sm_count, cudaStream_t stream)
 {
     const NormRopeParams p = with_units(p0, D, kBwdRows);
-    int blocks = blocks_of(p);
+    int blocks = blocks_of(p, kBwdThreads / 32);
     const int cap = sm_count * kBwdBlocks < kNormRopeMaxBlocks ? sm_count * kBwdBlocks : kNormRopeMaxBlocks;
     if (blocks > cap) blocks = cap;
     const cudaError_t e = launch_overlapped(
         p.interleaved ? norm_rope_bwd_kernel<D, T, true, kBwdRows> : norm_rope_bwd_kernel<D, T, false, kBwdRows>,
-        dim3(blocks), kThreads, 0, stream, p);
+        dim3(blocks), kBwdThreads, 0, stream, p);
     if (e != cudaSuccess || p.dw_part == nullptr) return e;
     return launch_overlapped(norm_rope_dw_kernel, dim3(2 * D / 32), 1024, 0, stream, p.dw_part, blocks, D, p.dw[0], p.dw[1]);
 }

@@ -38,7 +38,7 @@ struct NormRopeParams {
     float *dw[2] = {nullptr, nullptr};           // backward: gradient of each weight [d], or nullptr
 };
 
-constexpr int kNormRopeMaxBlocks = 512;  // partial sums of the weights' gradients at most
+constexpr int kNormRopeMaxBlocks = 640;  // partial sums of the weights' gradients at most
 
 cudaError_t launch_norm_rope(const NormRopeParams &p, int d, bool bf16, cudaStream_t stream);
 cudaError_t launch_norm_rope_bwd(const NormRopeParams &p, int d, bool bf16, int sm_count, cudaStream_t stream);
