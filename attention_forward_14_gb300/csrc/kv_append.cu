@@ -15,8 +15,8 @@
 // value no precision, since its rounding is relative.
 //
 // Measured, of 6.80 TB/s (a copy): 16-bit pool 6.2 TB/s at 8 x 1000 tokens of
-// 32 heads, d64 (21.4 us); e4m3 pool 3.2 TB/s at 4 x 4001 tokens of 8 heads,
-// d128, blocks of 16 (13.2 us: 42 MB are six microseconds of memory, and the
+// 32 heads, d64 (21.4 us); e4m3 pool 3.3 TB/s at 4 x 4001 tokens of 8 heads,
+// d128, blocks of 16 (13.0 us: 42 MB are six microseconds of memory, and the
 // angles, the rotation done twice and the conversions take half of the issue
 // slots meanwhile).
 #include "kv_append.h"
@@ -135,8 +135,10 @@ __device__ __forceinline__ uint32_t to_e4m3(float2 a, float2 b, float f)
 // time left in L1) and stores them: holding the rotated fp32 values instead
 // would take twice the registers.  Consecutive units are consecutive heads,
 // so a block's stores are contiguous in the pool.
+// (Four blocks on an SM, which takes nine registers of a thread: an append of
+// one token to 64 caches 4.3 us and not 4.8.)
 template <int D, typename T, bool ADJACENT, int WPU>
-__global__ void __launch_bounds__(kThreads) kv_append_e4m3_kernel(const __grid_constant__ KvAppendParams p)
+__global__ void __launch_bounds__(kThreads, 4) kv_append_e4m3_kernel(const __grid_constant__ KvAppendParams p)
 {
     constexpr int LPR = D / 8, RPW = 32 / LPR, ITER = 16 / RPW, BLOCK = 16 * WPU, UPC = kThreads / 32 / WPU;
     __shared__ uint32_t warp_max[kThreads / 32];

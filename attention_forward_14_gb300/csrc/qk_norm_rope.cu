@@ -12,8 +12,8 @@
 // and stay in registers, and the unit's rows are loaded before the first of
 // them is used, which keeps enough bytes in flight.
 //
-// Measured, of 6.80 TB/s (a copy): forward 5.37 TB/s at b2 h32+32 s4096 d128
-// (50.4 us), 4.56 at 30011 packed tokens of 16 + 4 heads, d64 (34.5 us; the
+// Measured, of 6.80 TB/s (a copy): forward 5.62 TB/s at b2 h32+32 s4096 d128
+// (48.1 us), 5.08 at 30011 packed tokens of 16 + 4 heads, d64 (31.0 us; the
 // four key heads fill a quarter of their unit, and two thirds of the issue
 // slots are taken); backward 5.09 (79.5 us) at the first shape, 3.1 at 8191
 // packed tokens (20.9 us, of which 2.8 are the launch that joins the partial
@@ -30,7 +30,10 @@ namespace attn {
 
 namespace {
 
-constexpr int kThreads = 256;
+// Of the forward: blocks that end, and make room, in smaller pieces.  256
+// threads: 50.9 us at b2 h32 s4096 d128, 128: 49.0, and in 56 registers (nine
+// blocks on an SM) 48.1; ten blocks: 48.6, twelve: 61.
+constexpr int kThreads = 128, kBlocks = 9;
 constexpr int kBwdThreads = 128, kBwdBlocks = 4;  // of the backward on an SM; the grid is what fits at a time
 constexpr int kBwdStages = 2;  // units of a warp on their way and at work
 
@@ -80,7 +83,7 @@ __device__ __forceinline__ void load_weight(const void *w, const RowLane &rl, fl
 }
 
 template <int D, typename T, bool ADJACENT, int ROWS>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p)
+__global__ void __launch_bounds__(kThreads, kBlocks) norm_rope_kernel(const __grid_constant__ NormRopeParams p)
 {
     constexpr int LPR = D / 8, RPW = 32 / LPR;
     await_previous();
