@@ -664,10 +664,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (it == n_units && threadIdx.x == 0) {
             // the item that this CTA begins and others go on with, if there is one
             const int64_t first_unit = u0 + it - j_end;
-            Kv8Cut c = {0, 0, 0, 0, 0};
+            Kv8Cut c = {0, 0, 0, 0};
             if (!item_ends && first_unit >= u0) {
                 c.parts = static_cast<int>(shared_out.owner(first_unit + at.n - 1) - blockIdx.x) + 1;
-                c.second = first_unit > u0 ? 1 : 0;
+                if (first_unit > u0) c.parts = -c.parts;
                 c.b = at.b;
                 c.hg = at.hg;
                 c.tile = at.tile;
@@ -680,67 +680,122 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// VEC consecutive fp32 values, past L1 (another kernel wrote them).
+template <int VEC>
+__device__ __forceinline__ void load_part(const float *src, float (&v)[VEC])
+{
+    if constexpr (VEC == 4) {
+        const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else {
+        const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
+        v[0] = x.x, v[1] = x.y;
+    }
+}
+
 // Joins the parts of an item that several CTAs share: the blockIdx.x-th of
 // such items, blockIdx.y the head of its group (or, of an item of 256 rows of
-// one head, which 16 of them).  A warp takes a row
-// and, when there are few rows, a share of its parts: the first parts' values
-// are on their way while it forms the weights of all of them.  The shares are
-// added up in a fixed order.
+// one head, which `rows` of them).  The shares are added up in a fixed order.
+//
+// Of two parts, as most items have when there are more items than CTAs, a
+// warp takes four rows at a time.  Of more, a warp takes a row and, when there
+// are few rows, a share of its parts: the first parts' values are on their way
+// while it forms the weights of all of them.
 template <int D, typename T>
-__global__ void __launch_bounds__(256) attn_kv8_join_kernel(const __grid_constant__ Kv8Params p, int grid)
+__global__ void __launch_bounds__(256) attn_kv8_join_kernel(const __grid_constant__ Kv8Params p, int grid, int rows)
 {
     constexpr int VEC = D / 32, LOADS = kKv8MaxCtas / 32, AHEAD = 8;
     __shared__ float red[8][D], weight[8][kKv8MaxCtas];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     await_previous();
     int64_t cta = -1;  // the one that begins the item
+    Kv8Cut cut;
     {
-        int parts[LOADS], before = 0;
+        int4 c[LOADS];
+        int before = 0;
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) parts[i] = lane + 32 * i < grid ? __ldcg(&p.cut[lane + 32 * i].parts) : 0;
+        for (int i = 0; i < LOADS; ++i)
+            c[i] = lane + 32 * i < grid ? __ldcg(reinterpret_cast<const int4 *>(p.cut + lane + 32 * i)) : make_int4(0, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
-            const uint32_t cuts = __ballot_sync(0xffffffffu, parts[i] > 0);
-            const bool it_is = parts[i] > 0 && before + __popc(cuts & ((1u << lane) - 1u)) == static_cast<int>(blockIdx.x);
+            const uint32_t cuts = __ballot_sync(0xffffffffu, c[i].x != 0);
+            const bool it_is = c[i].x != 0 && before + __popc(cuts & ((1u << lane) - 1u)) == static_cast<int>(blockIdx.x);
             const uint32_t found = __ballot_sync(0xffffffffu, it_is);
-            if (found != 0u) cta = 32 * i + __ffs(found) - 1;
+            if (found != 0u) {
+                const int src = __ffs(found) - 1;
+                cta = 32 * i + src;
+                cut.parts = __shfl_sync(0xffffffffu, c[i].x, src);
+                cut.b = __shfl_sync(0xffffffffu, c[i].y, src);
+                cut.hg = __shfl_sync(0xffffffffu, c[i].z, src);
+                cut.tile = __shfl_sync(0xffffffffu, c[i].w, src);
+            }
             before += __popc(cuts);
         }
     }
     if (cta < 0) return;
-    const Kv8Cut cut = p.cut[cta];
-    const int n = cut.parts;
+    const int n = abs(cut.parts);
     if (!ATTN_OPS_IN_BOUNDS(cta + n <= grid && cut.b >= 0 && cut.b < p.b && cut.tile >= 0 && cut.tile < p.tiles && cut.hg >= 0 &&
                                 cut.hg < (p.tile_rows > kKv8Tile ? p.h_kv : p.head_groups), p, SITE_OPS_PART))
         return;
     const bool many = p.tile_rows > kKv8Tile;
-    const int first = cut.tile * p.tile_rows + (many ? blockIdx.y * kKv8Tile : 0);  // of its key head's rows
-    const int nr = min(min(p.tile_rows, kKv8Tile), p.rows - first);
+    const int in_item = many ? blockIdx.y * rows : 0;              // of its rows, the block's first
+    const int first = cut.tile * p.tile_rows + in_item;            // of its key head's rows
+    const int nr = min(min(p.tile_rows - in_item, rows), p.rows - first);
     if (nr <= 0) return;
     auto part_of = [&](int k) {
-        return (2 * (cta + k) + (k == 0 ? cut.second : 0)) * (many ? p.tile_rows : kWarps * kKv8Tile) + blockIdx.y * kKv8Tile;
+        return (2 * (cta + k) + (k == 0 && cut.parts < 0 ? 1 : 0)) * (many ? p.tile_rows : kWarps * kKv8Tile) +
+               (many ? in_item : blockIdx.y * kKv8Tile);
     };
     const int64_t row0 = row_at(p, cut.b, many ? cut.hg : cut.hg * p.heads + static_cast<int>(blockIdx.y), first);
+    auto store = [&](int r, const float (&o)[VEC], float inv) {
+        uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(p.o) + (row0 + r) * D + lane * VEC);
+        if constexpr (VEC == 4)
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(Pair<T>::put(o[0] * inv, o[1] * inv), Pair<T>::put(o[2] * inv, o[3] * inv));
+        else
+            *dst = Pair<T>::put(o[0] * inv, o[1] * inv);
+    };
+    if (n == 2) {
+        constexpr int AT_ONCE = 4;
+        const int64_t part[2] = {part_of(0), part_of(1)};
+        for (int r0 = warp; r0 < nr; r0 += 8 * AT_ONCE) {
+            float2 ml[AT_ONCE][2];
+            float v[AT_ONCE][2][VEC];
+#pragma unroll
+            for (int i = 0; i < AT_ONCE; ++i) {
+                const int r = r0 + 8 * i;
+                if (r >= nr) continue;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    ml[i][k] = __ldcg(reinterpret_cast<const float2 *>(p.ml_part + (part[k] + r) * 2));
+                    load_part<VEC>(p.o_part + (part[k] + r) * D + lane * VEC, v[i][k]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < AT_ONCE; ++i) {
+                const int r = r0 + 8 * i;
+                if (r >= nr) continue;
+                const float m = fmaxf(ml[i][0].x, ml[i][1].x);
+                const float f0 = ml[i][0].x == m ? 1.f : ex2_approx(ml[i][0].x - m), f1 = ml[i][1].x == m ? 1.f : ex2_approx(ml[i][1].x - m);
+                const float l = fmaf(ml[i][1].y, f1, ml[i][0].y * f0);
+                float o[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) o[e] = fmaf(v[i][1][e], f1, v[i][0][e] * f0);
+                store(r, o, l == 0.f ? 0.f : 1.f / l);
+                if (lane == 0 && p.lse) p.lse[row0 + r] = lse_of(m, l);
+            }
+        }
+        return;
+    }
     const int wide = nr > 4 ? 8 : (nr > 2 ? 4 : nr);  // warps that have rows of their own
     const int sub = warp / wide, subs = 8 / wide;
     for (int r0 = 0; r0 < nr; r0 += wide) {
         const int r = r0 + warp % wide;
         const bool have = r < nr;
-        auto value = [&](int k, float (&v)[VEC]) {
-            const float *src = p.o_part + (part_of(k) + r) * D + lane * VEC;
-            if constexpr (VEC == 4) {
-                const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
-                v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-            } else {
-                const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
-                v[0] = x.x, v[1] = x.y;
-            }
-        };
         float v[AHEAD][VEC];
         auto load = [&](int k0) {
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i)
-                if (have && k0 + i * subs < n) value(k0 + i * subs, v[i]);
+                if (have && k0 + i * subs < n) load_part<VEC>(p.o_part + (part_of(k0 + i * subs) + r) * D + lane * VEC, v[i]);
         };
         load(sub);
         float2 a[LOADS];
@@ -759,7 +814,6 @@ __global__ void __launch_bounds__(256) attn_kv8_join_kernel(const __grid_constan
             l = fmaf(a[i].y, a[i].x, l);
         }
         l = row_sum<32>(l);
-        const float inv = l == 0.f ? 0.f : 1.f / l;
         if (have && sub == 0 && lane == 0 && p.lse) p.lse[row0 + r] = lse_of(m, l);
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) weight[warp][lane + 32 * i] = a[i].x;
@@ -787,11 +841,7 @@ __global__ void __launch_bounds__(256) attn_kv8_join_kernel(const __grid_constan
                     for (int i = 0; i < VEC; ++i) o[i] += red[warp + q * wide][lane * VEC + i];
             __syncthreads();
         }
-        if (sub == 0 && have) {
-            uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(p.o) + (row0 + r) * D + lane * VEC);
-#pragma unroll
-            for (int i = 0; i < VEC / 2; ++i) dst[i] = Pair<T>::put(o[2 * i] * inv, o[2 * i + 1] * inv);
-        }
+        if (sub == 0 && have) store(r, o, l == 0.f ? 0.f : 1.f / l);
     }
 }
 
@@ -817,9 +867,12 @@ cudaError_t launch_join_t(const Kv8LaunchArgs &a)
     const bool many = a.p.tile_rows > kKv8Tile;
     // no more items are cut than there are items, or cuts
     const int64_t items = static_cast<int64_t>(a.p.b) * (many ? a.p.h_kv : a.p.head_groups) * a.p.tiles;
+    // of an item of 256 rows a block takes 16, or with enough items to fill the GPU 64, whose loads it has on their
+    // way together (151 cut items of 256 rows: 39 us and XX)
+    const int rows = many && items >= a.grid ? 4 * kKv8Tile : kKv8Tile;
     const dim3 blocks(static_cast<unsigned>(items < a.grid - 1 ? items : a.grid - 1),
-                      static_cast<unsigned>(many ? a.p.tile_rows / kKv8Tile : a.p.heads));
-    return launch_overlapped(attn_kv8_join_kernel<D, T>, blocks, 256, 0, a.stream, a.p, a.grid);
+                      static_cast<unsigned>(many ? a.p.tile_rows / rows : a.p.heads));
+    return launch_overlapped(attn_kv8_join_kernel<D, T>, blocks, 256, 0, a.stream, a.p, a.grid, rows);
 }
 
 template <int D, typename T>

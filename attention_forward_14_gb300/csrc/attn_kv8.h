@@ -10,9 +10,8 @@
 namespace attn {
 
 // An item that a CTA begins and later CTAs go on with.
-struct Kv8Cut {
-    int32_t parts;        // CTAs that have a part (0: there is no such item)
-    int32_t second;       // 1: the item is not this CTA's first
+struct alignas(16) Kv8Cut {
+    int32_t parts;        // CTAs that have a part (0: there is no such item); negated when it is not this CTA's first
     int32_t b, hg, tile;  // batch element, group of key heads, tile of query rows
 };
 

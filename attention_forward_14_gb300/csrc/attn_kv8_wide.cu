@@ -689,10 +689,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             it += j_end - at.j;
             if (it == n_units && threadIdx.x == 0) {
                 // the item that this CTA begins and others go on with, if there is one
-                Kv8Cut c = {0, 0, 0, 0, 0};
+                Kv8Cut c = {0, 0, 0, 0};
                 if (!item_ends && first_unit >= u0) {
                     c.parts = static_cast<int>(shared_out.owner(first_unit + at.n - 1) - blockIdx.x) + 1;
-                    c.second = first_unit > u0 ? 1 : 0;
+                    if (first_unit > u0) c.parts = -c.parts;
                     c.b = at.b;
                     c.hg = at.kvh;
                     c.tile = at.blk;
