@@ -693,9 +693,11 @@ __device__ __forceinline__ void load_part(const float *src, float (&v)[VEC])
     }
 }
 
+constexpr int kJoinAhead = 8, kRounds = 2;
+
 // Joins the parts of an item that several CTAs share: the blockIdx.x-th of
-// such items, blockIdx.y the head of its group (or, of an item of 256 rows of
-// one head, which `rows` of them).  The shares are added up in a fixed order.
+// such items, blockIdx.y the head of its group and which `rows` of its rows.
+// The shares are added up in a fixed order.
 //
 // Of two parts, as most items have when there are more items than CTAs, a
 // warp takes four rows at a time.  Of more, a warp takes a row and, when there
@@ -704,7 +706,7 @@ __device__ __forceinline__ void load_part(const float *src, float (&v)[VEC])
 template <int D, typename T>
 __global__ void __launch_bounds__(256) attn_kv8_join_kernel(const __grid_constant__ Kv8Params p, int grid, int rows)
 {
-    constexpr int VEC = D / 32, LOADS = kKv8MaxCtas / 32, AHEAD = 8;
+    constexpr int VEC = D / 32, LOADS = kKv8MaxCtas / 32, AHEAD = kJoinAhead;
     __shared__ float red[8][D], weight[8][kKv8MaxCtas];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     await_previous();
@@ -738,15 +740,16 @@ __global__ void __launch_bounds__(256) attn_kv8_join_kernel(const __grid_constan
                                 cut.hg < (p.tile_rows > kKv8Tile ? p.h_kv : p.head_groups), p, SITE_OPS_PART))
         return;
     const bool many = p.tile_rows > kKv8Tile;
-    const int in_item = many ? blockIdx.y * rows : 0;              // of its rows, the block's first
+    const int pieces = p.tile_rows / rows, hw = blockIdx.y / pieces;
+    const int in_item = (blockIdx.y - hw * pieces) * rows;         // of its rows, the block's first
     const int first = cut.tile * p.tile_rows + in_item;            // of its key head's rows
-    const int nr = min(min(p.tile_rows - in_item, rows), p.rows - first);
+    const int nr = min(rows, p.rows - first);
     if (nr <= 0) return;
     auto part_of = [&](int k) {
-        return (2 * (cta + k) + (k == 0 && cut.parts < 0 ? 1 : 0)) * (many ? p.tile_rows : kWarps * kKv8Tile) +
-               (many ? in_item : blockIdx.y * kKv8Tile);
+        return (2 * (cta + k) + (k == 0 && cut.parts < 0 ? 1 : 0)) * (many ? kKv8WideRows : kWarps * kKv8Tile) + hw * kKv8Tile +
+               in_item;
     };
-    const int64_t row0 = row_at(p, cut.b, many ? cut.hg : cut.hg * p.heads + static_cast<int>(blockIdx.y), first);
+    const int64_t row0 = row_at(p, cut.b, many ? cut.hg : cut.hg * p.heads + hw, first);
     auto store = [&](int r, const float (&o)[VEC], float inv) {
         uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(p.o) + (row0 + r) * D + lane * VEC);
         if constexpr (VEC == 4)
@@ -867,11 +870,17 @@ cudaError_t launch_join_t(const Kv8LaunchArgs &a)
     const bool many = a.p.tile_rows > kKv8Tile;
     // no more items are cut than there are items, or cuts
     const int64_t items = static_cast<int64_t>(a.p.b) * (many ? a.p.h_kv : a.p.head_groups) * a.p.tiles;
-    // of an item of 256 rows a block takes 16, or with enough items to fill the GPU 64, whose loads it has on their
-    // way together (151 cut items of 256 rows: 39 us and XX)
-    const int rows = many && items >= a.grid ? 4 * kKv8Tile : kKv8Tile;
-    const dim3 blocks(static_cast<unsigned>(items < a.grid - 1 ? items : a.grid - 1),
-                      static_cast<unsigned>(many ? a.p.tile_rows / rows : a.p.heads));
+    // Rows of a block: up to the 64 whose loads it can have on their way, fewer while there are not enough blocks for
+    // the GPU and a warp would go through its share of a row's parts in more than kRounds rounds.  In us for the whole
+    // call, 16 rows and this: 256 rows of 256 items, 151 of them cut in two 488 and 442 (the join itself 39 and 14); one
+    // cache of 16383 tokens, 8 key heads, 4 rows 17.2 and 13.5; two of 16000, one key head, 256 rows 49.2 and 41.6.
+    const int64_t cuts = items < a.grid - 1 ? items : a.grid - 1;
+    const int heads = many ? 1 : a.p.heads, used = a.p.rows < a.p.tile_rows ? a.p.rows : a.p.tile_rows;
+    int rows = many ? 4 * kKv8Tile : a.p.tile_rows;
+    const int64_t parts = a.grid / items + 2;  // of an item, about
+    auto warps_a_row = [&] { const int n = rows < used ? rows : used; return n > 4 ? 1 : (n > 2 ? 2 : 8 / n); };
+    while (rows > 1 && cuts * heads * ((used + rows - 1) / rows) < a.grid && parts > kRounds * kJoinAhead * warps_a_row()) rows /= 2;
+    const dim3 blocks(static_cast<unsigned>(cuts), static_cast<unsigned>(heads * (a.p.tile_rows / rows)));
     return launch_overlapped(attn_kv8_join_kernel<D, T>, blocks, 256, 0, a.stream, a.p, a.grid, rows);
 }
 
