@@ -1450,10 +1450,10 @@ int attn_kvcache_append_paged(const void *k_new, const void *v_new, void *k_pool
 }
 
 // Query rows of one key head from which the kernel for many rows is taken.
-// Both, in us (16 rows at a time, and that one), at 8 caches of up to 16383
-// tokens and 8 key heads, d = 128: 32 rows 73 and 99, 48 rows 100 and 100, 64
-// rows 119 and 101; at one cache of 4000 tokens: 32 rows 30 and 22, 64 rows
-// 30 and 23.
+// Both, in us (16 rows at a time, and that one), with 8 key heads, d = 128: 8
+// caches of up to 16383 tokens, 32 rows 73 and 98, 48 rows 100 and 102, 64
+// rows 120 and 106; one cache of 16383 tokens, 32 rows 27 and 34, 64 rows 35
+// and 37; of 4000, 32 rows 19.4 and 19.8, 64 rows 22 and 21.
 constexpr int64_t kKv8WideFrom = 49;
 
 // Rows of the parts of a CTA's item: 16 of each head of a group, or 256.

@@ -30,13 +30,14 @@
 // log2(vs), with the sum of the weights divided by vs, tile by tile.
 //
 // What bounds it, at the last 2048 of 16384 tokens (causal, 32 heads on
-// 8 key heads, d = 128): 488 us, 1.06 of 1.91 PFLOP/s.  Without the
-// conversion (raw tiles fed as they are, wrong results) 420-439: a tile of
-// 128 keys serves two Q tiles only, so its conversion (16 KB read, 32 KB
-// written and read again by the products) takes the shared memory's time away
-// from them.  The rest is the softmax, one exponential for each score, in
-// step with the tensor cores.  At 64 rows (8 caches of up to 16383 tokens, 8
-// key heads) 101 us: the bytes of the cache and their conversion.
+// 8 key heads, d = 128): 442 us, 1.17 of 1.91 PFLOP/s, of which the join 14;
+// the tensor cores are at work half of the time.  Without the conversion (raw
+// tiles fed as they are, wrong results) 50 to 70 less: a tile of 128 keys
+// serves two Q tiles only, so its conversion (16 KB read, 32 KB written and
+// read again by the products) takes the shared memory's time away from them.
+// The rest is the softmax, one exponential for each score, in step with the
+// tensor cores.  At 64 rows (8 caches of up to 16383 tokens, 8 key heads) 101
+// to 106 us: the bytes of the cache and their conversion.
 #include "attn_kv8_common.cuh"
 
 namespace attn {
@@ -44,7 +45,7 @@ namespace attn {
 namespace {
 
 constexpr int kTileRows = 128, kItemRows = 2 * kTileRows, kTileKeys = 128;
-constexpr int kTeam = 3;  // warps that convert K tiles, and as many V tiles (1: 681 us at the chunk below, 3: 498)
+constexpr int kTeam = 3;  // warps that convert K tiles, and as many V tiles (1: 681 us at the chunk above, 3: 498 in the same run)
 constexpr int kThreads = (10 + 2 * kTeam) * 32;
 static_assert(kThreads % 128 == 0, "whole warpgroups: registers are dealt out by them");
 constexpr int kSoftmaxRegs = 200, kOtherRegs = 56;  // 256 * 200 + 256 * 56 = 512 * 128
