@@ -137,24 +137,27 @@ __device__ __forceinline__ void load_angles(const float *cos_t, const float *sin
     s[0] = b.x, s[1] = b.y, s[2] = b.z, s[3] = b.w;
 }
 
-// u rotated; u[0..1] is the lane's first run, u[2..3] its second.  Packed
-// two-wide arithmetic; a - b is a + (-b), and x (-s) is -(x s).
+// u rotated; u[0..1] is the lane's first run, u[2..3] its second.  The
+// products are formed two at a time and the sums one at a time: of packed
+// products and a packed sum the compiler makes fused multiply-adds, which
+// round once and not twice.
 template <bool ADJACENT>
 __device__ __forceinline__ void rotate(float2 (&u)[4], const float (&c)[4], const float (&s)[4])
 {
     if constexpr (ADJACENT) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            u[i] = __fadd2_rn(__fmul2_rn(u[i], make_float2(c[i], c[i])),
-                              __fmul2_rn(make_float2(u[i].y, u[i].x), make_float2(-s[i], s[i])));
+        for (int i = 0; i < 4; ++i) {
+            const float2 p = __fmul2_rn(u[i], make_float2(c[i], c[i])), q = __fmul2_rn(u[i], make_float2(s[i], s[i]));
+            u[i] = make_float2(__fsub_rn(p.x, q.y), __fadd_rn(p.y, q.x));
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const float2 a = u[i], b = u[i + 2];
             const float2 co = make_float2(c[2 * i], c[2 * i + 1]), si = make_float2(s[2 * i], s[2 * i + 1]);
-            const float2 ms = make_float2(-si.x, -si.y);
-            u[i] = __fadd2_rn(__fmul2_rn(a, co), __fmul2_rn(b, ms));
-            u[i + 2] = __fadd2_rn(__fmul2_rn(b, co), __fmul2_rn(a, si));
+            const float2 ac = __fmul2_rn(u[i], co), as = __fmul2_rn(u[i], si);
+            const float2 bc = __fmul2_rn(u[i + 2], co), bs = __fmul2_rn(u[i + 2], si);
+            u[i] = make_float2(__fsub_rn(ac.x, bs.x), __fsub_rn(ac.y, bs.y));
+            u[i + 2] = make_float2(__fadd_rn(bc.x, as.x), __fadd_rn(bc.y, as.y));
         }
     }
 }

@@ -100,6 +100,40 @@ def test_append(case):
 
 
 @gpu
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_keys_equal_the_formula_step_by_step_in_fp32(interleaved, dt):
+    """Each product and each sum rounded: no difference in any bit."""
+    b, h, s, d, page, pages, rot, block = 2, 5, 250, 128, 64, 4, 96, 32
+    g = torch.Generator().manual_seed(41)
+    k = torch.randn((b, h, s, d), generator=g).to(DT[dt]).to(DEV)
+    cos, sin = (t.to(DEV) for t in R.tables(page * pages, rot))
+    table = torch.arange(b * pages, dtype=torch.int32, device=DEV).reshape(b, pages)
+    lens = torch.zeros(b, dtype=torch.int32, device=DEV)
+    x = k.float()
+    i = torch.arange(rot // 2, device=DEV)
+    first, second = (2 * i, 2 * i + 1) if interleaved else (i, i + rot // 2)
+    c, sn = cos[:s], sin[:s]
+    want = x.clone()
+    p0, p1 = x[..., first] * c, x[..., second] * sn
+    want[..., first] = p0 - p1
+    p0, p1 = x[..., second] * c, x[..., first] * sn
+    want[..., second] = p0 + p1
+
+    def tokens(pool):
+        return pool.reshape(b, page * pages, h, d)[:, :s].transpose(1, 2)
+
+    kp, vp = (torch.zeros((b * pages, page, h, d), dtype=DT[dt], device=DEV) for _ in range(2))
+    af.attn_kvcache_append_paged(k, k, kp, vp, lens, table, cos, sin, interleaved)
+    assert torch.equal(tokens(kp), want.to(DT[dt]))
+    kp, vp = (torch.zeros((b * pages, page, h, d), dtype=torch.float8_e4m3fn, device=DEV) for _ in range(2))
+    ks, vs = (torch.zeros((b * pages, h, page // block), device=DEV) for _ in range(2))
+    af.attn_kvcache_append_paged(k, k, kp, vp, lens, table, cos, sin, interleaved, ks, vs)
+    scale = ks.transpose(1, 2).reshape(b, page * pages // block, h).repeat_interleave(block, 1)[:, :s].transpose(1, 2)[..., None]
+    assert torch.equal(tokens(kp).float(), (want / scale).to(torch.float8_e4m3fn).float())
+
+
+@gpu
 @pytest.mark.parametrize("block", [0, 16])
 def test_pages_outside_the_pool_are_not_written(block):
     case = (2, 2, 40, 64, 32, 3, block, 64, False, "bf16", (0, 20), None)
