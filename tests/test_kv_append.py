@@ -226,8 +226,8 @@ S3 = ctypes.c_int64 * 3
     (dict(k_new=P + 16384), -2), (dict(v_pool=P + 16384 + 64), -2), (dict(table=P + 2), -6), (dict(vs=None), -1),
 ])
 def test_refusals(lib, kw, code):
-    a = dict(k_new=P, v_new=P + 1024, k_pool=P + 16384, v_pool=P + 32768, ks=P + 2048, vs=P + 2048, lens=P + 3072, news=None,
-             table=P + 3072, cos=P + 4096, sin=P + 4096, st=(128, 64, 64), b=1, h=1, s=2, num_pages=4, page=32, pages=2,
+    a = dict(k_new=P, v_new=P + 1024, k_pool=P + 16384, v_pool=P + 32768, ks=P + 2048, vs=P + 2048, lens=P + 3328, news=None,
+             table=P + 3328, cos=P + 4096, sin=P + 4096, st=(128, 64, 64), b=1, h=1, s=2, num_pages=4, page=32, pages=2,
              block=16, d=64, rot=64, table_len=64, dtype=1)
     a.update(kw)
     st = None if a["st"] is None else S3(*a["st"])
