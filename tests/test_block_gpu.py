@@ -229,3 +229,67 @@ def test_calls_one_after_another_equal_calls_one_at_a_time():
 
     for a, c in zip(run(lambda: None), run(torch.cuda.synchronize)):
         assert a.float().isfinite().all() and torch.equal(a, c)
+
+
+def test_launches_after_copies_clears_and_other_streams():
+    """Eager and captured: each call follows, in its stream, a copy, a memset
+    or an event of another stream, and not only a kernel; and is followed by
+    copies out of its results."""
+    g = torch.Generator().manual_seed(31)
+    b, h, hkv, d, page, pages, block = 2, 8, 2, 64, 32, 4, 16
+    w = torch.rand(d, generator=g).half().to(DEV)
+    cos, sin = (t.to(DEV) for t in R.tables(pages * page, d))
+    table = torch.arange(b * pages, dtype=torch.int32, device=DEV).reshape(b, pages)
+    lens = torch.tensor([40, 77], dtype=torch.int32, device=DEV)
+    pos = torch.zeros((b, 1), dtype=torch.int32, device=DEV)
+    src = torch.randn(b, h, 1, d, generator=g).half().to(DEV)
+    pool, scale = R.random_pool(b * pages, page, hkv, d, block, 5)
+    pool, scale = pool.view(torch.uint8).to(DEV), scale.to(DEV)
+    other = torch.cuda.Stream()
+    x, grad = torch.empty_like(src), torch.empty_like(src)
+    kp, vp = torch.empty_like(pool), torch.empty_like(pool)
+    ks, vs = torch.empty_like(scale), torch.empty_like(scale)
+    now = torch.empty_like(lens)
+
+    def elsewhere(f):
+        here = torch.cuda.current_stream()
+        other.wait_stream(here)
+        with torch.cuda.stream(other):
+            f()
+        here.wait_stream(other)
+
+    def step():
+        kp.copy_(pool), vp.copy_(pool), ks.copy_(scale), vs.copy_(scale), now.copy_(lens), pos.copy_(lens[:, None])
+        x.copy_(src)                                   # a copy, right before
+        q, k = af.attn_qk_norm_rope(x, x[:, :hkv], w, w, cos, sin, pos)
+        elsewhere(lambda: ks[0].copy_(scale[0]))       # an event of another stream
+        e = (kp.view(torch.float8_e4m3fn), vp.view(torch.float8_e4m3fn))
+        af.attn_kvcache_append_paged(k, k, *e, now, table, k_scale=ks, v_scale=vs)
+        elsewhere(lambda: now.add_(1))
+        o, lse = af.attn_fwd_kvcache_paged_fp8(q, *e, ks, vs, now, table)
+        grad.zero_()                                   # a memset
+        dq, dk, dw, _ = af.attn_qk_norm_rope_bwd(grad, grad[:, :hkv], x, x[:, :hkv], w, w, cos, sin, pos)
+        grad.copy_(o)
+        dq2, dk2, dw2, _ = af.attn_qk_norm_rope_bwd(grad, grad[:, :hkv], x, x[:, :hkv], w, w, cos, sin, pos)
+        out = [q, k, o, lse, dq, dk, dw, dq2, dk2, dw2]
+        return [torch.empty_like(t).copy_(t) for t in out]
+
+    def waited():
+        torch.cuda.synchronize()
+        r = step()
+        torch.cuda.synchronize()
+        return [t.clone() for t in r]
+
+    want = waited()
+    assert all(t.float().isfinite().all() for t in want) and want[8].abs().sum() > 0 and not want[4].any()
+    for _ in range(20):
+        got = step()
+    assert all(torch.equal(a, c) for a, c in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(5):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        assert all(torch.equal(a, c) for a, c in zip(got, want))
