@@ -11,7 +11,7 @@
 //
 // A CTA, 16 warps:
 //   warps 0-3, 4-7  softmax group t, one thread to a row of Q tile t (128
-//                   rows); it also brings its row of Q and stores its row of O
+//                   rows); its warps also bring Q's rows and store O's
 //   warp  8         issues the matrix products
 //   warp  9         copies raw K and V tiles (128 keys, TMA) and their scales
 //   warps 10-15     convert raw tiles, even ones K's and odd ones V's, to fp16
@@ -193,6 +193,13 @@ __device__ __forceinline__ void wide_next(const Kv8Params &p, WidePlace &c)
 __device__ __forceinline__ void st_tile(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d));
+}
+
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
 }
 
 template <int D, typename T>
@@ -542,46 +549,50 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int n = seen.end > 0 ? j_end - at.j : 0;
             const int r = at.blk * kItemRows + t * kTileRows + row_in_tile;  // of the key head's rows
             const bool valid = r < p.rows;
-            const int64_t row = (static_cast<int64_t>(at.b) * p.h_kv + at.kvh) * p.rows + (valid ? r : 0);
+            const int64_t row0 = (static_cast<int64_t>(at.b) * p.h_kv + at.kvh) * p.rows;
+            const int warp_row = r - lane;  // of the key head's rows, the warp's first
             const bool tile_has_rows = at.blk * kItemRows + t * kTileRows < p.rows;
             float m = -INFINITY, l = 0.f, coef = 0.f;
             const int lim = p.causal ? at.len - p.sq + r % p.sq + 1 : at.len;  // keys this row sees
             if (n > 0 && tile_has_rows) {
-                // this row of Q, in fp16, into the tile
-                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) + row * D);
-                const uint32_t dst = sQ + t * C::TILE + row_in_tile * 128;
-                float up = 1.f, down = 1.f;
-                if constexpr (Elem<T>::BF16) {
-                    uint32_t mx = 0u;
-#pragma unroll 4
-                    for (int c = 0; c < D / 8; ++c) {
-                        const uint4 v = valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                // The warp's 32 rows of Q, all on their way at once, in fp16 into the tile.  LPR lanes share a
+                // row, so that an access is of whole rows (a row to a lane: 32 lines an access, 2 us an item more).
+                constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes of a row, rows of an access
+                const int c = lane % LPR;
+                // a negative scale turns Q's signs, so that a masked score is -inf in every case
+                const uint32_t turn = p.sl2e < 0.f ? 0x80008000u : 0u;
+                uint4 q[LPR];
+#pragma unroll
+                for (int i = 0; i < LPR; ++i) {
+                    const int rr = warp_row + i * RPI + lane / LPR;
+                    q[i] = rr < p.rows ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) + (row0 + rr) * D) + c)
+                                       : make_uint4(0u, 0u, 0u, 0u);
+                }
+                float down = 1.f;  // of the row that is this lane's in the softmax
+#pragma unroll
+                for (int i = 0; i < LPR; ++i) {
+                    uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+                    if constexpr (Elem<T>::BF16) {
+                        uint32_t mx = 0u;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) mx = max(mx, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
-                    }
-                    const int e = max(static_cast<int>(mx >> 7) - 127, -100);  // the row's largest at 2^14
-                    up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
-                    down = __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
-                }
-                // a negative scale turns Q's signs, so that a masked score is -inf in every case
-                coef = fabsf(p.sl2e) * down;
-                const uint32_t turn = p.sl2e < 0.f ? 0x80008000u : 0u;
-#pragma unroll 4
-                for (int c = 0; c < D / 8; ++c) {
-                    uint4 v = valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-                    if constexpr (Elem<T>::BF16) {
-                        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int off = LPR / 2; off > 0; off >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                        const int e2 = max(static_cast<int>(mx >> 7) - 127, -100);  // the row's largest at 2^14
+                        const float up = __uint_as_float(static_cast<uint32_t>(14 - e2 + 127) << 23);
+                        const int own = __shfl_sync(0xffffffffu, e2, (lane % RPI) * LPR);
+                        if (lane / RPI == i) down = __uint_as_float(static_cast<uint32_t>(own - 14 + 127) << 23);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const float2 f = Pair<T>::get(w[e]);
                             w[e] = Pair<__half>::put(f.x * up, f.y * up);
                         }
-                        v = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    st_shared_v4(dst + (c >> 3) * C::PANEL + (((c & 7) ^ (row_in_tile & 7)) << 4), v.x ^ turn, v.y ^ turn, v.z ^ turn,
-                                 v.w ^ turn);
+                    const int in_tile = (warp & 3) * 32 + i * RPI + lane / LPR;
+                    st_shared_v4(sQ + t * C::TILE + (c >> 3) * C::PANEL + in_tile * 128 + (((c & 7) ^ (in_tile & 7)) << 4),
+                                 w[0] ^ turn, w[1] ^ turn, w[2] ^ turn, w[3] ^ turn);
                 }
+                coef = fabsf(p.sl2e) * down;
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(B(ctl->q_full[t]));
@@ -648,9 +659,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                const int slot_row = static_cast<int>(t * kTileRows + row_in_tile);
-                const int64_t part = (2 * static_cast<int64_t>(blockIdx.x) + (first_unit > u0 ? 1 : 0)) * kItemRows + slot_row;
+                const int64_t part0 = (2 * static_cast<int64_t>(blockIdx.x) + (first_unit > u0 ? 1 : 0)) * kItemRows;
                 const float inv = !whole ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+                // 32 columns at a time pass through the warp's rows of the Q tile, whose products are done, so that the
+                // stores are of 128 (64) bytes of a row (a row to a lane: 32 lines a store, 4 us an item more)
+                const uint32_t pass = sQ + t * C::TILE + (warp & 3) * (32 * 128);
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
@@ -664,26 +677,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = nan_at[c] >> e & 1u ? 0x7FC00000u : o[e];
                     }
-                    if (!valid) continue;
-                    if (whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(p.o) + row * D + c * 32);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint32_t w[4];
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
 #pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                w[q] = Pair<T>::put(__uint_as_float(o[8 * e + 2 * q]) * inv, __uint_as_float(o[8 * e + 2 * q + 1]) * inv);
-                            dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
-                    } else {
-                        uint4 *dst = reinterpret_cast<uint4 *>(p.o_part + part * D + c * 32);
+                    for (int e = 0; e < 8; ++e)
+                        st_shared_v4(pass + lane * 128 + ((e ^ (lane & 7)) << 4), o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    __syncwarp();
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    for (int k = 0; k < 8; ++k) {  // rows 4 k .., eight lanes to a row
+                        const int in_warp = 4 * k + (lane >> 3), rr = warp_row + in_warp, col = c * 32 + (lane & 7) * 4;
+                        const float4 v = ld_shared_f4(pass + in_warp * 128 + (((lane & 7) ^ (in_warp & 7)) << 4));
+                        if (rr >= p.rows) continue;
+                        if (whole)
+                            *reinterpret_cast<uint2 *>(static_cast<T *>(p.o) + (row0 + rr) * D + col) =
+                                make_uint2(Pair<T>::put(v.x, v.y), Pair<T>::put(v.z, v.w));
+                        else
+                            *reinterpret_cast<float4 *>(p.o_part + (part0 + rr - at.blk * kItemRows) * D + col) = v;
                     }
+                    __syncwarp();
                 }
                 if (valid) {
-                    if (!whole) *reinterpret_cast<float2 *>(p.ml_part + part * 2) = make_float2(m, l);
-                    else if (p.lse) p.lse[row] = lse_of(m, l);
+                    if (!whole) *reinterpret_cast<float2 *>(p.ml_part + (part0 + r - at.blk * kItemRows) * 2) = make_float2(m, l);
+                    else if (p.lse) p.lse[row0 + r] = lse_of(m, l);
                 }
                 tc_fence_before();
             }
