@@ -700,9 +700,9 @@ constexpr int kJoinAhead = 8, kRounds = 2;
 // The shares are added up in a fixed order.
 //
 // Of two parts, as most items have when there are more items than CTAs, a
-// warp takes four rows at a time.  Of more, a warp takes a row and, when there
-// are few rows, a share of its parts: the first parts' values are on their way
-// while it forms the weights of all of them.
+// warp takes four rows at a time, of three or four two.  Of more, a warp takes
+// a row and, when there are few rows, a share of its parts: the first parts'
+// values are on their way while it forms the weights of all of them.
 template <int D, typename T>
 __global__ void __launch_bounds__(256) attn_kv8_join_kernel(const __grid_constant__ Kv8Params p, int grid, int rows)
 {
@@ -757,18 +757,20 @@ __global__ void __launch_bounds__(256) attn_kv8_join_kernel(const __grid_constan
         else
             *dst = Pair<T>::put(o[0] * inv, o[1] * inv);
     };
-    if (n == 2) {
-        constexpr int AT_ONCE = 4;
-        const int64_t part[2] = {part_of(0), part_of(1)};
+    auto join_few = [&](auto parts_, auto at_once_) {
+        constexpr int N = decltype(parts_)::value, AT_ONCE = decltype(at_once_)::value;
+        int64_t part[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) part[k] = part_of(k);
         for (int r0 = warp; r0 < nr; r0 += 8 * AT_ONCE) {
-            float2 ml[AT_ONCE][2];
-            float v[AT_ONCE][2][VEC];
+            float2 ml[AT_ONCE][N];
+            float v[AT_ONCE][N][VEC];
 #pragma unroll
             for (int i = 0; i < AT_ONCE; ++i) {
                 const int r = r0 + 8 * i;
                 if (r >= nr) continue;
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
+                for (int k = 0; k < N; ++k) {
                     ml[i][k] = __ldcg(reinterpret_cast<const float2 *>(p.ml_part + (part[k] + r) * 2));
                     load_part<VEC>(p.o_part + (part[k] + r) * D + lane * VEC, v[i][k]);
                 }
@@ -777,18 +779,24 @@ __global__ void __launch_bounds__(256) attn_kv8_join_kernel(const __grid_constan
             for (int i = 0; i < AT_ONCE; ++i) {
                 const int r = r0 + 8 * i;
                 if (r >= nr) continue;
-                const float m = fmaxf(ml[i][0].x, ml[i][1].x);
-                const float f0 = ml[i][0].x == m ? 1.f : ex2_approx(ml[i][0].x - m), f1 = ml[i][1].x == m ? 1.f : ex2_approx(ml[i][1].x - m);
-                const float l = fmaf(ml[i][1].y, f1, ml[i][0].y * f0);
-                float o[VEC];
+                float m = ml[i][0].x, l = 0.f, o[VEC] = {};
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) o[e] = fmaf(v[i][1][e], f1, v[i][0][e] * f0);
+                for (int k = 1; k < N; ++k) m = fmaxf(m, ml[i][k].x);
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    const float f = ml[i][k].x == m ? 1.f : ex2_approx(ml[i][k].x - m);
+                    l = fmaf(ml[i][k].y, f, l);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) o[e] = fmaf(v[i][k][e], f, o[e]);
+                }
                 store(r, o, l == 0.f ? 0.f : 1.f / l);
                 if (lane == 0 && p.lse) p.lse[row0 + r] = lse_of(m, l);
             }
         }
-        return;
-    }
+    };
+    if (n == 2) return join_few(std::integral_constant<int, 2>(), std::integral_constant<int, 4>());
+    if (n == 3) return join_few(std::integral_constant<int, 3>(), std::integral_constant<int, 2>());
+    if (n == 4) return join_few(std::integral_constant<int, 4>(), std::integral_constant<int, 2>());
     const int wide = nr > 4 ? 8 : (nr > 2 ? 4 : nr);  // warps that have rows of their own
     const int sub = warp / wide, subs = 8 / wide;
     for (int r0 = 0; r0 < nr; r0 += wide) {
@@ -870,16 +878,20 @@ cudaError_t launch_join_t(const Kv8LaunchArgs &a)
     const bool many = a.p.tile_rows > kKv8Tile;
     // no more items are cut than there are items, or cuts
     const int64_t items = static_cast<int64_t>(a.p.b) * (many ? a.p.h_kv : a.p.head_groups) * a.p.tiles;
-    // Rows of a block: up to the 64 whose loads it can have on their way, fewer while there are not enough blocks for
-    // the GPU and a warp would go through its share of a row's parts in more than kRounds rounds.  In us for the whole
-    // call, 16 rows and this: 256 rows of 256 items, 151 of them cut in two 488 and 442 (the join itself 39 and 14); one
-    // cache of 16383 tokens, 8 key heads, 4 rows 17.2 and 13.5; two of 16000, one key head, 256 rows 49.2 and 41.6.
+    // Rows of a block.  Of items of few parts as many as keep the GPU full of blocks, up to 64; of many parts eight, one
+    // for each warp, and fewer while there are not enough blocks for the GPU and a warp would go through its share of a
+    // row's parts in more than kRounds rounds.  In us for the whole call, 16 rows and this: 256 rows of 256 items, 151 of
+    // them cut in two 488 and 442 (the join itself 39 and 14); one cache of 16383 tokens, 8 key heads, 4 rows 17.2 and
+    // 13.5; two of 16000, one key head, 256 rows 49.2 and 41.6.
     const int64_t cuts = items < a.grid - 1 ? items : a.grid - 1;
     const int heads = many ? 1 : a.p.heads, used = a.p.rows < a.p.tile_rows ? a.p.rows : a.p.tile_rows;
-    int rows = many ? 4 * kKv8Tile : a.p.tile_rows;
     const int64_t parts = a.grid / items + 2;  // of an item, about
-    auto warps_a_row = [&] { const int n = rows < used ? rows : used; return n > 4 ? 1 : (n > 2 ? 2 : 8 / n); };
-    while (rows > 1 && cuts * heads * ((used + rows - 1) / rows) < a.grid && parts > kRounds * kJoinAhead * warps_a_row()) rows /= 2;
+    auto blocks_of = [&](int r) { return cuts * heads * ((used + r - 1) / r); };
+    auto warps_a_row = [&](int r) { const int n = r < used ? r : used; return n > 4 ? 1 : (n > 2 ? 2 : 8 / n); };
+    int rows = parts > 4 ? 8 : (many ? 4 * kKv8Tile : a.p.tile_rows);
+    if (parts <= 4)
+        while (rows > 8 && blocks_of(rows) < 2 * a.grid) rows /= 2;
+    while (rows > 1 && blocks_of(rows) < a.grid && parts > kRounds * kJoinAhead * warps_a_row(rows)) rows /= 2;
     const dim3 blocks(static_cast<unsigned>(cuts), static_cast<unsigned>(heads * (a.p.tile_rows / rows)));
     return launch_overlapped(attn_kv8_join_kernel<D, T>, blocks, 256, 0, a.stream, a.p, a.grid, rows);
 }
