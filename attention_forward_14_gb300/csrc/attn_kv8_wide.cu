@@ -30,13 +30,15 @@
 // log2(vs), with the sum of the weights divided by vs, tile by tile.
 //
 // What bounds it, at the last 2048 of 16384 tokens (causal, 32 heads on
-// 8 key heads, d = 128): 442 us, 1.17 of 1.91 PFLOP/s, of which the join 14;
+// 8 key heads, d = 128): 433 us, 1.19 of 1.91 PFLOP/s, of which the join 14;
 // the tensor cores are at work half of the time.  Without the conversion (raw
 // tiles fed as they are, wrong results) 50 to 70 less: a tile of 128 keys
 // serves two Q tiles only, so its conversion (16 KB read, 32 KB written and
 // read again by the products) takes the shared memory's time away from them.
 // The rest is the softmax, one exponential for each score, in step with the
-// tensor cores.  At 64 rows (8 caches of up to 16383 tokens, 8 key heads) 101
+// tensor cores.  A CTA with little to do is bound by its chain: 3 us until it
+// knows its share, 4 until Q is in place, 3 to the second tile's scores, 2 a
+// tile from there on, 4 to store 128 KB of a part.  At 64 rows (8 caches of up to 16383 tokens, 8 key heads) 101
 // to 106 us: the bytes of the cache and their conversion.
 #include "attn_kv8_common.cuh"
 
