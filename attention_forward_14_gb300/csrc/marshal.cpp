@@ -96,46 +96,44 @@ int dtype_code(const at::Tensor &t)
     fail(ATTN_ERR_DTYPE, std::string("unsupported dtype ") + c10::toString(t.scalar_type()));
 }
 
-// The stream of a call and the tensors allocated for it: on a stream that was
-// given, their memory is not handed out again before that stream is done.
+// The stream of a call and the memory allocated for it.  On a stream that was
+// given, the memory comes from that stream's pool: what the current stream
+// has let go of may still be in use there, and the given one does not wait
+// for that.
 class Call {
 public:
-    Call(const at::Tensor &t, PyObject *stream) : device_(t.device()), guard_(t.device()), given_(stream != Py_None)
+    Call(const at::Tensor &t, PyObject *stream)
+        : device_(t.device()), guard_(t.device()), current_(c10::cuda::getCurrentCUDAStream(device_.index()))
     {
-        if (given_) {
-            raw_ = reinterpret_cast<cudaStream_t>(PyLong_AsVoidPtr(stream));
-            if (PyErr_Occurred()) {
-                PyErr_Clear();
-                fail(ATTN_ERR_NULL, "stream must be a stream");
-            }
-        } else {
-            raw_ = c10::cuda::getCurrentCUDAStream(device_.index()).stream();
+        raw_ = current_.stream();
+        if (stream == Py_None) return;
+        raw_ = reinterpret_cast<cudaStream_t>(PyLong_AsVoidPtr(stream));
+        if (PyErr_Occurred()) {
+            PyErr_Clear();
+            fail(ATTN_ERR_NULL, "stream must be a stream");
         }
+        if (raw_ != current_.stream()) on_.reset_stream(c10::cuda::getStreamFromExternal(raw_, device_.index()));
     }
     void *stream() const { return raw_; }
+    // An output: the caller goes on with it on the current stream, so it is not handed out again before that is done.
     at::Tensor empty(at::IntArrayRef sizes, at::ScalarType type) const
     {
         at::Tensor t(at::detail::empty_cuda(sizes, type, device_, std::nullopt));
-        if (t.numel() > 0) used(t.storage().data_ptr());
+        if (raw_ != current_.stream() && t.numel() > 0)
+            c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), current_);
         return t;
     }
     // Memory that nobody sees: from the same allocator, without a tensor.
     c10::DataPtr scratch(int64_t bytes) const
     {
-        c10::DataPtr p = c10::cuda::CUDACachingAllocator::get()->allocate(static_cast<size_t>(bytes));
-        used(p);
-        return p;
+        return c10::cuda::CUDACachingAllocator::get()->allocate(static_cast<size_t>(bytes));
     }
 
 private:
-    void used(const c10::DataPtr &p) const
-    {
-        if (given_)
-            c10::cuda::CUDACachingAllocator::recordStream(p, c10::cuda::getStreamFromExternal(raw_, device_.index()));
-    }
     c10::Device device_;
     c10::cuda::CUDAGuard guard_;
-    bool given_;
+    c10::cuda::CUDAStream current_;
+    c10::cuda::OptionalCUDAStreamGuard on_;
     cudaStream_t raw_ = nullptr;
 };
 

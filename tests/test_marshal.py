@@ -1,0 +1,115 @@
+"""The Python entry of the operators around the attention: where its memory
+comes from, what it holds while it works, what it raises."""
+import pytest
+import torch
+
+import attention_forward_14_gb300 as af
+import ops_ref as R
+
+gpu = pytest.mark.gpu
+DEV = torch.device("cuda", 0)
+
+
+def norm_inputs(b=2, h=4, hkv=2, s=33, d=64, seed=1):
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randn((b, h, s, d), generator=g).half().to(DEV)
+    k = torch.randn((b, hkv, s, d), generator=g).half().to(DEV)
+    w = torch.rand(d, generator=g).half().to(DEV)
+    return q, k, w, w
+
+
+def cache_inputs(b=2, h=4, hkv=2, sq=1, d=64, page=64, pages=4, block=16, seed=2):
+    g = torch.Generator().manual_seed(seed)
+    kp, ks = R.random_pool(b * pages, page, hkv, d, block, seed)
+    vp, vs = R.random_pool(b * pages, page, hkv, d, block, seed + 1)
+    table = torch.randperm(b * pages, generator=g).reshape(b, pages).to(torch.int32)
+    lens = torch.full((b,), page * pages - 3, dtype=torch.int32)
+    q = torch.randn((b, h, sq, d), generator=g).half()
+    return [t.to(DEV) for t in (q, kp, vp, ks, vs, lens, table)]
+
+
+# Every call that allocates, at sizes that differ from one to the next.
+CALLS = {
+    "norm": lambda stream: af.attn_qk_norm_rope(*norm_inputs(), stream=stream),
+    "norm backward": lambda stream: af.attn_qk_norm_rope_bwd(*norm_inputs(seed=3)[:2], *norm_inputs(), stream=stream),
+    "attention": lambda stream: af.attn_fwd_kvcache_paged_fp8(*cache_inputs(), stream=stream),
+    "attention, many rows": lambda stream: af.attn_fwd_kvcache_paged_fp8(*cache_inputs(sq=40), stream=stream),
+}
+
+
+def _held(handle):
+    """Bytes that the allocator has from the driver for one stream, and bytes of them in use."""
+    torch.cuda.synchronize()
+    segments = [s for s in torch.cuda.memory_snapshot() if s["stream"] == handle and s["device"] == 0]
+    return sum(s["total_size"] for s in segments), sum(s["allocated_size"] for s in segments)
+
+
+@gpu
+@pytest.mark.parametrize("name", CALLS)
+def test_memory_of_a_call_on_a_given_stream_is_that_streams(name):
+    """Nothing is in flight here: only where the memory comes from is looked
+    at.  A block that the current stream has let go of must not serve a launch
+    on another one, which does not wait for what the block's last user does."""
+    here, side = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(here):
+        wanted = CALLS[name](None)                       # from the pool of `here`, workspace and all
+        free = [t for t in wanted if t is not None]
+        sizes = [t.numel() * t.element_size() for t in free]
+        addresses = {t.data_ptr() for t in free}
+        torch.cuda.synchronize()
+        del wanted, free
+        before = _held(here.cuda_stream)[0]
+        out = [t for t in CALLS[name](side) if t is not None]
+        torch.cuda.synchronize()
+    assert not addresses & {t.data_ptr() for t in out}
+    assert _held(here.cuda_stream)[0] == before
+    total, used = _held(side.cuda_stream)
+    assert used >= sum(sizes) and total >= used
+
+
+@gpu
+def test_calls_in_turn_on_the_current_and_on_a_given_stream():
+    """Long calls on the current stream and calls on another stream between
+    them, nothing waiting for anything: each has what it has alone."""
+    sets = [[*norm_inputs(4, 8, 8, 700 + 100 * i, 128, 10 + i)] for i in range(4)]
+    grads = [norm_inputs(4, 8, 8, 700 + 100 * i, 128, 20 + i)[:2] for i in range(4)]
+    caches = [cache_inputs(4, 8, 2, 1 + 39 * (i % 2), 128, 64, 16, 16, 30 + i) for i in range(4)]
+    side = torch.cuda.Stream()
+
+    def calls(i, stream):
+        return (*af.attn_qk_norm_rope(*sets[i], stream=stream), *af.attn_qk_norm_rope_bwd(*grads[i], *sets[i], stream=stream),
+                *af.attn_fwd_kvcache_paged_fp8(*caches[i], stream=stream))
+
+    want = []
+    for i in range(4):
+        want.append([t.clone() for t in calls(i, None)])
+        torch.cuda.synchronize()
+    side.wait_stream(torch.cuda.current_stream())
+    got = [[], [], [], []]
+    for _ in range(6):
+        for i in range(4):
+            got[i].append(calls(i, side if i % 2 else None))
+            if i % 2 == 0:
+                calls(i, None)  # its outputs are let go at once
+    torch.cuda.synchronize()
+    for i in range(4):
+        assert all(torch.equal(a, w) for r in got[i] for a, w in zip(r, want[i]))
+
+
+@gpu
+def test_an_output_on_a_given_stream_outlives_its_use_on_the_current_one():
+    """It is let go while the current stream still reads it: its memory is not
+    handed out again before that is done."""
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    q, k, w, _ = norm_inputs(2, 8, 8, 2000, 128)
+    want = af.attn_qk_norm_rope(q, k, w, w)[0]
+    torch.cuda.synchronize()
+    copies = []
+    for _ in range(20):
+        o, _ = af.attn_qk_norm_rope(q, k, w, w, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        copies.append(o + 0)
+        del o, _
+    torch.cuda.synchronize()
+    assert all(torch.equal(c, want) for c in copies)
