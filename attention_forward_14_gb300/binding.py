@@ -624,7 +624,8 @@ def attn_qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, po
     ``q_weight`` / ``k_weight`` [d] (None: no norm); ``cos`` / ``sin`` fp32
     [table_len, rot / 2] (None: no rotation); ``positions`` int32 [b, s], [s]
     or (packed) [total], None: 0..s-1.  ``interleaved``: adjacent pairs turn
-    instead of pairs (i, i + rot/2).  Negative positions are padding (zeros).
+    instead of pairs (i, i + rot/2).  Negative positions are padding (zeros),
+    also without tables.
     Returns (q_out, k_out), contiguous unless given."""
     return _marshal().qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, q_out, k_out,
                                    _handle(stream))

@@ -763,7 +763,7 @@ int norm_rope_common(NormRopeParams *p, const float *cos, const float *sin, cons
     *nothing = b * s == 0 || h + h_kv == 0;
     p->cos = cos;
     p->sin = sin;
-    p->pos = cos ? positions : nullptr;
+    p->pos = positions;
     p->pos_b = pos_stride;
     p->tokens = b * s;
     p->s = s;

@@ -41,13 +41,15 @@ constexpr int kBwdStages = 2;  // units of a warp on their way and at work
 template <int D>
 constexpr int heads_per_unit(int rows) { return rows * (32 / (D / 8)); }
 
-// False when a position lies outside the tables (the token's rows are then
-// zeros, and a position past the end is reported).
+// False for a token of padding (its position is negative, with tables or
+// without) and when a position lies past the tables, which is reported: the
+// token's rows are then zeros.
 __device__ __forceinline__ bool known_position(const NormRopeParams &p, int pos)
 {
-    if (p.cos == nullptr) return true;
-    if (pos >= p.table_len) record_status(p.status, ATTN_STATUS_POSITION, 0u);
-    return pos >= 0 && pos < p.table_len;
+    if (pos < 0) return false;
+    if (p.cos == nullptr || pos < p.table_len) return true;
+    record_status(p.status, ATTN_STATUS_POSITION, 0u);
+    return false;
 }
 
 // The unit of a warp: a token and ROWS rows of each of the warp's lane groups.

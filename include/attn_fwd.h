@@ -424,9 +424,11 @@ int64_t attn_bwd_varlen_workspace_bytes(int64_t batch, int64_t h,
  *                rot is a multiple of 16, at most d.
  *   positions  : device int32, token (b, s) at positions[b * pos_stride + s]
  *                (pos_stride 0: the same for every b), or NULL: position s.
- *                A token whose position is negative is padding: its outputs
- *                (and gradients) are 0.  So are those of a position at or
- *                past table_len, which also records ATTN_STATUS_POSITION.
+ *                A token whose position is negative is padding, with
+ *                tables or without: its outputs (and gradients) are 0, and
+ *                it adds nothing to a weight's gradient.  So it is for a
+ *                position at or past table_len, which also records
+ *                ATTN_STATUS_POSITION.
  *   eps        : finite, not negative.
  * Returns ATTN_OK or a negative ATTN_ERR_* code.
  */
