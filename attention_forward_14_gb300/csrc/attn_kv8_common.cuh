@@ -11,6 +11,10 @@ namespace attn {
 // P = 2^(x - m + kOffset) against a reference m that is raised when some x
 // exceeds it by more than kSlack: P <= 2^14, within fp16.
 constexpr float kOffset = 6.f, kSlack = 8.f;
+// Values with a smaller scale count as multiples of this one (it is the
+// smallest that an append gives a block), so that neither its logarithm nor
+// the weights divided by it leave fp32's range.
+constexpr float kLeastScale = 0x1p-64f;
 enum : uint32_t { SITE_KV8_FULL = 60, SITE_KV8_EMPTY = 61, SITE_KV8_Q = 62, SITE_KV8_CONV = 63, SITE_KV8_S = 64,
                   SITE_KV8_P = 65, SITE_KV8_O = 66 };
 
@@ -41,10 +45,11 @@ __device__ __forceinline__ float lg2_approx(float x)
     return y;
 }
 
+// (with subnormal results: x may be above 2^126)
 __device__ __forceinline__ float rcp_approx(float x)
 {
     float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 

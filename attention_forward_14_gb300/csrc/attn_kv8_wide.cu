@@ -27,7 +27,8 @@
 // a block of 128 tokens, an exact power of two for scales that are; a factor
 // below 2^-15 loses what is below 2^-34 of the tile's largest value), and that
 // scale enters the softmax's exponent: x = ks scale log2(e) (q . k) +
-// log2(vs), with the sum of the weights divided by vs, tile by tile.
+// log2(vs), with the sum of the weights divided by vs, tile by tile.  Of
+// values it is 2^-64 at least: the quotients stay within fp32.
 //
 // What bounds it, at the last 2048 of 16384 tokens (causal, 32 heads on
 // 8 key heads, d = 128): 433 us, 1.19 of 1.91 PFLOP/s, of which the join 14;
@@ -389,7 +390,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int off = 4; off > 0; off >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, off));
                     const float vref = __shfl_sync(0xffffffffu, ref, 8);  // of a K slot
-                    if (kv == 0 && wi == 0 && lane == 0) ctl->refs[tiles % kRefRing] = make_float2(ref, vref);
+                    if (kv == 1) ref = fmaxf(ref, kLeastScale);
+                    if (kv == 0 && wi == 0 && lane == 0)
+                        ctl->refs[tiles % kRefRing] = make_float2(ref, vref > 0.f ? fmaxf(vref, kLeastScale) : 0.f);
                     const float mul = ref > 0.f ? sc / ref : 0.f;  // lanes 0..7: of keys 16 lane ..
                     ok = warp_waits(B(ctl->conv_empty[cs]), ((n / C::CONV_SLOTS) & 1u) ^ 1u, SITE_KV8_CONV);
                     if (!ok) break;

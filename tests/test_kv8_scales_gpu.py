@@ -1,0 +1,103 @@
+"""Attention over an e4m3 paged cache with block scales of every size that the
+interface allows, in each of the kernels: few rows of a key head, one tile of
+128 rows, several of them.
+
+Bounds.  x is a score in log2 with its values' scale added, P = 2^(x - m + 6)
+rounded to fp16: by 2^-11 of it, and by 2^-25 where it is below 2^-14.  The
+largest P is 2^-2 at least (m is raised once some x exceeds it by 8), so the
+second adds up to n 2^-23 of the largest |V| over n keys.  A score's fp32 dot
+product is off by some 2^-22 of |q| |k|; O by twice that factor.  O's own
+rounding comes on top, and where the outputs are fp16 their subnormal half step.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import ops_ref as R
+import test_kv8 as K8
+
+pytestmark = pytest.mark.gpu
+
+# query rows of a key head: the kernel for few, one tile of the other, several items of it
+SQ = {"few": 3, "one tile": 30, "many": 150}
+D = 128
+
+
+def draw(rows, lens=(384, 200), seed=9, block=16, spread=0.0):
+    return K8.draw((2, 4, 2, SQ[rows], D, 64, 6, block, "bf16", True, lens), seed=seed, spread=spread, nan=False)
+
+
+def check(st, scale=1 / math.sqrt(D), floor=0.0):
+    o, lse = K8.call(st, True, scale)
+    o, lse = R.f64(o), R.f64(lse)
+    ro, rl = R.attend_paged(R.f64(st["q"]), R.f64(st["kp"]), R.f64(st["vp"]), R.f64(st["ks"]), R.f64(st["vs"]),
+                            st["lens"].numpy(), st["table"].numpy(), True, scale)
+    assert not np.isnan(o).any() and not np.isnan(lse).any()
+    dead = np.isinf(rl)
+    assert np.array_equal(np.isinf(lse), dead) and (lse[dead] < 0).all() and (o[dead] == 0).all()
+    q, n = R.f64(st["q"]), int(st["lens"].max())
+    group = q.shape[1] // st["kp"].shape[2]
+    err = np.zeros(q.shape[:3])
+    vmax = np.zeros(q.shape[:3])
+    for e in range(q.shape[0]):
+        pages = st["table"][e].numpy()
+        pages = pages[(pages >= 0) & (pages < st["kp"].shape[0])]
+        for h in range(q.shape[1]):
+            ks, vs = (R.f64(st[x])[pages, h // group].max() for x in ("ks", "vs"))
+            err[e, h] = 2.0 ** -22 * abs(scale) * np.linalg.norm(q[e, h], axis=-1) * ks * 448 * math.sqrt(D)
+            vmax[e, h] = vs * np.abs(R.f64(st["vp"])[pages, :, h // group]).max()
+    assert (np.abs(lse - rl)[~dead] <= (err + 2.0 ** -20 * (1 + np.abs(rl)))[~dead]).all(), np.abs(lse - rl)[~dead].max()
+    bound = R.HALF_STEP[torch.bfloat16] * np.abs(ro) + ((2.0 ** -11 + n * 2.0 ** -23 + 2 * err) * vmax)[..., None] + floor
+    assert (np.abs(o - ro) <= bound).all(), (np.abs(o - ro) - bound).max()
+    # and as a whole the roundings of P are independent: O is as good as its own type
+    for e in range(q.shape[0]):
+        for h in range(q.shape[1]):
+            assert np.linalg.norm((o - ro)[e, h]) <= 2 ** -7 * np.linalg.norm(ro[e, h]) + floor * math.sqrt(o[e, h].size)
+    return o, lse
+
+
+# what V's products lose below 2^-24 of the scale that they enter with, which is 2^-64 at least, times 448 / 2
+LOST = 2.0 ** (-64 - 25 + 9)
+
+
+@pytest.mark.parametrize("rows", ["one tile", "many"])
+@pytest.mark.parametrize("vs", [2.0 ** -127, 2.0 ** -130, 2.0 ** -149, 2.0 ** -126 / 448, 2.0 ** -100, 2.0 ** -70])
+def test_values_of_tiny_scales_among_others(rows, vs):
+    """One tile of 128 tokens of them, between tiles of ordinary scales."""
+    st = draw(rows)
+    for e in range(2):
+        st["vs"][st["table"][e, 2:4].long()] = float(np.float32(vs))
+    check(st, floor=LOST)
+
+
+@pytest.mark.parametrize("rows", ["one tile", "many"])
+@pytest.mark.parametrize("vs", [2.0 ** -130, 2.0 ** -126, 2.0 ** -90, 2.0 ** -60, 2.0 ** -30])
+def test_all_values_of_small_scales(rows, vs):
+    st = draw(rows)
+    st["vs"][:] = float(np.float32(vs))
+    check(st, floor=LOST)
+
+
+@pytest.mark.parametrize("rows", ["one tile", "many"])
+@pytest.mark.parametrize("vs", [2.0 ** 60, 2.0 ** 119, 2.0 ** 126 * 1.5, 2.0 ** 127])
+def test_all_values_of_large_scales(rows, vs):
+    """Values of 1 at most, so that their products with the scale are finite."""
+    st = draw(rows)
+    st["vp"] = (st["vp"].float() / 448).to(torch.float8_e4m3fn)
+    st["vs"][:] = float(np.float32(vs))
+    check(st)
+
+
+@pytest.mark.parametrize("rows", ["one tile", "many"])
+@pytest.mark.parametrize("ks", [2.0 ** -140, 2.0 ** -126, 2.0 ** -60])
+def test_keys_of_tiny_scales(rows, ks):
+    """Scores of (almost) nothing: the mean of the values."""
+    st = draw(rows)
+    st["ks"][:] = float(np.float32(ks))
+    check(st)
+    st = draw(rows)
+    for e in range(2):
+        st["ks"][st["table"][e, 2:4].long()] = float(np.float32(ks))
+    check(st)
