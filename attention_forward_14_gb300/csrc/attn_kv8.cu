@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float vs = h ? sc.w : sc.z;
             vzero[h] = vs < 1.1754944e-38f;
             vs = vzero[h] ? 1.f : vs;
-            lv[h] = lg2_approx(vs);
+            lv[h] = log2_scale(vs);
             ivs[h] = rcp_approx(vs);
         }
         // S^T: two tiles of 16 keys

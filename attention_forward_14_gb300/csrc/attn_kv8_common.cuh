@@ -38,11 +38,15 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar)
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-__device__ __forceinline__ float lg2_approx(float x)
+// log2 of a scale (a normal number): exact for a power of two.  (Of the whole
+// number at once the approximation is off by 2^-22 of the result, which for a
+// scale of 2^-64 is 2^-16 of every weight.)
+__device__ __forceinline__ float log2_scale(float x)
 {
+    const uint32_t b = __float_as_uint(x);
     float y;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(__uint_as_float((b & 0x7FFFFFu) | 0x3F800000u)));
+    return static_cast<float>(static_cast<int>(b >> 23) - 127) + y;
 }
 
 // (with subnormal results: x may be above 2^126)
@@ -107,10 +111,14 @@ __device__ __forceinline__ float warp_max(float v)
     return v;
 }
 
-// Natural log-sum-exp of a row from its reference and sum.
+// Natural log-sum-exp of a row from its reference and sum.  With the scales of
+// the values the two are large and opposite (a scale of 2^-64: some -64 and
+// 2^70), so the sum's exponent meets the reference before its logarithm does.
 __device__ __forceinline__ float lse_of(float m, float l)
 {
-    return l == 0.f ? -INFINITY : (m - kOffset + log2f(l)) * 0.69314718055994531f;
+    int e;
+    const float f = frexpf(l, &e);
+    return l == 0.f ? -INFINITY : (m - kOffset + static_cast<float>(e) + log2f(f)) * 0.69314718055994531f;
 }
 
 }  // namespace attn

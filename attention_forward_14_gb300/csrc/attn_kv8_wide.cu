@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after();
                     const float2 ref = *const_cast<const float2 *>(&ctl->refs[(tiles + i) % kRefRing]);
                     const float vs = ref.y > 0.f ? ref.y : 1.f;
-                    const float lv = lg2_approx(vs), c = fmaxf(coef * ref.x, 1e-30f);
+                    const float lv = log2_scale(vs), c = fmaxf(coef * ref.x, 1e-30f);
                     const int vis = lim - (at.j + i) * kTileKeys;  // columns >= vis are masked
                     const bool masked = __any_sync(0xffffffffu, vis < kTileKeys);
                     uint32_t s[128];

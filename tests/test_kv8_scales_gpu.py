@@ -101,3 +101,19 @@ def test_keys_of_tiny_scales(rows, ks):
     for e in range(2):
         st["ks"][st["table"][e, 2:4].long()] = float(np.float32(ks))
     check(st)
+
+
+@pytest.mark.parametrize("rows", SQ)
+@pytest.mark.parametrize("vs", [2.0 ** -64, 2.0 ** -31, 1.0, 2.0 ** 90])
+def test_lse_does_not_depend_on_the_values_scale(rows, vs):
+    """Scores of 0: the LSE of n keys is log n.  Up to 512 of them: log2 n is
+    below 9, so its half step is 2^-21 at most, the mantissa's logarithm is off
+    by 2^-24, the product with ln 2 by 2^-22, and each of the sum's parts by
+    2^-23 of itself: below 2^-20 together."""
+    st = draw(rows)
+    st["ks"][:] = 0.0
+    st["vs"][:] = vs
+    _, lse = K8.call(st, True)
+    for e, n in enumerate(st["lens"].tolist()):
+        seen = n - SQ[rows] + 1 + np.arange(SQ[rows])
+        assert (np.abs(R.f64(lse)[e] - np.log(np.maximum(seen, 1)))[:, seen > 0] <= 2.0 ** -20).all()
