@@ -784,8 +784,8 @@ __global__ void __launch_bounds__(256) attn_kv8_join_kernel(const __grid_constan
                 for (int k = 1; k < N; ++k) m = fmaxf(m, ml[i][k].x);
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
-                    const float f = ml[i][k].x == m ? 1.f : ex2_approx(ml[i][k].x - m);
-                    l = fmaf(ml[i][k].y, f, l);
+                    const float fh = half_step(ml[i][k].x, m), f = fh * fh;
+                    l = fmaf(ml[i][k].y * fh, fh, l);
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) o[e] = fmaf(v[i][k][e], f, o[e]);
                 }
@@ -821,8 +821,9 @@ __global__ void __launch_bounds__(256) attn_kv8_join_kernel(const __grid_constan
         m = warp_max(m);
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
-            a[i].x = a[i].x == m ? 1.f : ex2_approx(a[i].x - m);
-            l = fmaf(a[i].y, a[i].x, l);
+            const float fh = half_step(a[i].x, m);
+            a[i].x = fh * fh;
+            l = fmaf(a[i].y * fh, fh, l);
         }
         l = row_sum<32>(l);
         if (have && sub == 0 && lane == 0 && p.lse) p.lse[row0 + r] = lse_of(m, l);

@@ -104,6 +104,12 @@ struct Shares {
     }
 };
 
+// The square root of 2^(m - top), by which a sum with reference m is
+// multiplied twice to have reference top.  (At once 2^-126 and less would be
+// 0, while the sum itself may be 2^70: of keys whose values are zeros, before
+// any whose scale is large.)
+__device__ __forceinline__ float half_step(float m, float top) { return m == top ? 1.f : ex2_approx(0.5f * (m - top)); }
+
 __device__ __forceinline__ float warp_max(float v)
 {
 #pragma unroll

@@ -342,9 +342,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 cp_async4(smem_addr(to), (kv || lane >= 8 ? p.v_scale : p.k_scale) + sc);
                                 cp_async_arrive(bar);
                             } else {
-                                // keys past the end take no part in the tile's largest scale; a page
-                                // outside the pool is zeros, whatever its scale
-                                *to = there ? 1.f : 0.f;
+                                // keys past the end, and the zeros of a page outside the pool, take no part
+                                // in the tile's largest scale
+                                *to = 0.f;
                                 mbar_arrive(bar);
                             }
                         }
@@ -607,26 +607,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++s_it;
                     tc_fence_after();
                     const float2 ref = *const_cast<const float2 *>(&ctl->refs[(tiles + i) % kRefRing]);
-                    const float vs = ref.y > 0.f ? ref.y : 1.f;
-                    const float lv = log2_scale(vs), c = fmaxf(coef * ref.x, 1e-30f);
+                    const float c = fmaxf(coef * ref.x, 1e-30f);
                     const int vis = lim - (at.j + i) * kTileKeys;  // columns >= vis are masked
                     const bool masked = __any_sync(0xffffffffu, vis < kTileKeys);
                     uint32_t s[128];
                     tmem_ld128_wait(tS, s);
                     if (masked) mask_columns(s, vis, false);
                     const float raw = row_extreme<false>(s);
+                    float lv, ivs;
+                    if (ref.y > 0.f) {
+                        lv = log2_scale(ref.y);
+                        ivs = rcp_approx(ref.y);
+                    } else {
+                        // No values but zeros: only the weights matter, and any scale will do: a power of two that keeps
+                        // them within fp32 without raising the reference, which would push the P of values that are small
+                        // towards fp16's subnormals.
+                        lv = rintf(fminf(fmaxf(m - 16.f - raw * c, -64.f), 100.f));
+                        ivs = ex2_approx(-lv);
+                    }
                     const float mx = fmaf(raw, c, lv);
                     const float m_new = fmaxf(m, mx);
                     const bool need = m_new > m + kSlack;
                     if (__any_sync(0xffffffffu, need)) {
-                        const float f = m_new == m ? 1.f : ex2_approx(m - m_new);
-                        if (i > 0) rescale_rows<D>(tO, f);
-                        l *= f;
+                        const float f = half_step(m, m_new);
+                        if (i > 0) rescale_rows<D>(tO, f * f);
+                        l = l * f * f;
                         m = m_new;
                     }
                     const float use = (m == -INFINITY ? 0.f : m - kOffset) - lv;
                     const float2 sums = exp_store_tile<__half, false, false>(s, 0, c, use, tS, B(ctl->p_half[t]));
-                    l = fmaf(sums.x, rcp_approx(vs), l);
+                    l = fmaf(sums.x, ivs, l);
                     warp_announce_tmem(B(ctl->p_full[t]));
                 }
                 if (!ok) break;

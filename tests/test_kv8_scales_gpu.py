@@ -45,9 +45,9 @@ def check(st, scale=1 / math.sqrt(D), floor=0.0):
         pages = st["table"][e].numpy()
         pages = pages[(pages >= 0) & (pages < st["kp"].shape[0])]
         for h in range(q.shape[1]):
-            ks, vs = (R.f64(st[x])[pages, h // group].max() for x in ("ks", "vs"))
+            ks, vs = (R.f64(st[x])[pages, h // group].max(initial=0.0) for x in ("ks", "vs"))
             err[e, h] = 2.0 ** -22 * abs(scale) * np.linalg.norm(q[e, h], axis=-1) * ks * 448 * math.sqrt(D)
-            vmax[e, h] = vs * np.abs(R.f64(st["vp"])[pages, :, h // group]).max()
+            vmax[e, h] = vs * np.abs(R.f64(st["vp"])[pages, :, h // group]).max(initial=0.0)
     assert (np.abs(lse - rl)[~dead] <= (err + 2.0 ** -20 * (1 + np.abs(rl)))[~dead]).all(), np.abs(lse - rl)[~dead].max()
     bound = R.HALF_STEP[torch.bfloat16] * np.abs(ro) + ((2.0 ** -11 + n * 2.0 ** -23 + 2 * err) * vmax)[..., None] + floor
     assert (np.abs(o - ro) <= bound).all(), (np.abs(o - ro) - bound).max()
@@ -117,3 +117,62 @@ def test_lse_does_not_depend_on_the_values_scale(rows, vs):
     for e, n in enumerate(st["lens"].tolist()):
         seen = n - SQ[rows] + 1 + np.arange(SQ[rows])
         assert (np.abs(R.f64(lse)[e] - np.log(np.maximum(seen, 1)))[:, seen > 0] <= 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("rows", ["one tile", "many"])
+@pytest.mark.parametrize("vs", [2.0 ** -64, 2.0 ** -40, 2.0 ** -25, 1.0, 2.0 ** 60, 2.0 ** 119])
+@pytest.mark.parametrize("zeros", [[0], [3], [5], [2, 3], [0, 1, 4, 5]], ids=str)
+def test_zeros_among_values_of_one_scale(rows, vs, zeros):
+    """Pages whose blocks have a V scale of 0: keys with a weight, and no
+    value.  Two pages of 64 tokens are a whole tile of 128."""
+    st = draw(rows)
+    st["vp"] = (st["vp"].float() / 448).to(torch.float8_e4m3fn)
+    st["vs"][:] = vs
+    for e in range(2):
+        st["vs"][st["table"][e, zeros].long()] = 0.0
+    check(st)
+
+
+@pytest.mark.parametrize("rows", ["one tile", "many"])
+@pytest.mark.parametrize("vs", [2.0 ** -64, 2.0 ** -40, 2.0 ** -25, 1.0, 2.0 ** 60])
+def test_pages_outside_the_pool_among_values_of_one_scale(rows, vs):
+    st = draw(rows)
+    st["vs"][:] = vs
+    st["ks"] *= 2.0 ** -20
+    st["q"] *= 2.0 ** 10
+    st["table"][0, 1], st["table"][0, 2], st["table"][0, 3] = -1, 10 ** 6, -(2 ** 31)
+    st["table"][1, 0] = 2 ** 31 - 1
+    check(st)
+
+
+@pytest.mark.parametrize("rows", ["one tile", "many"])
+def test_nothing_but_zeros(rows):
+    """O is 0 and the LSE what the scores say."""
+    st = draw(rows)
+    st["vs"][:] = 0.0
+    o, _ = check(st)
+    assert (o == 0).all()
+    st = draw(rows)
+    st["table"][:] = -1
+    o, lse = check(st)
+    assert (o == 0).all()
+    seen = 200 - SQ[rows] + 1 + np.arange(SQ[rows])
+    assert np.abs(lse[1] - np.log(np.maximum(seen, 1)))[:, seen > 0].max() < 1e-5
+
+
+@pytest.mark.parametrize("rows", ["one tile", "many"])
+@pytest.mark.parametrize("gap", [-60.0, -20.0, 20.0, 60.0])
+def test_zeros_whose_scores_are_far_from_the_others(rows, gap):
+    """Keys of zero values that outweigh the others by 2^gap, or the reverse."""
+    st = draw(rows)
+    st["vs"][:] = 2.0 ** -20
+    st["q"] = torch.ones_like(st["q"])
+    kp = st["kp"].float() * 2.0 ** -8
+    st["ks"][:] = 1.0
+    for e in range(2):
+        far = st["table"][e, 2:4].long()
+        kp[far] = math.copysign(1.0, gap)
+        st["ks"][far] = 2.0 ** -7 * abs(gap) * math.log(2)
+        st["vs"][far] = 0.0
+    st["kp"] = kp.to(torch.float8_e4m3fn)
+    check(st, scale=1.0)
