@@ -36,11 +36,15 @@
 // conversions: 16 of them, one after another, take 560 clocks, the fp16
 // products they would replace 224.)
 //
-// Softmax, in log2: x = ks scale log2(e) (q . k8) + log2(vs).  P = 2^(x - m +
-// 6) carries the value scale, so O needs no product with it, and the sum of
-// the weights is sum(P) / vs, in fp32.  m follows the maximum of x lazily: it
-// is raised (and O and the sum rescaled) only when some x exceeds it by more
-// than 8, so P <= 2^14.
+// Softmax, in log2: s = ks scale log2(e) (q . k8), x = s + log2(vs).  A key's
+// weight is 2^(s - m + 6), summed in fp32, and what meets its values is P =
+// 2^(x - m + 6), so O needs no product with their scale.  m follows the
+// maximum of x lazily: it is raised (and O and the sum rescaled) only when some
+// x exceeds it by more than 8, so P <= 2^14.  In m a scale below 2^-64, zero
+// among them, counts as that: zeros weigh in the sum, and do not raise m above
+// the values beside them.  One exponential gives both, of x where vs >= 1 (to
+// its power of two) and of s where it is smaller: whichever is larger, so that
+// neither falls out of fp32 for the other's sake.
 //
 // What bounds it: the bytes of the cache.  8 caches of 1 to 16383 tokens (8
 // key heads, d = 128, 127 MB, 18.7 us at a copy's rate): 31.5 us, of which the
@@ -298,7 +302,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     cp_async4(sc, head_scales + from);
                     cp_async_arrive(bar);
                 } else {
-                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc), "f"(1.f) : "memory");
+                    // a page outside the pool, which reads as zeros, or no key that any row sees
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc), "f"(0.f) : "memory");
                     mbar_arrive(bar);
                 }
                 ++issued;
@@ -335,16 +340,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr bool PARTLY = decltype(partly)::value;
         const uint8_t *ks_at = mine + st * C::STAGE, *vs_at = ks_at + kWarps * C::KBYTES;
         const float4 sc = sc_ptr[st * kWarps];
-        // the scales of the two halves; a V scale of 0 is a block of zeros
-        float lv[2], ivs[2];
-        bool vzero[2];
+        // of the two halves: log2 of the values' scales as it enters the reference; e = 2^(s + lift - m + 6), of which
+        // a key's weight is e * weigh and its P e * times
+        float lv[2], lift[2], weigh[2], times[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            float vs = h ? sc.w : sc.z;
-            vzero[h] = vs < 1.1754944e-38f;
-            vs = vzero[h] ? 1.f : vs;
-            lv[h] = log2_scale(vs);
-            ivs[h] = rcp_approx(vs);
+            const float vs = h ? sc.w : sc.z;
+            lv[h] = log2_scale(fmaxf(vs, kLeastScale));
+            const int up = min(max(static_cast<int>(__float_as_uint(vs) >> 23), 127), 253);  // 1 at least, biased
+            lift[h] = static_cast<float>(up - 127);
+            weigh[h] = __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
+            times[h] = vs * weigh[h];
         }
         // S^T: two tiles of 16 keys
         float s[2][NT][4];
@@ -385,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        s[h][nt][i] = fmaf(c2[h][nt][0][i] + c2[h][nt][1][i], coef[nt][i & 1] * (h ? sc.y : sc.x), lv[h]);
+                        s[h][nt][i] = (c2[h][nt][0][i] + c2[h][nt][1][i]) * (coef[nt][i & 1] * (h ? sc.y : sc.x));
         }
         if constexpr (PARTLY) {
 #pragma unroll
@@ -402,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                top[nt][i] = fmaxf(max3f(s[0][nt][i], s[0][nt][2 + i], s[1][nt][i]), s[1][nt][2 + i]);
+                top[nt][i] = fmaxf(fmaxf(s[0][nt][i], s[0][nt][2 + i]) + lv[0], fmaxf(s[1][nt][i], s[1][nt][2 + i]) + lv[1]);
                 over = over || top[nt][i] > m[nt][i] + kSlack;
             }
         if (__any_sync(0xffffffffu, over)) {
@@ -414,9 +420,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, off));
                     n = fmaxf(n, m[nt][i]);
-                    const float f = n == m[nt][i] ? 1.f : ex2_approx(m[nt][i] - n);
+                    const float fh = half_step(m[nt][i], n), f = fh * fh;
                     m[nt][i] = n;
-                    l[nt][i] *= f;
+                    l[nt][i] = l[nt][i] * fh * fh;
 #pragma unroll
                     for (int j = 0; j < NO; ++j) {
                         acc[nt][j][i] *= f;
@@ -431,12 +437,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1] - kOffset;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float p0 = ex2_approx(s[h][nt][0] - b0), p1 = ex2_approx(s[h][nt][1] - b1);
-                const float p2 = ex2_approx(s[h][nt][2] - b0), p3 = ex2_approx(s[h][nt][3] - b1);
-                l[nt][0] = fmaf(p0 + p2, ivs[h], l[nt][0]);
-                l[nt][1] = fmaf(p1 + p3, ivs[h], l[nt][1]);
-                pb[h][nt][0] = transposed(vzero[h] ? 0u : Pair<__half>::put(p0, p1));
-                pb[h][nt][1] = transposed(vzero[h] ? 0u : Pair<__half>::put(p2, p3));
+                const float a0 = b0 - lift[h], a1 = b1 - lift[h];
+                const float2 e0 = make_float2(ex2_approx(s[h][nt][0] - a0), ex2_approx(s[h][nt][1] - a1));
+                const float2 e1 = make_float2(ex2_approx(s[h][nt][2] - a0), ex2_approx(s[h][nt][3] - a1));
+                l[nt][0] = fmaf(e0.x + e1.x, weigh[h], l[nt][0]);
+                l[nt][1] = fmaf(e0.y + e1.y, weigh[h], l[nt][1]);
+                const float2 f = make_float2(times[h], times[h]), p0 = __fmul2_rn(e0, f), p1 = __fmul2_rn(e1, f);
+                pb[h][nt][0] = transposed(Pair<__half>::put(p0.x, p0.y));
+                pb[h][nt][1] = transposed(Pair<__half>::put(p1.x, p1.y));
             }
         }
         // O^T += V^T P^T, 16 keys at a time
@@ -640,13 +648,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
                     for (int w = hw; w < kWarps; w += p.heads) {
                         const float2 a = ml[w * 8 + r8];
-                        const float f = a.x == mx ? 1.f : ex2_approx(a.x - mx);
+                        const float fh = half_step(a.x, mx), f = fh * fh;
                         const float4 v = *reinterpret_cast<const float4 *>(ob + (w * 8 + r8) * D + c4 * 4);
                         o.x = fmaf(v.x, f, o.x);
                         o.y = fmaf(v.y, f, o.y);
                         o.z = fmaf(v.z, f, o.z);
                         o.w = fmaf(v.w, f, o.w);
-                        lx = fmaf(a.y, f, lx);
+                        lx = fmaf(a.y * fh, fh, lx);
                     }
                     if (whole) {
                         const float inv = lx == 0.f ? 0.f : 1.f / lx;

@@ -62,7 +62,7 @@ def check(st, scale=1 / math.sqrt(D), floor=0.0):
 LOST = 2.0 ** (-64 - 25 + 9)
 
 
-@pytest.mark.parametrize("rows", ["one tile", "many"])
+@pytest.mark.parametrize("rows", SQ)
 @pytest.mark.parametrize("vs", [2.0 ** -127, 2.0 ** -130, 2.0 ** -149, 2.0 ** -126 / 448, 2.0 ** -100, 2.0 ** -70])
 def test_values_of_tiny_scales_among_others(rows, vs):
     """One tile of 128 tokens of them, between tiles of ordinary scales."""
@@ -72,7 +72,7 @@ def test_values_of_tiny_scales_among_others(rows, vs):
     check(st, floor=LOST)
 
 
-@pytest.mark.parametrize("rows", ["one tile", "many"])
+@pytest.mark.parametrize("rows", SQ)
 @pytest.mark.parametrize("vs", [2.0 ** -130, 2.0 ** -126, 2.0 ** -90, 2.0 ** -60, 2.0 ** -30])
 def test_all_values_of_small_scales(rows, vs):
     st = draw(rows)
@@ -80,7 +80,7 @@ def test_all_values_of_small_scales(rows, vs):
     check(st, floor=LOST)
 
 
-@pytest.mark.parametrize("rows", ["one tile", "many"])
+@pytest.mark.parametrize("rows", SQ)
 @pytest.mark.parametrize("vs", [2.0 ** 60, 2.0 ** 119, 2.0 ** 126 * 1.5, 2.0 ** 127])
 def test_all_values_of_large_scales(rows, vs):
     """Values of 1 at most, so that their products with the scale are finite."""
@@ -90,7 +90,7 @@ def test_all_values_of_large_scales(rows, vs):
     check(st)
 
 
-@pytest.mark.parametrize("rows", ["one tile", "many"])
+@pytest.mark.parametrize("rows", SQ)
 @pytest.mark.parametrize("ks", [2.0 ** -140, 2.0 ** -126, 2.0 ** -60])
 def test_keys_of_tiny_scales(rows, ks):
     """Scores of (almost) nothing: the mean of the values."""
@@ -119,7 +119,7 @@ def test_lse_does_not_depend_on_the_values_scale(rows, vs):
         assert (np.abs(R.f64(lse)[e] - np.log(np.maximum(seen, 1)))[:, seen > 0] <= 2.0 ** -20).all()
 
 
-@pytest.mark.parametrize("rows", ["one tile", "many"])
+@pytest.mark.parametrize("rows", SQ)
 @pytest.mark.parametrize("vs", [2.0 ** -64, 2.0 ** -40, 2.0 ** -25, 1.0, 2.0 ** 60, 2.0 ** 119])
 @pytest.mark.parametrize("zeros", [[0], [3], [5], [2, 3], [0, 1, 4, 5]], ids=str)
 def test_zeros_among_values_of_one_scale(rows, vs, zeros):
@@ -133,7 +133,7 @@ def test_zeros_among_values_of_one_scale(rows, vs, zeros):
     check(st)
 
 
-@pytest.mark.parametrize("rows", ["one tile", "many"])
+@pytest.mark.parametrize("rows", SQ)
 @pytest.mark.parametrize("vs", [2.0 ** -64, 2.0 ** -40, 2.0 ** -25, 1.0, 2.0 ** 60])
 def test_pages_outside_the_pool_among_values_of_one_scale(rows, vs):
     st = draw(rows)
@@ -145,7 +145,7 @@ def test_pages_outside_the_pool_among_values_of_one_scale(rows, vs):
     check(st)
 
 
-@pytest.mark.parametrize("rows", ["one tile", "many"])
+@pytest.mark.parametrize("rows", SQ)
 def test_nothing_but_zeros(rows):
     """O is 0 and the LSE what the scores say."""
     st = draw(rows)
@@ -160,7 +160,7 @@ def test_nothing_but_zeros(rows):
     assert np.abs(lse[1] - np.log(np.maximum(seen, 1)))[:, seen > 0].max() < 1e-5
 
 
-@pytest.mark.parametrize("rows", ["one tile", "many"])
+@pytest.mark.parametrize("rows", SQ)
 @pytest.mark.parametrize("gap", [-60.0, -20.0, 20.0, 60.0])
 def test_zeros_whose_scores_are_far_from_the_others(rows, gap):
     """Keys of zero values that outweigh the others by 2^gap, or the reverse."""
