@@ -174,20 +174,19 @@ struct Workspace {
     int64_t bytes = 0;
 };
 
-Workspace workspace(const Call &call, PyObject *o, int64_t need, c10::Device device)
+Workspace workspace(const Call &call, const at::Tensor *given, int64_t need, c10::Device device)
 {
     Workspace w;
-    if (o == Py_None) {
+    if (!given) {
         check(need < 0 ? static_cast<int>(need) : 0);
         w.own = call.scratch(need);
         w.p = w.own.get();
         w.bytes = need;
     } else {
-        const at::Tensor &t = tensor(o, "workspace");
-        if (t.device() != device || !t.is_contiguous())
+        if (given->device() != device || !given->is_contiguous())
             fail(ATTN_ERR_SHAPE, "workspace must be a contiguous tensor on the inputs' device");
-        w.p = ptr(t);
-        w.bytes = static_cast<int64_t>(t.nbytes());
+        w.p = ptr(*given);
+        w.bytes = static_cast<int64_t>(given->nbytes());
     }
     return w;
 }
@@ -195,29 +194,44 @@ Workspace workspace(const Call &call, PyObject *o, int64_t need, c10::Device dev
 // An output shaped and typed like its input: allocated (contiguous) or checked.
 struct Output {
     at::Tensor t;
-    PyObject *given;
     Dense dense;
-    PyObject *object() const
-    {
-        if (!given) return THPVariable_Wrap(t);
-        Py_INCREF(given);
-        return given;
-    }
 };
 
-Output output(const Call &call, const char *name, PyObject *o, const at::Tensor &like)
+Output output(const Call &call, const char *name, const at::Tensor *given, const at::Tensor &like)
 {
-    Output r{{}, o == Py_None ? nullptr : o, {}};
-    if (!r.given) {
+    Output r;
+    if (!given) {
         r.t = call.empty(like.sizes(), like.scalar_type());
     } else {
-        r.t = tensor(o, name);
+        r.t = *given;
         if (r.t.sizes() != like.sizes() || r.t.scalar_type() != like.scalar_type() || r.t.device() != like.device())
             fail(ATTN_ERR_SHAPE, std::string(name) + " must be shaped and typed like its input, on its device");
     }
     r.dense = as_dense(name, r.t);
     return r;
 }
+
+// What is returned for a tensor: the caller's own object where it gave one, None where there is none.
+PyObject *object(PyObject *given, const at::Tensor &t)
+{
+    if (given == Py_None && t.defined()) return THPVariable_Wrap(t);
+    Py_INCREF(given);
+    return given;
+}
+
+// The interpreter's lock, let go while a call allocates and launches, as the
+// other entry points do: both can wait for the device, and the device for a
+// host function that needs the lock.  No Python object is touched meanwhile.
+class WithoutLock {
+public:
+    WithoutLock() : state_(PyEval_SaveThread()) {}
+    ~WithoutLock() { PyEval_RestoreThread(state_); }
+    WithoutLock(const WithoutLock &) = delete;
+    WithoutLock &operator=(const WithoutLock &) = delete;
+
+private:
+    PyThreadState *state_;
+};
 
 struct Rotation {
     const float *cos = nullptr, *sin = nullptr;
@@ -289,12 +303,18 @@ PyObject *qk_norm_rope(PyObject *const *a)
     const Rotation r = rotation(a[4], a[5], in.q.device());
     const Positions pos = positions(a[6], in, r.cos != nullptr);
     const float eps = static_cast<float>(number(a[7], "eps"));
+    const int interleaved = truth(a[8]);
+    const at::Tensor *gq = maybe(a[9], "q_out"), *gk = maybe(a[10], "k_out");
     const Call call(in.q, a[11]);
-    const Output qo = output(call, "q_out", a[9], in.q), ko = output(call, "k_out", a[10], in.k);
-    check(g_lib.qk_norm_rope(ptr(in.q), ptr(in.k), ptr(in.wq), ptr(in.wk), r.cos, r.sin, pos.p, ptr(qo.t), ptr(ko.t),
-                            in.dq.st, in.dk.st, qo.dense.st, ko.dense.st, in.dq.b, in.dq.h, in.dk.h, in.dq.s, in.dq.d,
-                            r.rot, r.length, pos.stride, truth(a[8]), eps, in.dtype, call.stream()));
-    return Py_BuildValue("(NN)", qo.object(), ko.object());
+    Output qo, ko;
+    {
+        const WithoutLock unlocked;
+        qo = output(call, "q_out", gq, in.q), ko = output(call, "k_out", gk, in.k);
+        check(g_lib.qk_norm_rope(ptr(in.q), ptr(in.k), ptr(in.wq), ptr(in.wk), r.cos, r.sin, pos.p, ptr(qo.t), ptr(ko.t),
+                                 in.dq.st, in.dk.st, qo.dense.st, ko.dense.st, in.dq.b, in.dq.h, in.dk.h, in.dq.s, in.dq.d,
+                                 r.rot, r.length, pos.stride, interleaved, eps, in.dtype, call.stream()));
+    }
+    return Py_BuildValue("(NN)", object(a[9], qo.t), object(a[10], ko.t));
 }
 
 PyObject *qk_norm_rope_bwd(PyObject *const *a)
@@ -304,27 +324,28 @@ PyObject *qk_norm_rope_bwd(PyObject *const *a)
     const Rotation r = rotation(a[6], a[7], in.q.device());
     const Positions pos = positions(a[8], in, r.cos != nullptr);
     const float eps = static_cast<float>(number(a[9], "eps"));
+    const int interleaved = truth(a[10]);
+    const at::Tensor &dqo = tensor(a[0], "dq_out"), &dko = tensor(a[1], "dk_out");
+    const at::Tensor *gdq = maybe(a[11], "dq"), *gdk = maybe(a[12], "dk"), *gws = maybe(a[13], "workspace");
     const Call call(in.q, a[14]);
-    tensor(a[0], "dq_out"), tensor(a[1], "dk_out");  // these are not allocated here
-    const Output gq = output(call, "dq_out", a[0], in.q), gk = output(call, "dk_out", a[1], in.k);
-    const Output dq = output(call, "dq", a[11], in.q), dk = output(call, "dk", a[12], in.k);
+    Output dq, dk;
     at::Tensor dwq, dwk;
-    if (in.wq) dwq = call.empty({in.dq.d}, at::kFloat);
-    if (in.wk) dwk = call.empty({in.dq.d}, at::kFloat);
-    Workspace ws;
-    if (in.wq || in.wk || a[13] != Py_None)
-        ws = workspace(call, a[13], g_lib.qk_norm_rope_bwd_workspace_bytes(in.dq.d), in.q.device());
-    check(g_lib.qk_norm_rope_bwd(ptr(gq.t), ptr(gk.t), ptr(in.q), ptr(in.k), ptr(in.wq), ptr(in.wk), r.cos, r.sin, pos.p,
-                                ptr(dq.t), ptr(dk.t), in.wq ? dwq.data_ptr<float>() : nullptr,
-                                in.wk ? dwk.data_ptr<float>() : nullptr, gq.dense.st, gk.dense.st, in.dq.st, in.dk.st,
-                                dq.dense.st, dk.dense.st, in.dq.b, in.dq.h, in.dk.h, in.dq.s, in.dq.d, r.rot, r.length,
-                                pos.stride, truth(a[10]), eps, in.dtype, ws.p, ws.bytes, call.stream()));
-    auto or_none = [](const at::Tensor &t) {
-        if (t.defined()) return THPVariable_Wrap(t);
-        Py_INCREF(Py_None);
-        return Py_None;
-    };
-    return Py_BuildValue("(NNNN)", dq.object(), dk.object(), or_none(dwq), or_none(dwk));
+    {
+        const WithoutLock unlocked;
+        const Output gq = output(call, "dq_out", &dqo, in.q), gk = output(call, "dk_out", &dko, in.k);
+        dq = output(call, "dq", gdq, in.q), dk = output(call, "dk", gdk, in.k);
+        if (in.wq) dwq = call.empty({in.dq.d}, at::kFloat);
+        if (in.wk) dwk = call.empty({in.dq.d}, at::kFloat);
+        Workspace ws;
+        if (in.wq || in.wk || gws)
+            ws = workspace(call, gws, g_lib.qk_norm_rope_bwd_workspace_bytes(in.dq.d), in.q.device());
+        check(g_lib.qk_norm_rope_bwd(ptr(gq.t), ptr(gk.t), ptr(in.q), ptr(in.k), ptr(in.wq), ptr(in.wk), r.cos, r.sin, pos.p,
+                                     ptr(dq.t), ptr(dk.t), in.wq ? dwq.data_ptr<float>() : nullptr,
+                                     in.wk ? dwk.data_ptr<float>() : nullptr, gq.dense.st, gk.dense.st, in.dq.st, in.dk.st,
+                                     dq.dense.st, dk.dense.st, in.dq.b, in.dq.h, in.dk.h, in.dq.s, in.dq.d, r.rot, r.length,
+                                     pos.stride, interleaved, eps, in.dtype, ws.p, ws.bytes, call.stream()));
+    }
+    return Py_BuildValue("(NNNN)", object(a[11], dq.t), object(a[12], dk.t), object(Py_None, dwq), object(Py_None, dwk));
 }
 
 // A paged cache.
@@ -386,12 +407,16 @@ PyObject *kvcache_append_paged(PyObject *const *a)
                  news->device() != c.k.device() || !news->is_contiguous()))
         fail(ATTN_ERR_DTYPE, "new_seqlens must be an int32 tensor of b elements on the pools' device");
     const Rotation r = rotation(a[6], a[7], c.k.device());
+    const int interleaved = truth(a[8]);
     const Call call(c.k, a[12]);
-    check(g_lib.kvcache_append_paged(ptr(k), ptr(v), ptr(c.k), ptr(c.v), static_cast<float *>(ptr(c.ks)),
-                                    static_cast<float *>(ptr(c.vs)), static_cast<const int32_t *>(ptr(c.lens)),
-                                    static_cast<const int32_t *>(ptr(news)), static_cast<const int32_t *>(ptr(c.table)),
-                                    r.cos, r.sin, kd.st, vd.st, kd.b, kd.h, kd.s, c.num_pages, c.page_size,
-                                    c.pages_per_seq, c.block, kd.d, r.rot, r.length, truth(a[8]), dtype, call.stream()));
+    {
+        const WithoutLock unlocked;
+        check(g_lib.kvcache_append_paged(ptr(k), ptr(v), ptr(c.k), ptr(c.v), static_cast<float *>(ptr(c.ks)),
+                                         static_cast<float *>(ptr(c.vs)), static_cast<const int32_t *>(ptr(c.lens)),
+                                         static_cast<const int32_t *>(ptr(news)), static_cast<const int32_t *>(ptr(c.table)),
+                                         r.cos, r.sin, kd.st, vd.st, kd.b, kd.h, kd.s, c.num_pages, c.page_size,
+                                         c.pages_per_seq, c.block, kd.d, r.rot, r.length, interleaved, dtype, call.stream()));
+    }
     Py_RETURN_NONE;
 }
 
@@ -407,28 +432,31 @@ PyObject *fwd_kvcache_paged_fp8(PyObject *const *a)
     const Cache c = cache(a[1], a[2], a[3], a[4], a[5], a[6], b, hkv, d);
     if (!q.is_contiguous() || q.device() != c.k.device()) fail(ATTN_ERR_SHAPE, "q must be contiguous, on the pools' device");
     const double scale = a[8] == Py_None ? 1.0 / std::sqrt(static_cast<double>(d)) : number(a[8], "scale");
+    const int causal = truth(a[7]);
+    const at::Tensor *go = maybe(a[9], "o"), *glse = maybe(a[10], "lse"), *gws = maybe(a[11], "workspace");
     const Call call(q, a[12]);
-    const Output o = output(call, "o", a[9], q);
-    if (!o.t.is_contiguous()) fail(ATTN_ERR_SHAPE, "o must be contiguous");
+    Output o;
     at::Tensor lse;
-    if (a[10] == Py_None) {
-        lse = call.empty({b, h, sq}, at::kFloat);
-    } else {
-        lse = tensor(a[10], "lse");
-        if (lse.sizes() != at::IntArrayRef({b, h, sq}) || lse.scalar_type() != at::kFloat || !lse.is_contiguous() ||
-            lse.device() != q.device())
-            fail(ATTN_ERR_SHAPE, "lse must be contiguous fp32 [b, h, sq] on q's device");
+    {
+        const WithoutLock unlocked;
+        o = output(call, "o", go, q);
+        if (!o.t.is_contiguous()) fail(ATTN_ERR_SHAPE, "o must be contiguous");
+        if (!glse) {
+            lse = call.empty({b, h, sq}, at::kFloat);
+        } else {
+            lse = *glse;
+            if (lse.sizes() != at::IntArrayRef({b, h, sq}) || lse.scalar_type() != at::kFloat || !lse.is_contiguous() ||
+                lse.device() != q.device())
+                fail(ATTN_ERR_SHAPE, "lse must be contiguous fp32 [b, h, sq] on q's device");
+        }
+        const Workspace ws = workspace(call, gws, g_lib.fwd_kvcache_paged_fp8_workspace_bytes(b, h, hkv, sq, d), q.device());
+        check(g_lib.fwd_kvcache_paged_fp8(ptr(q), ptr(c.k), ptr(c.v), static_cast<const float *>(ptr(c.ks)),
+                                          static_cast<const float *>(ptr(c.vs)), static_cast<const int32_t *>(ptr(c.lens)),
+                                          static_cast<const int32_t *>(ptr(c.table)), ptr(o.t), lse.data_ptr<float>(), b, h,
+                                          hkv, sq, c.num_pages, c.page_size, c.pages_per_seq, c.block, d, causal,
+                                          static_cast<float>(scale), dtype, ws.p, ws.bytes, call.stream()));
     }
-    const Workspace ws = workspace(call, a[11], g_lib.fwd_kvcache_paged_fp8_workspace_bytes(b, h, hkv, sq, d), q.device());
-    check(g_lib.fwd_kvcache_paged_fp8(ptr(q), ptr(c.k), ptr(c.v), static_cast<const float *>(ptr(c.ks)),
-                                     static_cast<const float *>(ptr(c.vs)), static_cast<const int32_t *>(ptr(c.lens)),
-                                     static_cast<const int32_t *>(ptr(c.table)), ptr(o.t), lse.data_ptr<float>(), b, h, hkv,
-                                     sq, c.num_pages, c.page_size, c.pages_per_seq, c.block, d, truth(a[7]),
-                                     static_cast<float>(scale), dtype, ws.p, ws.bytes, call.stream()));
-    PyObject *l = a[10];
-    if (l == Py_None) l = THPVariable_Wrap(lse);
-    else Py_INCREF(l);
-    return Py_BuildValue("(NN)", o.object(), l);
+    return Py_BuildValue("(NN)", object(a[9], o.t), object(a[10], lse));
 }
 
 // Runs a function on its positional arguments; what it throws becomes a

@@ -1,9 +1,17 @@
 """The Python entry of the operators around the attention: where its memory
 comes from, what it holds while it works, what it raises."""
+import ctypes
+import os
+import shutil
+import subprocess
+import threading
+import time
+
 import pytest
 import torch
 
 import attention_forward_14_gb300 as af
+from attention_forward_14_gb300 import binding
 import ops_ref as R
 
 gpu = pytest.mark.gpu
@@ -113,3 +121,61 @@ def test_an_output_on_a_given_stream_outlives_its_use_on_the_current_one():
         del o, _
     torch.cuda.synchronize()
     assert all(torch.equal(c, want) for c in copies)
+
+
+class _StandIn:
+    """A library in place of the loaded one, whose functions sleep and succeed."""
+    SOURCE = r"""
+#include <stdint.h>
+#include <unistd.h>
+const char *last_error(void) { return ""; }
+int slow(void) { usleep(300000); return 0; }
+int64_t bytes(void) { return 1 << 20; }
+"""
+
+    def __init__(self, folder):
+        src, out = os.path.join(folder, "slow.c"), os.path.join(folder, "slow.so")
+        with open(src, "w") as f:
+            f.write(self.SOURCE)
+        subprocess.run(["gcc", "-shared", "-fPIC", "-o", out, src], check=True)
+        lib = ctypes.CDLL(out)
+        names = {"attn_last_error": "last_error", "attn_qk_norm_rope_bwd_workspace_bytes": "bytes",
+                 "attn_fwd_kvcache_paged_fp8_workspace_bytes": "bytes"}
+        for n in binding._MARSHALLED:
+            setattr(self, n, getattr(lib, names.get(n, "slow")))
+
+
+@gpu
+@pytest.mark.skipif(shutil.which("gcc") is None, reason="builds a small library")
+@pytest.mark.parametrize("name", [*CALLS, "append"])
+def test_other_threads_run_while_a_call_works(name, tmp_path):
+    """Nothing is launched: the library is one whose functions take 0.3 s."""
+    binding.load()
+    if name == "append":
+        q, kp, vp, ks, vs, lens, table = cache_inputs()
+        call = lambda: af.attn_kvcache_append_paged(q[:, :2], q[:, :2], kp, vp, lens, table, k_scale=ks, v_scale=vs)  # noqa: E731
+    else:
+        call = lambda: CALLS[name](None)  # noqa: E731
+    saved, beats, stop = binding._lib, [], threading.Event()
+
+    def beat():
+        while not stop.wait(0.005):
+            beats.append(time.monotonic())
+
+    other = threading.Thread(target=beat)
+    binding._lib = _StandIn(str(tmp_path))
+    try:
+        call()
+        other.start()
+        begun = time.monotonic()
+        call()
+        ended = time.monotonic()
+    finally:
+        stop.set()
+        binding._lib = saved
+        binding._marshal()
+        if other.ident:
+            other.join()
+    assert ended - begun >= 0.3
+    during = sum(begun < t < ended for t in beats)
+    assert during >= 10, during
