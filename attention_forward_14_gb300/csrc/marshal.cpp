@@ -19,6 +19,7 @@
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "attn_fwd.h"
@@ -474,10 +475,8 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
         PyObject *v = Py_BuildValue("(is)", e.code, e.msg.c_str());
         if (v) PyErr_SetObject(g_error ? g_error : PyExc_RuntimeError, v);
         Py_XDECREF(v);
-    } catch (const std::exception &e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
-    } catch (...) {
-        PyErr_SetString(PyExc_RuntimeError, "unknown error");
+    } catch (...) {  // as torch's own functions raise it (out of memory, a wrong index, ..)
+        torch::translate_exception_to_python(std::current_exception());
     }
     return nullptr;
 }

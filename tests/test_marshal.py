@@ -179,3 +179,29 @@ def test_other_threads_run_while_a_call_works(name, tmp_path):
     assert ended - begun >= 0.3
     during = sum(begun < t < ended for t in beats)
     assert during >= 10, during
+
+
+@gpu
+@pytest.mark.parametrize("name", CALLS)
+def test_running_out_of_memory_raises_what_torch_raises(name):
+    """The limit is the allocator's own, for this process.  A call that fails
+    so leaves nothing behind, and the same call works afterwards."""
+    want = CALLS[name](None)
+    torch.cuda.synchronize()
+    norm, cache = norm_inputs(4, 16, 16, 2048, 128), cache_inputs(4, 128, 1, 512, 128)
+    call = {"norm": lambda: af.attn_qk_norm_rope(*norm),
+            "norm backward": lambda: af.attn_qk_norm_rope_bwd(*norm[:2], *norm),
+            "attention": lambda: af.attn_fwd_kvcache_paged_fp8(*cache),
+            "attention, many rows": lambda: af.attn_fwd_kvcache_paged_fp8(*cache)}[name]
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(0).total_memory
+    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (4 << 20)) / total)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            call()
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    call()
+    got = CALLS[name](None)
+    torch.cuda.synchronize()
+    assert all(a is b is None or torch.equal(a, b) for a, b in zip(got, want))
