@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int shares = min((end - u_key + kStepKeys - 1) / kStepKeys, kWarps >> head_shift);
                 const int k = u_key + kshare * kStepKeys + 16 * half;
                 const int pg = page_shift >= 0 ? k >> page_shift : k / p.page_size, off = k - pg * p.page_size;
-                const int page = k < end ? __ldg(table + pg) : -1;
+                const int page = k < end ? table[pg] : -1;
                 const bool in = page >= 0 && page < p.num_pages;
                 const uint32_t st = issued % STAGES, bar = full_bar(st);
                 if (!__all_sync(0xffffffffu, wait(empty_bar(st), ((issued / STAGES) & 1u) ^ 1u, SITE_KV8_EMPTY))) break;
@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t w[D / 8];
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
-                const uint4 v = r < p.rows ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+                const uint4 v = r < p.rows ? src[i] : make_uint4(0u, 0u, 0u, 0u);
                 w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
             }
             float down = 1.f;

@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int group = lane & 7, k = j * kTileKeys + 16 * group;
                     const bool there = lane < 16 && 16 * group < left;
                     const int pg = page_shift >= 0 ? k >> page_shift : k / p.page_size, off = k - pg * p.page_size;
-                    const int page = there ? __ldg(table + pg) : -1;
+                    const int page = there ? table[pg] : -1;
                     const bool in = page >= 0 && page < p.num_pages;
                     const int tok = in ? page * p.page_size + off : nowhere;
                     const bool copies = there && lane < 8 && (16 * group) % p.box == 0;
@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < LPR; ++i) {
                     const int rr = warp_row + i * RPI + lane / LPR;
-                    q[i] = rr < p.rows ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) + (row0 + rr) * D) + c)
+                    q[i] = rr < p.rows ? reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) + (row0 + rr) * D)[c]
                                        : make_uint4(0u, 0u, 0u, 0u);
                 }
                 float down = 1.f;  // of the row that is this lane's in the softmax
@@ -658,13 +658,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int first = seen.all / kTileKeys * kTileKeys;
                     const int k1 = min(valid ? lim : 0, j_end * kTileKeys);
                     for (int k = max(first, at.j * kTileKeys); k < k1; ++k) {
-                        const int page = __ldg(table + k / p.page_size);
+                        const int page = table[k / p.page_size];
                         if (page < 0 || page >= p.num_pages) continue;
                         const uint4 *v = reinterpret_cast<const uint4 *>(
                             p.v_pool + ((static_cast<int64_t>(page) * p.page_size + k % p.page_size) * p.h_kv + at.kvh) * D);
 #pragma unroll
                         for (int c = 0; c < D / 32; ++c) {
-                            const uint4 a = __ldg(v + 2 * c), b = __ldg(v + 2 * c + 1);
+                            const uint4 a = v[2 * c], b = v[2 * c + 1];
                             const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {

@@ -79,8 +79,8 @@ __device__ __forceinline__ void load_weight(const void *w, const RowLane &rl, fl
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = 1.f;
     if (w) {
-        unpack4<T>(__ldg(reinterpret_cast<const uint2 *>(static_cast<const T *>(w) + rl.lo)), v);
-        unpack4<T>(__ldg(reinterpret_cast<const uint2 *>(static_cast<const T *>(w) + rl.hi)), v + 4);
+        unpack4<T>(*reinterpret_cast<const uint2 *>(static_cast<const T *>(w) + rl.lo), v);
+        unpack4<T>(*reinterpret_cast<const uint2 *>(static_cast<const T *>(w) + rl.hi), v + 4);
     }
 }
 
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) norm_rope_kernel(const __gr
         }
     }
     T *out = static_cast<T *>(sd.out) + u.bi * sd.ob + u.si * sd.os + (u.h0 + sub) * sd.oh;
-    const int pos = p.pos ? __ldg(p.pos + u.bi * p.pos_b + u.si) : static_cast<int>(u.si);
+    const int pos = p.pos ? p.pos[u.bi * p.pos_b + u.si] : static_cast<int>(u.si);
     if (!known_position(p, pos)) {
         const uint2 zero[2] = {make_uint2(0u, 0u), make_uint2(0u, 0u)};
         for (int i = 0; i < ROWS; ++i, out += RPW * sd.oh)
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) norm_rope_bwd_kernel(
         auto position = [&](uint32_t unit) {
             if (unit >= units) return 0;
             const At at = place(unit);
-            return p.pos ? __ldg(p.pos + at.bi * p.pos_b + at.si) : static_cast<int>(at.si);
+            return p.pos ? p.pos[at.bi * p.pos_b + at.si] : static_cast<int>(at.si);
         };
         auto fetch_row = [&](auto &to, const T *row, bool there) {
             if constexpr (ADJACENT) {

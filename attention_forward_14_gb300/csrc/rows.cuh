@@ -131,8 +131,8 @@ __device__ __forceinline__ void load_angles(const float *cos_t, const float *sin
                                             float (&c)[4], float (&s)[4])
 {
     if (!r.on) return;
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(cos_t + at + r.col));
-    const float4 b = __ldg(reinterpret_cast<const float4 *>(sin_t + at + r.col));
+    const float4 a = *reinterpret_cast<const float4 *>(cos_t + at + r.col);
+    const float4 b = *reinterpret_cast<const float4 *>(sin_t + at + r.col);
     c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w;
     s[0] = b.x, s[1] = b.y, s[2] = b.z, s[3] = b.w;
 }

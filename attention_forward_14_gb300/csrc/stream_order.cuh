@@ -15,6 +15,10 @@
 // That is needed in every block, also in one that has nothing to do, or a
 // kernel could complete before the one it follows, and the next one, which
 // waits for it alone, begin too early.
+//
+// Such a kernel is there before what it reads is written, so it reads with
+// plain loads: ld.global.nc (__ldg) is for memory that stays as it is for as
+// long as the kernel lives, and is not held behind the wait.
 #pragma once
 
 #include <cuda_runtime.h>
