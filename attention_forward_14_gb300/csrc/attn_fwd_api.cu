@@ -1426,6 +1426,17 @@ int attn_kvcache_append_paged(const void *k_new, const void *v_new, void *k_pool
             if (n.lo < c + pool_bytes && c < n.hi) return fail(ATTN_ERR_SHAPE, "k_new / v_new overlap k_pool / v_pool");
     if (pools[0] < pools[1] + pool_bytes && pools[1] < pools[0] + pool_bytes)
         return fail(ATTN_ERR_SHAPE, "k_pool and v_pool overlap");
+    if (e4m3) {  // keys and values are written at the same time, each with its scales
+        const uintptr_t bytes = static_cast<uintptr_t>(num_pages * h_kv * (page_size / scale_block)) * 4;
+        const uintptr_t sc[2] = {reinterpret_cast<uintptr_t>(k_scale), reinterpret_cast<uintptr_t>(v_scale)};
+        if (sc[0] < sc[1] + bytes && sc[1] < sc[0] + bytes) return fail(ATTN_ERR_SHAPE, "k_scale and v_scale overlap");
+        for (const uintptr_t at : sc) {
+            for (const uintptr_t c : pools)
+                if (at < c + pool_bytes && c < at + bytes) return fail(ATTN_ERR_SHAPE, "a scale array overlaps k_pool or v_pool");
+            for (const Extent &n : news)
+                if (at < n.hi && n.lo < at + bytes) return fail(ATTN_ERR_SHAPE, "k_new / v_new overlap k_scale / v_scale");
+        }
+    }
     DeviceInfo *di = nullptr;
     if ((rc = device_info(&di)) != ATTN_OK) return rc;
     p.x[0] = k_new, p.x[1] = v_new;

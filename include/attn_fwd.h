@@ -490,6 +490,7 @@ int64_t attn_qk_norm_rope_bwd_workspace_bytes(int64_t d);
  *   k_scale,
  *   v_scale      : fp32 [num_pages, h_kv, page_size / scale_block] of an
  *                  e4m3 pool, else NULL.
+ *                  Pools, scales and new tokens do not overlap one another.
  *   cache_seqlens: device int32 [b], tokens cached before this call (read,
  *                  not updated; clamped to the capacity pages_per_seq *
  *                  page_size).
