@@ -2,6 +2,7 @@
 // include/attn_fwd.h): argument validation, TMA tensor maps, persistent grid
 // sizing, dispatch to the <head_dim, dtype, causal> instances, device
 // watchdog status.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -731,13 +732,18 @@ Extent extent_of(const void *p, const int64_t *st, int64_t b, int64_t h, int64_t
     return {lo, lo + static_cast<uintptr_t>(last) * 2};
 }
 
-// Rows of an output must not coincide: no stride of an axis longer than one
-// may be shorter than a row.
+// Rows of an output must not coincide: the rows along the axes of smaller
+// strides fit within a stride.
 int validate_out_strides(const int64_t *st, int64_t b, int64_t h, int64_t s, int64_t d, const char *what)
 {
-    const int64_t n[3] = {b, h, s};
-    for (int i = 0; i < 3; ++i)
-        if (n[i] > 1 && st[i] < d) return fail(ATTN_ERR_SHAPE, "rows of %s overlap (stride %lld)", what, (long long)st[i]);
+    std::pair<int64_t, int64_t> axes[3] = {{st[0], b}, {st[1], h}, {st[2], s}};  // stride, length
+    std::sort(axes, axes + 3);
+    __int128 span = d;
+    for (const auto &a : axes) {
+        if (a.second <= 1) continue;
+        if (a.first < span) return fail(ATTN_ERR_SHAPE, "rows of %s overlap (stride %lld)", what, (long long)a.first);
+        span += static_cast<__int128>(a.first) * (a.second - 1);
+    }
     return ATTN_OK;
 }
 
@@ -802,6 +808,18 @@ int set_side(NormRopeSide *sd, const void *x, const void *w, const int64_t *xs, 
     sd->out = out;
     sd->xb = xs[0], sd->xh = xs[1], sd->xs = xs[2];
     sd->ob = os[0], sd->oh = os[1], sd->os = os[2];
+    return ATTN_OK;
+}
+
+// The queries' output must not be the keys' nor an input of theirs, nor the
+// other way round.
+int validate_apart(const NormRopeParams &p)
+{
+    const NormRopeSide &q = p.side[0], &k = p.side[1];
+    if (q.heads == 0 || k.heads == 0) return ATTN_OK;
+    if (q.out == k.out) return fail(ATTN_ERR_SHAPE, "the outputs for q and k are the same memory");
+    if (q.out == k.x || q.out == k.g || k.out == q.x || k.out == q.g)
+        return fail(ATTN_ERR_SHAPE, "an output of one side is an input of the other");
     return ATTN_OK;
 }
 
@@ -1281,6 +1299,7 @@ int attn_qk_norm_rope(const void *q, const void *k, const void *q_weight, const 
     if (rc != ATTN_OK || nothing) return rc;
     if ((rc = set_side(&p.side[0], q, q_weight, q_strides, q_out, q_out_strides, b, h, s, d, "q")) != ATTN_OK) return rc;
     if ((rc = set_side(&p.side[1], k, k_weight, k_strides, k_out, k_out_strides, b, h_kv, s, d, "k")) != ATTN_OK) return rc;
+    if ((rc = validate_apart(p)) != ATTN_OK) return rc;
     DeviceInfo *di = nullptr;
     if ((rc = device_info(&di)) != ATTN_OK) return rc;
     p.status = di->status;
@@ -1341,6 +1360,7 @@ int attn_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const void *q,
         sd.g = gs[i];
         sd.gb = gst[i][0], sd.gh = gst[i][1], sd.gs = gst[i][2];
     }
+    if ((rc = validate_apart(p)) != ATTN_OK) return rc;
     if (grads) {
         if (!workspace) return fail(ATTN_ERR_NULL, "workspace is NULL");
         if (!aligned(workspace, 16)) return fail(ATTN_ERR_ALIGN, "workspace must be 16-byte aligned");

@@ -416,7 +416,9 @@ int64_t attn_bwd_varlen_workspace_bytes(int64_t batch, int64_t h,
  *                of a fused projection's output, and the outputs have the
  *                layout that the attention reads.  A packed batch [total, h,
  *                d] is b = 1, s = total.  An output may be its input (the
- *                same strides); otherwise it must not overlap an input.
+ *                same strides); otherwise it must not overlap an input, nor
+ *                the other output.  Rows of an output must not coincide: each
+ *                stride spans the rows along the axes of smaller ones.
  *                h or h_kv may be 0.
  *   q_weight,
  *   k_weight   : [d] of dtype, 16-byte aligned, or NULL.
