@@ -544,7 +544,10 @@ int attn_kvcache_append_paged(const void *k_new, const void *v_new,
  *   v_pool       : e4m3 [num_pages, page_size, h_kv, d], 16-byte aligned.
  *   k_scale,
  *   v_scale      : fp32 [num_pages, h_kv, page_size / scale_block], finite,
- *                  not negative.
+ *                  not negative.  Where the V scales of one request differ by
+ *                  more than 2^96 (what is below 2^-64, zero among it,
+ *                  counting as 2^-64), weights of the keys with the smaller
+ *                  ones may be lost.
  *   cache_seqlens: device int32 [b], the tokens to attend to, the new ones
  *                  among them (clamped to 0..pages_per_seq * page_size).
  *   block_table  : device int32 [b, pages_per_seq]; a page index outside
@@ -561,12 +564,21 @@ int attn_kvcache_append_paged(const void *k_new, const void *v_new,
  * With `causal`, query i of element e sees keys j <= i + L - sq.  A row that
  * sees no key gets O = 0 and LSE = -inf.  Slots at or past L are not read
  * into the result.  The work is dealt out by the lengths on the device, so
- * batches of unequal lengths need no split count.  P is rounded to fp16
- * before the product with V; sums and statistics are fp32.  With 49 or more
- * query rows of a key head, keys and values enter the products divided by the
- * largest scale among 128 consecutive tokens, in fp16: exact for scales that
- * are powers of two within 2^15 of it; what is smaller loses bits below 2^-24
- * of that scale, other ratios round a value by 2^-11.
+ * batches of unequal lengths need no split count.  P, a key's weight times its
+ * values' scale with the row's largest between 2^-2 and 2^14, is rounded to
+ * fp16 before the product with V: by 2^-11 of it, or by 2^-25 where it is below
+ * 2^-14; sums and statistics are fp32.  With 49 or more query rows of a key
+ * head, keys and values enter the products divided by the largest scale among
+ * 128 consecutive tokens (of values 2^-64 at least),
+ * in fp16: exact for scales that are powers of two within 2^15 of it; what is
+ * smaller loses bits below 2^-24 of that scale, and other ratios round a value
+ * by 2^-10 (the ratio, and the product).
+ * A padded batch: the rows of q are the last sq of each request's L tokens, so
+ * its queries stand at the end of q's rows.  attn_kvcache_append_paged takes
+ * new tokens from the front of theirs (new_seqlens), so after an append of
+ * fewer than sq tokens either the request's queries are moved to the end of
+ * its rows (the rows before them see fewer keys, or none, and are left out),
+ * or the requests of unequal counts are asked one by one.
  * Returns ATTN_OK or a negative ATTN_ERR_* code.
  */
 int attn_fwd_kvcache_paged_fp8(const void *q, const void *k_pool,

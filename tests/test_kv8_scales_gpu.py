@@ -29,11 +29,11 @@ def draw(rows, lens=(384, 200), seed=9, block=16, spread=0.0):
     return K8.draw((2, 4, 2, SQ[rows], D, 64, 6, block, "bf16", True, lens), seed=seed, spread=spread, nan=False)
 
 
-def check(st, scale=1 / math.sqrt(D), floor=0.0):
-    o, lse = K8.call(st, True, scale)
+def check(st, scale=1 / math.sqrt(D), floor=0.0, rounded=0.0, causal=True):
+    o, lse = K8.call(st, causal, scale)
     o, lse = R.f64(o), R.f64(lse)
     ro, rl = R.attend_paged(R.f64(st["q"]), R.f64(st["kp"]), R.f64(st["vp"]), R.f64(st["ks"]), R.f64(st["vs"]),
-                            st["lens"].numpy(), st["table"].numpy(), True, scale)
+                            st["lens"].numpy(), st["table"].numpy(), causal, scale)
     assert not np.isnan(o).any() and not np.isnan(lse).any()
     dead = np.isinf(rl)
     assert np.array_equal(np.isinf(lse), dead) and (lse[dead] < 0).all() and (o[dead] == 0).all()
@@ -46,10 +46,11 @@ def check(st, scale=1 / math.sqrt(D), floor=0.0):
         pages = pages[(pages >= 0) & (pages < st["kp"].shape[0])]
         for h in range(q.shape[1]):
             ks, vs = (R.f64(st[x])[pages, h // group].max(initial=0.0) for x in ("ks", "vs"))
-            err[e, h] = 2.0 ** -22 * abs(scale) * np.linalg.norm(q[e, h], axis=-1) * ks * 448 * math.sqrt(D)
+            err[e, h] = (2.0 ** -22 + rounded) * abs(scale) * np.linalg.norm(q[e, h], axis=-1) * ks * 448 * math.sqrt(D)
             vmax[e, h] = vs * np.abs(R.f64(st["vp"])[pages, :, h // group]).max(initial=0.0)
-    assert (np.abs(lse - rl)[~dead] <= (err + 2.0 ** -20 * (1 + np.abs(rl)))[~dead]).all(), np.abs(lse - rl)[~dead].max()
-    bound = R.HALF_STEP[torch.bfloat16] * np.abs(ro) + ((2.0 ** -11 + n * 2.0 ** -23 + 2 * err) * vmax)[..., None] + floor
+    off = np.abs(lse[~dead] - rl[~dead])
+    assert (off <= err[~dead] + 2.0 ** -20 * (1 + np.abs(rl[~dead]))).all(), off.max()
+    bound = R.HALF_STEP[torch.bfloat16] * np.abs(ro) + ((2.0 ** -11 + rounded + n * 2.0 ** -23 + 2 * err) * vmax)[..., None] + floor
     assert (np.abs(o - ro) <= bound).all(), (np.abs(o - ro) - bound).max()
     # and as a whole the roundings of P are independent: O is as good as its own type
     for e in range(q.shape[0]):
@@ -176,3 +177,17 @@ def test_zeros_whose_scores_are_far_from_the_others(rows, gap):
         st["vs"][far] = 0.0
     st["kp"] = kp.to(torch.float8_e4m3fn)
     check(st, scale=1.0)
+
+
+@pytest.mark.parametrize("rows", SQ)
+@pytest.mark.parametrize("low", [-100, -64, -36, 0])
+def test_scales_of_values_as_far_apart_as_they_may_be(rows, low):
+    """2^96 between one page's values and the next one's, two pages' and the
+    next two's: the keys of the small ones keep their weights.  (2^-100 counts as 2^-64.)"""
+    for step in (1, 2):
+        st = draw(rows)
+        st["vp"] = (st["vp"].float() / 448).to(torch.float8_e4m3fn)
+        for e in range(2):
+            for i in range(6):
+                st["vs"][int(st["table"][e, i])] = 2.0 ** (max(low, -64) + 96 if i // step % 2 else low)
+        check(st, floor=LOST)
