@@ -659,8 +659,8 @@ def attn_kvcache_append_paged(k_new, v_new, k_pool, v_pool, cache_seqlens, block
     page_size / scale_block] (the cache of attn_fwd_kvcache_paged_fp8).  Token
     t of element e goes to position cache_seqlens[e] + t; ``new_seqlens`` int32
     [b] says how many of a padded batch's tokens are there.  ``cos`` / ``sin``
-    fp32 [at least the capacity, rot / 2]; None: no rotation.  cache_seqlens is
-    not updated."""
+    fp32 [at least the capacity, rot / 2]; None: no rotation (of keys that
+    attn_qk_norm_rope has rotated).  cache_seqlens is not updated."""
     _marshal().kvcache_append_paged(k_new, v_new, k_pool, v_pool, cache_seqlens, block_table, cos, sin, interleaved,
                                     k_scale, v_scale, new_seqlens, _handle(stream))
 
@@ -677,7 +677,9 @@ def attn_fwd_kvcache_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, cache_seqlen
     / v_scale fp32 [num_pages, h_kv, page_size / scale_block], block_table
     int32 [b, pages_per_seq].  Element e attends to its first cache_seqlens[e]
     tokens (the new ones among them: append first); h / h_kv query heads share
-    a key head.  ``workspace``: a CUDA uint8 tensor of
-    kvcache_paged_fp8_workspace_bytes bytes.  Returns (o, lse)."""
+    a key head.  The rows of q are the last sq of those tokens: in a padded
+    batch a request with fewer new ones has its queries at the end of its rows.
+    ``workspace``: a CUDA uint8 tensor of kvcache_paged_fp8_workspace_bytes
+    bytes.  Returns (o, lse)."""
     return _marshal().fwd_kvcache_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, cache_seqlens, block_table, causal,
                                             scale, o, lse, workspace, _handle(stream))
