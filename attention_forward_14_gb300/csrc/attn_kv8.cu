@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int h = 0; h < 2; ++h) {
             const float vs = h ? sc.w : sc.z;
             lv[h] = log2_scale(fmaxf(vs, kLeastScale));
-            const int up = min(max(static_cast<int>(__float_as_uint(vs) >> 23), 127), 253);  // 1 at least, biased
+            const int up = min(max(static_cast<int>(__float_as_uint(vs) << 1 >> 24), 127), 253);  // 1 at least, biased
             lift[h] = static_cast<float>(up - 127);
             weigh[h] = __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
             times[h] = vs * weigh[h];

@@ -191,3 +191,15 @@ def test_scales_of_values_as_far_apart_as_they_may_be(rows, low):
             for i in range(6):
                 st["vs"][int(st["table"][e, i])] = 2.0 ** (max(low, -64) + 96 if i // step % 2 else low)
         check(st, floor=LOST)
+
+
+@pytest.mark.parametrize("rows", SQ)
+def test_a_scale_of_minus_zero_is_a_scale_of_zero(rows):
+    st = draw(rows)
+    st["vs"][:, :, 1] = 0.0
+    st["ks"][:, :, 2] = 0.0
+    want = K8.call(st, True)
+    st["vs"][:, :, 1] = -0.0
+    st["ks"][:, :, 2] = -0.0
+    got = K8.call(st, True)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
