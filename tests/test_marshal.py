@@ -205,3 +205,72 @@ def test_running_out_of_memory_raises_what_torch_raises(name):
     got = CALLS[name](None)
     torch.cuda.synchronize()
     assert all(a is b is None or torch.equal(a, b) for a, b in zip(got, want))
+
+
+@gpu
+def test_a_given_stream_within_a_capture():
+    """Calls on a stream that the capturing one has forked, whose memory is
+    the graph's; eager calls of the same sizes run between the replays."""
+    q, k, w, _ = norm_inputs(4, 8, 8, 300, 128, 50)
+    cache = cache_inputs(4, 8, 2, 60, 128, 64, 8, 16, 51)
+    side = torch.cuda.Stream()
+
+    def step(stream):
+        a, b = af.attn_qk_norm_rope(q, k, w, w, stream=stream)
+        grads = af.attn_qk_norm_rope_bwd(a, b, q, k, w, w, stream=stream)
+        return (a, b, *grads, *af.attn_fwd_kvcache_paged_fp8(*cache, stream=stream))
+
+    want = [t.clone() for t in step(None)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = step(side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(4):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        step(None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@gpu
+def test_calls_from_several_threads():
+    """Each on a stream of its own, and all at once: the lock is let go."""
+    sets = [(norm_inputs(3, 8, 8, 200 + 50 * i, 128, 60 + i), cache_inputs(2, 8, 2, 1 + 25 * i, 128, 64, 8, 16, 70 + i))
+            for i in range(4)]
+
+    def step(i, stream):
+        norm, cache = sets[i]
+        a, b = af.attn_qk_norm_rope(*norm, stream=stream)
+        return (a, b, *af.attn_qk_norm_rope_bwd(a, b, *norm, stream=stream),
+                *af.attn_fwd_kvcache_paged_fp8(*cache, stream=stream))
+
+    want = [[t.clone() for t in step(i, None)] for i in range(4)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    wrong, gate = [], threading.Barrier(4)
+
+    def work(i):
+        try:
+            gate.wait(10)
+            for n in range(30):
+                if n % 2:
+                    got = step(i, streams[i])
+                else:
+                    with torch.cuda.stream(streams[i]):
+                        got = step(i, None)
+                streams[i].synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                    wrong.append((i, n))
+        except Exception as e:  # noqa: BLE001
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
