@@ -47,9 +47,9 @@
 // neither falls out of fp32 for the other's sake.
 //
 // What bounds it: the bytes of the cache.  8 caches of 1 to 16383 tokens (8
-// key heads, d = 128, 127 MB, 18.7 us at a copy's rate): 31.5 us, of which the
+// key heads, d = 128, 127 MB, 18.7 us at a copy's rate): 31.8 us, of which the
 // join 5; the same copies without any arithmetic take 24.6.  1001 tokens of
-// one cache: 9.3, two launches and their chains of loads.
+// one cache: 9.9 a call, two launches and their chains of loads.
 #include "attn_kv8_common.cuh"
 
 namespace attn {

@@ -45,7 +45,7 @@ constexpr int kKv8MaxCtas = 160;  // CTAs of a launch at most (sizes the workspa
 constexpr int kKv8Instances = 12;  // head dim {64, 128} x {fp16, bf16} x {8, 16, 256 rows}
 constexpr int kKv8Heads = 8;       // key heads of an item at most
 constexpr int kKv8WideRows = 256;  // query rows of an item of the kernel for many
-constexpr int kKv8Tile = 16;       // query rows of an item of the other, at most (and of a block of the join)
+constexpr int kKv8Tile = 16;       // query rows of an item of the other, at most
 
 struct Kv8LaunchArgs {
     CUtensorMap k, v;

@@ -31,7 +31,7 @@
 // values it is 2^-64 at least: the quotients stay within fp32.
 //
 // What bounds it, at the last 2048 of 16384 tokens (causal, 32 heads on
-// 8 key heads, d = 128): 433 us, 1.19 of 1.91 PFLOP/s, of which the join 14;
+// 8 key heads, d = 128): 437 us, 1.18 of 1.91 PFLOP/s, of which the join 14;
 // the tensor cores are at work half of the time.  Without the conversion (raw
 // tiles fed as they are, wrong results) 50 to 70 less: a tile of 128 keys
 // serves two Q tiles only, so its conversion (16 KB read, 32 KB written and

@@ -12,11 +12,11 @@
 // and stay in registers, and the unit's rows are loaded before the first of
 // them is used, which keeps enough bytes in flight.
 //
-// Measured, of 6.80 TB/s (a copy): forward 5.62 TB/s at b2 h32+32 s4096 d128
-// (48.1 us), 5.08 at 30011 packed tokens of 16 + 4 heads, d64 (31.0 us; the
+// Measured, of 6.80 TB/s (a copy): forward 5.71 TB/s at b2 h32+32 s4096 d128
+// (47.4 us), 5.21 at 30011 packed tokens of 16 + 4 heads, d64 (30.3 us; the
 // four key heads fill a quarter of their unit, and two thirds of the issue
-// slots are taken); backward 5.09 (79.5 us) at the first shape, 3.1 at 8191
-// packed tokens (20.9 us, of which 2.8 are the launch that joins the partial
+// slots are taken); backward 5.10 (79.4 us) at the first shape, 3.2 at 8191
+// packed tokens (20.3 us, of which 2.8 are the launch that joins the partial
 // sums and three to four units of latency a warp most of the rest).
 #include "qk_norm_rope.h"
 

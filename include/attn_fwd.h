@@ -515,8 +515,10 @@ int64_t attn_qk_norm_rope_bwd_workspace_bytes(int64_t d);
  * brings the largest finite |x| of the block's tokens to at most 448; a
  * stored value is x / scale rounded to e4m3 (an infinity is stored as +-448,
  * NaN as NaN).  A block that holds tokens of an earlier append keeps its
- * scale when that is large enough; otherwise its scale becomes the new
- * tokens' and the earlier tokens are stored again as their value under it.
+ * scale when the new tokens' own is not larger (and a stored value is x times
+ * 1 / scale in fp32, which matters for scales that are no powers of two);
+ * otherwise its scale becomes the new tokens' and the earlier tokens are
+ * stored again as their value under it.
  * A block that the new tokens begin takes no account of what it held.
  * Returns ATTN_OK or a negative ATTN_ERR_* code.
  */
