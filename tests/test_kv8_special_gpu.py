@@ -118,3 +118,14 @@ def test_graphs_with_new_lengths_and_two_streams(rows):
         again = af.attn_fwd_kvcache_paged_fp8(*args, causal=True)
         assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
         check({**st, "lens": torch.tensor(lens, dtype=torch.int32)})
+
+
+@pytest.mark.parametrize("case", [
+    (70, 2, 1, 1, 64, 16, 5, 16, "bf16", True, tuple((11 * i) % 81 for i in range(70))),      # more requests than a warp has lanes
+    (40, 2, 1, 26, 64, 16, 8, 16, "fp16", True, tuple((13 * i) % 129 for i in range(40))),    # the same, many rows
+    (34, 1, 1, 300, 128, 32, 12, 32, "bf16", True, tuple((37 * i) % 385 for i in range(34))),
+    (2, 4, 1, 2100, 64, 64, 40, 64, "bf16", True, (2500, 2099)),                              # more items of a head than lanes
+    (2, 4, 1, 2100, 64, 64, 5, 64, "fp16", False, (320, 0)),
+], ids=lambda c: "_".join(map(str, c[:10])))
+def test_more_requests_and_items_than_lanes(case):
+    K8.test_matches_the_definition(case)
