@@ -29,7 +29,8 @@ EXPORTS = ["attn_fwd", "attn_fwd_host", "attn_fwd_varlen", "attn_fwd_fp8", "attn
            "attn_fwd_watchdog_selftest", "attn_bwd_watchdog_selftest", "attn_version", "attn_bwd", "attn_bwd_workspace_bytes", "attn_bwd_varlen",
            "attn_bwd_varlen_workspace_bytes", "attn_fwd_kvcache", "attn_fwd_kvcache_paged", "attn_qk_norm_rope",
            "attn_qk_norm_rope_bwd", "attn_qk_norm_rope_bwd_workspace_bytes", "attn_kvcache_append_paged",
-           "attn_fwd_kvcache_paged_fp8", "attn_fwd_kvcache_paged_fp8_workspace_bytes"]
+           "attn_fwd_kvcache_paged_fp8", "attn_fwd_kvcache_paged_fp8_workspace_bytes", "attn_latent_append_paged",
+           "attn_fwd_latent_paged", "attn_fwd_latent_paged_workspace_bytes"]
 
 
 class AttnError(RuntimeError):
@@ -116,6 +117,12 @@ def _bind(lib):
     lib.attn_fwd_kvcache_paged_fp8.argtypes = [vp] * 9 + [i64] * 9 + [c_int, c_float, c_int, vp, i64, vp]
     lib.attn_fwd_kvcache_paged_fp8_workspace_bytes.restype = i64
     lib.attn_fwd_kvcache_paged_fp8_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
+    lib.attn_latent_append_paged.restype = c_int
+    lib.attn_latent_append_paged.argtypes = [vp] * 9 + [i64] * 6 + [c_int, c_float, c_int, vp]
+    lib.attn_fwd_latent_paged.restype = c_int
+    lib.attn_fwd_latent_paged.argtypes = [vp] * 9 + [i64] * 6 + [c_int, c_float, c_int, vp, i64, vp]
+    lib.attn_fwd_latent_paged_workspace_bytes.restype = i64
+    lib.attn_fwd_latent_paged_workspace_bytes.argtypes = [i64, i64, i64]
     return lib
 
 
@@ -590,7 +597,8 @@ def attn_bwd_varlen(q, k, v, o, dout, lse, cu_seqlens_q, cu_seqlens_k, max_seqle
 
 # What csrc/marshal.cpp calls, in the order in which it takes their addresses.
 _MARSHALLED = ("attn_last_error", "attn_qk_norm_rope", "attn_qk_norm_rope_bwd", "attn_qk_norm_rope_bwd_workspace_bytes",
-               "attn_kvcache_append_paged", "attn_fwd_kvcache_paged_fp8", "attn_fwd_kvcache_paged_fp8_workspace_bytes")
+               "attn_kvcache_append_paged", "attn_fwd_kvcache_paged_fp8", "attn_fwd_kvcache_paged_fp8_workspace_bytes",
+               "attn_latent_append_paged", "attn_fwd_latent_paged", "attn_fwd_latent_paged_workspace_bytes")
 _fast, _fast_lib = None, None
 
 
@@ -683,3 +691,44 @@ def attn_fwd_kvcache_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, cache_seqlen
     bytes.  Returns (o, lse)."""
     return _marshal().fwd_kvcache_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, cache_seqlens, block_table, causal,
                                             scale, o, lse, workspace, _handle(stream))
+
+
+def attn_latent_append_paged(kv_new, pool, cache_seqlens, block_table, norm_weight=None, cos=None, sin=None,
+                             eps: float = 1e-6, interleaved: bool = False, new_seqlens=None, stream=None):
+    """Write new tokens of latent attention into its paged cache, in place: the
+    first 512 values of a token (the latent, which all heads' keys and values
+    come from) normed, the last 64 (the heads' shared key part) rotated.
+
+    kv_new: [b, s_new, 576] fp16 or bf16, any strides (multiples of 8 elements)
+    with contiguous tokens; pool: [num_pages, page_size, 576] of its dtype.
+    ``norm_weight`` [512] (None: no norm); ``cos`` / ``sin`` fp32 [at least the
+    capacity, 32] (None: no rotation); ``interleaved``: adjacent pairs turn
+    instead of pairs (i, i + 32).  Token t of element e goes to position
+    cache_seqlens[e] + t; ``new_seqlens`` int32 [b] says how many of a padded
+    batch's tokens are there.  cache_seqlens is not updated."""
+    _marshal().latent_append_paged(kv_new, pool, cache_seqlens, block_table, norm_weight, cos, sin, eps, interleaved,
+                                   new_seqlens, _handle(stream))
+
+
+def latent_paged_workspace_bytes(b, h, sq) -> int:
+    lib = load()
+    return _check(int(lib.attn_fwd_latent_paged_workspace_bytes(b, h, sq)), lib)
+
+
+def attn_fwd_latent_paged(q, pool, cache_seqlens, block_table, scale: float, causal: bool = False, tree=None, o=None,
+                          lse=None, workspace=None, stream=None):
+    """Latent attention over its paged cache, absorbed form: queries that were
+    multiplied by the keys' projection against the tokens themselves, keys of
+    576 values and values of their first 512, shared by all heads.
+
+    q: [b, h, sq, 576] fp16 or bf16, any strides (multiples of 8 elements) with
+    contiguous rows; pool: [num_pages, page_size, 576], block_table int32 [b,
+    pages_per_seq].  Element e attends to its first cache_seqlens[e] tokens (the
+    new ones among them: append first); ``causal``: the rows of q are the last
+    sq of those.  ``tree`` int32 [b, sq, ceil(sq / 32)] instead: the last sq
+    tokens are drafted, and a query sees those whose bits are set (bit t % 32
+    of word t / 32), and all before them.  ``scale`` has no default: it goes by
+    the expanded keys' size.  ``workspace``: a CUDA uint8 tensor of
+    latent_paged_workspace_bytes bytes.  Returns (o [b, h, sq, 512], lse)."""
+    return _marshal().fwd_latent_paged(q, pool, cache_seqlens, block_table, scale, causal, tree, o, lse, workspace,
+                                       _handle(stream))

@@ -20,6 +20,7 @@
 #include "attn_fwd.h"
 #include "attn_kv8.h"
 #include "kv_append.h"
+#include "latent.h"
 #include "launch.h"
 #include "qk_norm_rope.h"
 #include "sched_ticket.h"
@@ -76,6 +77,7 @@ struct DeviceInfo {
     std::atomic<int> fwd_attr[kFwdInstances] = {};  // shared-memory opt-in set, per kernel instance
     std::atomic<int> bwd_attr[bwd::kBwdInstances] = {};
     std::atomic<int> kv8_attr[kKv8Instances] = {};
+    std::atomic<int> latent_attr[kLatentPagedInstances] = {};
 };
 DeviceInfo g_dev[kMaxDevices];
 
@@ -1601,6 +1603,177 @@ int attn_fwd_kvcache_paged_fp8(const void *q, const void *k_pool, const void *v_
     const cudaError_t e = wide ? launch_kv8_wide(a, static_cast<int>(d), dtype == ATTN_BF16)
                                : launch_kv8(a, static_cast<int>(d), dtype == ATTN_BF16);
     return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "kernel launch (e4m3 paged cache)");
+}
+
+// Whether two ranges of bytes share one.
+static bool overlap(const Extent &a, const Extent &b) { return a.lo < b.hi && b.lo < a.hi; }
+
+static Extent bytes_at(const void *p, int64_t n)
+{
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    return {lo, lo + static_cast<uintptr_t>(n)};
+}
+
+static int validate_dtype(int dtype)
+{
+    if (dtype != ATTN_FP16 && dtype != ATTN_BF16) return fail(ATTN_ERR_DTYPE, "dtype %d is not fp16 (0) or bf16 (1)", dtype);
+    return ATTN_OK;
+}
+
+int attn_latent_append_paged(const void *kv_new, void *pool, const void *norm_weight, const int32_t *cache_seqlens,
+                             const int32_t *new_seqlens, const int32_t *block_table, const float *cos, const float *sin,
+                             const int64_t *kv_strides, int64_t b, int64_t s_new, int64_t num_pages, int64_t page_size,
+                             int64_t pages_per_seq, int64_t table_len, int interleaved, float eps, int dtype, void *stream)
+{
+    g_err.clear();
+    int rc = validate_pages(num_pages, page_size, pages_per_seq, 0);
+    if (rc != ATTN_OK) return rc;
+    if (b < 0 || s_new < 0) return fail(ATTN_ERR_SHAPE, "negative size");
+    if (s_new > kMaxSeq || (b > 0 && s_new > INT32_MAX / b)) return fail(ATTN_ERR_SHAPE, "b * s_new above 2^31-1");
+    if ((rc = validate_dtype(dtype)) != ATTN_OK) return rc;
+    if (!std::isfinite(eps) || eps < 0.f) return fail(ATTN_ERR_SCALE, "eps must be finite and not negative");
+    if ((rc = validate_rotation(cos, sin, kLatentRope, table_len, kLatentRope)) != ATTN_OK) return rc;
+    const int64_t cap = pages_per_seq * page_size;
+    if (cos && table_len < cap)
+        return fail(ATTN_ERR_SHAPE, "the tables have %lld positions, fewer than the %lld of a request's pages",
+                    (long long)table_len, (long long)cap);
+    if (b * s_new == 0) return ATTN_OK;
+    if (!kv_new || !pool || !cache_seqlens || !block_table)
+        return fail(ATTN_ERR_NULL, "kv_new, pool, cache_seqlens or block_table is NULL");
+    if ((rc = validate_strides(kv_strides, "kv_new")) != ATTN_OK) return rc;
+    if (!aligned(kv_new, 16) || !aligned(pool, 16) || !aligned(norm_weight, 16))
+        return fail(ATTN_ERR_ALIGN, "kv_new, pool and norm_weight must be 16-byte aligned");
+    if (!aligned(cache_seqlens, 4) || !aligned(new_seqlens, 4) || !aligned(block_table, 4))
+        return fail(ATTN_ERR_ALIGN, "lengths and block_table must be 4-byte aligned");
+    // what is read must not lie in what is written
+    const Extent to = bytes_at(pool, num_pages * page_size * kLatentToken * 2);
+    if (overlap(extent_of(kv_new, kv_strides, b, 1, s_new, kLatentToken), to)) return fail(ATTN_ERR_SHAPE, "kv_new overlaps the pool");
+    if (norm_weight && overlap(bytes_at(norm_weight, kLatent * 2), to)) return fail(ATTN_ERR_SHAPE, "norm_weight overlaps the pool");
+    DeviceInfo *di = nullptr;
+    if ((rc = device_info(&di)) != ATTN_OK) return rc;
+    LatentAppendParams p;
+    p.x = kv_new;
+    p.xb = kv_strides[0], p.xs = kv_strides[2];
+    p.pool = pool;
+    p.weight = norm_weight;
+    p.cos = cos, p.sin = sin;
+    p.seqlens = cache_seqlens;
+    p.new_seqlens = new_seqlens;
+    p.block_table = block_table;
+    p.status = di->status;
+    p.b = b, p.s = s_new, p.num_pages = num_pages, p.pages_per_seq = pages_per_seq;
+    p.page_size = static_cast<int>(page_size);
+    p.interleaved = interleaved != 0;
+    p.eps = eps;
+    const cudaError_t e = launch_latent_append(p, dtype == ATTN_BF16, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "launch (latent cache append)");
+}
+
+// Query rows of an item: the smallest of 16, 32 and 64 that holds a request's.
+static int latent_tile_rows(int64_t rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64); }
+
+// Parts of the items that two or more teams share, at most two a CTA, and
+// what tells which they are.
+static int64_t latent_workspace(int64_t rows)
+{
+    return 2 * kLatentMaxCtas * latent_tile_rows(rows) * (int64_t(kLatent) * 4 + 16) +
+           kLatentMaxCtas * static_cast<int64_t>(sizeof(LatentCut));
+}
+
+static int validate_latent_sizes(int64_t b, int64_t h, int64_t sq)
+{
+    if (b < 0 || h < 0 || sq < 0) return fail(ATTN_ERR_SHAPE, "negative size: b=%lld h=%lld sq=%lld", (long long)b, (long long)h, (long long)sq);
+    if (sq > kMaxSeq || h > (1 << 20)) return fail(ATTN_ERR_SHAPE, "sq above 2^30 or more than 2^20 heads");
+    if (h > 0 && sq > (INT32_MAX - 1024) / h) return fail(ATTN_ERR_SHAPE, "more than 2^31 - 1024 query rows of one request");
+    if (b > 0 && h * sq / 16 + 1 > INT32_MAX / b) return fail(ATTN_ERR_SHAPE, "too many query rows");
+    return ATTN_OK;
+}
+
+int64_t attn_fwd_latent_paged_workspace_bytes(int64_t b, int64_t h, int64_t sq)
+{
+    g_err.clear();
+    const int rc = validate_latent_sizes(b, h, sq);
+    return rc != ATTN_OK ? rc : latent_workspace(h * sq);
+}
+
+int attn_fwd_latent_paged(const void *q, const void *pool, const int32_t *cache_seqlens, const int32_t *block_table,
+                          const int32_t *tree, void *o, float *lse, const int64_t *q_strides, const int64_t *o_strides,
+                          int64_t b, int64_t h, int64_t sq, int64_t num_pages, int64_t page_size, int64_t pages_per_seq,
+                          int causal, float scale, int dtype, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    g_err.clear();
+    int rc = validate_pages(num_pages, page_size, pages_per_seq, 0);
+    if (rc == ATTN_OK) rc = validate_latent_sizes(b, h, sq);
+    if (rc == ATTN_OK) rc = validate_dtype(dtype);
+    if (rc != ATTN_OK) return rc;
+    if (!std::isfinite(scale)) return fail(ATTN_ERR_SCALE, "scale is not finite");
+    if (tree && causal) return fail(ATTN_ERR_SHAPE, "a tree says which of the new tokens a query sees: causal must be 0");
+    if (b * h * sq == 0) return ATTN_OK;
+    if (!q || !pool || !o || !cache_seqlens || !block_table)
+        return fail(ATTN_ERR_NULL, "q, pool, o, cache_seqlens or block_table is NULL");
+    if ((rc = validate_strides(q_strides, "q")) != ATTN_OK) return rc;
+    if ((rc = validate_strides(o_strides, "o")) != ATTN_OK) return rc;
+    if ((rc = validate_out_strides(o_strides, b, h, sq, kLatent, "o")) != ATTN_OK) return rc;
+    if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(o, 16)) return fail(ATTN_ERR_ALIGN, "q, pool and o must be 16-byte aligned");
+    if (!aligned(lse, 4) || !aligned(cache_seqlens, 4) || !aligned(block_table, 4) || !aligned(tree, 4))
+        return fail(ATTN_ERR_ALIGN, "lse, cache_seqlens, block_table and tree must be 4-byte aligned");
+    const int64_t rows = h * sq, need = latent_workspace(rows);
+    if (!workspace) return fail(ATTN_ERR_NULL, "workspace is NULL (%lld bytes needed)", (long long)need);
+    if (!aligned(workspace, 16)) return fail(ATTN_ERR_ALIGN, "workspace must be 16-byte aligned");
+    if (workspace_bytes < need)
+        return fail(ATTN_ERR_SHAPE, "workspace too small: %lld bytes, need %lld", (long long)workspace_bytes, (long long)need);
+    // rows of o are written while others' q and the pool are still read
+    const Extent out = extent_of(o, o_strides, b, h, sq, kLatent);
+    if (overlap(out, extent_of(q, q_strides, b, h, sq, kLatentToken)) || overlap(out, bytes_at(pool, num_pages * page_size * kLatentToken * 2)))
+        return fail(ATTN_ERR_SHAPE, "o overlaps q or the pool");
+    DeviceInfo *di = nullptr;
+    if ((rc = device_info(&di)) != ATTN_OK) return rc;
+    LatentPagedArgs a;
+    LatentPagedParams &p = a.p;
+    p.box = 128;
+    while (page_size % p.box != 0) p.box /= 2;  // a box lies in one page
+    const cuuint64_t dims[3] = {kLatentToken, static_cast<cuuint64_t>(num_pages * page_size), 1};
+    const cuuint64_t strides[2] = {kLatentToken * 2, kLatentToken * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(p.box), 1};
+    if ((rc = encode_map(&a.pool, dtype == ATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, pool, dims,
+                         strides, box, CU_TENSOR_MAP_SWIZZLE_128B, "latent pool")) != ATTN_OK)
+        return rc;
+    const int tile = latent_tile_rows(rows);
+    p.q = q, p.o = o, p.lse = lse;
+    p.qb = q_strides[0], p.qh = q_strides[1], p.qs = q_strides[2];
+    p.ob = o_strides[0], p.oh = o_strides[1], p.os = o_strides[2];
+    p.seqlens = cache_seqlens;
+    p.block_table = block_table;
+    p.tree = tree;
+    p.status = di->status;
+    p.o_part = static_cast<float *>(workspace);
+    p.ml_part = reinterpret_cast<float4 *>(p.o_part + 2 * kLatentMaxCtas * int64_t(tile) * kLatent);
+    p.cut = reinterpret_cast<LatentCut *>(p.ml_part + 2 * kLatentMaxCtas * tile);
+    p.sl2e = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+    p.b = static_cast<int32_t>(b);
+    p.h = static_cast<int32_t>(h);
+    p.sq = static_cast<int32_t>(sq);
+    p.rows = static_cast<int32_t>(rows);
+    p.tiles = static_cast<int32_t>((rows + tile - 1) / tile);
+    p.team = p.tiles <= kLatentMaxTeam ? p.tiles : 2;
+    p.groups = (p.tiles + p.team - 1) / p.team;
+    p.cap = static_cast<int32_t>(pages_per_seq * page_size);
+    p.page_size = static_cast<int32_t>(page_size);
+    p.pages_per_seq = static_cast<int32_t>(pages_per_seq);
+    p.num_pages = static_cast<int32_t>(num_pages);
+    p.mask = tree ? LATENT_MASK_TREE : (causal ? LATENT_MASK_CAUSAL : LATENT_MASK_NONE);
+    p.tree_words = static_cast<int32_t>((sq + 31) / 32);
+    p.timeout_ns = kDefaultTimeoutNs;
+    // no more teams than units in full caches
+    const double units = static_cast<double>(b) * p.groups * static_cast<double>((p.cap + 127) / 128);
+    int teams = (di->sm_count < kLatentMaxCtas ? di->sm_count : kLatentMaxCtas) / p.team;
+    if (units < teams) teams = static_cast<int>(units);
+    a.tile_rows = tile;
+    a.grid = teams * p.team;
+    a.stream = static_cast<cudaStream_t>(stream);
+    a.attr_ready = di->latent_attr;
+    const cudaError_t e = launch_latent_paged(a, dtype == ATTN_BF16);
+    return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "kernel launch (latent paged cache)");
 }
 
 const char *attn_last_error(void) { return g_err.c_str(); }

@@ -89,9 +89,9 @@ constexpr int kMinUnits = 2;
 struct Shares {
     int64_t per, rem;
     int ctas;
-    __device__ __forceinline__ Shares(int64_t total, int grid)
+    __device__ __forceinline__ Shares(int64_t total, int grid, int min_units = kMinUnits)
     {
-        ctas = static_cast<int>(min(static_cast<int64_t>(grid), max(total / kMinUnits, int64_t(1))));
+        ctas = static_cast<int>(min(static_cast<int64_t>(grid), max(total / min_units, int64_t(1))));
         per = quotient(total, ctas);
         rem = total - per * ctas;
     }

@@ -1,0 +1,83 @@
+// Latent attention: a token's keys and values are one vector that all heads
+// share, [latent (512) | rotated key part (64)].  Parameters and launches of
+// the append to its paged cache, of the attention over that cache, and of the
+// expanded form (a head's keys are 128 values of its own and the shared 64,
+// its values 128) with its gradients.
+#pragma once
+
+#include <atomic>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+namespace attn {
+
+constexpr int kLatent = 512, kLatentRope = 64, kLatentToken = kLatent + kLatentRope;
+
+// ---------------------------------------------------------------- append
+
+struct LatentAppendParams {
+    const void *x;               // [b, s, 576] by strides (elements)
+    int64_t xb, xs;
+    void *pool;                  // [num_pages, page_size, 576]
+    const void *weight;          // [512] or nullptr: no norm
+    const float *cos, *sin;      // [>= capacity, 32], or nullptr: no rotation
+    const int32_t *seqlens;      // [b] cached tokens
+    const int32_t *new_seqlens;  // [b] new tokens, or nullptr: s
+    const int32_t *block_table;  // [b, pages_per_seq]
+    uint32_t *status;
+    int64_t b, s, num_pages, pages_per_seq;
+    int page_size, interleaved;
+    float eps;
+};
+
+cudaError_t launch_latent_append(const LatentAppendParams &p, bool bf16, cudaStream_t stream);
+
+// ---------------------------------------------------------------- paged attention
+
+// An item that a team of CTAs begins and later teams go on with.
+struct alignas(16) LatentCut {
+    int32_t parts;  // teams that have a part (0: there is no such item); negated when it is not this team's first
+    int32_t entry;  // which item
+    int32_t pad[2];
+};
+
+enum LatentMask { LATENT_MASK_NONE = 0, LATENT_MASK_CAUSAL = 1, LATENT_MASK_TREE = 2 };
+
+struct LatentPagedParams {
+    const void *q;               // [b, h, sq, 576] by strides (elements)
+    void *o;                     // [b, h, sq, 512] by strides
+    int64_t qb, qh, qs, ob, oh, os;
+    float *lse;                  // [b, h, sq] or nullptr
+    const int32_t *seqlens;      // [b]
+    const int32_t *block_table;  // [b, pages_per_seq]
+    const int32_t *tree;         // [b, sq, tree_words] or nullptr
+    uint32_t *status;
+    float *o_part;               // [2 * grid][tile rows][512]: parts of the items that several teams share
+    float4 *ml_part;             // [2 * grid][tile rows]: their reference (log2), sum, sum as rounded
+    LatentCut *cut;              // [teams]
+    float sl2e;                  // scale * log2(e)
+    int32_t b, h, sq, rows;      // rows = h * sq, row i * h + head
+    int32_t tiles;               // ceil(rows / tile rows)
+    int32_t team, groups;        // CTAs that work on the same keys, a tile of rows each; ceil(tiles / team)
+    int32_t cap, page_size, pages_per_seq, num_pages;
+    int32_t mask, tree_words;
+    int32_t box;                 // tokens of a copy: 128, 64, 32 or 16, a divisor of page_size
+    uint64_t timeout_ns;
+};
+
+constexpr int kLatentMaxCtas = 160;  // CTAs of a launch at most (sizes the workspace)
+constexpr int kLatentMaxTeam = 4;
+constexpr int kLatentPagedInstances = 6;  // {fp16, bf16} x {16, 32, 64 rows}
+
+struct LatentPagedArgs {
+    CUtensorMap pool;
+    LatentPagedParams p;
+    int tile_rows, grid;
+    cudaStream_t stream;
+    std::atomic<int> *attr_ready;  // the library's flags, for the current device: shared-memory opt-in set, per instance
+};
+
+cudaError_t launch_latent_paged(const LatentPagedArgs &a, bool bf16);
+
+}  // namespace attn

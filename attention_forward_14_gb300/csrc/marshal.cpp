@@ -38,6 +38,9 @@ struct Library {
     decltype(&attn_kvcache_append_paged) kvcache_append_paged;
     decltype(&attn_fwd_kvcache_paged_fp8) fwd_kvcache_paged_fp8;
     decltype(&attn_fwd_kvcache_paged_fp8_workspace_bytes) fwd_kvcache_paged_fp8_workspace_bytes;
+    decltype(&attn_latent_append_paged) latent_append_paged;
+    decltype(&attn_fwd_latent_paged) fwd_latent_paged;
+    decltype(&attn_fwd_latent_paged_workspace_bytes) fwd_latent_paged_workspace_bytes;
 } g_lib;
 
 struct Err {
@@ -461,6 +464,110 @@ PyObject *fwd_kvcache_paged_fp8(PyObject *const *a)
     return Py_BuildValue("(NN)", object(a[9], o.t), object(a[10], lse));
 }
 
+// The paged cache of latent attention: a pool of tokens, not of keys and values.
+struct LatentCache {
+    const at::Tensor &pool, &lens, &table;
+    int64_t num_pages, page_size, pages_per_seq;
+};
+
+constexpr int64_t kLatent = 512, kToken = 576;
+
+LatentCache latent_cache(PyObject *po, PyObject *lo, PyObject *to, const at::Tensor &like, int64_t b)
+{
+    LatentCache c{tensor(po, "pool"), tensor(lo, "cache_seqlens"), tensor(to, "block_table"), 0, 0, 0};
+    if (c.pool.dim() != 3 || c.pool.size(2) != kToken)
+        fail(ATTN_ERR_SHAPE, "pool " + shape_of(c.pool) + " must be [num_pages, page_size, 576]");
+    c.num_pages = c.pool.size(0);
+    c.page_size = c.pool.size(1);
+    if (!c.pool.is_cuda() || c.pool.scalar_type() != like.scalar_type())
+        fail(ATTN_ERR_DTYPE, "the pool must be a CUDA tensor of the new tokens' or queries' dtype");
+    if (c.table.dim() != 2 || c.table.size(0) != b || c.table.scalar_type() != at::kInt)
+        fail(ATTN_ERR_SHAPE, "block_table must be int32 [b, pages_per_seq]");
+    c.pages_per_seq = c.table.size(1);
+    if (c.lens.dim() != 1 || c.lens.size(0) != b || c.lens.scalar_type() != at::kInt)
+        fail(ATTN_ERR_DTYPE, "cache_seqlens must be an int32 tensor of b elements");
+    for (const at::Tensor *t : {&c.pool, &c.lens, &c.table})
+        if (t->device() != like.device() || !t->is_contiguous())
+            fail(ATTN_ERR_SHAPE, "pool, block_table and cache_seqlens must be contiguous, on the inputs' device");
+    return c;
+}
+
+PyObject *latent_append_paged(PyObject *const *a)
+{
+    // kv_new, pool, cache_seqlens, block_table, norm_weight, cos, sin, eps, interleaved, new_seqlens, stream
+    const at::Tensor &x = tensor(a[0], "kv_new");
+    if (x.dim() != 3 || x.size(2) != kToken) fail(ATTN_ERR_SHAPE, "kv_new " + shape_of(x) + " must be [b, s_new, 576]");
+    const int dtype = dtype_code(x);
+    if (x.stride(2) != 1 && x.numel() > 0) fail(ATTN_ERR_SHAPE, "the values of a token of kv_new must be contiguous");
+    const int64_t b = x.size(0), s = x.size(1);
+    const int64_t st[3] = {b > 1 ? x.stride(0) : 0, 0, s > 1 ? x.stride(1) : 0};
+    const LatentCache c = latent_cache(a[1], a[2], a[3], x, b);
+    const at::Tensor *w = maybe(a[4], "norm_weight"), *news = maybe(a[9], "new_seqlens");
+    if (w && (w->dim() != 1 || w->size(0) != kLatent || w->scalar_type() != x.scalar_type() || w->device() != x.device() ||
+              !w->is_contiguous()))
+        fail(ATTN_ERR_SHAPE, "norm_weight must be a contiguous [512] tensor typed like kv_new, on its device");
+    if (news && (news->dim() != 1 || news->size(0) != b || news->scalar_type() != at::kInt || news->device() != x.device() ||
+                 !news->is_contiguous()))
+        fail(ATTN_ERR_DTYPE, "new_seqlens must be an int32 tensor of b elements on the pool's device");
+    const Rotation r = rotation(a[5], a[6], x.device());
+    if (r.cos && r.rot != kToken - kLatent) fail(ATTN_ERR_SHAPE, "cos and sin must be [table_len, 32]");
+    const float eps = static_cast<float>(number(a[7], "eps"));
+    const int interleaved = truth(a[8]);
+    const Call call(x, a[10]);
+    {
+        const WithoutLock unlocked;
+        check(g_lib.latent_append_paged(ptr(x), ptr(c.pool), ptr(w), static_cast<const int32_t *>(ptr(c.lens)),
+                                        static_cast<const int32_t *>(ptr(news)), static_cast<const int32_t *>(ptr(c.table)), r.cos,
+                                        r.sin, st, b, s, c.num_pages, c.page_size, c.pages_per_seq, r.length, interleaved, eps,
+                                        dtype, call.stream()));
+    }
+    Py_RETURN_NONE;
+}
+
+PyObject *fwd_latent_paged(PyObject *const *a)
+{
+    // q, pool, cache_seqlens, block_table, scale, causal, tree, o, lse, workspace, stream
+    const at::Tensor &q = tensor(a[0], "q");
+    if (q.dim() != 4 || q.size(3) != kToken) fail(ATTN_ERR_SHAPE, "q " + shape_of(q) + " must be [b, h, sq, 576]");
+    const int dtype = dtype_code(q);
+    if (!q.is_cuda()) fail(ATTN_ERR_SHAPE, "q must be a CUDA tensor");
+    const Dense qd = as_dense("q", q);
+    const LatentCache c = latent_cache(a[1], a[2], a[3], q, qd.b);
+    const float scale = static_cast<float>(number(a[4], "scale"));
+    const int causal = truth(a[5]);
+    const at::Tensor *tree = maybe(a[6], "tree"), *go = maybe(a[7], "o"), *glse = maybe(a[8], "lse"), *gws = maybe(a[9], "workspace");
+    if (tree && (tree->sizes() != at::IntArrayRef({qd.b, qd.s, (qd.s + 31) / 32}) || tree->scalar_type() != at::kInt ||
+                 tree->device() != q.device() || !tree->is_contiguous()))
+        fail(ATTN_ERR_SHAPE, "tree must be contiguous int32 [b, sq, ceil(sq / 32)] on q's device");
+    const Call call(q, a[10]);
+    at::Tensor o, lse;
+    {
+        const WithoutLock unlocked;
+        if (!go) {
+            o = call.empty({qd.b, qd.h, qd.s, kLatent}, q.scalar_type());
+        } else {
+            o = *go;
+            if (o.sizes() != at::IntArrayRef({qd.b, qd.h, qd.s, kLatent}) || o.scalar_type() != q.scalar_type() || o.device() != q.device())
+                fail(ATTN_ERR_SHAPE, "o must be [b, h, sq, 512], typed like q, on its device");
+        }
+        if (!glse) {
+            lse = call.empty({qd.b, qd.h, qd.s}, at::kFloat);
+        } else {
+            lse = *glse;
+            if (lse.sizes() != at::IntArrayRef({qd.b, qd.h, qd.s}) || lse.scalar_type() != at::kFloat || !lse.is_contiguous() ||
+                lse.device() != q.device())
+                fail(ATTN_ERR_SHAPE, "lse must be contiguous fp32 [b, h, sq] on q's device");
+        }
+        const Dense od = as_dense("o", o);
+        const Workspace ws = workspace(call, gws, g_lib.fwd_latent_paged_workspace_bytes(qd.b, qd.h, qd.s), q.device());
+        check(g_lib.fwd_latent_paged(ptr(q), ptr(c.pool), static_cast<const int32_t *>(ptr(c.lens)),
+                                     static_cast<const int32_t *>(ptr(c.table)), static_cast<const int32_t *>(ptr(tree)), ptr(o),
+                                     lse.data_ptr<float>(), qd.st, od.st, qd.b, qd.h, qd.s, c.num_pages, c.page_size,
+                                     c.pages_per_seq, causal, scale, dtype, ws.p, ws.bytes, call.stream()));
+    }
+    return Py_BuildValue("(NN)", object(a[7], o), object(a[8], lse));
+}
+
 // Runs a function on its positional arguments; what it throws becomes a
 // Python exception.
 template <PyObject *(*F)(PyObject *const *), int N>
@@ -509,7 +616,9 @@ PyMethodDef g_methods[] = {
     method<qk_norm_rope_bwd, 15>("qk_norm_rope_bwd"),
     method<kvcache_append_paged, 13>("kvcache_append_paged"),
     method<fwd_kvcache_paged_fp8, 13>("fwd_kvcache_paged_fp8"),
-    method<bind, 8>("bind"),
+    method<latent_append_paged, 11>("latent_append_paged"),
+    method<fwd_latent_paged, 11>("fwd_latent_paged"),
+    method<bind, 11>("bind"),
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -600,6 +600,96 @@ int64_t attn_fwd_kvcache_paged_fp8_workspace_bytes(int64_t b, int64_t h,
                                                    int64_t h_kv, int64_t sq,
                                                    int64_t d);
 
+/*
+ * Latent attention: a token's keys and values are one vector that all heads
+ * share, [latent (512 values) | rotated key part (64)].  Where a head's key is
+ * [W_k latent | key part] and its value W_v latent, the scores of a query
+ * (qn, qr) are (W_k^T qn) . latent + qr . key part: with the query multiplied
+ * by the keys' projection (absorbed form) the vectors themselves are keys of
+ * 576 values and values of 512, and the cache holds nothing else.
+ *
+ * attn_latent_append_paged: new tokens into that cache.  For every token
+ *   latent   = norm_weight * x * (mean(x^2) + eps)^(-1/2)  of the first 512
+ *              values (norm_weight NULL: as they are)
+ *   key part = R(position) of the last 64 (cos, sin NULL: as it is), with
+ *              pairs (i, i + 32), or adjacent ones when `interleaved`
+ * fp32 arithmetic, one rounding at the end.
+ *   kv_new       : [b, s_new, 576] of dtype, 16-byte aligned; kv_strides[0]
+ *                  and [2] are the strides of b and of s_new in elements
+ *                  (multiples of 8); [1] is not used.
+ *   pool         : [num_pages, page_size, 576] of dtype, contiguous, 16-byte
+ *                  aligned.  It must not overlap what is read.
+ *   norm_weight  : [512] of dtype, 16-byte aligned, or NULL.
+ *   cos, sin     : fp32 [table_len, 32], table_len at least the capacity, or
+ *                  both NULL.
+ *   cache_seqlens, new_seqlens, block_table, page_size (a positive multiple
+ *                  of 16), pages_per_seq: as for attn_kvcache_append_paged.
+ * Token t of element e goes to position L + t (L the clamped cached length),
+ * by which its key part is rotated.  Tokens at or past the capacity, and pages
+ * outside the pool, are not written.
+ * Returns ATTN_OK or a negative ATTN_ERR_* code.
+ */
+int attn_latent_append_paged(const void *kv_new, void *pool,
+                             const void *norm_weight,
+                             const int32_t *cache_seqlens,
+                             const int32_t *new_seqlens,
+                             const int32_t *block_table, const float *cos,
+                             const float *sin, const int64_t *kv_strides,
+                             int64_t b, int64_t s_new, int64_t num_pages,
+                             int64_t page_size, int64_t pages_per_seq,
+                             int64_t table_len, int interleaved, float eps,
+                             int dtype, void *stream);
+
+/*
+ * Latent attention over its paged cache (absorbed form):
+ *   O[b, h, i, :] = sum_j P[i, j] c_j[0..511],
+ *   P[i, :] = softmax_j(scale * q[b, h, i, :] . c_j  [+ mask])
+ * over the tokens c_j of element b's cache.
+ *   q            : [b, h, sq, 576] of dtype by strides (of b, of the head, of
+ *                  sq, in elements, multiples of 8), 16-byte aligned.
+ *   pool         : [num_pages, page_size, 576] of dtype, contiguous, 16-byte
+ *                  aligned.
+ *   cache_seqlens: device int32 [b], the tokens to attend to, the new ones
+ *                  among them: append first (clamped to 0..pages_per_seq *
+ *                  page_size).
+ *   block_table  : device int32 [b, pages_per_seq]; a page index outside the
+ *                  pool reads as zeros.
+ *   o            : [b, h, sq, 512] of dtype by strides, 16-byte aligned; its
+ *                  rows must not coincide, nor overlap q or the pool.
+ *   lse          : fp32 [b, h, sq], contiguous, or NULL.
+ *   causal       : nonzero: query i of element e, L cached tokens, sees keys
+ *                  j <= i + L - sq.
+ *   tree         : device int32 [b, sq, ceil(sq / 32)], or NULL (with
+ *                  causal: refused): the last sq cached tokens are drafted ones,
+ *                  and query i sees the t-th of them (key L - sq + t) when bit
+ *                  t % 32 of word t / 32 of its row is set, and every key
+ *                  before them.
+ *   scale        : finite multiplier of the scores (of the expanded form's key
+ *                  size, in general).
+ *   workspace    : caller-owned device scratch, 16-byte aligned, of at least
+ *                  attn_fwd_latent_paged_workspace_bytes(b, h, sq) bytes; its
+ *                  contents on entry do not matter.  Calls on different
+ *                  streams need different workspaces.
+ * A row that sees no key gets O = 0 and LSE = -inf.  Slots at or past L are
+ * not read into the result, and what a row does not see does not reach it,
+ * NaN and infinities included.  The work is dealt out by the lengths on the
+ * device.  fp32 accumulation and statistics; P is rounded to dtype before its
+ * product, and O divided by the sum of P as rounded.
+ * Returns ATTN_OK or a negative ATTN_ERR_* code.
+ */
+int attn_fwd_latent_paged(const void *q, const void *pool,
+                          const int32_t *cache_seqlens,
+                          const int32_t *block_table, const int32_t *tree,
+                          void *o, float *lse, const int64_t *q_strides,
+                          const int64_t *o_strides, int64_t b, int64_t h,
+                          int64_t sq, int64_t num_pages, int64_t page_size,
+                          int64_t pages_per_seq, int causal, float scale,
+                          int dtype, void *workspace, int64_t workspace_bytes,
+                          void *stream);
+
+/* Bytes of workspace attn_fwd_latent_paged needs, or a negative code. */
+int64_t attn_fwd_latent_paged_workspace_bytes(int64_t b, int64_t h, int64_t sq);
+
 /* Thread-local message describing the last non-OK return on this thread
  * ("" if none).  The pointer stays valid until the next call on the thread. */
 const char *attn_last_error(void);
