@@ -1740,6 +1740,7 @@ int attn_fwd_latent_paged(const void *q, const void *pool, const int32_t *cache_
         return rc;
     const int tile = latent_tile_rows(rows);
     p.q = q, p.o = o, p.lse = lse;
+    p.pool = static_cast<const uint8_t *>(pool);
     p.qb = q_strides[0], p.qh = q_strides[1], p.qs = q_strides[2];
     p.ob = o_strides[0], p.oh = o_strides[1], p.os = o_strides[2];
     p.seqlens = cache_seqlens;

@@ -79,6 +79,7 @@ struct LatentCtl {
     uint64_t q_full, s_full, p_full, pv_done, dirty, clean, mma_done;
     uint32_t tmem_base, abort;
     int32_t query[64];       // the query of each row
+    float ref[64];           // the reference of each row, which its scores are less in the exponent
     float inv[64];
     float red[2][4][32];     // of a softmax group's warps: a value for each of its rows
     float red2[2][4][32];
@@ -116,11 +117,13 @@ __device__ __forceinline__ int entry_units(const LatentPagedParams &p, int entry
     return units_for(group_end(p, latent_len(p, b), entry - b * p.groups, tile_rows));
 }
 
-__device__ __forceinline__ int64_t latent_total(const LatentPagedParams &p, int tile_rows)
+// (`mine`: entry_units of entry `lane`, which both this and latent_place begin with)
+__device__ __forceinline__ int64_t latent_total(const LatentPagedParams &p, int mine, int tile_rows)
 {
     const int lane = threadIdx.x & 31, entries = p.b * p.groups;
-    int64_t t = 0;
-    for (int e = lane; e < entries; e += 32) t += entry_units(p, e, tile_rows);
+    int64_t t = mine;
+#pragma unroll 4
+    for (int e = 32 + lane; e < entries; e += 32) t += entry_units(p, e, tile_rows);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
     return t;
@@ -139,12 +142,12 @@ __device__ __forceinline__ void set_entry(const LatentPagedParams &p, LatentPlac
 }
 
 // The place of unit u (< total), by every lane of a warp.
-__device__ __forceinline__ LatentPlace latent_place(const LatentPagedParams &p, int64_t u, int tile_rows)
+__device__ __forceinline__ LatentPlace latent_place(const LatentPagedParams &p, int mine, int64_t u, int tile_rows)
 {
     const int lane = threadIdx.x & 31, entries = p.b * p.groups;
     LatentPlace c{};
     for (int e0 = 0; e0 < entries; e0 += 32) {
-        int64_t inc = entry_units(p, e0 + lane, tile_rows);
+        int64_t inc = e0 == 0 ? mine : entry_units(p, e0 + lane, tile_rows);
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int64_t o = __shfl_up_sync(0xffffffffu, inc, off);
@@ -178,6 +181,20 @@ __device__ __forceinline__ bool group_any(int barrier, bool v)
     return r != 0u;
 }
 
+// 16 bytes to shared memory, or zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16u : 0u) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Brings `bytes` (a multiple of 16) from `src` on into the L2.
+__device__ __forceinline__ void l2_prefetch(const uint8_t *src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
 // v[c] over the warp's lanes (their sum, or largest): lane l has it for
 // column l % C.  A step halves the columns that a lane looks after.
 template <int C, typename F>
@@ -198,6 +215,9 @@ __device__ __forceinline__ float reduce_columns(float (&v)[C], F f)
         }
     return v[0];
 }
+
+// Natural log-sum-exp of a row from its reference and sum.
+__device__ __forceinline__ float latent_lse(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f; }
 
 // Instruction descriptor of O^T: both operands MN-major.
 __host__ __device__ constexpr uint32_t idesc_mn(int M, int N, bool bf16) { return idesc_f16(M, N, bf16, true) | (1u << 15); }
@@ -280,13 +300,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     await_previous();
 
     const int team = blockIdx.x / p.team, rank = blockIdx.x - team * p.team;
-    const Shares shared_out(latent_total(p, N), static_cast<int>(gridDim.x) / p.team, 1);
+    const int mine = entry_units(p, lane, N);
+    const Shares shared_out(latent_total(p, mine, N), static_cast<int>(gridDim.x) / p.team, 1);
     const bool works = team < shared_out.ctas;
     // (a team that gives up on a wait leaves it so: the join must not meet what was in the workspace)
     if (threadIdx.x == 0 && rank == 0) p.cut[team] = LatentCut{0, 0, {0, 0}};
     const int64_t u0 = works ? shared_out.start(team) : 0;
     const int n_units = works ? static_cast<int>(shared_out.start(team + 1) - u0) : 0;
-    LatentPlace at = latent_place(p, u0, N);
+    LatentPlace at = latent_place(p, mine, u0, N);
     auto place_in_bounds = [&]() {
         const bool ok = ATTN_OPS_IN_BOUNDS(at.b >= 0 && at.b < p.b && at.group >= 0 && at.group < p.groups && at.j >= 0 && at.j < at.n,
                                            p, SITE_OPS_UNIT);
@@ -317,13 +338,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int j_end = min(at.n, at.j + n_units - it);
                 const int tiles = item_tiles(j_end);
                 const int32_t *table = p.block_table + static_cast<int64_t>(at.b) * p.pages_per_seq;
-                for (int t = 0; ok && t < tiles; ++t) {
+                // where the lane's keys of a tile lie: a copy begins there, or none (-1)
+                auto token_of = [&](int t) {
                     const int k = (at.j + t) * kTileKeys + 16 * group;
-                    const bool there = lane < 16 && k < at.len && (16 * group) % p.box == 0;
-                    const int pg = k / p.page_size, off = k - pg * p.page_size;
-                    const int page = there ? table[pg] : -1;
-                    const bool in = page >= 0 && page < p.num_pages;
-                    const int token = in ? page * p.page_size + off : nowhere;
+                    if (t >= tiles || lane >= 16 || k >= at.len || (16 * group) % p.box != 0) return -1;
+                    const int pg = k / p.page_size, page = table[pg];
+                    return page >= 0 && page < p.num_pages ? page * p.page_size + (k - pg * p.page_size) : nowhere;
+                };
+                int next = token_of(0);
+                for (int t = 0; ok && t < tiles; ++t) {
+                    const int token = next;
+                    const bool there = token >= 0;
+                    next = token_of(t + 1);
+                    // The next tile is on its way to the L2 meanwhile: a slot that is let go waits for that only.  The
+                    // tokens of a page lie one after another; half of a copy's to a lane.
+                    if (next >= 0 && next != nowhere && rank == (at.j + t) % p.team)
+                        l2_prefetch(p.pool + (static_cast<int64_t>(next) * 2 + side * p.box) * kLatentToken, p.box * kLatentToken);
                     const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, there) & 0xFFu);
                     for (int pr = 0; ok && pr < kPairs; ++pr, ++np) {
                         const uint32_t st = np % C::PAIR_SLOTS, bar = B(ctl->pair_full[st]);
@@ -481,6 +511,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t row0 = first_row();
             const int nr = static_cast<int>(min(static_cast<int64_t>(N), max(p.rows - row0, int64_t(0))));
             const int all = all_see(), before = at.len - p.sq;
+            // The rows of the group's half that see key k: query by query, since a query's heads stand together.
+            auto rows_that_see = [&](int k) {
+                uint32_t sees = 0u;
+                if (k >= at.len) return sees;
+                const int drafted = k - before;
+                const int32_t *tree = p.tree + static_cast<int64_t>(at.b) * p.sq * p.tree_words + (drafted >> 5);
+                const int first = ctl->query[w * COLS], last = ctl->query[w * COLS + COLS - 1];
+                int r = static_cast<int>(first * static_cast<int64_t>(p.h) - row0) - w * COLS;  // the query's first row
+#pragma unroll 4
+                for (int i = first; i <= last; ++i, r += p.h) {
+                    bool one = true;
+                    if (p.mask == LATENT_MASK_CAUSAL) one = drafted <= i;
+                    if (p.mask == LATENT_MASK_TREE && drafted >= 0)
+                        one = (tree[static_cast<int64_t>(i) * p.tree_words] >> (drafted & 31) & 1) != 0;
+                    const int lo = max(r, 0), n = min(r + p.h, 32) - lo;  // n >= 1
+                    if (one) sees |= (n < 32 ? (1u << n) - 1u : ~0u) << lo;
+                }
+                return sees;
+            };
             // what is needed of each row of the group's half
             if (key < COLS) {
                 const int r = w * COLS + key;
@@ -490,74 +539,87 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ctl->o_at[r] = at.b * p.ob + head * p.oh + i * p.os;
             }
             if (tiles > 0) {
+                // 72 pieces of 16 bytes a row, all of them on their way at once; eight lanes to a panel's row
                 const T *q = static_cast<const T *>(p.q) + at.b * p.qb;
-                for (int c = threadIdx.x; c < N * (kLatentToken / 8); c += 256) {
-                    const int r = c / (kLatentToken / 8), ch = c - r * (kLatentToken / 8);
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < nr) {
-                        const int row = static_cast<int>(row0) + r, i = row / p.h, head = row - i * p.h;
-                        v = reinterpret_cast<const uint4 *>(q + head * p.qh + i * p.qs)[ch];
-                    }
-                    st_shared_v4(sQ + (ch >> 3) * C::Q_PANEL + r * 128 + (((ch & 7) ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
+                const int sub = lane & 7;
+                for (int r = warp * 4 + (lane >> 3); r < N; r += 32) {
+                    const int row = static_cast<int>(row0) + min(r, nr - 1), i = row / p.h, head = row - i * p.h;
+                    const uint4 *src = reinterpret_cast<const uint4 *>(q + head * p.qh + i * p.qs) + sub;
+                    const uint32_t to = sQ + r * 128 + ((sub ^ (r & 7)) << 4);
+#pragma unroll
+                    for (int pn = 0; pn < kPanels; ++pn) cp_async16(to + pn * C::Q_PANEL, src + pn * 8, r < nr);
                 }
+                cp_async_wait_all();
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(B(ctl->q_full));
             }
-            group_sync();
-            float m[COLS], l[COLS], lr[COLS];
+            if (key < COLS) ctl->ref[w * COLS + key] = 0.f;
+            float2 l[COLS / 2], lr[COLS / 2];
 #pragma unroll
-            for (int c = 0; c < COLS; ++c) m[c] = -INFINITY, l[c] = 0.f, lr[c] = 0.f;
+            for (int c = 0; c < COLS / 2; ++c) l[c] = lr[c] = make_float2(0.f, 0.f);
+            uint32_t unset = COLS == 32 ? ~0u : (1u << COLS) - 1u;  // rows without a reference: they have seen no key yet
+            group_sync();
             for (int t = 0; t < tiles; ++t, ++tile_it, ++nk) {
                 if (ok) ok = warp_waits(B(ctl->s_full), tile_it & 1u, SITE_LAT_S);
                 tc_fence_after();
-                const int k0 = (at.j + t) * kTileKeys, k = k0 + key;
-                float x[COLS];
+                const int k0 = (at.j + t) * kTileKeys;
+                float2 x[COLS / 2];  // the scores less their rows' references
                 {
                     uint32_t s[COLS];
                     tmem_load(tS, s);
+                    const float2 scale2 = make_float2(p.sl2e, p.sl2e);
+                    const float2 *ref = reinterpret_cast<const float2 *>(ctl->ref + w * COLS);
 #pragma unroll
-                    for (int c = 0; c < COLS; ++c) x[c] = __uint_as_float(s[c]) * p.sl2e;
-                }
-                if (k0 + kTileKeys > all) {
-                    const int drafted = k - before;
-                    const int32_t *tree = p.tree + static_cast<int64_t>(at.b) * p.sq * p.tree_words + (drafted >> 5);
-#pragma unroll
-                    for (int c = 0; c < COLS; ++c) {
-                        const int i = ctl->query[w * COLS + c];
-                        bool sees = k < at.len;
-                        if (p.mask == LATENT_MASK_CAUSAL) sees = sees && drafted <= i;
-                        if (p.mask == LATENT_MASK_TREE && sees && drafted >= 0)
-                            sees = (tree[static_cast<int64_t>(i) * p.tree_words] >> (drafted & 31) & 1) != 0;
-                        x[c] = sees ? x[c] : -INFINITY;
+                    for (int c = 0; c < COLS / 2; ++c) {
+                        const float2 m = ref[c];
+                        x[c] = __ffma2_rn(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), scale2,
+                                          make_float2(-m.x, -m.y));
                     }
                 }
-                bool over = false;
+                if (k0 + kTileKeys > all) {
+                    const uint32_t sees = rows_that_see(k0 + key);
 #pragma unroll
-                for (int c = 0; c < COLS; ++c) over = over || x[c] > m[c] + kSlackLog2;
-                if (group_any(bar_id, over)) {
+                    for (int c = 0; c < COLS / 2; ++c) {
+                        x[c].x = sees >> (2 * c) & 1 ? x[c].x : -INFINITY;
+                        x[c].y = sees >> (2 * c + 1) & 1 ? x[c].y : -INFINITY;
+                    }
+                }
+                float top = x[0].x;
+#pragma unroll
+                for (int c = 0; c < COLS / 2; ++c) top = max3f(top, x[c].x, x[c].y);
+                if (group_any(bar_id, top > kSlackLog2 || unset != 0u)) {
                     float v[COLS];
 #pragma unroll
-                    for (int c = 0; c < COLS; ++c) v[c] = x[c];
-                    const float top = reduce_columns<COLS>(v, [](float a, float b) { return fmaxf(a, b); });
-                    if (lane < COLS) ctl->red[w][in_group][lane] = top;
-                    group_sync();
+                    for (int c = 0; c < COLS / 2; ++c) v[2 * c] = x[c].x, v[2 * c + 1] = x[c].y;
+                    const float up = reduce_columns<COLS>(v, [](float a, float b) { return fmaxf(a, b); });
+                    if (lane < COLS) ctl->red[w][in_group][lane] = up;
                     if (t > 0) {  // O^T has the tiles before: let the last one's products end
                         if (ok) ok = warp_waits(B(ctl->pv_done), (tile_it - 1) & 1u, SITE_LAT_O);
                         tc_fence_after();
                     }
+                    group_sync();
+                    // by how much each row's reference rises (is set)
+                    float own = 0.f;
 #pragma unroll
                     for (int c = 0; c < COLS; ++c) {
-                        const float n = fmaxf(fmaxf(fmaxf(ctl->red[w][0][c], ctl->red[w][1][c]),
-                                                    fmaxf(ctl->red[w][2][c], ctl->red[w][3][c])), m[c]);
-                        const float f = m[c] == n ? 1.f : ex2_approx(m[c] - n);
-                        m[c] = n;
-                        l[c] *= f;
-                        lr[c] *= f;
-                        v[c] = f;
+                        const float mx = fmaxf(fmaxf(ctl->red[w][0][c], ctl->red[w][1][c]), fmaxf(ctl->red[w][2][c], ctl->red[w][3][c]));
+                        const bool first = unset >> c & 1;
+                        const float rise = first ? (mx > -INFINITY ? mx : 0.f) : fmaxf(mx, 0.f);
+                        if (mx > -INFINITY) unset &= ~(1u << c);
+                        if (c & 1) x[c / 2].y -= rise;
+                        else x[c / 2].x -= rise;
+                        v[c] = first ? 1.f : ex2_approx(-rise);
+                        own = c == key ? rise : own;
+                    }
+                    if (key < COLS) ctl->ref[w * COLS + key] += own;
+#pragma unroll
+                    for (int c = 0; c < COLS / 2; ++c) {
+                        l[c] = __fmul2_rn(l[c], make_float2(v[2 * c], v[2 * c + 1]));
+                        lr[c] = __fmul2_rn(lr[c], make_float2(v[2 * c], v[2 * c + 1]));
                     }
                     if (t > 0) {
-#pragma unroll
+#pragma unroll 1
                         for (int j = 0; j < kPairs; ++j) {
                             uint32_t o[COLS];
                             tmem_load(tO + j * N, o);
@@ -567,24 +629,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         tmem_wait_st();
                     }
+                    group_sync();  // the references, before they are read again
                 }
                 // this key's weights, into its row of P^T
                 const uint32_t row = sKey + (nk % C::KEY_SLOTS) * C::PANEL + key * 128;
-                uint32_t pk[COLS / 2];
 #pragma unroll
-                for (int c = 0; c < COLS; c += 2) {
-                    const float p0 = ex2_approx(x[c] - (m[c] == -INFINITY ? 0.f : m[c]));
-                    const float p1 = ex2_approx(x[c + 1] - (m[c + 1] == -INFINITY ? 0.f : m[c + 1]));
-                    l[c] += p0;
-                    l[c + 1] += p1;
-                    pk[c / 2] = Pair<T>::put(p0, p1);
-                    const float2 r = Pair<T>::get(pk[c / 2]);
-                    lr[c] += r.x;
-                    lr[c + 1] += r.y;
+                for (int c = 0; c < COLS / 8; ++c) {
+                    uint32_t pk[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 v = make_float2(ex2_approx(x[4 * c + e].x), ex2_approx(x[4 * c + e].y));
+                        l[4 * c + e] = __fadd2_rn(l[4 * c + e], v);
+                        pk[e] = Pair<T>::put(v.x, v.y);
+                        lr[4 * c + e] = __fadd2_rn(lr[4 * c + e], Pair<T>::get(pk[e]));
+                    }
+                    st_shared_v4(row + (((w * (COLS / 8) + c) ^ (key & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
                 }
-#pragma unroll
-                for (int c = 0; c < COLS / 8; ++c)
-                    st_shared_v4(row + (((w * (COLS / 8) + c) ^ (key & 7)) << 4), pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
@@ -596,30 +656,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool whole = first_unit >= u0 && item_ends;
             const int64_t part0 = (2 * static_cast<int64_t>(blockIdx.x) + (first_unit > u0 ? 1 : 0)) * N;
             {
-                const float ls = reduce_columns<COLS>(l, [](float a, float b) { return a + b; });
-                const float lrs = reduce_columns<COLS>(lr, [](float a, float b) { return a + b; });
+                float v[COLS];
+#pragma unroll
+                for (int c = 0; c < COLS / 2; ++c) v[2 * c] = l[c].x, v[2 * c + 1] = l[c].y;
+                const float ls = reduce_columns<COLS>(v, [](float a, float b) { return a + b; });
+#pragma unroll
+                for (int c = 0; c < COLS / 2; ++c) v[2 * c] = lr[c].x, v[2 * c + 1] = lr[c].y;
+                const float lrs = reduce_columns<COLS>(v, [](float a, float b) { return a + b; });
                 if (lane < COLS) {
                     ctl->red[w][in_group][lane] = ls;
                     ctl->red2[w][in_group][lane] = lrs;
                 }
             }
             group_sync();
-            // (all threads hold the same m; a row's is written by the thread that has its sums)
-#pragma unroll
-            for (int c = 0; c < COLS; ++c) {
-                if (key != c) continue;
-                const int r = w * COLS + c;
-                const float ls = (ctl->red[w][0][c] + ctl->red[w][1][c]) + (ctl->red[w][2][c] + ctl->red[w][3][c]);
-                const float lrs = (ctl->red2[w][0][c] + ctl->red2[w][1][c]) + (ctl->red2[w][2][c] + ctl->red2[w][3][c]);
+            if (key < COLS) {
+                const int r = w * COLS + key;
+                const float ls = (ctl->red[w][0][key] + ctl->red[w][1][key]) + (ctl->red[w][2][key] + ctl->red[w][3][key]);
+                const float lrs = (ctl->red2[w][0][key] + ctl->red2[w][1][key]) + (ctl->red2[w][2][key] + ctl->red2[w][3][key]);
                 ctl->inv[r] = !whole ? 1.f : (ls == 0.f ? 0.f : 1.f / lrs);
                 if (r < nr) {
                     if (!whole) {
-                        p.ml_part[part0 + r] = make_float4(m[c], ls, lrs, 0.f);
+                        p.ml_part[part0 + r] = make_float4(ls == 0.f ? -INFINITY : ctl->ref[r], ls, lrs, 0.f);
                     } else if (p.lse) {
                         const int64_t row = row0 + r;
                         const int i = ctl->query[r], head = static_cast<int>(row - static_cast<int64_t>(i) * p.h);
-                        p.lse[(static_cast<int64_t>(at.b) * p.h + head) * p.sq + i] =
-                            ls == 0.f ? -INFINITY : (m[c] + log2f(ls)) * 0.69314718055994531f;
+                        p.lse[(static_cast<int64_t>(at.b) * p.h + head) * p.sq + i] = latent_lse(ctl->ref[r], ls);
                     }
                 }
             }
@@ -787,7 +848,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_latent_join_kernel(const
             __syncthreads();
         }
         if (have && lane == 0 && (alone || warp == 0) && p.lse)
-            p.lse[(static_cast<int64_t>(b) * p.h + head) * p.sq + i] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+            p.lse[(static_cast<int64_t>(b) * p.h + head) * p.sq + i] = latent_lse(m, l);
         __syncwarp();
     }
 }

@@ -49,6 +49,7 @@ struct LatentPagedParams {
     void *o;                     // [b, h, sq, 512] by strides
     int64_t qb, qh, qs, ob, oh, os;
     float *lse;                  // [b, h, sq] or nullptr
+    const uint8_t *pool;         // [num_pages, page_size, 576] (copied through its map, prefetched directly)
     const int32_t *seqlens;      // [b]
     const int32_t *block_table;  // [b, pages_per_seq]
     const int32_t *tree;         // [b, sq, tree_words] or nullptr
