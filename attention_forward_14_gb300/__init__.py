@@ -8,6 +8,7 @@ is no fallback path.
 from .binding import (  # noqa: F401
     AttnError,
     attn_bwd,
+    attn_bwd_latent,
     attn_bwd_varlen,
     attn_fwd,
     attn_fwd_fp8,
@@ -15,6 +16,7 @@ from .binding import (  # noqa: F401
     attn_fwd_kvcache,
     attn_fwd_kvcache_paged,
     attn_fwd_kvcache_paged_fp8,
+    attn_fwd_latent,
     attn_fwd_latent_paged,
     attn_fwd_splitkv,
     attn_fwd_varlen,
@@ -22,6 +24,7 @@ from .binding import (  # noqa: F401
     attn_latent_append_paged,
     attn_qk_norm_rope,
     attn_qk_norm_rope_bwd,
+    bwd_latent_workspace_bytes,
     bwd_workspace_bytes,
     kvcache_paged_fp8_workspace_bytes,
     latent_paged_workspace_bytes,

@@ -30,7 +30,8 @@ EXPORTS = ["attn_fwd", "attn_fwd_host", "attn_fwd_varlen", "attn_fwd_fp8", "attn
            "attn_bwd_varlen_workspace_bytes", "attn_fwd_kvcache", "attn_fwd_kvcache_paged", "attn_qk_norm_rope",
            "attn_qk_norm_rope_bwd", "attn_qk_norm_rope_bwd_workspace_bytes", "attn_kvcache_append_paged",
            "attn_fwd_kvcache_paged_fp8", "attn_fwd_kvcache_paged_fp8_workspace_bytes", "attn_latent_append_paged",
-           "attn_fwd_latent_paged", "attn_fwd_latent_paged_workspace_bytes"]
+           "attn_fwd_latent_paged", "attn_fwd_latent_paged_workspace_bytes", "attn_fwd_latent", "attn_bwd_latent",
+           "attn_bwd_latent_workspace_bytes"]
 
 
 class AttnError(RuntimeError):
@@ -123,6 +124,12 @@ def _bind(lib):
     lib.attn_fwd_latent_paged.argtypes = [vp] * 9 + [i64] * 6 + [c_int, c_float, c_int, vp, i64, vp]
     lib.attn_fwd_latent_paged_workspace_bytes.restype = i64
     lib.attn_fwd_latent_paged_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.attn_fwd_latent.restype = c_int
+    lib.attn_fwd_latent.argtypes = [vp] * 10 + [i64] + [vp] * 2 + [i64] * 6 + [c_int, c_float, c_int, vp]
+    lib.attn_bwd_latent.restype = c_int
+    lib.attn_bwd_latent.argtypes = [vp] * 14 + [i64] * 6 + [c_int, c_float, c_int, vp, i64, vp]
+    lib.attn_bwd_latent_workspace_bytes.restype = i64
+    lib.attn_bwd_latent_workspace_bytes.argtypes = [i64, i64, i64]
     return lib
 
 
@@ -598,7 +605,8 @@ def attn_bwd_varlen(q, k, v, o, dout, lse, cu_seqlens_q, cu_seqlens_k, max_seqle
 # What csrc/marshal.cpp calls, in the order in which it takes their addresses.
 _MARSHALLED = ("attn_last_error", "attn_qk_norm_rope", "attn_qk_norm_rope_bwd", "attn_qk_norm_rope_bwd_workspace_bytes",
                "attn_kvcache_append_paged", "attn_fwd_kvcache_paged_fp8", "attn_fwd_kvcache_paged_fp8_workspace_bytes",
-               "attn_latent_append_paged", "attn_fwd_latent_paged", "attn_fwd_latent_paged_workspace_bytes")
+               "attn_latent_append_paged", "attn_fwd_latent_paged", "attn_fwd_latent_paged_workspace_bytes",
+               "attn_fwd_latent", "attn_bwd_latent", "attn_bwd_latent_workspace_bytes")
 _fast, _fast_lib = None, None
 
 
@@ -732,3 +740,35 @@ def attn_fwd_latent_paged(q, pool, cache_seqlens, block_table, scale: float, cau
     latent_paged_workspace_bytes bytes.  Returns (o [b, h, sq, 512], lse)."""
     return _marshal().fwd_latent_paged(q, pool, cache_seqlens, block_table, scale, causal, tree, o, lse, workspace,
                                        _handle(stream))
+
+
+def attn_fwd_latent(q, k_nope, k_rope, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, max_seqlen_k: int,
+                    causal: bool = False, scale: float | None = None, o=None, lse=None, stream=None):
+    """Latent attention, expanded form, over packed sequences: a head's keys
+    are 128 values of its own and the 64 of ``k_rope`` that all heads share,
+    its values 128.
+
+    q: [total_q, h, 192], k_nope / v: [total_k, h, 128], k_rope: [total_k, 64];
+    fp16 or bf16, any strides (multiples of 8 elements) with contiguous rows, so
+    that views of the projections need no copy; cu_seqlens_*: int32 CUDA tensors
+    [batch + 1].  ``scale`` defaults to 1 / sqrt(192).  Returns (o [total_q, h,
+    128], lse [h, total_q])."""
+    return _marshal().fwd_latent(q, k_nope, k_rope, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, causal,
+                                 scale, o, lse, _handle(stream))
+
+
+def bwd_latent_workspace_bytes(h: int, total_q: int, total_k: int) -> int:
+    lib = load()
+    return _check(int(lib.attn_bwd_latent_workspace_bytes(h, total_q, total_k)), lib)
+
+
+def attn_bwd_latent(q, k_nope, k_rope, v, o, dout, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int,
+                    max_seqlen_k: int, causal: bool = False, scale: float | None = None, dq=None, dk_nope=None,
+                    dk_rope=None, dv=None, workspace=None, stream=None):
+    """Gradients (dq, dk_nope, dk_rope, dv) of attn_fwd_latent for the output
+    gradient ``dout``, from the forward's ``o`` and ``lse``; dk_rope is summed
+    over the heads.  Outputs may be given, with any strides (``dk_nope`` and
+    ``dv`` as the two parts of a fused projection's gradient); ``workspace`` is
+    a CUDA uint8 tensor of bwd_latent_workspace_bytes bytes."""
+    return _marshal().bwd_latent(q, k_nope, k_rope, v, o, dout, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                                 max_seqlen_k, causal, scale, dq, dk_nope, dk_rope, dv, workspace, _handle(stream))

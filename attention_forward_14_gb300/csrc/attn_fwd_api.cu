@@ -78,6 +78,8 @@ struct DeviceInfo {
     std::atomic<int> bwd_attr[bwd::kBwdInstances] = {};
     std::atomic<int> kv8_attr[kKv8Instances] = {};
     std::atomic<int> latent_attr[kLatentPagedInstances] = {};
+    std::atomic<int> latent_fwd_attr[kLatentFwdInstances] = {};
+    std::atomic<int> latent_bwd_attr[kLatentBwdInstances] = {};
 };
 DeviceInfo g_dev[kMaxDevices];
 
@@ -1775,6 +1777,211 @@ int attn_fwd_latent_paged(const void *q, const void *pool, const int32_t *cache_
     a.attr_ready = di->latent_attr;
     const cudaError_t e = launch_latent_paged(a, dtype == ATTN_BF16);
     return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "kernel launch (latent paged cache)");
+}
+
+// A packed tensor of the expanded form: [tokens, heads, d], the d values of a
+// row contiguous, by the strides of a token and of a head (elements).
+struct Rows {
+    const char *name;
+    const void *p;
+    int64_t tokens, heads, d;
+    int64_t st[2];
+    Extent extent() const
+    {
+        const int64_t s3[3] = {0, st[1], st[0]};
+        return extent_of(p, s3, 1, heads, tokens, d);
+    }
+};
+
+static int validate_rows(const Rows &r, bool out)
+{
+    if (r.tokens * r.heads == 0) return ATTN_OK;
+    if (!r.p) return fail(ATTN_ERR_NULL, "%s is NULL", r.name);
+    if (!aligned(r.p, 16)) return fail(ATTN_ERR_ALIGN, "%s must be 16-byte aligned", r.name);
+    const int64_t n[2] = {r.tokens, r.heads};
+    for (int i = 0; i < 2; ++i)
+        if (n[i] > 1 && (r.st[i] <= 0 || r.st[i] % 8 != 0 || r.st[i] >= (int64_t(1) << 39)))
+            return fail(ATTN_ERR_ALIGN, "strides of %s must be positive multiples of 8 elements (16 bytes) below 2^39", r.name);
+    const int64_t s3[3] = {0, r.st[1], r.st[0]};
+    return out ? validate_out_strides(s3, 1, r.heads, r.tokens, r.d, r.name) : ATTN_OK;
+}
+
+// Two outputs share no value: apart, or the rows of one between the rows of
+// the other (as the two parts of a projection's gradient lie).
+static int validate_rows_apart(const Rows &a, const Rows &b)
+{
+    if (a.tokens * a.heads == 0 || b.tokens * b.heads == 0 || !overlap(a.extent(), b.extent())) return ATTN_OK;
+    const int64_t step = a.heads > 1 ? a.st[1] : a.st[0];
+    const bool alike = a.heads == b.heads && a.tokens == b.tokens && (a.heads == 1 || a.st[1] == b.st[1]) &&
+                       (a.tokens == 1 || (a.st[0] == b.st[0] && a.st[0] % step == 0));
+    if (alike && step > 0) {
+        const int64_t bytes = static_cast<const char *>(b.p) - static_cast<const char *>(a.p), at = ((bytes / 2) % step + step) % step;
+        if (bytes % 2 == 0 && at >= a.d && step - at >= b.d) return ATTN_OK;
+    }
+    return fail(ATTN_ERR_SHAPE, "%s and %s overlap", a.name, b.name);
+}
+
+// Copies of `rows` tokens x 64 values of one head.  (Of a tensor without tokens, which nothing is copied from: of `other`.)
+static int make_map_rows(CUtensorMap *map, const Rows &r, int dtype, int rows, const void *other)
+{
+    const bool none = r.tokens * r.heads == 0;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(r.d), static_cast<cuuint64_t>(none ? 1 : r.heads),
+                                static_cast<cuuint64_t>(none ? 1 : r.tokens)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>((!none && r.heads > 1 ? r.st[1] : r.d) * 2),
+                                   static_cast<cuuint64_t>((!none && r.tokens > 1 ? r.st[0] : r.d) * 2)};
+    const cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(rows)};
+    return encode_map(map, dtype == ATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, none ? other : r.p,
+                      dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, r.name);
+}
+
+static int validate_latent_seqs(LatentSeqs *s, const int32_t *cu_q, const int32_t *cu_k, int64_t batch, int64_t h, int64_t total_q,
+                                int64_t total_k, int64_t max_q, int64_t max_k, int causal, float scale, int dtype)
+{
+    if (batch < 0 || h < 0 || total_q < 0 || total_k < 0 || max_q < 0 || max_k < 0) return fail(ATTN_ERR_SHAPE, "negative size");
+    if (total_q > kMaxSeq || total_k > kMaxSeq || max_q > total_q || max_k > total_k)
+        return fail(ATTN_ERR_SHAPE, "totals above 2^30 or max lengths above the totals");
+    if (h > (1 << 20) || (h > 0 && (total_q + 16) / 16 > INT32_MAX / h)) return fail(ATTN_ERR_SHAPE, "too many rows or more than 2^20 heads");
+    const int64_t blocks = std::max(max_q, max_k) / 16 + 1;
+    if (batch > 0 && h > 0 && blocks > INT32_MAX / batch / h) return fail(ATTN_ERR_SHAPE, "too many work units");
+    const int rc = validate_dtype(dtype);
+    if (rc != ATTN_OK) return rc;
+    if (!std::isfinite(scale)) return fail(ATTN_ERR_SCALE, "scale is not finite");
+    if (!aligned(cu_q, 4) || !aligned(cu_k, 4)) return fail(ATTN_ERR_ALIGN, "cu_seqlens must be 4-byte aligned");
+    s->cu_q = cu_q, s->cu_k = cu_k;
+    s->batch = static_cast<int32_t>(batch), s->h = static_cast<int32_t>(h);
+    s->total_q = static_cast<int32_t>(total_q), s->total_k = static_cast<int32_t>(total_k);
+    s->max_q = static_cast<int32_t>(max_q), s->max_k = static_cast<int32_t>(max_k);
+    s->causal = causal != 0;
+    s->sl2e = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+    s->scale = scale;
+    s->timeout_ns = kDefaultTimeoutNs;
+    return ATTN_OK;
+}
+
+// Heads whose blocks are taken together: as many as fill the GPU.
+static int latent_group(int64_t h, int64_t blocks, int sm_count)
+{
+    return static_cast<int>(std::max<int64_t>(1, std::min(h, (sm_count + blocks - 1) / std::max<int64_t>(blocks, 1))));
+}
+
+int attn_fwd_latent(const void *q, const void *k_nope, const void *k_rope, const void *v, void *o, float *lse,
+                    const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, const int64_t *q_strides, const int64_t *k_nope_strides,
+                    int64_t k_rope_stride, const int64_t *v_strides, const int64_t *o_strides, int64_t batch, int64_t h,
+                    int64_t total_q, int64_t total_k, int64_t max_seqlen_q, int64_t max_seqlen_k, int causal, float scale, int dtype,
+                    void *stream)
+{
+    g_err.clear();
+    LatentFwdArgs a;
+    LatentFwdParams &p = a.p;
+    int rc = validate_latent_seqs(&p.s, cu_seqlens_q, cu_seqlens_k, batch, h, total_q, total_k, max_seqlen_q, max_seqlen_k, causal, scale,
+                                  dtype);
+    if (rc != ATTN_OK || batch * h * max_seqlen_q == 0) return rc;
+    if (!cu_seqlens_q || !cu_seqlens_k) return fail(ATTN_ERR_NULL, "cu_seqlens_q or cu_seqlens_k is NULL");
+    if (!q_strides || !k_nope_strides || !v_strides || !o_strides) return fail(ATTN_ERR_NULL, "strides are NULL");
+    const Rows rq{"q", q, total_q, h, kLatentKey, {q_strides[0], q_strides[1]}};
+    const Rows rk{"k_nope", k_nope, total_k, h, kLatentNope, {k_nope_strides[0], k_nope_strides[1]}};
+    const Rows rr{"k_rope", k_rope, total_k, 1, kLatentRope, {k_rope_stride, 0}};
+    const Rows rv{"v", v, total_k, h, kLatentValue, {v_strides[0], v_strides[1]}};
+    const Rows ro{"o", o, total_q, h, kLatentValue, {o_strides[0], o_strides[1]}};
+    for (const Rows *r : {&rq, &rk, &rr, &rv})
+        if ((rc = validate_rows(*r, false)) != ATTN_OK) return rc;
+    if ((rc = validate_rows(ro, true)) != ATTN_OK) return rc;
+    if (!aligned(lse, 4)) return fail(ATTN_ERR_ALIGN, "lse must be 4-byte aligned");
+    for (const Rows *r : {&rq, &rk, &rr, &rv})
+        if (r->tokens > 0 && overlap(r->extent(), ro.extent())) return fail(ATTN_ERR_SHAPE, "o overlaps %s", r->name);
+    DeviceInfo *di = nullptr;
+    if ((rc = device_info(&di)) != ATTN_OK) return rc;
+    if ((rc = make_map_rows(&a.q, rq, dtype, 128, q)) != ATTN_OK || (rc = make_map_rows(&a.k, rk, dtype, 128, q)) != ATTN_OK ||
+        (rc = make_map_rows(&a.r, rr, dtype, 128, q)) != ATTN_OK || (rc = make_map_rows(&a.v, rv, dtype, 128, q)) != ATTN_OK)
+        return rc;
+    p.s.status = di->status;
+    p.o = o;
+    p.ot = o_strides[0], p.oh = o_strides[1];
+    p.lse = lse;
+    p.blocks = static_cast<int32_t>((max_seqlen_q + 255) / 256);
+    p.group = latent_group(h, p.blocks, di->sm_count);
+    a.units = static_cast<unsigned>(batch * h * p.blocks);
+    a.stream = static_cast<cudaStream_t>(stream);
+    a.attr_ready = di->latent_fwd_attr;
+    const cudaError_t e = launch_latent_fwd(a, dtype == ATTN_BF16);
+    return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "kernel launch (latent forward)");
+}
+
+static int64_t latent_dsum_bytes(int64_t h, int64_t total_q) { return (h * total_q * 4 + 255) / 256 * 256; }
+
+int64_t attn_bwd_latent_workspace_bytes(int64_t h, int64_t total_q, int64_t total_k)
+{
+    g_err.clear();
+    if (h < 0 || h > (1 << 20) || total_q < 0 || total_q > kMaxSeq || total_k < 0 || total_k > kMaxSeq)
+        return fail(ATTN_ERR_SHAPE, "invalid workspace query of the latent backward");
+    return latent_dsum_bytes(h, total_q) + h * total_k * kLatentRope * 4;
+}
+
+int attn_bwd_latent(const void *q, const void *k_nope, const void *k_rope, const void *v, const void *o, const void *dout,
+                    const float *lse, void *dq, void *dk_nope, void *dk_rope, void *dv, const int32_t *cu_seqlens_q,
+                    const int32_t *cu_seqlens_k, const int64_t *strides, int64_t batch, int64_t h, int64_t total_q, int64_t total_k,
+                    int64_t max_seqlen_q, int64_t max_seqlen_k, int causal, float scale, int dtype, void *workspace,
+                    int64_t workspace_bytes, void *stream)
+{
+    g_err.clear();
+    LatentBwdArgs a;
+    LatentBwdParams &p = a.p;
+    int rc = validate_latent_seqs(&p.s, cu_seqlens_q, cu_seqlens_k, batch, h, total_q, total_k, max_seqlen_q, max_seqlen_k, causal, scale,
+                                  dtype);
+    if (rc != ATTN_OK || batch * h * (max_seqlen_q + max_seqlen_k) == 0) return rc;
+    if (!cu_seqlens_q || !cu_seqlens_k) return fail(ATTN_ERR_NULL, "cu_seqlens_q or cu_seqlens_k is NULL");
+    if (!strides) return fail(ATTN_ERR_NULL, "strides are NULL");
+    const auto rows = [&](const char *name, const void *t, int64_t tokens, int64_t heads, int64_t d, int i) {
+        return Rows{name, t, tokens, heads, d, {strides[2 * i], strides[2 * i + 1]}};
+    };
+    const Rows in[6] = {rows("q", q, total_q, h, kLatentKey, 0),         rows("k_nope", k_nope, total_k, h, kLatentNope, 1),
+                        rows("k_rope", k_rope, total_k, 1, kLatentRope, 2), rows("v", v, total_k, h, kLatentValue, 3),
+                        rows("o", o, total_q, h, kLatentValue, 4),       rows("dout", dout, total_q, h, kLatentValue, 5)};
+    const Rows out[4] = {rows("dq", dq, total_q, h, kLatentKey, 6), rows("dk_nope", dk_nope, total_k, h, kLatentNope, 7),
+                         rows("dk_rope", dk_rope, total_k, 1, kLatentRope, 8), rows("dv", dv, total_k, h, kLatentValue, 9)};
+    for (const Rows &r : in)
+        if ((rc = validate_rows(r, false)) != ATTN_OK) return rc;
+    for (const Rows &r : out)
+        if ((rc = validate_rows(r, true)) != ATTN_OK) return rc;
+    if (total_q > 0 && !lse) return fail(ATTN_ERR_NULL, "lse is NULL");
+    if (!aligned(lse, 4)) return fail(ATTN_ERR_ALIGN, "lse must be 4-byte aligned");
+    const int64_t dsum = latent_dsum_bytes(h, total_q), need = dsum + h * total_k * kLatentRope * 4;
+    if (!workspace) return fail(ATTN_ERR_NULL, "workspace is NULL (%lld bytes needed)", (long long)need);
+    if (!aligned(workspace, 16)) return fail(ATTN_ERR_ALIGN, "workspace must be 16-byte aligned");
+    if (workspace_bytes < need)
+        return fail(ATTN_ERR_SHAPE, "workspace too small: %lld bytes, need %lld", (long long)workspace_bytes, (long long)need);
+    for (int i = 0; i < 4; ++i) {
+        for (const Rows &r : in)
+            if (r.tokens > 0 && out[i].tokens > 0 && overlap(r.extent(), out[i].extent()))
+                return fail(ATTN_ERR_SHAPE, "%s overlaps %s", out[i].name, r.name);
+        for (int j = 0; j < i; ++j)
+            if ((rc = validate_rows_apart(out[i], out[j])) != ATTN_OK) return rc;
+    }
+    DeviceInfo *di = nullptr;
+    if ((rc = device_info(&di)) != ATTN_OK) return rc;
+    const std::pair<CUtensorMap *, std::pair<const Rows *, int>> maps[7] = {
+        {&a.q, {&in[0], 128}}, {&a.q_half, {&in[0], 64}}, {&a.dout, {&in[5], 128}}, {&a.dout_half, {&in[5], 64}},
+        {&a.k, {&in[1], 128}}, {&a.r, {&in[2], 128}},     {&a.v, {&in[3], 128}}};
+    for (const auto &m : maps)
+        if ((rc = make_map_rows(m.first, *m.second.first, dtype, m.second.second, workspace)) != ATTN_OK) return rc;
+    p.s.status = di->status;
+    p.o = o, p.dout = dout;
+    p.ot = in[4].st[0], p.oh = in[4].st[1], p.gt = in[5].st[0], p.gh = in[5].st[1];
+    p.lse = lse;
+    p.dsum = static_cast<float *>(workspace);
+    p.kr_part = reinterpret_cast<float *>(static_cast<char *>(workspace) + dsum);
+    p.dq = dq, p.dkn = dk_nope, p.dkr = dk_rope, p.dv = dv;
+    p.dqt = out[0].st[0], p.dqh = out[0].st[1];
+    p.dknt = out[1].st[0], p.dknh = out[1].st[1];
+    p.dkrt = out[2].st[0];
+    p.dvt = out[3].st[0], p.dvh = out[3].st[1];
+    p.q_blocks = static_cast<int32_t>((max_seqlen_q + 127) / 128);
+    p.k_blocks = static_cast<int32_t>((max_seqlen_k + 127) / 128);
+    p.group = latent_group(h, std::max(p.q_blocks, p.k_blocks), di->sm_count);
+    a.stream = static_cast<cudaStream_t>(stream);
+    a.attr_ready = di->latent_bwd_attr;
+    const cudaError_t e = launch_latent_bwd(a, dtype == ATTN_BF16);
+    return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "kernel launch (latent backward)");
 }
 
 const char *attn_last_error(void) { return g_err.c_str(); }

@@ -81,4 +81,69 @@ struct LatentPagedArgs {
 
 cudaError_t launch_latent_paged(const LatentPagedArgs &a, bool bf16);
 
+// ---------------------------------------------------------------- expanded form
+
+constexpr int kLatentNope = 128, kLatentKey = kLatentNope + kLatentRope, kLatentValue = 128;
+
+// Packed sequences: queries [total_q, h, 192], keys [total_k, h, 128] and
+// [total_k, 64], values [total_k, h, 128]; the tensors by strides.
+struct LatentSeqs {
+    const int32_t *cu_q, *cu_k;  // [batch + 1]
+    int32_t batch, h;
+    int32_t total_q, total_k;
+    int32_t max_q, max_k;
+    int32_t causal;
+    float sl2e;                  // scale * log2(e)
+    float scale;
+    uint32_t *status;
+    uint64_t timeout_ns;
+};
+
+struct LatentFwdParams {
+    LatentSeqs s;
+    void *o;                     // [total_q, h, 128] by strides (elements)
+    int64_t ot, oh;              // of a token, of a head
+    float *lse;                  // [h, total_q] or nullptr
+    int32_t blocks;              // ceil(max_q / 256)
+    int32_t group;               // heads whose units are taken together
+};
+
+struct LatentFwdArgs {
+    CUtensorMap q, k, r, v;
+    LatentFwdParams p;
+    unsigned units;
+    cudaStream_t stream;
+    std::atomic<int> *attr_ready;
+};
+
+constexpr int kLatentFwdInstances = 4;  // {fp16, bf16} x {causal, not}
+
+cudaError_t launch_latent_fwd(const LatentFwdArgs &a, bool bf16);
+
+struct LatentBwdParams {
+    LatentSeqs s;
+    const void *o, *dout;        // [total_q, h, 128] by strides (elements)
+    int64_t ot, oh, gt, gh;
+    const float *lse;            // [h, total_q]
+    float *dsum;                 // [h, total_q]: sum over a row of dO * O
+    float *kr_part;              // [h, total_k, 64]: each head's gradient of the shared key part
+    void *dq, *dkn, *dkr, *dv;   // by strides of a token and of a head
+    int64_t dqt, dqh, dknt, dknh, dkrt, dvt, dvh;
+    int32_t q_blocks, k_blocks;  // ceil(max_q / 128), ceil(max_k / 128)
+    int32_t group;               // heads whose units are taken together
+};
+
+struct LatentBwdArgs {
+    CUtensorMap q, dout;         // 128 rows a copy
+    CUtensorMap q_half, dout_half;  // 64 rows a copy
+    CUtensorMap k, r, v;
+    LatentBwdParams p;
+    cudaStream_t stream;
+    std::atomic<int> *attr_ready;
+};
+
+constexpr int kLatentBwdInstances = 8;  // {keys, queries} x {fp16, bf16} x {causal, not}
+
+cudaError_t launch_latent_bwd(const LatentBwdArgs &a, bool bf16);
+
 }  // namespace attn

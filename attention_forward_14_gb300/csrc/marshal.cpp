@@ -41,6 +41,9 @@ struct Library {
     decltype(&attn_latent_append_paged) latent_append_paged;
     decltype(&attn_fwd_latent_paged) fwd_latent_paged;
     decltype(&attn_fwd_latent_paged_workspace_bytes) fwd_latent_paged_workspace_bytes;
+    decltype(&attn_fwd_latent) fwd_latent;
+    decltype(&attn_bwd_latent) bwd_latent;
+    decltype(&attn_bwd_latent_workspace_bytes) bwd_latent_workspace_bytes;
 } g_lib;
 
 struct Err {
@@ -568,6 +571,127 @@ PyObject *fwd_latent_paged(PyObject *const *a)
     return Py_BuildValue("(NN)", object(a[7], o), object(a[8], lse));
 }
 
+// A packed tensor of the expanded form, [tokens, heads, d], or [tokens, d] of
+// one that all heads share: strides of a token and of a head.
+struct PackedRows {
+    int64_t tokens, heads;
+    int64_t st[2];
+};
+
+PackedRows packed_rows(const char *name, const at::Tensor &t, int64_t tokens, int64_t heads, int64_t d, const at::Tensor &like)
+{
+    const bool one = heads == 0;  // no axis of heads
+    if (t.dim() != (one ? 2 : 3) || t.size(0) != tokens || (!one && t.size(1) != heads) || t.size(-1) != d)
+        fail(ATTN_ERR_SHAPE, std::string(name) + " " + shape_of(t) + " must be [" + std::to_string(tokens) + ", " +
+                                 (one ? "" : std::to_string(heads) + ", ") + std::to_string(d) + "]");
+    if (t.scalar_type() != like.scalar_type() || t.device() != like.device())
+        fail(ATTN_ERR_DTYPE, std::string(name) + " must be of q's dtype, on its device");
+    if (t.numel() > 0 && t.stride(-1) != 1) fail(ATTN_ERR_SHAPE, std::string("the values of a row of ") + name + " must be contiguous");
+    return {tokens, one ? 1 : heads, {t.stride(0), one ? 0 : t.stride(1)}};
+}
+
+struct LatentInputs {
+    const at::Tensor &q, &kn, &kr, &v, &cq, &ck;
+    int64_t tq, tk, h, batch, max_q, max_k;
+    PackedRows rq, rkn, rkr, rv;
+    int dtype, causal;
+    float scale;
+};
+
+int64_t whole(PyObject *o, const char *name)
+{
+    const long long v = PyLong_AsLongLong(o);
+    if (v == -1 && PyErr_Occurred()) {
+        PyErr_Clear();
+        fail(ATTN_ERR_SHAPE, std::string(name) + " must be a whole number");
+    }
+    return v;
+}
+
+// q, k_nope, k_rope, v at a[0..3]; cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, causal, scale at b[0..5]
+LatentInputs latent_inputs(PyObject *const *a, PyObject *const *b)
+{
+    LatentInputs r{tensor(a[0], "q"), tensor(a[1], "k_nope"), tensor(a[2], "k_rope"), tensor(a[3], "v"),
+                   tensor(b[0], "cu_seqlens_q"), tensor(b[1], "cu_seqlens_k"), 0, 0, 0, 0, 0, 0, {}, {}, {}, {}, 0, 0, 0.f};
+    r.dtype = dtype_code(r.q);
+    if (r.q.dim() != 3 || r.kn.dim() != 3) fail(ATTN_ERR_SHAPE, "q must be [total_q, h, 192] and k_nope [total_k, h, 128]");
+    if (!r.q.is_cuda()) fail(ATTN_ERR_SHAPE, "q must be a CUDA tensor");
+    r.tq = r.q.size(0), r.tk = r.kn.size(0), r.h = r.q.size(1);
+    if (r.h == 0) fail(ATTN_ERR_SHAPE, "q has no heads");
+    r.rq = packed_rows("q", r.q, r.tq, r.h, 192, r.q);
+    r.rkn = packed_rows("k_nope", r.kn, r.tk, r.h, 128, r.q);
+    r.rkr = packed_rows("k_rope", r.kr, r.tk, 0, 64, r.q);
+    r.rv = packed_rows("v", r.v, r.tk, r.h, 128, r.q);
+    for (const at::Tensor *t : {&r.cq, &r.ck})
+        if (t->dim() != 1 || t->size(0) < 1 || t->size(0) != r.cq.size(0) || t->scalar_type() != at::kInt || t->device() != r.q.device() ||
+            !t->is_contiguous())
+            fail(ATTN_ERR_DTYPE, "cu_seqlens must be contiguous int32 tensors of batch + 1 elements on q's device");
+    r.batch = r.cq.size(0) - 1;
+    r.max_q = whole(b[2], "max_seqlen_q");
+    r.max_k = whole(b[3], "max_seqlen_k");
+    r.causal = truth(b[4]);
+    r.scale = static_cast<float>(b[5] == Py_None ? 1.0 / std::sqrt(192.0) : number(b[5], "scale"));
+    return r;
+}
+
+PyObject *fwd_latent(PyObject *const *a)
+{
+    // q, k_nope, k_rope, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, causal, scale, o, lse, stream
+    const LatentInputs in = latent_inputs(a, a + 4);
+    const at::Tensor *go = maybe(a[10], "o"), *glse = maybe(a[11], "lse");
+    const Call call(in.q, a[12]);
+    at::Tensor o, lse;
+    {
+        const WithoutLock unlocked;
+        o = go ? *go : call.empty({in.tq, in.h, 128}, in.q.scalar_type());
+        const PackedRows ro = packed_rows("o", o, in.tq, in.h, 128, in.q);
+        lse = glse ? *glse : call.empty({in.h, in.tq}, at::kFloat);
+        if (lse.sizes() != at::IntArrayRef({in.h, in.tq}) || lse.scalar_type() != at::kFloat || !lse.is_contiguous() ||
+            lse.device() != in.q.device())
+            fail(ATTN_ERR_SHAPE, "lse must be contiguous fp32 [h, total_q] on q's device");
+        check(g_lib.fwd_latent(ptr(in.q), ptr(in.kn), ptr(in.kr), ptr(in.v), ptr(o), lse.data_ptr<float>(),
+                               static_cast<const int32_t *>(ptr(in.cq)), static_cast<const int32_t *>(ptr(in.ck)), in.rq.st, in.rkn.st,
+                               in.rkr.st[0], in.rv.st, ro.st, in.batch, in.h, in.tq, in.tk, in.max_q, in.max_k, in.causal, in.scale,
+                               in.dtype, call.stream()));
+    }
+    return Py_BuildValue("(NN)", object(a[10], o), object(a[11], lse));
+}
+
+PyObject *bwd_latent(PyObject *const *a)
+{
+    // q, k_nope, k_rope, v, o, dout, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, causal, scale, dq, dk_nope,
+    // dk_rope, dv, workspace, stream
+    const LatentInputs in = latent_inputs(a, a + 7);
+    const at::Tensor &o = tensor(a[4], "o"), &dout = tensor(a[5], "dout"), &lse = tensor(a[6], "lse");
+    const PackedRows ro = packed_rows("o", o, in.tq, in.h, 128, in.q), rg = packed_rows("dout", dout, in.tq, in.h, 128, in.q);
+    if (lse.sizes() != at::IntArrayRef({in.h, in.tq}) || lse.scalar_type() != at::kFloat || !lse.is_contiguous() ||
+        lse.device() != in.q.device())
+        fail(ATTN_ERR_SHAPE, "lse must be contiguous fp32 [h, total_q] on q's device");
+    const at::Tensor *given[4] = {maybe(a[13], "dq"), maybe(a[14], "dk_nope"), maybe(a[15], "dk_rope"), maybe(a[16], "dv")};
+    const at::Tensor *gws = maybe(a[17], "workspace");
+    const Call call(in.q, a[18]);
+    at::Tensor out[4];
+    {
+        const WithoutLock unlocked;
+        const char *names[4] = {"dq", "dk_nope", "dk_rope", "dv"};
+        const at::Tensor *like[4] = {&in.q, &in.kn, &in.kr, &in.v};
+        PackedRows r[4];
+        for (int i = 0; i < 4; ++i) {
+            out[i] = given[i] ? *given[i] : call.empty(like[i]->sizes(), in.q.scalar_type());
+            r[i] = packed_rows(names[i], out[i], like[i]->size(0), i == 2 ? 0 : in.h, like[i]->size(-1), in.q);
+        }
+        const PackedRows *all[10] = {&in.rq, &in.rkn, &in.rkr, &in.rv, &ro, &rg, &r[0], &r[1], &r[2], &r[3]};
+        int64_t st[20];
+        for (int i = 0; i < 10; ++i) st[2 * i] = all[i]->st[0], st[2 * i + 1] = all[i]->st[1];
+        const Workspace ws = workspace(call, gws, g_lib.bwd_latent_workspace_bytes(in.h, in.tq, in.tk), in.q.device());
+        check(g_lib.bwd_latent(ptr(in.q), ptr(in.kn), ptr(in.kr), ptr(in.v), ptr(o), ptr(dout), lse.data_ptr<float>(), ptr(out[0]),
+                               ptr(out[1]), ptr(out[2]), ptr(out[3]), static_cast<const int32_t *>(ptr(in.cq)),
+                               static_cast<const int32_t *>(ptr(in.ck)), st, in.batch, in.h, in.tq, in.tk, in.max_q, in.max_k, in.causal,
+                               in.scale, in.dtype, ws.p, ws.bytes, call.stream()));
+    }
+    return Py_BuildValue("(NNNN)", object(a[13], out[0]), object(a[14], out[1]), object(a[15], out[2]), object(a[16], out[3]));
+}
+
 // Runs a function on its positional arguments; what it throws becomes a
 // Python exception.
 template <PyObject *(*F)(PyObject *const *), int N>
@@ -618,7 +742,9 @@ PyMethodDef g_methods[] = {
     method<fwd_kvcache_paged_fp8, 13>("fwd_kvcache_paged_fp8"),
     method<latent_append_paged, 11>("latent_append_paged"),
     method<fwd_latent_paged, 11>("fwd_latent_paged"),
-    method<bind, 11>("bind"),
+    method<fwd_latent, 13>("fwd_latent"),
+    method<bwd_latent, 19>("bwd_latent"),
+    method<bind, 14>("bind"),
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -690,6 +690,76 @@ int attn_fwd_latent_paged(const void *q, const void *pool,
 /* Bytes of workspace attn_fwd_latent_paged needs, or a negative code. */
 int64_t attn_fwd_latent_paged_workspace_bytes(int64_t b, int64_t h, int64_t sq);
 
+/*
+ * Latent attention, expanded form, over packed sequences: prompts and
+ * training.  For head n, with keys K = [k_nope of the head | k_rope of all]:
+ *   O = softmax(scale * (q[.., 0..127] k_nope^T + q[.., 128..191] k_rope^T)
+ *               [+ causal mask]) V
+ * for every sequence of the batch, as attn_fwd_varlen has them (cu_seqlens_q
+ * and _k, max_seqlen_q and _k, the mask bottom-right aligned; a sequence whose
+ * offsets fall outside the totals is skipped).
+ *   q            : [total_q, h, 192] of dtype; strides {token, head} in
+ *                  elements (positive multiples of 8), 16-byte aligned.
+ *   k_nope, v    : [total_k, h, 128], the same; both can be views of one
+ *                  projection's output.
+ *   k_rope       : [total_k, 64]; k_rope_stride of a token.
+ *   o            : [total_q, h, 128] by strides; its rows must not coincide,
+ *                  nor overlap an input.
+ *   lse          : fp32 [h, total_q], or NULL.
+ * A row that sees no key gets O = 0 and LSE = -inf; what lies behind a
+ * sequence's end does not reach it.  fp32 accumulation and statistics; P is
+ * rounded to dtype before its product, and O divided by the sum of P as
+ * rounded.  Asynchronous on `stream`.
+ * Returns ATTN_OK or a negative ATTN_ERR_* code.
+ */
+int attn_fwd_latent(const void *q, const void *k_nope, const void *k_rope,
+                    const void *v, void *o, float *lse,
+                    const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                    const int64_t *q_strides, const int64_t *k_nope_strides,
+                    int64_t k_rope_stride, const int64_t *v_strides,
+                    const int64_t *o_strides, int64_t batch, int64_t h,
+                    int64_t total_q, int64_t total_k, int64_t max_seqlen_q,
+                    int64_t max_seqlen_k, int causal, float scale, int dtype,
+                    void *stream);
+
+/*
+ * Gradients of attn_fwd_latent for the gradient dout of its output:
+ *   P  = exp(scale * S - lse),  dS = P * (dout V^T - rowsum(dout * o))
+ *   dq = scale * dS [k_nope | k_rope],     dv = P^T dout
+ *   dk_nope = scale * dS^T q[.., 0..127]
+ *   dk_rope = scale * sum over heads of dS^T q[.., 128..191]
+ *   o, lse       : the forward's outputs for these inputs.
+ *   dq, dk_nope, dk_rope, dv : shaped like q, k_nope, k_rope, v.  An output's
+ *                  rows must not coincide, nor overlap an input's or another
+ *                  output's (dk_nope and dv may be the two parts of one
+ *                  [total_k, h, 256] tensor).
+ *   strides      : {token, head} of q, k_nope, k_rope, v, o, dout, dq,
+ *                  dk_nope, dk_rope, dv, in this order (20 values, positive
+ *                  multiples of 8 elements; k_rope and dk_rope have one head).
+ *   workspace    : caller-owned device scratch, 16-byte aligned, of at least
+ *                  attn_bwd_latent_workspace_bytes(h, total_q, total_k) bytes
+ *                  (a value for each row, and in fp32 each head's part of
+ *                  dk_rope); its contents on entry do not matter.  Calls on
+ *                  different streams need different workspaces.
+ * The outputs of every sequence are written in full (zeros where a gradient
+ * is zero).  All sums are added in a fixed order: equal calls give equal bits.
+ * P and dS are rounded to dtype before their products.
+ * Returns ATTN_OK or a negative ATTN_ERR_* code.
+ */
+int attn_bwd_latent(const void *q, const void *k_nope, const void *k_rope,
+                    const void *v, const void *o, const void *dout,
+                    const float *lse, void *dq, void *dk_nope, void *dk_rope,
+                    void *dv, const int32_t *cu_seqlens_q,
+                    const int32_t *cu_seqlens_k, const int64_t *strides,
+                    int64_t batch, int64_t h, int64_t total_q,
+                    int64_t total_k, int64_t max_seqlen_q,
+                    int64_t max_seqlen_k, int causal, float scale, int dtype,
+                    void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace attn_bwd_latent needs, or a negative code. */
+int64_t attn_bwd_latent_workspace_bytes(int64_t h, int64_t total_q,
+                                        int64_t total_k);
+
 /* Thread-local message describing the last non-OK return on this thread
  * ("" if none).  The pointer stays valid until the next call on the thread. */
 const char *attn_last_error(void);

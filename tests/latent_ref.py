@@ -134,3 +134,72 @@ def cache(b, page, pages, dtype, seed, spare=2):
     pool = torch.randn((n, page, TOKEN), generator=g).to(dtype)
     table = torch.randperm(n, generator=g)[:b * pages].reshape(b, pages).to(torch.int32)
     return pool, table
+
+
+# ------------------------------------------------------------------ expanded form
+
+NOPE, KEY, VALUE = 128, 192, 128
+
+
+def causal_seen(n, m, causal):
+    return np.ones((n, m), dtype=bool) if not causal else np.arange(m) <= np.arange(n)[:, None] + m - n
+
+
+def sequences(cu_q, cu_k):
+    for a, b, c, d in zip(cu_q[:-1], cu_q[1:], cu_k[:-1], cu_k[1:]):
+        yield slice(int(a), int(b)), slice(int(c), int(d))
+
+
+def expanded(q, kn, kr, v, cu_q, cu_k, causal, scale):
+    """(O [t, h, 128], LSE [h, t], sum of P |v|, largest scale sum |q k| [h, t])."""
+    o, a = np.zeros((*q.shape[:2], VALUE)), np.zeros((*q.shape[:2], VALUE))
+    lse, size = np.full((q.shape[1], q.shape[0]), -np.inf), np.zeros((q.shape[1], q.shape[0]))
+    for qs, ks in sequences(cu_q, cu_k):
+        seen = causal_seen(qs.stop - qs.start, ks.stop - ks.start, causal)
+        if seen.size == 0:
+            continue
+        for i in range(q.shape[1]):
+            k = np.concatenate([kn[ks, i], kr[ks]], 1)
+            o[qs, i], lse[i, qs], a[qs, i], size[i, qs] = attend(q[qs, i], k, v[ks, i], seen, scale)
+    return o, lse, a, size
+
+
+def expanded_grads(q, kn, kr, v, g, cu_q, cu_k, causal, scale, half, o_error):
+    """The gradients by the formula, each with a bound of its error for o off by o_error: {name: (value, bound)}.
+
+    P is off by twice a score's error (its own and LSE's) and rounded; dP by its sums in fp32; D by what o is off; dS by
+    all of these and its rounding; sums over queries or keys by 2^-15 of the sums of magnitudes; then the output's
+    rounding."""
+    names = dict(dq=q, dk_nope=kn, dk_rope=kr, dv=v)
+    val, err = ({n: np.zeros(x.shape) for n, x in names.items()} for _ in range(2))
+    for qs, ks in sequences(cu_q, cu_k):
+        seen = causal_seen(qs.stop - qs.start, ks.stop - ks.start, causal)
+        if seen.size == 0:
+            continue
+        for i in range(q.shape[1]):
+            qi, vi, gi = q[qs, i], v[ks, i], g[qs, i]
+            k = np.concatenate([kn[ks, i], kr[ks]], 1)
+            s = scale * (qi @ k.T)
+            s[~seen] = -np.inf
+            some = seen.any(1)
+            m = np.where(some, s.max(1, initial=-np.inf), 0.0)
+            p = np.exp(s - m[:, None])
+            p /= np.where(some, p.sum(1), 1.0)[:, None]
+            dp = gi @ vi.T
+            d = (p * dp).sum(1, keepdims=True)
+            ds = p * (dp - d)
+            size = abs(scale) * np.where(seen, np.abs(qi) @ np.abs(k).T, 0.0).max(1, initial=0.0)
+            ep = 2 * score_error(size, 12)[:, None]
+            edp = 24 * 2.0 ** -23 * (np.abs(gi) @ np.abs(vi).T)
+            ed = (np.abs(gi) * o_error[qs, i]).sum(1, keepdims=True) + 2.0 ** -20 * (np.abs(gi) @ np.abs(vi).T * p).sum(1, keepdims=True)
+            eds = p * (ep * np.abs(dp - d) + edp + ed) + half * np.abs(ds) + 2.0 ** -15 * np.abs(ds)
+            val["dv"][ks, i] = p.T @ gi
+            err["dv"][ks, i] = ((half + ep + 2.0 ** -15) * p).T @ np.abs(gi)
+            val["dq"][qs, i] = scale * ds @ k
+            err["dq"][qs, i] = abs(scale) * eds @ np.abs(k)
+            dk, ek = scale * ds.T @ qi, abs(scale) * eds.T @ np.abs(qi)
+            val["dk_nope"][ks, i], err["dk_nope"][ks, i] = dk[:, :NOPE], ek[:, :NOPE]
+            val["dk_rope"][ks] += dk[:, NOPE:]
+            err["dk_rope"][ks] += ek[:, NOPE:]
+    # (fp16's smallest step, for a P or dS below its smallest normal: half of 2^-24 for each key or query)
+    return {n: (val[n], err[n] + half * np.abs(val[n]) + 2.0 ** -25 * 64) for n in names}
