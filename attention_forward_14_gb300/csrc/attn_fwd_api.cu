@@ -1959,11 +1959,10 @@ int attn_bwd_latent(const void *q, const void *k_nope, const void *k_rope, const
     }
     DeviceInfo *di = nullptr;
     if ((rc = device_info(&di)) != ATTN_OK) return rc;
-    const std::pair<CUtensorMap *, std::pair<const Rows *, int>> maps[7] = {
-        {&a.q, {&in[0], 128}}, {&a.q_half, {&in[0], 64}}, {&a.dout, {&in[5], 128}}, {&a.dout_half, {&in[5], 64}},
-        {&a.k, {&in[1], 128}}, {&a.r, {&in[2], 128}},     {&a.v, {&in[3], 128}}};
-    for (const auto &m : maps)
-        if ((rc = make_map_rows(m.first, *m.second.first, dtype, m.second.second, workspace)) != ATTN_OK) return rc;
+    CUtensorMap *maps[5][2] = {{&a.q, &a.q_half}, {&a.k, &a.k_half}, {&a.r, &a.r_half}, {&a.v, &a.v_half}, {&a.dout, &a.dout_half}};
+    for (int i = 0; i < 5; ++i)
+        for (int half = 0; half < 2; ++half)
+            if ((rc = make_map_rows(maps[i][half], in[i < 4 ? i : 5], dtype, half ? 64 : 128, workspace)) != ATTN_OK) return rc;
     p.s.status = di->status;
     p.o = o, p.dout = dout;
     p.ot = in[4].st[0], p.oh = in[4].st[1], p.gt = in[5].st[0], p.gh = in[5].st[1];

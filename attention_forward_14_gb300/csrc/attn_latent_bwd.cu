@@ -92,21 +92,34 @@ __device__ __forceinline__ void store_piece(uint32_t taddr, float f, uint32_t pa
     __syncwarp();
 }
 
+// Row `row` of a panel of 64 values to 32 columns of this thread's lane.
+__device__ __forceinline__ void move_panel_row(uint32_t panel, int row, uint32_t taddr)
+{
+    uint32_t v[32];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint4 x = ld_shared_u4(panel + row * 128 + ((e ^ (row & 7)) << 4));
+        v[4 * e] = x.x, v[4 * e + 1] = x.y, v[4 * e + 2] = x.z, v[4 * e + 3] = x.w;
+    }
+    tmem_st32(taddr, v);
+}
+
 // ---------------------------------------------------------------- dK, dV
 
 constexpr int kKeys = 128, kQueries = 64;  // of a unit, of a tile
 struct KeysCfg {
     static constexpr int HALF = kQueries * 128;           // a panel of a tile of queries
     static constexpr int STAGE = 5 * HALF, STAGES = 3;    // Q (3 panels), dO (2)
-    static constexpr int LD_OFF = 1024;                   // of each stage: LSE in log2 [64], D [64]
+    static constexpr int LD_OFF = 1024;                   // of each stage: -LSE in log2 [64], -D [64]
     static constexpr int K_OFF = 4096, V_OFF = K_OFF + 3 * kPanel, Q_OFF = V_OFF + 2 * kPanel;
     static constexpr int SMEM = Q_OFF + STAGES * STAGE + 1024;
-    static constexpr int TM_DV = 0, TM_DK = 128, TM_S = 320, TM_DP = 384, TM_P = 448, TM_DS = 480;
+    // P^T and dS^T take the place of S^T and dP^T, each half of the queries that of its own scores
+    static constexpr int TM_DV = 0, TM_DK = 128, TM_S = 320, TM_DP = 384, TM_V = 448;
     static_assert(SMEM <= 232448 && LD_OFF + STAGES * 512 <= K_OFF, "shared memory budget");
 };
 
 struct KeysCtl {
-    uint64_t kv_full, full[3], empty[3], ld_full[3];
+    uint64_t v_full, k_full, v_moved, full[3], empty[3], ld_full[3];
     uint64_t s_full, dp_full, p_full, ds_full, acc_full;
     uint32_t tmem_base, abort;
 };
@@ -154,7 +167,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const BoundedWaits waits{&ctl->abort, p.s.status, p.s.timeout_ns};
     if (threadIdx.x == 0) {
-        mbar_init(B(ctl->kv_full), 1);
+        mbar_init(B(ctl->v_full), 1);
+        mbar_init(B(ctl->k_full), 1);
+        mbar_init(B(ctl->v_moved), 8);
         for (int i = 0; i < C::STAGES; ++i) {
             mbar_init(B(ctl->full[i]), 1);
             mbar_init(B(ctl->empty[i]), 1);
@@ -183,12 +198,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             // -------------------------------------------------------- copies
             const uint64_t pol = l2_evict_normal();
             if (elect_one()) {
-                const uint32_t bar = B(ctl->kv_full);
-                mbar_arrive_expect_tx(bar, 5 * kPanel);
+                uint32_t bar = B(ctl->v_full);
+                mbar_arrive_expect_tx(bar, 2 * kPanel);
+                for (int pn = 0; pn < 2; ++pn) tma_load_3d(base + C::V_OFF + pn * kPanel, &tmV, bar, pn * 64, un.head, un.k0 + key0, pol);
+                bar = B(ctl->k_full);
+                mbar_arrive_expect_tx(bar, 3 * kPanel);
                 tma_load_3d(base + C::K_OFF, &tmK, bar, 0, un.head, un.k0 + key0, pol);
                 tma_load_3d(base + C::K_OFF + kPanel, &tmK, bar, 64, un.head, un.k0 + key0, pol);
                 tma_load_3d(base + C::K_OFF + 2 * kPanel, &tmR, bar, 0, 0, un.k0 + key0, pol);
-                for (int pn = 0; pn < 2; ++pn) tma_load_3d(base + C::V_OFF + pn * kPanel, &tmV, bar, pn * 64, un.head, un.k0 + key0, pol);
             }
             __syncwarp();
             int i = 0;
@@ -205,7 +222,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // wait (bounded) for the last copies, so that none lands after the CTA
             for (int k = max(i - C::STAGES, 0); k < i; ++k) drain_wait(B(ctl->full[k % C::STAGES]), (k / C::STAGES) & 1u, p.s.timeout_ns);
-            drain_wait(B(ctl->kv_full), 0u, p.s.timeout_ns);
+            drain_wait(B(ctl->v_full), 0u, p.s.timeout_ns);
+            drain_wait(B(ctl->k_full), 0u, p.s.timeout_ns);
         } else if (warp == 10) {
             // -------------------------------------------------------- LSE and D of a tile's queries
             const int64_t row0 = static_cast<int64_t>(un.head) * p.s.total_q + un.q0;
@@ -216,15 +234,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int q = (first + i) * kQueries + h * 32 + lane;
-                    to[h * 32 + lane] = q < un.sq ? lse_log2(p.lse[row0 + q]) : INFINITY;
-                    to[64 + h * 32 + lane] = q < un.sq ? p.dsum[row0 + q] : 0.f;
+                    to[h * 32 + lane] = q < un.sq ? -lse_log2(p.lse[row0 + q]) : -INFINITY;
+                    to[64 + h * 32 + lane] = q < un.sq ? -p.dsum[row0 + q] : 0.f;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(B(ctl->ld_full[st]));
             }
         } else if (warp == 8) {
             // -------------------------------------------------------- products
-            const uint32_t dk = desc_lo(base + C::K_OFF, 16), dv = desc_lo(base + C::V_OFF, 16);
+            const uint32_t dk = desc_lo(base + C::K_OFF, 16);
             const uint32_t dq_k = desc_lo(base + C::Q_OFF, 16), dq_mn = desc_lo(base + C::Q_OFF, C::HALF);
             auto stage_there = [&](int i) {
                 const uint32_t st = i % C::STAGES;
@@ -246,16 +264,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto issue_dp = [&](uint32_t st) {
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    mma_ss(tmem + C::TM_DP, dv + (((kk / 4) * kPanel + (kk % 4) * 32) >> 4),
+                    mma_ts(tmem + C::TM_DP, tmem + C::TM_V + kk * 8,
                            dq_k + ((st * C::STAGE + (3 + kk / 4) * C::HALF + (kk % 4) * 32) >> 4), IDESC_S, kk > 0 ? 1u : 0u);
                 tc_commit(B(ctl->dp_full));
             };
-            bool ok = waits.warp(B(ctl->kv_full), 0u, SITE_LB_KV) && stage_there(0);
+            // k-step kk of a tile's queries, 16 of them, in P^T or dS^T: 32 queries to each half
+            auto at_step = [](int kk) { return (kk / 2) * 32 + (kk % 2) * 8; };
+            bool ok = waits.warp(B(ctl->k_full), 0u, SITE_LB_KV) && stage_there(0);
             if (ok) {
-                if (elect_one()) {
-                    issue_s(0u);
-                    issue_dp(0u);
-                }
+                if (elect_one()) issue_s(0u);
+                __syncwarp();
+                ok = waits.warp(B(ctl->v_moved), 0u, SITE_LB_KV);
+                tc_fence_after();
+                if (ok && elect_one()) issue_dp(0u);
                 __syncwarp();
             }
             for (int i = 0; ok && i < n; ++i) {
@@ -267,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)  // 16 queries a step
-                        mma_ts(tmem + C::TM_DV, tmem + C::TM_P + kk * 8, dq_mn + ((st * C::STAGE + 3 * C::HALF + kk * 2048) >> 4), IDESC_DV,
+                        mma_ts(tmem + C::TM_DV, tmem + C::TM_S + at_step(kk), dq_mn + ((st * C::STAGE + 3 * C::HALF + kk * 2048) >> 4), IDESC_DV,
                                (i > 0 || kk > 0) ? 1u : 0u);
                     if (more) issue_s(next);
                 }
@@ -277,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_ts(tmem + C::TM_DK, tmem + C::TM_DS + kk * 8, dq_mn + ((st * C::STAGE + kk * 2048) >> 4), IDESC_DK,
+                        mma_ts(tmem + C::TM_DK, tmem + C::TM_DP + at_step(kk), dq_mn + ((st * C::STAGE + kk * 2048) >> 4), IDESC_DK,
                                (i > 0 || kk > 0) ? 1u : 0u);
                     tc_commit(B(ctl->empty[st]));
                     if (more) issue_dp(next);
@@ -295,57 +316,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         regs_inc<kSoftmaxRegs>();
         const int w = warp >> 2, in_unit = (warp & 3) * 32 + lane, key = key0 + in_unit;
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16, at = tmem + lane_off;
-        bool ok = true;
-        for (int i = 0; i < n; ++i) {
+        // the keys' values as an operand in tensor memory, half of them by each group
+        bool ok = waits.warp(B(ctl->v_full), 0u, SITE_LB_KV);
+        if (ok) {
+            move_panel_row(base + C::V_OFF + w * kPanel, in_unit, at + C::TM_V + w * 32);
+            warp_announce_tmem(B(ctl->v_moved));
+        }
+        for (int i = 0; ok && i < n; ++i) {
             const uint32_t st = i % C::STAGES;
             const float *ld = reinterpret_cast<const float *>(smem + C::LD_OFF + st * 512) + w * 32;
             const int q0 = (first + i) * kQueries + w * 32;
             ok = waits.warp(B(ctl->ld_full[st]), (i / C::STAGES) & 1u, SITE_LB_LD) && waits.warp(B(ctl->s_full), i & 1u, SITE_LB_S);
             if (!ok) break;
             tc_fence_after();
-            uint32_t s[32];
-            tmem_ld32_wait(at + C::TM_S + w * 32, s);
-            float pr[32];
-#pragma unroll
-            for (int c = 0; c < 32; c += 4) {
-                const float4 lse = *reinterpret_cast<const float4 *>(ld + c);
-                pr[c] = ex2_approx(fmaf(__uint_as_float(s[c]), p.s.sl2e, -lse.x));
-                pr[c + 1] = ex2_approx(fmaf(__uint_as_float(s[c + 1]), p.s.sl2e, -lse.y));
-                pr[c + 2] = ex2_approx(fmaf(__uint_as_float(s[c + 2]), p.s.sl2e, -lse.z));
-                pr[c + 3] = ex2_approx(fmaf(__uint_as_float(s[c + 3]), p.s.sl2e, -lse.w));
-            }
             // queries [lo, hi) of the 32 see this key
             const int lo = CAUSAL ? key - off - q0 : 0, hi = un.sq - q0;
-            const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < 32);
-            if (masked) {
+            // (two instances: of one, the compiler makes selects that every tile pays for, a third of the instructions)
+            auto tile = [&](auto masked) __attribute__((always_inline)) {
+                constexpr bool MASKED = decltype(masked)::value;
+                const float2 scale2 = make_float2(p.s.sl2e, p.s.sl2e);
+                float2 pr[16];
+                uint32_t s[32], pk[16];
+                tmem_ld32_wait(at + C::TM_S + w * 32, s);
 #pragma unroll
-                for (int c = 0; c < 32; ++c) pr[c] = c >= lo && c < hi ? pr[c] : 0.f;
-            }
-            uint32_t pk[16];
+                for (int c = 0; c < 16; ++c) {
+                    const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), scale2,
+                                                reinterpret_cast<const float2 *>(ld)[c]);
+                    pr[c] = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                    if constexpr (MASKED) {
+                        pr[c].x = 2 * c >= lo && 2 * c < hi ? pr[c].x : 0.f;
+                        pr[c].y = 2 * c + 1 >= lo && 2 * c + 1 < hi ? pr[c].y : 0.f;
+                    }
+                    pk[c] = Pair<T>::put(pr[c].x, pr[c].y);
+                }
+                tmem_st16(at + C::TM_S + w * 32, pk);
+                warp_announce_tmem(B(ctl->p_full));
+                if (!(ok = waits.warp(B(ctl->dp_full), i & 1u, SITE_LB_DP))) return;
+                tc_fence_after();
+                tmem_ld32_wait(at + C::TM_DP + w * 32, s);
 #pragma unroll
-            for (int c = 0; c < 16; ++c) pk[c] = Pair<T>::put(pr[2 * c], pr[2 * c + 1]);
-            tmem_st16(at + C::TM_P + w * 16, pk);
-            warp_announce_tmem(B(ctl->p_full));
-            ok = waits.warp(B(ctl->dp_full), i & 1u, SITE_LB_DP);
+                for (int c = 0; c < 16; ++c) {
+                    float2 x = __fmul2_rn(pr[c], __fadd2_rn(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])),
+                                                            reinterpret_cast<const float2 *>(ld + 64)[c]));
+                    if constexpr (MASKED) {  // (a masked dP may be anything)
+                        x.x = 2 * c >= lo && 2 * c < hi ? x.x : 0.f;
+                        x.y = 2 * c + 1 >= lo && 2 * c + 1 < hi ? x.y : 0.f;
+                    }
+                    pk[c] = Pair<T>::put(x.x, x.y);
+                }
+                tmem_st16(at + C::TM_DP + w * 32, pk);
+                warp_announce_tmem(B(ctl->ds_full));
+            };
+            if (__any_sync(0xffffffffu, lo > 0 || hi < 32)) tile(std::true_type());
+            else tile(std::false_type());
             if (!ok) break;
-            tc_fence_after();
-            tmem_ld32_wait(at + C::TM_DP + w * 32, s);
-#pragma unroll
-            for (int c = 0; c < 32; c += 4) {
-                const float4 d = *reinterpret_cast<const float4 *>(ld + 64 + c);
-                pr[c] *= __uint_as_float(s[c]) - d.x;
-                pr[c + 1] *= __uint_as_float(s[c + 1]) - d.y;
-                pr[c + 2] *= __uint_as_float(s[c + 2]) - d.z;
-                pr[c + 3] *= __uint_as_float(s[c + 3]) - d.w;
-            }
-            if (masked) {
-#pragma unroll
-                for (int c = 0; c < 32; ++c) pr[c] = c >= lo && c < hi ? pr[c] : 0.f;
-            }
-#pragma unroll
-            for (int c = 0; c < 16; ++c) pk[c] = Pair<T>::put(pr[2 * c], pr[2 * c + 1]);
-            tmem_st16(at + C::TM_DS + w * 16, pk);
-            warp_announce_tmem(B(ctl->ds_full));
         }
         if (ok) ok = waits.warp(B(ctl->acc_full), 0u, SITE_LB_ACC);
         if (ok) {
@@ -394,19 +418,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------- dQ
 
 struct QueriesCfg {
-    static constexpr int K_SLOTS = 7, V_SLOTS = 2;        // panels: K_j's three stay until dQ has met them
-    static constexpr int Q_OFF = 1024, G_OFF = Q_OFF + 3 * kPanel, K_OFF = G_OFF + 2 * kPanel, V_OFF = K_OFF + K_SLOTS * kPanel;
-    static constexpr int SMEM = V_OFF + V_SLOTS * kPanel + 1024;
-    static constexpr int TM_DQ = 0, TM_S = 192, TM_DP = 320, TM_DS = 448;
-    static_assert(SMEM <= 232448, "shared memory budget");
+    static constexpr int TILE = 64;                       // keys
+    static constexpr int HALF = TILE * 128;               // a panel of a tile of keys
+    static constexpr int STAGE = 5 * HALF, STAGES = 4;    // K (3 panels), V (2)
+    static constexpr int G_OFF = 1024, KV_OFF = G_OFF + 2 * kPanel;
+    // Q's three panels pass through the last stage, and what is behind it, on their way to tensor memory
+    static constexpr int Q_OFF = KV_OFF + (STAGES - 1) * STAGE;
+    static constexpr int SMEM = Q_OFF + 3 * kPanel + 1024;
+    // dS takes the place of dP, each half of the keys that of its own; two tiles' dP
+    static constexpr int TM_DQ = 0, TM_S = 192, TM_DP = 256, TM_Q = 384;
+    static_assert(3 * kPanel >= STAGE && SMEM <= 232448, "shared memory budget");
 };
 
 struct QueriesCtl {
-    uint64_t q_full, k_full[7], k_empty[7], v_full, v_empty;
+    uint64_t q_full, g_full, q_moved, full[4], empty[4];
     uint64_t s_full, s_free, dp_full, ds_full, acc_full;
     uint32_t tmem_base, abort;
 };
-static_assert(sizeof(QueriesCtl) <= QueriesCfg::Q_OFF, "control block");
+static_assert(sizeof(QueriesCtl) <= QueriesCfg::G_OFF, "control block");
 
 template <typename T, bool CAUSAL>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -415,9 +444,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ LatentBwdParams p)
 {
     using C = QueriesCfg;
-    constexpr int ROWS = 128, TILE = 128;
+    constexpr int ROWS = 128, TILE = C::TILE;
     constexpr bool BF16 = Elem<T>::BF16;
-    constexpr uint32_t IDESC_S = idesc_f16(ROWS, TILE, BF16, false), IDESC_DQ = idesc_f16(ROWS, 64, BF16, true);
+    constexpr uint32_t IDESC_S = idesc_f16(ROWS, TILE, BF16, false), IDESC_DQ = idesc_f16(ROWS, 192, BF16, true);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw_addr = smem_addr(smem_raw);
     const uint32_t base = (raw_addr + 1023u) & ~1023u;
@@ -446,12 +475,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const BoundedWaits waits{&ctl->abort, p.s.status, p.s.timeout_ns};
     if (threadIdx.x == 0) {
         mbar_init(B(ctl->q_full), 1);
-        for (int i = 0; i < C::K_SLOTS; ++i) {
-            mbar_init(B(ctl->k_full[i]), 1);
-            mbar_init(B(ctl->k_empty[i]), 1);
+        mbar_init(B(ctl->g_full), 1);
+        mbar_init(B(ctl->q_moved), 8);
+        for (int i = 0; i < C::STAGES; ++i) {
+            mbar_init(B(ctl->full[i]), 1);
+            mbar_init(B(ctl->empty[i]), 1);
         }
-        mbar_init(B(ctl->v_full), 1);
-        mbar_init(B(ctl->v_empty), 1);
         mbar_init(B(ctl->s_full), 1);
         mbar_init(B(ctl->s_free), 8);
         mbar_init(B(ctl->dp_full), 1);
@@ -472,110 +501,82 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp >= 8) {
         regs_dec<kOtherRegs>();
         if (warp == 9) {
-            // -------------------------------------------------------- copies: Q, dO, the keys
+            // -------------------------------------------------------- copies: Q, dO, the keys and values
             const uint64_t pol = l2_evict_normal();
+            const int tok = un.q0 + un.row0;
             if (elect_one()) {
-                const uint32_t bar = B(ctl->q_full);
-                const int tok = un.q0 + un.row0;
-                mbar_arrive_expect_tx(bar, 5 * kPanel);
+                uint32_t bar = B(ctl->q_full);
+                mbar_arrive_expect_tx(bar, 3 * kPanel);
                 for (int pn = 0; pn < 3; ++pn) tma_load_3d(base + C::Q_OFF + pn * kPanel, &tmQ, bar, pn * 64, un.head, tok, pol);
-                for (int pn = 0; pn < 2; ++pn) tma_load_3d(base + C::G_OFF + pn * kPanel, &tmG, bar, pn * 64, un.head, tok, pol);
             }
             __syncwarp();
-            uint32_t np = 0u;
-            bool ok = true;
-            for (int j = 0; ok && j < n; ++j) {
-                for (int pn = 0; ok && pn < 3; ++pn) {
-                    const uint32_t st = np % C::K_SLOTS, bar = B(ctl->k_full[st]);
-                    ok = waits.warp(B(ctl->k_empty[st]), ((np / C::K_SLOTS) & 1u) ^ 1u, SITE_LB_EMPTY);
-                    if (!ok) break;
-                    if (elect_one()) {
-                        mbar_arrive_expect_tx(bar, kPanel);
-                        if (pn < 2) tma_load_3d(base + C::K_OFF + st * kPanel, &tmK, bar, pn * 64, un.head, un.k0 + j * TILE, pol);
-                        else tma_load_3d(base + C::K_OFF + st * kPanel, &tmR, bar, 0, 0, un.k0 + j * TILE, pol);
-                    }
-                    __syncwarp();
-                    ++np;
-                }
-            }
-            // wait (bounded) for the last copies, so that none lands after the CTA
-            for (uint32_t i = np > C::K_SLOTS ? np - C::K_SLOTS : 0u; i < np; ++i)
-                drain_wait(B(ctl->k_full[i % C::K_SLOTS]), (i / C::K_SLOTS) & 1u, p.s.timeout_ns);
-            drain_wait(B(ctl->q_full), 0u, p.s.timeout_ns);
-        } else if (warp == 10) {
-            // -------------------------------------------------------- copies: the values
-            const uint64_t pol = l2_evict_normal();
             int j = 0;
             for (; j < n; ++j) {
-                if (!waits.warp(B(ctl->v_empty), (j & 1u) ^ 1u, SITE_LB_EMPTY)) break;
+                const uint32_t st = j % C::STAGES, bar = B(ctl->full[st]), at = base + C::KV_OFF + st * C::STAGE;
+                const int key = un.k0 + j * TILE;
+                if (j == C::STAGES - 1 && !waits.warp(B(ctl->q_moved), 0u, SITE_LB_KV)) break;
+                if (!waits.warp(B(ctl->empty[st]), ((j / C::STAGES) & 1u) ^ 1u, SITE_LB_EMPTY)) break;
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(B(ctl->v_full), 2 * kPanel);
-                    for (int pn = 0; pn < 2; ++pn)
-                        tma_load_3d(base + C::V_OFF + pn * kPanel, &tmV, B(ctl->v_full), pn * 64, un.head, un.k0 + j * TILE, pol);
+                    mbar_arrive_expect_tx(bar, C::STAGE);
+                    for (int pn = 0; pn < 2; ++pn) tma_load_3d(at + pn * C::HALF, &tmK, bar, pn * 64, un.head, key, pol);
+                    tma_load_3d(at + 2 * C::HALF, &tmR, bar, 0, 0, key, pol);
+                    for (int pn = 0; pn < 2; ++pn) tma_load_3d(at + (3 + pn) * C::HALF, &tmV, bar, pn * 64, un.head, key, pol);
+                    if (j == 0) {
+                        mbar_arrive_expect_tx(B(ctl->g_full), 2 * kPanel);
+                        for (int pn = 0; pn < 2; ++pn)
+                            tma_load_3d(base + C::G_OFF + pn * kPanel, &tmG, B(ctl->g_full), pn * 64, un.head, tok, pol);
+                    }
                 }
                 __syncwarp();
             }
-            if (j > 0) drain_wait(B(ctl->v_full), (j - 1) & 1u, p.s.timeout_ns);
+            // wait (bounded) for the last copies, so that none lands after the CTA
+            for (int k = max(j - C::STAGES, 0); k < j; ++k) drain_wait(B(ctl->full[k % C::STAGES]), (k / C::STAGES) & 1u, p.s.timeout_ns);
+            drain_wait(B(ctl->q_full), 0u, p.s.timeout_ns);
+            if (j > 0) drain_wait(B(ctl->g_full), 0u, p.s.timeout_ns);
         } else if (warp == 8) {
             // -------------------------------------------------------- products
-            const uint32_t dq = desc_lo(base + C::Q_OFF, 16), dg = desc_lo(base + C::G_OFF, 16), dv = desc_lo(base + C::V_OFF, 16);
-            const uint32_t dk = desc_lo(base + C::K_OFF, 16), dk_mn = desc_lo(base + C::K_OFF, kPanel);
-            bool ok = true;
-            // S of tile j, a panel of the keys at a time
-            auto scores = [&](int j) {
-                for (uint32_t pn = 0; pn < 3; ++pn) {
-                    const uint32_t np = 3u * j + pn, st = np % C::K_SLOTS;
-                    if (!waits.warp(B(ctl->k_full[st]), (np / C::K_SLOTS) & 1u, SITE_LB_FULL)) return false;
-                    // keys past the end of the sequence: dS is 0 there, and so must be what it meets
-                    if (un.sk - j * TILE < TILE) zero_panel_rows(base + C::K_OFF + st * kPanel, un.sk - j * TILE, TILE);
-                    tc_fence_after();
-                    if (elect_one()) {
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_ss(tmem + C::TM_S, dq + ((pn * kPanel + kk * 32) >> 4), dk + ((st * kPanel + kk * 32) >> 4), IDESC_S,
-                                   (pn > 0 || kk > 0) ? 1u : 0u);
-                        if (pn == 2) tc_commit(B(ctl->s_full));
-                    }
-                    __syncwarp();
-                }
-                return true;
-            };
-            auto grads = [&](int j) {  // dP of tile j
-                if (!waits.warp(B(ctl->v_full), j & 1u, SITE_LB_FULL)) return false;
+            const uint32_t dg = desc_lo(base + C::G_OFF, 16), dkv = desc_lo(base + C::KV_OFF, 16);
+            const uint32_t dk_mn = desc_lo(base + C::KV_OFF, C::HALF);
+            auto scores = [&](int j) {  // S and dP of tile j
+                const uint32_t st = j % C::STAGES, kv = dkv + ((st * C::STAGE) >> 4);
+                if (!waits.warp(B(ctl->full[st]), (j / C::STAGES) & 1u, SITE_LB_FULL)) return false;
+                // keys past the end of the sequence: dS is 0 there, and so must be what it meets
+                if (un.sk - j * TILE < TILE)
+                    for (int pn = 0; pn < 3; ++pn)
+                        zero_panel_rows(base + C::KV_OFF + st * C::STAGE + pn * C::HALF, un.sk - j * TILE, TILE);
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
+                    for (int kk = 0; kk < 12; ++kk)
+                        mma_ts(tmem + C::TM_S, tmem + C::TM_Q + kk * 8, kv + (((kk / 4) * C::HALF + (kk % 4) * 32) >> 4), IDESC_S,
+                               kk > 0 ? 1u : 0u);
+                    tc_commit(B(ctl->s_full));
+#pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
-                        mma_ss(tmem + C::TM_DP, dg + (((kk / 4) * kPanel + (kk % 4) * 32) >> 4), dv + (((kk / 4) * kPanel + (kk % 4) * 32) >> 4),
-                               IDESC_S, kk > 0 ? 1u : 0u);
-                    tc_commit(B(ctl->v_empty));
+                        mma_ss(tmem + C::TM_DP + (j & 1) * 64, dg + (((kk / 4) * kPanel + (kk % 4) * 32) >> 4),
+                               kv + (((3 + kk / 4) * C::HALF + (kk % 4) * 32) >> 4), IDESC_S, kk > 0 ? 1u : 0u);
                     tc_commit(B(ctl->dp_full));
                 }
                 __syncwarp();
                 return true;
             };
-            ok = waits.warp(B(ctl->q_full), 0u, SITE_LB_KV) && scores(0) && grads(0);
+            bool ok = waits.warp(B(ctl->q_moved), 0u, SITE_LB_KV) && waits.warp(B(ctl->g_full), 0u, SITE_LB_KV) && scores(0);
             for (int j = 0; ok && j < n; ++j) {
-                const bool more = j + 1 < n;
-                if (more) {
+                if (j + 1 < n) {
                     if (!(ok = waits.warp(B(ctl->s_free), j & 1u, SITE_LB_S))) break;
                     if (!(ok = scores(j + 1))) break;
                 }
                 if (!(ok = waits.warp(B(ctl->ds_full), j & 1u, SITE_LB_DS))) break;
                 tc_fence_after();
                 if (elect_one()) {
+                    const uint32_t st = j % C::STAGES;
 #pragma unroll
-                    for (uint32_t pn = 0; pn < 3; ++pn) {
-                        const uint32_t st = (3u * j + pn) % C::K_SLOTS;
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)  // 16 keys a step
-                            mma_ts(tmem + C::TM_DQ + pn * 64, tmem + C::TM_DS + kk * 8, dk_mn + ((st * kPanel + kk * 2048) >> 4), IDESC_DQ,
-                                   (j > 0 || kk > 0) ? 1u : 0u);
-                        tc_commit(B(ctl->k_empty[st]));
-                    }
+                    for (int kk = 0; kk < TILE / 16; ++kk)  // 16 keys a step, 32 to each half
+                        mma_ts(tmem + C::TM_DQ, tmem + C::TM_DP + (j & 1) * 64 + (kk / 2) * 32 + (kk % 2) * 8,
+                               dk_mn + ((st * C::STAGE + kk * 2048) >> 4), IDESC_DQ, (j > 0 || kk > 0) ? 1u : 0u);
+                    tc_commit(B(ctl->empty[st]));
                 }
                 __syncwarp();
-                if (more && !(ok = grads(j + 1))) break;
             }
             if (elect_one()) tc_commit(B(ctl->acc_full));
             __syncwarp();
@@ -585,49 +586,57 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ------------------------------------------------------------ dS: a query to a thread, half of the keys
         regs_inc<kSoftmaxRegs>();
-        const int w = warp >> 2, q = un.row0 + (warp & 3) * 32 + lane;
+        const int w = warp >> 2, in_unit = (warp & 3) * 32 + lane, q = un.row0 + in_unit;
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16, at = tmem + lane_off;
         const int64_t stat = static_cast<int64_t>(un.head) * p.s.total_q + un.q0 + q;
         const float lse = q < un.sq ? lse_log2(p.lse[stat]) : INFINITY, d = q < un.sq ? p.dsum[stat] : 0.f;
         const int lim = CAUSAL ? min(q + 1 + un.sk - un.sq, un.sk) : un.sk;
         const float2 scale2 = make_float2(p.s.sl2e, p.s.sl2e), lse2 = make_float2(-lse, -lse), d2 = make_float2(-d, -d);
-        bool ok = true;
-        for (int j = 0; j < n; ++j) {
+        // Q as an operand in tensor memory
+        bool ok = waits.warp(B(ctl->q_full), 0u, SITE_LB_KV);
+        if (ok) {
+            for (int pn = w; pn < 3; pn += 2) move_panel_row(base + C::Q_OFF + pn * kPanel, in_unit, at + C::TM_Q + pn * 32);
+            warp_announce_tmem(B(ctl->q_moved));
+        }
+        for (int j = 0; ok && j < n; ++j) {
             if (!(ok = waits.warp(B(ctl->s_full), j & 1u, SITE_LB_S))) break;
             tc_fence_after();
-            const int vis = lim - j * TILE - w * 64;  // columns >= vis are masked
-            const bool masked = __any_sync(0xffffffffu, vis < 64);
-            uint32_t s[64];
-            tmem_ld64_wait(at + C::TM_S + w * 64, s);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(B(ctl->s_free));
-            float2 pr[32];
+            const int vis = lim - j * TILE - w * 32;  // columns >= vis are masked
+            auto tile = [&](auto masked) __attribute__((always_inline)) {
+                uint32_t s[32], pk[16];
+                tmem_ld32_wait(at + C::TM_S + w * 32, s);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(B(ctl->s_free));
+                float2 pr[16];
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-                const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), scale2, lse2);
-                pr[c] = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-            }
-            if (!(ok = waits.warp(B(ctl->dp_full), j & 1u, SITE_LB_DP))) break;
-            tc_fence_after();
-            tmem_ld64_wait(at + C::TM_DP + w * 64, s);
-            uint32_t pk[32];
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-                float2 x = __fmul2_rn(pr[c], __fadd2_rn(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), d2));
-                if (masked) {
-                    x.x = 2 * c < vis ? x.x : 0.f;
-                    x.y = 2 * c + 1 < vis ? x.y : 0.f;
+                for (int c = 0; c < 16; ++c) {
+                    const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), scale2, lse2);
+                    pr[c] = make_float2(ex2_approx(x.x), ex2_approx(x.y));
                 }
-                pk[c] = Pair<T>::put(x.x, x.y);
-            }
-            tmem_st32(at + C::TM_DS + w * 32, pk);
-            warp_announce_tmem(B(ctl->ds_full));
+                if (!(ok = waits.warp(B(ctl->dp_full), j & 1u, SITE_LB_DP))) return;
+                tc_fence_after();
+                const uint32_t tDP = at + C::TM_DP + (j & 1) * 64 + w * 32;
+                tmem_ld32_wait(tDP, s);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    float2 x = __fmul2_rn(pr[c], __fadd2_rn(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), d2));
+                    if constexpr (decltype(masked)::value) {
+                        x.x = 2 * c < vis ? x.x : 0.f;
+                        x.y = 2 * c + 1 < vis ? x.y : 0.f;
+                    }
+                    pk[c] = Pair<T>::put(x.x, x.y);
+                }
+                tmem_st16(tDP, pk);
+                warp_announce_tmem(B(ctl->ds_full));
+            };
+            if (__any_sync(0xffffffffu, vis < 32)) tile(std::true_type());
+            else tile(std::false_type());
         }
         if (ok) ok = waits.warp(B(ctl->acc_full), 0u, SITE_LB_ACC);
         if (ok) {
             tc_fence_after();
-            const uint32_t pass = base + C::Q_OFF + warp * 4096;  // the tile of queries is not needed any more
+            const uint32_t pass = base + C::G_OFF + warp * 4096;  // dO's rows are not needed any more
             const int warp_q = un.row0 + (warp & 3) * 32;
 #pragma unroll 1
             for (int piece = w; piece < 6; piece += 2)
@@ -698,7 +707,7 @@ cudaError_t launch_t(const LatentBwdArgs &a)
     }
     if (e == cudaSuccess && a.p.q_blocks > 0)
         e = launch_overlapped(latent_bwd_queries_kernel<T, CAUSAL>, dim3(seq_heads * a.p.q_blocks), kThreads, QueriesCfg::SMEM, a.stream, a.q,
-                              a.dout, a.k, a.r, a.v, a.p);
+                              a.dout, a.k_half, a.r_half, a.v_half, a.p);
     return e;
 }
 

@@ -256,22 +256,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(ok = waits.warp(B(ctl->s_full[t]), j & 1u, SITE_LF_S))) break;
                 tc_fence_after();
                 const int vis = lim - j * kKeys;  // columns >= vis are masked
-                uint32_t s[128];
-                tmem_ld128_wait(tS, s);
-                if (__any_sync(0xffffffffu, vis < kKeys)) mask_columns(s, vis, neg);
-                const float mx = (neg ? row_extreme<true>(s) : row_extreme<false>(s)) * c;
-                const float m_new = fmaxf(m, mx);
-                if (__any_sync(0xffffffffu, m_new > m + 8.f)) {
-                    const float f = m_new == m ? 1.f : ex2_approx(m - m_new);
-                    if (j > 0) rescale_rows<kLatentValue>(tO, f);
-                    l *= f;
-                    lr *= f;
-                    m = m_new;
-                }
-                const float2 sums = exp_store_tile<T, false>(s, 0, c, m == -INFINITY ? 0.f : m, tS, B(ctl->p_half[t]));
-                l += sums.x;
-                lr += sums.y;
-                warp_announce_tmem(B(ctl->p_full[t]));
+                // (two instances: of one, the compiler makes selects that every tile pays for)
+                auto tile = [&](auto masked) __attribute__((always_inline)) {
+                    uint32_t s[128];
+                    tmem_ld128_wait(tS, s);
+                    if constexpr (decltype(masked)::value) mask_columns(s, vis, neg);
+                    const float mx = (neg ? row_extreme<true>(s) : row_extreme<false>(s)) * c;
+                    const float m_new = fmaxf(m, mx);
+                    if (__any_sync(0xffffffffu, m_new > m + 8.f)) {
+                        const float f = m_new == m ? 1.f : ex2_approx(m - m_new);
+                        if (j > 0) rescale_rows<kLatentValue>(tO, f);
+                        l *= f;
+                        lr *= f;
+                        m = m_new;
+                    }
+                    const float2 sums = exp_store_tile<T, false>(s, 0, c, m == -INFINITY ? 0.f : m, tS, B(ctl->p_half[t]));
+                    l += sums.x;
+                    lr += sums.y;
+                    warp_announce_tmem(B(ctl->p_full[t]));
+                };
+                if (__any_sync(0xffffffffu, vis < kKeys)) tile(std::true_type());
+                else tile(std::false_type());
             }
             if (ok) ok = waits.warp(B(ctl->o_full[t]), 0u, SITE_LF_O);
             if (ok) {

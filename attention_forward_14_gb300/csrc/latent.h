@@ -134,9 +134,8 @@ struct LatentBwdParams {
 };
 
 struct LatentBwdArgs {
-    CUtensorMap q, dout;         // 128 rows a copy
-    CUtensorMap q_half, dout_half;  // 64 rows a copy
-    CUtensorMap k, r, v;
+    CUtensorMap q, dout, k, r, v;                           // 128 rows a copy
+    CUtensorMap q_half, dout_half, k_half, r_half, v_half;  // 64 rows a copy
     LatentBwdParams p;
     cudaStream_t stream;
     std::atomic<int> *attr_ready;
