@@ -24,6 +24,7 @@
 
 #include "attn_kv8_common.cuh"
 #include "latent_seq.cuh"
+#include "mma_issue.cuh"
 #include "tmem_cols.cuh"
 
 namespace attn {
@@ -241,6 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(B(ctl->ld_full[st]));
             }
         } else if (warp == 8) {
+            const uint32_t leader = issuing_lane();
             // -------------------------------------------------------- products
             const uint32_t dk = desc_lo(base + C::K_OFF, 16);
             const uint32_t dq_k = desc_lo(base + C::Q_OFF, 16), dq_mn = desc_lo(base + C::Q_OFF, C::HALF);
@@ -257,26 +259,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto issue_s = [&](uint32_t st) {
 #pragma unroll
                 for (int kk = 0; kk < 12; ++kk)
-                    mma_ss(tmem + C::TM_S, dk + (((kk / 4) * kPanel + (kk % 4) * 32) >> 4),
+                    mma_ss_by(leader, tmem + C::TM_S, dk + (((kk / 4) * kPanel + (kk % 4) * 32) >> 4),
                            dq_k + ((st * C::STAGE + (kk / 4) * C::HALF + (kk % 4) * 32) >> 4), IDESC_S, kk > 0 ? 1u : 0u);
-                tc_commit(B(ctl->s_full));
+                tc_commit_by(leader, B(ctl->s_full));
             };
             auto issue_dp = [&](uint32_t st) {
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    mma_ts(tmem + C::TM_DP, tmem + C::TM_V + kk * 8,
+                    mma_ts_by(leader, tmem + C::TM_DP, tmem + C::TM_V + kk * 8,
                            dq_k + ((st * C::STAGE + (3 + kk / 4) * C::HALF + (kk % 4) * 32) >> 4), IDESC_S, kk > 0 ? 1u : 0u);
-                tc_commit(B(ctl->dp_full));
+                tc_commit_by(leader, B(ctl->dp_full));
             };
             // k-step kk of a tile's queries, 16 of them, in P^T or dS^T: 32 queries to each half
             auto at_step = [](int kk) { return (kk / 2) * 32 + (kk % 2) * 8; };
             bool ok = waits.warp(B(ctl->k_full), 0u, SITE_LB_KV) && stage_there(0);
             if (ok) {
-                if (elect_one()) issue_s(0u);
-                __syncwarp();
+                issue_s(0u);
                 ok = waits.warp(B(ctl->v_moved), 0u, SITE_LB_KV);
                 tc_fence_after();
-                if (ok && elect_one()) issue_dp(0u);
+                if (ok) issue_dp(0u);
                 __syncwarp();
             }
             for (int i = 0; ok && i < n; ++i) {
@@ -285,28 +286,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (more && !(ok = stage_there(i + 1))) break;
                 if (!(ok = waits.warp(B(ctl->p_full), i & 1u, SITE_LB_P))) break;
                 tc_fence_after();
-                if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)  // 16 queries a step
-                        mma_ts(tmem + C::TM_DV, tmem + C::TM_S + at_step(kk), dq_mn + ((st * C::STAGE + 3 * C::HALF + kk * 2048) >> 4), IDESC_DV,
-                               (i > 0 || kk > 0) ? 1u : 0u);
-                    if (more) issue_s(next);
-                }
-                __syncwarp();
+                for (int kk = 0; kk < 4; ++kk)  // 16 queries a step
+                    mma_ts_by(leader, tmem + C::TM_DV, tmem + C::TM_S + at_step(kk), dq_mn + ((st * C::STAGE + 3 * C::HALF + kk * 2048) >> 4), IDESC_DV,
+                           (i > 0 || kk > 0) ? 1u : 0u);
+                if (more) issue_s(next);
                 if (!(ok = waits.warp(B(ctl->ds_full), i & 1u, SITE_LB_DS))) break;
                 tc_fence_after();
-                if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_ts(tmem + C::TM_DK, tmem + C::TM_DP + at_step(kk), dq_mn + ((st * C::STAGE + kk * 2048) >> 4), IDESC_DK,
-                               (i > 0 || kk > 0) ? 1u : 0u);
-                    tc_commit(B(ctl->empty[st]));
-                    if (more) issue_dp(next);
-                }
-                __syncwarp();
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_ts_by(leader, tmem + C::TM_DK, tmem + C::TM_DP + at_step(kk), dq_mn + ((st * C::STAGE + kk * 2048) >> 4), IDESC_DK,
+                           (i > 0 || kk > 0) ? 1u : 0u);
+                tc_commit_by(leader, B(ctl->empty[st]));
+                if (more) issue_dp(next);
             }
             // every product completes before the sums are read and tensor memory is freed
-            if (elect_one()) tc_commit(B(ctl->acc_full));
+            tc_commit_by(leader, B(ctl->acc_full));
             __syncwarp();
             drain_wait(B(ctl->acc_full), 0u, p.s.timeout_ns);
             __syncwarp();
@@ -534,6 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             drain_wait(B(ctl->q_full), 0u, p.s.timeout_ns);
             if (j > 0) drain_wait(B(ctl->g_full), 0u, p.s.timeout_ns);
         } else if (warp == 8) {
+            const uint32_t leader = issuing_lane();
             // -------------------------------------------------------- products
             const uint32_t dg = desc_lo(base + C::G_OFF, 16), dkv = desc_lo(base + C::KV_OFF, 16);
             const uint32_t dk_mn = desc_lo(base + C::KV_OFF, C::HALF);
@@ -545,19 +541,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int pn = 0; pn < 3; ++pn)
                         zero_panel_rows(base + C::KV_OFF + st * C::STAGE + pn * C::HALF, un.sk - j * TILE, TILE);
                 tc_fence_after();
-                if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 12; ++kk)
-                        mma_ts(tmem + C::TM_S, tmem + C::TM_Q + kk * 8, kv + (((kk / 4) * C::HALF + (kk % 4) * 32) >> 4), IDESC_S,
-                               kk > 0 ? 1u : 0u);
-                    tc_commit(B(ctl->s_full));
+                for (int kk = 0; kk < 12; ++kk)
+                    mma_ts_by(leader, tmem + C::TM_S, tmem + C::TM_Q + kk * 8, kv + (((kk / 4) * C::HALF + (kk % 4) * 32) >> 4), IDESC_S,
+                           kk > 0 ? 1u : 0u);
+                tc_commit_by(leader, B(ctl->s_full));
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_ss(tmem + C::TM_DP + (j & 1) * 64, dg + (((kk / 4) * kPanel + (kk % 4) * 32) >> 4),
-                               kv + (((3 + kk / 4) * C::HALF + (kk % 4) * 32) >> 4), IDESC_S, kk > 0 ? 1u : 0u);
-                    tc_commit(B(ctl->dp_full));
-                }
-                __syncwarp();
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_ss_by(leader, tmem + C::TM_DP + (j & 1) * 64, dg + (((kk / 4) * kPanel + (kk % 4) * 32) >> 4),
+                           kv + (((3 + kk / 4) * C::HALF + (kk % 4) * 32) >> 4), IDESC_S, kk > 0 ? 1u : 0u);
+                tc_commit_by(leader, B(ctl->dp_full));
                 return true;
             };
             bool ok = waits.warp(B(ctl->q_moved), 0u, SITE_LB_KV) && waits.warp(B(ctl->g_full), 0u, SITE_LB_KV) && scores(0);
@@ -568,17 +561,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!(ok = waits.warp(B(ctl->ds_full), j & 1u, SITE_LB_DS))) break;
                 tc_fence_after();
-                if (elect_one()) {
+                {
                     const uint32_t st = j % C::STAGES;
 #pragma unroll
                     for (int kk = 0; kk < TILE / 16; ++kk)  // 16 keys a step, 32 to each half
-                        mma_ts(tmem + C::TM_DQ, tmem + C::TM_DP + (j & 1) * 64 + (kk / 2) * 32 + (kk % 2) * 8,
+                        mma_ts_by(leader, tmem + C::TM_DQ, tmem + C::TM_DP + (j & 1) * 64 + (kk / 2) * 32 + (kk % 2) * 8,
                                dk_mn + ((st * C::STAGE + kk * 2048) >> 4), IDESC_DQ, (j > 0 || kk > 0) ? 1u : 0u);
-                    tc_commit(B(ctl->empty[st]));
+                    tc_commit_by(leader, B(ctl->empty[st]));
                 }
-                __syncwarp();
             }
-            if (elect_one()) tc_commit(B(ctl->acc_full));
+            tc_commit_by(leader, B(ctl->acc_full));
             __syncwarp();
             drain_wait(B(ctl->acc_full), 0u, p.s.timeout_ns);
             __syncwarp();

@@ -19,6 +19,7 @@
 
 #include "attn_kv8_common.cuh"
 #include "latent_seq.cuh"
+#include "mma_issue.cuh"
 
 namespace attn {
 
@@ -150,6 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             drain_wait(B(ctl->q_full[0]), 0u, p.s.timeout_ns);
             if (two) drain_wait(B(ctl->q_full[1]), 0u, p.s.timeout_ns);
         } else if (warp == 8) {
+            const uint32_t leader = issuing_lane();
             // -------------------------------------------------------- products
             bool ok = true;
             const uint32_t dq = desc_lo(sQ, 16), dk = desc_lo(sRing, 16), dv = desc_lo(sRing, kPanel);
@@ -163,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto issue_qk = [&](int t, uint32_t first) {
 #pragma unroll
                 for (int kk = 0; kk < 12; ++kk)  // 16 values a step
-                    mma_ss(tmem + t * 128, dq + (((t * kQPanels + kk / 4) * kPanel + (kk % 4) * 32) >> 4),
+                    mma_ss_by(leader, tmem + t * 128, dq + (((t * kQPanels + kk / 4) * kPanel + (kk % 4) * 32) >> 4),
                            dk + ((((first + kk / 4) % kSlots) * kPanel + (kk % 4) * 32) >> 4), IDESC_QK, kk > 0 ? 1u : 0u);
             };
             // a panel of V at a time: the two need not be neighbours in the ring
@@ -173,32 +175,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int k2 = 0; k2 < 4; ++k2) {  // 16 keys a step
                         const int kk = half * 4 + k2;
-                        mma_ts(tmem + kTmO + t * 128 + pn * 64, tmem + t * 128 + kk * 8,
+                        mma_ts_by(leader, tmem + kTmO + t * 128 + pn * 64, tmem + t * 128 + kk * 8,
                                dv + ((((first + pn) % kSlots) * kPanel + kk * 2048) >> 4), IDESC_PV, (accumulate || kk > 0) ? 1u : 0u);
                     }
             };
             auto release = [&](uint32_t first, int count) {
-                for (int i = 0; i < count; ++i) tc_commit(B(ctl->empty[(first + i) % kSlots]));
+                for (int i = 0; i < count; ++i) tc_commit_by(leader, B(ctl->empty[(first + i) % kSlots]));
             };
             ok = waits.warp(B(ctl->q_full[0]), 0u, SITE_LF_Q);
             if (ok && panels_there(0u, kKPanels)) {
-                if (elect_one()) {
-                    issue_qk(0, 0u);
-                    tc_commit(B(ctl->s_full[0]));
-                }
-                __syncwarp();
+                issue_qk(0, 0u);
+                tc_commit_by(leader, B(ctl->s_full[0]));
             }
             if (ok && two) ok = waits.warp(B(ctl->q_full[1]), 0u, SITE_LF_Q);
             if (ok) {
                 tc_fence_after();
-                if (elect_one()) {
-                    if (two) {
-                        issue_qk(1, 0u);
-                        tc_commit(B(ctl->s_full[1]));
-                    }
-                    release(0u, kKPanels);
+                if (two) {
+                    issue_qk(1, 0u);
+                    tc_commit_by(leader, B(ctl->s_full[1]));
                 }
-                __syncwarp();
+                release(0u, kKPanels);
             }
             for (int j = 0; ok && j < n; ++j) {
                 const uint32_t vs = 5u * j + 3u, ks = vs + 2u, par = j & 1u;
@@ -214,26 +210,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool final = t == 1 || !two;  // of the tile's products
                     if (!(ok = waits.warp(B(ctl->p_half[t]), par, SITE_LF_P))) break;
                     tc_fence_after();
-                    if (elect_one()) issue_pv(t, vs, j > 0, 0);
-                    __syncwarp();
+                    issue_pv(t, vs, j > 0, 0);
                     if (!(ok = waits.warp(B(ctl->p_full[t]), par, SITE_LF_P))) break;
                     tc_fence_after();
-                    if (elect_one()) {
-                        issue_pv(t, vs, true, 1);
-                        if (final) release(vs, kVPanels);
-                        if (more) {
-                            issue_qk(t, ks);
-                            tc_commit(B(ctl->s_full[t]));
-                            if (final) release(ks, kKPanels);
-                        } else {
-                            tc_commit(B(ctl->o_full[t]));
-                        }
+                    issue_pv(t, vs, true, 1);
+                    if (final) release(vs, kVPanels);
+                    if (more) {
+                        issue_qk(t, ks);
+                        tc_commit_by(leader, B(ctl->s_full[t]));
+                        if (final) release(ks, kKPanels);
+                    } else {
+                        tc_commit_by(leader, B(ctl->o_full[t]));
                     }
-                    __syncwarp();
                 }
             }
             // every product completes before tensor memory is freed
-            if (elect_one()) tc_commit(B(ctl->mma_done));
+            tc_commit_by(leader, B(ctl->mma_done));
             __syncwarp();
             drain_wait(B(ctl->mma_done), 0u, p.s.timeout_ns);
             __syncwarp();

@@ -41,6 +41,7 @@
 #include "latent.h"
 
 #include "attn_kv8_common.cuh"
+#include "mma_issue.cuh"
 #include "tmem_cols.cuh"
 
 namespace attn {
@@ -428,6 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 set_entry(p, at, at.entry + 1, N);
             }
         } else if (warp == 8) {
+            const uint32_t leader = issuing_lane();
             // -------------------------------------------------------- products
             uint32_t np = 0u, nk = 0u, n_dirty = 0u, q_it = 0u, tile_it = 0u;
             bool ok = true;
@@ -446,50 +448,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t st = (np + pr) % C::PAIR_SLOTS;
                         if (!(ok = warp_waits(B(ctl->pair_full[st]), ((np + pr) / C::PAIR_SLOTS) & 1u, SITE_LAT_FULL))) break;
                         tc_fence_after();
-                        if (elect_one()) {
 #pragma unroll
-                            for (int kk = 0; kk < 8; ++kk)  // 16 values a step
-                                mma_ss(tmem + C::TM_S, dk_pair + ((st * C::PAIR + (kk / 4) * C::PANEL + (kk % 4) * 32) >> 4),
-                                       dq + (((2 * pr + kk / 4) * C::Q_PANEL + (kk % 4) * 32) >> 4), IDESC_S, (pr > 0 || kk > 0) ? 1u : 0u);
-                        }
-                        __syncwarp();
+                        for (int kk = 0; kk < 8; ++kk)  // 16 values a step
+                            mma_ss_by(leader, tmem + C::TM_S, dk_pair + ((st * C::PAIR + (kk / 4) * C::PANEL + (kk % 4) * 32) >> 4),
+                                   dq + (((2 * pr + kk / 4) * C::Q_PANEL + (kk % 4) * 32) >> 4), IDESC_S, (pr > 0 || kk > 0) ? 1u : 0u);
                     }
                     if (!ok) break;
                     const uint32_t ks = nk % C::KEY_SLOTS;
                     if (!(ok = warp_waits(B(ctl->key_full[ks]), (nk / C::KEY_SLOTS) & 1u, SITE_LAT_FULL))) break;
                     tc_fence_after();
-                    if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_ss(tmem + C::TM_S, dk_key + ((ks * C::PANEL + kk * 32) >> 4), dq + ((8 * C::Q_PANEL + kk * 32) >> 4),
-                                   IDESC_S, 1u);
-                        tc_commit(B(ctl->s_full));
-                        if (dirty) mbar_arrive(B(ctl->dirty));
-                    }
-                    __syncwarp();
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_ss_by(leader, tmem + C::TM_S, dk_key + ((ks * C::PANEL + kk * 32) >> 4), dq + ((8 * C::Q_PANEL + kk * 32) >> 4),
+                               IDESC_S, 1u);
+                    tc_commit_by(leader, B(ctl->s_full));
+                    if (dirty && leader) mbar_arrive(B(ctl->dirty));
                     // O^T
                     if (dirty && !(ok = warp_waits(B(ctl->clean), n_dirty++ & 1u, SITE_LAT_CLEAN))) break;
                     if (!(ok = warp_waits(B(ctl->p_full), tile_it & 1u, SITE_LAT_P))) break;
                     tc_fence_after();
-                    if (elect_one()) {
+                    {
                         for (int pr = 0; pr < kPairs; ++pr) {
                             const uint32_t st = (np + pr) % C::PAIR_SLOTS;
 #pragma unroll
                             for (int kk = 0; kk < 8; ++kk)  // 16 keys a step
-                                mma_ss(tmem + C::TM_O + pr * N, dv + ((st * C::PAIR + kk * 2048) >> 4),
+                                mma_ss_by(leader, tmem + C::TM_O + pr * N, dv + ((st * C::PAIR + kk * 2048) >> 4),
                                        dp + ((ks * C::PANEL + kk * 2048) >> 4), IDESC_O, (t > 0 || kk > 0) ? 1u : 0u);
-                            tc_commit(B(ctl->pair_empty[st]));
+                            tc_commit_by(leader, B(ctl->pair_empty[st]));
                         }
-                        tc_commit(B(ctl->key_empty[ks]));
-                        tc_commit(B(ctl->pv_done));
+                        tc_commit_by(leader, B(ctl->key_empty[ks]));
+                        tc_commit_by(leader, B(ctl->pv_done));
                     }
-                    __syncwarp();
                 }
                 it += j_end - at.j;
                 set_entry(p, at, at.entry + 1, N);
             }
             // every product completes before tensor memory is freed
-            if (elect_one()) tc_commit(B(ctl->mma_done));
+            tc_commit_by(leader, B(ctl->mma_done));
             __syncwarp();
             drain_wait(B(ctl->mma_done), 0u, p.timeout_ns);
             __syncwarp();
