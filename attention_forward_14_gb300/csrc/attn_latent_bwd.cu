@@ -36,7 +36,7 @@ constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;  // 256 * 216 + 128 * 72 = 38
 constexpr int kPanel = 128 * 128;                   // 128 rows of 64 values
 constexpr float kLog2e = 1.4426950408889634f;
 
-enum : uint32_t { SITE_LB_EMPTY = 100, SITE_LB_FULL = 101, SITE_LB_KV = 102, SITE_LB_LD = 103, SITE_LB_S = 104, SITE_LB_P = 105,
+enum : uint32_t { SITE_LB_EMPTY = 100, SITE_LB_FULL = 101, SITE_LB_KV = 102, SITE_LB_S = 104, SITE_LB_P = 105,
                   SITE_LB_DP = 106, SITE_LB_DS = 107, SITE_LB_ACC = 108 };
 
 // ---------------------------------------------------------------- D
@@ -246,15 +246,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             // -------------------------------------------------------- products
             const uint32_t dk = desc_lo(base + C::K_OFF, 16);
             const uint32_t dq_k = desc_lo(base + C::Q_OFF, 16), dq_mn = desc_lo(base + C::Q_OFF, C::HALF);
-            auto stage_there = [&](int i) {
+            auto stage_full = [&](int i) { return B(ctl->full[i % C::STAGES]); };
+            auto stage_parity = [&](int i) { return static_cast<uint32_t>(i / C::STAGES) & 1u; };
+            auto clean = [&](int i) {
                 const uint32_t st = i % C::STAGES;
-                if (!waits.warp(B(ctl->full[st]), (i / C::STAGES) & 1u, SITE_LB_FULL)) return false;
                 // queries past the end of the sequence: their weights are 0, and so must be what they meet
                 const int valid = un.sq - (first + i) * kQueries;
                 if (valid < kQueries)
                     for (int pn = 0; pn < 5; ++pn) zero_panel_rows(base + C::Q_OFF + st * C::STAGE + pn * C::HALF, valid, kQueries);
                 tc_fence_after();
-                return true;
             };
             auto issue_s = [&](uint32_t st) {
 #pragma unroll
@@ -272,19 +272,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             // k-step kk of a tile's queries, 16 of them, in P^T or dS^T: 32 queries to each half
             auto at_step = [](int kk) { return (kk / 2) * 32 + (kk % 2) * 8; };
-            bool ok = waits.warp(B(ctl->k_full), 0u, SITE_LB_KV) && stage_there(0);
+            bool ok = waits.warp(B(ctl->k_full), 0u, stage_full(0), 0u, SITE_LB_KV);
             if (ok) {
+                clean(0);
                 issue_s(0u);
                 ok = waits.warp(B(ctl->v_moved), 0u, SITE_LB_KV);
                 tc_fence_after();
                 if (ok) issue_dp(0u);
-                __syncwarp();
             }
             for (int i = 0; ok && i < n; ++i) {
                 const uint32_t st = i % C::STAGES, next = (i + 1) % C::STAGES;
                 const bool more = i + 1 < n;
-                if (more && !(ok = stage_there(i + 1))) break;
-                if (!(ok = waits.warp(B(ctl->p_full), i & 1u, SITE_LB_P))) break;
+                ok = more ? waits.warp(B(ctl->p_full), i & 1u, stage_full(i + 1), stage_parity(i + 1), SITE_LB_P)
+                          : waits.warp(B(ctl->p_full), i & 1u, SITE_LB_P);
+                if (!ok) break;
+                if (more) clean(i + 1);
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)  // 16 queries a step
@@ -321,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t st = i % C::STAGES;
             const float *ld = reinterpret_cast<const float *>(smem + C::LD_OFF + st * 512) + w * 32;
             const int q0 = (first + i) * kQueries + w * 32;
-            ok = waits.warp(B(ctl->ld_full[st]), (i / C::STAGES) & 1u, SITE_LB_LD) && waits.warp(B(ctl->s_full), i & 1u, SITE_LB_S);
+            ok = waits.warp(B(ctl->ld_full[st]), (i / C::STAGES) & 1u, B(ctl->s_full), i & 1u, SITE_LB_S);
             if (!ok) break;
             tc_fence_after();
             // queries [lo, hi) of the 32 see this key
@@ -535,7 +537,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t dk_mn = desc_lo(base + C::KV_OFF, C::HALF);
             auto scores = [&](int j) {  // S and dP of tile j
                 const uint32_t st = j % C::STAGES, kv = dkv + ((st * C::STAGE) >> 4);
-                if (!waits.warp(B(ctl->full[st]), (j / C::STAGES) & 1u, SITE_LB_FULL)) return false;
+                const uint32_t full = B(ctl->full[st]), par = (j / C::STAGES) & 1u;
+                // the scores of the tile before have been read
+                if (!(j > 0 ? waits.warp(full, par, B(ctl->s_free), (j - 1) & 1u, SITE_LB_FULL) : waits.warp(full, par, SITE_LB_FULL)))
+                    return false;
                 // keys past the end of the sequence: dS is 0 there, and so must be what it meets
                 if (un.sk - j * TILE < TILE)
                     for (int pn = 0; pn < 3; ++pn)
@@ -555,10 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             bool ok = waits.warp(B(ctl->q_moved), 0u, SITE_LB_KV) && waits.warp(B(ctl->g_full), 0u, SITE_LB_KV) && scores(0);
             for (int j = 0; ok && j < n; ++j) {
-                if (j + 1 < n) {
-                    if (!(ok = waits.warp(B(ctl->s_free), j & 1u, SITE_LB_S))) break;
-                    if (!(ok = scores(j + 1))) break;
-                }
+                if (j + 1 < n && !(ok = scores(j + 1))) break;
                 if (!(ok = waits.warp(B(ctl->ds_full), j & 1u, SITE_LB_DS))) break;
                 tc_fence_after();
                 {

@@ -38,7 +38,7 @@ constexpr int kTmO = 256;  // O_t at kTmO + t * 128; S_t at t * 128
 enum : uint32_t { SITE_LF_EMPTY = 90, SITE_LF_FULL = 91, SITE_LF_Q = 92, SITE_LF_S = 93, SITE_LF_P = 94, SITE_LF_O = 95 };
 
 struct FwdCtl {
-    uint64_t full[kSlots], empty[kSlots];
+    uint64_t k_full[2], v_full[2], empty[kSlots];  // of even and of odd tiles; of each panel's slot
     uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], mma_done;
     uint32_t tmem_base, abort;
 };
@@ -85,11 +85,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     BoundedWaits waits{&ctl->abort, p.s.status, p.s.timeout_ns};
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kSlots; ++i) {
-            mbar_init(B(ctl->full[i]), 1);
-            mbar_init(B(ctl->empty[i]), 1);
-        }
+        for (int i = 0; i < kSlots; ++i) mbar_init(B(ctl->empty[i]), 1);
         for (int t = 0; t < 2; ++t) {
+            mbar_init(B(ctl->k_full[t]), 1);
+            mbar_init(B(ctl->v_full[t]), 1);
             mbar_init(B(ctl->q_full[t]), 1);
             mbar_init(B(ctl->s_full[t]), 1);
             mbar_init(B(ctl->p_half[t]), 4);
@@ -116,12 +115,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t pol = l2_evict_normal();
             uint32_t np = 0u;
             bool ok = true;
-            auto panel = [&](const CUtensorMap *map, int c0, int c1, int tok) {
-                const uint32_t st = np % kSlots, bar = B(ctl->full[st]);
+            // the first panel of a tile announces the bytes of all of them
+            auto panel = [&](const CUtensorMap *map, uint32_t bar, int first_of, int c0, int c1, int tok) {
+                const uint32_t st = np % kSlots;
                 if (ok) ok = waits.warp(B(ctl->empty[st]), ((np / kSlots) & 1u) ^ 1u, SITE_LF_EMPTY);
                 if (!ok) return;
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(bar, kPanel);
+                    if (first_of > 0) mbar_arrive_expect_tx(bar, first_of * kPanel);
                     tma_load_3d(sRing + st * kPanel, map, bar, c0, c1, tok, pol);
                 }
                 __syncwarp();
@@ -137,17 +137,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             };
             q_tile(0);
-            for (int j = 0; ok && j < n; ++j) {
+            int j = 0;
+            for (; ok && j < n; ++j) {
                 const int tok = un.k0 + j * kKeys;
-                panel(&tmK, 0, un.head, tok);
-                panel(&tmK, 64, un.head, tok);
-                panel(&tmR, 0, 0, tok);
+                const uint32_t kb = B(ctl->k_full[j & 1]), vb = B(ctl->v_full[j & 1]);
+                panel(&tmK, kb, kKPanels, 0, un.head, tok);
+                panel(&tmK, kb, 0, 64, un.head, tok);
+                panel(&tmR, kb, 0, 0, 0, tok);
                 if (j == 0 && two) q_tile(1);
-                panel(&tmV, 0, un.head, tok);
-                panel(&tmV, 64, un.head, tok);
+                panel(&tmV, vb, kVPanels, 0, un.head, tok);
+                panel(&tmV, vb, 0, 64, un.head, tok);
             }
             // wait (bounded) for the last copies, so that none lands after the CTA
-            for (uint32_t i = np > kSlots ? np - kSlots : 0u; i < np; ++i) drain_wait(B(ctl->full[i % kSlots]), (i / kSlots) & 1u, p.s.timeout_ns);
+            for (int k = max(j - 2, 0); k < j; ++k) {
+                drain_wait(B(ctl->k_full[k & 1]), (k >> 1) & 1u, p.s.timeout_ns);
+                drain_wait(B(ctl->v_full[k & 1]), (k >> 1) & 1u, p.s.timeout_ns);
+            }
             drain_wait(B(ctl->q_full[0]), 0u, p.s.timeout_ns);
             if (two) drain_wait(B(ctl->q_full[1]), 0u, p.s.timeout_ns);
         } else if (warp == 8) {
@@ -156,17 +161,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             const uint32_t dq = desc_lo(sQ, 16), dk = desc_lo(sRing, 16), dv = desc_lo(sRing, kPanel);
             // K_j's panels are numbers 5 j .. 5 j + 2, V_j's 5 j + 3 and 5 j + 4
-            auto panels_there = [&](uint32_t first, int count) {
-                for (int i = 0; ok && i < count; ++i)
-                    ok = waits.warp(B(ctl->full[(first + i) % kSlots]), ((first + i) / kSlots) & 1u, SITE_LF_FULL);
-                tc_fence_after();
-                return ok;
-            };
-            auto issue_qk = [&](int t, uint32_t first) {
+            auto let_go = [&](uint32_t panel) { tc_commit_by(leader, B(ctl->empty[panel % kSlots])); };
+            auto issue_qk = [&](int t, uint32_t first, bool final) {
 #pragma unroll
-                for (int kk = 0; kk < 12; ++kk)  // 16 values a step
+                for (int kk = 0; kk < 12; ++kk) {  // 16 values a step
                     mma_ss_by(leader, tmem + t * 128, dq + (((t * kQPanels + kk / 4) * kPanel + (kk % 4) * 32) >> 4),
-                           dk + ((((first + kk / 4) % kSlots) * kPanel + (kk % 4) * 32) >> 4), IDESC_QK, kk > 0 ? 1u : 0u);
+                              dk + ((((first + kk / 4) % kSlots) * kPanel + (kk % 4) * 32) >> 4), IDESC_QK, kk > 0 ? 1u : 0u);
+                    if (kk % 4 == 3 && final) let_go(first + kk / 4);
+                }
+                tc_commit_by(leader, B(ctl->s_full[t]));
             };
             // a panel of V at a time: the two need not be neighbours in the ring
             auto issue_pv = [&](int t, uint32_t first, bool accumulate, int half) {
@@ -176,34 +179,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k2 = 0; k2 < 4; ++k2) {  // 16 keys a step
                         const int kk = half * 4 + k2;
                         mma_ts_by(leader, tmem + kTmO + t * 128 + pn * 64, tmem + t * 128 + kk * 8,
-                               dv + ((((first + pn) % kSlots) * kPanel + kk * 2048) >> 4), IDESC_PV, (accumulate || kk > 0) ? 1u : 0u);
+                                  dv + ((((first + pn) % kSlots) * kPanel + kk * 2048) >> 4), IDESC_PV, (accumulate || kk > 0) ? 1u : 0u);
                     }
             };
-            auto release = [&](uint32_t first, int count) {
-                for (int i = 0; i < count; ++i) tc_commit_by(leader, B(ctl->empty[(first + i) % kSlots]));
-            };
-            ok = waits.warp(B(ctl->q_full[0]), 0u, SITE_LF_Q);
-            if (ok && panels_there(0u, kKPanels)) {
-                issue_qk(0, 0u);
-                tc_commit_by(leader, B(ctl->s_full[0]));
-            }
-            if (ok && two) ok = waits.warp(B(ctl->q_full[1]), 0u, SITE_LF_Q);
+            ok = waits.warp(B(ctl->q_full[0]), 0u, B(ctl->k_full[0]), 0u, SITE_LF_Q);
             if (ok) {
                 tc_fence_after();
-                if (two) {
-                    issue_qk(1, 0u);
-                    tc_commit_by(leader, B(ctl->s_full[1]));
-                }
-                release(0u, kKPanels);
+                issue_qk(0, 0u, !two);
+            }
+            if (ok && two) {
+                ok = waits.warp(B(ctl->q_full[1]), 0u, SITE_LF_Q);
+                tc_fence_after();
+                if (ok) issue_qk(1, 0u, true);
             }
             for (int j = 0; ok && j < n; ++j) {
                 const uint32_t vs = 5u * j + 3u, ks = vs + 2u, par = j & 1u;
+                const uint32_t vb = B(ctl->v_full[par]), vpar = (j >> 1) & 1u;
                 const bool more = j + 1 < n;
-                if (!panels_there(vs, kVPanels)) break;
+                ok = more ? waits.warp(vb, vpar, B(ctl->k_full[par ^ 1u]), ((j + 1) >> 1) & 1u, SITE_LF_FULL) : waits.warp(vb, vpar, SITE_LF_FULL);
+                if (!ok) break;
                 // keys past the end of the sequence: their weights are 0, and so must be what they meet
                 if (un.sk - j * kKeys < kKeys)
                     for (int pn = 0; pn < kVPanels; ++pn) zero_panel_rows(sRing + ((vs + pn) % kSlots) * kPanel, un.sk - j * kKeys, kKeys);
-                if (more && !panels_there(ks, kKPanels)) break;
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     if (t == 1 && !two) break;
@@ -214,14 +211,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!(ok = waits.warp(B(ctl->p_full[t]), par, SITE_LF_P))) break;
                     tc_fence_after();
                     issue_pv(t, vs, true, 1);
-                    if (final) release(vs, kVPanels);
-                    if (more) {
-                        issue_qk(t, ks);
-                        tc_commit_by(leader, B(ctl->s_full[t]));
-                        if (final) release(ks, kKPanels);
-                    } else {
-                        tc_commit_by(leader, B(ctl->o_full[t]));
-                    }
+                    if (final) let_go(vs), let_go(vs + 1u);
+                    if (more) issue_qk(t, ks, final);
+                    else tc_commit_by(leader, B(ctl->o_full[t]));
                 }
             }
             // every product completes before tensor memory is freed

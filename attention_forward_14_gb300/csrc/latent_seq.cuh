@@ -61,6 +61,13 @@ struct BoundedWaits {
             }
         }
     }
+    // two of them: the second is looked at while the first's answer is on its way
+    __device__ __forceinline__ bool warp(uint32_t bar_a, uint32_t parity_a, uint32_t bar_b, uint32_t parity_b, uint32_t site) const
+    {
+        bool a = mbar_try_wait(bar_a, parity_a), b = mbar_try_wait(bar_b, parity_b);
+        if (!(a && b)) a = one(bar_a, parity_a, site), b = one(bar_b, parity_b, site);
+        return static_cast<bool>(__all_sync(0xffffffffu, a && b));
+    }
     // by every lane of a warp, with a warp-uniform result
     __device__ __forceinline__ bool warp(uint32_t bar, uint32_t parity, uint32_t site) const
     {
