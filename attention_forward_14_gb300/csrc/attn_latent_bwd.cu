@@ -143,30 +143,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     KeysCtl *ctl = reinterpret_cast<KeysCtl *>(smem);
     auto B = [&](const uint64_t &bar) { return smem_addr(&bar); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    await_previous();
-
-    const LatentUnit un = latent_unit(p.s, blockIdx.x, p.k_blocks, p.group, kKeys, false);
-    if (un.row0 >= un.sk) return;
-    const int key0 = un.row0, off = un.sk - un.sq;  // query i sees keys j <= i + off
-    if (!ATTN_OPS_IN_BOUNDS(un.head < p.s.h && un.q0 + un.sq <= p.s.total_q && un.k0 + un.sk <= p.s.total_k, p.s, SITE_OPS_UNIT)) return;
-    const int first = CAUSAL ? max(key0 - off, 0) / kQueries : 0;  // tile of queries
-    const int n = max((un.sq + kQueries - 1) / kQueries - first, 0);
-
-    auto dv_row = [&](int key) { return static_cast<T *>(p.dv) + (un.k0 + key) * p.dvt + un.head * p.dvh; };
-    auto dkn_row = [&](int key) { return static_cast<T *>(p.dkn) + (un.k0 + key) * p.dknt + un.head * p.dknh; };
-    auto dkr_row = [&](int key) { return p.kr_part + (static_cast<int64_t>(un.head) * p.s.total_k + un.k0 + key) * kLatentRope; };
-    if (n == 0) {  // keys that no query sees
-        for (int i = threadIdx.x; i < kKeys * 16; i += kThreads) {
-            const int key = key0 + i / 16, c = i % 16;
-            if (key >= un.sk) break;
-            reinterpret_cast<uint4 *>(dv_row(key))[c] = make_uint4(0u, 0u, 0u, 0u);
-            reinterpret_cast<uint4 *>(dkn_row(key))[c] = make_uint4(0u, 0u, 0u, 0u);
-            reinterpret_cast<uint4 *>(dkr_row(key))[c] = make_uint4(0u, 0u, 0u, 0u);
-        }
-        return;
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmG);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmR);
+        tma_prefetch_desc(&tmV);
     }
-
-    const BoundedWaits waits{&ctl->abort, p.s.status, p.s.timeout_ns};
+    await_previous();
+    const LatentWork work = latent_work(p.s, blockIdx.x, p.k_blocks, p.group, kKeys, false);  // in its memory's time, what follows
     if (threadIdx.x == 0) {
         mbar_init(B(ctl->v_full), 1);
         mbar_init(B(ctl->k_full), 1);
@@ -192,6 +177,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
+    const auto done = [&]() {
+        if (warp == 8) tmem_dealloc(tmem, 512);
+    };
+
+    const LatentUnit un = latent_unit(p.s, work);
+    if (un.row0 >= un.sk) return done();
+    const int key0 = un.row0, off = un.sk - un.sq;  // query i sees keys j <= i + off
+    if (!ATTN_OPS_IN_BOUNDS(un.head < p.s.h && un.q0 + un.sq <= p.s.total_q && un.k0 + un.sk <= p.s.total_k, p.s, SITE_OPS_UNIT)) return done();
+    const int first = CAUSAL ? max(key0 - off, 0) / kQueries : 0;  // tile of queries
+    const int n = max((un.sq + kQueries - 1) / kQueries - first, 0);
+
+    auto dv_row = [&](int key) { return static_cast<T *>(p.dv) + (un.k0 + key) * p.dvt + un.head * p.dvh; };
+    auto dkn_row = [&](int key) { return static_cast<T *>(p.dkn) + (un.k0 + key) * p.dknt + un.head * p.dknh; };
+    auto dkr_row = [&](int key) { return p.kr_part + (static_cast<int64_t>(un.head) * p.s.total_k + un.k0 + key) * kLatentRope; };
+    if (n == 0) {  // keys that no query sees
+        for (int i = threadIdx.x; i < kKeys * 16; i += kThreads) {
+            const int key = key0 + i / 16, c = i % 16;
+            if (key >= un.sk) break;
+            reinterpret_cast<uint4 *>(dv_row(key))[c] = make_uint4(0u, 0u, 0u, 0u);
+            reinterpret_cast<uint4 *>(dkn_row(key))[c] = make_uint4(0u, 0u, 0u, 0u);
+            reinterpret_cast<uint4 *>(dkr_row(key))[c] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        return done();
+    }
+    const BoundedWaits waits{&ctl->abort, p.s.status, p.s.timeout_ns};
 
     if (warp >= 8) {
         regs_dec<kOtherRegs>();
@@ -451,25 +461,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     QueriesCtl *ctl = reinterpret_cast<QueriesCtl *>(smem);
     auto B = [&](const uint64_t &bar) { return smem_addr(&bar); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    await_previous();
-
-    const LatentUnit un = latent_unit(p.s, blockIdx.x, p.q_blocks, p.group, ROWS, true);
-    if (un.row0 >= un.sq) return;
-    if (!ATTN_OPS_IN_BOUNDS(un.head < p.s.h && un.q0 + un.sq <= p.s.total_q && un.k0 + un.sk <= p.s.total_k, p.s, SITE_OPS_UNIT)) return;
-    const int last = min(un.row0 + ROWS, un.sq) - 1;
-    const int kend = CAUSAL ? max(min(un.sk, last + 1 + un.sk - un.sq), 0) : un.sk;
-    const int n = (kend + TILE - 1) / TILE;
-    auto dq_row = [&](int q) { return static_cast<T *>(p.dq) + (un.q0 + q) * p.dqt + un.head * p.dqh; };
-    if (n == 0) {  // rows that see no key
-        for (int i = threadIdx.x; i < ROWS * (kLatentKey / 8); i += kThreads) {
-            const int q = un.row0 + i / (kLatentKey / 8);
-            if (q >= un.sq) break;
-            reinterpret_cast<uint4 *>(dq_row(q))[i % (kLatentKey / 8)] = make_uint4(0u, 0u, 0u, 0u);
-        }
-        return;
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmG);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmR);
+        tma_prefetch_desc(&tmV);
     }
-
-    const BoundedWaits waits{&ctl->abort, p.s.status, p.s.timeout_ns};
+    await_previous();
+    const LatentWork work = latent_work(p.s, blockIdx.x, p.q_blocks, p.group, ROWS, true);  // in its memory's time, what follows
     if (threadIdx.x == 0) {
         mbar_init(B(ctl->q_full), 1);
         mbar_init(B(ctl->g_full), 1);
@@ -494,6 +494,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
+    const auto done = [&]() {
+        if (warp == 8) tmem_dealloc(tmem, 512);
+    };
+
+    const LatentUnit un = latent_unit(p.s, work);
+    if (un.row0 >= un.sq) return done();
+    if (!ATTN_OPS_IN_BOUNDS(un.head < p.s.h && un.q0 + un.sq <= p.s.total_q && un.k0 + un.sk <= p.s.total_k, p.s, SITE_OPS_UNIT)) return done();
+    const int last = min(un.row0 + ROWS, un.sq) - 1;
+    const int kend = CAUSAL ? max(min(un.sk, last + 1 + un.sk - un.sq), 0) : un.sk;
+    const int n = (kend + TILE - 1) / TILE;
+    auto dq_row = [&](int q) { return static_cast<T *>(p.dq) + (un.q0 + q) * p.dqt + un.head * p.dqh; };
+    if (n == 0) {  // rows that see no key
+        for (int i = threadIdx.x; i < ROWS * (kLatentKey / 8); i += kThreads) {
+            const int q = un.row0 + i / (kLatentKey / 8);
+            if (q >= un.sq) break;
+            reinterpret_cast<uint4 *>(dq_row(q))[i % (kLatentKey / 8)] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        return done();
+    }
+    const BoundedWaits waits{&ctl->abort, p.s.status, p.s.timeout_ns};
 
     if (warp >= 8) {
         regs_dec<kOtherRegs>();

@@ -39,10 +39,37 @@ enum : uint32_t { SITE_LF_EMPTY = 90, SITE_LF_FULL = 91, SITE_LF_Q = 92, SITE_LF
 
 struct FwdCtl {
     uint64_t k_full[2], v_full[2], empty[kSlots];  // of even and of odd tiles; of each panel's slot
-    uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], mma_done;
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], mma_done;
     uint32_t tmem_base, abort;
 };
 static_assert(sizeof(FwdCtl) <= kCtl, "control block");
+
+// p = 2^(s * c - m) for the 128 scores of a row, rounded to T into the first 64
+// tensor-memory columns at tS (asynchronous stores).  Returns the sum of p and
+// the sum of p as rounded.
+template <typename T>
+__device__ __forceinline__ float2 store_weights(const uint32_t (&s)[128], float c, float m, uint32_t tS)
+{
+    const float2 c2 = make_float2(c, c), m2 = make_float2(-m, -m);
+    float2 l[2], lr[2];
+    l[0] = l[1] = lr[0] = lr[1] = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const int e = 64 * h + 2 * i;
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, m2);
+            const float2 v = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            l[i & 1] = __fadd2_rn(l[i & 1], v);
+            pk[i] = Pair<T>::put(v.x, v.y);
+            lr[i & 1] = __fadd2_rn(lr[i & 1], Pair<T>::get(pk[i]));
+        }
+        tmem_st32(tS + 32 * h, pk);
+    }
+    const float2 a = __fadd2_rn(l[0], l[1]), b = __fadd2_rn(lr[0], lr[1]);
+    return make_float2(a.x + a.y, b.x + b.y);
+}
 
 template <typename T, bool CAUSAL>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -52,7 +79,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 {
     constexpr bool BF16 = Elem<T>::BF16;
     constexpr uint32_t IDESC_QK = idesc_f16(kRows, kKeys, BF16, false);
-    constexpr uint32_t IDESC_PV = idesc_f16(kRows, 64, BF16, true);
+    constexpr uint32_t IDESC_PV = idesc_f16(kRows, 128, BF16, true), IDESC_PV_HALF = idesc_f16(kRows, 64, BF16, true);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw_addr = smem_addr(smem_raw);
     const uint32_t base = (raw_addr + 1023u) & ~1023u;
@@ -61,29 +88,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sQ = base + kQOff, sRing = base + kRingOff;
     auto B = [&](const uint64_t &bar) { return smem_addr(&bar); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    await_previous();
-
-    // The unit: rows row0 .. of sequence seq; heads of a group together, heaviest blocks first.
-    const LatentUnit un = latent_unit(p.s, blockIdx.x, p.blocks, p.group, kUnitRows, true);
-    if (un.row0 >= un.sq) return;
-    const int last = min(un.row0 + kUnitRows, un.sq) - 1;
-    const int kend = CAUSAL ? max(min(un.sk, last + 1 + un.sk - un.sq), 0) : un.sk;
-    const int n = (kend + kKeys - 1) / kKeys;
-    const bool two = un.row0 + kRows < un.sq;  // Q tile 1 has rows
-    if (!ATTN_OPS_IN_BOUNDS(un.head < p.s.h && un.q0 + un.sq <= p.s.total_q && un.k0 + un.sk <= p.s.total_k, p.s, SITE_OPS_UNIT)) return;
-    if (n == 0) {  // rows that see no key
-        for (int i = threadIdx.x; i < kUnitRows * (kLatentValue / 8); i += kThreads) {
-            const int r = un.row0 + i / (kLatentValue / 8);
-            if (r >= un.sq) break;
-            reinterpret_cast<uint4 *>(static_cast<T *>(p.o) + (un.q0 + r) * p.ot + un.head * p.oh)[i % (kLatentValue / 8)] =
-                make_uint4(0u, 0u, 0u, 0u);
-        }
-        for (int r = un.row0 + threadIdx.x; p.lse && r <= last; r += kThreads)
-            p.lse[static_cast<int64_t>(un.head) * p.s.total_q + un.q0 + r] = -INFINITY;
-        return;
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmR);
+        tma_prefetch_desc(&tmV);
     }
-
-    BoundedWaits waits{&ctl->abort, p.s.status, p.s.timeout_ns};
+    await_previous();
+    const LatentWork work = latent_work(p.s, blockIdx.x, p.blocks, p.group, kUnitRows, true);  // in its memory's time, what follows
     if (threadIdx.x == 0) {
         for (int i = 0; i < kSlots; ++i) mbar_init(B(ctl->empty[i]), 1);
         for (int t = 0; t < 2; ++t) {
@@ -91,7 +103,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(B(ctl->v_full[t]), 1);
             mbar_init(B(ctl->q_full[t]), 1);
             mbar_init(B(ctl->s_full[t]), 1);
-            mbar_init(B(ctl->p_half[t]), 4);
             mbar_init(B(ctl->p_full[t]), 4);
             mbar_init(B(ctl->o_full[t]), 1);
         }
@@ -107,6 +118,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
+    const auto done = [&]() {
+        if (warp == 8) tmem_dealloc(tmem, 512);
+    };
+
+    // rows row0 .. of sequence seq: heads of a group together, heaviest blocks first
+    const LatentUnit un = latent_unit(p.s, work);
+    if (un.row0 >= un.sq) return done();
+    const int last = min(un.row0 + kUnitRows, un.sq) - 1;
+    const int kend = CAUSAL ? max(min(un.sk, last + 1 + un.sk - un.sq), 0) : un.sk;
+    const int n = (kend + kKeys - 1) / kKeys;
+    const bool two = un.row0 + kRows < un.sq;  // Q tile 1 has rows
+    if (!ATTN_OPS_IN_BOUNDS(un.head < p.s.h && un.q0 + un.sq <= p.s.total_q && un.k0 + un.sk <= p.s.total_k, p.s, SITE_OPS_UNIT)) return done();
+    if (n == 0) {  // rows that see no key
+        for (int i = threadIdx.x; i < kUnitRows * (kLatentValue / 8); i += kThreads) {
+            const int r = un.row0 + i / (kLatentValue / 8);
+            if (r >= un.sq) break;
+            reinterpret_cast<uint4 *>(static_cast<T *>(p.o) + (un.q0 + r) * p.ot + un.head * p.oh)[i % (kLatentValue / 8)] =
+                make_uint4(0u, 0u, 0u, 0u);
+        }
+        for (int r = un.row0 + threadIdx.x; p.lse && r <= last; r += kThreads)
+            p.lse[static_cast<int64_t>(un.head) * p.s.total_q + un.q0 + r] = -INFINITY;
+        return done();
+    }
+    BoundedWaits waits{&ctl->abort, p.s.status, p.s.timeout_ns};
 
     if (warp >= 8) {
         regs_dec<kOtherRegs>();
@@ -171,16 +206,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_commit_by(leader, B(ctl->s_full[t]));
             };
-            // a panel of V at a time: the two need not be neighbours in the ring
-            auto issue_pv = [&](int t, uint32_t first, bool accumulate, int half) {
+            auto issue_pv = [&](int t, uint32_t first, bool accumulate) {
+                const uint32_t o = tmem + kTmO + t * 128, pt = tmem + t * 128, v = first % kSlots;
+                if (v + 1u < kSlots) {
 #pragma unroll
-                for (int pn = 0; pn < 2; ++pn)
+                    for (int kk = 0; kk < 8; ++kk)  // 16 keys a step
+                        mma_ts_by(leader, o, pt + kk * 8, dv + ((v * kPanel + kk * 2048) >> 4), IDESC_PV, (accumulate || kk > 0) ? 1u : 0u);
+                } else {  // the ring's last slot and its first, a panel at a time
+#pragma unroll 1
+                    for (uint32_t pn = 0; pn < 2; ++pn)
 #pragma unroll
-                    for (int k2 = 0; k2 < 4; ++k2) {  // 16 keys a step
-                        const int kk = half * 4 + k2;
-                        mma_ts_by(leader, tmem + kTmO + t * 128 + pn * 64, tmem + t * 128 + kk * 8,
-                                  dv + ((((first + pn) % kSlots) * kPanel + kk * 2048) >> 4), IDESC_PV, (accumulate || kk > 0) ? 1u : 0u);
-                    }
+                        for (int kk = 0; kk < 8; ++kk)
+                            mma_ts_by(leader, o + pn * 64, pt + kk * 8, dv + ((((v + pn) % kSlots) * kPanel + kk * 2048) >> 4), IDESC_PV_HALF,
+                                      (accumulate || kk > 0) ? 1u : 0u);
+                }
             };
             ok = waits.warp(B(ctl->q_full[0]), 0u, B(ctl->k_full[0]), 0u, SITE_LF_Q);
             if (ok) {
@@ -194,10 +233,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             for (int j = 0; ok && j < n; ++j) {
                 const uint32_t vs = 5u * j + 3u, ks = vs + 2u, par = j & 1u;
-                const uint32_t vb = B(ctl->v_full[par]), vpar = (j >> 1) & 1u;
                 const bool more = j + 1 < n;
-                ok = more ? waits.warp(vb, vpar, B(ctl->k_full[par ^ 1u]), ((j + 1) >> 1) & 1u, SITE_LF_FULL) : waits.warp(vb, vpar, SITE_LF_FULL);
-                if (!ok) break;
+                if (!(ok = waits.warp(B(ctl->v_full[par]), (j >> 1) & 1u, SITE_LF_FULL))) break;
                 // keys past the end of the sequence: their weights are 0, and so must be what they meet
                 if (un.sk - j * kKeys < kKeys)
                     for (int pn = 0; pn < kVPanels; ++pn) zero_panel_rows(sRing + ((vs + pn) % kSlots) * kPanel, un.sk - j * kKeys, kKeys);
@@ -205,12 +242,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int t = 0; t < 2; ++t) {
                     if (t == 1 && !two) break;
                     const bool final = t == 1 || !two;  // of the tile's products
-                    if (!(ok = waits.warp(B(ctl->p_half[t]), par, SITE_LF_P))) break;
-                    tc_fence_after();
-                    issue_pv(t, vs, j > 0, 0);
                     if (!(ok = waits.warp(B(ctl->p_full[t]), par, SITE_LF_P))) break;
                     tc_fence_after();
-                    issue_pv(t, vs, true, 1);
+                    issue_pv(t, vs, j > 0);
+                    if (t == 0 && more && !(ok = waits.warp(B(ctl->k_full[par ^ 1u]), ((j + 1) >> 1) & 1u, SITE_LF_FULL))) break;
                     if (final) let_go(vs), let_go(vs + 1u);
                     if (more) issue_qk(t, ks, final);
                     else tc_commit_by(leader, B(ctl->o_full[t]));
@@ -254,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         lr *= f;
                         m = m_new;
                     }
-                    const float2 sums = exp_store_tile<T, false>(s, 0, c, m == -INFINITY ? 0.f : m, tS, B(ctl->p_half[t]));
+                    const float2 sums = store_weights<T>(s, c, m == -INFINITY ? 0.f : m, tS);
                     l += sums.x;
                     lr += sums.y;
                     warp_announce_tmem(B(ctl->p_full[t]));

@@ -20,21 +20,32 @@ struct LatentUnit {
 // the blocks of some heads together, so that the L2 holds what they share; of
 // queries (`last_first`) the later blocks, which see more keys, first.  A
 // sequence whose offsets fall outside the totals is empty.
-__device__ __forceinline__ LatentUnit latent_unit(const LatentSeqs &s, unsigned u, int blocks, int group, int rows, bool last_first)
+struct LatentWork {
+    int head, row0, q0, q1, k0, k1;
+};
+
+// (What the answer takes from memory is on its way when this returns, and
+// looked at by latent_unit.)
+__device__ __forceinline__ LatentWork latent_work(const LatentSeqs &s, unsigned u, int blocks, int group, int rows, bool last_first)
 {
     const unsigned per_seq = static_cast<unsigned>(blocks) * s.h, seq = u / per_seq;
+    LatentWork w;
+    w.q0 = s.cu_q[seq], w.q1 = s.cu_q[seq + 1], w.k0 = s.cu_k[seq], w.k1 = s.cu_k[seq + 1];
     u -= seq * per_seq;
     const unsigned hg = u / (blocks * group);
     u -= hg * blocks * group;
     const int heads = min(group, s.h - static_cast<int>(hg) * group);
     const int blk = u / heads;
-    LatentUnit un;
-    un.head = hg * group + u - blk * heads;
-    un.q0 = s.cu_q[seq], un.sq = s.cu_q[seq + 1] - un.q0;
-    un.k0 = s.cu_k[seq], un.sk = s.cu_k[seq + 1] - un.k0;
+    w.head = hg * group + u - blk * heads;
+    w.row0 = (last_first ? blocks - 1 - blk : blk) * rows;
+    return w;
+}
+
+__device__ __forceinline__ LatentUnit latent_unit(const LatentSeqs &s, const LatentWork &w)
+{
+    LatentUnit un{w.head, w.row0, w.q0, w.q1 - w.q0, w.k0, w.k1 - w.k0};
     if (un.q0 < 0 || un.sq < 0 || un.q0 > s.total_q - un.sq || un.k0 < 0 || un.sk < 0 || un.k0 > s.total_k - un.sk)
         un.q0 = un.sq = un.k0 = un.sk = 0;
-    un.row0 = (last_first ? blocks - 1 - blk : blk) * rows;
     return un;
 }
 
