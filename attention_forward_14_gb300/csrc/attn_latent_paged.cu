@@ -316,11 +316,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         return ok;
     };
     // Of an item: the CTA's first row, its tiles within the share, and the keys that all of its rows see.
-    auto first_row = [&]() { return static_cast<int64_t>(at.group * p.team + rank) * N; };
-    auto item_tiles = [&](int j_end) { return at.end > 0 && first_row() < p.rows ? j_end - at.j : 0; };
+    auto first_row = [&](const LatentPlace &c) { return static_cast<int64_t>(c.group * p.team + rank) * N; };
+    auto item_tiles = [&](const LatentPlace &c, int j_end) { return c.end > 0 && first_row(c) < p.rows ? j_end - c.j : 0; };
     auto all_see = [&]() {
         if (p.mask == LATENT_MASK_NONE) return at.len;
-        const int i0 = p.mask == LATENT_MASK_TREE ? -1 : static_cast<int>(first_row()) / p.h;
+        const int i0 = p.mask == LATENT_MASK_TREE ? -1 : static_cast<int>(first_row(at)) / p.h;
         return min(max(at.len - p.sq + i0 + 1, 0), at.len);
     };
 
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int it = 0; ok && it < n_units;) {
                 if (!place_in_bounds()) break;
                 const int j_end = min(at.n, at.j + n_units - it);
-                const int tiles = item_tiles(j_end);
+                const int tiles = item_tiles(at, j_end);
                 const int32_t *table = p.block_table + static_cast<int64_t>(at.b) * p.pages_per_seq;
                 // where the lane's keys of a tile lie: a copy begins there, or none (-1)
                 auto token_of = [&](int t) {
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int it = 0; ok && it < n_units;) {
                 if (!place_in_bounds()) break;
                 const int j_end = min(at.n, at.j + n_units - it);
-                const int tiles = item_tiles(j_end);
+                const int tiles = item_tiles(at, j_end);
                 const int all = all_see();
                 for (int t = 0; ok && t < tiles; ++t, np += kPairs) {
                     const int k0 = (at.j + t) * kTileKeys;
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int it = 0; ok && it < n_units;) {
                 if (!place_in_bounds()) break;
                 const int j_end = min(at.n, at.j + n_units - it);
-                const int tiles = item_tiles(j_end);
+                const int tiles = item_tiles(at, j_end);
                 const int all = all_see();
                 if (tiles > 0) ok = warp_waits(B(ctl->q_full), q_it++ & 1u, SITE_LAT_Q);
                 for (int t = 0; ok && t < tiles; ++t, np += kPairs, ++nk, ++tile_it) {
@@ -499,11 +499,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto group_sync = [&]() { named_barrier(bar_id, 128); };
         uint32_t tile_it = 0u, nk = 0u;
         bool ok = true;
+        // An item's rows of Q: 72 pieces of 16 bytes a row, all of them on their way at once; eight lanes to a panel's row.
+        auto ask_q = [&](const LatentPlace &c) {
+            const int64_t row0 = first_row(c);
+            const int nr = static_cast<int>(min(static_cast<int64_t>(N), p.rows - row0)), sub = lane & 7;
+            const T *q = static_cast<const T *>(p.q) + c.b * p.qb;
+            for (int r = warp * 4 + (lane >> 3); r < N; r += 32) {
+                const int row = static_cast<int>(row0) + min(r, nr - 1), i = row / p.h, head = row - i * p.h;
+                const uint4 *src = reinterpret_cast<const uint4 *>(q + head * p.qh + i * p.qs) + sub;
+                const uint32_t to = sQ + r * 128 + ((sub ^ (r & 7)) << 4);
+#pragma unroll
+                for (int pn = 0; pn < kPanels; ++pn) cp_async16(to + pn * C::Q_PANEL, src + pn * 8, r < nr);
+            }
+        };
+        auto give_q = [&]() {
+            cp_async_wait_all();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(B(ctl->q_full));
+        };
         for (int it = 0; it < n_units;) {
             if (!place_in_bounds()) break;
             const int j_end = min(at.n, at.j + n_units - it);
-            const int tiles = item_tiles(j_end);
-            const int64_t row0 = first_row();
+            const int tiles = item_tiles(at, j_end);
+            const int64_t row0 = first_row(at);
             const int nr = static_cast<int>(min(static_cast<int64_t>(N), max(p.rows - row0, int64_t(0))));
             const int all = all_see(), before = at.len - p.sq;
             // The rows of the group's half that see key k: query by query, since a query's heads stand together.
@@ -533,21 +552,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ctl->query[r] = i;
                 ctl->o_at[r] = at.b * p.ob + head * p.oh + i * p.os;
             }
-            if (tiles > 0) {
-                // 72 pieces of 16 bytes a row, all of them on their way at once; eight lanes to a panel's row
-                const T *q = static_cast<const T *>(p.q) + at.b * p.qb;
-                const int sub = lane & 7;
-                for (int r = warp * 4 + (lane >> 3); r < N; r += 32) {
-                    const int row = static_cast<int>(row0) + min(r, nr - 1), i = row / p.h, head = row - i * p.h;
-                    const uint4 *src = reinterpret_cast<const uint4 *>(q + head * p.qh + i * p.qs) + sub;
-                    const uint32_t to = sQ + r * 128 + ((sub ^ (r & 7)) << 4);
-#pragma unroll
-                    for (int pn = 0; pn < kPanels; ++pn) cp_async16(to + pn * C::Q_PANEL, src + pn * 8, r < nr);
-                }
-                cp_async_wait_all();
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(B(ctl->q_full));
+            if (it == 0 && tiles > 0) {
+                ask_q(at);
+                give_q();
             }
             if (key < COLS) ctl->ref[w * COLS + key] = 0.f;
             float2 l[COLS / 2], lr[COLS / 2];
@@ -645,6 +652,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(B(ctl->p_full));
             }
+            // The next item's Q, as soon as the last scores are there: its first products run while this one is stored.
+            LatentPlace next = at;
+            set_entry(p, next, at.entry + 1, N);
+            const int left = n_units - it - (j_end - at.j);
+            const bool goes_on = left > 0 && item_tiles(next, min(next.n, left)) > 0;
+            if (goes_on) ask_q(next);
             // the item ends, or goes on in the next team
             const bool item_ends = j_end == at.n;
             const int64_t first_unit = u0 + it - at.j;  // of the item
@@ -680,6 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             group_sync();
+            if (goes_on) give_q();
             if (tiles > 0) {
                 if (ok) ok = warp_waits(B(ctl->pv_done), (tile_it - 1) & 1u, SITE_LAT_O);
                 tc_fence_after();
@@ -722,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     p.cut[team] = LatentCut{first_unit > u0 ? -parts : parts, at.entry, {0, 0}};
                 }
             }
-            set_entry(p, at, at.entry + 1, N);
+            at = next;
         }
     }
     tc_fence_before();
