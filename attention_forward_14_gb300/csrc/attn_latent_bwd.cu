@@ -439,7 +439,10 @@ struct QueriesCfg {
 
 struct QueriesCtl {
     uint64_t q_full, g_full, q_moved, full[4], empty[4];
-    uint64_t s_full, s_free, dp_full, ds_full, acc_full;
+    // (of dP and dS one for each of the two tiles: a tile's dP may be there
+    // before the slowest warp has looked for that of the tile before, and one
+    // barrier's phase would then be the other again)
+    uint64_t s_full, s_free, dp_full[2], ds_full[2], acc_full;
     uint32_t tmem_base, abort;
 };
 static_assert(sizeof(QueriesCtl) <= QueriesCfg::G_OFF, "control block");
@@ -480,8 +483,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(B(ctl->s_full), 1);
         mbar_init(B(ctl->s_free), 8);
-        mbar_init(B(ctl->dp_full), 1);
-        mbar_init(B(ctl->ds_full), 8);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(B(ctl->dp_full[i]), 1);
+            mbar_init(B(ctl->ds_full[i]), 8);
+        }
         mbar_init(B(ctl->acc_full), 1);
         ctl->abort = 0u;
         fence_barrier_init();
@@ -575,13 +580,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int kk = 0; kk < 8; ++kk)
                     mma_ss_by(leader, tmem + C::TM_DP + (j & 1) * 64, dg + (((kk / 4) * kPanel + (kk % 4) * 32) >> 4),
                            kv + (((3 + kk / 4) * C::HALF + (kk % 4) * 32) >> 4), IDESC_S, kk > 0 ? 1u : 0u);
-                tc_commit_by(leader, B(ctl->dp_full));
+                tc_commit_by(leader, B(ctl->dp_full[j & 1]));
                 return true;
             };
             bool ok = waits.warp(B(ctl->q_moved), 0u, SITE_LB_KV) && waits.warp(B(ctl->g_full), 0u, SITE_LB_KV) && scores(0);
             for (int j = 0; ok && j < n; ++j) {
                 if (j + 1 < n && !(ok = scores(j + 1))) break;
-                if (!(ok = waits.warp(B(ctl->ds_full), j & 1u, SITE_LB_DS))) break;
+                if (!(ok = waits.warp(B(ctl->ds_full[j & 1]), (j >> 1) & 1u, SITE_LB_DS))) break;
                 tc_fence_after();
                 {
                     const uint32_t st = j % C::STAGES;
@@ -628,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), scale2, lse2);
                     pr[c] = make_float2(ex2_approx(x.x), ex2_approx(x.y));
                 }
-                if (!(ok = waits.warp(B(ctl->dp_full), j & 1u, SITE_LB_DP))) return;
+                if (!(ok = waits.warp(B(ctl->dp_full[j & 1]), (j >> 1) & 1u, SITE_LB_DP))) return;
                 tc_fence_after();
                 const uint32_t tDP = at + C::TM_DP + (j & 1) * 64 + w * 32;
                 tmem_ld32_wait(tDP, s);
@@ -642,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     pk[c] = Pair<T>::put(x.x, x.y);
                 }
                 tmem_st16(tDP, pk);
-                warp_announce_tmem(B(ctl->ds_full));
+                warp_announce_tmem(B(ctl->ds_full[j & 1]));
             };
             if (__any_sync(0xffffffffu, vis < 32)) tile(std::true_type());
             else tile(std::false_type());

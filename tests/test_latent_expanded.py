@@ -119,6 +119,23 @@ def test_equal_calls_give_equal_bits():
 
 
 @gpu
+@pytest.mark.parametrize("causal", [False, True])
+def test_many_calls_in_a_row(causal):
+    """Small calls queued behind one another, whose warps run at uneven paces: no wait gives up, and all give equal bits."""
+    case = (4, (320,), (1024,), causal, "fp16")
+    q, kn, kr, v, gr, cu = make(case)
+    ins, packed = call(q, kn, kr, v, cu, case)
+    gr = on_gpu(gr)
+    binding.status_clear()
+    o, lse = af.attn_fwd_latent(*ins, *packed, causal=causal)
+    first = af.attn_bwd_latent(*ins, o, gr, lse, *packed, causal=causal)
+    for _ in range(200):
+        got = [af.attn_bwd_latent(*ins, o, gr, lse, *packed, causal=causal) for _ in range(20)]
+        assert all(torch.equal(a, b) for g in got for a, b in zip(g, first))
+    assert binding.status()[0] == 0
+
+
+@gpu
 def test_given_outputs_between_one_another():
     """o and the gradients into views of larger tensors; nothing else of those is written."""
     case = (4, (130, 3), (200, 3), True, "bf16")
