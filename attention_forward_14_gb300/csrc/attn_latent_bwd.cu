@@ -4,20 +4,23 @@
 //   dV = P^T dO,  dQ = scale dS [K_nope | K_rope],
 //   dK_nope = scale dS^T Q_nope,  dK_rope = scale sum over heads of dS^T Q_rope
 //
-// Four launches, in which every sum is added up in a fixed order:
+// Three launches, in which every sum is added up in a fixed order:
 //   D of every row;
-//   dK and dV: a CTA takes 128 keys of one head and streams the queries that
-//     see them, 64 at a time.  Keys are the lanes of tensor memory: S^T and
-//     dP^T (64 columns each), from which P^T and dS^T are left there as 16-bit
-//     operands (32 columns each), and the sums dV (128 columns) and dK (192):
-//     all 512.  A head's share of the shared key part's gradient is written in
-//     fp32;
-//   dQ: a CTA takes 128 queries of one head and streams the keys that they
-//     see, 128 at a time: S, dP (128 columns each), dS (64), and the sum dQ
-//     (192).  It computes S and dP again: 38% more products than one pass
-//     would take, but dK's 192 columns leave that one no room for dQ in tensor
-//     memory, and there are no sums by atomics;
+//   the units of keys, and behind them those of queries, which fill the SMs
+//   that the last of keys leave;
 //   the sum over the heads of the shared key part's gradient.
+// A unit of keys (dK, dV) is 128 keys of one head, to which the queries that
+// see them are streamed, 64 at a time.  Keys are the lanes of tensor memory:
+// S^T and dP^T (64 columns each), whose places P^T and dS^T take as 16-bit
+// operands, the sums dV (128 columns) and dK (192), and V as an operand (64):
+// all 512.  A head's share of the shared key part's gradient is written in
+// fp32.
+// A unit of queries (dQ) is 128 queries of one head, to which the keys that
+// they see are streamed, 64 at a time: S (64 columns), two tiles' dP (64
+// each), whose places dS takes, the sum dQ (192), and Q as an operand (96).
+// It computes S and dP again: 38% more products than one pass would take, but
+// dK's 192 columns leave that one no room for dQ in tensor memory, and there
+// are no sums by atomics.
 // In both, the softmax warps work on P while the tensor cores work on the sums
 // of the tile before, and on dS while they work on the next tile's scores.
 #include "latent.h"
@@ -127,10 +130,8 @@ struct KeysCtl {
 static_assert(sizeof(KeysCtl) <= KeysCfg::LD_OFF, "control block");
 
 template <typename T, bool CAUSAL>
-__global__ void __launch_bounds__(kThreads, 1)
-    latent_bwd_keys_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
-                           const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmR,
-                           const __grid_constant__ CUtensorMap tmV, const __grid_constant__ LatentBwdParams p)
+__device__ __forceinline__ void latent_bwd_keys(const CUtensorMap &tmQ, const CUtensorMap &tmG, const CUtensorMap &tmK, const CUtensorMap &tmR,
+                                 const CUtensorMap &tmV, const LatentBwdParams &p, unsigned unit)
 {
     using C = KeysCfg;
     constexpr bool BF16 = Elem<T>::BF16;
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tmV);
     }
     await_previous();
-    const LatentWork work = latent_work(p.s, blockIdx.x, p.k_blocks, p.group, kKeys, false);  // in its memory's time, what follows
+    const LatentCu cu = latent_cu(p.s);  // in its memory's time, what follows
     if (threadIdx.x == 0) {
         mbar_init(B(ctl->v_full), 1);
         mbar_init(B(ctl->k_full), 1);
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == 8) tmem_dealloc(tmem, 512);
     };
 
-    const LatentUnit un = latent_unit(p.s, work);
+    const LatentUnit un = latent_unit<kKeys, true>(p.s, cu, unit, p.k_slots, p.group);
     if (un.row0 >= un.sk) return done();
     const int key0 = un.row0, off = un.sk - un.sq;  // query i sees keys j <= i + off
     if (!ATTN_OPS_IN_BOUNDS(un.head < p.s.h && un.q0 + un.sq <= p.s.total_q && un.k0 + un.sk <= p.s.total_k, p.s, SITE_OPS_UNIT)) return done();
@@ -448,10 +449,8 @@ struct QueriesCtl {
 static_assert(sizeof(QueriesCtl) <= QueriesCfg::G_OFF, "control block");
 
 template <typename T, bool CAUSAL>
-__global__ void __launch_bounds__(kThreads, 1)
-    latent_bwd_queries_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
-                              const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmR,
-                              const __grid_constant__ CUtensorMap tmV, const __grid_constant__ LatentBwdParams p)
+__device__ __forceinline__ void latent_bwd_queries(const CUtensorMap &tmQ, const CUtensorMap &tmG, const CUtensorMap &tmK, const CUtensorMap &tmR,
+                                    const CUtensorMap &tmV, const LatentBwdParams &p, unsigned unit)
 {
     using C = QueriesCfg;
     constexpr int ROWS = 128, TILE = C::TILE;
@@ -472,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tmV);
     }
     await_previous();
-    const LatentWork work = latent_work(p.s, blockIdx.x, p.q_blocks, p.group, ROWS, true);  // in its memory's time, what follows
+    const LatentCu cu = latent_cu(p.s);  // in its memory's time, what follows
     if (threadIdx.x == 0) {
         mbar_init(B(ctl->q_full), 1);
         mbar_init(B(ctl->g_full), 1);
@@ -503,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == 8) tmem_dealloc(tmem, 512);
     };
 
-    const LatentUnit un = latent_unit(p.s, work);
+    const LatentUnit un = latent_unit<ROWS, false>(p.s, cu, unit, p.q_slots, p.group);
     if (un.row0 >= un.sq) return done();
     if (!ATTN_OPS_IN_BOUNDS(un.head < p.s.h && un.q0 + un.sq <= p.s.total_q && un.k0 + un.sk <= p.s.total_k, p.s, SITE_OPS_UNIT)) return done();
     const int last = min(un.row0 + ROWS, un.sq) - 1;
@@ -671,6 +670,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// Both: the units of keys, and behind them those of queries, which fill the SMs that the last of keys leave.
+template <typename T, bool CAUSAL>
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_bwd_kernel(const __grid_constant__ LatentBwdMaps m, const __grid_constant__ LatentBwdParams p, unsigned key_units)
+{
+    if (blockIdx.x < key_units)
+        latent_bwd_keys<T, CAUSAL>(m.q_half, m.dout_half, m.k, m.r, m.v, p, blockIdx.x);
+    else
+        latent_bwd_queries<T, CAUSAL>(m.q, m.dout, m.k_half, m.r_half, m.v_half, p, blockIdx.x - key_units);
+}
+
 // ---------------------------------------------------------------- the shared key part
 
 // 16 keys of a sequence to a block: their heads' shares, summed in the heads' order.
@@ -678,10 +688,9 @@ template <typename T>
 __global__ void __launch_bounds__(256) latent_rope_sum_kernel(const __grid_constant__ LatentBwdParams p)
 {
     await_previous();
-    const int per = p.k_blocks * 8, seq = blockIdx.x / per;
-    const int key = (blockIdx.x - seq * per) * 16 + (threadIdx.x >> 4), c = threadIdx.x & 15;
-    const int q0 = p.s.cu_q[seq], sq = p.s.cu_q[seq + 1] - q0, k0 = p.s.cu_k[seq], sk = p.s.cu_k[seq + 1] - k0;
-    if (q0 < 0 || sq < 0 || q0 > p.s.total_q - sq || k0 < 0 || sk < 0 || k0 > p.s.total_k - sk || key >= sk) return;
+    const LatentUnit un = latent_slot<kKeys, true>(p.s, latent_cu(p.s), blockIdx.x / 8);
+    const int key = un.row0 + (blockIdx.x % 8) * 16 + (threadIdx.x >> 4), c = threadIdx.x & 15, k0 = un.k0;
+    if (key >= un.sk) return;
     const float4 *x = reinterpret_cast<const float4 *>(p.kr_part + static_cast<int64_t>(k0 + key) * kLatentRope) + c;
     const int64_t step = static_cast<int64_t>(p.s.total_k) * (kLatentRope / 4);
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -710,23 +719,16 @@ template <typename T, bool CAUSAL>
 cudaError_t launch_t(const LatentBwdArgs &a)
 {
     const LatentSeqs &s = a.p.s;
-    std::atomic<int> *ready = a.attr_ready + (Elem<T>::BF16 ? 4 : 0) + (CAUSAL ? 2 : 0);
-    cudaError_t e = opt_in(ready[0], latent_bwd_keys_kernel<T, CAUSAL>, KeysCfg::SMEM);
-    if (e == cudaSuccess) e = opt_in(ready[1], latent_bwd_queries_kernel<T, CAUSAL>, QueriesCfg::SMEM);
-    const unsigned seq_heads = static_cast<unsigned>(s.batch) * s.h;
+    constexpr int SMEM = KeysCfg::SMEM > QueriesCfg::SMEM ? KeysCfg::SMEM : QueriesCfg::SMEM;
+    cudaError_t e = opt_in(a.attr_ready[(Elem<T>::BF16 ? 2 : 0) + (CAUSAL ? 1 : 0)], latent_bwd_kernel<T, CAUSAL>, SMEM);
+    const unsigned key_units = static_cast<unsigned>(s.h) * a.p.k_slots, units = key_units + static_cast<unsigned>(s.h) * a.p.q_slots;
     if (e == cudaSuccess && s.total_q > 0)
         e = launch_overlapped(latent_dsum_kernel<T>, dim3(static_cast<unsigned>((static_cast<int64_t>(s.total_q) * s.h + 15) / 16)), 256, 0,
                               a.stream, a.p);
-    if (a.p.k_blocks > 0) {
-        if (e == cudaSuccess)
-            e = launch_overlapped(latent_bwd_keys_kernel<T, CAUSAL>, dim3(seq_heads * a.p.k_blocks), kThreads, KeysCfg::SMEM, a.stream,
-                                  a.q_half, a.dout_half, a.k, a.r, a.v, a.p);
-        if (e == cudaSuccess)
-            e = launch_overlapped(latent_rope_sum_kernel<T>, dim3(static_cast<unsigned>(s.batch) * a.p.k_blocks * 8), 256, 0, a.stream, a.p);
-    }
-    if (e == cudaSuccess && a.p.q_blocks > 0)
-        e = launch_overlapped(latent_bwd_queries_kernel<T, CAUSAL>, dim3(seq_heads * a.p.q_blocks), kThreads, QueriesCfg::SMEM, a.stream, a.q,
-                              a.dout, a.k_half, a.r_half, a.v_half, a.p);
+    if (e == cudaSuccess && units > 0)
+        e = launch_overlapped(latent_bwd_kernel<T, CAUSAL>, dim3(units), kThreads, SMEM, a.stream, a.maps, a.p, key_units);
+    if (e == cudaSuccess && key_units > 0)
+        e = launch_overlapped(latent_rope_sum_kernel<T>, dim3(static_cast<unsigned>(a.p.k_slots) * 8), 256, 0, a.stream, a.p);
     return e;
 }
 

@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tmV);
     }
     await_previous();
-    const LatentWork work = latent_work(p.s, blockIdx.x, p.blocks, p.group, kUnitRows, true);  // in its memory's time, what follows
+    const LatentCu cu = latent_cu(p.s);  // in its memory's time, what follows
     if (threadIdx.x == 0) {
         for (int i = 0; i < kSlots; ++i) mbar_init(B(ctl->empty[i]), 1);
         for (int t = 0; t < 2; ++t) {
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     // rows row0 .. of sequence seq: heads of a group together, heaviest blocks first
-    const LatentUnit un = latent_unit(p.s, work);
+    const LatentUnit un = latent_unit<kUnitRows, false>(p.s, cu, blockIdx.x, p.slots, p.group);
     if (un.row0 >= un.sq) return done();
     const int last = min(un.row0 + kUnitRows, un.sq) - 1;
     const int kend = CAUSAL ? max(min(un.sk, last + 1 + un.sk - un.sq), 0) : un.sk;

@@ -91,7 +91,6 @@ struct LatentSeqs {
     const int32_t *cu_q, *cu_k;  // [batch + 1]
     int32_t batch, h;
     int32_t total_q, total_k;
-    int32_t max_q, max_k;
     int32_t causal;
     float sl2e;                  // scale * log2(e)
     float scale;
@@ -104,7 +103,7 @@ struct LatentFwdParams {
     void *o;                     // [total_q, h, 128] by strides (elements)
     int64_t ot, oh;              // of a token, of a head
     float *lse;                  // [h, total_q] or nullptr
-    int32_t blocks;              // ceil(max_q / 256)
+    int32_t slots;               // of 256 queries: total_q / 256 + batch
     int32_t group;               // heads whose units are taken together
 };
 
@@ -129,19 +128,23 @@ struct LatentBwdParams {
     float *kr_part;              // [h, total_k, 64]: each head's gradient of the shared key part
     void *dq, *dkn, *dkr, *dv;   // by strides of a token and of a head
     int64_t dqt, dqh, dknt, dknh, dkrt, dvt, dvh;
-    int32_t q_blocks, k_blocks;  // ceil(max_q / 128), ceil(max_k / 128)
+    int32_t q_slots, k_slots;    // of 128 queries, of 128 keys (0: there are none)
     int32_t group;               // heads whose units are taken together
 };
 
-struct LatentBwdArgs {
+struct LatentBwdMaps {
     CUtensorMap q, dout, k, r, v;                           // 128 rows a copy
     CUtensorMap q_half, dout_half, k_half, r_half, v_half;  // 64 rows a copy
+};
+
+struct LatentBwdArgs {
+    LatentBwdMaps maps;
     LatentBwdParams p;
     cudaStream_t stream;
     std::atomic<int> *attr_ready;
 };
 
-constexpr int kLatentBwdInstances = 8;  // {keys, queries} x {fp16, bf16} x {causal, not}
+constexpr int kLatentBwdInstances = 4;  // {fp16, bf16} x {causal, not}
 
 cudaError_t launch_latent_bwd(const LatentBwdArgs &a, bool bf16);
 

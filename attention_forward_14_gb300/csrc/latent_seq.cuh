@@ -16,36 +16,66 @@ struct LatentUnit {
     int k0, sk;       // its first key token, its keys
 };
 
-// Unit u of sequences x groups of heads x blocks of rows x heads of a group:
-// the blocks of some heads together, so that the L2 holds what they share; of
-// queries (`last_first`) the later blocks, which see more keys, first.  A
-// sequence whose offsets fall outside the totals is empty.
-struct LatentWork {
-    int head, row0, q0, q1, k0, k1;
+// The offsets of the sequence of this lane's number, of 32 from `first` on.
+struct LatentCu {
+    int first;
+    int q0, q1, k0, k1;
 };
 
-// (What the answer takes from memory is on its way when this returns, and
-// looked at by latent_unit.)
-__device__ __forceinline__ LatentWork latent_work(const LatentSeqs &s, unsigned u, int blocks, int group, int rows, bool last_first)
+__device__ __forceinline__ LatentCu latent_cu(const LatentSeqs &s, int first = 0)
 {
-    const unsigned per_seq = static_cast<unsigned>(blocks) * s.h, seq = u / per_seq;
-    LatentWork w;
-    w.q0 = s.cu_q[seq], w.q1 = s.cu_q[seq + 1], w.k0 = s.cu_k[seq], w.k1 = s.cu_k[seq + 1];
-    u -= seq * per_seq;
-    const unsigned hg = u / (blocks * group);
-    u -= hg * blocks * group;
-    const int heads = min(group, s.h - static_cast<int>(hg) * group);
-    const int blk = u / heads;
-    w.head = hg * group + u - blk * heads;
-    w.row0 = (last_first ? blocks - 1 - blk : blk) * rows;
-    return w;
+    const int i = first + (threadIdx.x & 31);
+    if (i >= s.batch) return {first, -1, -1, -1, -1};
+    return {first, s.cu_q[i], s.cu_q[i + 1], s.cu_k[i], s.cu_k[i + 1]};
 }
 
-__device__ __forceinline__ LatentUnit latent_unit(const LatentSeqs &s, const LatentWork &w)
+// The sequence and first row of a slot, by all lanes of a warp (`cu`: of the
+// first 32 sequences).  The blocks of ROWS rows of a sequence that begins at
+// token t and is the i-th stand in the slots from t / ROWS + i on: none meets
+// the next one's, and of total / ROWS + batch slots no more than one a
+// sequence is empty, however their lengths differ.  (A grid of batch times
+// the longest one's blocks, most of them empty: 115 us, not 103, for the
+// outputs of 6001 tokens in four sequences of 1 to 3107, 16 heads.)  An empty
+// slot's unit has no rows; of a sequence whose offsets fall outside the totals
+// all slots are empty.
+template <int ROWS, bool OF_KEYS>
+__device__ __forceinline__ LatentUnit latent_slot(const LatentSeqs &s, LatentCu cu, int slot)
 {
-    LatentUnit un{w.head, w.row0, w.q0, w.q1 - w.q0, w.k0, w.k1 - w.k0};
-    if (un.q0 < 0 || un.sq < 0 || un.q0 > s.total_q - un.sq || un.k0 < 0 || un.sk < 0 || un.k0 > s.total_k - un.sk)
-        un.q0 = un.sq = un.k0 = un.sk = 0;
+    const int lane = threadIdx.x & 31;
+    if (s.batch > 32) {  // 32 sequences among which it is, if the offsets do not decrease
+        const int32_t *starts = OF_KEYS ? s.cu_k : s.cu_q;
+        int lo = 0, n = s.batch;
+        while (n > 32) {
+            const int step = (n + 31) / 32, i = lane * step;
+            const uint32_t before = __ballot_sync(0xffffffffu, i < n && starts[lo + i] / ROWS + lo + i <= slot);
+            const int at = before ? (31 - __clz(before)) * step : 0;
+            lo += at;
+            n = min(step, n - at);
+        }
+        cu = latent_cu(s, lo);
+    }
+    const int t0 = OF_KEYS ? cu.k0 : cu.q0, t1 = OF_KEYS ? cu.k1 : cu.q1;
+    const int blk = slot - t0 / ROWS - cu.first - lane;
+    const bool in = 0 <= cu.q0 && cu.q0 <= cu.q1 && cu.q1 <= s.total_q && 0 <= cu.k0 && cu.k0 <= cu.k1 && cu.k1 <= s.total_k && t0 < t1 &&
+                    0 <= blk && blk <= (t1 - t0 - 1) / ROWS;
+    const uint32_t found = __ballot_sync(0xffffffffu, in);
+    if (found == 0u) return {0, 0, 0, 0, 0, 0};
+    const int src = __ffs(found) - 1;
+    auto from = [&](int v) { return __shfl_sync(0xffffffffu, v, src); };
+    return {0, from(blk) * ROWS, from(cu.q0), from(cu.q1 - cu.q0), from(cu.k0), from(cu.k1 - cu.k0)};
+}
+
+// Unit u of groups of heads x slots x heads of a group: the blocks of some
+// heads together, so that the L2 holds what they share; of queries the later
+// blocks, which see more keys, first.
+template <int ROWS, bool OF_KEYS>
+__device__ __forceinline__ LatentUnit latent_unit(const LatentSeqs &s, const LatentCu &cu, unsigned u, int slots, int group)
+{
+    const unsigned hg = u / (static_cast<unsigned>(slots) * group);
+    u -= hg * slots * group;
+    const int heads = min(group, s.h - static_cast<int>(hg) * group), slot = u / heads;
+    LatentUnit un = latent_slot<ROWS, OF_KEYS>(s, cu, OF_KEYS ? slot : slots - 1 - slot);
+    un.head = hg * group + u - slot * heads;
     return un;
 }
 

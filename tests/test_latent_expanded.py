@@ -28,6 +28,9 @@ CASES = [
     (5, (65,), (700,), False, "bf16"),
     (1, (900,), (130,), False, "bf16"),
     (17, (40, 20), (40, 20), True, "fp16"),
+    (1, tuple((37 * i) % 150 for i in range(70)), tuple((53 * i) % 140 for i in range(70)), True, "bf16"),  # many sequences
+    (2, tuple(i % 4 for i in range(1100)), tuple(i % 3 for i in range(1100)), False, "fp16"),
+    (1, (0,) * 40 + (300,) + (0,) * 40, (7,) * 40 + (400,) + (0,) * 40, True, "bf16"),
 ]
 
 
@@ -53,7 +56,7 @@ def call(q, kn, kr, v, cu, case, **kw):
 
 
 @gpu
-@pytest.mark.parametrize("case", CASES, ids=str)
+@pytest.mark.parametrize("case", CASES, ids=lambda c: str(c)[:60])
 def test_forward_and_gradients(case):
     q, kn, kr, v, gr, cu = make(case)
     causal, half = case[3], R.HALF_STEP[q.dtype]
@@ -240,7 +243,7 @@ BAD = [
     (dict(q=None), -1), (dict(kn=None), -1), (dict(kr=None), -1), (dict(v=None), -1), (dict(cu=None), -1),
     (dict(q=AT["q"] + 8), -6), (dict(v=AT["v"] + 2), -6), (dict(lse=AT["lse"] + 2), -6), (dict(cu=AT["cu"] + 1), -6),
     (dict(batch=-1), -2), (dict(h=-1), -2), (dict(tq=-1), -2), (dict(mq=11), -2), (dict(mk=13), -2), (dict(tq=1 << 31, mq=1), -2),
-    (dict(dt=5), -4), (dict(scale=float("nan")), -5),
+    (dict(dt=5), -4), (dict(scale=float("nan")), -5), (dict(batch=1 << 28), -2), (dict(batch=1 << 20, h=1 << 11), -2),
 ]
 
 
