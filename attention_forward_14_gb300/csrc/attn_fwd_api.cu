@@ -1768,7 +1768,7 @@ int attn_fwd_latent_paged(const void *q, const void *pool, const int32_t *cache_
     p.tree_words = static_cast<int32_t>((sq + 31) / 32);
     p.timeout_ns = kDefaultTimeoutNs;
     // no more teams than units in full caches
-    const double units = static_cast<double>(b) * p.groups * static_cast<double>((p.cap + 127) / 128);
+    const double units = static_cast<double>(b) * p.groups * static_cast<double>((p.cap + 127) / 128 + latent_item_cost(tile));
     int teams = (di->sm_count < kLatentMaxCtas ? di->sm_count : kLatentMaxCtas) / p.team;
     if (units < teams) teams = static_cast<int>(units);
     a.tile_rows = tile;

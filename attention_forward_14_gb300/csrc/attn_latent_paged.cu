@@ -41,6 +41,7 @@
 #include "latent.h"
 
 #include "attn_kv8_common.cuh"
+#include "latent_seq.cuh"
 #include "mma_issue.cuh"
 #include "tmem_cols.cuh"
 
@@ -64,7 +65,7 @@ struct LatentCfg {
     static constexpr int Q_PANEL = N * 128;
     static constexpr int COLS = N / 2;                   // rows (columns of S^T) of a softmax thread
     static constexpr int PAIR_SLOTS = N == 64 ? 4 : 5, KEY_SLOTS = N == 16 ? 2 : 1;
-    static constexpr int CTL = 4096;
+    static constexpr int CTL = 5120;
     static constexpr int Q_OFF = CTL;
     static constexpr int PAIR_OFF = Q_OFF + kPanels * Q_PANEL;
     static constexpr int KEY_OFF = PAIR_OFF + PAIR_SLOTS * PAIR;
@@ -84,9 +85,10 @@ struct LatentCtl {
     float inv[64];
     float red[2][4][32];     // of a softmax group's warps: a value for each of its rows
     float red2[2][4][32];
+    float shrink[2][4][32];
     int64_t o_at[64];        // where each row of o begins (elements)
 };
-static_assert(sizeof(LatentCtl) <= 4096, "control block");
+static_assert(sizeof(LatentCtl) <= LatentCfg<16>::CTL, "control block");
 
 // ---------------------------------------------------------------- work
 
@@ -102,7 +104,7 @@ __device__ __forceinline__ int group_end(const LatentPagedParams &p, int len, in
 struct LatentPlace {
     int entry;         // b * groups + group
     int b, group;
-    int j, n;          // unit of the item, units of the item
+    int j, n;          // unit of the item (negative: of its cost), units of the item
     int len, end;      // cached keys; those that some row sees
 };
 
@@ -111,11 +113,12 @@ __device__ __forceinline__ int latent_len(const LatentPagedParams &p, int b) { r
 // One unit at least, which writes the rows of an item that sees no key.
 __device__ __forceinline__ int units_for(int end) { return max((end + kTileKeys - 1) / kTileKeys, 1); }
 
+// An item's units and, before them, as many as its beginning and end cost.
 __device__ __forceinline__ int entry_units(const LatentPagedParams &p, int entry, int tile_rows)
 {
     if (entry >= p.b * p.groups) return 0;
     const int b = entry / p.groups;
-    return units_for(group_end(p, latent_len(p, b), entry - b * p.groups, tile_rows));
+    return latent_item_cost(tile_rows) + units_for(group_end(p, latent_len(p, b), entry - b * p.groups, tile_rows));
 }
 
 // (`mine`: entry_units of entry `lane`, which both this and latent_place begin with)
@@ -123,7 +126,7 @@ __device__ __forceinline__ int64_t latent_total(const LatentPagedParams &p, int 
 {
     const int lane = threadIdx.x & 31, entries = p.b * p.groups;
     int64_t t = mine;
-#pragma unroll 4
+#pragma unroll 1
     for (int e = 32 + lane; e < entries; e += 32) t += entry_units(p, e, tile_rows);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
@@ -135,7 +138,7 @@ __device__ __forceinline__ void set_entry(const LatentPagedParams &p, LatentPlac
     c.entry = entry;
     c.b = entry / p.groups;
     c.group = entry - c.b * p.groups;
-    c.j = 0;
+    c.j = -latent_item_cost(tile_rows);
     if (c.b >= p.b) return;
     c.len = latent_len(p, c.b);
     c.end = group_end(p, c.len, c.group, tile_rows);
@@ -147,6 +150,7 @@ __device__ __forceinline__ LatentPlace latent_place(const LatentPagedParams &p, 
 {
     const int lane = threadIdx.x & 31, entries = p.b * p.groups;
     LatentPlace c{};
+#pragma unroll 1
     for (int e0 = 0; e0 < entries; e0 += 32) {
         int64_t inc = e0 == 0 ? mine : entry_units(p, e0 + lane, tile_rows);
 #pragma unroll
@@ -163,7 +167,7 @@ __device__ __forceinline__ LatentPlace latent_place(const LatentPagedParams &p, 
         const int64_t before = __shfl_sync(0xffffffffu, inc, src > 0 ? src - 1 : 0);
         if (src > 0) u -= before;
         set_entry(p, c, e0 + src, tile_rows);
-        c.j = static_cast<int>(u);
+        c.j += static_cast<int>(u);
         break;
     }
     return c;
@@ -180,6 +184,14 @@ __device__ __forceinline__ bool group_any(int barrier, bool v)
                  : "r"(v ? 1u : 0u), "r"(barrier)
                  : "memory");
     return r != 0u;
+}
+
+// The largest of a warp's values (NaN only if all are).
+__device__ __forceinline__ float warp_top(float v)
+{
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
 
 // 16 bytes to shared memory, or zeros.
@@ -251,24 +263,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto B = [&](const uint64_t &bar) { return smem_addr(&bar); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile uint32_t *abort_flag = &ctl->abort;
-
-    auto wait = [&](uint32_t bar, uint32_t parity, uint32_t site) {
-        if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
-        const uint64_t t0 = global_timer_ns();
-        while (true) {
-            for (int i = 0; i < 64; ++i)
-                if (mbar_try_wait(bar, parity)) return true;
-            if (*abort_flag) return false;
-            if (global_timer_ns() - t0 > p.timeout_ns) {
-                *abort_flag = 1u;
-                record_status(p.status, STATUS_TIMEOUT, site);
-                return false;
-            }
-        }
-    };
-    auto warp_waits = [&](uint32_t bar, uint32_t parity, uint32_t site) {
-        return static_cast<bool>(__all_sync(0xffffffffu, wait(bar, parity, site)));
-    };
+    const BoundedWaits waits{&ctl->abort, p.status, p.timeout_ns};
+    auto warp_waits = [&](uint32_t bar, uint32_t parity, uint32_t site) { return waits.warp(bar, parity, site); };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::PAIR_SLOTS; ++i) {
@@ -317,7 +313,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // Of an item: the CTA's first row, its tiles within the share, and the keys that all of its rows see.
     auto first_row = [&](const LatentPlace &c) { return static_cast<int64_t>(c.group * p.team + rank) * N; };
-    auto item_tiles = [&](const LatentPlace &c, int j_end) { return c.end > 0 && first_row(c) < p.rows ? j_end - c.j : 0; };
+    auto has_tiles = [&](const LatentPlace &c) { return c.end > 0 && first_row(c) < p.rows; };
+    auto item_tiles = [&](int j_end) { return has_tiles(at) ? j_end - at.j : 0; };
+    // To the item's first unit in the share; false if there is none.
+    auto enter = [&](int &it) {
+        const int skip = min(max(-at.j, 0), n_units - it);
+        at.j += skip, it += skip;
+        return it < n_units && place_in_bounds();
+    };
     auto all_see = [&]() {
         if (p.mask == LATENT_MASK_NONE) return at.len;
         const int i0 = p.mask == LATENT_MASK_TREE ? -1 : static_cast<int>(first_row(at)) / p.h;
@@ -335,9 +338,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t np = 0u, nk = 0u;  // pairs and key parts copied
             bool ok = true;
             for (int it = 0; ok && it < n_units;) {
-                if (!place_in_bounds()) break;
+                if (!enter(it)) break;
                 const int j_end = min(at.n, at.j + n_units - it);
-                const int tiles = item_tiles(at, j_end);
+                const int tiles = item_tiles(j_end);
                 const int32_t *table = p.block_table + static_cast<int64_t>(at.b) * p.pages_per_seq;
                 // where the lane's keys of a tile lie: a copy begins there, or none (-1)
                 auto token_of = [&](int t) {
@@ -356,6 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (next >= 0 && next != nowhere && rank == (at.j + t) % p.team)
                         l2_prefetch(p.pool + (static_cast<int64_t>(next) * 2 + side * p.box) * kLatentToken, p.box * kLatentToken);
                     const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, there) & 0xFFu);
+#pragma unroll 1
                     for (int pr = 0; ok && pr < kPairs; ++pr, ++np) {
                         const uint32_t st = np % C::PAIR_SLOTS, bar = B(ctl->pair_full[st]);
                         ok = warp_waits(B(ctl->pair_empty[st]), ((np / C::PAIR_SLOTS) & 1u) ^ 1u, SITE_LAT_EMPTY);
@@ -380,8 +384,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 set_entry(p, at, at.entry + 1, N);
             }
             // wait (bounded) for the last copies, so that none lands after the CTA
+#pragma unroll 1
             for (uint32_t i = np > C::PAIR_SLOTS ? np - C::PAIR_SLOTS : 0u; i < np; ++i)
                 drain_wait(B(ctl->pair_full[i % C::PAIR_SLOTS]), (i / C::PAIR_SLOTS) & 1u, p.timeout_ns);
+#pragma unroll 1
             for (uint32_t i = nk > C::KEY_SLOTS ? nk - C::KEY_SLOTS : 0u; i < nk; ++i)
                 drain_wait(B(ctl->key_full[i % C::KEY_SLOTS]), (i / C::KEY_SLOTS) & 1u, p.timeout_ns);
         } else if (warp >= 10) {
@@ -392,9 +398,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t np = 0u, n_dirty = 0u;
             bool ok = true;
             for (int it = 0; ok && it < n_units;) {
-                if (!place_in_bounds()) break;
+                if (!enter(it)) break;
                 const int j_end = min(at.n, at.j + n_units - it);
-                const int tiles = item_tiles(at, j_end);
+                const int tiles = item_tiles(j_end);
                 const int all = all_see();
                 for (int t = 0; ok && t < tiles; ++t, np += kPairs) {
                     const int k0 = (at.j + t) * kTileKeys;
@@ -403,13 +409,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     ++n_dirty;
                     const int left = min(at.len - k0, kTileKeys), whole = max(all - k0, 0);
+#pragma unroll 1
                     for (int pr = warp - 10; ok && pr < kPairs; pr += 2) {
                         const uint32_t n = np + pr, st = n % C::PAIR_SLOTS;
                         // (the issuing warp has seen it; this orders the copies before what follows)
                         ok = warp_waits(B(ctl->pair_full[st]), (n / C::PAIR_SLOTS) & 1u, SITE_LAT_FULL);
                         if (!ok) break;
+#pragma unroll 1
                         for (int side = 0; side < 2; ++side) {
                             uint8_t *panel = smem + C::PAIR_OFF + st * C::PAIR + side * C::PANEL;
+#pragma unroll 1
                             for (int c = whole * 8 + lane; c < left * 8; c += 32) {
                                 uint4 *v = reinterpret_cast<uint4 *>(panel) + c;
                                 const uint4 a = *v;
@@ -417,6 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                            finite_halves<BF16>(a.z), finite_halves<BF16>(a.w));
                                 if (f.x != a.x || f.y != a.y || f.z != a.z || f.w != a.w) *v = f;
                             }
+#pragma unroll 1
                             for (int c = left * 8 + lane; c < kTileKeys * 8; c += 32)
                                 reinterpret_cast<uint4 *>(panel)[c] = make_uint4(0u, 0u, 0u, 0u);
                         }
@@ -436,14 +446,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t dq = desc_lo(sQ, 16), dk_pair = desc_lo(sPair, 16), dk_key = desc_lo(sKey, 16);
             const uint32_t dv = desc_lo(sPair, C::PANEL), dp = desc_lo(sKey, 16);
             for (int it = 0; ok && it < n_units;) {
-                if (!place_in_bounds()) break;
+                if (!enter(it)) break;
                 const int j_end = min(at.n, at.j + n_units - it);
-                const int tiles = item_tiles(at, j_end);
+                const int tiles = item_tiles(j_end);
                 const int all = all_see();
                 if (tiles > 0) ok = warp_waits(B(ctl->q_full), q_it++ & 1u, SITE_LAT_Q);
                 for (int t = 0; ok && t < tiles; ++t, np += kPairs, ++nk, ++tile_it) {
                     const bool dirty = (at.j + t + 1) * kTileKeys > all;
                     // S^T
+#pragma unroll 1
                     for (int pr = 0; pr < kPairs; ++pr) {
                         const uint32_t st = (np + pr) % C::PAIR_SLOTS;
                         if (!(ok = warp_waits(B(ctl->pair_full[st]), ((np + pr) / C::PAIR_SLOTS) & 1u, SITE_LAT_FULL))) break;
@@ -468,6 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!(ok = warp_waits(B(ctl->p_full), tile_it & 1u, SITE_LAT_P))) break;
                     tc_fence_after();
                     {
+#pragma unroll 1
                         for (int pr = 0; pr < kPairs; ++pr) {
                             const uint32_t st = (np + pr) % C::PAIR_SLOTS;
 #pragma unroll
@@ -498,12 +510,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tS = tmem + lane_off + C::TM_S + w * COLS, tO = tmem + lane_off + C::TM_O + w * COLS;
         auto group_sync = [&]() { named_barrier(bar_id, 128); };
         uint32_t tile_it = 0u, nk = 0u;
-        bool ok = true;
+        bool ok = true, asked = false;
         // An item's rows of Q: 72 pieces of 16 bytes a row, all of them on their way at once; eight lanes to a panel's row.
         auto ask_q = [&](const LatentPlace &c) {
             const int64_t row0 = first_row(c);
             const int nr = static_cast<int>(min(static_cast<int64_t>(N), p.rows - row0)), sub = lane & 7;
             const T *q = static_cast<const T *>(p.q) + c.b * p.qb;
+#pragma unroll 1
             for (int r = warp * 4 + (lane >> 3); r < N; r += 32) {
                 const int row = static_cast<int>(row0) + min(r, nr - 1), i = row / p.h, head = row - i * p.h;
                 const uint4 *src = reinterpret_cast<const uint4 *>(q + head * p.qh + i * p.qs) + sub;
@@ -519,9 +532,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(B(ctl->q_full));
         };
         for (int it = 0; it < n_units;) {
-            if (!place_in_bounds()) break;
+            if (!enter(it)) break;
             const int j_end = min(at.n, at.j + n_units - it);
-            const int tiles = item_tiles(at, j_end);
+            const int tiles = item_tiles(j_end);
             const int64_t row0 = first_row(at);
             const int nr = static_cast<int>(min(static_cast<int64_t>(N), max(p.rows - row0, int64_t(0))));
             const int all = all_see(), before = at.len - p.sq;
@@ -533,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int32_t *tree = p.tree + static_cast<int64_t>(at.b) * p.sq * p.tree_words + (drafted >> 5);
                 const int first = ctl->query[w * COLS], last = ctl->query[w * COLS + COLS - 1];
                 int r = static_cast<int>(first * static_cast<int64_t>(p.h) - row0) - w * COLS;  // the query's first row
-#pragma unroll 4
+#pragma unroll 1
                 for (int i = first; i <= last; ++i, r += p.h) {
                     bool one = true;
                     if (p.mask == LATENT_MASK_CAUSAL) one = drafted <= i;
@@ -552,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ctl->query[r] = i;
                 ctl->o_at[r] = at.b * p.ob + head * p.oh + i * p.os;
             }
-            if (it == 0 && tiles > 0) {
+            if (tiles > 0 && !asked) {
                 ask_q(at);
                 give_q();
             }
@@ -591,42 +604,49 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < COLS / 2; ++c) top = max3f(top, x[c].x, x[c].y);
                 if (group_any(bar_id, top > kSlackLog2 || unset != 0u)) {
-                    float v[COLS];
+                    float up = 0.f;  // lane c: of column c
 #pragma unroll
-                    for (int c = 0; c < COLS / 2; ++c) v[2 * c] = x[c].x, v[2 * c + 1] = x[c].y;
-                    const float up = reduce_columns<COLS>(v, [](float a, float b) { return fmaxf(a, b); });
+                    for (int c = 0; c < COLS / 2; ++c) {
+                        const float a = warp_top(x[c].x), b = warp_top(x[c].y);
+                        up = lane == 2 * c ? a : (lane == 2 * c + 1 ? b : up);
+                    }
                     if (lane < COLS) ctl->red[w][in_group][lane] = up;
                     if (t > 0) {  // O^T has the tiles before: let the last one's products end
                         if (ok) ok = warp_waits(B(ctl->pv_done), (tile_it - 1) & 1u, SITE_LAT_O);
                         tc_fence_after();
                     }
                     group_sync();
-                    // by how much each row's reference rises (is set)
-                    float own = 0.f;
-#pragma unroll
-                    for (int c = 0; c < COLS; ++c) {
-                        const float mx = fmaxf(fmaxf(ctl->red[w][0][c], ctl->red[w][1][c]), fmaxf(ctl->red[w][2][c], ctl->red[w][3][c]));
-                        const bool first = unset >> c & 1;
-                        const float rise = first ? (mx > -INFINITY ? mx : 0.f) : fmaxf(mx, 0.f);
-                        if (mx > -INFINITY) unset &= ~(1u << c);
-                        if (c & 1) x[c / 2].y -= rise;
-                        else x[c / 2].x -= rise;
-                        v[c] = first ? 1.f : ex2_approx(-rise);
-                        own = c == key ? rise : own;
+                    // by how much each row's reference rises (is set): a column's by its lane of every warp, for itself
+                    float *rise = ctl->red2[w][in_group], *shrink = ctl->shrink[w][in_group];
+                    if (lane < COLS) {
+                        const float mx = fmaxf(fmaxf(ctl->red[w][0][lane], ctl->red[w][1][lane]), fmaxf(ctl->red[w][2][lane], ctl->red[w][3][lane]));
+                        const bool first = unset >> lane & 1;
+                        const float by = first ? (mx > -INFINITY ? mx : 0.f) : fmaxf(mx, 0.f);
+                        up = mx;
+                        rise[lane] = by;
+                        shrink[lane] = first ? 1.f : ex2_approx(-by);
+                        if (in_group == 0) ctl->ref[w * COLS + lane] += by;
                     }
-                    if (key < COLS) ctl->ref[w * COLS + key] += own;
+                    unset &= ~__ballot_sync(0xffffffffu, lane < COLS && up > -INFINITY);
+                    __syncwarp();
 #pragma unroll
                     for (int c = 0; c < COLS / 2; ++c) {
-                        l[c] = __fmul2_rn(l[c], make_float2(v[2 * c], v[2 * c + 1]));
-                        lr[c] = __fmul2_rn(lr[c], make_float2(v[2 * c], v[2 * c + 1]));
+                        const float2 by = reinterpret_cast<const float2 *>(rise)[c];
+                        x[c] = __fadd2_rn(x[c], make_float2(-by.x, -by.y));
                     }
                     if (t > 0) {
+                        const float2 *f = reinterpret_cast<const float2 *>(shrink);
+#pragma unroll
+                        for (int c = 0; c < COLS / 2; ++c) l[c] = __fmul2_rn(l[c], f[c]), lr[c] = __fmul2_rn(lr[c], f[c]);
 #pragma unroll 1
                         for (int j = 0; j < kPairs; ++j) {
                             uint32_t o[COLS];
                             tmem_load(tO + j * N, o);
 #pragma unroll
-                            for (int c = 0; c < COLS; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * v[c]);
+                            for (int c = 0; c < COLS / 2; ++c) {
+                                const float2 v = __fmul2_rn(make_float2(__uint_as_float(o[2 * c]), __uint_as_float(o[2 * c + 1])), f[c]);
+                                o[2 * c] = __float_as_uint(v.x), o[2 * c + 1] = __float_as_uint(v.y);
+                            }
                             tmem_store(tO + j * N, o);
                         }
                         tmem_wait_st();
@@ -655,9 +675,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // The next item's Q, as soon as the last scores are there: its first products run while this one is stored.
             LatentPlace next = at;
             set_entry(p, next, at.entry + 1, N);
-            const int left = n_units - it - (j_end - at.j);
-            const bool goes_on = left > 0 && item_tiles(next, min(next.n, left)) > 0;
+            const bool goes_on = n_units - it - (j_end - at.j) > latent_item_cost(N) && has_tiles(next);
             if (goes_on) ask_q(next);
+            asked = goes_on;
             // the item ends, or goes on in the next team
             const bool item_ends = j_end == at.n;
             const int64_t first_unit = u0 + it - at.j;  // of the item
@@ -693,11 +713,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             group_sync();
-            if (goes_on) give_q();
             if (tiles > 0) {
                 if (ok) ok = warp_waits(B(ctl->pv_done), (tile_it - 1) & 1u, SITE_LAT_O);
                 tc_fence_after();
             }
+            if (goes_on) give_q();
 #pragma unroll 1
             for (int j = 0; j < kPairs; ++j) {
                 uint32_t o[COLS];

@@ -67,6 +67,15 @@ struct LatentPagedParams {
     uint64_t timeout_ns;
 };
 
+// What an item's beginning and end (its first weights, its store, the way to
+// the next one) cost, in units.  The teams' shares are equal with it: for 64
+// rows 0, 1, 2, 3, 4 of them took 60, 49, 45, 45, 47 us for trees of 13 tokens
+// (8 requests, 300 to 4000 tokens, 32 heads), and 49, 43, 43, 45, 45 for 64
+// requests of 100 to 1024 tokens, 128 heads; for 16 rows 0 to 3 24.0, 22.8,
+// 22.9, 25.7 for those requests with 16 heads; for 32 rows 0 to 3 43.3, 42.5,
+// 43.0, 43.6 for 48 of 100 to 2048 tokens.
+__host__ __device__ constexpr int latent_item_cost(int tile_rows) { return tile_rows == 64 ? 2 : 1; }
+
 constexpr int kLatentMaxCtas = 160;  // CTAs of a launch at most (sizes the workspace)
 constexpr int kLatentMaxTeam = 4;
 constexpr int kLatentPagedInstances = 6;  // {fp16, bf16} x {16, 32, 64 rows}

@@ -91,16 +91,18 @@ struct BoundedWaits {
         if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
         volatile uint32_t *flag = abort;
         const uint64_t t0 = global_timer_ns();
-        while (true) {
+        bool late = false;
+#pragma unroll 1
+        while (!late) {
+#pragma unroll 1
             for (int i = 0; i < 64; ++i)
                 if (mbar_try_wait(bar, parity)) return true;
             if (*flag) return false;
-            if (global_timer_ns() - t0 > timeout_ns) {
-                *flag = 1u;
-                record_status(status, STATUS_TIMEOUT, site);
-                return false;
-            }
+            late = global_timer_ns() - t0 > timeout_ns;
         }
+        *flag = 1u;
+        record_status(status, STATUS_TIMEOUT, site);
+        return false;
     }
     // two of them: the second is looked at while the first's answer is on its way
     __device__ __forceinline__ bool warp(uint32_t bar_a, uint32_t parity_a, uint32_t bar_b, uint32_t parity_b, uint32_t site) const
