@@ -144,14 +144,6 @@ __device__ __forceinline__ void latent_bwd_keys(const CUtensorMap &tmQ, const CU
     KeysCtl *ctl = reinterpret_cast<KeysCtl *>(smem);
     auto B = [&](const uint64_t &bar) { return smem_addr(&bar); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
-        tma_prefetch_desc(&tmQ);
-        tma_prefetch_desc(&tmG);
-        tma_prefetch_desc(&tmK);
-        tma_prefetch_desc(&tmR);
-        tma_prefetch_desc(&tmV);
-    }
-    await_previous();
     const LatentCu cu = latent_cu(p.s);  // in its memory's time, what follows
     if (threadIdx.x == 0) {
         mbar_init(B(ctl->v_full), 1);
@@ -463,14 +455,6 @@ __device__ __forceinline__ void latent_bwd_queries(const CUtensorMap &tmQ, const
     QueriesCtl *ctl = reinterpret_cast<QueriesCtl *>(smem);
     auto B = [&](const uint64_t &bar) { return smem_addr(&bar); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
-        tma_prefetch_desc(&tmQ);
-        tma_prefetch_desc(&tmG);
-        tma_prefetch_desc(&tmK);
-        tma_prefetch_desc(&tmR);
-        tma_prefetch_desc(&tmV);
-    }
-    await_previous();
     const LatentCu cu = latent_cu(p.s);  // in its memory's time, what follows
     if (threadIdx.x == 0) {
         mbar_init(B(ctl->q_full), 1);
@@ -675,7 +659,13 @@ template <typename T, bool CAUSAL>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_bwd_kernel(const __grid_constant__ LatentBwdMaps m, const __grid_constant__ LatentBwdParams p, unsigned key_units)
 {
-    if (blockIdx.x < key_units)
+    const bool keys = blockIdx.x < key_units;
+    if (threadIdx.x == 0)
+        for (const CUtensorMap *map : {keys ? &m.q_half : &m.q, keys ? &m.dout_half : &m.dout, keys ? &m.k : &m.k_half,
+                                       keys ? &m.r : &m.r_half, keys ? &m.v : &m.v_half})
+            tma_prefetch_desc(map);
+    await_previous();
+    if (keys)
         latent_bwd_keys<T, CAUSAL>(m.q_half, m.dout_half, m.k, m.r, m.v, p, blockIdx.x);
     else
         latent_bwd_queries<T, CAUSAL>(m.q, m.dout, m.k_half, m.r_half, m.v_half, p, blockIdx.x - key_units);
