@@ -1698,6 +1698,25 @@ int64_t attn_fwd_latent_paged_workspace_bytes(int64_t b, int64_t h, int64_t sq)
     return rc != ATTN_OK ? rc : latent_workspace(h * sq);
 }
 
+// CTAs of a team: the most, since the cache leaves memory once for a team, of
+// the numbers that leave hardly more CTAs without a tile or a team than the
+// best.  (Teams of 1, 2: 128 heads of 64 requests, two tiles, 139, 111 us; of
+// 2, 4, 8: 512 queries of 128 heads, 1024 tiles, 1155, 1148, 1139.  Five tiles
+// in teams of 2 and of 5, 16 requests of 2000 to 4096 tokens: 72, 59 us; 20
+// tiles in teams of 2, 7 and 10: 184, 191, 180.)
+static int latent_team(int tiles, int sms)
+{
+    // CTAs' time for a tile of each, times the tiles
+    const auto cost = [&](int t) { return static_cast<double>((tiles + t - 1) / t * t) / (sms / t * t); };
+    const int most = std::min({tiles, kLatentMaxTeam, sms});
+    if (most < 2) return 1;
+    double least = cost(2);
+    for (int t = 3; t <= most; ++t) least = std::min(least, cost(t));
+    int team = most;
+    while (cost(team) > 1.015 * least) --team;
+    return team;
+}
+
 int attn_fwd_latent_paged(const void *q, const void *pool, const int32_t *cache_seqlens, const int32_t *block_table,
                           const int32_t *tree, void *o, float *lse, const int64_t *q_strides, const int64_t *o_strides,
                           int64_t b, int64_t h, int64_t sq, int64_t num_pages, int64_t page_size, int64_t pages_per_seq,
@@ -1758,7 +1777,8 @@ int attn_fwd_latent_paged(const void *q, const void *pool, const int32_t *cache_
     p.sq = static_cast<int32_t>(sq);
     p.rows = static_cast<int32_t>(rows);
     p.tiles = static_cast<int32_t>((rows + tile - 1) / tile);
-    p.team = p.tiles <= kLatentMaxTeam ? p.tiles : 2;
+    const int sms = di->sm_count < kLatentMaxCtas ? di->sm_count : kLatentMaxCtas;
+    p.team = latent_team(p.tiles, sms);
     p.groups = (p.tiles + p.team - 1) / p.team;
     p.cap = static_cast<int32_t>(pages_per_seq * page_size);
     p.page_size = static_cast<int32_t>(page_size);
@@ -1769,7 +1789,7 @@ int attn_fwd_latent_paged(const void *q, const void *pool, const int32_t *cache_
     p.timeout_ns = kDefaultTimeoutNs;
     // no more teams than units in full caches
     const double units = static_cast<double>(b) * p.groups * static_cast<double>((p.cap + 127) / 128 + latent_item_cost(tile));
-    int teams = (di->sm_count < kLatentMaxCtas ? di->sm_count : kLatentMaxCtas) / p.team;
+    int teams = sms / p.team;
     if (units < teams) teams = static_cast<int>(units);
     a.tile_rows = tile;
     a.grid = teams * p.team;

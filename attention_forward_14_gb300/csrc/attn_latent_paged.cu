@@ -6,7 +6,7 @@
 // (row i * h + head: the heads of one query stand together).
 //
 // Work.  An item is 16, 32 or 64 rows of one request, a unit 128 of the keys
-// that some of its rows see.  A team of up to four CTAs takes the same units
+// that some of its rows see.  A team of up to twelve CTAs takes the same units
 // for neighbouring items of a request, so that the cache leaves memory once
 // for all of them.  The units of all items, in order, are dealt to the teams
 // in equal contiguous shares, from the lengths that the device holds; an item

@@ -77,7 +77,7 @@ struct LatentPagedParams {
 __host__ __device__ constexpr int latent_item_cost(int tile_rows) { return tile_rows == 64 ? 2 : 1; }
 
 constexpr int kLatentMaxCtas = 160;  // CTAs of a launch at most (sizes the workspace)
-constexpr int kLatentMaxTeam = 4;
+constexpr int kLatentMaxTeam = 12;
 constexpr int kLatentPagedInstances = 6;  // {fp16, bf16} x {16, 32, 64 rows}
 
 struct LatentPagedArgs {

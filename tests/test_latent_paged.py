@@ -36,6 +36,8 @@ CASES = [
     (2, 4, 70, 32, 10, (300, 70), "tree", "bf16"),                 # three words of bits
     (1, 16, 4, 64, 2, (3,), "tree", "bf16"),                       # fewer keys than drafted
     (1, 128, 3, 64, 5, (300,), "tree", "bf16"),
+    (2, 64, 11, 64, 6, (300, 384), "causal", "fp16"),              # a team of eleven
+    (1, 64, 13, 128, 3, (384,), "tree", "bf16"),                   # thirteen tiles
     (40, 2, 1, 16, 9, tuple(range(3, 123, 3)), "causal", "bf16"),  # more requests than a warp has lanes
 ]
 
