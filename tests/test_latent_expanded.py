@@ -180,6 +180,21 @@ def test_sequences_outside_the_totals_are_left():
 
 
 @gpu
+@pytest.mark.parametrize("nq,nk", [((5, 200), (0, 0)), ((0, 0), (5, 200))], ids=["no keys", "no queries"])
+def test_nothing_on_one_side(nq, nk):
+    """No keys in any sequence: outputs and gradients of the queries are zero; no queries: those of the keys."""
+    case = (2, nq, nk, True, "bf16")
+    q, kn, kr, v, gr, cu = make(case, seed=25)
+    ins, packed = call(q, kn, kr, v, cu, case)
+    o, lse = torch.full(gr.shape, 3.0, dtype=q.dtype, device="cuda"), torch.full((2, sum(nq)), 3.0, device="cuda")
+    af.attn_fwd_latent(*ins, *packed, causal=True, o=o, lse=lse)
+    assert (o == 0).all() and torch.isneginf(lse).all()
+    out = [torch.full(t.shape, 3.0, dtype=q.dtype, device="cuda") for t in (q, kn, kr, v)]
+    af.attn_bwd_latent(*ins, o, on_gpu(gr), lse, *packed, causal=True, dq=out[0], dk_nope=out[1], dk_rope=out[2], dv=out[3])
+    assert all((t == 0).all() for t in out)
+
+
+@gpu
 @pytest.mark.parametrize("scale", [2.0, -0.5, 0.0])
 def test_scales(scale):
     case = (2, (200,), (200,), True, "fp16")
