@@ -18,12 +18,13 @@
 //
 // What bounds it: the round from a tile's scores over its weights to its
 // products; the tensor cores would take 2560 clocks for two tiles of scores,
-// which take 3600.  Two sequences of 4096 tokens, 32 heads, causal: 248 us,
-// 1.39 PFLOP/s; 265 when calls keep the GPU at its power limit.  (Timed
-// without them, the exponentials cost nothing, the sum of the weights as
-// rounded 15 us: it stays, since with a reference up to 2^8 below a row's
-// maximum the rounding of one large weight would show.)  One sequence of 300
-// tokens, 8 heads: 10.3 us, the chain of a launch and of three tiles.
+// which take 3500, and are active for 61% of the time.  Two sequences of 4096
+// tokens, 32 heads, causal: 244 us, 1.41 PFLOP/s; 262 when calls keep the GPU
+// at its power limit.  (Timed without them, the exponentials cost nothing, the
+// sum of the weights as rounded 11 us: it stays, since with a reference up to
+// 2^8 below a row's maximum the rounding of one large weight would show.  Two
+// warps to a row's keys, sixteen in all: 370 us.)  One sequence of 300 tokens,
+// 8 heads: 10.3 us, the chain of a launch and of three tiles.
 #include "latent.h"
 
 #include "attn_kv8_common.cuh"
@@ -60,8 +61,9 @@ template <typename T>
 __device__ __forceinline__ float2 store_weights(const uint32_t (&s)[128], float c, float m, uint32_t tS)
 {
     const float2 c2 = make_float2(c, c), m2 = make_float2(-m, -m);
-    float2 l[2], lr[2];
-    l[0] = l[1] = lr[0] = lr[1] = make_float2(0.f, 0.f);
+    float2 l[2];
+    float lr[4] = {0.f, 0.f, 0.f, 0.f};
+    l[0] = l[1] = make_float2(0.f, 0.f);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         uint32_t pk[32];
@@ -72,12 +74,12 @@ __device__ __forceinline__ float2 store_weights(const uint32_t (&s)[128], float 
             const float2 v = make_float2(ex2_approx(x.x), ex2_approx(x.y));
             l[i & 1] = __fadd2_rn(l[i & 1], v);
             pk[i] = Pair<T>::put(v.x, v.y);
-            lr[i & 1] = __fadd2_rn(lr[i & 1], Pair<T>::get(pk[i]));
+            lr[i & 3] = add_halves<T>(pk[i], lr[i & 3]);
         }
         tmem_st32(tS + 32 * h, pk);
     }
-    const float2 a = __fadd2_rn(l[0], l[1]), b = __fadd2_rn(lr[0], lr[1]);
-    return make_float2(a.x + a.y, b.x + b.y);
+    const float2 a = __fadd2_rn(l[0], l[1]);
+    return make_float2(a.x + a.y, (lr[0] + lr[1]) + (lr[2] + lr[3]));
 }
 
 template <typename T, bool CAUSAL>
