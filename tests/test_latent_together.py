@@ -172,6 +172,15 @@ def step(seed, stream=None):
 step.inputs = {}
 
 
+@pytest.fixture(scope="module", autouse=True)
+def memory_given_back():
+    """The last tests' gigabytes, too, which later tests that count what is reserved would find."""
+    yield
+    step.inputs.clear()
+    if torch.cuda.is_available():
+        torch.cuda.empty_cache()
+
+
 def same(a, b):
     return all(torch.equal(x, y) for x, y in zip(a, b, strict=True))
 
