@@ -696,8 +696,9 @@ int64_t attn_fwd_latent_paged_workspace_bytes(int64_t b, int64_t h, int64_t sq);
  *   O = softmax(scale * (q[.., 0..127] k_nope^T + q[.., 128..191] k_rope^T)
  *               [+ causal mask]) V
  * for every sequence of the batch, as attn_fwd_varlen has them (cu_seqlens_q
- * and _k, max_seqlen_q and _k, the mask bottom-right aligned; a sequence whose
- * offsets fall outside the totals is skipped).
+ * and _k, offsets that do not decrease; max_seqlen_q and _k; the mask
+ * bottom-right aligned; a sequence whose offsets fall outside the totals is
+ * skipped).
  *   q            : [total_q, h, 192] of dtype; strides {token, head} in
  *                  elements (positive multiples of 8), 16-byte aligned.
  *   k_nope, v    : [total_k, h, 128], the same; both can be views of one
