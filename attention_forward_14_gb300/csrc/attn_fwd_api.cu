@@ -1687,7 +1687,7 @@ static int validate_latent_sizes(int64_t b, int64_t h, int64_t sq)
     if (b < 0 || h < 0 || sq < 0) return fail(ATTN_ERR_SHAPE, "negative size: b=%lld h=%lld sq=%lld", (long long)b, (long long)h, (long long)sq);
     if (sq > kMaxSeq || h > (1 << 20)) return fail(ATTN_ERR_SHAPE, "sq above 2^30 or more than 2^20 heads");
     if (h > 0 && sq > (INT32_MAX - 1024) / h) return fail(ATTN_ERR_SHAPE, "more than 2^31 - 1024 query rows of one request");
-    if (b > 0 && h * sq / 16 + 1 > INT32_MAX / b) return fail(ATTN_ERR_SHAPE, "too many query rows");
+    if (b > 0 && h * sq / 16 + 1 > (1 << 30) / b) return fail(ATTN_ERR_SHAPE, "too many query rows");
     return ATTN_OK;
 }
 

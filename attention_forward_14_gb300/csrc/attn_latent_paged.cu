@@ -39,8 +39,8 @@
 // rows of A let 64 query rows keep O and S in tensor memory), the rest is the
 // softmax between the two products.  Shared memory has no room for a second
 // tile beside Q (72 KB) and this one (144 KB) that the tensor cores could work
-// on meanwhile.  64 requests of 1000 to 8191 tokens, 128 heads: 111 us, 0.70
-// PFLOP/s; 512 queries of 128 heads on 8192 tokens: 1.14 ms, 0.99 PFLOP/s.
+// on meanwhile.  64 requests of 1000 to 8191 tokens, 128 heads: 107 us, 0.72
+// PFLOP/s; 512 queries of 128 heads on 8192 tokens: 1.09 ms, 1.04 PFLOP/s.
 // The code is kept short (waits, copies and first weights in rolled loops):
 // what is executed once in a call comes from memory at its first use.
 //
@@ -133,16 +133,25 @@ __device__ __forceinline__ int entry_units(const LatentPagedParams &p, int entry
     return latent_item_cost(tile_rows) + units_for(group_end(p, latent_len(p, b), entry - b * p.groups, tile_rows));
 }
 
-// (`mine`: entry_units of entry `lane`, which both this and latent_place begin with)
-__device__ __forceinline__ int64_t latent_total(const LatentPagedParams &p, int mine, int tile_rows)
+// Where the units of the entries stand, held by a warp: a lane has as many
+// neighbouring entries as the others, and the number of units up to its last.
+struct LatentIndex {
+    int64_t upto;
+    int each;
+};
+
+__device__ __forceinline__ LatentIndex latent_index(const LatentPagedParams &p, int tile_rows)
 {
-    const int lane = threadIdx.x & 31, entries = p.b * p.groups;
-    int64_t t = mine;
-#pragma unroll 1
-    for (int e = 32 + lane; e < entries; e += 32) t += entry_units(p, e, tile_rows);
+    const int lane = threadIdx.x & 31, each = (p.b * p.groups + 31) / 32;
+    int64_t t = 0;
+#pragma unroll 2
+    for (int i = 0; i < each; ++i) t += entry_units(p, lane * each + i, tile_rows);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-    return t;
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, t, off);
+        if (lane >= off) t += o;
+    }
+    return {t, each};
 }
 
 __device__ __forceinline__ void set_entry(const LatentPagedParams &p, LatentPlace &c, int entry, int tile_rows)
@@ -158,26 +167,29 @@ __device__ __forceinline__ void set_entry(const LatentPagedParams &p, LatentPlac
 }
 
 // The place of unit u (< total), by every lane of a warp.
-__device__ __forceinline__ LatentPlace latent_place(const LatentPagedParams &p, int mine, int64_t u, int tile_rows)
+__device__ __forceinline__ LatentPlace latent_place(const LatentPagedParams &p, const LatentIndex &x, int64_t u, int tile_rows)
 {
-    const int lane = threadIdx.x & 31, entries = p.b * p.groups;
+    const int lane = threadIdx.x & 31;
+    const int at = __popc(__ballot_sync(0xffffffffu, x.upto <= u));  // the lane that has it
+    const int64_t before = __shfl_sync(0xffffffffu, x.upto, max(at - 1, 0));
+    if (at > 0) u -= before;
     LatentPlace c{};
+    const int end = (at + 1) * x.each;
 #pragma unroll 1
-    for (int e0 = 0; e0 < entries; e0 += 32) {
-        int64_t inc = e0 == 0 ? mine : entry_units(p, e0 + lane, tile_rows);
+    for (int e0 = at * x.each; e0 < end; e0 += 32) {
+        int inc = x.each > 1 && e0 + lane < end ? entry_units(p, e0 + lane, tile_rows) : 0;
+        int src = 0;
+        if (x.each > 1) {  // (32 entries have less than 2^24 units each)
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int64_t o = __shfl_up_sync(0xffffffffu, inc, off);
-            if (lane >= off) inc += o;
+            for (int off = 1; off < 32; off <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, inc, off);
+                if (lane >= off) inc += o;
+            }
+            src = __popc(__ballot_sync(0xffffffffu, inc <= u));
+            const int past = __shfl_sync(0xffffffffu, inc, min(max(src - 1, 0), 31));
+            if (src > 0) u -= past;
+            if (src == 32) continue;
         }
-        const uint32_t past = __ballot_sync(0xffffffffu, inc > u);
-        if (past == 0u) {
-            u -= __shfl_sync(0xffffffffu, inc, 31);
-            continue;
-        }
-        const int src = __ffs(past) - 1;
-        const int64_t before = __shfl_sync(0xffffffffu, inc, src > 0 ? src - 1 : 0);
-        if (src > 0) u -= before;
         set_entry(p, c, e0 + src, tile_rows);
         c.j += static_cast<int>(u);
         break;
@@ -309,14 +321,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     await_previous();
 
     const int team = blockIdx.x / p.team, rank = blockIdx.x - team * p.team;
-    const int mine = entry_units(p, lane, N);
-    const Shares shared_out(latent_total(p, mine, N), static_cast<int>(gridDim.x) / p.team, 1);
+    const LatentIndex index = latent_index(p, N);
+    const Shares shared_out(__shfl_sync(0xffffffffu, index.upto, 31), static_cast<int>(gridDim.x) / p.team, 1);
     const bool works = team < shared_out.ctas;
     // (a team that gives up on a wait leaves it so: the join must not meet what was in the workspace)
     if (threadIdx.x == 0 && rank == 0) p.cut[team] = LatentCut{0, 0, {0, 0}};
     const int64_t u0 = works ? shared_out.start(team) : 0;
     const int n_units = works ? static_cast<int>(shared_out.start(team + 1) - u0) : 0;
-    LatentPlace at = latent_place(p, mine, u0, N);
+    LatentPlace at = latent_place(p, index, u0, N);
     auto place_in_bounds = [&]() {
         const bool ok = ATTN_OPS_IN_BOUNDS(at.b >= 0 && at.b < p.b && at.group >= 0 && at.group < p.groups && at.j >= 0 && at.j < at.n,
                                            p, SITE_OPS_UNIT);

@@ -39,6 +39,7 @@ CASES = [
     (2, 64, 11, 64, 6, (300, 384), "causal", "fp16"),              # a team of eleven
     (1, 64, 13, 128, 3, (384,), "tree", "bf16"),                   # thirteen tiles
     (40, 2, 1, 16, 9, tuple(range(3, 123, 3)), "causal", "bf16"),  # more requests than a warp has lanes
+    (70, 1, 1, 16, 20, tuple((91 * i) % 321 for i in range(70)), "none", "fp16"),  # and than two for each lane
 ]
 
 
