@@ -1701,7 +1701,7 @@ int64_t attn_fwd_latent_paged_workspace_bytes(int64_t b, int64_t h, int64_t sq)
 // CTAs of a team: the most, since the cache leaves memory once for a team, of
 // the numbers that leave hardly more CTAs without a tile or a team than the
 // best.  (Teams of 1, 2: 128 heads of 64 requests, two tiles, 139, 111 us; of
-// 2, 4, 8: 512 queries of 128 heads, 1024 tiles, 1155, 1148, 1139.  Five tiles
+// 2, 4, 8: 512 queries of 128 heads, 1024 tiles, 1155, 1148, 1139 at the time.  Five tiles
 // in teams of 2 and of 5, 16 requests of 2000 to 4096 tokens: 72, 59 us; 20
 // tiles in teams of 2, 7 and 10: 184, 191, 180.)
 static int latent_team(int tiles, int sms)
