@@ -29,9 +29,9 @@
 // of a unit of queries 1500, its products 1150.  Two sequences of 4096 tokens,
 // 32 heads, causal: 880 us (512 and 370 of them in the two kinds of units, 23
 // for D, 13 for the sum over heads), 1.02 PFLOP/s of what one pass needs, 1.4
-// of what is computed.  4001 packed tokens, 16 heads: 126 us.  Persistent
-// CTAs that claim units and bring the next one's operands meanwhile gained 30
-// us for dQ and lost as much for dK and dV.
+// of what is computed.  4001 packed tokens, 16 heads: 126 us.  (Persistent
+// CTAs that claim units and bring the next one's operands meanwhile took 525
+// us for dK and dV and 326 for dQ, in two launches.)
 #include "latent.h"
 
 #include "attn_kv8_common.cuh"
