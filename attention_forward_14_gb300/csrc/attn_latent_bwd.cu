@@ -27,9 +27,9 @@
 // What bounds it: the tensor cores and the round between them and the softmax
 // warps.  A tile of a unit of keys takes 1690 clocks, its products 1470; one
 // of a unit of queries 1500, its products 1150.  Two sequences of 4096 tokens,
-// 32 heads, causal: 880 us (512 and 370 of them in the two kinds of units, 23
-// for D, 13 for the sum over heads), 1.02 PFLOP/s of what one pass needs, 1.4
-// of what is computed.  4001 packed tokens, 16 heads: 126 us.  (Persistent
+// 32 heads, causal: 880 us (23 of them for D, 13 for the sum over heads; the
+// two kinds of units in launches of their own took 512 and 370), 1.02 PFLOP/s
+// of what one pass needs, 1.4 of what is computed.  4001 packed tokens, 16 heads: 126 us.  (Persistent
 // CTAs that claim units and bring the next one's operands meanwhile took 525
 // us for dK and dV and 326 for dQ, in two launches.)
 #include "latent.h"
