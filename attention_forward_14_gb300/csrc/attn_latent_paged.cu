@@ -418,7 +418,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // -------------------------------------------------------- cleaning
             // The scores of keys that a row does not see are replaced, but 0 times a value is 0 for finite values
             // only.  Behind the length: zeros.  Of keys that some rows see: NaN and infinities become zeros, since a
-            // row that sees such a key has a score that is NaN or infinite itself, and with it NaN everywhere.
+            // row that sees such a key has a score that is NaN or infinite itself, and with it NaN everywhere.  So the
+            // tile is touched when its scores are complete, not only issued: they are formed from what was there.
             uint32_t np = 0u, n_dirty = 0u;
             bool ok = true;
             for (int it = 0; ok && it < n_units;) {
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mma_ss_by(leader, tmem + C::TM_S, dk_key + ((ks * C::PANEL + kk * 32) >> 4), dq + ((8 * C::Q_PANEL + kk * 32) >> 4),
                                IDESC_S, 1u);
                     tc_commit_by(leader, B(ctl->s_full));
-                    if (dirty && leader) mbar_arrive(B(ctl->dirty));
+                    if (dirty) tc_commit_by(leader, B(ctl->dirty));  // the scores are of the values as they were
                     // O^T
                     if (dirty && !(ok = warp_waits(B(ctl->clean), n_dirty++ & 1u, SITE_LAT_CLEAN))) break;
                     if (!(ok = warp_waits(B(ctl->p_full), tile_it & 1u, SITE_LAT_P))) break;
