@@ -77,7 +77,7 @@ struct LatentCfg {
     static constexpr int Q_PANEL = N * 128;
     static constexpr int COLS = N / 2;                   // rows (columns of S^T) of a softmax thread
     static constexpr int PAIR_SLOTS = N == 64 ? 4 : 5, KEY_SLOTS = N == 16 ? 2 : 1;
-    static constexpr int CTL = 5120;
+    static constexpr int CTL = 9216;
     static constexpr int Q_OFF = CTL;
     static constexpr int PAIR_OFF = Q_OFF + kPanels * Q_PANEL;
     static constexpr int KEY_OFF = PAIR_OFF + PAIR_SLOTS * PAIR;
@@ -99,6 +99,8 @@ struct LatentCtl {
     float red2[2][4][32];
     float shrink[2][4][32];
     int64_t o_at[64];        // where each row of o begins (elements)
+    uint32_t lost[2][kLatent];  // of a softmax group's rows, a bit each: those in which a value of O is 0 times infinity
+    uint32_t any_lost[2];
 };
 static_assert(sizeof(LatentCtl) <= LatentCfg<16>::CTL, "control block");
 
@@ -307,8 +309,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(B(ctl->clean), 2);
         mbar_init(B(ctl->mma_done), 1);
         ctl->abort = 0u;
+        ctl->any_lost[0] = ctl->any_lost[1] = 0u;
         fence_barrier_init();
     }
+    for (int i = threadIdx.x; i < 2 * kLatent; i += kThreads) ctl->lost[0][i] = 0u;
     if (warp == 8) {
         tmem_alloc(smem_addr(&ctl->tmem_base), 512);
         tmem_relinquish();
@@ -417,9 +421,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp >= 10) {
             // -------------------------------------------------------- cleaning
             // The scores of keys that a row does not see are replaced, but 0 times a value is 0 for finite values
-            // only.  Behind the length: zeros.  Of keys that some rows see: NaN and infinities become zeros, since a
-            // row that sees such a key has a score that is NaN or infinite itself, and with it NaN everywhere.  So the
-            // tile is touched when its scores are complete, not only issued: they are formed from what was there.
+            // only.  Behind the length: zeros.  Of keys that some rows see: NaN and infinities become zeros.  A row
+            // that sees such a key has a score of NaN or infinity, and with NaN and +infinity it has NaN everywhere;
+            // with -infinity the weight is 0, and the softmax warps keep account of what the zeros replaced.  The tile
+            // is touched when its scores are complete, not only issued: they are formed from what was there.
             uint32_t np = 0u, n_dirty = 0u;
             bool ok = true;
             for (int it = 0; ok && it < n_units;) {
@@ -582,6 +587,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 return sees;
             };
+            // Key k, whose score is -infinity for `rows` of the group's half, which see it: 0 times its infinite values
+            // is NaN.  (In a tile that all rows see whole, the product itself comes to that.)
+            auto lose = [&](int k, uint32_t rows) {
+                const int pg = k / p.page_size, page = p.block_table[static_cast<int64_t>(at.b) * p.pages_per_seq + pg];
+                if (page < 0 || page >= p.num_pages) return;
+                const uint16_t *c = reinterpret_cast<const uint16_t *>(p.pool) +
+                                    (static_cast<int64_t>(page) * p.page_size + (k - pg * p.page_size)) * kLatentToken;
+#pragma unroll 1
+                for (int i = 0; i < kLatent; ++i) {
+                    if (finite_halves<BF16>(c[i]) == c[i]) continue;
+                    atomicOr(&ctl->lost[w][i], rows);
+                    ctl->any_lost[w] = 1u;
+                }
+            };
             // what is needed of each row of the group's half
             if (key < COLS) {
                 const int r = w * COLS + key;
@@ -619,6 +638,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (k0 + kTileKeys > all) {
                     const uint32_t sees = rows_that_see(k0 + key);
+                    float low = x[0].x;
+#pragma unroll
+                    for (int c = 0; c < COLS / 2; ++c) low = min3f(low, x[c].x, x[c].y);
+                    if (low == -INFINITY) {
+                        uint32_t rows = 0u;
+#pragma unroll
+                        for (int c = 0; c < COLS / 2; ++c)
+                            rows |= (x[c].x == -INFINITY ? 1u : 0u) << (2 * c) | (x[c].y == -INFINITY ? 2u : 0u) << (2 * c);
+                        if ((rows & sees) != 0u) lose(k0 + key, rows & sees);
+                    }
+                    __syncwarp();
 #pragma unroll
                     for (int c = 0; c < COLS / 2; ++c) {
                         x[c].x = sees >> (2 * c) & 1 ? x[c].x : -INFINITY;
@@ -743,6 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
             }
             if (goes_on) give_q();
+            const bool lost = ctl->any_lost[w] != 0u;
 #pragma unroll 1
             for (int j = 0; j < kPairs; ++j) {
                 uint32_t o[COLS];
@@ -753,6 +784,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int c = 0; c < COLS; ++c) o[c] = 0u;
                 }
                 const int col = j * 128 + key;
+                if (lost) {
+                    const uint32_t rows = ctl->lost[w][col];
+                    ctl->lost[w][col] = 0u;
+#pragma unroll
+                    for (int c = 0; c < COLS; ++c) o[c] = rows >> c & 1 ? 0x7FFFFFFFu : o[c];
+                }
                 if (!whole) {
 #pragma unroll
                     for (int c = 0; c < COLS; ++c)
@@ -773,6 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_before();
             group_sync();  // before the rows' values are written again
+            if (key == 0) ctl->any_lost[w] = 0u;
             it += j_end - at.j;
             if (it == n_units && threadIdx.x == 0 && rank == 0) {
                 // the item that this team begins and others go on with, if there is one

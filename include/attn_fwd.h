@@ -670,11 +670,14 @@ int attn_latent_append_paged(const void *kv_new, void *pool,
  *                  attn_fwd_latent_paged_workspace_bytes(b, h, sq) bytes; its
  *                  contents on entry do not matter.  Calls on different
  *                  streams need different workspaces.
- * A row that sees no key gets O = 0 and LSE = -inf.  Slots at or past L are
- * not read into the result, and what a row does not see does not reach it,
- * NaN and infinities included.  The work is dealt out by the lengths on the
- * device.  fp32 accumulation and statistics; P is rounded to dtype before its
- * product, and O divided by the sum of P as rounded.
+ * A row that sees no key gets O = 0 and LSE = -inf, and so does one whose
+ * scores are all -inf.  Slots at or past L are not read into the result, and
+ * what a row does not see does not reach it, NaN and infinities included.
+ * What it sees does as the formula has it: a score of NaN or +inf makes the
+ * row NaN, and where the score of an infinite value is -inf, with a weight of
+ * 0, the row is NaN in that value's place.  The work is dealt out by the
+ * lengths on the device.  fp32 accumulation and statistics; P is rounded to
+ * dtype before its product, and O divided by the sum of P as rounded.
  * Returns ATTN_OK or a negative ATTN_ERR_* code.
  */
 int attn_fwd_latent_paged(const void *q, const void *pool,

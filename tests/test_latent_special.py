@@ -7,6 +7,7 @@ import torch
 
 import attention_forward_14_gb300 as af
 import latent_ref as L
+import ops_ref as R
 import test_latent_paged as P
 
 gpu = pytest.mark.gpu
@@ -53,3 +54,69 @@ def test_nan_reaches_the_rows_that_see_it_and_no_other(shape, dt):
         assert o[rows].isnan().all() and lse[rows].isnan().all(), f"column {col}"
         assert torch.equal(o[~rows], ref[~rows]) and torch.equal(lse[~rows], rlse[~rows]), f"column {col}"
         assert ref.isfinite().all()
+
+
+def by_definition(q, c, seen):
+    """One query: q [576], c [n, 576], seen [n], of which some may not be finite: O, LSE, the sum of P |v| of finite values
+    and the largest scale sum |q k|."""
+    c = c[seen]
+    with np.errstate(invalid="ignore", over="ignore", divide="ignore"):
+        s = SCALE * (c * q).sum(1)
+        m = s.max(initial=-np.inf)
+        if m == -np.inf:  # nothing is seen, or nothing but scores of -infinity
+            return np.zeros(L.LATENT), m, np.zeros(L.LATENT), 0.0
+        p = np.exp(s - m)
+        o, lse = (p[:, None] * c[:, :L.LATENT]).sum(0) / p.sum(), m + np.log(p.sum())
+    fin = np.where(np.isfinite(c), np.abs(c), 0.0)
+    return o, lse, np.nan_to_num(p) @ fin[:, :L.LATENT] / max(np.nan_to_num(p).sum(), 1e-300), SCALE * (fin @ np.abs(q)).max()
+
+
+# b, h, sq, lengths, mask, whether the tiles in which the tokens stand are seen whole by all rows
+INFINITE = [
+    (3, 4, 3, (700, 133, 513), "causal", False),
+    (3, 3, 5, (700, 135, 514), "tree", False),
+    (2, 8, 4, (300, 260), "causal", False),
+    (2, 32, 2, (300, 260), "causal", False),
+    (2, 13, 10, (300, 260), "tree", False),
+    (3, 16, 2, (700, 384, 513), "none", True),
+    (2, 32, 2, (300, 260), "causal", True),
+    (200, 2, 3, tuple(3 + (7 * i) % 60 for i in range(200)), "causal", False),  # more items than teams: most are not cut
+    (200, 33, 1, tuple(2 + (7 * i) % 60 for i in range(200)), "causal", False),
+    (2, 5, 2, (1, 2), "causal", False),
+]
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("case", INFINITE, ids=lambda c: str(c)[:60])
+def test_infinities_act_as_the_formula_has_it(case, dt):
+    """Infinite values, of either sign, in tokens that some rows see: NaN where the score is +infinity or NaN, and where it
+    is -infinity NaN in the values' own places alone, in whole tiles and in those that a mask or the length cuts."""
+    b, h, sq, lens, mask, whole = case
+    q, pool, lens, table, tree = P.make((b, h, sq, 64, 12 if max(lens) > 64 else 1, lens, mask, dt), seed=211)
+    for e in range(b):
+        n = int(lens[e])
+        for i, columns in enumerate([(3,), (140, 200), (300, 511, 575), (384,)][:1 if n < 100 else 4]):
+            j = (5 + 9 * i if whole else max(n - 1 - (e + i) % min(sq, 3), 0))
+            if whole or i == e % 4 or n < 100:
+                pool[table[e, j // 64].long(), j % 64, list(columns)] = float("inf") * (-1) ** (e + i)
+    o, lse = (L.f64(t) for t in run(q, pool, lens, table, tree, mask))
+    fq, fp, half = L.f64(q), L.f64(pool), R.HALF_STEP[q.dtype]
+    alone = 0
+    for e in range(b):
+        n = int(lens[e])
+        c = np.concatenate([fp[int(p)] for p in table[e]])[:n]
+        seen = L.visible(sq, n, mask == "causal", None if tree is None else tree[e].numpy().view(np.uint32))
+        for i in range(sq):
+            for k in range(h):
+                want, wlse, absolute, size = by_definition(fq[e, k, i], c, seen[i])
+                assert np.array_equal(np.isnan(o[e, k, i]), np.isnan(want)), f"{e} {k} {i}"
+                assert np.isnan(lse[e, k, i]) == np.isnan(wlse)
+                if np.isnan(wlse):
+                    continue
+                alone += np.isnan(want).any()
+                fin = ~np.isnan(want)
+                bound = L.output_error(want, absolute, np.array(size), half, L.TOKEN // 16)
+                L.check(torch.from_numpy(o[e, k, i][fin]), want[fin], bound[fin], f"O {e} {k} {i}")
+                assert lse[e, k, i] == wlse or abs(lse[e, k, i] - wlse) <= L.score_error(size, L.TOKEN // 16) + 2.0 ** -20 * (1 + abs(wlse))
+    assert alone > 0 or case[3] == (1, 2)  # rows with NaN in some places
