@@ -276,9 +276,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
             const uint32_t tS = tmem + lane_off + t * 128, tO = tmem + lane_off + kTmO + t * 128;
             const int row = un.row0 + t * kRows + in_tile;
-            const bool neg = p.s.sl2e < 0.f;
-            // (a scale of 0 as the smallest that still turns -inf into -inf)
+            // (a scale of 0, or next to it, as the smallest that still turns -inf into -inf)
             const float c = fabsf(p.s.sl2e) < 1e-30f ? 1e-30f : p.s.sl2e;
+            const bool neg = c < 0.f;
             const int lim = CAUSAL ? min(row + 1 + un.sk - un.sq, un.sk) : un.sk;  // keys this row sees
             float m = -INFINITY, l = 0.f, lr = 0.f;
             bool ok = true;
