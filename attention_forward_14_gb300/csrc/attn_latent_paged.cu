@@ -271,6 +271,17 @@ __device__ __forceinline__ uint32_t finite_halves(uint32_t w)
     return w;
 }
 
+// A bit for each of a query's h rows from r on that is one of 32: none where
+// the 32 lie past a request's last row, which counts as the last query's.
+__host__ __device__ constexpr uint32_t rows_of_query(int r, int h)
+{
+    const int lo = r > 0 ? r : 0, n = (r + h < 32 ? r + h : 32) - lo;
+    return n <= 0 ? 0u : (n < 32 ? (1u << n) - 1u : ~0u) << lo;
+}
+// (an undefined shift is no constant)
+static_assert(rows_of_query(-8, 4) == 0u && rows_of_query(-4, 4) == 0u && rows_of_query(32, 4) == 0u && rows_of_query(-1, 4) == 7u &&
+              rows_of_query(28, 8) == 0xF0000000u && rows_of_query(0, 32) == ~0u && rows_of_query(-40, 100) == ~0u);
+
 template <int N, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_latent_paged_kernel(const __grid_constant__ CUtensorMap tmPool, const __grid_constant__ LatentPagedParams p)
@@ -582,8 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (p.mask == LATENT_MASK_CAUSAL) one = drafted <= i;
                     if (p.mask == LATENT_MASK_TREE && drafted >= 0)
                         one = (tree[static_cast<int64_t>(i) * p.tree_words] >> (drafted & 31) & 1) != 0;
-                    const int lo = max(r, 0), n = min(r + p.h, 32) - lo;  // n >= 1
-                    if (one) sees |= (n < 32 ? (1u << n) - 1u : ~0u) << lo;
+                    if (one) sees |= rows_of_query(r, p.h);
                 }
                 return sees;
             };

@@ -120,3 +120,13 @@ def test_infinities_act_as_the_formula_has_it(case, dt):
                 L.check(torch.from_numpy(o[e, k, i][fin]), want[fin], bound[fin], f"O {e} {k} {i}")
                 assert lse[e, k, i] == wlse or abs(lse[e, k, i] - wlse) <= L.score_error(size, L.TOKEN // 16) + 2.0 ** -20 * (1 + abs(wlse))
     assert alone > 0 or case[3] == (1, 2)  # rows with NaN in some places
+
+
+@gpu
+@pytest.mark.parametrize("h,sq", [(1, 1), (4, 1), (8, 1), (2, 4), (17, 1), (16, 1), (3, 11), (33, 1), (32, 1), (40, 2), (65, 1)])
+@pytest.mark.parametrize("mask", ["none", "causal", "tree"])
+def test_halves_of_a_tile_past_the_last_row(h, sq, mask):
+    """Rows that do not fill the first half of a tile, just fill it, or begin the second."""
+    q, pool, lens, table, tree = P.make((3, h, sq, 64, 4, (sq, 131, 250), mask, "bf16"), seed=71)
+    o, lse = run(q, pool, lens, table, tree, mask)
+    P.compare(o, lse, q, pool, lens, table, mask == "causal", tree)
