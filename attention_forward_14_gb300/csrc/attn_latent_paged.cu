@@ -275,11 +275,11 @@ __device__ __forceinline__ uint32_t finite_halves(uint32_t w)
 // the 32 lie past a request's last row, which counts as the last query's.
 __host__ __device__ constexpr uint32_t rows_of_query(int r, int h)
 {
-    const int lo = r > 0 ? r : 0, n = (r + h < 32 ? r + h : 32) - lo;
-    return n <= 0 ? 0u : (n < 32 ? (1u << n) - 1u : ~0u) << lo;
+    const int lo = r > 0 ? r : 0, end = r + h < 32 ? r + h : 32, n = end > lo ? end - lo : 0;
+    return (n < 32 ? (1u << n) - 1u : ~0u) << lo;
 }
 // (an undefined shift is no constant)
-static_assert(rows_of_query(-8, 4) == 0u && rows_of_query(-4, 4) == 0u && rows_of_query(32, 4) == 0u && rows_of_query(-1, 4) == 7u &&
+static_assert(rows_of_query(-8, 4) == 0u && rows_of_query(-4, 4) == 0u && rows_of_query(31, 4) == 0x80000000u && rows_of_query(-1, 4) == 7u &&
               rows_of_query(28, 8) == 0xF0000000u && rows_of_query(0, 32) == ~0u && rows_of_query(-40, 100) == ~0u);
 
 template <int N, typename T>
