@@ -18,20 +18,23 @@
 // A unit of queries (dQ) is 128 queries of one head, to which the keys that
 // they see are streamed, 64 at a time: S (64 columns), two tiles' dP (64
 // each), whose places dS takes, the sum dQ (192), and Q as an operand (96).
-// It computes S and dP again: 38% more products than one pass would take, but
-// dK's 192 columns leave that one no room for dQ in tensor memory, and there
-// are no sums by atomics.
+// It computes S and dP again: 38% more products than one pass would take.  One
+// pass over keys has no room in tensor memory for a running dQ beside dK's 192
+// columns; it would add up each tile's in global memory, in an order that is
+// not fixed or that units wait for.  That pass has not been built and measured
+// here; two give equal calls equal bits without either.
 // In both, the softmax warps work on P while the tensor cores work on the sums
 // of the tile before, and on dS while they work on the next tile's scores.
 //
 // What bounds it: the tensor cores and the round between them and the softmax
 // warps.  A tile of a unit of keys takes 1690 clocks, its products 1470; one
 // of a unit of queries 1500, its products 1150.  Two sequences of 4096 tokens,
-// 32 heads, causal: 880 us (23 of them for D, 13 for the sum over heads; the
-// two kinds of units in launches of their own took 512 and 370), 1.02 PFLOP/s
-// of what one pass needs, 1.4 of what is computed.  4001 packed tokens, 16 heads: 126 us.  (Persistent
-// CTAs that claim units and bring the next one's operands meanwhile took 525
-// us for dK and dV and 326 for dQ, in two launches.)
+// 32 heads, causal: 864 us a call in bursts of eight (23 of them for D, 13 for
+// the sum over heads; the two kinds of units in launches of their own took 512
+// and 370), 1.03 PFLOP/s of what one pass needs, 1.43 of what is computed; 920
+// to 934 back to back, at the power limit.  4001 packed tokens, 16 heads: 126
+// us.  (Persistent CTAs that claim units and bring the next one's operands
+// meanwhile took 525 us for dK and dV and 326 for dQ, in two launches.)
 #include "latent.h"
 
 #include "attn_kv8_common.cuh"

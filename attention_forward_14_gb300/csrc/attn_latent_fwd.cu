@@ -19,8 +19,9 @@
 // What bounds it: the round from a tile's scores over its weights to its
 // products; the tensor cores would take 2560 clocks for two tiles of scores,
 // which take 3500, and are active for 61% of the time.  Two sequences of 4096
-// tokens, 32 heads, causal: 244 us, 1.41 PFLOP/s; 262 when calls keep the GPU
-// at its power limit.  (Timed without them, the exponentials cost nothing, the
+// tokens, 32 heads, causal: 242 us a call in bursts of eight, at 2070 MHz, 1.42
+// PFLOP/s; 259 to 266 back to back, which keeps the GPU at its power limit
+// (1.79 to 1.84 GHz).  (Timed without them, the exponentials cost nothing, the
 // sum of the weights as rounded 11 us: it stays, since with a reference up to
 // 2^8 below a row's maximum the rounding of one large weight would show.  Two
 // warps to a row's keys, sixteen in all: 370 us.)  One sequence of 300 tokens,

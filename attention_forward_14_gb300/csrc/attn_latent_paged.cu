@@ -33,14 +33,14 @@
 // P^T takes the place of the tile's key parts once the scores are there.
 //
 // What bounds it.  16 rows: memory (32 requests of up to 16383 tokens, fp16:
-// 67 us, of which the join 5 and some 10 the ramp; between them the cache at
+// 66 us, of which the join 5 and some 10 the ramp; between them the cache at
 // 6.2 TB/s).  64 rows: a tile of 128 keys takes 2.6 us, of which the tensor
 // cores work 1.7 (their N of 64 takes 3/4 of the rate of 128: keys as the
 // rows of A let 64 query rows keep O and S in tensor memory), the rest is the
 // softmax between the two products.  Shared memory has no room for a second
 // tile beside Q (72 KB) and this one (144 KB) that the tensor cores could work
 // on meanwhile.  64 requests of 1000 to 8191 tokens, 128 heads: 107 us, 0.72
-// PFLOP/s; 512 queries of 128 heads on 8192 tokens: 1.09 ms, 1.04 PFLOP/s.
+// PFLOP/s; 512 queries of 128 heads on 8192 tokens: 1.10 ms, 1.03 PFLOP/s.
 // The code is kept short (waits, copies and first weights in rolled loops):
 // what is executed once in a call comes from memory at its first use.
 //

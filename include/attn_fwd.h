@@ -711,9 +711,11 @@ int64_t attn_fwd_latent_paged_workspace_bytes(int64_t b, int64_t h, int64_t sq);
  *                  nor overlap an input.
  *   lse          : fp32 [h, total_q], or NULL.
  * A row that sees no key gets O = 0 and LSE = -inf; what lies behind a
- * sequence's end does not reach it.  fp32 accumulation and statistics; P is
- * rounded to dtype before its product, and O divided by the sum of P as
- * rounded.  Asynchronous on `stream`.
+ * sequence's end does not reach it.  NaN and infinities within a sequence are
+ * not kept from rows of the same tile that the causal mask hides them from
+ * (their weight is 0, and 0 times them is NaN), here and in the gradients.
+ * fp32 accumulation and statistics; P is rounded to dtype before its product,
+ * and O divided by the sum of P as rounded.  Asynchronous on `stream`.
  * Returns ATTN_OK or a negative ATTN_ERR_* code.
  */
 int attn_fwd_latent(const void *q, const void *k_nope, const void *k_rope,
@@ -746,7 +748,8 @@ int attn_fwd_latent(const void *q, const void *k_nope, const void *k_rope,
  *                  dk_rope); its contents on entry do not matter.  Calls on
  *                  different streams need different workspaces.
  * The outputs of every sequence are written in full (zeros where a gradient
- * is zero).  All sums are added in a fixed order: equal calls give equal bits.
+ * is zero); with h = 0 nothing is.  All sums are added in a fixed order: equal
+ * calls give equal bits.
  * P and dS are rounded to dtype before their products.
  * Returns ATTN_OK or a negative ATTN_ERR_* code.
  */
